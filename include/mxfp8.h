@@ -347,6 +347,130 @@ int mxfp8_debug_force_path(int path);
  */
 int mxfp8_debug_plan(int64_t M, int64_t N, int64_t K, int* path, int* splits);
 
+/*
+ * ---------------------------------------------------------------------------
+ * FP8 with one scale for each block of 128, and the layer's training side.
+ *
+ * Element types of entries that take either.
+ */
+typedef enum { MXFP8_F32 = 0, MXFP8_BF16 = 1 } mxfp8_dtype;
+
+/*
+ * The 128-block linear layer ("unified block-scale FP8", flashinfer PR #4026,
+ * beside the MXFP8 mode above):
+ *   y[m, n] = bf16( sum_k deq(q(x))[m, k] * deq(W)[n, k] + bias[n] )
+ * W: E4M3 with an fp32 scale for each 128 x 128 block; x: bf16, quantized to
+ * E4M3 with a power-of-two scale (UE8M0) for each 1 x 128 block,
+ *   scale = the smallest power of two s with amax / s <= 448, elements
+ *   RNE(v / s); a block of zeros gets byte 0, a block that holds an infinity
+ *   or NaN gets byte 0xFF (NaN) and makes the outputs it enters NaN.
+ * Sums in fp32, one rounding to bf16.  K is any multiple of 16 (>= 16, at most
+ * 2^24), N any; the last blocks may be partial.
+ *
+ * mxfp8_quantize_b128: x_bf16 [M, K] row stride ldx (ldx >= K, ldx % 8 == 0,
+ *   16-byte aligned) -> q_e4m3 [M, K] row stride ldq (ldq >= K, ldq % 16 == 0,
+ *   16-byte aligned), s_e8m0 [M, ceil(K/128)] row stride lds.
+ * mxfp8_quantize_act_packed_b128: the same into the packed operand layout
+ *   (256-byte aligned buffers of mxfp8_packed_act_b128_bytes: rows and K
+ *   padded to 128 with zeros, one scale byte per 32 elements as for MXFP8,
+ *   so mxfp8_unpack_weight reads them where K % 256 == 0).  The packed activations are also the layer's 8-bit
+ *   activation checkpoint: mxfp8_linear_wgrad reads them.
+ * mxfp8_dequantize_act_packed: packed activations of either quantizer
+ *   (mxfp8_quantize_act_packed or the above) -> x_bf16 [M, K] row stride ldx
+ *   (ldx >= K, ldx % 8 == 0, 16-byte aligned): the values the checkpoint
+ *   holds, for backward passes other than the linear layer's.
+ * mxfp8_quantize_weight_b128: w_bf16 [N, K] row stride ldw (ldw % 8 == 0,
+ *   16-byte aligned) -> any of: E4M3 q [N, K] (row stride ldq, ldq % 16 == 0)
+ *   with fp32 s [ceil(N/128), ceil(K/128)] (row stride lds); the prepared
+ *   weight (w_packed, s_packed); the prepared transposed weight (wt_packed,
+ *   st_packed).  Pairs not wanted are NULL.  The rule above with 128 x 128
+ *   blocks (its power of two stored as fp32).
+ * mxfp8_prepare_weight_b128: one-time layout of a quantized weight.  w_e4m3
+ *   [N, K] row stride ldw (ldw % 16 == 0, 16-byte aligned), w_s fp32
+ *   [ceil(N/128), ceil(K/128)] row stride lds, any values.  transpose != 0
+ *   prepares W^T (K rows, summed over N; N % 16 == 0 then), which turns the
+ *   layer into its input gradient dX = deq(q(dY)) deq(W): a 128 x 128 block's
+ *   scale is its transpose's.  Outputs 256-byte aligned, of
+ *   mxfp8_prepared_weight_b128_bytes(N, K), or (K, N) if transposed.
+ * mxfp8_linear_b128: arguments as mxfp8_linear, workspace of
+ *   mxfp8_linear_b128_workspace_bytes.
+ * mxfp8_gemm_packed_b128: the GEMM alone on activations of
+ *   mxfp8_quantize_act_packed_b128; workspace of
+ *   mxfp8_gemm_packed_b128_workspace_bytes (fp32 partials where K is split).
+ * Workspaces need no initialization; calls sharing one are ordered on one
+ * stream.
+ */
+int mxfp8_quantize_b128(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, void* q_e4m3, int64_t ldq,
+                        void* s_e8m0, int64_t lds, void* stream);
+int mxfp8_packed_act_b128_bytes(int64_t M, int64_t K, size_t* q_bytes, size_t* s_bytes);
+int mxfp8_quantize_act_packed_b128(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, void* q_packed,
+                                   void* s_packed, void* stream);
+int mxfp8_dequantize_act_packed(const void* q_packed, const void* s_packed, int64_t M, int64_t K, void* x_bf16,
+                                int64_t ldx, void* stream);
+int mxfp8_prepared_weight_b128_bytes(int64_t N, int64_t K, size_t* w_bytes, size_t* s_bytes);
+int mxfp8_prepare_weight_b128(const void* w_e4m3, const float* w_s, int64_t N, int64_t K, int64_t ldw, int64_t lds,
+                              int transpose, void* w_packed, void* s_packed, void* stream);
+int mxfp8_quantize_weight_b128(const void* w_bf16, int64_t N, int64_t K, int64_t ldw, void* q_e4m3, int64_t ldq,
+                               float* s, int64_t lds, void* w_packed, void* s_packed, void* wt_packed,
+                               void* st_packed, void* stream);
+int mxfp8_linear_b128_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes);
+int mxfp8_linear_b128(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, const void* w_packed,
+                      const void* s_packed, int64_t N, const void* bias_bf16, void* y_bf16, int64_t ldy,
+                      void* workspace, size_t workspace_bytes, void* stream);
+int mxfp8_gemm_packed_b128_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes);
+int mxfp8_gemm_packed_b128(const void* q_packed, const void* s_packed, int64_t M, int64_t K, const void* w_packed,
+                           const void* ws_packed, int64_t N, const void* bias_bf16, void* y_bf16, int64_t ldy,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Weight and bias gradient of a linear layer from its 8-bit activation
+ * checkpoint:
+ *   dw[n, k] = sum_m dy[m, n] * deq(X)[m, k],   db[n] = sum_m dy[m, n]
+ * X: packed activations of mxfp8_quantize_act_packed or
+ * mxfp8_quantize_act_packed_b128 for this (M, K).  Products exact, sums in
+ * fp32 in a fixed order.
+ *   dy_bf16 [M, N] row stride lddy (lddy >= N, lddy % 8 == 0, lddy <= 2^24,
+ *           16-byte aligned), N % 8 == 0
+ *   dw      [N, K] row stride lddw (lddw >= K, lddw % 8 == 0), 16-byte
+ *           aligned: fp32 (MXFP8_F32) or bf16 (MXFP8_BF16, rounded once)
+ *   db      fp32 [N] or NULL
+ *   accumulate != 0: dw += and db += (fp32 dw only; MXFP8_E_SHAPE else)
+ * M == 0 writes zeros (or leaves dw, db as they are if accumulating).
+ * workspace of mxfp8_linear_wgrad_workspace_bytes, 256-byte aligned.
+ */
+int mxfp8_linear_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes);
+int mxfp8_linear_wgrad(const void* dy_bf16, int64_t M, int64_t N, int64_t lddy, const void* q_packed,
+                       const void* s_packed, int64_t K, void* dw, int dw_dtype, int64_t lddw, float* db,
+                       int accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Load-balance and z loss of the routed layer's router, the tokens of each
+ * expert, and the gradient with respect to the logits:
+ *   p = softmax(logits[t, :]), lse = log sum_e exp(logits[t, e]) (over all E)
+ *   counts[e] = counted tokens whose topk largest logits hold e (ties: lower
+ *               e first; the selection of mxfp8_moe_grouped)
+ *   used      = n, the tokens counted
+ *   loss      = coef E / (topk n^2) sum_e counts[e] sum_t p[t, e]
+ *               + z_coef / n sum_t lse[t]^2                     (0 if n == 0)
+ *   dlogits[t, e] = g ( coef E / (topk n^2) p[t, e] (counts[e] - sum_j counts[j] p[t, j])
+ *               + 2 z_coef / n lse[t] p[t, e] ),  g = *grad_loss (1 if NULL)
+ * A token is counted if valid is NULL or valid[t] != 0, and one of its logits
+ * is not -inf; the others get zero gradients.  A NaN or +inf logit of a
+ * counted token makes the loss and that token's gradients NaN.
+ *   logits, dlogits [T, E], row strides ldl, ldd >= E, fp32 or bf16 (`dtype`)
+ *   valid bytes [T]; loss fp32 [1]; counts int32 [E]; used int32 [1]
+ * 1 <= E <= 256, 1 <= topk <= min(E, 16), T >= 0 (T == 0: loss 0, counts 0).
+ * The backward call takes counts and used as the forward call (or a sum of
+ * several forward calls' over data-parallel ranks) left them, on the device.
+ */
+int mxfp8_moe_balance_workspace_bytes(int64_t T, int64_t E, size_t* bytes);
+int mxfp8_moe_balance(const void* logits, int dtype, int64_t T, int64_t E, int64_t ldl, int64_t topk,
+                      const uint8_t* valid, float coef, float z_coef, float* loss, int* counts, int* used,
+                      void* workspace, size_t workspace_bytes, void* stream);
+int mxfp8_moe_balance_backward(const void* logits, int dtype, int64_t T, int64_t E, int64_t ldl, int64_t topk,
+                               const uint8_t* valid, float coef, float z_coef, const int* counts, const int* used,
+                               const float* grad_loss, void* dlogits, int64_t ldd, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,6 +18,10 @@ _API = (
     "moe_debug_capture",
     "PreparedWeightFP4", "prepare_weight_fp4", "quantize_fp4", "mxfp8_quantize_fp4", "mxfp8_prepared_weight_fp4_bytes", "mxfp8_prepare_weight_fp4",
     "mxfp8_linear_w4a8_workspace_bytes", "mxfp8_linear_w4a8",
+    "PreparedWeightB128", "prepare_weight_b128", "prepare_weight_b128_bf16", "quantize_weight_b128",
+    "quantize_act_b128", "quantize_act_packed_b128", "linear_b128", "linear_wgrad",
+    "mxfp8_linear_b128", "mxfp8_linear_b128_workspace_bytes", "mxfp8_prepared_weight_b128_bytes",
+    "moe_balance", "moe_balance_backward", "moe_balance_loss",
     "mxfp8_status_string", "MXFP8Error",
 )
 

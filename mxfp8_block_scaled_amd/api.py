@@ -12,6 +12,7 @@ wrappers (the apply path of vLLM PR #52204: assert bf16, view the input as
 ``[-1, K]``, run the layer, restore the leading dims).
 """
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -57,6 +58,26 @@ _SIGNATURES = {
     "mxfp8_gemm_prequant_workspace_bytes": ([_i64, _i64, _i64, ctypes.POINTER(_sz)], ctypes.c_int),
     "mxfp8_gemm_prequant": ([_vp, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _sz, _vp],
                             ctypes.c_int),
+    "mxfp8_quantize_b128": ([_vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp], ctypes.c_int),
+    "mxfp8_packed_act_b128_bytes": ([_i64, _i64, ctypes.POINTER(_sz), ctypes.POINTER(_sz)], ctypes.c_int),
+    "mxfp8_quantize_act_packed_b128": ([_vp, _i64, _i64, _i64, _vp, _vp, _vp], ctypes.c_int),
+    "mxfp8_dequantize_act_packed": ([_vp, _vp, _i64, _i64, _vp, _i64, _vp], ctypes.c_int),
+    "mxfp8_prepared_weight_b128_bytes": ([_i64, _i64, ctypes.POINTER(_sz), ctypes.POINTER(_sz)], ctypes.c_int),
+    "mxfp8_prepare_weight_b128": ([_vp, _vp, _i64, _i64, _i64, _i64, ctypes.c_int, _vp, _vp, _vp], ctypes.c_int),
+    "mxfp8_quantize_weight_b128": ([_vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp],
+                                   ctypes.c_int),
+    "mxfp8_linear_b128_workspace_bytes": ([_i64, _i64, _i64, ctypes.POINTER(_sz)], ctypes.c_int),
+    "mxfp8_linear_b128": ([_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _sz, _vp], ctypes.c_int),
+    "mxfp8_gemm_packed_b128_workspace_bytes": ([_i64, _i64, _i64, ctypes.POINTER(_sz)], ctypes.c_int),
+    "mxfp8_gemm_packed_b128": ([_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _sz, _vp], ctypes.c_int),
+    "mxfp8_linear_wgrad_workspace_bytes": ([_i64, _i64, _i64, ctypes.POINTER(_sz)], ctypes.c_int),
+    "mxfp8_linear_wgrad": ([_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, ctypes.c_int, _i64, _vp, ctypes.c_int, _vp,
+                            _sz, _vp], ctypes.c_int),
+    "mxfp8_moe_balance_workspace_bytes": ([_i64, _i64, ctypes.POINTER(_sz)], ctypes.c_int),
+    "mxfp8_moe_balance": ([_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, ctypes.c_float, ctypes.c_float, _vp, _vp,
+                           _vp, _vp, _sz, _vp], ctypes.c_int),
+    "mxfp8_moe_balance_backward": ([_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, ctypes.c_float, ctypes.c_float,
+                                    _vp, _vp, _vp, _vp, _i64, _vp], ctypes.c_int),
 }
 
 # Static scratch of mxfp8_linear_noalloc (bytes; MXFP8_NOALLOC_SCRATCH_BYTES).
@@ -393,13 +414,16 @@ def prepare_weight_fp4(w_e2m1, w_s):
 def linear(x, pw, bias=None, out=None, workspace=None):
     """The MXFP8 dense linear layer: ``y = bf16(deq(q(x)) @ deq(W).T + bias)``.
 
-    ``x`` bf16 ``[..., K]`` (GPU), ``pw`` a PreparedWeight (MXFP8) or a
-    PreparedWeightFP4 (MXFP4, the W4A8 layer), ``bias`` bf16 ``[N]``
-    or None.  Returns bf16 ``[..., N]`` (contiguous).  ``workspace``: an
+    ``x`` bf16 ``[..., K]`` (GPU), ``pw`` a PreparedWeight (MXFP8), a
+    PreparedWeightFP4 (MXFP4, the W4A8 layer) or a PreparedWeightB128 (FP8
+    with 128-blocks), ``bias`` bf16 ``[N]`` or None.  Returns bf16 ``[..., N]`` (contiguous).  ``workspace``: an
     optional uint8 GPU tensor of at least ``mxfp8_linear_workspace_bytes``
-    (``mxfp8_linear_w4a8_workspace_bytes`` for MXFP4) bytes, 256-byte
+    (``mxfp8_linear_w4a8_workspace_bytes`` for MXFP4,
+    ``mxfp8_linear_b128_workspace_bytes`` for 128-blocks) bytes, 256-byte
     aligned, owned by the caller; by default a cached buffer per (device,
-    stream) is used."""
+    stream) is used (128-blocks: a fresh one from torch's allocator)."""
+    if isinstance(pw, PreparedWeightB128):
+        return _linear_prepared_b128(x, pw, bias, out, workspace)
     assert x.dtype == torch.bfloat16, f"MXFP8 linear requires bfloat16 activations, got {x.dtype}"
     _require_cuda(x, "x")
     K = pw.K
@@ -430,14 +454,29 @@ class PackedActivation:
     """Activations quantized into the GEMM's packed operand layout (rows padded
     to 128): the first kernel of the large-M path."""
 
-    def __init__(self, q_packed, s_packed, M, K):
+    def __init__(self, q_packed, s_packed, M, K, block=32):
         self.q_packed = q_packed
         self.s_packed = s_packed
         self.M = M
         self.K = K
+        self.block = block     # elements that share a scale: 32 (MX) or 128
+
+    @property
+    def device(self):
+        return self.q_packed.device
+
+    def dequantize(self):
+        """The activations the 8-bit values stand for, bf16 ``[M, K]``."""
+        x = torch.empty((self.M, self.K), dtype=torch.bfloat16, device=self.device)
+        with _on(self.device):
+            _check(lib().mxfp8_dequantize_act_packed(_ptr(self.q_packed), _ptr(self.s_packed), self.M, self.K,
+                                                     _ptr(x), self.K, _stream(self.device)),
+                   "mxfp8_dequantize_act_packed")
+        return x
 
     def unpack(self):
-        """(E4M3 ``[M_pad, K]``, UE8M0 ``[M_pad, K/32]``) as uint8 tensors."""
+        """(E4M3 ``[M_pad, K]``, UE8M0 ``[M_pad, K/32]``) as uint8 tensors
+        (K % 256 == 0)."""
         return PreparedWeight(self.q_packed, self.s_packed, self.M, self.K).unpack()
 
 
@@ -459,13 +498,293 @@ def quantize_act_packed(x):
 
 def gemm_packed(pa, pw, bias=None):
     """The GEMM + epilogue on packed activations (the second kernel of the
-    large-M path)."""
+    large-M path), for activations and a weight of the same scale block."""
     assert pa.K == pw.K
+    b128 = isinstance(pw, PreparedWeightB128)
+    if pa.block != (128 if b128 else 32):
+        raise ValueError(f"activations with a scale per {pa.block} elements do not go with this weight")
     y = torch.empty((pa.M, pw.N), dtype=torch.bfloat16, device=pa.q_packed.device)
+    if b128:
+        bias = _bias(bias, pw.N)
+        _same_device(pa.q_packed, pw.w_packed, bias)
+        with _on(pa.device):
+            ws = _scratch(_bytes("mxfp8_gemm_packed_b128_workspace_bytes", pa.M, pw.N, pa.K), pa.device)
+            _check(lib().mxfp8_gemm_packed_b128(_ptr(pa.q_packed), _ptr(pa.s_packed), pa.M, pa.K, _ptr(pw.w_packed),
+                                                _ptr(pw.s_packed), pw.N, _ptr(bias), _ptr(y), y.stride(0), _ptr(ws),
+                                                ws.numel(), _stream(pa.device)), "mxfp8_gemm_packed_b128")
+        return y
     _check(mxfp8_gemm_packed(_ptr(pa.q_packed), _ptr(pa.s_packed), pa.M, pa.K, _ptr(pw.w_packed),
                              _ptr(pw.s_packed), pw.N, _ptr(bias), _ptr(y), y.stride(0),
                              _stream(pa.q_packed.device)), "mxfp8_gemm_packed")
     return y
+
+
+# ---------------------------------------------------------------------------
+# FP8 with 128-blocks, and the layer's training side
+# ---------------------------------------------------------------------------
+
+def _on(device):
+    """Context in which ``device`` is the current one (the library launches on
+    the current device)."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _same_device(first, *rest):
+    for t in rest:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"operands on {first.device} and {t.device}")
+
+
+def _scratch(need, device):
+    """A workspace for one call.  From torch's caching allocator each time, so
+    that it follows the allocator's rules for streams and captured graphs: a
+    graph keeps its own, and no two calls share one unless their order allows."""
+    return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+
+
+def _bytes(query, *sizes):
+    b = _sz()
+    _check(getattr(lib(), query)(*sizes, ctypes.byref(b)), query)
+    return b.value
+
+
+def _rows(x, name):
+    """bf16 ``[..., K]`` -> ``[M, K]`` as the library takes it: rows
+    contiguous, 16-byte aligned, strides of whole 16 bytes."""
+    if x.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be bfloat16, got {x.dtype}")
+    _require_cuda(x, name)
+    x2 = x.reshape(-1, x.shape[-1])
+    if x2.stride(-1) != 1 or x2.stride(0) % 8 != 0 or x2.stride(0) < x2.shape[1] or x2.data_ptr() % 16 != 0:
+        x2 = x2.clone(memory_format=torch.contiguous_format)
+    return x2
+
+
+def _bias(bias, N):
+    if bias is None:
+        return None
+    if bias.dtype != torch.bfloat16 or bias.numel() != N:
+        raise ValueError(f"bias must be bfloat16 [{N}]")
+    return bias.contiguous()
+
+
+def mxfp8_linear_b128_workspace_bytes(M, N, K):
+    return _bytes("mxfp8_linear_b128_workspace_bytes", M, N, K)
+
+
+def mxfp8_linear_b128(x, M, K, ldx, wp, sp, N, bias, y, ldy, ws, ws_bytes, stream):
+    return lib().mxfp8_linear_b128(x, M, K, ldx, wp, sp, N, bias, y, ldy, ws, ws_bytes, stream)
+
+
+def mxfp8_prepared_weight_b128_bytes(N, K):
+    w, s = _sz(), _sz()
+    _check(lib().mxfp8_prepared_weight_b128_bytes(N, K, ctypes.byref(w), ctypes.byref(s)),
+           "mxfp8_prepared_weight_b128_bytes")
+    return w.value, s.value
+
+
+class PreparedWeightB128(PreparedWeight):
+    """An FP8 weight with an fp32 scale for each 128 x 128 block after the
+    one-time preparation (packed E4M3 payload, rows and K padded to 128, and
+    fp32 scales ``[ceil(N/128), ceil(K/128)]``)."""
+
+    def unpack(self):
+        raise NotImplementedError("128-block weights have no unpack entry")
+
+
+def _empty_b128(N, K, device):
+    wb, sb = mxfp8_prepared_weight_b128_bytes(N, K)
+    return PreparedWeightB128(torch.empty(wb, dtype=torch.uint8, device=device),
+                              torch.empty(sb // 4, dtype=torch.float32, device=device), N, K)
+
+
+def prepare_weight_b128(w_q, w_s, transpose=False):
+    """FP8 weight ``w_q`` E4M3 ``[N, K]`` (uint8 or float8_e4m3fn) with fp32
+    scales ``w_s`` ``[ceil(N/128), ceil(K/128)]`` -> PreparedWeightB128.
+    ``transpose``: of the transposed weight, for the input gradient
+    ``linear(dy, prepared)``."""
+    w_q = _as_bytes(w_q)
+    _require_cuda(w_q, "w_q")
+    _same_device(w_q, w_s)
+    N, K = w_q.shape
+    if w_s.dtype != torch.float32 or w_s.dim() != 2 or w_s.shape[0] < -(-N // 128) or w_s.shape[1] < -(-K // 128):
+        raise ValueError(f"w_s must be float32 [{-(-N // 128)}, {-(-K // 128)}]")
+    if w_q.stride(-1) != 1 or w_q.stride(0) % 16 != 0 or w_q.stride(0) < K or w_q.data_ptr() % 16 != 0:
+        w_q = w_q.clone(memory_format=torch.contiguous_format)
+    if w_s.stride(-1) != 1 or w_s.stride(0) < w_s.shape[1]:
+        w_s = w_s.contiguous()
+    with _on(w_q.device):
+        pw = _empty_b128(K, N, w_q.device) if transpose else _empty_b128(N, K, w_q.device)
+        _check(lib().mxfp8_prepare_weight_b128(_ptr(w_q), _ptr(w_s), N, K, w_q.stride(0), w_s.stride(0),
+                                               int(transpose), _ptr(pw.w_packed), _ptr(pw.s_packed),
+                                               _stream(w_q.device)), "mxfp8_prepare_weight_b128")
+    return pw
+
+
+def _linear_prepared_b128(x, pw, bias, out, workspace):
+    """``linear`` with a PreparedWeightB128."""
+    x2 = _rows(x, "x")
+    (M, K), N = x2.shape, pw.N
+    if K != pw.K:
+        raise ValueError(f"x has {K} columns, the weight {pw.K}")
+    bias = _bias(bias, N)
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    elif out.dtype != torch.bfloat16 or tuple(out.shape) != (M, N) or out.stride(1) != 1 or out.stride(0) < N:
+        raise ValueError(f"out must be bfloat16 [{M}, {N}] with contiguous rows that do not overlap")
+    _same_device(x2, pw.w_packed, bias, out, workspace)
+    with _on(x.device):
+        ws = workspace if workspace is not None else _scratch(mxfp8_linear_b128_workspace_bytes(M, N, K), x.device)
+        _check(mxfp8_linear_b128(_ptr(x2), M, K, x2.stride(0), _ptr(pw.w_packed), _ptr(pw.s_packed), N, _ptr(bias),
+                                 _ptr(out), out.stride(0), _ptr(ws), ws.numel(), _stream(x.device)),
+               "mxfp8_linear_b128")
+    return out.view(*x.shape[:-1], N)
+
+
+def quantize_weight_b128(w):
+    """bf16 ``w[N, K]`` (GPU) -> (E4M3 bytes uint8 ``[N, K]``, fp32 scales
+    ``[ceil(N/128), ceil(K/128)]``, powers of two)."""
+    w = _rows(w, "w")
+    N, K = w.shape
+    q = torch.empty((N, K), dtype=torch.uint8, device=w.device)
+    s = torch.empty((-(-N // 128), -(-K // 128)), dtype=torch.float32, device=w.device)
+    with _on(w.device):
+        _check(lib().mxfp8_quantize_weight_b128(_ptr(w), N, K, w.stride(0), _ptr(q), K, _ptr(s), s.shape[1], None,
+                                                None, None, None, _stream(w.device)), "mxfp8_quantize_weight_b128")
+    return q, s
+
+
+def prepare_weight_b128_bf16(w, transposed=True):
+    """bf16 ``w[N, K]`` -> (PreparedWeightB128 of w, PreparedWeightB128 of
+    w^T or None): ``quantize_weight_b128`` and ``prepare_weight_b128`` of both
+    orientations in one pass over the weight."""
+    w = _rows(w, "w")
+    N, K = w.shape
+    with _on(w.device):
+        pw = _empty_b128(N, K, w.device)
+        pt = _empty_b128(K, N, w.device) if transposed else None
+        _check(lib().mxfp8_quantize_weight_b128(_ptr(w), N, K, w.stride(0), None, 0, None, 0, _ptr(pw.w_packed),
+                                                _ptr(pw.s_packed), _ptr(pt.w_packed) if pt else None,
+                                                _ptr(pt.s_packed) if pt else None, _stream(w.device)),
+               "mxfp8_quantize_weight_b128")
+    return pw, pt
+
+
+def quantize_act_b128(x):
+    """bf16 ``x[..., K]`` (GPU, K % 16 == 0) -> (E4M3 bytes uint8 ``[M, K]``,
+    UE8M0 bytes uint8 ``[M, ceil(K/128)]``)."""
+    x2 = _rows(x, "x")
+    M, K = x2.shape
+    q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+    s = torch.empty((M, -(-K // 128)), dtype=torch.uint8, device=x.device)
+    with _on(x.device):
+        _check(lib().mxfp8_quantize_b128(_ptr(x2), M, K, x2.stride(0), _ptr(q), K, _ptr(s), s.shape[1],
+                                         _stream(x.device)), "mxfp8_quantize_b128")
+    return q, s
+
+
+def quantize_act_packed_b128(x):
+    """bf16 ``x[..., K]`` (GPU, K % 16 == 0) -> PackedActivation with a scale
+    per 128 elements: the operand of ``gemm_packed`` and, kept until the
+    backward pass, the 8-bit activation checkpoint ``linear_wgrad`` reads."""
+    x2 = _rows(x, "x")
+    M, K = x2.shape
+    q, s = _sz(), _sz()
+    _check(lib().mxfp8_packed_act_b128_bytes(max(M, 1), K, ctypes.byref(q), ctypes.byref(s)),
+           "mxfp8_packed_act_b128_bytes")
+    with _on(x.device):
+        qp = torch.empty(q.value if M else 0, dtype=torch.uint8, device=x.device)
+        sp = torch.empty(s.value if M else 0, dtype=torch.uint8, device=x.device)
+        _check(lib().mxfp8_quantize_act_packed_b128(_ptr(x2), M, K, x2.stride(0), _ptr(qp), _ptr(sp),
+                                                    _stream(x.device)), "mxfp8_quantize_act_packed_b128")
+    return PackedActivation(qp, sp, M, K, block=128)
+
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1}   # mxfp8_dtype
+
+
+def linear_wgrad(dy, pa, dtype=torch.float32, bias_grad=False, out=None, out_bias=None, accumulate=False):
+    """Weight gradient from the 8-bit activation checkpoint ``pa`` (a
+    PackedActivation of either quantizer): ``dw[N, K] = dy^T deq(pa)``.
+
+    ``dy`` bf16 ``[..., N]`` with M rows, N % 8 == 0.  Returns ``dw`` (``dtype``
+    float32 or bfloat16; ``out`` if given), or ``(dw, db)`` with ``bias_grad``,
+    ``db`` the fp32 column sums of dy (``out_bias`` if given).  ``accumulate``
+    adds to ``out`` (fp32) and ``out_bias`` instead of overwriting them."""
+    d2 = _rows(dy, "dy")
+    M, N = d2.shape
+    if M != pa.M:
+        raise ValueError(f"dy has {M} rows, the checkpoint {pa.M}")
+    if accumulate and (out is None or (bias_grad and out_bias is None)):
+        raise ValueError("accumulate needs the tensors to add to")
+    if out is None:
+        out = torch.empty((N, pa.K), dtype=dtype, device=dy.device)
+    if tuple(out.shape) != (N, pa.K) or out.dtype not in _DTYPES or out.stride(-1) != 1:
+        raise ValueError(f"out must be float32 or bfloat16 [{N}, {pa.K}] with contiguous rows")
+    if accumulate and out.dtype != torch.float32:
+        raise ValueError("accumulate needs a float32 out")
+    if bias_grad and out_bias is None:
+        out_bias = torch.empty(N, dtype=torch.float32, device=dy.device)
+    db = out_bias if bias_grad else None
+    if db is not None and (db.dtype != torch.float32 or tuple(db.shape) != (N,) or not db.is_contiguous()):
+        raise ValueError(f"out_bias must be contiguous float32 [{N}]")
+    _same_device(d2, pa.q_packed, out, db)
+    with _on(dy.device):
+        ws = _scratch(_bytes("mxfp8_linear_wgrad_workspace_bytes", M, N, pa.K), dy.device)
+        _check(lib().mxfp8_linear_wgrad(_ptr(d2), M, N, d2.stride(0), _ptr(pa.q_packed), _ptr(pa.s_packed), pa.K,
+                                        _ptr(out), _DTYPES[out.dtype], out.stride(0), _ptr(db), int(accumulate),
+                                        _ptr(ws), ws.numel(), _stream(dy.device)), "mxfp8_linear_wgrad")
+    return (out, db) if bias_grad else out
+
+
+class _LinearB128(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, bias):
+        pw, pt = prepare_weight_b128_bf16(w, transposed=x.requires_grad)
+        ctx.shape, ctx.pt, ctx.pa = x.shape, pt, None
+        ctx.types = w.dtype, None if bias is None else bias.dtype
+        if w.requires_grad or (bias is not None and bias.requires_grad):
+            ctx.pa = quantize_act_packed_b128(x)
+            y = gemm_packed(ctx.pa, pw, bias)
+        else:
+            y = linear(x.reshape(-1, x.shape[-1]), pw, bias)
+        return y.view(*x.shape[:-1], pw.N)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        d2 = _rows(dy, "dy")
+        dx = dw = db = None
+        if ctx.needs_input_grad[0]:
+            dx = linear(d2, ctx.pt).view(ctx.shape)
+        if ctx.needs_input_grad[1] or ctx.needs_input_grad[2]:
+            want = ctx.needs_input_grad[2]
+            got = linear_wgrad(d2, ctx.pa, dtype=ctx.types[0], bias_grad=want)
+            dw, db = got if want else (got, None)
+            db = None if db is None else db.to(ctx.types[1])
+        return dx, dw if ctx.needs_input_grad[1] else None, db
+
+
+def linear_b128(x, w, bias=None):
+    """The 128-block FP8 linear layer from a bf16 weight, with gradients:
+    ``y = bf16(deq(q(x)) @ deq(q(w)).T + bias)``, x ``[..., K]``, w ``[N, K]``,
+    bias ``[N]``, all bf16; N and K multiples of 16.
+
+    The forward pass quantizes the weight (one pass, both orientations) and
+    keeps the activations as the 8-bit checkpoint its GEMM reads.  Backward:
+    ``dx = deq(q(dy)) @ deq(q(w))``, dy quantized like activations;
+    ``dw = dy^T @ deq(q(x))`` and ``db`` from bf16 dy.  The quantizations
+    are passed straight through."""
+    for t, name in ((x, "x"), (w, "w")) + (((bias, "bias"),) if bias is not None else ()):
+        if t.dtype != torch.bfloat16:
+            raise ValueError(f"{name} must be bfloat16, got {t.dtype}")
+        _require_cuda(t, name)
+    if w.dim() != 2 or x.shape[-1] != w.shape[1] or w.shape[0] % 16 or w.shape[1] % 16:
+        raise ValueError(f"x [..., K] and w [N, K] with N and K multiples of 16, got {tuple(x.shape)}, {tuple(w.shape)}")
+    _same_device(x, w, bias)
+    return _LinearB128.apply(x, w, bias)
 
 
 # ---------------------------------------------------------------------------
@@ -559,3 +878,84 @@ def moe_debug_capture(act=None, q=None, s=None, ids=None, wts=None):
     the routed expert (int32 ``[T*k]``) and routing weight (fp32 ``[T*k]``) of
     later MoE calls; no arguments turns it off."""
     _check(mxfp8_moe_debug_capture(_ptr(act), _ptr(q), _ptr(s), _ptr(ids), _ptr(wts)), "mxfp8_moe_debug_capture")
+
+
+def _router_args(logits, valid):
+    if logits.dtype not in _DTYPES or logits.dim() != 2:
+        raise ValueError(f"logits must be float32 or bfloat16 [T, E], got {logits.dtype} {tuple(logits.shape)}")
+    _require_cuda(logits, "logits")
+    if logits.stride(-1) != 1 or logits.stride(0) < logits.shape[1]:
+        logits = logits.contiguous()
+    if valid is not None:
+        if valid.dtype not in (torch.bool, torch.uint8) or tuple(valid.shape) != (logits.shape[0],):
+            raise ValueError(f"valid must be bool or uint8 [{logits.shape[0]}]")
+        valid = valid.contiguous()
+        _same_device(logits, valid)
+    return logits, valid
+
+
+def moe_balance(logits, topk, valid=None, coef=1e-2, z_coef=0.0):
+    """Load-balance and z loss of the router of ``moe_grouped``: ``(loss,
+    counts, used)``, fp32 scalar, int32 ``[E]`` tokens of each expert, int32
+    ``[1]`` tokens counted.
+
+    ``loss = coef E / (topk n^2) sum_e counts[e] sum_t softmax(logits)[t, e] +
+    z_coef / n sum_t logsumexp(logits[t])^2`` over the n tokens with ``valid``
+    set and a logit other than -inf.  ``logits`` ``[T, E]`` fp32 or bf16; the
+    gradient is ``moe_balance_backward``'s (``moe_balance_loss`` for autograd)."""
+    logits, valid = _router_args(logits, valid)
+    T, E = logits.shape
+    d = logits.device
+    with _on(d):
+        loss = torch.empty((), dtype=torch.float32, device=d)
+        counts = torch.empty(E, dtype=torch.int32, device=d)
+        used = torch.empty(1, dtype=torch.int32, device=d)
+        ws = _scratch(_bytes("mxfp8_moe_balance_workspace_bytes", T, E), d)
+        _check(lib().mxfp8_moe_balance(_ptr(logits), _DTYPES[logits.dtype], T, E, logits.stride(0), topk,
+                                       _ptr(valid), coef, z_coef, _ptr(loss), _ptr(counts), _ptr(used), _ptr(ws),
+                                       ws.numel(), _stream(d)), "mxfp8_moe_balance")
+    return loss, counts, used
+
+
+def moe_balance_backward(logits, topk, counts, used, valid=None, coef=1e-2, z_coef=0.0, grad=None):
+    """Gradient of ``moe_balance``'s loss with respect to the logits (their
+    shape and type), counts held constant.  ``counts`` and ``used`` as
+    ``moe_balance`` returned them, or summed over data-parallel ranks;
+    ``grad``: fp32 GPU scalar that multiplies it (None: 1)."""
+    logits, valid = _router_args(logits, valid)
+    T, E = logits.shape
+    if counts.dtype != torch.int32 or counts.shape != (E,) or used.dtype != torch.int32 or used.numel() != 1:
+        raise ValueError(f"counts must be int32 [{E}] and used int32 [1]")
+    if grad is not None and (grad.dtype != torch.float32 or grad.numel() != 1):
+        raise ValueError("grad must be one float32")
+    counts = counts.contiguous()
+    _same_device(logits, counts, used, grad)
+    with _on(logits.device):
+        d = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+        _check(lib().mxfp8_moe_balance_backward(_ptr(logits), _DTYPES[logits.dtype], T, E, logits.stride(0), topk,
+                                                _ptr(valid), coef, z_coef, _ptr(counts), _ptr(used), _ptr(grad),
+                                                _ptr(d), E, _stream(logits.device)), "mxfp8_moe_balance_backward")
+    return d
+
+
+class _MoEBalance(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, topk, valid, coef, z_coef):
+        loss, counts, used = moe_balance(logits, topk, valid, coef, z_coef)
+        ctx.save_for_backward(logits, counts, used, valid)
+        ctx.args = topk, coef, z_coef
+        ctx.mark_non_differentiable(counts)
+        return loss, counts
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad, _):
+        logits, counts, used, valid = ctx.saved_tensors
+        topk, coef, z_coef = ctx.args
+        return moe_balance_backward(logits, topk, counts, used, valid, coef, z_coef, grad), None, None, None, None
+
+
+def moe_balance_loss(logits, topk, valid=None, coef=1e-2, z_coef=0.0):
+    """``moe_balance`` for autograd: ``(loss, counts)``, the loss
+    differentiable with respect to ``logits``."""
+    return _MoEBalance.apply(logits, topk, valid, coef, z_coef)

@@ -1,0 +1,327 @@
+// C ABI (include/mxfp8.h) of the 128-block FP8 layer, the weight gradient
+// from 8-bit activation checkpoints and the router's balance loss: argument
+// validation on the host, device check, launches.  Nothing here allocates
+// device memory or synchronizes.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "launch_b128.hpp"
+#include "mxfp8.h"
+
+namespace {
+
+using mxfp8::b128_blocks;
+
+bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+
+constexpr int64_t kMaxRows = (int64_t)1 << 30, kMaxK = (int64_t)1 << 24;
+
+// A blocked axis that is summed over: 16-byte chunks of E4M3 bytes, 32-bit
+// offsets inside a packed 128-row group.
+bool summed_ok(int64_t K) { return K >= 16 && K % 16 == 0 && K <= kMaxK; }
+bool rows_ok(int64_t N) { return N >= 1 && N <= kMaxRows; }
+// Workgroup count of a launch with one workgroup per 128 x 128 tile.
+bool tiles_ok(int64_t N, int64_t K) { return b128_blocks(N) * b128_blocks(K) <= INT32_MAX; }
+bool act_grid_ok(int64_t M, int64_t K) {
+  return b128_blocks(M) * b128_blocks(K) * 8 <= INT32_MAX;   // packed quantizer: bands x 128-blocks at most
+}
+
+size_t act_bytes(int64_t M, int64_t K) { return (size_t)b128_blocks(M) * 128 * (size_t)b128_blocks(K) * 128; }
+size_t act_scale_bytes(int64_t M, int64_t K) { return act_bytes(M, K) / 32; }
+
+int check_weight(const void* wp, const void* sp, int64_t N, int64_t K) {
+  if (!wp || !sp) return MXFP8_E_NULLPTR;
+  if (!rows_ok(N) || !summed_ok(K)) return MXFP8_E_SHAPE;
+  if (!aligned(wp, 256) || !aligned(sp, 256)) return MXFP8_E_ALIGN;
+  return MXFP8_OK;
+}
+
+int check_out(const void* y, int64_t N, int64_t ldy, const void* bias) {
+  if (!y) return MXFP8_E_NULLPTR;
+  if (ldy < N) return MXFP8_E_LD;
+  if (!aligned(y, 2) || (bias && !aligned(bias, 2))) return MXFP8_E_ALIGN;
+  return MXFP8_OK;
+}
+
+// The tile GEMM's grid and the split-K reduce's (one thread per 4 outputs)
+// in 32-bit range.
+bool gemm_grid_ok(int64_t M, int64_t N) {
+  return b128_blocks(N) * ((M + 63) / 64) * mxfp8::kMaxSplitK <= INT32_MAX && M * ((N + 3) / 4) / 256 < INT32_MAX;
+}
+
+size_t part_bytes(int64_t M, int64_t N, mxfp8::B128Plan p) {
+  return p.splits > 1 ? round_up((size_t)p.splits * (size_t)M * (size_t)((N + 3) / 4 * 4) * 4, 256) : 0;
+}
+
+size_t linear_ws(int64_t M, int64_t N, int64_t K) {
+  if (M <= mxfp8::kB128DecodeMaxM) return 256;
+  return round_up(act_bytes(M, K), 256) + round_up(act_scale_bytes(M, K), 256) +
+         part_bytes(M, N, mxfp8::b128_plan(M, N, K));
+}
+
+int check_logits(const void* logits, int dtype, int64_t T, int64_t E, int64_t ldl, int64_t topk) {
+  if (T < 0 || T > ((int64_t)1 << 31) - 1 || E < 1 || E > mxfp8::kMoeMaxExperts || topk < 1 || topk > E ||
+      topk > mxfp8::kMoeMaxTopk || (dtype != MXFP8_F32 && dtype != MXFP8_BF16))
+    return MXFP8_E_SHAPE;
+  if (T == 0) return MXFP8_OK;
+  if (!logits) return MXFP8_E_NULLPTR;
+  if (ldl < E) return MXFP8_E_LD;
+  if (!aligned(logits, dtype == MXFP8_F32 ? 4 : 2)) return MXFP8_E_ALIGN;
+  return MXFP8_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int mxfp8_quantize_b128(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, void* q_e4m3, int64_t ldq,
+                        void* s_e8m0, int64_t lds, void* stream) {
+  if (M < 0 || M > kMaxRows || !summed_ok(K)) return MXFP8_E_SHAPE;
+  if (M == 0) return MXFP8_OK;
+  if (!x_bf16 || !q_e4m3 || !s_e8m0) return MXFP8_E_NULLPTR;
+  if (ldx < K || ldx % 8 != 0 || ldq < K || ldq % 16 != 0 || lds < b128_blocks(K)) return MXFP8_E_LD;
+  if (!aligned(x_bf16, 16) || !aligned(q_e4m3, 16)) return MXFP8_E_ALIGN;
+  if (M * b128_blocks(K) / 16 >= INT32_MAX) return MXFP8_E_SHAPE;
+  if (int st = mxfp8::check_device_current()) return st;
+  return mxfp8::launch_quantize_b128(x_bf16, M, K, ldx, q_e4m3, ldq, s_e8m0, lds, (hipStream_t)stream);
+}
+
+int mxfp8_packed_act_b128_bytes(int64_t M, int64_t K, size_t* q_bytes, size_t* s_bytes) {
+  if (!q_bytes || !s_bytes) return MXFP8_E_NULLPTR;
+  if (!rows_ok(M) || !summed_ok(K)) return MXFP8_E_SHAPE;
+  *q_bytes = act_bytes(M, K);
+  *s_bytes = act_scale_bytes(M, K);
+  return MXFP8_OK;
+}
+
+int mxfp8_quantize_act_packed_b128(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, void* q_packed,
+                                   void* s_packed, void* stream) {
+  if (M < 0 || M > kMaxRows || !summed_ok(K)) return MXFP8_E_SHAPE;
+  if (M == 0) return MXFP8_OK;
+  if (!x_bf16 || !q_packed || !s_packed) return MXFP8_E_NULLPTR;
+  if (ldx < K || ldx % 8 != 0) return MXFP8_E_LD;
+  if (!aligned(x_bf16, 16) || !aligned(q_packed, 256) || !aligned(s_packed, 256)) return MXFP8_E_ALIGN;
+  if (!act_grid_ok(M, K)) return MXFP8_E_SHAPE;
+  if (int st = mxfp8::check_device_current()) return st;
+  return mxfp8::launch_quantize_packed_b128(x_bf16, M, K, ldx, q_packed, s_packed, (hipStream_t)stream);
+}
+
+int mxfp8_dequantize_act_packed(const void* q_packed, const void* s_packed, int64_t M, int64_t K, void* x_bf16,
+                                int64_t ldx, void* stream) {
+  if (M < 0 || M > kMaxRows || !summed_ok(K)) return MXFP8_E_SHAPE;
+  if (M == 0) return MXFP8_OK;
+  if (!q_packed || !s_packed || !x_bf16) return MXFP8_E_NULLPTR;
+  if (ldx < K || ldx % 8 != 0) return MXFP8_E_LD;
+  if (!aligned(x_bf16, 16) || !aligned(q_packed, 256) || !aligned(s_packed, 256)) return MXFP8_E_ALIGN;
+  if (M * (K / 16) / 256 >= INT32_MAX) return MXFP8_E_SHAPE;
+  if (int st = mxfp8::check_device_current()) return st;
+  return mxfp8::launch_dequantize_packed(q_packed, s_packed, M, K, x_bf16, ldx, (hipStream_t)stream);
+}
+
+int mxfp8_prepared_weight_b128_bytes(int64_t N, int64_t K, size_t* w_bytes, size_t* s_bytes) {
+  if (!w_bytes || !s_bytes) return MXFP8_E_NULLPTR;
+  if (!rows_ok(N) || !summed_ok(K)) return MXFP8_E_SHAPE;
+  *w_bytes = act_bytes(N, K);
+  *s_bytes = (size_t)b128_blocks(N) * (size_t)b128_blocks(K) * 4;
+  return MXFP8_OK;
+}
+
+int mxfp8_prepare_weight_b128(const void* w_e4m3, const float* w_s, int64_t N, int64_t K, int64_t ldw, int64_t lds,
+                              int transpose, void* w_packed, void* s_packed, void* stream) {
+  if (!summed_ok(K) || (transpose ? !summed_ok(N) : !rows_ok(N))) return MXFP8_E_SHAPE;
+  if (!w_e4m3 || !w_s || !w_packed || !s_packed) return MXFP8_E_NULLPTR;
+  if (ldw < K || ldw % 16 != 0 || lds < b128_blocks(K)) return MXFP8_E_LD;
+  if (!aligned(w_e4m3, 16) || !aligned(w_s, 4) || !aligned(w_packed, 256) || !aligned(s_packed, 256))
+    return MXFP8_E_ALIGN;
+  if (!tiles_ok(N, K)) return MXFP8_E_SHAPE;
+  if (int st = mxfp8::check_device_current()) return st;
+  return mxfp8::launch_pack_b128(w_e4m3, w_s, N, K, ldw, lds, transpose, w_packed, s_packed, (hipStream_t)stream);
+}
+
+int mxfp8_quantize_weight_b128(const void* w_bf16, int64_t N, int64_t K, int64_t ldw, void* q_e4m3, int64_t ldq,
+                               float* s, int64_t lds, void* w_packed, void* s_packed, void* wt_packed,
+                               void* st_packed, void* stream) {
+  if (!summed_ok(K) || (wt_packed ? !summed_ok(N) : !rows_ok(N))) return MXFP8_E_SHAPE;
+  if (!w_bf16 || (!q_e4m3 != !s) || (!w_packed != !s_packed) || (!wt_packed != !st_packed)) return MXFP8_E_NULLPTR;
+  if (!q_e4m3 && !w_packed && !wt_packed) return MXFP8_E_NULLPTR;
+  if (ldw < K || ldw % 8 != 0) return MXFP8_E_LD;
+  if (q_e4m3 && (ldq < K || ldq % 16 != 0 || lds < b128_blocks(K))) return MXFP8_E_LD;
+  if (!aligned(w_bf16, 16) || !aligned(q_e4m3, 16) || !aligned(s, 4)) return MXFP8_E_ALIGN;
+  if (!aligned(w_packed, 256) || !aligned(s_packed, 256) || !aligned(wt_packed, 256) || !aligned(st_packed, 256))
+    return MXFP8_E_ALIGN;
+  if (!tiles_ok(N, K)) return MXFP8_E_SHAPE;
+  if (int st = mxfp8::check_device_current()) return st;
+  return mxfp8::launch_quantize_weight_b128(w_bf16, N, K, ldw, q_e4m3, ldq, s, lds, w_packed, s_packed, wt_packed,
+                                            st_packed, (hipStream_t)stream);
+}
+
+int mxfp8_linear_b128_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  if (!bytes) return MXFP8_E_NULLPTR;
+  if (M < 0 || M > kMaxRows || !rows_ok(N) || !summed_ok(K)) return MXFP8_E_SHAPE;
+  *bytes = linear_ws(M, N, K);
+  return MXFP8_OK;
+}
+
+int mxfp8_linear_b128(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, const void* w_packed,
+                      const void* s_packed, int64_t N, const void* bias_bf16, void* y_bf16, int64_t ldy,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  if (M < 0 || M > kMaxRows) return MXFP8_E_SHAPE;
+  if (int st = check_weight(w_packed, s_packed, N, K)) return st;
+  if (M == 0) return MXFP8_OK;
+  if (!x_bf16) return MXFP8_E_NULLPTR;
+  if (int st = check_out(y_bf16, N, ldy, bias_bf16)) return st;
+  if (ldx < K || ldx % 8 != 0) return MXFP8_E_LD;
+  if (!aligned(x_bf16, 16)) return MXFP8_E_ALIGN;
+  if (!gemm_grid_ok(M, N) || !act_grid_ok(M, K)) return MXFP8_E_SHAPE;
+  if (!workspace || workspace_bytes < linear_ws(M, N, K)) return MXFP8_E_WORKSPACE;
+  if (!aligned(workspace, 256)) return MXFP8_E_ALIGN;
+  if (int st = mxfp8::check_device_current()) return st;
+  hipStream_t s = (hipStream_t)stream;
+  const float* wsc = (const float*)s_packed;
+  if (M <= mxfp8::kB128DecodeMaxM)
+    return mxfp8::launch_gemm_b128_decode(x_bf16, ldx, M, K, w_packed, wsc, N, bias_bf16, y_bf16, ldy, s);
+  uint8_t* q = (uint8_t*)workspace;
+  uint8_t* sc = q + round_up(act_bytes(M, K), 256);
+  uint8_t* part = sc + round_up(act_scale_bytes(M, K), 256);
+  if (int st = mxfp8::launch_quantize_packed_b128(x_bf16, M, K, ldx, q, sc, s)) return st;
+  return mxfp8::launch_gemm_b128_tile(q, sc, M, K, w_packed, wsc, N, bias_bf16, y_bf16, ldy, s,
+                                      mxfp8::b128_plan(M, N, K), part);
+}
+
+int mxfp8_gemm_packed_b128_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  if (!bytes) return MXFP8_E_NULLPTR;
+  if (M < 0 || M > kMaxRows || !rows_ok(N) || !summed_ok(K)) return MXFP8_E_SHAPE;
+  const size_t b = M == 0 ? 0 : part_bytes(M, N, mxfp8::b128_plan(M, N, K));
+  *bytes = b > 256 ? b : 256;
+  return MXFP8_OK;
+}
+
+int mxfp8_gemm_packed_b128(const void* q_packed, const void* s_packed, int64_t M, int64_t K, const void* w_packed,
+                           const void* ws_packed, int64_t N, const void* bias_bf16, void* y_bf16, int64_t ldy,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  if (M < 0 || M > kMaxRows) return MXFP8_E_SHAPE;
+  if (int st = check_weight(w_packed, ws_packed, N, K)) return st;
+  if (M == 0) return MXFP8_OK;
+  if (!q_packed || !s_packed) return MXFP8_E_NULLPTR;
+  if (int st = check_out(y_bf16, N, ldy, bias_bf16)) return st;
+  if (!aligned(q_packed, 256) || !aligned(s_packed, 256)) return MXFP8_E_ALIGN;
+  if (!gemm_grid_ok(M, N)) return MXFP8_E_SHAPE;
+  size_t need = 0;
+  mxfp8_gemm_packed_b128_workspace_bytes(M, N, K, &need);
+  if (!workspace || workspace_bytes < need) return MXFP8_E_WORKSPACE;
+  if (!aligned(workspace, 256)) return MXFP8_E_ALIGN;
+  if (int st = mxfp8::check_device_current()) return st;
+  return mxfp8::launch_gemm_b128_tile(q_packed, s_packed, M, K, w_packed, (const float*)ws_packed, N, bias_bf16,
+                                      y_bf16, ldy, (hipStream_t)stream, mxfp8::b128_plan(M, N, K), workspace);
+}
+
+int mxfp8_linear_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  if (!bytes) return MXFP8_E_NULLPTR;
+  if (M < 0 || M > kMaxRows || !rows_ok(N) || N % 8 != 0 || !summed_ok(K)) return MXFP8_E_SHAPE;
+  const mxfp8::WgradPlan p = mxfp8::wgrad_plan(M, N, K);
+  *bytes = round_up(mxfp8::wgrad_dw_bytes(N, K, p), 256) + round_up(mxfp8::wgrad_db_bytes(N, K, p), 256);
+  return MXFP8_OK;
+}
+
+int mxfp8_linear_wgrad(const void* dy_bf16, int64_t M, int64_t N, int64_t lddy, const void* q_packed,
+                       const void* s_packed, int64_t K, void* dw, int dw_dtype, int64_t lddw, float* db,
+                       int accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+  if (M < 0 || M > kMaxRows || !rows_ok(N) || N % 8 != 0 || !summed_ok(K)) return MXFP8_E_SHAPE;
+  if ((dw_dtype != MXFP8_F32 && dw_dtype != MXFP8_BF16) || (accumulate && dw_dtype != MXFP8_F32)) return MXFP8_E_SHAPE;
+  if (!dw || (M > 0 && (!dy_bf16 || !q_packed || !s_packed))) return MXFP8_E_NULLPTR;
+  if (lddw < K || lddw % 8 != 0) return MXFP8_E_LD;
+  // 64 rows of dY are addressed with 32-bit byte offsets.
+  if (M > 0 && (lddy < N || lddy % 8 != 0 || lddy > kMaxK)) return MXFP8_E_LD;
+  if (!aligned(dw, 16) || !aligned(db, 4)) return MXFP8_E_ALIGN;
+  if (M > 0 && (!aligned(dy_bf16, 16) || !aligned(q_packed, 256) || !aligned(s_packed, 256))) return MXFP8_E_ALIGN;
+  const mxfp8::WgradPlan p = mxfp8::wgrad_plan(M, N, K);
+  if (b128_blocks(N) * b128_blocks(K) * p.splits > INT32_MAX || N * (K / 4) / 256 >= INT32_MAX - N)
+    return MXFP8_E_SHAPE;
+  size_t need = 0;
+  mxfp8_linear_wgrad_workspace_bytes(M, N, K, &need);
+  if (!workspace || workspace_bytes < need) return MXFP8_E_WORKSPACE;
+  if (!aligned(workspace, 256)) return MXFP8_E_ALIGN;
+  if (int st = mxfp8::check_device_current()) return st;
+  mxfp8::WgradArgs a;
+  a.dy = dy_bf16;
+  a.M = M;
+  a.N = N;
+  a.lddy = lddy;
+  a.qp = q_packed;
+  a.sp = s_packed;
+  a.K = K;
+  a.dw = dw;
+  a.lddw = lddw;
+  a.out_bf16 = dw_dtype == MXFP8_BF16;
+  a.accumulate = accumulate != 0;
+  a.db = db;
+  a.part_dw = (float*)workspace;
+  a.part_db = (float*)((uint8_t*)workspace + round_up(mxfp8::wgrad_dw_bytes(N, K, p), 256));
+  return mxfp8::launch_wgrad(a, p, (hipStream_t)stream);
+}
+
+int mxfp8_moe_balance_workspace_bytes(int64_t T, int64_t E, size_t* bytes) {
+  if (!bytes) return MXFP8_E_NULLPTR;
+  if (T < 0 || E < 1 || E > mxfp8::kMoeMaxExperts) return MXFP8_E_SHAPE;
+  *bytes = mxfp8::balance_ws_bytes(T, E);
+  return MXFP8_OK;
+}
+
+int mxfp8_moe_balance(const void* logits, int dtype, int64_t T, int64_t E, int64_t ldl, int64_t topk,
+                      const uint8_t* valid, float coef, float z_coef, float* loss, int* counts, int* used,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  if (int st = check_logits(logits, dtype, T, E, ldl, topk)) return st;
+  if (!loss || !counts || !used) return MXFP8_E_NULLPTR;
+  if (!aligned(loss, 4) || !aligned(counts, 4) || !aligned(used, 4)) return MXFP8_E_ALIGN;
+  if (!workspace || workspace_bytes < mxfp8::balance_ws_bytes(T, E)) return MXFP8_E_WORKSPACE;
+  if (!aligned(workspace, 256)) return MXFP8_E_ALIGN;
+  if (int st = mxfp8::check_device_current()) return st;
+  mxfp8::BalanceArgs a = {};
+  a.logits = logits;
+  a.bf16 = dtype == MXFP8_BF16;
+  a.T = T;
+  a.E = E;
+  a.ldl = ldl;
+  a.topk = topk;
+  a.valid = valid;
+  a.coef = coef;
+  a.z_coef = z_coef;
+  a.counts = counts;
+  a.used = used;
+  a.loss = loss;
+  a.ws = workspace;
+  return mxfp8::launch_balance(a, (hipStream_t)stream);
+}
+
+int mxfp8_moe_balance_backward(const void* logits, int dtype, int64_t T, int64_t E, int64_t ldl, int64_t topk,
+                               const uint8_t* valid, float coef, float z_coef, const int* counts, const int* used,
+                               const float* grad_loss, void* dlogits, int64_t ldd, void* stream) {
+  if (int st = check_logits(logits, dtype, T, E, ldl, topk)) return st;
+  if (T == 0) return MXFP8_OK;
+  if (!counts || !used || !dlogits) return MXFP8_E_NULLPTR;
+  if (ldd < E) return MXFP8_E_LD;
+  if (!aligned(dlogits, dtype == MXFP8_F32 ? 4 : 2) || !aligned(counts, 4) || !aligned(used, 4) ||
+      !aligned(grad_loss, 4))
+    return MXFP8_E_ALIGN;
+  if (int st = mxfp8::check_device_current()) return st;
+  mxfp8::BalanceArgs a = {};
+  a.logits = logits;
+  a.bf16 = dtype == MXFP8_BF16;
+  a.T = T;
+  a.E = E;
+  a.ldl = ldl;
+  a.topk = topk;
+  a.valid = valid;
+  a.coef = coef;
+  a.z_coef = z_coef;
+  a.counts = const_cast<int*>(counts);
+  a.used = const_cast<int*>(used);
+  a.grad_loss = grad_loss;
+  a.dlogits = dlogits;
+  a.ldd = ldd;
+  return mxfp8::launch_balance_backward(a, (hipStream_t)stream);
+}
+
+}  // extern "C"

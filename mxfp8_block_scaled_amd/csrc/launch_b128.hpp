@@ -1,0 +1,119 @@
+// Internal launchers of the 128-block FP8 layer, the weight gradient from
+// 8-bit activation checkpoints and the router's balance loss.  As in
+// launch.hpp, arguments were validated by the C entry points (api_b128.cpp),
+// and each returns 0 or -7 (launch error).
+#pragma once
+
+#include "common.hpp"
+#include "launch.hpp"
+
+namespace mxfp8 {
+
+constexpr int64_t kB128 = 128;   // elements of a scale block along each blocked axis
+__host__ __device__ inline int64_t b128_blocks(int64_t n) { return (n + kB128 - 1) / kB128; }
+
+// Scale byte of a 128-block from the bf16 bits of its largest magnitude (the
+// rule is stated in quant_b128.hip).
+__device__ inline uint32_t b128_scale_byte(uint32_t amax) {
+  const int f = (int)(amax >> 7), up = (int)(amax & 0x7Fu) > 96 ? 1 : 0;
+  return amax >= 0x7F80u ? 0xFFu : (uint32_t)max(f - 8 + up, 0);
+}
+// Its value, with the UE8M0 NaN as an fp32 NaN.
+__device__ inline float b128_scale_value(uint32_t sb) {
+  return __uint_as_float(sb == 0xFFu ? 0x7FC00000u : sb ? sb << 23 : 0x00400000u);
+}
+
+// Sixteen E4M3 bytes of one scale -> sixteen bf16, two 16-byte words.
+__device__ inline void widen16(const uint4& q, float scale, uint4* out) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  uint32_t d[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    d[2 * e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[e], scale, false));
+    d[2 * e + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[e], scale, true));
+  }
+  out[0] = make_uint4(d[0], d[1], d[2], d[3]);
+  out[1] = make_uint4(d[4], d[5], d[6], d[7]);
+}
+
+// x bf16 [M, K] (K % 16 == 0) -> E4M3 [M, K] + UE8M0 [M, ceil(K / 128)].
+int launch_quantize_b128(const void* x, int64_t M, int64_t K, int64_t ldx, void* q, int64_t ldq, void* s, int64_t lds,
+                         hipStream_t stream);
+// The same in the packed operand layout (rows padded to 128, K to 128).
+int launch_quantize_packed_b128(const void* x, int64_t M, int64_t K, int64_t ldx, void* qp, void* sp,
+                                hipStream_t stream);
+// Packed activations (either scale block) -> bf16 [M, K].
+int launch_dequantize_packed(const void* qp, const void* sp, int64_t M, int64_t K, void* x, int64_t ldx,
+                             hipStream_t stream);
+// E4M3 [N, K] + fp32 [ceil(N / 128), ceil(K / 128)] -> the packed weight (of
+// its transpose if `transpose`) and its scales, one per (128-row group, block).
+int launch_pack_b128(const void* w, const void* ws, int64_t N, int64_t K, int64_t ldw, int64_t ldws, int transpose,
+                     void* wp, void* sp, hipStream_t stream);
+// bf16 weight [N, K] -> any of row-major (q, s), packed (wp, sp) and packed
+// transposed (wtp, stp); null outputs are skipped.
+int launch_quantize_weight_b128(const void* w, int64_t N, int64_t K, int64_t ldw, void* q, int64_t ldq, void* s,
+                                int64_t lds, void* wp, void* sp, void* wtp, void* stp, hipStream_t stream);
+
+// Decode GEMM: M <= 16 bf16 rows, quantized inside, against the packed weight.
+constexpr int64_t kB128DecodeMaxM = 16;
+int launch_gemm_b128_decode(const void* x, int64_t ldx, int64_t M, int64_t K, const void* wp, const float* wsc,
+                            int64_t N, const void* bias, void* y, int64_t ldy, hipStream_t stream);
+
+// Tile GEMM on packed activations.  splits > 1 cuts K into that many runs of
+// 128-blocks, whose fp32 partials go to `part` (splits * M * round_up(N, 4)
+// floats) and are added in order by launch_splitk_reduce.
+struct B128Plan {
+  int mt;       // activation rows per tile: 64, 128 or 256
+  int splits;
+};
+B128Plan b128_plan(int64_t M, int64_t N, int64_t K);
+int launch_gemm_b128_tile(const void* qp, const void* sp, int64_t M, int64_t K, const void* wp, const float* wsc,
+                          int64_t N, const void* bias, void* y, int64_t ldy, hipStream_t stream, B128Plan plan,
+                          void* part);
+
+// Weight gradient dW[n, k] = sum_m dY[m, n] X[m, k] from packed 8-bit
+// activations (either scale block), and db[n] = sum_m dY[m, n].
+struct WgradPlan {
+  int tile;     // edge of a workgroup's dW tile: 128 or 256
+  int splits;   // runs of 64 rows each workgroup's M is cut into
+};
+WgradPlan wgrad_plan(int64_t M, int64_t N, int64_t K);
+// fp32 partials: dW [splits][N][K] (splits > 1), then db [splits * tiles_k][N].
+size_t wgrad_dw_bytes(int64_t N, int64_t K, WgradPlan p);
+size_t wgrad_db_bytes(int64_t N, int64_t K, WgradPlan p);
+struct WgradArgs {
+  const void* dy;       // bf16 [M, N], row stride lddy
+  int64_t M, N, lddy;
+  const void* qp;       // packed activations [M, K] and their scales
+  const void* sp;
+  int64_t K;
+  void* dw;             // [N, K], row stride lddw: fp32, or bf16 if out_bf16
+  int64_t lddw;
+  int out_bf16;
+  int accumulate;       // dw += and db += (dw fp32)
+  float* db;            // [N] or null
+  float* part_dw;
+  float* part_db;
+};
+int launch_wgrad(const WgradArgs& a, WgradPlan p, hipStream_t stream);
+
+// Load-balance and z loss of a router (balance.hip).
+struct BalanceArgs {
+  const void* logits;      // [T, E] fp32 or bf16, row stride ldl
+  int bf16;
+  int64_t T, E, ldl, topk;
+  const uint8_t* valid;    // [T] or null
+  float coef, z_coef;
+  int* counts;             // [E]
+  int* used;               // [1]
+  float* loss;             // [1] (forward)
+  const float* grad_loss;  // [1] or null (= 1)
+  void* dlogits;           // [T, E], type of logits, row stride ldd (backward)
+  int64_t ldd;
+  void* ws;                // forward partials
+};
+size_t balance_ws_bytes(int64_t T, int64_t E);
+int launch_balance(const BalanceArgs& a, hipStream_t stream);
+int launch_balance_backward(const BalanceArgs& a, hipStream_t stream);
+
+}  // namespace mxfp8
