@@ -423,6 +423,15 @@ int mxfp8_gemm_packed_b128(const void* q_packed, const void* s_packed, int64_t M
                            void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Test hook: pin the tiles of the 128-block GEMM (M > 16 and the packed
+ * entry): 0 = by shape, 64 / 128 = 128 columns x that many rows (with K
+ * splits), 256 = 256 x 128 tiles where the shape allows (K > 384, N % 8 == 0,
+ * y 16-byte aligned with ldy % 8 == 0), else 128.  The workspace queries
+ * follow it.  Process-wide; returns the previous value, or MXFP8_E_SHAPE.
+ */
+int mxfp8_debug_force_b128(int tile);
+
+/*
  * Weight and bias gradient of a linear layer from its 8-bit activation
  * checkpoint:
  *   dw[n, k] = sum_m dy[m, n] * deq(X)[m, k],   db[n] = sum_m dy[m, n]

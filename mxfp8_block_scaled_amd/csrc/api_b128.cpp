@@ -217,6 +217,11 @@ int mxfp8_gemm_packed_b128(const void* q_packed, const void* s_packed, int64_t M
                                       y_bf16, ldy, (hipStream_t)stream, mxfp8::b128_plan(M, N, K), workspace);
 }
 
+int mxfp8_debug_force_b128(int tile) {
+  if (tile != 0 && tile != 64 && tile != 128 && tile != 256) return MXFP8_E_SHAPE;
+  return mxfp8::b128_force(tile);
+}
+
 int mxfp8_linear_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes) {
   if (!bytes) return MXFP8_E_NULLPTR;
   if (M < 0 || M > kMaxRows || !rows_ok(N) || N % 8 != 0 || !summed_ok(K)) return MXFP8_E_SHAPE;

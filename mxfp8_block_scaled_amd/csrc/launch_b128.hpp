@@ -63,9 +63,10 @@ int launch_gemm_b128_decode(const void* x, int64_t ldx, int64_t M, int64_t K, co
 // 128-blocks, whose fp32 partials go to `part` (splits * M * round_up(N, 4)
 // floats) and are added in order by launch_splitk_reduce.
 struct B128Plan {
-  int mt;       // activation rows per tile: 64, 128 or 256
+  int mt;       // 64 or 128: activation rows of a 128-column tile; 256: the large tiles
   int splits;
 };
+int b128_force(int mt);   // test hook: pins mt (0: by shape); returns the previous value
 B128Plan b128_plan(int64_t M, int64_t N, int64_t K);
 int launch_gemm_b128_tile(const void* qp, const void* sp, int64_t M, int64_t K, const void* wp, const float* wsc,
                           int64_t N, const void* bias, void* y, int64_t ldy, hipStream_t stream, B128Plan plan,

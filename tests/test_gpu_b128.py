@@ -259,3 +259,45 @@ def test_graph_replays(M):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("tile", [64, 128, 256])
+@pytest.mark.parametrize("M,N,K", [(17, 8, 512), (128, 256, 528), (129, 264, 640), (300, 520, 1152), (700, 1024, 2064),
+                                   (257, 136, 8336)])
+def test_every_tile_form(tile, M, N, K):
+    """Each tile form on shapes of one and many tiles, partial ones and a
+    single weight group among them; persistent workgroups with several tiles."""
+    x = spiky(M, K, M + N + K)
+    wq, ws = make_weight(N, K, N + K)
+    bias = randn((N,), 9)
+    pw = api.prepare_weight_b128(wq.to(dev()), ws.to(dev()))
+    prev = api.mxfp8_debug_force_b128(tile)
+    try:
+        out = torch.full((M + 1, N + 16), 3.0, dtype=torch.bfloat16, device=dev())
+        y = api.linear(x.to(dev()), pw, bias.to(dev()), out=out[:M, :N])
+        z = api.linear(x.to(dev()), pw, bias.to(dev()))
+    finally:
+        api.mxfp8_debug_force_b128(prev)
+    check_linear(x, wq, ws, bias, y)
+    assert torch.equal(y, z)
+    assert (out[M] == 3.0).all() and (out[:, N:] == 3.0).all()
+
+
+def test_many_tiles_per_workgroup():
+    """More large tiles than compute units: the pipeline runs from tile to
+    tile.  Every output against the small tiles', and a sample of rows against
+    64 bits."""
+    M, N, K = 4200, 4360, 640
+    x, (wq, ws) = spiky(M, K, 1), make_weight(N, K, 2)
+    pw = api.prepare_weight_b128(wq.to(dev()), ws.to(dev()))
+    bias = randn((N,), 3).to(dev())
+    y = {}
+    for tile in (128, 256):
+        prev = api.mxfp8_debug_force_b128(tile)
+        try:
+            y[tile] = api.linear(x.to(dev()), pw, bias)
+        finally:
+            api.mxfp8_debug_force_b128(prev)
+    assert torch.equal(y[128], y[256])    # the same blocks in the same order
+    rows = torch.arange(0, M, 97)
+    check_linear(x[rows], wq, ws, bias.cpu(), y[256][rows.to(dev())])
