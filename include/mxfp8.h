@@ -453,6 +453,13 @@ int mxfp8_linear_wgrad(const void* dy_bf16, int64_t M, int64_t N, int64_t lddy, 
                        int accumulate, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Test hook: pin the dW tile of mxfp8_linear_wgrad: 0 = by shape, 128 or 256
+ * (M == 0 always takes 128).  The workspace query follows it.  Process-wide;
+ * returns the previous value, or MXFP8_E_SHAPE.
+ */
+int mxfp8_debug_force_wgrad(int tile);
+
+/*
  * Load-balance and z loss of the routed layer's router, the tokens of each
  * expert, and the gradient with respect to the logits:
  *   p = softmax(logits[t, :]), lse = log sum_e exp(logits[t, e]) (over all E)

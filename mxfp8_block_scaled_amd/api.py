@@ -71,6 +71,7 @@ _SIGNATURES = {
     "mxfp8_gemm_packed_b128_workspace_bytes": ([_i64, _i64, _i64, ctypes.POINTER(_sz)], ctypes.c_int),
     "mxfp8_gemm_packed_b128": ([_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _sz, _vp], ctypes.c_int),
     "mxfp8_debug_force_b128": ([ctypes.c_int], ctypes.c_int),
+    "mxfp8_debug_force_wgrad": ([ctypes.c_int], ctypes.c_int),
     "mxfp8_linear_wgrad_workspace_bytes": ([_i64, _i64, _i64, ctypes.POINTER(_sz)], ctypes.c_int),
     "mxfp8_linear_wgrad": ([_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, ctypes.c_int, _i64, _vp, ctypes.c_int, _vp,
                             _sz, _vp], ctypes.c_int),
@@ -581,6 +582,10 @@ def mxfp8_linear_b128(x, M, K, ldx, wp, sp, N, bias, y, ldy, ws, ws_bytes, strea
 
 def mxfp8_debug_force_b128(tile):
     return lib().mxfp8_debug_force_b128(tile)
+
+
+def mxfp8_debug_force_wgrad(tile):
+    return lib().mxfp8_debug_force_wgrad(tile)
 
 
 def mxfp8_prepared_weight_b128_bytes(N, K):

@@ -226,8 +226,13 @@ int mxfp8_linear_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* 
   if (!bytes) return MXFP8_E_NULLPTR;
   if (M < 0 || M > kMaxRows || !rows_ok(N) || N % 8 != 0 || !summed_ok(K)) return MXFP8_E_SHAPE;
   const mxfp8::WgradPlan p = mxfp8::wgrad_plan(M, N, K);
-  *bytes = round_up(mxfp8::wgrad_dw_bytes(N, K, p), 256) + round_up(mxfp8::wgrad_db_bytes(N, K, p), 256);
+  *bytes = round_up(mxfp8::wgrad_dw_bytes(M, N, K, p), 256) + round_up(mxfp8::wgrad_db_bytes(M, N, K, p), 256);
   return MXFP8_OK;
+}
+
+int mxfp8_debug_force_wgrad(int tile) {
+  if (tile != 0 && tile != 128 && tile != 256) return MXFP8_E_SHAPE;
+  return mxfp8::wgrad_force(tile);
 }
 
 int mxfp8_linear_wgrad(const void* dy_bf16, int64_t M, int64_t N, int64_t lddy, const void* q_packed,
@@ -263,7 +268,7 @@ int mxfp8_linear_wgrad(const void* dy_bf16, int64_t M, int64_t N, int64_t lddy, 
   a.accumulate = accumulate != 0;
   a.db = db;
   a.part_dw = (float*)workspace;
-  a.part_db = (float*)((uint8_t*)workspace + round_up(mxfp8::wgrad_dw_bytes(N, K, p), 256));
+  a.part_db = (float*)((uint8_t*)workspace + round_up(mxfp8::wgrad_dw_bytes(M, N, K, p), 256));
   return mxfp8::launch_wgrad(a, p, (hipStream_t)stream);
 }
 

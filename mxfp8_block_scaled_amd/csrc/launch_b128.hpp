@@ -76,12 +76,14 @@ int launch_gemm_b128_tile(const void* qp, const void* sp, int64_t M, int64_t K, 
 // activations (either scale block), and db[n] = sum_m dY[m, n].
 struct WgradPlan {
   int tile;     // edge of a workgroup's dW tile: 128 or 256
-  int splits;   // runs of 64 rows each workgroup's M is cut into
+  int splits;   // tile 128: runs of 64-token steps each tile's tokens are cut into
+  int runs;     // tile 256: workgroups, one equal run of the (tile, step) units each
 };
 WgradPlan wgrad_plan(int64_t M, int64_t N, int64_t K);
-// fp32 partials: dW [splits][N][K] (splits > 1), then db [splits * tiles_k][N].
-size_t wgrad_dw_bytes(int64_t N, int64_t K, WgradPlan p);
-size_t wgrad_db_bytes(int64_t N, int64_t K, WgradPlan p);
+int wgrad_force(int tile);   // test hook: pins the tile (0: by shape); returns the previous value
+// fp32 partials of dW, then of db.
+size_t wgrad_dw_bytes(int64_t M, int64_t N, int64_t K, WgradPlan p);
+size_t wgrad_db_bytes(int64_t M, int64_t N, int64_t K, WgradPlan p);
 struct WgradArgs {
   const void* dy;       // bf16 [M, N], row stride lddy
   int64_t M, N, lddy;

@@ -28,6 +28,8 @@
 //    workgroup does 1 / tiles_k of it.
 // Partial sums of split runs and of db go to the workspace and are added in
 // a fixed order: results do not depend on timing.
+#include <algorithm>
+
 #include "common.hpp"
 #include "launch_b128.hpp"
 #include "tile_core.hpp"
@@ -56,7 +58,7 @@ struct WgLds {
 }  // namespace
 
 template <int kT, bool kBias>
-__global__ __launch_bounds__(kWgThreads, kT == 128 ? 2 : 1) void wgrad_kernel(
+__global__ __launch_bounds__(kWgThreads, 2) void wgrad_kernel(
     const uint16_t* __restrict__ dy, int64_t M, int N, int64_t lddy, const uint8_t* __restrict__ qp,
     const uint8_t* __restrict__ sp, int K, int KS, int tiles_n, int tiles_k, int splits, void* __restrict__ out,
     int64_t ldo, int64_t split_stride, int out_bf16, int accumulate, float* __restrict__ part_db) {
@@ -258,48 +260,421 @@ __global__ __launch_bounds__(256) void wgrad_reduce_kernel(const float* __restri
   db[n] = accumulate ? db[n] + a : a;
 }
 
-WgradPlan wgrad_plan(int64_t M, int64_t N, int64_t K) {
-  WgradPlan p;
-  p.tile = 128;
-  const int64_t tiles = ((N + p.tile - 1) / p.tile) * ((K + p.tile - 1) / p.tile);
-  const int64_t steps = (M + kWgStep - 1) / kWgStep, want = 512;   // two workgroups per compute unit
-  int64_t s = 1;
-  while (s < 16 && tiles * s < want && steps / (2 * s) >= 4) s *= 2;
-  p.splits = (int)s;
-  return p;
+// ---------------------------------------------------------------------------
+// Large tiles: 256 x 256 of dW per workgroup, four waves 2 x 2, each 128 x 128
+// (64 MFMAs per 32 tokens and wave, accumulators in the 256 AGPRs).
+//  * The (tile, step) units, tile by tile, are cut into one equal run per
+//    workgroup, so the chip is full whatever the number of tiles.  A run
+//    holds at most two tiles it does not own whole, its first and its last;
+//    their sums go to the workgroup's two slots of the workspace in lane
+//    order, and wgrad_join adds a tile's pieces in token order.
+//  * A step has two 32-token halves with a fragment set each.  During half 0
+//    the fragments of half 1 are read; then everything in flight has landed,
+//    the step's one barrier, and during half 1 the next step's first
+//    fragments are read while the step's own buffer is refilled for the step
+//    after next (dY copies and the widened X) and X is loaded one step
+//    further.
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int kBigT = 256;
+constexpr int kBigPitch = kBigT * 2;
+constexpr int kBigOp = kWgStep * kBigPitch;        // 32 KiB: one operand's stage
+constexpr int kBigLds = 4 * kBigOp;                // dY x 2, X x 2
+constexpr int kBigTileFloats = kBigT * kBigT;
+
+// Runs: workgroup w of G takes units [U w / G, U (w + 1) / G) of U.
+__host__ __device__ inline int64_t run_start(int64_t U, int G, int64_t w) { return U * w / G; }
+__host__ __device__ inline int run_of(int64_t U, int G, int64_t unit) { return (int)(((unit + 1) * G - 1) / U); }
+
+}  // namespace
+
+template <bool kBias>
+__global__ __launch_bounds__(kWgThreads, 1) void wgrad_big_kernel(
+    const uint16_t* __restrict__ dy, int64_t M, int N, int64_t lddy, const uint8_t* __restrict__ qp,
+    const uint8_t* __restrict__ sp, int K, int KS, int tiles_k, int tiles, int steps, void* __restrict__ dw,
+    int64_t lddw, int out_bf16, int accumulate, float* __restrict__ part, float* __restrict__ part_db, int pieces) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wk = wave & 1, wn = wave >> 1;
+  const int i = lane & 15, g = lane >> 4;
+  const int G = (int)gridDim.x, w = (int)blockIdx.x;
+  const int64_t U = (int64_t)tiles * steps;
+  const int64_t u0 = run_start(U, G, w), u1 = run_start(U, G, w + 1);
+
+  // Fragment addresses (see wgrad_kernel): the swizzle is the lane's own, so
+  // buffer, half and row offset are immediates.
+  const int fx = slot_xor(8 * g + (i >> 2));
+  const uint32_t lds0 = tile::lds_addr(smem);
+  uint32_t xa[8], ya[8];
+#pragma unroll
+  for (int a = 0; a < 8; ++a) {
+    const uint32_t o = lds0 + (uint32_t)((8 * g + (i >> 2)) * kBigPitch + ((a ^ fx) * 32) + (i & 3) * 8);
+    xa[a] = o + 2 * kBigOp + wk * 256;
+    ya[a] = o + wn * 256;
+  }
+  auto sy = [&](int b) { return smem + b * kBigOp; };
+  auto sx = [&](int b) { return smem + (2 + b) * kBigOp; };
+  auto frag = [&](uint32_t at, int b, int h) {
+    lds_s16x4* const p = (lds_s16x4*)(at + (uint32_t)(b * kBigOp + h * 32 * kBigPitch));
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p + 4 * kBigPitch / 8);
+    const s16x8 r = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    return __builtin_bit_cast(bf16x8, r);
+  };
+
+  // X: the thread's four 16-byte chunks of a step lie in one token row
+  // m = 16 wave + lane / 4, one per 64-K piece.  Pieces past K and past the
+  // group are other columns' data or zeros; their outputs are not stored.
+  const int xm = 16 * wave + (lane >> 2), xc = (lane & 3) ^ swz(lane >> 2);
+  uint32_t xdst[4];
+#pragma unroll
+  for (int v = 0; v < 4; ++v) xdst[v] = (uint32_t)(xm * kBigPitch + (((v * 4 + xc) ^ slot_xor(xm)) * 32));
+  const uint32_t xvoff = (uint32_t)wave * KS * kPieceBytes + (uint32_t)lane * 16u;
+  const uint32_t svoff = (uint32_t)scale_off(xm, xc >> 1);
+  const uint32_t gbytes = (uint32_t)KS * kTileBytes, sbytes = (uint32_t)KS * kTileScaleBytes;
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  struct X {
+    u32x4 q[4];
+    uint32_t s[4];
+  };
+  auto store_x = [&](const X& x, int v, uint8_t* st) {
+    uint4 d[2];
+    widen16(make_uint4(x.q[v][0], x.q[v][1], x.q[v][2], x.q[v][3]), b128_scale_value(x.s[v]), d);
+    *reinterpret_cast<uint4*>(st + xdst[v]) = d[0];
+    *reinterpret_cast<uint4*>(st + xdst[v] + 16) = d[1];
+  };
+
+  v4f acc[8][8];
+  float accb[4];
+
+  for (int64_t u = u0; u < u1;) {
+    const int t = (int)(u / steps), sa = (int)(u - (int64_t)t * steps);
+    const int sb = (int)min((int64_t)steps, sa + (u1 - u));
+    const int tn = t / tiles_k, tk = t - tn * tiles_k;
+    const int n0 = tn * kBigT, k0 = tk * kBigT;
+
+    // dY: lane l of copy c takes LDS bytes [16 l, + 16) of its KiB: two token
+    // rows of 512 bytes, 32-byte slot c holding logical slot c ^ f(m).
+    uint32_t vy[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const int m = (wave * 8 + c) * 2 + (lane >> 5), p = lane & 31;
+      vy[c] = (uint32_t)((int64_t)m * lddy + n0 + ((p >> 1) ^ slot_xor(m)) * 16 + (p & 1) * 8) * 2u;
+    }
+    auto dy_rsrc = [&](int s) {
+      const int64_t m0 = (int64_t)min(s, sb - 1) * kWgStep;
+      const int64_t rows = min(M - m0, (int64_t)kWgStep);
+      return tile::buffer_rsrc(dy + m0 * lddy, (uint32_t)(((rows - 1) * lddy + N) * 2));
+    };
+    auto copy_dy = [&](int c, tile::i4v r, uint8_t* st) { tile::b2l_16(vy[c], r, 0u, st + (wave * 8 + c) * 1024); };
+    auto load_x = [&](int s, X& x) {
+      const int sc = min(s, sb - 1);
+      const __amdgpu_buffer_rsrc_t qr = raw_rsrc(qp + (size_t)(sc >> 1) * gbytes, gbytes);
+      const __amdgpu_buffer_rsrc_t sr = raw_rsrc(sp + (size_t)(sc >> 1) * sbytes, sbytes);
+      const int half = sc & 1, ks = k0 / kStepK;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        x.q[v] = __builtin_amdgcn_raw_buffer_load_b128(qr, xvoff, (uint32_t)(half * 4 * KS + ks + v) * kPieceBytes, 0);
+        x.s[v] = __builtin_amdgcn_raw_buffer_load_b8(sr, svoff, (uint32_t)((ks + v) * kTileScaleBytes + half * 2), 0);
+      }
+    };
+
+#pragma unroll
+    for (int a = 0; a < 8; ++a) {
+      if (a < 4) accb[a] = 0.0f;
+#pragma unroll
+      for (int b = 0; b < 8; ++b) acc[a][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    // Both buffers filled, X of the third step on its way.  (The barrier:
+    // the last tile's fragments have been read by every wave.)
+    tile::wait_vmcnt<0>();
+    __syncthreads();
+    X xr;
+    {
+      const tile::i4v r0 = dy_rsrc(sa), r1 = dy_rsrc(sa + 1);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) copy_dy(c, r0, sy(0));
+#pragma unroll
+      for (int c = 0; c < 8; ++c) copy_dy(c, r1, sy(1));
+      X x1;
+      load_x(sa, xr);
+      load_x(sa + 1, x1);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) store_x(xr, v, sx(0));
+#pragma unroll
+      for (int v = 0; v < 4; ++v) store_x(x1, v, sx(1));
+      load_x(sa + 2, xr);
+    }
+    tile::wait_vmcnt<0>();
+    __syncthreads();
+    bf16x8 ax[8], ay[8], bx[8], by[8];   // fragments of half 0 and of half 1
+#pragma unroll
+    for (int a = 0; a < 8; ++a) {
+      ax[a] = frag(xa[a], 0, 0);
+      ay[a] = frag(ya[a], 0, 0);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+
+    int phase = sa % tiles_k;
+    // db: the two waves that hold the same dY fragments take four each; the
+    // dot product with ones adds a pair of bf16 to the fp32 sum.
+    auto add_bias = [&](const bf16x8 (&fy)[8]) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const auto q = __builtin_bit_cast(u32x4, wk ? fy[b + 4] : fy[b]);
+        const bf16x2 one = {(__bf16)1.0f, (__bf16)1.0f};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          accb[b] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, (uint32_t)q[e]), one, accb[b], false);
+      }
+    };
+    // One step on buffer b.  A fragment of X is read where its predecessor
+    // has one row of MFMAs left, one of dY into the other set.  The empty asm statements keep the MFMAs in their
+    // places between the reads, writes and copies.
+    auto step = [&](int s, auto B) {
+      constexpr int b = decltype(B)::value;
+      const bool with_bias = kBias && phase == tk;
+      phase = phase + 1 == tiles_k ? 0 : phase + 1;
+      tile::static_for<0, 64>([&](auto J) {
+        constexpr int j = decltype(J)::value, a = j >> 3, c = j & 7;
+        acc[a][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ax[a], ay[c], acc[a][c], 0, 0, 0);
+        asm volatile("" : "+a"(acc[a][c]));
+        if constexpr (c == 1) by[a] = frag(ya[a], b, 1);
+        if constexpr (c == 4) bx[a] = frag(xa[a], b, 1);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      if (with_bias) add_bias(ay);
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+#pragma unroll
+      for (int v = 0; v < 4; ++v) asm volatile("" : "+v"(xr.q[v]), "+v"(xr.s[v]));   // landed: no wait further down
+      const tile::i4v r = dy_rsrc(s + 2);
+      tile::static_for<0, 64>([&](auto J) {
+        constexpr int j = decltype(J)::value, a = j >> 3, c = j & 7;
+        acc[a][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bx[a], by[c], acc[a][c], 0, 0, 0);
+        asm volatile("" : "+a"(acc[a][c]));
+        if constexpr (c == 1) ay[a] = frag(ya[a], b ^ 1, 0);
+        if constexpr (c == 4) ax[a] = frag(xa[a], b ^ 1, 0);
+        if constexpr (j % 3 == 2 && j / 3 < 8) copy_dy(j / 3, r, sy(b));
+        if constexpr (j % 8 == 6 && j / 8 < 4) store_x(xr, j / 8, sx(b));
+        if constexpr (j == 38) load_x(s + 3, xr);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      if (with_bias) add_bias(by);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    };
+    for (int s = sa; s < sb; s += 2) {
+      step(s, std::integral_constant<int, 0>{});
+      if (s + 1 < sb) step(s + 1, std::integral_constant<int, 1>{});
+    }
+
+    // Lane (i, g) holds D[k = 128 wk + 16 a + 4 g + j][n = 128 wn + 16 b + i].
+    const bool whole = sa == 0 && sb == steps;
+    if (whole) {
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        const int n = n0 + wn * 128 + b * 16 + i;
+        if (n < N) {
+#pragma unroll
+          for (int a = 0; a < 8; ++a) {
+            const int k = k0 + wk * 128 + a * 16 + 4 * g;
+            if (k < K) {
+              if (out_bf16) {
+                *reinterpret_cast<uint2*>((uint16_t*)dw + (size_t)n * lddw + k) =
+                    make_uint2(pack_bf16x2(acc[a][b][0], acc[a][b][1]), pack_bf16x2(acc[a][b][2], acc[a][b][3]));
+              } else {
+                v4f* d = reinterpret_cast<v4f*>((float*)dw + (size_t)n * lddw + k);
+                *d = accumulate ? *d + acc[a][b] : acc[a][b];
+              }
+            }
+          }
+        }
+      }
+    } else {
+      // slot 0: the piece at the start of the run, 1: at its end
+      v4f* d = reinterpret_cast<v4f*>(part + ((size_t)w * 2 + (u == u0 ? 0 : 1)) * kBigTileFloats) + wave * 4096 + lane;
+#pragma unroll
+      for (int a = 0; a < 8; ++a)
+#pragma unroll
+        for (int b = 0; b < 8; ++b) d[(a * 8 + b) * 64] = acc[a][b];
+    }
+    if constexpr (kBias) {
+      const int piece = w - run_of(U, G, (int64_t)t * steps);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        float v = accb[b];
+        v += __shfl_xor(v, 16);
+        v += __shfl_xor(v, 32);
+        if (g == 0) part_db[((size_t)t * pieces + piece) * kBigT + wn * 128 + wk * 64 + b * 16 + i] = v;
+      }
+    }
+    u += sb - sa;
+  }
+  tile::wait_vmcnt<0>();   // no copy may land after the workgroup's LDS is given away
 }
 
-size_t wgrad_dw_bytes(int64_t N, int64_t K, WgradPlan p) {
-  return p.splits > 1 ? (size_t)p.splits * (size_t)N * (size_t)K * 4 : 0;
-}
-size_t wgrad_db_bytes(int64_t N, int64_t K, WgradPlan p) {
-  return (size_t)p.splits * (size_t)((K + p.tile - 1) / p.tile) * (size_t)N * 4;
+// Joins the large tiles that several runs share, in token order (grid: 16
+// workgroups per tile; those of whole tiles leave), and the parts of db (the
+// last workgroups, sixteen columns each): over the tiles of a column of tiles and their pieces.
+__global__ __launch_bounds__(256) void wgrad_join_kernel(const float* __restrict__ part, int64_t U, int G, int tiles,
+                                                         int tiles_k, int steps, int N, int K, void* __restrict__ dw,
+                                                         int64_t lddw, int out_bf16, int accumulate,
+                                                         const float* __restrict__ part_db, int pieces,
+                                                         float* __restrict__ db) {
+  const int tid = threadIdx.x;
+  if ((int)blockIdx.x >= tiles * 16) {
+    // sixteen columns: thread (q, c) adds the tiles q, q + 16, ... along k
+    __shared__ float red[16][17];
+    const int c = tid & 15, q = tid >> 4;
+    const int n = ((int)blockIdx.x - tiles * 16) * 16 + c, tn = n / kBigT;
+    float v = 0.0f;
+    if (n < N) {
+      for (int tk = q; tk < tiles_k; tk += 16) {
+        const int t = tn * tiles_k + tk;
+        const int np = run_of(U, G, (int64_t)(t + 1) * steps - 1) - run_of(U, G, (int64_t)t * steps) + 1;
+        for (int p = 0; p < np; ++p) v += part_db[((size_t)t * pieces + p) * kBigT + n % kBigT];
+      }
+    }
+    red[q][c] = v;
+    __syncthreads();
+    if (q != 0 || n >= N) return;
+    v = 0.0f;
+#pragma unroll
+    for (int p = 0; p < 16; ++p) v += red[p][c];
+    db[n] = accumulate ? db[n] + v : v;
+    return;
+  }
+  const int t = (int)blockIdx.x >> 4, sub = (int)blockIdx.x & 15;
+  const int w0 = run_of(U, G, (int64_t)t * steps), w1 = run_of(U, G, (int64_t)(t + 1) * steps - 1);
+  if (w0 == w1) return;   // one run owns the tile (and stored it)
+  const int tn = t / tiles_k, tk = t - tn * tiles_k;
+  for (int c = 0; c < 4; ++c) {
+    const int e = sub * 1024 + c * 256 + tid;   // v4f of the tile, lane order: wave, (a, b), lane
+    v4f v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int w = w0; w <= w1; ++w) {
+      // a piece lies at the start of its run unless the run began in an earlier tile
+      const int slot = run_start(U, G, w) >= (int64_t)t * steps ? 0 : 1;
+      v += reinterpret_cast<const v4f*>(part + ((size_t)w * 2 + slot) * kBigTileFloats)[e];
+    }
+    const int wave = e >> 12, ab = (e >> 6) & 63, lane = e & 63;
+    const int n = tn * kBigT + (wave >> 1) * 128 + (ab & 7) * 16 + (lane & 15);
+    const int k = tk * kBigT + (wave & 1) * 128 + (ab >> 3) * 16 + 4 * (lane >> 4);
+    if (n >= N || k >= K) continue;
+    if (out_bf16) {
+      *reinterpret_cast<uint2*>((uint16_t*)dw + (size_t)n * lddw + k) =
+          make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    } else {
+      v4f* d = reinterpret_cast<v4f*>((float*)dw + (size_t)n * lddw + k);
+      *d = accumulate ? *d + v : v;
+    }
+  }
 }
 
 namespace {
-template <int kT, bool kBias>
-int launch_wgrad_k(const WgradArgs& a, WgradPlan p, hipStream_t stream) {
-  constexpr int lds = WgLds<kT>::kBytes;
+std::atomic<int> g_force_wgrad{0};
+constexpr int64_t kRuns = 256;   // compute units
+}
+
+int wgrad_force(int tile) { return g_force_wgrad.exchange(tile); }
+
+WgradPlan wgrad_plan(int64_t M, int64_t N, int64_t K) {
+  WgradPlan p;
+  const int64_t steps = (M + kWgStep - 1) / kWgStep;
+  const int64_t big = ((N + 255) / 256) * ((K + 255) / 256);
+  const int force = g_force_wgrad.load(std::memory_order_relaxed);
+  // Large tiles once every compute unit gets a run of sixteen steps.
+  p.tile = big * steps >= kRuns * 16 ? 256 : 128;
+  if (force) p.tile = force;
+  if (steps == 0) p.tile = 128;
+  p.splits = 1;
+  p.runs = 0;
+  if (p.tile == 256) {
+    // One run per compute unit, of eight steps at least; as many runs as
+    // tiles where that leaves few units idle, for then no tile is shared.
+    p.runs = (int)std::min(kRuns, std::max<int64_t>(1, big * steps / 8));
+    if (big <= kRuns && big * 8 >= kRuns * 7) p.runs = (int)big;
+    return p;
+  }
+  const int64_t tiles = ((N + 127) / 128) * ((K + 127) / 128);
+  // two workgroups per compute unit
+  while (p.splits < 16 && tiles * p.splits < 512 && steps / (2 * p.splits) >= 4) p.splits *= 2;
+  return p;
+}
+
+namespace {
+struct BigShape {
+  int64_t tiles_n, tiles_k, tiles, steps, U, pieces;
+  bool shared;   // some tile belongs to several runs
+};
+BigShape big_shape(int64_t M, int64_t N, int64_t K, WgradPlan p) {
+  BigShape b;
+  b.tiles_n = (N + kBigT - 1) / kBigT;
+  b.tiles_k = (K + kBigT - 1) / kBigT;
+  b.tiles = b.tiles_n * b.tiles_k;
+  b.steps = (M + kWgStep - 1) / kWgStep;
+  b.U = b.tiles * b.steps;
+  b.shared = b.tiles % p.runs != 0;
+  b.pieces = b.shared ? b.steps / (b.U / p.runs) + 2 : 1;
+  return b;
+}
+}  // namespace
+
+size_t wgrad_dw_bytes(int64_t M, int64_t N, int64_t K, WgradPlan p) {
+  if (p.tile == 256) return big_shape(M, N, K, p).shared ? (size_t)p.runs * 2 * kBigTileFloats * 4 : 0;
+  return p.splits > 1 ? (size_t)p.splits * (size_t)N * (size_t)K * 4 : 0;
+}
+size_t wgrad_db_bytes(int64_t M, int64_t N, int64_t K, WgradPlan p) {
+  if (p.tile == 256) {
+    const BigShape b = big_shape(M, N, K, p);
+    return (size_t)b.tiles * (size_t)b.pieces * kBigT * 4;
+  }
+  return (size_t)p.splits * (size_t)((K + 127) / 128) * (size_t)N * 4;
+}
+
+namespace {
+template <bool kBias>
+int launch_small(const WgradArgs& a, WgradPlan p, hipStream_t stream) {
+  constexpr int lds = WgLds<128>::kBytes;
   static std::atomic<int> lds_set[kMaxDevices];
-  if (!set_lds_limit_once((const void*)wgrad_kernel<kT, kBias>, lds, lds_set)) return -7;
-  const int tiles_n = (int)((a.N + kT - 1) / kT), tiles_k = (int)((a.K + kT - 1) / kT);
+  if (!set_lds_limit_once((const void*)wgrad_kernel<128, kBias>, lds, lds_set)) return -7;
+  const int tiles_n = (int)((a.N + 127) / 128), tiles_k = (int)((a.K + 127) / 128);
   const bool direct = p.splits == 1;
-  hipLaunchKernelGGL((wgrad_kernel<kT, kBias>), dim3((unsigned)(tiles_n * tiles_k * p.splits)), dim3(kWgThreads), lds,
+  hipLaunchKernelGGL((wgrad_kernel<128, kBias>), dim3((unsigned)(tiles_n * tiles_k * p.splits)), dim3(kWgThreads), lds,
                      stream, (const uint16_t*)a.dy, a.M, (int)a.N, a.lddy, (const uint8_t*)a.qp,
                      (const uint8_t*)a.sp, (int)a.K, (int)(2 * b128_blocks(a.K)), tiles_n, tiles_k, p.splits,
                      direct ? a.dw : (void*)a.part_dw, direct ? a.lddw : a.K, a.N * a.K, direct ? a.out_bf16 : 0,
                      direct ? a.accumulate : 0, a.part_db);
   return hipGetLastError() == hipSuccess ? 0 : -7;
 }
+
+template <bool kBias>
+int launch_big(const WgradArgs& a, WgradPlan p, hipStream_t stream) {
+  static std::atomic<int> lds_set[kMaxDevices];
+  if (!set_lds_limit_once((const void*)wgrad_big_kernel<kBias>, kBigLds, lds_set)) return -7;
+  const BigShape b = big_shape(a.M, a.N, a.K, p);
+  hipLaunchKernelGGL(wgrad_big_kernel<kBias>, dim3((unsigned)p.runs), dim3(kWgThreads), kBigLds, stream,
+                     (const uint16_t*)a.dy, a.M, (int)a.N, a.lddy, (const uint8_t*)a.qp, (const uint8_t*)a.sp,
+                     (int)a.K, (int)(2 * b128_blocks(a.K)), (int)b.tiles_k, (int)b.tiles, (int)b.steps, a.dw, a.lddw,
+                     a.out_bf16, a.accumulate, a.part_dw, a.part_db, (int)b.pieces);
+  if (hipGetLastError() != hipSuccess) return -7;
+  if (!b.shared && !kBias) return 0;
+  const int join = b.shared ? (int)b.tiles : 0, cols = kBias ? (int)((a.N + 15) / 16) : 0;
+  hipLaunchKernelGGL(wgrad_join_kernel, dim3((unsigned)(join * 16 + cols)), dim3(256), 0, stream, a.part_dw, b.U,
+                     p.runs, join, (int)b.tiles_k, (int)b.steps, (int)a.N, (int)a.K, a.dw, a.lddw, a.out_bf16,
+                     a.accumulate, a.part_db, (int)b.pieces, a.db);
+  return hipGetLastError() == hipSuccess ? 0 : -7;
+}
 }  // namespace
 
 int launch_wgrad(const WgradArgs& a, WgradPlan p, hipStream_t stream) {
   const bool bias = a.db != nullptr;
-  int st;
-  st = bias ? launch_wgrad_k<128, true>(a, p, stream) : launch_wgrad_k<128, false>(a, p, stream);
+  if (p.tile == 256) return bias ? launch_big<true>(a, p, stream) : launch_big<false>(a, p, stream);
+  const int st = bias ? launch_small<true>(a, p, stream) : launch_small<false>(a, p, stream);
   if (st || (p.splits == 1 && !bias)) return st;
   const int64_t quads = p.splits > 1 ? a.N * (a.K / 4) : 0, total = quads + (bias ? a.N : 0);
-  const int parts_db = p.splits * (int)((a.K + p.tile - 1) / p.tile);
+  const int parts_db = p.splits * (int)((a.K + 127) / 128);
   hipLaunchKernelGGL(wgrad_reduce_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, stream, a.part_dw,
                      p.splits, a.N, a.K, a.dw, a.lddw, a.out_bf16, a.accumulate, quads, a.part_db, parts_db, a.db);
   return hipGetLastError() == hipSuccess ? 0 : -7;

@@ -245,3 +245,29 @@ def test_mx_layer_weight_gradient():
     y = api.gemm_packed(pa, pw)
     assert y.shape == (200, 256)
     check_dw(api.linear_wgrad(dy.to(dev()), pa), None, dy, f64(pa.dequantize()))
+
+
+@pytest.mark.parametrize("tile", [128, 256])
+@pytest.mark.parametrize("M,N,K,form", [(1, 8, 16, "b128"), (64, 256, 256, "mx"), (65, 264, 272, "b128"), (200, 520, 512, "mx"),
+                                        (1000, 248, 1040, "b128"), (5000, 768, 528, "b128"), (640, 2304, 2304, "mx")])
+def test_wgrad_tile_forms(tile, M, N, K, form):
+    """Each form on shapes of few and many tiles; runs that end inside a tile,
+    at its border, and hold several; accumulation and bf16 through the join."""
+    x, dy = spiky(M, K, M + K), randn((M, N), N, 1e-3)
+    pa = keep(x, form)
+    X = f64(pa.dequantize())
+    base, base_b = torch.randn(N, K), torch.randn(N)
+    prev = api.mxfp8_debug_force_wgrad(tile)
+    try:
+        dw, db = api.linear_wgrad(dy.to(dev()), pa, bias_grad=True)
+        half = api.linear_wgrad(dy.to(dev()), pa, dtype=torch.bfloat16)
+        acc = api.linear_wgrad(dy.to(dev()), pa, bias_grad=True, out=base.to(dev()), out_bias=base_b.to(dev()), accumulate=True)
+        again = api.linear_wgrad(dy.to(dev()), pa)
+        none = api.linear_wgrad(torch.empty(0, N, dtype=torch.bfloat16, device=dev()),
+                                api.quantize_act_packed_b128(torch.empty(0, K, dtype=torch.bfloat16, device=dev())))
+    finally:
+        api.mxfp8_debug_force_wgrad(prev)
+    check_dw(dw, db, dy, X)
+    check_dw(half, None, dy, X)
+    check_dw(*acc, dy, X, base, base_b)
+    assert torch.equal(dw, again) and not none.any()
