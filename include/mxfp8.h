@@ -393,7 +393,7 @@ typedef enum { MXFP8_F32 = 0, MXFP8_BF16 = 1 } mxfp8_dtype;
  *   scale is its transpose's.  Outputs 256-byte aligned, of
  *   mxfp8_prepared_weight_b128_bytes(N, K), or (K, N) if transposed.
  * mxfp8_linear_b128: arguments as mxfp8_linear, workspace of
- *   mxfp8_linear_b128_workspace_bytes.
+ *   mxfp8_linear_b128_workspace_bytes (0 for M <= 16: NULL is fine then).
  * mxfp8_gemm_packed_b128: the GEMM alone on activations of
  *   mxfp8_quantize_act_packed_b128; workspace of
  *   mxfp8_gemm_packed_b128_workspace_bytes (fp32 partials where K is split).
@@ -442,15 +442,15 @@ int mxfp8_debug_force_b128(int tile);
  *           16-byte aligned), N % 8 == 0
  *   dw      [N, K] row stride lddw (lddw >= K, lddw % 8 == 0), 16-byte
  *           aligned: fp32 (MXFP8_F32) or bf16 (MXFP8_BF16, rounded once)
- *   db      fp32 [N] or NULL
- *   accumulate != 0: dw += and db += (fp32 dw only; MXFP8_E_SHAPE else)
+ *   db      [N] or NULL, fp32 or bf16 (db_dtype)
+ *   accumulate != 0: dw += and db += (fp32 only; MXFP8_E_SHAPE else)
  * M == 0 writes zeros (or leaves dw, db as they are if accumulating).
  * workspace of mxfp8_linear_wgrad_workspace_bytes, 256-byte aligned.
  */
 int mxfp8_linear_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes);
 int mxfp8_linear_wgrad(const void* dy_bf16, int64_t M, int64_t N, int64_t lddy, const void* q_packed,
-                       const void* s_packed, int64_t K, void* dw, int dw_dtype, int64_t lddw, float* db,
-                       int accumulate, void* workspace, size_t workspace_bytes, void* stream);
+                       const void* s_packed, int64_t K, void* dw, int dw_dtype, int64_t lddw, void* db,
+                       int db_dtype, int accumulate, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Test hook: pin the dW tile of mxfp8_linear_wgrad: 0 = by shape, 128 or 256

@@ -14,6 +14,7 @@ wrappers (the apply path of vLLM PR #52204: assert bf16, view the input as
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -73,8 +74,8 @@ _SIGNATURES = {
     "mxfp8_debug_force_b128": ([ctypes.c_int], ctypes.c_int),
     "mxfp8_debug_force_wgrad": ([ctypes.c_int], ctypes.c_int),
     "mxfp8_linear_wgrad_workspace_bytes": ([_i64, _i64, _i64, ctypes.POINTER(_sz)], ctypes.c_int),
-    "mxfp8_linear_wgrad": ([_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, ctypes.c_int, _i64, _vp, ctypes.c_int, _vp,
-                            _sz, _vp], ctypes.c_int),
+    "mxfp8_linear_wgrad": ([_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, ctypes.c_int, _i64, _vp, ctypes.c_int,
+                            ctypes.c_int, _vp, _sz, _vp], ctypes.c_int),
     "mxfp8_moe_balance_workspace_bytes": ([_i64, _i64, ctypes.POINTER(_sz)], ctypes.c_int),
     "mxfp8_moe_balance": ([_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, ctypes.c_float, ctypes.c_float, _vp, _vp,
                            _vp, _vp, _sz, _vp], ctypes.c_int),
@@ -122,11 +123,14 @@ def _check(status, where):
 
 
 def _stream(device=None):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    """Handle of the device's current stream (an int; the Stream object that
+    torch.cuda.current_stream builds costs more than a small kernel)."""
+    index = None if device is None else device.index
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 # ---------------------------------------------------------------------------
@@ -525,11 +529,14 @@ def gemm_packed(pa, pw, bias=None):
 # FP8 with 128-blocks, and the layer's training side
 # ---------------------------------------------------------------------------
 
+_HERE_ALREADY = contextlib.nullcontext()
+
+
 def _on(device):
     """Context in which ``device`` is the current one (the library launches on
     the current device)."""
     if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+        return _HERE_ALREADY
     return torch.cuda.device(device)
 
 
@@ -546,7 +553,10 @@ def _scratch(need, device):
     return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
 
 
+@functools.lru_cache(maxsize=4096)
 def _bytes(query, *sizes):
+    """A host-only size query (a function of the sizes and the forced paths;
+    the hooks that force one clear the cache)."""
     b = _sz()
     _check(getattr(lib(), query)(*sizes, ctypes.byref(b)), query)
     return b.value
@@ -558,8 +568,9 @@ def _rows(x, name):
     if x.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be bfloat16, got {x.dtype}")
     _require_cuda(x, name)
-    x2 = x.reshape(-1, x.shape[-1])
-    if x2.stride(-1) != 1 or x2.stride(0) % 8 != 0 or x2.stride(0) < x2.shape[1] or x2.data_ptr() % 16 != 0:
+    x2 = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
+    row, col = x2.stride()
+    if col != 1 or row % 8 != 0 or row < x2.shape[1] or x2.data_ptr() % 16 != 0:
         x2 = x2.clone(memory_format=torch.contiguous_format)
     return x2
 
@@ -581,10 +592,12 @@ def mxfp8_linear_b128(x, M, K, ldx, wp, sp, N, bias, y, ldy, ws, ws_bytes, strea
 
 
 def mxfp8_debug_force_b128(tile):
+    _bytes.cache_clear()
     return lib().mxfp8_debug_force_b128(tile)
 
 
 def mxfp8_debug_force_wgrad(tile):
+    _bytes.cache_clear()
     return lib().mxfp8_debug_force_wgrad(tile)
 
 
@@ -646,11 +659,12 @@ def _linear_prepared_b128(x, pw, bias, out, workspace):
         raise ValueError(f"out must be bfloat16 [{M}, {N}] with contiguous rows that do not overlap")
     _same_device(x2, pw.w_packed, bias, out, workspace)
     with _on(x.device):
-        ws = workspace if workspace is not None else _scratch(mxfp8_linear_b128_workspace_bytes(M, N, K), x.device)
-        _check(mxfp8_linear_b128(_ptr(x2), M, K, x2.stride(0), _ptr(pw.w_packed), _ptr(pw.s_packed), N, _ptr(bias),
-                                 _ptr(out), out.stride(0), _ptr(ws), ws.numel(), _stream(x.device)),
-               "mxfp8_linear_b128")
-    return out.view(*x.shape[:-1], N)
+        need = _bytes("mxfp8_linear_b128_workspace_bytes", M, N, K)
+        ws = workspace if workspace is not None or need == 0 else _scratch(need, x.device)
+        _check(lib().mxfp8_linear_b128(_ptr(x2), M, K, x2.stride(0), _ptr(pw.w_packed), _ptr(pw.s_packed), N,
+                                       _ptr(bias), _ptr(out), out.stride(0), _ptr(ws), 0 if ws is None else ws.numel(),
+                                       _stream(x.device)), "mxfp8_linear_b128")
+    return out if x.dim() == 2 else out.view(*x.shape[:-1], N)
 
 
 def quantize_weight_b128(w):
@@ -721,8 +735,9 @@ def linear_wgrad(dy, pa, dtype=torch.float32, bias_grad=False, out=None, out_bia
 
     ``dy`` bf16 ``[..., N]`` with M rows, N % 8 == 0.  Returns ``dw`` (``dtype``
     float32 or bfloat16; ``out`` if given), or ``(dw, db)`` with ``bias_grad``,
-    ``db`` the fp32 column sums of dy (``out_bias`` if given).  ``accumulate``
-    adds to ``out`` (fp32) and ``out_bias`` instead of overwriting them."""
+    ``db`` the column sums of dy (``out_bias``, float32 or bfloat16, if given,
+    else fp32).  ``accumulate`` adds to ``out`` and ``out_bias`` (both fp32)
+    instead of overwriting them."""
     d2 = _rows(dy, "dy")
     M, N = d2.shape
     if M != pa.M:
@@ -733,48 +748,51 @@ def linear_wgrad(dy, pa, dtype=torch.float32, bias_grad=False, out=None, out_bia
         out = torch.empty((N, pa.K), dtype=dtype, device=dy.device)
     if tuple(out.shape) != (N, pa.K) or out.dtype not in _DTYPES or out.stride(-1) != 1:
         raise ValueError(f"out must be float32 or bfloat16 [{N}, {pa.K}] with contiguous rows")
-    if accumulate and out.dtype != torch.float32:
-        raise ValueError("accumulate needs a float32 out")
-    if bias_grad and out_bias is None:
-        out_bias = torch.empty(N, dtype=torch.float32, device=dy.device)
-    db = out_bias if bias_grad else None
-    if db is not None and (db.dtype != torch.float32 or tuple(db.shape) != (N,) or not db.is_contiguous()):
-        raise ValueError(f"out_bias must be contiguous float32 [{N}]")
+    db = None
+    if bias_grad:
+        db = out_bias if out_bias is not None else torch.empty(N, dtype=torch.float32, device=dy.device)
+        if db.dtype not in _DTYPES or tuple(db.shape) != (N,) or not db.is_contiguous():
+            raise ValueError(f"out_bias must be contiguous float32 or bfloat16 [{N}]")
+    if accumulate and (out.dtype != torch.float32 or (db is not None and db.dtype != torch.float32)):
+        raise ValueError("accumulate needs float32 outputs")
     _same_device(d2, pa.q_packed, out, db)
     with _on(dy.device):
         ws = _scratch(_bytes("mxfp8_linear_wgrad_workspace_bytes", M, N, pa.K), dy.device)
         _check(lib().mxfp8_linear_wgrad(_ptr(d2), M, N, d2.stride(0), _ptr(pa.q_packed), _ptr(pa.s_packed), pa.K,
-                                        _ptr(out), _DTYPES[out.dtype], out.stride(0), _ptr(db), int(accumulate),
-                                        _ptr(ws), ws.numel(), _stream(dy.device)), "mxfp8_linear_wgrad")
+                                        _ptr(out), _DTYPES[out.dtype], out.stride(0), _ptr(db),
+                                        0 if db is None else _DTYPES[db.dtype], int(accumulate), _ptr(ws), ws.numel(),
+                                        _stream(dy.device)), "mxfp8_linear_wgrad")
     return (out, db) if bias_grad else out
 
 
 class _LinearB128(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, bias):
-        pw, pt = prepare_weight_b128_bf16(w, transposed=x.requires_grad)
-        ctx.shape, ctx.pt, ctx.pa = x.shape, pt, None
-        ctx.types = w.dtype, None if bias is None else bias.dtype
-        if w.requires_grad or (bias is not None and bias.requires_grad):
+        need_x, need_w, need_b = ctx.needs_input_grad
+        pw, ctx.pt = prepare_weight_b128_bf16(w, transposed=need_x)
+        ctx.shape, ctx.pa = x.shape, None
+        if need_w or need_b:
             ctx.pa = quantize_act_packed_b128(x)
             y = gemm_packed(ctx.pa, pw, bias)
         else:
             y = linear(x.reshape(-1, x.shape[-1]), pw, bias)
-        return y.view(*x.shape[:-1], pw.N)
+        return y if x.dim() == 2 else y.view(*x.shape[:-1], pw.N)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
+        need_x, need_w, need_b = ctx.needs_input_grad
         d2 = _rows(dy, "dy")
         dx = dw = db = None
-        if ctx.needs_input_grad[0]:
-            dx = linear(d2, ctx.pt).view(ctx.shape)
-        if ctx.needs_input_grad[1] or ctx.needs_input_grad[2]:
-            want = ctx.needs_input_grad[2]
-            got = linear_wgrad(d2, ctx.pa, dtype=ctx.types[0], bias_grad=want)
-            dw, db = got if want else (got, None)
-            db = None if db is None else db.to(ctx.types[1])
-        return dx, dw if ctx.needs_input_grad[1] else None, db
+        if need_x:
+            dx = linear(d2, ctx.pt)
+            dx = dx if len(ctx.shape) == 2 else dx.view(ctx.shape)
+        if need_b:
+            db = torch.empty(d2.shape[1], dtype=torch.bfloat16, device=d2.device)
+            dw, db = linear_wgrad(d2, ctx.pa, dtype=torch.bfloat16, bias_grad=True, out_bias=db)
+        elif need_w:
+            dw = linear_wgrad(d2, ctx.pa, dtype=torch.bfloat16)
+        return dx, dw if need_w else None, db
 
 
 def linear_b128(x, w, bias=None):

@@ -56,7 +56,7 @@ size_t part_bytes(int64_t M, int64_t N, mxfp8::B128Plan p) {
 }
 
 size_t linear_ws(int64_t M, int64_t N, int64_t K) {
-  if (M <= mxfp8::kB128DecodeMaxM) return 256;
+  if (M <= mxfp8::kB128DecodeMaxM) return 0;
   return round_up(act_bytes(M, K), 256) + round_up(act_scale_bytes(M, K), 256) +
          part_bytes(M, N, mxfp8::b128_plan(M, N, K));
 }
@@ -175,7 +175,8 @@ int mxfp8_linear_b128(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, con
   if (ldx < K || ldx % 8 != 0) return MXFP8_E_LD;
   if (!aligned(x_bf16, 16)) return MXFP8_E_ALIGN;
   if (!gemm_grid_ok(M, N) || !act_grid_ok(M, K)) return MXFP8_E_SHAPE;
-  if (!workspace || workspace_bytes < linear_ws(M, N, K)) return MXFP8_E_WORKSPACE;
+  const size_t need = linear_ws(M, N, K);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MXFP8_E_WORKSPACE;
   if (!aligned(workspace, 256)) return MXFP8_E_ALIGN;
   if (int st = mxfp8::check_device_current()) return st;
   hipStream_t s = (hipStream_t)stream;
@@ -236,15 +237,17 @@ int mxfp8_debug_force_wgrad(int tile) {
 }
 
 int mxfp8_linear_wgrad(const void* dy_bf16, int64_t M, int64_t N, int64_t lddy, const void* q_packed,
-                       const void* s_packed, int64_t K, void* dw, int dw_dtype, int64_t lddw, float* db,
-                       int accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+                       const void* s_packed, int64_t K, void* dw, int dw_dtype, int64_t lddw, void* db,
+                       int db_dtype, int accumulate, void* workspace, size_t workspace_bytes, void* stream) {
   if (M < 0 || M > kMaxRows || !rows_ok(N) || N % 8 != 0 || !summed_ok(K)) return MXFP8_E_SHAPE;
-  if ((dw_dtype != MXFP8_F32 && dw_dtype != MXFP8_BF16) || (accumulate && dw_dtype != MXFP8_F32)) return MXFP8_E_SHAPE;
+  if (dw_dtype != MXFP8_F32 && dw_dtype != MXFP8_BF16) return MXFP8_E_SHAPE;
+  if (db && db_dtype != MXFP8_F32 && db_dtype != MXFP8_BF16) return MXFP8_E_SHAPE;
+  if (accumulate && (dw_dtype != MXFP8_F32 || (db && db_dtype != MXFP8_F32))) return MXFP8_E_SHAPE;
   if (!dw || (M > 0 && (!dy_bf16 || !q_packed || !s_packed))) return MXFP8_E_NULLPTR;
   if (lddw < K || lddw % 8 != 0) return MXFP8_E_LD;
   // 64 rows of dY are addressed with 32-bit byte offsets.
   if (M > 0 && (lddy < N || lddy % 8 != 0 || lddy > kMaxK)) return MXFP8_E_LD;
-  if (!aligned(dw, 16) || !aligned(db, 4)) return MXFP8_E_ALIGN;
+  if (!aligned(dw, 16) || !aligned(db, db_dtype == MXFP8_F32 ? 4 : 2)) return MXFP8_E_ALIGN;
   if (M > 0 && (!aligned(dy_bf16, 16) || !aligned(q_packed, 256) || !aligned(s_packed, 256))) return MXFP8_E_ALIGN;
   const mxfp8::WgradPlan p = mxfp8::wgrad_plan(M, N, K);
   if (b128_blocks(N) * b128_blocks(K) * p.splits > INT32_MAX || N * (K / 4) / 256 >= INT32_MAX - N)
@@ -267,6 +270,7 @@ int mxfp8_linear_wgrad(const void* dy_bf16, int64_t M, int64_t N, int64_t lddy, 
   a.out_bf16 = dw_dtype == MXFP8_BF16;
   a.accumulate = accumulate != 0;
   a.db = db;
+  a.db_bf16 = db_dtype == MXFP8_BF16;
   a.part_dw = (float*)workspace;
   a.part_db = (float*)((uint8_t*)workspace + round_up(mxfp8::wgrad_dw_bytes(M, N, K, p), 256));
   return mxfp8::launch_wgrad(a, p, (hipStream_t)stream);

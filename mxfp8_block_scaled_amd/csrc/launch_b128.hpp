@@ -94,7 +94,8 @@ struct WgradArgs {
   int64_t lddw;
   int out_bf16;
   int accumulate;       // dw += and db += (dw fp32)
-  float* db;            // [N] or null
+  void* db;             // [N] or null: fp32, or bf16 if db_bf16
+  int db_bf16;
   float* part_dw;
   float* part_db;
 };

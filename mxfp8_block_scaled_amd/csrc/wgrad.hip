@@ -48,6 +48,11 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 __device__ inline int slot_xor(int m) { return (m & 3) | ((m >> 1) & 4); }
 
+__device__ inline void store_db(void* db, int bf16, int accumulate, int64_t n, float v) {
+  if (bf16) ((uint16_t*)db)[n] = (uint16_t)pack_bf16x2(v, 0.0f);
+  else ((float*)db)[n] = accumulate ? ((float*)db)[n] + v : v;
+}
+
 template <int kT>
 struct WgLds {
   static constexpr int kPitch = kT * 2;
@@ -232,13 +237,31 @@ __global__ __launch_bounds__(kWgThreads, 2) void wgrad_kernel(
   }
 }
 
-// dw = sum of the split partials in order (+ dw), db = sum of its partials in
-// order.  One thread per 4 k of dW, then one per n of db.
+// dw = sum of the split partials in order (+ dw): one thread per 4 k.  db =
+// sum of its partials: the last workgroups, sixteen columns each, thread
+// (q, c) parts q, q + 16, ... of column c, then the sixteen sums in order.
 __global__ __launch_bounds__(256) void wgrad_reduce_kernel(const float* __restrict__ part, int splits, int64_t N,
                                                            int64_t K, void* __restrict__ dw, int64_t lddw,
                                                            int out_bf16, int accumulate, int64_t quads,
                                                            const float* __restrict__ part_db, int parts_db,
-                                                           float* __restrict__ db) {
+                                                           void* __restrict__ db, int db_bf16) {
+  const int64_t dw_blocks = (quads + 255) / 256;
+  if ((int64_t)blockIdx.x >= dw_blocks) {
+    __shared__ float red[16][17];
+    const int c = threadIdx.x & 15, q = threadIdx.x >> 4;
+    const int64_t n = ((int64_t)blockIdx.x - dw_blocks) * 16 + c;
+    float v = 0.0f;
+    if (n < N)
+      for (int p = q; p < parts_db; p += 16) v += part_db[(size_t)p * N + n];
+    red[q][c] = v;
+    __syncthreads();
+    if (q != 0 || n >= N) return;
+    v = 0.0f;
+#pragma unroll
+    for (int p = 0; p < 16; ++p) v += red[p][c];
+    store_db(db, db_bf16, accumulate, n, v);
+    return;
+  }
   const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (t < quads) {
     const int64_t per_row = K / 4, n = t / per_row, k = (t - n * per_row) * 4;
@@ -253,11 +276,6 @@ __global__ __launch_bounds__(256) void wgrad_reduce_kernel(const float* __restri
     }
     return;
   }
-  const int64_t n = t - quads;
-  if (n >= N || db == nullptr) return;
-  float a = 0.0f;
-  for (int p = 0; p < parts_db; ++p) a += part_db[(size_t)p * N + n];
-  db[n] = accumulate ? db[n] + a : a;
 }
 
 // ---------------------------------------------------------------------------
@@ -522,7 +540,7 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(const float* __restrict
                                                          int tiles_k, int steps, int N, int K, void* __restrict__ dw,
                                                          int64_t lddw, int out_bf16, int accumulate,
                                                          const float* __restrict__ part_db, int pieces,
-                                                         float* __restrict__ db) {
+                                                         void* __restrict__ db, int db_bf16) {
   const int tid = threadIdx.x;
   if ((int)blockIdx.x >= tiles * 16) {
     // sixteen columns: thread (q, c) adds the tiles q, q + 16, ... along k
@@ -543,7 +561,7 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(const float* __restrict
     v = 0.0f;
 #pragma unroll
     for (int p = 0; p < 16; ++p) v += red[p][c];
-    db[n] = accumulate ? db[n] + v : v;
+    store_db(db, db_bf16, accumulate, n, v);
     return;
   }
   const int t = (int)blockIdx.x >> 4, sub = (int)blockIdx.x & 15;
@@ -663,7 +681,7 @@ int launch_big(const WgradArgs& a, WgradPlan p, hipStream_t stream) {
   const int join = b.shared ? (int)b.tiles : 0, cols = kBias ? (int)((a.N + 15) / 16) : 0;
   hipLaunchKernelGGL(wgrad_join_kernel, dim3((unsigned)(join * 16 + cols)), dim3(256), 0, stream, a.part_dw, b.U,
                      p.runs, join, (int)b.tiles_k, (int)b.steps, (int)a.N, (int)a.K, a.dw, a.lddw, a.out_bf16,
-                     a.accumulate, a.part_db, (int)b.pieces, a.db);
+                     a.accumulate, a.part_db, (int)b.pieces, a.db, a.db_bf16);
   return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 }  // namespace
@@ -673,10 +691,11 @@ int launch_wgrad(const WgradArgs& a, WgradPlan p, hipStream_t stream) {
   if (p.tile == 256) return bias ? launch_big<true>(a, p, stream) : launch_big<false>(a, p, stream);
   const int st = bias ? launch_small<true>(a, p, stream) : launch_small<false>(a, p, stream);
   if (st || (p.splits == 1 && !bias)) return st;
-  const int64_t quads = p.splits > 1 ? a.N * (a.K / 4) : 0, total = quads + (bias ? a.N : 0);
+  const int64_t quads = p.splits > 1 ? a.N * (a.K / 4) : 0;
+  const int64_t blocks = (quads + 255) / 256 + (bias ? (a.N + 15) / 16 : 0);
   const int parts_db = p.splits * (int)((a.K + 127) / 128);
-  hipLaunchKernelGGL(wgrad_reduce_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, stream, a.part_dw,
-                     p.splits, a.N, a.K, a.dw, a.lddw, a.out_bf16, a.accumulate, quads, a.part_db, parts_db, a.db);
+  hipLaunchKernelGGL(wgrad_reduce_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a.part_dw, p.splits, a.N, a.K, a.dw,
+                     a.lddw, a.out_bf16, a.accumulate, quads, a.part_db, parts_db, a.db, a.db_bf16);
   return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 

@@ -68,12 +68,16 @@ def test_weight_b128():
 def test_linear_b128(M):
     N, K = 130, 272
     ws = api.mxfp8_linear_b128_workspace_bytes(M, N, K)
-    assert ws >= (256 if M <= 16 else 384 * 384)
+    assert ws == 0 if M <= 16 else ws >= 384 * 384
     refuse(api.mxfp8_linear_b128, (P, M, K, K, P, P, N, None, P, N, P, ws, None), [
         (1, -1, SHAPE), (1, 0, OK), (2, 264, SHAPE), (6, 0, SHAPE), (0, None, NULLPTR), (4, None, NULLPTR),
-        (5, None, NULLPTR), (8, None, NULLPTR), (3, 264, LD), (3, 276, LD), (9, 129, LD), (10, None, WORKSPACE),
-        (11, ws - 1, WORKSPACE), (10, P + 64, ALIGN), (0, P + 8, ALIGN), (4, P + 64, ALIGN), (5, P + 64, ALIGN),
-        (7, P + 1, ALIGN), (8, P + 1, ALIGN)])
+        (5, None, NULLPTR), (8, None, NULLPTR), (3, 264, LD), (3, 276, LD), (9, 129, LD), (10, P + 64, ALIGN),
+        (0, P + 8, ALIGN), (4, P + 64, ALIGN), (5, P + 64, ALIGN), (7, P + 1, ALIGN), (8, P + 1, ALIGN)])
+    if ws:
+        refuse(api.mxfp8_linear_b128, (P, M, K, K, P, P, N, None, P, N, P, ws, None), [
+            (10, None, WORKSPACE), (11, ws - 1, WORKSPACE)])
+    else:                                          # decode: no workspace
+        expect_no_device(api.mxfp8_linear_b128, P, M, K, K, P, P, N, None, P, N, None, 0, None)
     need = api._bytes("mxfp8_gemm_packed_b128_workspace_bytes", M, N, K)
     refuse(api.lib().mxfp8_gemm_packed_b128, (P, P, M, K, P, P, N, None, P, N, P, need, None), [
         (2, -1, SHAPE), (2, 0, OK), (3, 264, SHAPE), (6, 0, SHAPE), (0, None, NULLPTR), (1, None, NULLPTR),
@@ -98,15 +102,16 @@ def test_wgrad():
     M, N, K = 100, 136, 272
     fn = api.lib().mxfp8_linear_wgrad
     need = api._bytes("mxfp8_linear_wgrad_workspace_bytes", M, N, K)
-    ok = (P, M, N, N, P, P, K, P, 0, K, P, 0, P, need, None)
+    ok = (P, M, N, N, P, P, K, P, 0, K, P, 0, 0, P, need, None)
     refuse(fn, ok, [
         (1, -1, SHAPE), (2, 0, SHAPE), (2, 132, SHAPE), (6, 264, SHAPE), (8, 2, SHAPE), (0, None, NULLPTR),
         (4, None, NULLPTR), (5, None, NULLPTR), (7, None, NULLPTR), (3, 128, LD), (3, 140, LD), (3, (1 << 24) + 8, LD),
         (9, 264, LD), (9, 276, LD), (0, P + 8, ALIGN), (7, P + 8, ALIGN), (10, P + 2, ALIGN), (4, P + 16, ALIGN),
-        (5, P + 16, ALIGN), (12, None, WORKSPACE), (13, need - 1, WORKSPACE), (12, P + 16, ALIGN)])
-    bf16 = list(ok)
-    bf16[8], bf16[11] = 1, 1
-    assert fn(*bf16) == SHAPE                      # accumulation is fp32
+        (5, P + 16, ALIGN), (11, 2, SHAPE), (13, None, WORKSPACE), (14, need - 1, WORKSPACE), (13, P + 16, ALIGN)])
+    for at in (8, 11):                             # accumulation is fp32
+        bf16 = list(ok)
+        bf16[at], bf16[12] = 1, 1
+        assert fn(*bf16) == SHAPE
     empty = list(ok)
     empty[0] = empty[4] = empty[5] = None          # no tokens: no operands
     empty[1], empty[3] = 0, 0

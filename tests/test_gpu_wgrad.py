@@ -52,6 +52,9 @@ def test_wgrad(M, N, K, form, dtype):
     dw, db = api.linear_wgrad(dy.to(dev()), pa, dtype=dtype, bias_grad=True)
     assert dw.dtype == dtype and dw.shape == (N, K) and db.dtype == torch.float32
     check_dw(dw, db, dy, X)
+    half = torch.empty(N, dtype=torch.bfloat16, device=dev())
+    assert api.linear_wgrad(dy.to(dev()), pa, dtype=dtype, bias_grad=True, out_bias=half)[1] is half
+    assert torch.equal(half, db.to(torch.bfloat16))
     assert torch.equal(dw, api.linear_wgrad(dy.to(dev()), pa, dtype=dtype))
 
 
