@@ -424,10 +424,11 @@ int mxfp8_gemm_packed_b128(const void* q_packed, const void* s_packed, int64_t M
 
 /*
  * Test hook: pin the tiles of the 128-block GEMM (M > 16 and the packed
- * entry): 0 = by shape, 64 / 128 = 128 columns x that many rows (with K
- * splits), 256 = 256 x 128 tiles where the shape allows (K > 384, N % 8 == 0,
- * y 16-byte aligned with ldy % 8 == 0), else 128.  The workspace queries
- * follow it.  Process-wide; returns the previous value, or MXFP8_E_SHAPE.
+ * entry): 0 = by shape, 64 / 128 = 128 weight rows x that many activation
+ * rows (with K splits), 256 / 512 = 256 x 128 / 256 x 256.  All but 64 need
+ * N % 8 == 0, and y 16-byte aligned with ldy % 8 == 0 where K is not split;
+ * else the 64-row tiles run.  The workspace queries follow it.  Process-wide;
+ * returns the previous value, or MXFP8_E_SHAPE.
  */
 int mxfp8_debug_force_b128(int tile);
 

@@ -219,7 +219,7 @@ int mxfp8_gemm_packed_b128(const void* q_packed, const void* s_packed, int64_t M
 }
 
 int mxfp8_debug_force_b128(int tile) {
-  if (tile != 0 && tile != 64 && tile != 128 && tile != 256) return MXFP8_E_SHAPE;
+  if (tile != 0 && tile != 64 && tile != 128 && tile != 256 && tile != 512) return MXFP8_E_SHAPE;
   return mxfp8::b128_force(tile);
 }
 

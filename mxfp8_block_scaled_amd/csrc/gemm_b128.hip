@@ -198,37 +198,40 @@ int launch_gemm_b128_decode(const void* x, int64_t ldx, int64_t M, int64_t K, co
 }
 
 // ---------------------------------------------------------------------------
-// Tiles: one 128-row weight group x kMT activation rows per workgroup over a
-// run of 128-blocks, four waves 2 x 2; wave (wn, wm) owns weight rows
+// Small tiles: one 128-row weight group x 64 activation rows per workgroup over
+// a run of 128-blocks, four waves 2 x 2; wave (wn, wm) owns weight rows
 // 32 a + 16 wn + i and activation rows 32 b + 16 wm + i, so the byte of a
 // row's scale inside its packed word (rows r + 32 k, byte k) is b, an
 // immediate op_sel.  Stages of 64 K come straight from global memory into
-// LDS; a 128-block reads a pair of stages; two pairs are in flight.
+// LDS; a 128-block reads a pair of stages; kDepth pairs are in LDS
+// (three: two workgroups share a compute unit and cover each other's waits).
 // ---------------------------------------------------------------------------
 namespace {
 constexpr int kB128Threads = 256;
 
-template <int kMT>
-struct B128Lds {
+constexpr int kMT = 64;      // activation rows
+constexpr int kDepth = 3;    // pairs of stages (128-blocks) in LDS
+
+struct SmallLds {
   static constexpr int kW = kGroupRows * kStepK;
   static constexpr int kX = kMT * kStepK;
   // + the activations' 256-byte scale tile, copied by wave 0; the other
   // waves' scale copies go to slots of their own, so every wave issues the
   // same number of copies (the waits count them per wave).
   static constexpr int kStage = kW + kX + 1024;
-  static constexpr int kBytes = 4 * kStage;
+  static constexpr int kBytes = 2 * kDepth * kStage;
   static constexpr int kCopies = 2 * (2 + kMT / 64 + 1);
   static constexpr int kPitchY = 128 * 2 + 16;
   static_assert(kMT * kPitchY <= kBytes, "the output staging fits in the stages");
 };
 }  // namespace
 
-template <int kMT, bool kPart>
-__global__ __launch_bounds__(kB128Threads, 2) void gemm_b128_kernel(
+template <bool kPart>
+__global__ __launch_bounds__(kB128Threads, 2) void gemm_b128_small_kernel(
     const uint8_t* __restrict__ qp, const uint8_t* __restrict__ sp, int M, int KB, const uint8_t* __restrict__ wp,
     const float* __restrict__ wsc, int N, const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, int64_t ldy,
     int tiles_n, int tiles_m, int splits, int vec, float* __restrict__ part, int64_t ldp) {
-  using L = B128Lds<kMT>;
+  using L = SmallLds;
   constexpr int kNB = kMT / 32;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
 
@@ -255,25 +258,22 @@ __global__ __launch_bounds__(kB128Threads, 2) void gemm_b128_kernel(
             brsrc, (uint32_t)(n0 + 32 * a + 16 * wn + 4 * g + j) * 2u, 0, 0);
   }
 
-  // Copies: wave w takes bands w and w + 4 of the weight group and of the
-  // activation group (kMT = 64: band 4 h + w of half h of group tm / 2).
-  const int h = kMT == 64 ? (tm & 1) : 0;
-  const int xg = kMT == 64 ? (tm >> 1) : tm;
+  // Copies: wave w takes bands w and w + 4 of the weight group and band
+  // 4 h + w of the activation group, whose half h is the tile's.
+  const int h = tm & 1, xg = tm >> 1;
   const uint32_t gbytes = (uint32_t)KS * kTileBytes, sbytes = (uint32_t)KS * kTileScaleBytes;
   const tile::i4v wr = tile::buffer_rsrc(wp + (size_t)tn * gbytes, gbytes);
   const tile::i4v xr = tile::buffer_rsrc(qp + (size_t)xg * gbytes, gbytes);
   const tile::i4v sr = tile::buffer_rsrc(sp + (size_t)xg * sbytes, sbytes);
   const uint32_t lo16 = (uint32_t)lane * 16u;
   const uint32_t vw0 = (uint32_t)wave * KS * kPieceBytes + lo16, vw1 = vw0 + 4u * KS * kPieceBytes;
-  const uint32_t vx0 = (uint32_t)(kMT == 64 ? 4 * h + wave : wave) * KS * kPieceBytes + lo16;
-  const uint32_t vx1 = vx0 + 4u * KS * kPieceBytes;
+  const uint32_t vx = (uint32_t)(4 * h + wave) * KS * kPieceBytes + lo16;
   const uint32_t vs = (uint32_t)lane * 4u;
   auto issue_stage = [&](int ks, uint8_t* st) {
     const uint32_t off = (uint32_t)ks * kPieceBytes;
     tile::b2l_16(vw0, wr, off, st + wave * 1024);
     tile::b2l_16(vw1, wr, off, st + 4096 + wave * 1024);
-    tile::b2l_16(vx0, xr, off, st + L::kW + wave * 1024);
-    if constexpr (kMT == 128) tile::b2l_16(vx1, xr, off, st + L::kW + 4096 + wave * 1024);
+    tile::b2l_16(vx, xr, off, st + L::kW + wave * 1024);
     tile::b2l_4(vs, sr, (uint32_t)ks * kTileScaleBytes, st + L::kW + L::kX + wave * 256);
   };
   auto stage_ptr = [&](int s) { return smem + s * L::kStage; };
@@ -294,35 +294,37 @@ __global__ __launch_bounds__(kB128Threads, 2) void gemm_b128_kernel(
     for (int b = 0; b < kNB; ++b) acc[a][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
   const float* wsg = wsc + (size_t)tn * KB;
-  issue_stage(2 * p0, stage_ptr(0));
-  issue_stage(2 * p0 + 1, stage_ptr(1));
-  if (p0 + 1 < p1) {
-    issue_stage(2 * p0 + 2, stage_ptr(2));
-    issue_stage(2 * p0 + 3, stage_ptr(3));
+  // Every step issues one block's copies, past the run's end those of its
+  // last block again (into a buffer nobody reads any more), so the wait for
+  // block p always leaves the copies of kDepth - 1 newer blocks in flight.
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d) {
+    const int q = min(p0 + d, p1 - 1);
+    issue_stage(2 * q, stage_ptr(2 * d));
+    issue_stage(2 * q + 1, stage_ptr(2 * d + 1));
   }
+  int at = 0;   // the block's pair of stages
   for (int p = p0; p < p1; ++p) {
     const float ws = scalar_scale(wsg, p);
-    if (p + 1 < p1)
-      tile::wait_vmcnt<L::kCopies>();
-    else
-      tile::wait_vmcnt<0>();
+    tile::wait_vmcnt<(kDepth - 1) * L::kCopies>();
     __builtin_amdgcn_s_barrier();
-    const int par = (p - p0) & 1;
-    const uint8_t* ev = stage_ptr(2 * par);
+    const uint8_t* ev = stage_ptr(2 * at);
     const uint8_t* od = ev + L::kStage;
     v8i wf[4], xf[kNB];
 #pragma unroll
     for (int a = 0; a < 4; ++a) wf[a] = frag(ev, od, offW + 32 * kStepK * a);
 #pragma unroll
     for (int b = 0; b < kNB; ++b) xf[b] = frag(ev, od, offX + 32 * kStepK * b);
-    int sx = *reinterpret_cast<const int*>(((g >> 1) ? od : ev) + offSX);
-    if constexpr (kMT == 64) sx = (int)((uint32_t)sx >> (16 * h));
+    // the word's bytes are rows r + 32 k of the 128-row group: the half's are 2 h + b
+    const int sx = (int)(*reinterpret_cast<const uint32_t*>(((g >> 1) ? od : ev) + offSX) >> (16 * h));
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
-    if (p + 2 < p1) {
-      issue_stage(2 * p + 4, stage_ptr(2 * par));
-      issue_stage(2 * p + 5, stage_ptr(2 * par + 1));
+    {
+      const int q = min(p + kDepth, p1 - 1);
+      issue_stage(2 * q, stage_ptr(2 * at));
+      issue_stage(2 * q + 1, stage_ptr(2 * at + 1));
     }
+    at = at + 1 == kDepth ? 0 : at + 1;
     tile::static_for<0, 4>([&](auto A) {
       constexpr int a = decltype(A)::value;
       tile::static_for<0, kNB>([&](auto B) {
@@ -334,6 +336,8 @@ __global__ __launch_bounds__(kB128Threads, 2) void gemm_b128_kernel(
       });
     });
   }
+
+  tile::wait_vmcnt<0>();   // the last copies, before their LDS is reused or given away
 
   // Lane (i, g) holds D[n = 32 a + 16 wn + 4 g + j][m = 32 b + 16 wm + i].
   const int mt0 = tm * kMT;
@@ -383,31 +387,37 @@ __global__ __launch_bounds__(kB128Threads, 2) void gemm_b128_kernel(
 }
 
 // ---------------------------------------------------------------------------
-// Large tiles: 256 weight rows (two groups) x 128 activation rows per
-// workgroup, four waves 2 x 2, each 128 x 64 (32 MFMAs per 128-block).
-//  * The accumulators are 128 vector registers per lane; the operand
+// Large tiles: kG weight groups (128 kG rows) x 128 activation rows per
+// workgroup, four waves 2 x 2, each 64 kG x 64 (16 kG MFMAs per 128-block).
+//  * The accumulators are 64 kG vector registers per lane; the operand
 //    fragments of the current and of the next block sit in registers too
-//    (96 + 96, one wave per SIMD has 512), so no MFMA waits for LDS.
-//  * LDS holds three blocks (3 x 49 KiB).  At the top of step p the copies of
-//    p + 1 have landed everywhere (own vmcnt, then the one barrier of the
-//    step), every wave has read p, and the copies of p + 3 go out into p's
-//    buffer: a copy has two whole steps to land.
+//    (96 + 96 for kG = 2; one wave per SIMD has 512), so no MFMA waits for
+//    LDS.
+//  * LDS holds kDepth blocks (3 x 49 or 4 x 33 KiB).  At the top of step p the
+//    copies of p + 1 have landed everywhere (own vmcnt, then the one barrier
+//    of the step), every wave has read p, and the copies of p + kDepth go out
+//    into p's buffer: a copy has kDepth - 1 whole steps to land.
 //  * The MFMAs of a step carry between them the v_fma of the results three
-//    MFMAs back (nearer ones are not there yet), the LDS reads of the next step's fragments and the copies.
-//  * Workgroups are persistent and the pipeline runs across tiles: the last
-//    steps of a tile copy and read the next one's first blocks.  The epilogue
-//    issues a fixed sixteen 16-byte stores per wave (rows and columns outside
-//    are dropped by the buffer bounds), left in flight into the next tile.
+//    MFMAs back (nearer ones are not there yet), the LDS reads of the next
+//    step's fragments and the copies.
+//  * Workgroups are persistent and the pipeline runs across items (a tile, or
+//    with kPart a tile's run of blocks): the last steps of an item copy and
+//    read the next one's first blocks.  The epilogue issues a fixed number of
+//    16-byte stores per wave (rows and columns outside are dropped by the
+//    buffer bounds), left in flight into the next item.
 // ---------------------------------------------------------------------------
 namespace {
 
-constexpr int kBigX = 16384;                       // activation pieces inside a 64-K half
-constexpr int kBigHalf = 16384 + 8192;             // 256 weight rows + 128 activation rows x 64 B
-constexpr int kBigScale = 2 * kBigHalf;            // two 256-byte scale tiles, then two unused slots
-constexpr int kBigBlock = 2 * kBigHalf + 1024;
-constexpr int kBigLds = 3 * kBigBlock;             // 150528
-constexpr int kBigCopies = 13;                     // per wave and block
-constexpr int kBigStores = 16;                     // per wave and tile
+template <int kG>
+struct BigLds {
+  static constexpr int kX = 8192 * kG;               // activation pieces inside a 64-K half
+  static constexpr int kHalf = kX + 8192;
+  static constexpr int kScale = 2 * kHalf;           // two 256-byte scale tiles, then two unused slots
+  static constexpr int kBlock = kScale + 1024;
+  static constexpr int kDepth = kG == 2 ? 3 : 4;     // blocks in LDS
+  static constexpr int kBytes = kDepth * kBlock;
+  static constexpr int kCopies = 4 * kG + 5;         // per wave and block
+};
 
 // Tile order: bands of eight activation tiles, inside a band the weight tiles
 // outermost, so the tiles a die runs together share both operands.
@@ -424,12 +434,45 @@ __device__ inline BigTile big_tile(int item, int tiles_n, int tiles_m) {
   return t;
 }
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// Stores two neighbouring 16-column tiles of a wave (lane (i, g) holds columns
+// 4 g .. + 3 of row i of each) as bf16: exchanging the odd 16-lane rows of the
+// first with the even ones of the second gives every lane eight consecutive
+// columns, of the first tile for even g, of the second for odd g.  at: the
+// byte offset of its eight, past the end to drop them.
+__device__ inline void store_pair(const v4f& lo, const v4f& hi, const float (&bl)[4], const float (&bh)[4],
+                                  __amdgpu_buffer_rsrc_t yr, uint32_t at) {
+  const uint32_t l0 = pack_bf16x2(lo[0] + bl[0], lo[1] + bl[1]), l1 = pack_bf16x2(lo[2] + bl[2], lo[3] + bl[3]);
+  const uint32_t h0 = pack_bf16x2(hi[0] + bh[0], hi[1] + bh[1]), h1 = pack_bf16x2(hi[2] + bh[2], hi[3] + bh[3]);
+  const auto s0 = __builtin_amdgcn_permlane16_swap(l0, h0, false, false);
+  const auto s1 = __builtin_amdgcn_permlane16_swap(l1, h1, false, false);
+  const u32x4 o = {s0[0], s1[0], s0[1], s1[1]};
+  __builtin_amdgcn_raw_buffer_store_b128(o, yr, at, 0, 0);
+}
+constexpr uint32_t kDrop = 0xFFFFFFF0u;
+
+// Bias of columns n .. n + 3 (0 past N, and with a null bias).
+__device__ inline void bias4(const uint16_t* bias, int N, int n, float (&v)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = 0.0f;
+  if (bias == nullptr) return;   // no load: waiting for one would drain the copies in flight
+  const __amdgpu_buffer_rsrc_t r = raw_rsrc(bias, (uint32_t)N * 2u);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    v[j] = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, (uint32_t)(n + j) * 2u, 0, 0) << 16);
+}
+
 }  // namespace
 
+template <int kG, bool kPart>
 __global__ __launch_bounds__(kB128Threads, 1) void gemm_b128_big_kernel(
     const uint8_t* __restrict__ qp, const uint8_t* __restrict__ sp, int M, int KB, const uint8_t* __restrict__ wp,
     const float* __restrict__ wsc, int N, const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, int64_t ldy,
-    int GN, int tiles_n, int tiles_m, int total) {
+    int GN, int tiles_n, int tiles_m, int lsplits, int total, float* __restrict__ part, int64_t ldp) {
+  using L = BigLds<kG>;
+  constexpr int kA = 4 * kG;                          // 16-row weight fragments per wave
+  constexpr int kStores = kPart ? 4 * kA : 2 * kA;    // per wave and item
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -438,60 +481,69 @@ __global__ __launch_bounds__(kB128Threads, 1) void gemm_b128_big_kernel(
   const int KS = 2 * KB;
   const uint32_t gbytes = (uint32_t)KS * kTileBytes, sbytes = (uint32_t)KS * kTileScaleBytes;
 
-  // This workgroup's tiles: items wg, wg + grid, ... of the die-wise order.
+  // This workgroup's items: wg, wg + grid, ... of the die-wise order.
   const int grid = (int)gridDim.x;
   const int mine = (total - (int)blockIdx.x + grid - 1) / grid;
-  const int steps = mine * KB;
-  auto tile_at = [&](int j) { return big_tile(xcd_remap((int)blockIdx.x + j * grid, total), tiles_n, tiles_m); };
+  struct Item {
+    BigTile t;
+    int split, p0, p1;
+  };
+  auto item_at = [&](int j) {
+    const int id = xcd_remap((int)blockIdx.x + j * grid, total);
+    Item r;
+    r.split = kPart ? id & ((1 << lsplits) - 1) : 0;   // a power of two of them
+    r.t = big_tile(kPart ? id >> lsplits : id, tiles_n, tiles_m);
+    const int each = KB >> lsplits, more = KB & ((1 << lsplits) - 1);   // the first `more` runs are one longer
+    r.p0 = kPart ? r.split * each + min(r.split, more) : 0;
+    r.p1 = kPart ? r.p0 + each + (r.split < more ? 1 : 0) : KB;
+    return r;
+  };
 
-  // Copy side: the tile the next copies belong to.
+  // Copy side: the item the next copies belong to.
+  // (Carried from step to step as addresses: resources carried through the
+  // loop end up in vector registers.)
   struct Src {
+    const uint8_t *w0, *w1, *x, *s;
+  };
+  struct Rsrc {
     tile::i4v w0, w1, x, s;
   };
   auto src_of = [&](BigTile t) {
-    Src r;
-    const int g1 = min(2 * t.tn + 1, GN - 1);      // past the last group: any data, its columns are dropped
-    r.w0 = tile::buffer_rsrc(wp + (size_t)(2 * t.tn) * gbytes, gbytes);
-    r.w1 = tile::buffer_rsrc(wp + (size_t)g1 * gbytes, gbytes);
-    r.x = tile::buffer_rsrc(qp + (size_t)t.tm * gbytes, gbytes);
-    r.s = tile::buffer_rsrc(sp + (size_t)t.tm * sbytes, sbytes);
-    return r;
+    const int g1 = kG == 2 ? min(2 * t.tn + 1, GN - 1) : t.tn;   // past the last group: any data, its columns are dropped
+    return Src{wp + (size_t)(kG * t.tn) * gbytes, wp + (size_t)g1 * gbytes, qp + (size_t)t.tm * gbytes,
+               sp + (size_t)t.tm * sbytes};
+  };
+  auto rsrc_of = [&](const Src& r) {
+    return Rsrc{tile::buffer_rsrc(r.w0, gbytes), tile::buffer_rsrc(r.w1, gbytes), tile::buffer_rsrc(r.x, gbytes),
+                tile::buffer_rsrc(r.s, sbytes)};
   };
   const uint32_t v0 = (uint32_t)wave * KS * kPieceBytes + (uint32_t)lane * 16u, v1 = v0 + 4u * KS * kPieceBytes;
   const uint32_t vs = (uint32_t)lane * 4u;
-  auto copy = [&](int j, const Src& r, int p, uint8_t* st) {
-    const uint32_t off = (uint32_t)(2 * p) * kPieceBytes;
-    uint8_t* b = st + wave * 1024;
-    switch (j) {
-      case 0: tile::b2l_16(v0, r.w0, off, b); break;
-      case 1: tile::b2l_16(v1, r.w0, off, b + 4096); break;
-      case 2: tile::b2l_16(v0, r.w1, off, b + 8192); break;
-      case 3: tile::b2l_16(v1, r.w1, off, b + 12288); break;
-      case 4: tile::b2l_16(v0, r.x, off, b + kBigX); break;
-      case 5: tile::b2l_16(v1, r.x, off, b + kBigX + 4096); break;
-      case 6: tile::b2l_16(v0, r.w0, off + kPieceBytes, b + kBigHalf); break;
-      case 7: tile::b2l_16(v1, r.w0, off + kPieceBytes, b + kBigHalf + 4096); break;
-      case 8: tile::b2l_16(v0, r.w1, off + kPieceBytes, b + kBigHalf + 8192); break;
-      case 9: tile::b2l_16(v1, r.w1, off + kPieceBytes, b + kBigHalf + 12288); break;
-      case 10: tile::b2l_16(v0, r.x, off + kPieceBytes, b + kBigHalf + kBigX); break;
-      case 11: tile::b2l_16(v1, r.x, off + kPieceBytes, b + kBigHalf + kBigX + 4096); break;
-      default:
-        // waves 0 and 1 copy the block's two scale tiles, 2 and 3 copy them to the unused slots
-        tile::b2l_4(vs, r.s, (uint32_t)(2 * p + (wave & 1)) * kTileScaleBytes, st + kBigScale + wave * 256);
-        break;
+  // Copy j of a block: both 64-K halves of the wave's two bands of each
+  // weight group, then of the activation group, then a scale tile (waves 2
+  // and 3 copy theirs to the unused slots).
+  auto copy = [&](auto J, const Rsrc& r, int p, uint8_t* st) {
+    constexpr int j = decltype(J)::value;
+    if constexpr (j < 4 * kG + 4) {
+      constexpr int half = j & 1, band = (j >> 1) & 1, op = j >> 2;   // op: weight groups, then activations
+      const uint32_t off = (uint32_t)(2 * p + half) * kPieceBytes;
+      uint8_t* const at = st + half * L::kHalf + op * 8192 + band * 4096 + wave * 1024;
+      tile::b2l_16(band ? v1 : v0, op == kG ? r.x : op == 1 ? r.w1 : r.w0, off, at);
+    } else {
+      tile::b2l_4(vs, r.s, (uint32_t)(2 * p + (wave & 1)) * kTileScaleBytes, st + L::kScale + wave * 256);
     }
   };
 
-  const int offW = wn * 8192 + tile_off(i, g);
-  const int offX = kBigX + 16 * wm * kStepK + tile_off(i, g);
-  const int offS = kBigScale + (g >> 1) * 256 + (16 * wm + i) * 8 + (g & 1) * 4;
+  const int offW = wn * 4096 * kG + tile_off(i, g);
+  const int offX = L::kX + 16 * wm * kStepK + tile_off(i, g);
+  const int offS = L::kScale + (g >> 1) * 256 + (16 * wm + i) * 8 + (g & 1) * 4;
   struct Frags {
-    v8i w[8], x[4];
+    v8i w[kA], x[4];
     int s;
   };
   auto rd16 = [](const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); };
   auto frag = [&](const uint8_t* st, int off) {
-    const uint4 lo = rd16(st + off), hi = rd16(st + off + kBigHalf);
+    const uint4 lo = rd16(st + off), hi = rd16(st + off + L::kHalf);
     return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
   };
   // Part j of the fragment reads of a block: its scale word and activation
@@ -499,7 +551,232 @@ __global__ __launch_bounds__(kB128Threads, 1) void gemm_b128_big_kernel(
   auto read = [&](int j, const uint8_t* st, Frags& f) {
     if (j == 0) f.s = *reinterpret_cast<const int*>(st + offS);
     if (j < 4) f.x[j] = frag(st, offX + 32 * kStepK * j);
-    else if (j < 12) f.w[j - 4] = frag(st, offW + 16 * kStepK * (j - 4));
+    else f.w[j - 4] = frag(st, offW + 16 * kStepK * (j - 4));
+  };
+
+  v4f acc[kA][4];
+  auto clear = [&] {
+#pragma unroll
+    for (int a = 0; a < kA; ++a)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) acc[a][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+  clear();
+
+  // Positions in the flattened (item, block) sequence: of the copies
+  // (kDepth steps ahead) and of the MFMAs.  Past the last item the copies go on with
+  // its blocks again (never used), so the steps need no branch and the waits
+  // no other counts.
+  Item ci = item_at(0), mi = ci;
+  int cj = 0, cp = ci.p0, mj = 0, mp = 0;
+  Src src = src_of(ci.t);
+  auto advance_copy = [&] {
+    if (++cp == ci.p1) {
+      cj = min(cj + 1, mine - 1);
+      ci = item_at(cj);
+      cp = ci.p0;
+      src = src_of(ci.t);
+    }
+  };
+  auto scales_of = [&](BigTile t) {
+    return wsc + (size_t)(kG == 2 ? min(2 * t.tn + wn, GN - 1) : t.tn) * KB;
+  };
+  const float* wsg = scales_of(mi.t);
+  auto buf = [&](int b) { return smem + b * L::kBlock; };
+#pragma unroll
+  for (int s = 0; s < L::kDepth; ++s) {
+    const Rsrc rs = rsrc_of(src);
+    tile::static_for<0, L::kCopies>([&](auto J) { copy(J, rs, cp, buf(s)); });
+    advance_copy();
+  }
+  tile::wait_vmcnt<(L::kDepth - 1) * L::kCopies>();
+  __builtin_amdgcn_s_barrier();
+  Frags f0, f1;
+#pragma unroll
+  for (int j = 0; j < 4 + kA; ++j) read(j, buf(0), f0);
+  float ws = scalar_scale(wsg, mi.p0);
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+
+  // Lane (i, g) holds D[n = 64 kG wn + 16 a + 4 g + j][m = 32 b + 16 wm + i].
+  auto epilogue = [&](const Item& it) {
+    const int n0 = (it.t.tn * 2 + wn) * 64 * kG, m0 = it.t.tm * 128;
+    const int rows = min(128, M - m0);
+    if constexpr (kPart) {
+      const __amdgpu_buffer_rsrc_t pr = raw_rsrc(part + ((size_t)it.split * M + m0) * ldp, (uint32_t)(rows * ldp * 4));
+#pragma unroll
+      for (int a = 0; a < kA; ++a)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int n = n0 + 16 * a + 4 * g, m = 32 * b + 16 * wm + i;
+          const uint32_t at = (n < ldp && m < rows) ? (uint32_t)((m * ldp + n) * 4) : kDrop;
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[a][b]), pr, at, 0, 0);
+        }
+    } else {
+      const int nl = 16 * (g & 1) + 8 * (g >> 1);
+      const __amdgpu_buffer_rsrc_t yr =
+          raw_rsrc(y + (size_t)m0 * ldy, (uint32_t)(((int64_t)(rows - 1) * ldy + N) * 2));
+#pragma unroll
+      for (int a = 0; a < kA; a += 2) {
+        const int n = n0 + 16 * a + nl;
+        float bl[4], bh[4];
+        bias4(bias, N, n0 + 16 * a + 4 * g, bl);
+        bias4(bias, N, n0 + 16 * a + 16 + 4 * g, bh);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int m = 32 * b + 16 * wm + i;   // N % 8 == 0: eight columns are all in or all out
+          store_pair(acc[a][b], acc[a + 1][b], bl, bh, yr,
+                     (n < N && m < rows) ? (uint32_t)(((int64_t)m * ldy + n) * 2) : kDrop);
+        }
+      }
+    }
+    clear();
+  };
+
+  bool stores = false;   // the stores of the last epilogue may be outstanding
+  auto step = [&](Frags& f, Frags& fn, int rb) {
+    // Newer than the copies of the next block: those of the kDepth - 2 after
+    // it, and in an item's first kDepth - 1 steps the last epilogue's stores.
+    constexpr int kNewer = (L::kDepth - 2) * L::kCopies;
+    if (stores && mp < L::kDepth - 1) tile::wait_vmcnt<kNewer + kStores>();
+    else tile::wait_vmcnt<kNewer>();
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    uint8_t* const st_free = buf(rb);
+    const uint8_t* const st_next = buf(rb == L::kDepth - 1 ? 0 : rb + 1);
+    v4f d[4];
+    const Rsrc rs = rsrc_of(src);
+    const int p = __builtin_amdgcn_readfirstlane(cp);
+    // The empty asm statements keep each MFMA and each result's v_fma in its
+    // place in the stream of reads and copies: as pure operations they would
+    // otherwise sink below all of them.
+    tile::static_for<0, 4 * kA + 3>([&](auto J) {
+      constexpr int j = decltype(J)::value;
+      if constexpr (j < 4 * kA) {
+        d[j & 3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(f.w[j >> 2], f.x[j & 3], v4f{0.0f, 0.0f, 0.0f, 0.0f},
+                                                                    0, 0, 0, kUnitScales, j & 3, f.s);
+        asm volatile("" : "+v"(d[j & 3]));
+      }
+      // kG = 2: a read and a copy every other MFMA; kG = 1: one of each.
+      constexpr int k2 = kG == 2 ? j >> 1 : j;
+      if constexpr ((kG == 1 || (j & 1) == 0) && k2 < 4 + kA) read(k2, st_next, fn);
+      if constexpr ((kG == 1 || (j & 1) == 1) && k2 < L::kCopies)
+        copy(std::integral_constant<int, (k2 < L::kCopies ? k2 : 0)>{}, rs, p, st_free);
+      if constexpr (j >= 3) {
+        constexpr int k = j - 3;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[k >> 2][k & 3][e] = fmaf(d[k & 3][e], ws, acc[k >> 2][k & 3][e]);
+        asm volatile("" : "+v"(acc[k >> 2][k & 3]));
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    advance_copy();
+    if (mi.p0 + ++mp == mi.p1) {
+      epilogue(mi);
+      stores = true;
+      mp = 0;
+      mj = mj + 1;
+      mi = item_at(min(mj, mine - 1));
+      wsg = scales_of(mi.t);
+    }
+    ws = scalar_scale(wsg, mi.p0 + mp);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  };
+  int rb = 0;
+  while (mj < mine) {
+    step(f0, f1, rb);
+    rb = rb == L::kDepth - 1 ? 0 : rb + 1;
+    if (mj >= mine) break;
+    step(f1, f0, rb);
+    rb = rb == L::kDepth - 1 ? 0 : rb + 1;
+  }
+  tile::wait_vmcnt<0>();   // no copy may land after the workgroup's LDS is given away
+}
+
+// ---------------------------------------------------------------------------
+// Wide tiles: 256 x 256 per workgroup, eight waves 2 (n) x 4 (m), each 128 x 64
+// as above, two waves per SIMD.  A third fewer operand bytes per product than
+// the 256 x 128 tiles; 256 registers per wave leave no room for a second set
+// of fragments, so weight fragments are read two ahead and the SIMD's other
+// wave covers what latency is left.
+//  * LDS holds two blocks (2 x 65 KiB).  After a wave's last reads of block p
+//    comes the step's one barrier: then p + 1 has landed everywhere, p's
+//    buffer is free, the first fragments of p + 1 are read under the last
+//    MFMAs of p, and the copies of p + 2 go out with the MFMAs of p + 1.
+//  * Persistent, with the same epilogue.
+// 8192 x 28672 x 8192: 1538 us (2.50 PFLOP/s; 256 x 128 tiles 1769, 128 x 128
+// 2304); 4096^3: 60, 67, 84.  What bounds it: the MFMAs alone, without v_fma,
+// reads and copies, take 1250 us of the 256 x 128 form's time at the clock
+// the card holds under them, the v_fma 250 more.
+// ---------------------------------------------------------------------------
+namespace {
+constexpr int kWideThreads = 512;
+constexpr int kWideX = 16384;                        // activation pieces inside a 64-K half
+constexpr int kWideHalf = 32768;                     // (256 + 256 rows) x 64 B
+constexpr int kWideScale = 2 * kWideHalf;            // eight 256-byte slots: [half][group], four unused
+constexpr int kWideBlock = kWideScale + 2048;
+constexpr int kWideLds = 2 * kWideBlock;             // 135168
+constexpr int kWideCopies = 9;                       // per wave and block
+}  // namespace
+
+__global__ __launch_bounds__(kWideThreads, 1) void gemm_b128_wide_kernel(
+    const uint8_t* __restrict__ qp, const uint8_t* __restrict__ sp, int M, int KB, const uint8_t* __restrict__ wp,
+    const float* __restrict__ wsc, int N, const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, int64_t ldy,
+    int GN, int GM, int tiles_n, int tiles_m, int total) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wave & 1, wm = (wave >> 1) & 1, wx = wave >> 2;   // weight group, row half, activation group
+  const int i = lane & 15, g = lane >> 4;
+  const int KS = 2 * KB;
+  const uint32_t gbytes = (uint32_t)KS * kTileBytes, sbytes = (uint32_t)KS * kTileScaleBytes;
+  const int grid = (int)gridDim.x;
+  const int mine = (total - (int)blockIdx.x + grid - 1) / grid;
+  const int steps = mine * KB;
+  auto tile_at = [&](int j) { return big_tile(xcd_remap((int)blockIdx.x + j * grid, total), tiles_n, tiles_m); };
+
+  // Copies: wave w takes band w of both weight groups and both activation
+  // groups, and one of the block's four scale tiles (waves 4 .. 7 copy them
+  // again, to the unused slots).
+  struct Src {
+    tile::i4v w0, w1, x0, x1, s;
+  };
+  auto src_of = [&](BigTile t) {
+    Src r;
+    const int g1 = min(2 * t.tn + 1, GN - 1), m1 = min(2 * t.tm + 1, GM - 1);
+    r.w0 = tile::buffer_rsrc(wp + (size_t)(2 * t.tn) * gbytes, gbytes);
+    r.w1 = tile::buffer_rsrc(wp + (size_t)g1 * gbytes, gbytes);
+    r.x0 = tile::buffer_rsrc(qp + (size_t)(2 * t.tm) * gbytes, gbytes);
+    r.x1 = tile::buffer_rsrc(qp + (size_t)m1 * gbytes, gbytes);
+    r.s = tile::buffer_rsrc(sp + (size_t)((wave & 1) ? m1 : 2 * t.tm) * sbytes, sbytes);
+    return r;
+  };
+  const uint32_t v0 = (uint32_t)wave * KS * kPieceBytes + (uint32_t)lane * 16u;
+  const uint32_t vs = (uint32_t)lane * 4u;
+  auto copy = [&](int j, const Src& r, int p, uint8_t* st) {
+    const uint32_t off = (uint32_t)(2 * p) * kPieceBytes;
+    uint8_t* b = st + wave * 1024;
+    switch (j) {
+      case 0: tile::b2l_16(v0, r.w0, off, b); break;
+      case 1: tile::b2l_16(v0, r.w1, off, b + 8192); break;
+      case 2: tile::b2l_16(v0, r.x0, off, b + kWideX); break;
+      case 3: tile::b2l_16(v0, r.x1, off, b + kWideX + 8192); break;
+      case 4: tile::b2l_16(v0, r.w0, off + kPieceBytes, b + kWideHalf); break;
+      case 5: tile::b2l_16(v0, r.w1, off + kPieceBytes, b + kWideHalf + 8192); break;
+      case 6: tile::b2l_16(v0, r.x0, off + kPieceBytes, b + kWideHalf + kWideX); break;
+      case 7: tile::b2l_16(v0, r.x1, off + kPieceBytes, b + kWideHalf + kWideX + 8192); break;
+      default:
+        tile::b2l_4(vs, r.s, (uint32_t)(2 * p + ((wave >> 1) & 1)) * kTileScaleBytes, st + kWideScale + wave * 256);
+        break;
+    }
+  };
+
+  const int offW = wn * 8192 + tile_off(i, g);
+  const int offX = kWideX + wx * 8192 + 16 * wm * kStepK + tile_off(i, g);
+  const int offS = kWideScale + (2 * (g >> 1) + wx) * 256 + (16 * wm + i) * 8 + (g & 1) * 4;
+  auto rd16 = [](const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); };
+  auto frag = [&](const uint8_t* st, int off) {
+    const uint4 lo = rd16(st + off), hi = rd16(st + off + kWideHalf);
+    return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
   };
 
   v4f acc[8][4];
@@ -511,12 +788,8 @@ __global__ __launch_bounds__(kB128Threads, 1) void gemm_b128_big_kernel(
   };
   clear();
 
-  // Positions in the flattened (tile, block) sequence: of the copies (three
-  // steps ahead) and of the MFMAs.
   int cj = 0, cp = 0, mj = 0, mp = 0;
   Src src = src_of(tile_at(0));
-  // Past the last tile the copies go on with its blocks again (never used),
-  // so the steps need no branch and the waits no other counts.
   auto advance_copy = [&] {
     if (++cp == KB) {
       cp = 0;
@@ -526,117 +799,93 @@ __global__ __launch_bounds__(kB128Threads, 1) void gemm_b128_big_kernel(
   };
   BigTile cur = tile_at(0);
   const float* wsg = wsc + (size_t)min(2 * cur.tn + wn, GN - 1) * KB;
-  auto buf = [&](int b) { return smem + b * kBigBlock; };
+  auto buf = [&](int b) { return smem + b * kWideBlock; };
+  // A block's copies 0 .. 4 go out at the end of a step, the others at the
+  // start of the next.
+  constexpr int kEarly = 5;
 #pragma unroll
-  for (int s = 0; s < 3; ++s) {   // KB >= 4: three blocks of the first tile
+  for (int j = 0; j < kWideCopies; ++j) copy(j, src, cp, buf(0));
+  advance_copy();
 #pragma unroll
-    for (int j = 0; j < kBigCopies; ++j) copy(j, src, cp, buf(s));
-    advance_copy();
-  }
-  tile::wait_vmcnt<2 * kBigCopies>();
+  for (int j = 0; j < kEarly; ++j) copy(j, src, cp, buf(1));
+  tile::wait_vmcnt<kEarly>();
   __builtin_amdgcn_s_barrier();
-  Frags f0, f1;
-#pragma unroll
-  for (int j = 0; j < 12; ++j) read(j, buf(0), f0);
+  v8i x[4], w[3];
   float ws = scalar_scale(wsg, 0);
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  int sx = *reinterpret_cast<const int*>(buf(0) + offS);
+#pragma unroll
+  for (int b = 0; b < 4; ++b) x[b] = frag(buf(0), offX + 32 * kStepK * b);
+  w[0] = frag(buf(0), offW);
+  w[1] = frag(buf(0), offW + 16 * kStepK);
 
-  // Lane (i, g) holds D[n = 128 wn + 16 a + 4 g + j][m = 32 b + 16 wm + i].
-  // Exchanging the odd 16-lane rows of tile a with the even ones of tile a + 1
-  // gives every lane eight consecutive n: rows 0, 2 of tile a, rows 1, 3 of
-  // tile a + 1.
   auto epilogue = [&](BigTile t) {
-    const int n0 = t.tn * 256 + wn * 128, m0 = t.tm * 128;
+    const int n0 = t.tn * 256 + wn * 128, m0 = t.tm * 256 + wx * 128;
     const int nl = 16 * (g & 1) + 8 * (g >> 1);
-    const int rows = min(128, M - m0);
-    const __amdgpu_buffer_rsrc_t yr =
-        raw_rsrc(y + (size_t)m0 * ldy, (uint32_t)(((int64_t)(rows - 1) * ldy + N) * 2));
-    const __amdgpu_buffer_rsrc_t br = raw_rsrc(bias, bias != nullptr ? (uint32_t)N * 2u : 0u);
+    const int rows = max(0, min(128, M - m0));
+    const __amdgpu_buffer_rsrc_t yr = raw_rsrc(
+        y + (size_t)min(m0, M - 1) * ldy, rows > 0 ? (uint32_t)(((int64_t)(rows - 1) * ldy + N) * 2) : 0u);
 #pragma unroll
     for (int a = 0; a < 8; a += 2) {
       const int n = n0 + 16 * a + nl;
-      const int nb = n0 + 16 * a + 4 * g;
-      float bv[2][4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          bv[h][j] = __uint_as_float(
-              (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(br, (uint32_t)(nb + 16 * h + j) * 2u, 0, 0) << 16);
+      float bl[4], bh[4];
+      bias4(bias, N, n0 + 16 * a + 4 * g, bl);
+      bias4(bias, N, n0 + 16 * a + 16 + 4 * g, bh);
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        uint32_t q[2][2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const v4f v = acc[a + h][b];
-          q[h][0] = pack_bf16x2(v[0] + bv[h][0], v[1] + bv[h][1]);
-          q[h][1] = pack_bf16x2(v[2] + bv[h][2], v[3] + bv[h][3]);
-        }
-        const auto s0 = __builtin_amdgcn_permlane16_swap(q[0][0], q[1][0], false, false);
-        const auto s1 = __builtin_amdgcn_permlane16_swap(q[0][1], q[1][1], false, false);
-        typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-        const u32x4 o = {s0[0], s1[0], s0[1], s1[1]};
-        // a column past N (N % 8 == 0: whole stores) or a row past M gets an offset past the end
         const int m = 32 * b + 16 * wm + i;
-        const uint32_t at = (n < N && m < rows) ? (uint32_t)(((int64_t)m * ldy + n) * 2) : 0xFFFFFFF0u;
-        __builtin_amdgcn_raw_buffer_store_b128(o, yr, at, 0, 0);
+        store_pair(acc[a][b], acc[a + 1][b], bl, bh, yr,
+                   (n < N && m < rows) ? (uint32_t)(((int64_t)m * ldy + n) * 2) : kDrop);
       }
     }
     clear();
   };
 
-  int s = 0;
-  bool stores = false;   // the stores of the last epilogue may be outstanding
-  auto step = [&](Frags& f, Frags& fn, int rb) {
-    // Newer than the copies of s + 1: those of s + 2, and in a tile's first
-    // two steps the last epilogue's stores.
-    if (stores && mp < 2) tile::wait_vmcnt<kBigCopies + kBigStores>();
-    else tile::wait_vmcnt<kBigCopies>();
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    uint8_t* const st_free = buf(rb);
-    const uint8_t* const st_next = buf(rb == 2 ? 0 : rb + 1);
+  for (int s = 0; s < steps; ++s) {
+    uint8_t* const st = buf(s & 1);
+    uint8_t* const other = buf((s & 1) ^ 1);
     v4f d[4];
-    // The empty asm statements keep each MFMA and each result's v_fma in its
-    // place in the stream of reads and copies: as pure operations they would
-    // otherwise sink below all of them.
+    int sxn = 0;
     tile::static_for<0, 35>([&](auto J) {
       constexpr int j = decltype(J)::value;
       if constexpr (j < 32) {
-        d[j & 3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(f.w[j >> 2], f.x[j & 3], v4f{0.0f, 0.0f, 0.0f, 0.0f},
-                                                                    0, 0, 0, kUnitScales, j & 3, f.s);
+        d[j & 3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[(j >> 2) % 3], x[j & 3],
+                                                                    v4f{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, kUnitScales,
+                                                                    j & 3, sx);
         asm volatile("" : "+v"(d[j & 3]));
       }
-      if constexpr (j < 24 && (j & 1) == 0) read(j >> 1, st_next, fn);
-      if constexpr (j < 26 && (j & 1) == 1) copy(j >> 1, src, cp, st_free);
+      if constexpr (j < 24 && (j & 3) == 0) w[(j / 4 + 2) % 3] = frag(st, offW + 16 * kStepK * (j / 4 + 2));
+      // the rest of block s + 1 (its buffer is free since the last barrier)
+      if constexpr (j < kWideCopies - kEarly) copy(kEarly + j, src, cp, other);
+      if constexpr (j == kWideCopies - kEarly) advance_copy();
       if constexpr (j >= 3) {
         constexpr int k = j - 3;
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[k >> 2][k & 3][e] = fmaf(d[k & 3][e], ws, acc[k >> 2][k & 3][e]);
         asm volatile("" : "+v"(acc[k >> 2][k & 3]));
       }
+      if constexpr (j == 25) {
+        // This wave has read the block, its copies of the next have landed;
+        // past the barrier both hold for all.
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+      }
+      if constexpr (j >= 26 && j < 26 + kEarly) copy(j - 26, src, cp, st);
+      // the next block's first fragments, each where its register is free
+      if constexpr (j == 27) sxn = *reinterpret_cast<const int*>(other + offS);
+      if constexpr (j == 28) w[0] = frag(other, offW);
+      if constexpr (j >= 29 && j < 33) x[j - 29] = frag(other, offX + 32 * kStepK * (j - 29));
+      if constexpr (j == 32) w[1] = frag(other, offW + 16 * kStepK);
       __builtin_amdgcn_sched_barrier(0);
     });
-    advance_copy();
+    sx = sxn;
     if (++mp == KB) {
       epilogue(cur);
-      stores = true;
       mp = 0;
       mj = min(mj + 1, mine - 1);
       cur = tile_at(mj);
       wsg = wsc + (size_t)min(2 * cur.tn + wn, GN - 1) * KB;
     }
     ws = scalar_scale(wsg, mp);
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    ++s;
-  };
-  int rb = 0;
-  while (s < steps) {
-    step(f0, f1, rb);
-    rb = rb == 2 ? 0 : rb + 1;
-    if (s >= steps) break;
-    step(f1, f0, rb);
-    rb = rb == 2 ? 0 : rb + 1;
   }
   tile::wait_vmcnt<0>();   // no copy may land after the workgroup's LDS is given away
 }
@@ -649,17 +898,21 @@ int b128_force(int mt) { return g_force_mt.exchange(mt); }
 
 // The form and K splits with the least estimated time.  The estimates are
 // lines through measurements on MI355X (us; M 17 .. 8192, N and K 512 ..
-// 28672): a start of about 5, a cost per 128-block and round of workgroups
-// (two of the 64- and 128-row tiles share a compute unit; alone on it one
-// walks its blocks almost twice as fast), and for K splits a second launch
-// and the partials' way to memory and back at about 4 TB/s.  For example
-// M = 1024, N = K = 4096: 64-row tiles 26, 128-row 33, large 32;
-// M = 2048: 53, 40, 36; M = 256, N = 512, K = 8192: 13 with eight splits, 51
-// with large tiles.
+// 28672): a start, a cost per 128-block and round of workgroups, and for K
+// splits a second launch and the partials' way to memory and back.  For
+// example, at N = K = 4096 (64-row, 128-row, 256 x 128, 256 x 256 tiles):
+//   M = 256    18   22   30   43  (with K splits in the first two)
+//   M = 1024   27   26   34   46
+//   M = 2048   50   47   37   49
+//   M = 4096  100   90   69   59
+// All four forms move 10 to 20 TB/s from L2 into LDS, so the bytes a tile
+// reads for its products decide, where there are tiles for all compute units.
 B128Plan b128_plan(int64_t M, int64_t N, int64_t K) {
-  const int64_t G = b128_blocks(N), KB = b128_blocks(K);
+  const int64_t G = b128_blocks(N), KB = b128_blocks(K), GM = b128_blocks(M);
   const int force = g_force_mt.load(std::memory_order_relaxed);
-  B128Plan best = {128, 1};
+  // the larger forms write whole 16-byte pieces and address a tile's rows with 32 bits
+  const bool whole = N % 8 == 0 && N <= ((int64_t)1 << 22);
+  B128Plan best = {64, 1};
   double best_us = 1e30;
   auto offer = [&](int mt, int splits, double us) {
     if (us < best_us) {
@@ -667,66 +920,89 @@ B128Plan b128_plan(int64_t M, int64_t N, int64_t K) {
       best = {mt, splits};
     }
   };
-  for (int mt = 64; mt <= 128; mt *= 2) {
-    if (force && force != mt && !(force == 256 && mt == 128)) continue;
-    const int64_t tiles = G * ((M + mt - 1) / mt);
-    for (int s = 1; s <= kMaxSplitK && (s == 1 || KB / s >= 2); s *= 2) {
-      const int64_t items = tiles * s, rounds = (items + 511) / 512;
-      const double block = mt == 64 ? (items <= 256 ? 0.35 : 0.67 * (double)rounds)
-                                    : (items <= 256 ? 0.8 : 1.1 * (double)rounds);
-      const double join = s > 1 ? 3.0 + (double)s * (double)M * (double)N * 8.0 / 4e6 : 0.0;
-      offer(mt, s, 4.5 + block * (double)((KB + s - 1) / s) + join);
-    }
+  auto join = [&](int s) { return s > 1 ? 3.0 + (double)s * (double)M * (double)N * 8.0 / 4e6 : 0.0; };
+  auto blocks = [&](int s) { return (double)((KB + s - 1) / s); };
+  auto wanted = [&](int mt) { return !force || force == mt || !whole; };
+  const int64_t small = G * ((M + 63) / 64);
+  for (int s = 1; wanted(64) && s <= kMaxSplitK && (s == 1 || KB / s >= 2); s *= 2) {
+    const int64_t items = small * s;
+    offer(64, s, 4.5 + (items <= 256 ? 0.35 : 0.67 * (double)((items + 511) / 512)) * blocks(s) + join(s));
   }
-  // Large tiles need a run of four blocks and whole 16-byte stores.
-  if ((!force || force == 256) && KB >= 4 && N % 8 == 0) {
-    const int64_t tiles = (G + 1) / 2 * ((M + 127) / 128), rounds = (tiles + 255) / 256;
-    const double us = 5.0 + (tiles <= 128 ? 0.73 : 0.95 * (double)rounds) * (double)KB;
-    if (force == 256) best_us = 1e30;
-    offer(256, 1, us);
-  }
+  if (!whole) return best;
+  for (int s = 1; wanted(128) && s <= kMaxSplitK && (s == 1 || KB / s >= 2); s *= 2)
+    offer(128, s, 4.5 + 0.65 * (double)((G * GM * s + 255) / 256) * blocks(s) + join(s));
+  const int64_t large = (G + 1) / 2 * GM, wide = (G + 1) / 2 * ((GM + 1) / 2);
+  if (wanted(256)) offer(256, 1, 5.0 + (large <= 128 ? 0.75 : 0.95 * (double)((large + 255) / 256)) * blocks(1));
+  if (wanted(512)) offer(512, 1, 5.0 + (wide <= 128 ? 1.25 : 1.7 * (double)((wide + 255) / 256)) * blocks(1));
   return best;
 }
 
 namespace {
-template <int kMT, bool kPart>
-int launch_b128_k(const void* qp, const void* sp, int64_t M, int64_t K, const void* wp, const float* wsc, int64_t N,
-                  const void* bias, void* y, int64_t ldy, hipStream_t stream, int splits, void* part) {
-  constexpr int lds = B128Lds<kMT>::kBytes;
+
+int persistent_grid(int total) {
+  const int cus = device_cu_count();
+  return total <= cus ? total : (cus >= 8 ? cus - cus % 8 : cus);
+}
+
+template <bool kPart>
+int launch_small(const void* qp, const void* sp, int64_t M, int64_t K, const void* wp, const float* wsc, int64_t N,
+                 const void* bias, void* y, int64_t ldy, hipStream_t stream, int splits, void* part) {
+  constexpr int lds = SmallLds::kBytes;
   static std::atomic<int> lds_set[kMaxDevices];
-  if (!set_lds_limit_once((const void*)gemm_b128_kernel<kMT, kPart>, lds, lds_set)) return -7;
+  if (!set_lds_limit_once((const void*)gemm_b128_small_kernel<kPart>, lds, lds_set)) return -7;
   const int G = (int)b128_blocks(N), tiles_m = (int)((M + kMT - 1) / kMT);
   const int vec = (ldy % 8 == 0) && (((uintptr_t)y & 15) == 0);
-  hipLaunchKernelGGL((gemm_b128_kernel<kMT, kPart>), dim3((unsigned)(G * tiles_m * splits)), dim3(kB128Threads), lds,
+  hipLaunchKernelGGL(gemm_b128_small_kernel<kPart>, dim3((unsigned)(G * tiles_m * splits)), dim3(kB128Threads), lds,
                      stream, (const uint8_t*)qp, (const uint8_t*)sp, (int)M, (int)b128_blocks(K), (const uint8_t*)wp,
                      wsc, (int)N, (const uint16_t*)bias, (uint16_t*)y, ldy, G, tiles_m, splits, vec, (float*)part,
                      (N + 3) / 4 * 4);
   return hipGetLastError() == hipSuccess ? 0 : -7;
 }
+
+template <int kG, bool kPart>
+int launch_large(const void* qp, const void* sp, int64_t M, int64_t K, const void* wp, const float* wsc, int64_t N,
+                 const void* bias, void* y, int64_t ldy, hipStream_t stream, int splits, void* part) {
+  constexpr int lds = BigLds<kG>::kBytes;
+  static std::atomic<int> lds_set[kMaxDevices];
+  if (!set_lds_limit_once((const void*)gemm_b128_big_kernel<kG, kPart>, lds, lds_set)) return -7;
+  const int GN = (int)b128_blocks(N), tiles_n = (GN + kG - 1) / kG, tiles_m = (int)b128_blocks(M);
+  const int total = tiles_n * tiles_m * splits;
+  hipLaunchKernelGGL((gemm_b128_big_kernel<kG, kPart>), dim3((unsigned)persistent_grid(total)), dim3(kB128Threads), lds,
+                     stream, (const uint8_t*)qp, (const uint8_t*)sp, (int)M, (int)b128_blocks(K), (const uint8_t*)wp,
+                     wsc, (int)N, (const uint16_t*)bias, (uint16_t*)y, ldy, GN, tiles_n, tiles_m,
+                     __builtin_ctz((unsigned)splits), total, (float*)part, (N + 3) / 4 * 4);
+  return hipGetLastError() == hipSuccess ? 0 : -7;
+}
+
+int launch_wide(const void* qp, const void* sp, int64_t M, int64_t K, const void* wp, const float* wsc, int64_t N,
+                const void* bias, void* y, int64_t ldy, hipStream_t stream) {
+  static std::atomic<int> lds_set[kMaxDevices];
+  if (!set_lds_limit_once((const void*)gemm_b128_wide_kernel, kWideLds, lds_set)) return -7;
+  const int GN = (int)b128_blocks(N), GM = (int)b128_blocks(M), tiles_n = (GN + 1) / 2, tiles_m = (GM + 1) / 2;
+  const int total = tiles_n * tiles_m;
+  hipLaunchKernelGGL(gemm_b128_wide_kernel, dim3((unsigned)persistent_grid(total)), dim3(kWideThreads), kWideLds,
+                     stream, (const uint8_t*)qp, (const uint8_t*)sp, (int)M, (int)b128_blocks(K), (const uint8_t*)wp,
+                     wsc, (int)N, (const uint16_t*)bias, (uint16_t*)y, ldy, GN, GM, tiles_n, tiles_m, total);
+  return hipGetLastError() == hipSuccess ? 0 : -7;
+}
+
 }  // namespace
 
 int launch_gemm_b128_tile(const void* qp, const void* sp, int64_t M, int64_t K, const void* wp, const float* wsc,
                           int64_t N, const void* bias, void* y, int64_t ldy, hipStream_t stream, B128Plan plan,
                           void* part) {
-  auto go = [&](auto one, auto many) {
-    return plan.splits > 1 ? many(qp, sp, M, K, wp, wsc, N, bias, y, ldy, stream, plan.splits, part)
-                           : one(qp, sp, M, K, wp, wsc, N, bias, y, ldy, stream, 1, part);
-  };
-  if (plan.mt == 256 && ldy % 8 == 0 && ((uintptr_t)y & 15) == 0 && ldy <= (1 << 23)) {
-    static std::atomic<int> lds_set[kMaxDevices];
-    if (!set_lds_limit_once((const void*)gemm_b128_big_kernel, kBigLds, lds_set)) return -7;
-    const int GN = (int)b128_blocks(N), tiles_n = (GN + 1) / 2, tiles_m = (int)b128_blocks(M);
-    const int total = tiles_n * tiles_m, cus = device_cu_count();
-    const int grid = total <= cus ? total : (cus >= 8 ? cus - cus % 8 : cus);
-    hipLaunchKernelGGL(gemm_b128_big_kernel, dim3((unsigned)grid), dim3(kB128Threads), kBigLds, stream,
-                       (const uint8_t*)qp, (const uint8_t*)sp, (int)M, (int)b128_blocks(K), (const uint8_t*)wp, wsc,
-                       (int)N, (const uint16_t*)bias, (uint16_t*)y, ldy, GN, tiles_n, tiles_m, total);
-    return hipGetLastError() == hipSuccess ? 0 : -7;
+  int st;
+  if (plan.splits > 1) {
+    st = plan.mt == 64 ? launch_small<true>(qp, sp, M, K, wp, wsc, N, bias, y, ldy, stream, plan.splits, part)
+                       : launch_large<1, true>(qp, sp, M, K, wp, wsc, N, bias, y, ldy, stream, plan.splits, part);
+    return st ? st : launch_splitk_reduce((const float*)part, plan.splits, M, N, (N + 3) / 4 * 4, bias, y, ldy, stream);
   }
-  const int st = plan.mt == 64 ? go(launch_b128_k<64, false>, launch_b128_k<64, true>)
-                               : go(launch_b128_k<128, false>, launch_b128_k<128, true>);
-  if (st || plan.splits == 1) return st;
-  return launch_splitk_reduce((const float*)part, plan.splits, M, N, (N + 3) / 4 * 4, bias, y, ldy, stream);
+  // The larger forms store y in 16-byte pieces with 32-bit offsets.
+  const bool whole = ldy % 8 == 0 && ((uintptr_t)y & 15) == 0 && ldy <= (1 << 23);
+  if (plan.mt == 64 || !whole) return launch_small<false>(qp, sp, M, K, wp, wsc, N, bias, y, ldy, stream, 1, nullptr);
+  if (plan.mt == 128) return launch_large<1, false>(qp, sp, M, K, wp, wsc, N, bias, y, ldy, stream, 1, nullptr);
+  if (plan.mt == 256) return launch_large<2, false>(qp, sp, M, K, wp, wsc, N, bias, y, ldy, stream, 1, nullptr);
+  return launch_wide(qp, sp, M, K, wp, wsc, N, bias, y, ldy, stream);
 }
 
 }  // namespace mxfp8

@@ -63,7 +63,7 @@ int launch_gemm_b128_decode(const void* x, int64_t ldx, int64_t M, int64_t K, co
 // 128-blocks, whose fp32 partials go to `part` (splits * M * round_up(N, 4)
 // floats) and are added in order by launch_splitk_reduce.
 struct B128Plan {
-  int mt;       // 64 or 128: activation rows of a 128-column tile; 256: the large tiles
+  int mt;       // 64 or 128: activation rows of a 128-column tile; 256: large tiles; 512: wide tiles
   int splits;
 };
 int b128_force(int mt);   // test hook: pins mt (0: by shape); returns the previous value

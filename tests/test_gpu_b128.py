@@ -261,9 +261,10 @@ def test_graph_replays(M):
         assert torch.equal(y, want)
 
 
-@pytest.mark.parametrize("tile", [64, 128, 256])
+@pytest.mark.parametrize("tile", [64, 128, 256, 512])
 @pytest.mark.parametrize("M,N,K", [(17, 8, 512), (128, 256, 528), (129, 264, 640), (300, 520, 1152), (700, 1024, 2064),
-                                   (257, 136, 8336)])
+                                   (257, 136, 8336), (70, 264, 16),
+                                   (140, 1032, 256), (100, 130, 640)])
 def test_every_tile_form(tile, M, N, K):
     """Each tile form on shapes of one and many tiles, partial ones and a
     single weight group among them; persistent workgroups with several tiles."""
@@ -292,12 +293,12 @@ def test_many_tiles_per_workgroup():
     pw = api.prepare_weight_b128(wq.to(dev()), ws.to(dev()))
     bias = randn((N,), 3).to(dev())
     y = {}
-    for tile in (128, 256):
+    for tile in (128, 256, 512):
         prev = api.mxfp8_debug_force_b128(tile)
         try:
             y[tile] = api.linear(x.to(dev()), pw, bias)
         finally:
             api.mxfp8_debug_force_b128(prev)
-    assert torch.equal(y[128], y[256])    # the same blocks in the same order
+    assert torch.equal(y[128], y[256]) and torch.equal(y[128], y[512])    # the same blocks in the same order
     rows = torch.arange(0, M, 97)
     check_linear(x[rows], wq, ws, bias.cpu(), y[256][rows.to(dev())])
