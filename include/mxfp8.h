@@ -454,6 +454,32 @@ int mxfp8_linear_wgrad(const void* dy_bf16, int64_t M, int64_t N, int64_t lddy, 
                        int db_dtype, int accumulate, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * A training step of the 128-block layer in two calls, from a bf16 master
+ * weight (the entries above in the order a step needs them, one call's
+ * overhead instead of three):
+ *   forward   quantizes the weight (and, with MXFP8_KEEP_DX, its transpose)
+ *             and the activations, y = the layer; `kept` receives what the
+ *             backward call reads: the transposed prepared weight
+ *             (MXFP8_KEEP_DX) and the packed activations (MXFP8_KEEP_DW).
+ *   backward  dx = deq(q(dy)) deq(q(w)) (dy quantized like activations),
+ *             dw = dy^T deq(q(x)), db = column sums of dy; each NULL if not
+ *             wanted (db needs dw), MXFP8_E_SHAPE if its operand was not kept.
+ * N and K multiples of 16; arguments as in the entries above; kept and
+ * workspaces 256-byte aligned, sizes from mxfp8_linear_b128_layer_bytes.
+ * `kept` is not changed by the backward call (it can be called again).
+ */
+#define MXFP8_KEEP_DX 1
+#define MXFP8_KEEP_DW 2
+int mxfp8_linear_b128_layer_bytes(int64_t M, int64_t N, int64_t K, int keep, size_t* kept_bytes,
+                                  size_t* forward_ws_bytes, size_t* backward_ws_bytes);
+int mxfp8_linear_b128_forward(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, const void* w_bf16, int64_t N,
+                              int64_t ldw, const void* bias_bf16, void* y_bf16, int64_t ldy, int keep, void* kept,
+                              void* workspace, size_t workspace_bytes, void* stream);
+int mxfp8_linear_b128_backward(const void* dy_bf16, int64_t M, int64_t N, int64_t lddy, int64_t K, int keep,
+                               const void* kept, void* dx_bf16, int64_t lddx, void* dw, int dw_dtype, int64_t lddw,
+                               void* db, int db_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Test hook: pin the dW tile of mxfp8_linear_wgrad: 0 = by shape, 128 or 256
  * (M == 0 always takes 128).  The workspace query follows it.  Process-wide;
  * returns the previous value, or MXFP8_E_SHAPE.

@@ -71,6 +71,12 @@ _SIGNATURES = {
     "mxfp8_linear_b128": ([_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _sz, _vp], ctypes.c_int),
     "mxfp8_gemm_packed_b128_workspace_bytes": ([_i64, _i64, _i64, ctypes.POINTER(_sz)], ctypes.c_int),
     "mxfp8_gemm_packed_b128": ([_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _sz, _vp], ctypes.c_int),
+    "mxfp8_linear_b128_layer_bytes": ([_i64, _i64, _i64, ctypes.c_int, ctypes.POINTER(_sz), ctypes.POINTER(_sz),
+                                       ctypes.POINTER(_sz)], ctypes.c_int),
+    "mxfp8_linear_b128_forward": ([_vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, ctypes.c_int, _vp, _vp, _sz,
+                                   _vp], ctypes.c_int),
+    "mxfp8_linear_b128_backward": ([_vp, _i64, _i64, _i64, _i64, ctypes.c_int, _vp, _vp, _i64, _vp, ctypes.c_int, _i64,
+                                    _vp, ctypes.c_int, _vp, _sz, _vp], ctypes.c_int),
     "mxfp8_debug_force_b128": ([ctypes.c_int], ctypes.c_int),
     "mxfp8_debug_force_wgrad": ([ctypes.c_int], ctypes.c_int),
     "mxfp8_linear_wgrad_workspace_bytes": ([_i64, _i64, _i64, ctypes.POINTER(_sz)], ctypes.c_int),
@@ -593,11 +599,13 @@ def mxfp8_linear_b128(x, M, K, ldx, wp, sp, N, bias, y, ldy, ws, ws_bytes, strea
 
 def mxfp8_debug_force_b128(tile):
     _bytes.cache_clear()
+    _layer_bytes.cache_clear()
     return lib().mxfp8_debug_force_b128(tile)
 
 
 def mxfp8_debug_force_wgrad(tile):
     _bytes.cache_clear()
+    _layer_bytes.cache_clear()
     return lib().mxfp8_debug_force_wgrad(tile)
 
 
@@ -765,33 +773,48 @@ def linear_wgrad(dy, pa, dtype=torch.float32, bias_grad=False, out=None, out_bia
     return (out, db) if bias_grad else out
 
 
+@functools.lru_cache(maxsize=4096)
+def _layer_bytes(M, N, K, keep):
+    """(kept, forward workspace, backward workspace) bytes of a training step."""
+    out = [_sz() for _ in range(3)]
+    _check(lib().mxfp8_linear_b128_layer_bytes(M, N, K, keep, *[ctypes.byref(o) for o in out]),
+           "mxfp8_linear_b128_layer_bytes")
+    return tuple(o.value for o in out)
+
+
 class _LinearB128(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, bias):
         need_x, need_w, need_b = ctx.needs_input_grad
-        pw, ctx.pt = prepare_weight_b128_bf16(w, transposed=need_x)
-        ctx.shape, ctx.pa = x.shape, None
-        if need_w or need_b:
-            ctx.pa = quantize_act_packed_b128(x)
-            y = gemm_packed(ctx.pa, pw, bias)
-        else:
-            y = linear(x.reshape(-1, x.shape[-1]), pw, bias)
-        return y if x.dim() == 2 else y.view(*x.shape[:-1], pw.N)
+        x2, w2, bias = _rows(x, "x"), _rows(w, "w"), _bias(bias, w.shape[0])
+        (M, K), N, d = x2.shape, w2.shape[0], x.device
+        keep = (1 if need_x else 0) | (2 if need_w or need_b else 0)
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=d)
+        with _on(d):
+            kept_bytes, ws_bytes, ctx.ws_bytes = _layer_bytes(M, N, K, keep)
+            kept, ws = _scratch(kept_bytes, d), _scratch(ws_bytes, d)
+            _check(lib().mxfp8_linear_b128_forward(_ptr(x2), M, K, x2.stride(0), _ptr(w2), N, w2.stride(0), _ptr(bias),
+                                                   _ptr(y), N, keep, _ptr(kept), _ptr(ws), ws_bytes, _stream(d)),
+                   "mxfp8_linear_b128_forward")
+        ctx.kept, ctx.keep, ctx.sizes, ctx.shape = kept, keep, (M, N, K), x.shape
+        return y if x.dim() == 2 else y.view(*x.shape[:-1], N)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         need_x, need_w, need_b = ctx.needs_input_grad
-        d2 = _rows(dy, "dy")
-        dx = dw = db = None
-        if need_x:
-            dx = linear(d2, ctx.pt)
-            dx = dx if len(ctx.shape) == 2 else dx.view(ctx.shape)
-        if need_b:
-            db = torch.empty(d2.shape[1], dtype=torch.bfloat16, device=d2.device)
-            dw, db = linear_wgrad(d2, ctx.pa, dtype=torch.bfloat16, bias_grad=True, out_bias=db)
-        elif need_w:
-            dw = linear_wgrad(d2, ctx.pa, dtype=torch.bfloat16)
+        d2, (M, N, K), d = _rows(dy, "dy"), ctx.sizes, dy.device
+        new = functools.partial(torch.empty, dtype=torch.bfloat16, device=d)
+        dx = new((M, K)) if need_x else None
+        dw = new((N, K)) if need_w or need_b else None
+        db = new(N) if need_b else None
+        with _on(d):
+            ws = _scratch(ctx.ws_bytes, d)
+            _check(lib().mxfp8_linear_b128_backward(_ptr(d2), M, N, d2.stride(0), K, ctx.keep, _ptr(ctx.kept), _ptr(dx),
+                                                    K, _ptr(dw), 1, K, _ptr(db), 1, _ptr(ws), ws.numel(), _stream(d)),
+                   "mxfp8_linear_b128_backward")
+        if need_x and len(ctx.shape) != 2:
+            dx = dx.view(ctx.shape)
         return dx, dw if need_w else None, db
 
 

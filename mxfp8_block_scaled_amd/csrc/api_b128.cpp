@@ -61,6 +61,40 @@ size_t linear_ws(int64_t M, int64_t N, int64_t K) {
          part_bytes(M, N, mxfp8::b128_plan(M, N, K));
 }
 
+// What the layer's forward call keeps for its backward call: the transposed
+// prepared weight (MXFP8_KEEP_DX), then the packed activations (MXFP8_KEEP_DW).
+struct Kept {
+  uint8_t *wt, *st, *q, *s;
+};
+size_t kept_layout(int64_t M, int64_t N, int64_t K, int keep, uint8_t* base, Kept* k) {
+  size_t off = 0;
+  auto take = [&](bool want, size_t bytes) {
+    uint8_t* p = want && base ? base + off : nullptr;
+    if (want) off += round_up(bytes, 256);
+    return p;
+  };
+  const bool dx = keep & MXFP8_KEEP_DX, dw = (keep & MXFP8_KEEP_DW) && M > 0;
+  Kept v;
+  v.wt = take(dx, act_bytes(K, N));
+  v.st = take(dx, (size_t)b128_blocks(N) * b128_blocks(K) * 4);
+  v.q = take(dw, act_bytes(M, K));
+  v.s = take(dw, act_scale_bytes(M, K));
+  if (k) *k = v;
+  return off;
+}
+
+// Forward workspace: the prepared weight and its scales, then the GEMM's
+// (activations that are not kept, partials).
+size_t forward_weight_bytes(int64_t N, int64_t K) {
+  return round_up(act_bytes(N, K), 256) + round_up((size_t)b128_blocks(N) * b128_blocks(K) * 4, 256);
+}
+
+int check_layer(int64_t M, int64_t N, int64_t K, int keep) {
+  if (M < 0 || M > kMaxRows || !summed_ok(N) || !summed_ok(K) || (keep & ~(MXFP8_KEEP_DX | MXFP8_KEEP_DW)))
+    return MXFP8_E_SHAPE;
+  return MXFP8_OK;
+}
+
 int check_logits(const void* logits, int dtype, int64_t T, int64_t E, int64_t ldl, int64_t topk) {
   if (T < 0 || T > ((int64_t)1 << 31) - 1 || E < 1 || E > mxfp8::kMoeMaxExperts || topk < 1 || topk > E ||
       topk > mxfp8::kMoeMaxTopk || (dtype != MXFP8_F32 && dtype != MXFP8_BF16))
@@ -274,6 +308,83 @@ int mxfp8_linear_wgrad(const void* dy_bf16, int64_t M, int64_t N, int64_t lddy, 
   a.part_dw = (float*)workspace;
   a.part_db = (float*)((uint8_t*)workspace + round_up(mxfp8::wgrad_dw_bytes(M, N, K, p), 256));
   return mxfp8::launch_wgrad(a, p, (hipStream_t)stream);
+}
+
+int mxfp8_linear_b128_layer_bytes(int64_t M, int64_t N, int64_t K, int keep, size_t* kept_bytes,
+                                  size_t* forward_ws_bytes, size_t* backward_ws_bytes) {
+  if (!kept_bytes || !forward_ws_bytes || !backward_ws_bytes) return MXFP8_E_NULLPTR;
+  if (int st = check_layer(M, N, K, keep)) return st;
+  *kept_bytes = kept_layout(M, N, K, keep, nullptr, nullptr);
+  size_t fwd = 0;
+  if (M > 0 && (keep & MXFP8_KEEP_DW)) mxfp8_gemm_packed_b128_workspace_bytes(M, N, K, &fwd);
+  else if (M > 0) mxfp8_linear_b128_workspace_bytes(M, N, K, &fwd);
+  *forward_ws_bytes = forward_weight_bytes(N, K) + fwd;
+  // the two products of the backward call run one after the other
+  size_t dx = 0, dw = 0;
+  if (keep & MXFP8_KEEP_DX) mxfp8_linear_b128_workspace_bytes(M, K, N, &dx);
+  if (keep & MXFP8_KEEP_DW) mxfp8_linear_wgrad_workspace_bytes(M, N, K, &dw);
+  *backward_ws_bytes = dx > dw ? dx : dw;
+  return MXFP8_OK;
+}
+
+int mxfp8_linear_b128_forward(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, const void* w_bf16, int64_t N,
+                              int64_t ldw, const void* bias_bf16, void* y_bf16, int64_t ldy, int keep, void* kept,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  if (int st = check_layer(M, N, K, keep)) return st;
+  size_t kept_bytes = 0, need = 0, back = 0;
+  mxfp8_linear_b128_layer_bytes(M, N, K, keep, &kept_bytes, &need, &back);
+  if (!w_bf16 || (kept_bytes > 0 && !kept) || (M > 0 && !x_bf16)) return MXFP8_E_NULLPTR;
+  if (ldw < K || ldw % 8 != 0 || (M > 0 && (ldx < K || ldx % 8 != 0))) return MXFP8_E_LD;
+  if (M > 0)
+    if (int st = check_out(y_bf16, N, ldy, bias_bf16)) return st;
+  if (!aligned(w_bf16, 16) || !aligned(kept, 256) || (M > 0 && !aligned(x_bf16, 16))) return MXFP8_E_ALIGN;
+  if (!tiles_ok(N, K) || !gemm_grid_ok(M, N) || !act_grid_ok(M, K)) return MXFP8_E_SHAPE;
+  if (!workspace || workspace_bytes < need) return MXFP8_E_WORKSPACE;
+  if (!aligned(workspace, 256)) return MXFP8_E_ALIGN;
+  Kept k;
+  kept_layout(M, N, K, keep, (uint8_t*)kept, &k);
+  uint8_t* wp = (uint8_t*)workspace;
+  uint8_t* sp = wp + round_up(act_bytes(N, K), 256);
+  uint8_t* rest = wp + forward_weight_bytes(N, K);
+  const size_t rest_bytes = workspace_bytes - forward_weight_bytes(N, K);
+  if (int st = mxfp8_quantize_weight_b128(w_bf16, N, K, ldw, nullptr, 0, nullptr, 0, wp, sp, k.wt, k.st, stream))
+    return st;
+  if (M == 0) return MXFP8_OK;
+  if (!(keep & MXFP8_KEEP_DW))
+    return mxfp8_linear_b128(x_bf16, M, K, ldx, wp, sp, N, bias_bf16, y_bf16, ldy, rest, rest_bytes, stream);
+  if (int st = mxfp8_quantize_act_packed_b128(x_bf16, M, K, ldx, k.q, k.s, stream)) return st;
+  return mxfp8_gemm_packed_b128(k.q, k.s, M, K, wp, sp, N, bias_bf16, y_bf16, ldy, rest, rest_bytes, stream);
+}
+
+int mxfp8_linear_b128_backward(const void* dy_bf16, int64_t M, int64_t N, int64_t lddy, int64_t K, int keep,
+                               const void* kept, void* dx_bf16, int64_t lddx, void* dw, int dw_dtype, int64_t lddw,
+                               void* db, int db_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  if (int st = check_layer(M, N, K, keep)) return st;
+  if ((dx_bf16 && !(keep & MXFP8_KEEP_DX)) || (dw && !(keep & MXFP8_KEEP_DW)) || (db && !dw)) return MXFP8_E_SHAPE;
+  size_t kept_bytes = 0, fwd = 0, need = 0;
+  mxfp8_linear_b128_layer_bytes(M, N, K, keep, &kept_bytes, &fwd, &need);
+  if (kept_bytes > 0 && !kept) return MXFP8_E_NULLPTR;
+  if (!aligned(kept, 256)) return MXFP8_E_ALIGN;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MXFP8_E_WORKSPACE;
+  Kept k;
+  kept_layout(M, N, K, keep, (uint8_t*)kept, &k);
+  // the weight gradient's checks cover dY as well; a refusal after the first
+  // product would leave half a result, so both sets come first
+  if (dx_bf16 && M > 0) {
+    if (!dy_bf16) return MXFP8_E_NULLPTR;
+    if (int st = check_out(dx_bf16, K, lddx, nullptr)) return st;
+    if (lddy < N || lddy % 8 != 0) return MXFP8_E_LD;
+    if (!aligned(dy_bf16, 16) || !aligned(workspace, 256)) return MXFP8_E_ALIGN;
+    if (!gemm_grid_ok(M, K) || !act_grid_ok(M, N)) return MXFP8_E_SHAPE;
+  }
+  if (dw) {
+    if (int st = mxfp8_linear_wgrad(dy_bf16, M, N, lddy, k.q, k.s, K, dw, dw_dtype, lddw, db, db_dtype, 0, workspace,
+                                    workspace_bytes, stream))
+      return st;
+  }
+  if (!dx_bf16 || M == 0) return MXFP8_OK;
+  return mxfp8_linear_b128(dy_bf16, M, N, lddy, k.wt, k.st, K, nullptr, dx_bf16, lddx, workspace, workspace_bytes,
+                           stream);
 }
 
 int mxfp8_moe_balance_workspace_bytes(int64_t T, int64_t E, size_t* bytes) {

@@ -118,6 +118,42 @@ def test_wgrad():
     expect_no_device(fn, *empty)
 
 
+@pytest.mark.parametrize("keep", [0, 1, 2, 3])
+@pytest.mark.parametrize("M", [4, 100])
+def test_training_step(keep, M):
+    N, K = 144, 272
+    kept, fws, bws = api._layer_bytes(M, N, K, keep)
+    assert (kept > 0) == (keep > 0)
+    fwd, bwd = api.lib().mxfp8_linear_b128_forward, api.lib().mxfp8_linear_b128_backward
+    refuse(fwd, (P, M, K, K, P, N, K, P, P, N, keep, P, P, fws, None), [
+        (1, -1, SHAPE), (2, 264, SHAPE), (5, 136, SHAPE), (10, 4, SHAPE), (0, None, NULLPTR), (4, None, NULLPTR),
+        (8, None, NULLPTR), (3, 264, LD), (3, 276, LD), (6, 264, LD), (9, 143, LD), (0, P + 8, ALIGN), (4, P + 8, ALIGN),
+        (7, P + 1, ALIGN), (11, P + 16, ALIGN), (12, None, WORKSPACE), (13, fws - 1, WORKSPACE), (12, P + 16, ALIGN)])
+    dx, dw = (P if keep & 1 else None), (P if keep & 2 else None)
+    ok = (P, M, N, N, K, keep, P, dx, K, dw, 1, K, dw, 1, P, bws, None)
+    cases = [(1, -1, SHAPE), (2, 136, SHAPE), (4, 264, SHAPE), (5, 4, SHAPE), (6, P + 16, ALIGN)]
+    if keep:
+        cases += [(0, None, NULLPTR), (3, 136, LD), (3, 146, LD), (0, P + 8, ALIGN), (6, None, NULLPTR)]
+        assert fwd(P, M, K, K, P, N, K, P, P, N, keep, None, P, fws, None) == NULLPTR
+    if bws:
+        cases += [(14, None, WORKSPACE), (15, bws - 1, WORKSPACE), (14, P + 16, ALIGN)]
+    if keep & 1:
+        cases += [(8, 271, LD), (7, P + 1, ALIGN)]
+    else:
+        cases += [(7, P, SHAPE)]                   # its operand was not kept
+    if keep & 2:
+        cases += [(10, 2, SHAPE), (11, 264, LD), (9, P + 8, ALIGN), (13, 2, SHAPE), (9, None, SHAPE)]
+    else:
+        cases += [(9, P, SHAPE), (12, P, SHAPE)]
+    if keep:
+        refuse(bwd, ok, cases)
+    else:
+        for at, value, status in cases:
+            args = list(ok)
+            args[at] = value
+            assert bwd(*args) == status
+
+
 def test_balance():
     lib = api.lib()
     need = api._bytes("mxfp8_moe_balance_workspace_bytes", 50, 24)

@@ -274,3 +274,32 @@ def test_wgrad_tile_forms(tile, M, N, K, form):
     check_dw(half, None, dy, X)
     check_dw(*acc, dy, X, base, base_b)
     assert torch.equal(dw, again) and not none.any()
+
+
+def test_linear_b128_of_no_tokens():
+    x = torch.empty(0, 64, dtype=torch.bfloat16, device=dev(), requires_grad=True)
+    w, b = spiky(32, 64, 1).to(dev()).requires_grad_(), randn((32,), 2).to(dev()).requires_grad_()
+    y = api.linear_b128(x, w, b)
+    assert y.shape == (0, 32)
+    dx, dw, db = torch.autograd.grad(y, (x, w, b), torch.empty_like(y))
+    assert dx.shape == (0, 64) and not dw.any() and not db.any()
+
+
+@pytest.mark.parametrize("M", [7, 300])
+def test_step_calls_are_their_parts(M):
+    """The two-call step gives bit for bit what its parts give, from views with
+    strides, and can run backward twice."""
+    N, K = 144, 272
+    wide_x, wide_w, wide_d = spiky(M, K + 32, 1).to(dev()), spiky(N, K + 48, 2).to(dev()), randn((M, N + 24), 3).to(dev())
+    x, w, dy, b = wide_x[:, 16:16 + K], wide_w[:, 8:8 + K], wide_d[:, 8:8 + N], randn((N,), 4).to(dev())
+    leaves = [t.detach().requires_grad_() for t in (x, w, b)]
+    y = api.linear_b128(*leaves)
+    got = torch.autograd.grad(y, leaves, dy, retain_graph=True)
+    again = torch.autograd.grad(y, leaves, dy)
+    pw, pt = api.prepare_weight_b128_bf16(w)
+    pa = api.quantize_act_packed_b128(x)
+    db = torch.empty(N, dtype=torch.bfloat16, device=dev())
+    dw, db = api.linear_wgrad(dy, pa, dtype=torch.bfloat16, bias_grad=True, out_bias=db)
+    assert torch.equal(y, api.gemm_packed(pa, pw, b))
+    for p, q, r in zip(got, (api.linear(dy, pt), dw, db), again):
+        assert torch.equal(p, q) and torch.equal(p, r)
