@@ -26,7 +26,8 @@ CALIB_SOURCES = ["calib.hip"]
 ARCH = "gfx950"
 
 SOURCES = ["api.cpp", "quant.hip", "pack.hip", "gemm_tile.hip", "gemm_skinny.hip", "gemm_mid.hip", "gemm_slab.hip", "gemm_med.hip", "moe.hip", "noalloc.hip",
-           "api_b128.cpp", "quant_b128.hip", "gemm_b128.hip", "wgrad.hip", "balance.hip"]
+           "api_b128.cpp", "quant_b128.hip", "gemm_b128.hip", "wgrad.hip", "wgrad_small.hip",
+           "balance.hip"]
 
 # -packed-fp32-ops: hipcc must not form v_pk_{add,mul,fma}_f32 (the host pass
 # warns that it does not know the feature; that is harmless).
@@ -36,9 +37,11 @@ FLAGS = [
     "-Wno-unused-result", "-I", INCLUDE, "-I", CSRC,
 ]
 
-# The 128-block GEMM adds every MFMA result with vector FMAs: results in VGPRs,
-# not in AGPRs they would first have to be copied from.
-FILE_FLAGS = {"gemm_b128.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+# MFMA results in VGPRs: the 128-block GEMM adds every one with vector FMAs and
+# would first have to copy it from an AGPR; the small weight-gradient tiles
+# fit in VGPRs and the compiler moves them to and from AGPRs otherwise.
+VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+FILE_FLAGS = {"gemm_b128.hip": VGPR_FORM, "wgrad_small.hip": VGPR_FORM}
 
 
 def hipcc():

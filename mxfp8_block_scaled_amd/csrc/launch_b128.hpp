@@ -100,6 +100,8 @@ struct WgradArgs {
   float* part_db;
 };
 int launch_wgrad(const WgradArgs& a, WgradPlan p, hipStream_t stream);
+// Its small-tile form (wgrad_small.hip).
+int launch_wgrad_small(const WgradArgs& a, int splits, hipStream_t stream);
 
 // Load-balance and z loss of a router (balance.hip).
 struct BalanceArgs {

@@ -12,271 +12,28 @@
 // Both operands have the summed axis as their slow axis.  They are staged in
 // LDS as they lie in memory and read with the transposing LDS load
 // (ds_read_b64_tr_b16: sixteen lanes read four rows of sixteen columns and
-// each gets one column's four rows).
-//  * A workgroup owns kT x kT of dW and a run of 64-token steps; four waves
-//    2 x 2.  X is the MFMA A operand, so a lane ends with four consecutive k
-//    of one n: dW rows are written in 16-byte pieces.
-//  * Stages are double-buffered: dY goes straight from global memory into
-//    LDS, X through registers (loaded a step ahead, widened and written while
-//    the MFMAs of the current step run).
-//  * LDS rows are cut into 32-byte slots (one 16-column fragment); slot c of
-//    row m sits at c ^ f(m), f = bits 0, 1, 3 of m: the four rows one
-//    transposing read takes and the next lane group's four (8 further) land
-//    on different banks.
-//  * db costs one more MFMA per dY fragment (A = ones).  Step s of the sum is
-//    done by the workgroups with tile index s % tiles_k along k, so every
-//    workgroup does 1 / tiles_k of it.
-// Partial sums of split runs and of db go to the workspace and are added in
-// a fixed order: results do not depend on timing.
+// each gets one column's four rows).  X is the MFMA A operand, so a lane ends
+// with four consecutive k of one n: dW rows are written in 16-byte pieces.
+// LDS rows are cut into 32-byte slots (one 16-column fragment); slot c of row
+// m sits at c ^ f(m), f = bits 0, 1, 3 of m: the four rows one transposing
+// read takes and the next lane group's four (8 further) land on different
+// banks.
+//
+// db takes the dY fragments as they come by: step s is added by the
+// workgroups with tile index s % tiles_k along k, so each does 1 / tiles_k.
+// Partial sums of tiles whose tokens several workgroups share, and of db, go
+// to the workspace and are added in a fixed order: results do not depend on
+// timing.
+//
+// This file: the large tiles and the choice of the form (wgrad_plan);
+// wgrad_small.hip: the small tiles.
 #include <algorithm>
 
-#include "common.hpp"
-#include "launch_b128.hpp"
-#include "tile_core.hpp"
+#include "wgrad.hpp"
 
 namespace mxfp8 {
 
-namespace {
-
-constexpr int kWgThreads = 256;
-constexpr int kWgStep = 64;   // tokens per step
-
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-
-__device__ inline int slot_xor(int m) { return (m & 3) | ((m >> 1) & 4); }
-
-__device__ inline void store_db(void* db, int bf16, int accumulate, int64_t n, float v) {
-  if (bf16) ((uint16_t*)db)[n] = (uint16_t)pack_bf16x2(v, 0.0f);
-  else ((float*)db)[n] = accumulate ? ((float*)db)[n] + v : v;
-}
-
-template <int kT>
-struct WgLds {
-  static constexpr int kPitch = kT * 2;
-  static constexpr int kOp = kWgStep * kPitch;   // one operand's stage
-  static constexpr int kBytes = 4 * kOp;         // two operands, two stages
-};
-
-}  // namespace
-
-template <int kT, bool kBias>
-__global__ __launch_bounds__(kWgThreads, 2) void wgrad_kernel(
-    const uint16_t* __restrict__ dy, int64_t M, int N, int64_t lddy, const uint8_t* __restrict__ qp,
-    const uint8_t* __restrict__ sp, int K, int KS, int tiles_n, int tiles_k, int splits, void* __restrict__ out,
-    int64_t ldo, int64_t split_stride, int out_bf16, int accumulate, float* __restrict__ part_db) {
-  using L = WgLds<kT>;
-  constexpr int kF = kT / 32;       // 16-wide fragments per wave and axis
-  constexpr int kXV = kT / 64;      // 16-byte X chunks per thread and step
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wk = wave & 1, wn = wave >> 1;
-  const int i = lane & 15, g = lane >> 4;
-  const int item = xcd_remap((int)blockIdx.x, (int)gridDim.x);
-  const int split = item % splits, t = item / splits;
-  const int tn = t / tiles_k, tk = t - tn * tiles_k;
-  const int n0 = tn * kT, k0 = tk * kT;
-  const int64_t steps = (M + kWgStep - 1) / kWgStep;
-  const int64_t s0 = steps * split / splits, s1 = steps * (split + 1) / splits;
-
-  // dY: lane l of a copy takes LDS bytes [16 l, 16 l + 16) of its KiB, i.e.
-  // half h of slot c of row m, which holds logical slot c ^ f(m).  Rows past
-  // M are past the resource's end and read zero; columns past N belong to
-  // outputs that are not stored.
-  constexpr int kLanesRow = L::kPitch / 16, kRowsCopy = 64 / kLanesRow, kCopies = kWgStep / kRowsCopy / 4;
-  uint32_t vy[kCopies];
-#pragma unroll
-  for (int c = 0; c < kCopies; ++c) {
-    const int m = (wave * kCopies + c) * kRowsCopy + lane / kLanesRow, p = lane % kLanesRow;
-    const int col = ((p >> 1) ^ slot_xor(m)) * 16 + (p & 1) * 8;
-    vy[c] = (uint32_t)((int64_t)m * lddy + n0 + col) * 2u;
-  }
-  auto issue_dy = [&](int64_t s, uint8_t* st) {
-    const int64_t m0 = s * kWgStep, rows = min(M - m0, (int64_t)kWgStep);
-    const tile::i4v r = tile::buffer_rsrc(dy + m0 * lddy, (uint32_t)(((rows - 1) * lddy + N) * 2));
-#pragma unroll
-    for (int c = 0; c < kCopies; ++c) tile::b2l_16(vy[c], r, 0u, st + (wave * kCopies + c) * 1024);
-  };
-  // X: chunk j = tid + 256 v of the step's tile: piece (band, 64-K step) in
-  // storage order, lane = chunk of the piece.  The group's scale byte of the
-  // chunk's row and 32-block goes with it.
-  struct X {
-    uint4 q[kXV];
-    uint32_t s[kXV];
-  };
-  uint32_t xoff[kXV], soff[kXV], xdst[kXV];
-  bool xin[kXV];
-#pragma unroll
-  for (int v = 0; v < kXV; ++v) {
-    const int piece = wave + 4 * v;                 // 0 .. kT/16 - 1: (band of 4) x (kT / 64 K steps)
-    const int band = piece & 3, kst = piece >> 2;
-    const int rr = lane >> 2, pos = lane & 3;
-    const int c = pos ^ swz(rr);                    // logical 16-byte chunk
-    const int m = band * 16 + rr;
-    const int ks = k0 / kStepK + kst;
-    xin[v] = ks < KS;
-    xoff[v] = (uint32_t)((size_t)band * KS * kPieceBytes + (size_t)ks * kPieceBytes + lane * 16);
-    // scale_off of row m of this half group (rows 64 .. 127: + 2)
-    soff[v] = (uint32_t)(ks * kTileScaleBytes + scale_off(m, c >> 1));
-    const int col16 = kst * 4 + c;                  // 32-byte slot of the bf16 row
-    xdst[v] = (uint32_t)(m * L::kPitch + (col16 ^ slot_xor(m)) * 32);
-  }
-  auto load_x = [&](int64_t s, X& x) {
-    const int64_t grp = s >> 1;
-    const int half = (int)(s & 1);
-    const uint8_t* q = qp + (size_t)grp * KS * kTileBytes + (size_t)half * 4 * KS * kPieceBytes;
-    const uint8_t* sc = sp + (size_t)grp * KS * kTileScaleBytes + half * 2;
-#pragma unroll
-    for (int v = 0; v < kXV; ++v) {
-      x.q[v] = make_uint4(0u, 0u, 0u, 0u);
-      x.s[v] = 0;
-      if (xin[v]) {
-        x.q[v] = *reinterpret_cast<const uint4*>(q + xoff[v]);
-        x.s[v] = sc[soff[v]];
-      }
-    }
-  };
-  auto store_x = [&](const X& x, uint8_t* st) {
-#pragma unroll
-    for (int v = 0; v < kXV; ++v) {
-      uint4 d[2];
-      widen16(x.q[v], b128_scale_value(x.s[v]), d);
-      *reinterpret_cast<uint4*>(st + xdst[v]) = d[0];
-      *reinterpret_cast<uint4*>(st + xdst[v] + 16) = d[1];
-    }
-  };
-
-  // Fragment f (sixteen columns) and 32-token half h of a stage: lane (i, g)
-  // gets tokens 32 h + 8 g .. + 7 of column i.
-  const int fr = 8 * g + (i >> 2);   // first token row the lane addresses; + 4 for the second read
-  auto frag = [&](const uint8_t* st, int c16, int h) {
-    const int m = 32 * h + fr;
-    const uint8_t* p = st + m * L::kPitch + ((c16 ^ slot_xor(m)) * 32) + (i & 3) * 8;
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * L::kPitch));
-    const s16x8 r = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-    return __builtin_bit_cast(bf16x8, r);
-  };
-
-  v4f acc[kF][kF];
-  v4f accb[kF];
-#pragma unroll
-  for (int a = 0; a < kF; ++a) {
-    accb[a] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int b = 0; b < kF; ++b) acc[a][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  }
-  bf16x8 ones;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) ones[e] = (__bf16)1.0f;
-
-  auto sy = [&](int b) { return smem + b * L::kOp; };
-  auto sx = [&](int b) { return smem + (2 + b) * L::kOp; };
-  X xr;
-  if (s0 < s1) {
-    issue_dy(s0, sy(0));
-    load_x(s0, xr);
-    store_x(xr, sx(0));
-    if (s0 + 1 < s1) load_x(s0 + 1, xr);
-  }
-  int phase = (int)(s0 % tiles_k);
-  for (int64_t s = s0; s < s1; ++s) {
-    const int par = (int)(s - s0) & 1;
-    // This step's dY copies and X stores of every wave have landed; the
-    // other buffers, read in the previous step, are free after the barrier.
-    tile::wait_vmcnt<0>();
-    __syncthreads();
-    if (s + 1 < s1) {
-      issue_dy(s + 1, sy(par ^ 1));
-      store_x(xr, sx(par ^ 1));
-      if (s + 2 < s1) load_x(s + 2, xr);
-    }
-    const bool with_bias = kBias && wk == 0 && phase == tk;
-    phase = phase + 1 == tiles_k ? 0 : phase + 1;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      bf16x8 fx[kF], fy[kF];
-#pragma unroll
-      for (int a = 0; a < kF; ++a) fx[a] = frag(sx(par), wk * kF + a, h);
-#pragma unroll
-      for (int b = 0; b < kF; ++b) fy[b] = frag(sy(par), wn * kF + b, h);
-#pragma unroll
-      for (int a = 0; a < kF; ++a)
-#pragma unroll
-        for (int b = 0; b < kF; ++b) acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[a], fy[b], acc[a][b], 0, 0, 0);
-      if (with_bias) {
-#pragma unroll
-        for (int b = 0; b < kF; ++b) accb[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, fy[b], accb[b], 0, 0, 0);
-      }
-    }
-  }
-
-  // Lane (i, g) holds D[k = 16 a + 4 g + j][n = 16 b + i] of its wave's tile.
-  float* of = (float*)out + (size_t)split * split_stride;
-#pragma unroll
-  for (int b = 0; b < kF; ++b) {
-    const int n = n0 + (wn * kF + b) * 16 + i;
-    if (n >= N) continue;
-#pragma unroll
-    for (int a = 0; a < kF; ++a) {
-      const int k = k0 + (wk * kF + a) * 16 + 4 * g;
-      if (k >= K) continue;   // K % 16 == 0: a quad is all in or all out
-      if (out_bf16) {
-        *reinterpret_cast<uint2*>((uint16_t*)out + (size_t)n * ldo + k) =
-            make_uint2(pack_bf16x2(acc[a][b][0], acc[a][b][1]), pack_bf16x2(acc[a][b][2], acc[a][b][3]));
-      } else {
-        v4f* d = reinterpret_cast<v4f*>(of + (size_t)n * ldo + k);
-        *d = accumulate ? *d + acc[a][b] : acc[a][b];
-      }
-    }
-    // every row of the ones product holds the column sums
-    if (kBias && wk == 0 && g == 0) part_db[((size_t)split * tiles_k + tk) * N + n] = accb[b][0];
-  }
-}
-
-// dw = sum of the split partials in order (+ dw): one thread per 4 k.  db =
-// sum of its partials: the last workgroups, sixteen columns each, thread
-// (q, c) parts q, q + 16, ... of column c, then the sixteen sums in order.
-__global__ __launch_bounds__(256) void wgrad_reduce_kernel(const float* __restrict__ part, int splits, int64_t N,
-                                                           int64_t K, void* __restrict__ dw, int64_t lddw,
-                                                           int out_bf16, int accumulate, int64_t quads,
-                                                           const float* __restrict__ part_db, int parts_db,
-                                                           void* __restrict__ db, int db_bf16) {
-  const int64_t dw_blocks = (quads + 255) / 256;
-  if ((int64_t)blockIdx.x >= dw_blocks) {
-    __shared__ float red[16][17];
-    const int c = threadIdx.x & 15, q = threadIdx.x >> 4;
-    const int64_t n = ((int64_t)blockIdx.x - dw_blocks) * 16 + c;
-    float v = 0.0f;
-    if (n < N)
-      for (int p = q; p < parts_db; p += 16) v += part_db[(size_t)p * N + n];
-    red[q][c] = v;
-    __syncthreads();
-    if (q != 0 || n >= N) return;
-    v = 0.0f;
-#pragma unroll
-    for (int p = 0; p < 16; ++p) v += red[p][c];
-    store_db(db, db_bf16, accumulate, n, v);
-    return;
-  }
-  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (t < quads) {
-    const int64_t per_row = K / 4, n = t / per_row, k = (t - n * per_row) * 4;
-    v4f a = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 0; s < splits; ++s) a += *reinterpret_cast<const v4f*>(part + ((size_t)s * N + n) * K + k);
-    if (out_bf16) {
-      *reinterpret_cast<uint2*>((uint16_t*)dw + (size_t)n * lddw + k) =
-          make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
-    } else {
-      v4f* d = reinterpret_cast<v4f*>((float*)dw + (size_t)n * lddw + k);
-      *d = accumulate ? *d + a : a;
-    }
-    return;
-  }
-}
+using namespace wgrad;
 
 // ---------------------------------------------------------------------------
 // Large tiles: 256 x 256 of dW per workgroup, four waves 2 x 2, each 128 x 128
@@ -597,28 +354,39 @@ constexpr int64_t kRuns = 256;   // compute units
 
 int wgrad_force(int tile) { return g_force_wgrad.exchange(tile); }
 
+// The form with the least estimated time (us, lines through measurements on
+// MI355X: N and K 256 .. 8192, M 64 .. 16384): a start, a cost per 64-token
+// step and per tile of a workgroup, and the second launch with its partials'
+// way to memory and back where a tile's tokens are shared.  For example, small
+// and large tiles: 512 x 1024 x 1024 (M, N, K) 16 and 31; 1000 x 2064 x 2032
+// 43 and 43; 1000 x 4096 x 4096 83 and 54; 4096^3 255 and 142.  Without tokens
+// the small form writes the zeros.
 WgradPlan wgrad_plan(int64_t M, int64_t N, int64_t K) {
-  WgradPlan p;
   const int64_t steps = (M + kWgStep - 1) / kWgStep;
-  const int64_t big = ((N + 255) / 256) * ((K + 255) / 256);
   const int force = g_force_wgrad.load(std::memory_order_relaxed);
-  // Large tiles once every compute unit gets a run of sixteen steps.
-  p.tile = big * steps >= kRuns * 16 ? 256 : 128;
-  if (force) p.tile = force;
-  if (steps == 0) p.tile = 128;
-  p.splits = 1;
-  p.runs = 0;
-  if (p.tile == 256) {
-    // One run per compute unit, of eight steps at least; as many runs as
-    // tiles where that leaves few units idle, for then no tile is shared.
-    p.runs = (int)std::min(kRuns, std::max<int64_t>(1, big * steps / 8));
-    if (big <= kRuns && big * 8 >= kRuns * 7) p.runs = (int)big;
-    return p;
-  }
+  WgradPlan best = {128, 1, 0};
+  if (steps == 0) return best;
+  double best_us = 1e30;
   const int64_t tiles = ((N + 127) / 128) * ((K + 127) / 128);
-  // two workgroups per compute unit
-  while (p.splits < 16 && tiles * p.splits < 512 && steps / (2 * p.splits) >= 4) p.splits *= 2;
-  return p;
+  for (int s = 1; force != 256 && s <= 8 && (s == 1 || steps / s >= 2); s *= 2) {
+    const double rounds = (double)((tiles * s + kRuns - 1) / kRuns);
+    const double us = 8.0 + rounds * (2.0 + 0.9 * (double)((steps + s - 1) / s)) +
+                      (s > 1 ? 3.0 + (double)s * (double)N * (double)K * 8.0 / 4e6 : 0.0);
+    if (us < best_us) {
+      best_us = us;
+      best = {128, s, 0};
+    }
+  }
+  if (force == 128) return best;
+  // Large tiles: one run per compute unit, of eight steps at least; as many
+  // runs as tiles where that leaves few units idle, for then no tile is shared.
+  const int64_t big = ((N + 255) / 256) * ((K + 255) / 256);
+  int64_t runs = std::min(kRuns, std::max<int64_t>(1, big * steps / 8));
+  if (big <= kRuns && big * 8 >= kRuns * 7) runs = big;
+  const double us = 10.0 + 12.0 * (double)((big + runs - 1) / runs) + 1.8 * (double)((big * steps + runs - 1) / runs) +
+                    (big % runs != 0 ? 4.0 + 0.12 * (double)runs : 0.0);
+  if (force == 256 || us < best_us) best = {256, 1, (int)runs};
+  return best;
 }
 
 namespace {
@@ -653,21 +421,6 @@ size_t wgrad_db_bytes(int64_t M, int64_t N, int64_t K, WgradPlan p) {
 
 namespace {
 template <bool kBias>
-int launch_small(const WgradArgs& a, WgradPlan p, hipStream_t stream) {
-  constexpr int lds = WgLds<128>::kBytes;
-  static std::atomic<int> lds_set[kMaxDevices];
-  if (!set_lds_limit_once((const void*)wgrad_kernel<128, kBias>, lds, lds_set)) return -7;
-  const int tiles_n = (int)((a.N + 127) / 128), tiles_k = (int)((a.K + 127) / 128);
-  const bool direct = p.splits == 1;
-  hipLaunchKernelGGL((wgrad_kernel<128, kBias>), dim3((unsigned)(tiles_n * tiles_k * p.splits)), dim3(kWgThreads), lds,
-                     stream, (const uint16_t*)a.dy, a.M, (int)a.N, a.lddy, (const uint8_t*)a.qp,
-                     (const uint8_t*)a.sp, (int)a.K, (int)(2 * b128_blocks(a.K)), tiles_n, tiles_k, p.splits,
-                     direct ? a.dw : (void*)a.part_dw, direct ? a.lddw : a.K, a.N * a.K, direct ? a.out_bf16 : 0,
-                     direct ? a.accumulate : 0, a.part_db);
-  return hipGetLastError() == hipSuccess ? 0 : -7;
-}
-
-template <bool kBias>
 int launch_big(const WgradArgs& a, WgradPlan p, hipStream_t stream) {
   static std::atomic<int> lds_set[kMaxDevices];
   if (!set_lds_limit_once((const void*)wgrad_big_kernel<kBias>, kBigLds, lds_set)) return -7;
@@ -687,16 +440,8 @@ int launch_big(const WgradArgs& a, WgradPlan p, hipStream_t stream) {
 }  // namespace
 
 int launch_wgrad(const WgradArgs& a, WgradPlan p, hipStream_t stream) {
-  const bool bias = a.db != nullptr;
-  if (p.tile == 256) return bias ? launch_big<true>(a, p, stream) : launch_big<false>(a, p, stream);
-  const int st = bias ? launch_small<true>(a, p, stream) : launch_small<false>(a, p, stream);
-  if (st || (p.splits == 1 && !bias)) return st;
-  const int64_t quads = p.splits > 1 ? a.N * (a.K / 4) : 0;
-  const int64_t blocks = (quads + 255) / 256 + (bias ? (a.N + 15) / 16 : 0);
-  const int parts_db = p.splits * (int)((a.K + 127) / 128);
-  hipLaunchKernelGGL(wgrad_reduce_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a.part_dw, p.splits, a.N, a.K, a.dw,
-                     a.lddw, a.out_bf16, a.accumulate, quads, a.part_db, parts_db, a.db, a.db_bf16);
-  return hipGetLastError() == hipSuccess ? 0 : -7;
+  if (p.tile == 128) return launch_wgrad_small(a, p.splits, stream);
+  return a.db != nullptr ? launch_big<true>(a, p, stream) : launch_big<false>(a, p, stream);
 }
 
 }  // namespace mxfp8
