@@ -4,6 +4,8 @@
 // device memory or synchronizes.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "launch_b128.hpp"
@@ -51,6 +53,102 @@ bool gemm_grid_ok(int64_t M, int64_t N) {
   return b128_blocks(N) * ((M + 63) / 64) * mxfp8::kMaxSplitK <= INT32_MAX && M * ((N + 3) / 4) / 256 < INT32_MAX;
 }
 
+// Test hooks: pinned forms (0: by shape).
+std::atomic<int> g_force_mt{0}, g_force_wgrad{0};
+
+// The form and K splits with the least estimated time.  The estimates are
+// lines through measurements on MI355X (us; M 17 .. 8192, N and K 512 ..
+// 28672): a start, a cost per 128-block and round of workgroups, and for K
+// splits a second launch and the partials' way to memory and back.  For
+// example, at N = K = 4096 (64-row, 128-row, 256 x 128, 256 x 256 tiles):
+//   M = 256    18   22   30   43  (with K splits in the first two)
+//   M = 1024   27   26   34   46
+//   M = 2048   50   47   37   49
+//   M = 4096  100   90   69   59
+// All four forms move 10 to 20 TB/s from L2 into LDS, so the bytes a tile
+// reads for its products decide, where there are tiles for all compute units.
+mxfp8::B128Plan b128_plan(int64_t M, int64_t N, int64_t K) {
+  const int64_t G = b128_blocks(N), KB = b128_blocks(K), GM = b128_blocks(M);
+  const int force = g_force_mt.load(std::memory_order_relaxed);
+  // the larger forms write whole 16-byte pieces and address a tile's rows with 32 bits
+  const bool whole = N % 8 == 0 && N <= ((int64_t)1 << 22);
+  mxfp8::B128Plan best = {64, 1};
+  double best_us = 1e30;
+  auto offer = [&](int mt, int splits, double us) {
+    if (us < best_us) {
+      best_us = us;
+      best = {mt, splits};
+    }
+  };
+  auto join = [&](int s) { return s > 1 ? 3.0 + (double)s * (double)M * (double)N * 8.0 / 4e6 : 0.0; };
+  auto blocks = [&](int s) { return (double)((KB + s - 1) / s); };
+  auto wanted = [&](int mt) { return !force || force == mt || !whole; };
+  const int64_t small = G * ((M + 63) / 64);
+  for (int s = 1; wanted(64) && s <= mxfp8::kMaxSplitK && (s == 1 || KB / s >= 2); s *= 2) {
+    const int64_t items = small * s;
+    offer(64, s, 4.5 + (items <= 256 ? 0.35 : 0.67 * (double)((items + 511) / 512)) * blocks(s) + join(s));
+  }
+  if (!whole) return best;
+  for (int s = 1; wanted(128) && s <= mxfp8::kMaxSplitK && (s == 1 || KB / s >= 2); s *= 2)
+    offer(128, s, 4.5 + 0.65 * (double)((G * GM * s + 255) / 256) * blocks(s) + join(s));
+  const int64_t large = (G + 1) / 2 * GM, wide = (G + 1) / 2 * ((GM + 1) / 2);
+  if (wanted(256)) offer(256, 1, 5.0 + (large <= 128 ? 0.75 : 0.95 * (double)((large + 255) / 256)) * blocks(1));
+  if (wanted(512)) offer(512, 1, 5.0 + (wide <= 128 ? 1.25 : 1.7 * (double)((wide + 255) / 256)) * blocks(1));
+  return best;
+}
+
+constexpr int64_t kRuns = 256;   // compute units
+
+// The form with the least estimated time (us, lines through measurements on
+// MI355X: N and K 256 .. 8192, M 64 .. 16384): a start, a cost per 64-token
+// step and per tile of a workgroup, and the second launch with its partials'
+// way to memory and back where a tile's tokens are shared.  For example, small
+// and large tiles: 512 x 1024 x 1024 (M, N, K) 16 and 31; 1000 x 2064 x 2032
+// 43 and 43; 1000 x 4096 x 4096 83 and 54; 4096^3 255 and 142.  Without tokens
+// the small form writes the zeros.
+mxfp8::WgradPlan wgrad_plan(int64_t M, int64_t N, int64_t K) {
+  const int64_t steps = (M + mxfp8::kWgStep - 1) / mxfp8::kWgStep;
+  const int force = g_force_wgrad.load(std::memory_order_relaxed);
+  auto small = [&](int s) {
+    return mxfp8::WgradPlan{128, s, 0, (N + 127) / 128, (K + 127) / 128, steps, 1};
+  };
+  mxfp8::WgradPlan best = small(1);
+  if (steps == 0) return best;
+  double best_us = 1e30;
+  const int64_t tiles = best.tiles();
+  for (int s = 1; force != 256 && s <= 8 && (s == 1 || steps / s >= 2); s *= 2) {
+    const double rounds = (double)((tiles * s + kRuns - 1) / kRuns);
+    const double us = 8.0 + rounds * (2.0 + 0.9 * (double)((steps + s - 1) / s)) +
+                      (s > 1 ? 3.0 + (double)s * (double)N * (double)K * 8.0 / 4e6 : 0.0);
+    if (us < best_us) {
+      best_us = us;
+      best = small(s);
+    }
+  }
+  if (force == 128) return best;
+  // Large tiles: one run per compute unit, of eight steps at least; as many
+  // runs as tiles where that leaves few units idle, for then no tile is shared.
+  const int64_t bn = (N + 255) / 256, bk = (K + 255) / 256, big = bn * bk;
+  int64_t runs = std::min(kRuns, std::max<int64_t>(1, big * steps / 8));
+  if (big <= kRuns && big * 8 >= kRuns * 7) runs = big;
+  const double us = 10.0 + 12.0 * (double)((big + runs - 1) / runs) + 1.8 * (double)((big * steps + runs - 1) / runs) +
+                    (big % runs != 0 ? 4.0 + 0.12 * (double)runs : 0.0);
+  // A shared tile's pieces: its steps over the shortest run, and one more at either end.
+  const int64_t pieces = big % runs != 0 ? steps / (big * steps / runs) + 2 : 1;
+  if (force == 256 || us < best_us) best = {256, 1, (int)runs, bn, bk, steps, pieces};
+  return best;
+}
+
+// fp32 partials of dW, then of db.
+size_t wgrad_dw_bytes(int64_t N, int64_t K, const mxfp8::WgradPlan& p) {
+  if (p.tile == 256) return p.shared() ? (size_t)p.runs * 2 * mxfp8::kWgradTileFloats * 4 : 0;
+  return p.splits > 1 ? (size_t)p.splits * (size_t)N * (size_t)K * 4 : 0;
+}
+size_t wgrad_db_bytes(int64_t N, const mxfp8::WgradPlan& p) {
+  if (p.tile == 256) return (size_t)p.tiles() * (size_t)p.pieces * 256 * 4;
+  return (size_t)p.splits * (size_t)p.tiles_k * (size_t)N * 4;
+}
+
 size_t part_bytes(int64_t M, int64_t N, mxfp8::B128Plan p) {
   return p.splits > 1 ? round_up((size_t)p.splits * (size_t)M * (size_t)((N + 3) / 4 * 4) * 4, 256) : 0;
 }
@@ -58,7 +156,7 @@ size_t part_bytes(int64_t M, int64_t N, mxfp8::B128Plan p) {
 size_t linear_ws(int64_t M, int64_t N, int64_t K) {
   if (M <= mxfp8::kB128DecodeMaxM) return 0;
   return round_up(act_bytes(M, K), 256) + round_up(act_scale_bytes(M, K), 256) +
-         part_bytes(M, N, mxfp8::b128_plan(M, N, K));
+         part_bytes(M, N, b128_plan(M, N, K));
 }
 
 // What the layer's forward call keeps for its backward call: the transposed
@@ -222,13 +320,13 @@ int mxfp8_linear_b128(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, con
   uint8_t* part = sc + round_up(act_scale_bytes(M, K), 256);
   if (int st = mxfp8::launch_quantize_packed_b128(x_bf16, M, K, ldx, q, sc, s)) return st;
   return mxfp8::launch_gemm_b128_tile(q, sc, M, K, w_packed, wsc, N, bias_bf16, y_bf16, ldy, s,
-                                      mxfp8::b128_plan(M, N, K), part);
+                                      b128_plan(M, N, K), part);
 }
 
 int mxfp8_gemm_packed_b128_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes) {
   if (!bytes) return MXFP8_E_NULLPTR;
   if (M < 0 || M > kMaxRows || !rows_ok(N) || !summed_ok(K)) return MXFP8_E_SHAPE;
-  const size_t b = M == 0 ? 0 : part_bytes(M, N, mxfp8::b128_plan(M, N, K));
+  const size_t b = M == 0 ? 0 : part_bytes(M, N, b128_plan(M, N, K));
   *bytes = b > 256 ? b : 256;
   return MXFP8_OK;
 }
@@ -249,25 +347,25 @@ int mxfp8_gemm_packed_b128(const void* q_packed, const void* s_packed, int64_t M
   if (!aligned(workspace, 256)) return MXFP8_E_ALIGN;
   if (int st = mxfp8::check_device_current()) return st;
   return mxfp8::launch_gemm_b128_tile(q_packed, s_packed, M, K, w_packed, (const float*)ws_packed, N, bias_bf16,
-                                      y_bf16, ldy, (hipStream_t)stream, mxfp8::b128_plan(M, N, K), workspace);
+                                      y_bf16, ldy, (hipStream_t)stream, b128_plan(M, N, K), workspace);
 }
 
 int mxfp8_debug_force_b128(int tile) {
   if (tile != 0 && tile != 64 && tile != 128 && tile != 256 && tile != 512) return MXFP8_E_SHAPE;
-  return mxfp8::b128_force(tile);
+  return g_force_mt.exchange(tile);
 }
 
 int mxfp8_linear_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes) {
   if (!bytes) return MXFP8_E_NULLPTR;
   if (M < 0 || M > kMaxRows || !rows_ok(N) || N % 8 != 0 || !summed_ok(K)) return MXFP8_E_SHAPE;
-  const mxfp8::WgradPlan p = mxfp8::wgrad_plan(M, N, K);
-  *bytes = round_up(mxfp8::wgrad_dw_bytes(M, N, K, p), 256) + round_up(mxfp8::wgrad_db_bytes(M, N, K, p), 256);
+  const mxfp8::WgradPlan p = wgrad_plan(M, N, K);
+  *bytes = round_up(wgrad_dw_bytes(N, K, p), 256) + round_up(wgrad_db_bytes(N, p), 256);
   return MXFP8_OK;
 }
 
 int mxfp8_debug_force_wgrad(int tile) {
   if (tile != 0 && tile != 128 && tile != 256) return MXFP8_E_SHAPE;
-  return mxfp8::wgrad_force(tile);
+  return g_force_wgrad.exchange(tile);
 }
 
 int mxfp8_linear_wgrad(const void* dy_bf16, int64_t M, int64_t N, int64_t lddy, const void* q_packed,
@@ -283,7 +381,7 @@ int mxfp8_linear_wgrad(const void* dy_bf16, int64_t M, int64_t N, int64_t lddy, 
   if (M > 0 && (lddy < N || lddy % 8 != 0 || lddy > kMaxK)) return MXFP8_E_LD;
   if (!aligned(dw, 16) || !aligned(db, db_dtype == MXFP8_F32 ? 4 : 2)) return MXFP8_E_ALIGN;
   if (M > 0 && (!aligned(dy_bf16, 16) || !aligned(q_packed, 256) || !aligned(s_packed, 256))) return MXFP8_E_ALIGN;
-  const mxfp8::WgradPlan p = mxfp8::wgrad_plan(M, N, K);
+  const mxfp8::WgradPlan p = wgrad_plan(M, N, K);
   if (b128_blocks(N) * b128_blocks(K) * p.splits > INT32_MAX || N * (K / 4) / 256 >= INT32_MAX - N)
     return MXFP8_E_SHAPE;
   size_t need = 0;
@@ -306,7 +404,7 @@ int mxfp8_linear_wgrad(const void* dy_bf16, int64_t M, int64_t N, int64_t lddy, 
   a.db = db;
   a.db_bf16 = db_dtype == MXFP8_BF16;
   a.part_dw = (float*)workspace;
-  a.part_db = (float*)((uint8_t*)workspace + round_up(mxfp8::wgrad_dw_bytes(M, N, K, p), 256));
+  a.part_db = (float*)((uint8_t*)workspace + round_up(wgrad_dw_bytes(N, K, p), 256));
   return mxfp8::launch_wgrad(a, p, (hipStream_t)stream);
 }
 
@@ -390,7 +488,7 @@ int mxfp8_linear_b128_backward(const void* dy_bf16, int64_t M, int64_t N, int64_
 int mxfp8_moe_balance_workspace_bytes(int64_t T, int64_t E, size_t* bytes) {
   if (!bytes) return MXFP8_E_NULLPTR;
   if (T < 0 || E < 1 || E > mxfp8::kMoeMaxExperts) return MXFP8_E_SHAPE;
-  *bytes = mxfp8::balance_ws_bytes(T, E);
+  *bytes = mxfp8::balance_ws_bytes(E);
   return MXFP8_OK;
 }
 
@@ -400,7 +498,7 @@ int mxfp8_moe_balance(const void* logits, int dtype, int64_t T, int64_t E, int64
   if (int st = check_logits(logits, dtype, T, E, ldl, topk)) return st;
   if (!loss || !counts || !used) return MXFP8_E_NULLPTR;
   if (!aligned(loss, 4) || !aligned(counts, 4) || !aligned(used, 4)) return MXFP8_E_ALIGN;
-  if (!workspace || workspace_bytes < mxfp8::balance_ws_bytes(T, E)) return MXFP8_E_WORKSPACE;
+  if (!workspace || workspace_bytes < mxfp8::balance_ws_bytes(E)) return MXFP8_E_WORKSPACE;
   if (!aligned(workspace, 256)) return MXFP8_E_ALIGN;
   if (int st = mxfp8::check_device_current()) return st;
   mxfp8::BalanceArgs a = {};

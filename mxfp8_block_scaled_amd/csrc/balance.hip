@@ -28,8 +28,7 @@
 #include <climits>
 #include <type_traits>
 
-#include "common.hpp"
-#include "launch_b128.hpp"
+#include "b128.hpp"
 
 namespace mxfp8 {
 
@@ -37,7 +36,6 @@ namespace {
 
 constexpr int kBalThreads = 512;
 constexpr int kBalTokens = kBalThreads / 16;   // tokens a workgroup works on at a time
-constexpr int kBalMaxBlocks = 512;             // two per compute unit: few partials to read back
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu, kKeyPosInf = 0xFF800000u;   // order_key of the infinities
 
 template <int kCtrl>
@@ -464,11 +462,6 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(const void* __res
       }
     }
   }
-}
-
-size_t balance_ws_bytes(int64_t T, int64_t E) {
-  (void)T;
-  return 16 * 8 + (size_t)kBalMaxBlocks * ((size_t)E * 8 + 8) + 8;
 }
 
 namespace {

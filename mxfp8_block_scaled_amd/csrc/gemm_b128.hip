@@ -11,8 +11,7 @@
 // register.  Four v_fma (16 cycles) against one MFMA (32 cycles) fit in the
 // MFMA's shadow; the price is that the accumulators have to be ordinary
 // vector registers, half of the register file.
-#include "common.hpp"
-#include "launch_b128.hpp"
+#include "b128.hpp"
 #include "tile_core.hpp"
 
 namespace mxfp8 {
@@ -509,7 +508,8 @@ __global__ __launch_bounds__(kB128Threads, 1) void gemm_b128_big_kernel(
     tile::i4v w0, w1, x, s;
   };
   auto src_of = [&](BigTile t) {
-    const int g1 = kG == 2 ? min(2 * t.tn + 1, GN - 1) : t.tn;   // past the last group: any data, its columns are dropped
+    // past the last group: any data, its columns are dropped
+    const int g1 = kG == 2 ? min(2 * t.tn + 1, GN - 1) : t.tn;
     return Src{wp + (size_t)(kG * t.tn) * gbytes, wp + (size_t)g1 * gbytes, qp + (size_t)t.tm * gbytes,
                sp + (size_t)t.tm * sbytes};
   };
@@ -652,7 +652,7 @@ __global__ __launch_bounds__(kB128Threads, 1) void gemm_b128_big_kernel(
     tile::static_for<0, 4 * kA + 3>([&](auto J) {
       constexpr int j = decltype(J)::value;
       if constexpr (j < 4 * kA) {
-        d[j & 3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(f.w[j >> 2], f.x[j & 3], v4f{0.0f, 0.0f, 0.0f, 0.0f},
+        d[j & 3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(f.w[j >> 2], f.x[j & 3], v4f{0, 0, 0, 0},
                                                                     0, 0, 0, kUnitScales, j & 3, f.s);
         asm volatile("" : "+v"(d[j & 3]));
       }
@@ -888,53 +888,6 @@ __global__ __launch_bounds__(kWideThreads, 1) void gemm_b128_wide_kernel(
     ws = scalar_scale(wsg, mp);
   }
   tile::wait_vmcnt<0>();   // no copy may land after the workgroup's LDS is given away
-}
-
-namespace {
-std::atomic<int> g_force_mt{0};
-}
-
-int b128_force(int mt) { return g_force_mt.exchange(mt); }
-
-// The form and K splits with the least estimated time.  The estimates are
-// lines through measurements on MI355X (us; M 17 .. 8192, N and K 512 ..
-// 28672): a start, a cost per 128-block and round of workgroups, and for K
-// splits a second launch and the partials' way to memory and back.  For
-// example, at N = K = 4096 (64-row, 128-row, 256 x 128, 256 x 256 tiles):
-//   M = 256    18   22   30   43  (with K splits in the first two)
-//   M = 1024   27   26   34   46
-//   M = 2048   50   47   37   49
-//   M = 4096  100   90   69   59
-// All four forms move 10 to 20 TB/s from L2 into LDS, so the bytes a tile
-// reads for its products decide, where there are tiles for all compute units.
-B128Plan b128_plan(int64_t M, int64_t N, int64_t K) {
-  const int64_t G = b128_blocks(N), KB = b128_blocks(K), GM = b128_blocks(M);
-  const int force = g_force_mt.load(std::memory_order_relaxed);
-  // the larger forms write whole 16-byte pieces and address a tile's rows with 32 bits
-  const bool whole = N % 8 == 0 && N <= ((int64_t)1 << 22);
-  B128Plan best = {64, 1};
-  double best_us = 1e30;
-  auto offer = [&](int mt, int splits, double us) {
-    if (us < best_us) {
-      best_us = us;
-      best = {mt, splits};
-    }
-  };
-  auto join = [&](int s) { return s > 1 ? 3.0 + (double)s * (double)M * (double)N * 8.0 / 4e6 : 0.0; };
-  auto blocks = [&](int s) { return (double)((KB + s - 1) / s); };
-  auto wanted = [&](int mt) { return !force || force == mt || !whole; };
-  const int64_t small = G * ((M + 63) / 64);
-  for (int s = 1; wanted(64) && s <= kMaxSplitK && (s == 1 || KB / s >= 2); s *= 2) {
-    const int64_t items = small * s;
-    offer(64, s, 4.5 + (items <= 256 ? 0.35 : 0.67 * (double)((items + 511) / 512)) * blocks(s) + join(s));
-  }
-  if (!whole) return best;
-  for (int s = 1; wanted(128) && s <= kMaxSplitK && (s == 1 || KB / s >= 2); s *= 2)
-    offer(128, s, 4.5 + 0.65 * (double)((G * GM * s + 255) / 256) * blocks(s) + join(s));
-  const int64_t large = (G + 1) / 2 * GM, wide = (G + 1) / 2 * ((GM + 1) / 2);
-  if (wanted(256)) offer(256, 1, 5.0 + (large <= 128 ? 0.75 : 0.95 * (double)((large + 255) / 256)) * blocks(1));
-  if (wanted(512)) offer(512, 1, 5.0 + (wide <= 128 ? 1.25 : 1.7 * (double)((wide + 255) / 256)) * blocks(1));
-  return best;
 }
 
 namespace {

@@ -4,37 +4,12 @@
 // and each returns 0 or -7 (launch error).
 #pragma once
 
-#include "common.hpp"
 #include "launch.hpp"
 
 namespace mxfp8 {
 
 constexpr int64_t kB128 = 128;   // elements of a scale block along each blocked axis
 __host__ __device__ inline int64_t b128_blocks(int64_t n) { return (n + kB128 - 1) / kB128; }
-
-// Scale byte of a 128-block from the bf16 bits of its largest magnitude (the
-// rule is stated in quant_b128.hip).
-__device__ inline uint32_t b128_scale_byte(uint32_t amax) {
-  const int f = (int)(amax >> 7), up = (int)(amax & 0x7Fu) > 96 ? 1 : 0;
-  return amax >= 0x7F80u ? 0xFFu : (uint32_t)max(f - 8 + up, 0);
-}
-// Its value, with the UE8M0 NaN as an fp32 NaN.
-__device__ inline float b128_scale_value(uint32_t sb) {
-  return __uint_as_float(sb == 0xFFu ? 0x7FC00000u : sb ? sb << 23 : 0x00400000u);
-}
-
-// Sixteen E4M3 bytes of one scale -> sixteen bf16, two 16-byte words.
-__device__ inline void widen16(const uint4& q, float scale, uint4* out) {
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-  uint32_t d[8];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    d[2 * e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[e], scale, false));
-    d[2 * e + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[e], scale, true));
-  }
-  out[0] = make_uint4(d[0], d[1], d[2], d[3]);
-  out[1] = make_uint4(d[4], d[5], d[6], d[7]);
-}
 
 // x bf16 [M, K] (K % 16 == 0) -> E4M3 [M, K] + UE8M0 [M, ceil(K / 128)].
 int launch_quantize_b128(const void* x, int64_t M, int64_t K, int64_t ldx, void* q, int64_t ldq, void* s, int64_t lds,
@@ -66,8 +41,6 @@ struct B128Plan {
   int mt;       // 64 or 128: activation rows of a 128-column tile; 256: large tiles; 512: wide tiles
   int splits;
 };
-int b128_force(int mt);   // test hook: pins mt (0: by shape); returns the previous value
-B128Plan b128_plan(int64_t M, int64_t N, int64_t K);
 int launch_gemm_b128_tile(const void* qp, const void* sp, int64_t M, int64_t K, const void* wp, const float* wsc,
                           int64_t N, const void* bias, void* y, int64_t ldy, hipStream_t stream, B128Plan plan,
                           void* part);
@@ -75,15 +48,17 @@ int launch_gemm_b128_tile(const void* qp, const void* sp, int64_t M, int64_t K, 
 // Weight gradient dW[n, k] = sum_m dY[m, n] X[m, k] from packed 8-bit
 // activations (either scale block), and db[n] = sum_m dY[m, n].
 struct WgradPlan {
-  int tile;     // edge of a workgroup's dW tile: 128 or 256
-  int splits;   // tile 128: runs of 64-token steps each tile's tokens are cut into
-  int runs;     // tile 256: workgroups, one equal run of the (tile, step) units each
+  int tile;          // edge of a workgroup's dW tile: 128 or 256
+  int splits;        // tile 128: runs of 64-token steps each tile's tokens are cut into
+  int runs;          // tile 256: workgroups, one equal run of the (tile, step) units each
+  int64_t tiles_n, tiles_k;
+  int64_t steps;     // 64-token steps
+  int64_t pieces;    // tile 256: most runs that share a tile (1: none is shared)
+  int64_t tiles() const { return tiles_n * tiles_k; }
+  bool shared() const { return pieces > 1; }
 };
-WgradPlan wgrad_plan(int64_t M, int64_t N, int64_t K);
-int wgrad_force(int tile);   // test hook: pins the tile (0: by shape); returns the previous value
-// fp32 partials of dW, then of db.
-size_t wgrad_dw_bytes(int64_t M, int64_t N, int64_t K, WgradPlan p);
-size_t wgrad_db_bytes(int64_t M, int64_t N, int64_t K, WgradPlan p);
+constexpr int kWgStep = 64;                        // tokens per step
+constexpr int64_t kWgradTileFloats = 256 * 256;    // a large tile's partial in the workspace
 struct WgradArgs {
   const void* dy;       // bf16 [M, N], row stride lddy
   int64_t M, N, lddy;
@@ -118,7 +93,9 @@ struct BalanceArgs {
   int64_t ldd;
   void* ws;                // forward partials
 };
-size_t balance_ws_bytes(int64_t T, int64_t E);
+constexpr int kBalMaxBlocks = 512;   // forward workgroups, each with partials in the workspace
+// [16] doubles, then per forward workgroup sums and counts of the experts, z and n, then the arrival count.
+inline size_t balance_ws_bytes(int64_t E) { return 16 * 8 + (size_t)kBalMaxBlocks * ((size_t)E * 8 + 8) + 8; }
 int launch_balance(const BalanceArgs& a, hipStream_t stream);
 int launch_balance_backward(const BalanceArgs& a, hipStream_t stream);
 

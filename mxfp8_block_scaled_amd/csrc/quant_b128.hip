@@ -11,8 +11,7 @@
 // output it enters is NaN.  A power of two costs a floating-point element
 // grid no precision, makes the dequantized value exact in bf16 (an E4M3 value
 // has four significant bits), and lets the scaled MFMA apply it.
-#include "common.hpp"
-#include "launch_b128.hpp"
+#include "b128.hpp"
 
 namespace mxfp8 {
 

@@ -25,10 +25,7 @@
 // to the workspace and are added in a fixed order: results do not depend on
 // timing.
 //
-// This file: the large tiles and the choice of the form (wgrad_plan);
-// wgrad_small.hip: the small tiles.
-#include <algorithm>
-
+// This file: the large tiles; wgrad_small.hip: the small tiles.
 #include "wgrad.hpp"
 
 namespace mxfp8 {
@@ -56,7 +53,6 @@ constexpr int kBigT = 256;
 constexpr int kBigPitch = kBigT * 2;
 constexpr int kBigOp = kWgStep * kBigPitch;        // 32 KiB: one operand's stage
 constexpr int kBigLds = 4 * kBigOp;                // dY x 2, X x 2
-constexpr int kBigTileFloats = kBigT * kBigT;
 
 // Runs: workgroup w of G takes units [U w / G, U (w + 1) / G) of U.
 __host__ __device__ inline int64_t run_start(int64_t U, int G, int64_t w) { return U * w / G; }
@@ -269,7 +265,8 @@ __global__ __launch_bounds__(kWgThreads, 1) void wgrad_big_kernel(
       }
     } else {
       // slot 0: the piece at the start of the run, 1: at its end
-      v4f* d = reinterpret_cast<v4f*>(part + ((size_t)w * 2 + (u == u0 ? 0 : 1)) * kBigTileFloats) + wave * 4096 + lane;
+      v4f* d = reinterpret_cast<v4f*>(part + ((size_t)w * 2 + (u == u0 ? 0 : 1)) * kWgradTileFloats);
+      d += wave * 4096 + lane;
 #pragma unroll
       for (int a = 0; a < 8; ++a)
 #pragma unroll
@@ -331,7 +328,7 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(const float* __restrict
     for (int w = w0; w <= w1; ++w) {
       // a piece lies at the start of its run unless the run began in an earlier tile
       const int slot = run_start(U, G, w) >= (int64_t)t * steps ? 0 : 1;
-      v += reinterpret_cast<const v4f*>(part + ((size_t)w * 2 + slot) * kBigTileFloats)[e];
+      v += reinterpret_cast<const v4f*>(part + ((size_t)w * 2 + slot) * kWgradTileFloats)[e];
     }
     const int wave = e >> 12, ab = (e >> 6) & 63, lane = e & 63;
     const int n = tn * kBigT + (wave >> 1) * 128 + (ab & 7) * 16 + (lane & 15);
@@ -348,93 +345,20 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(const float* __restrict
 }
 
 namespace {
-std::atomic<int> g_force_wgrad{0};
-constexpr int64_t kRuns = 256;   // compute units
-}
-
-int wgrad_force(int tile) { return g_force_wgrad.exchange(tile); }
-
-// The form with the least estimated time (us, lines through measurements on
-// MI355X: N and K 256 .. 8192, M 64 .. 16384): a start, a cost per 64-token
-// step and per tile of a workgroup, and the second launch with its partials'
-// way to memory and back where a tile's tokens are shared.  For example, small
-// and large tiles: 512 x 1024 x 1024 (M, N, K) 16 and 31; 1000 x 2064 x 2032
-// 43 and 43; 1000 x 4096 x 4096 83 and 54; 4096^3 255 and 142.  Without tokens
-// the small form writes the zeros.
-WgradPlan wgrad_plan(int64_t M, int64_t N, int64_t K) {
-  const int64_t steps = (M + kWgStep - 1) / kWgStep;
-  const int force = g_force_wgrad.load(std::memory_order_relaxed);
-  WgradPlan best = {128, 1, 0};
-  if (steps == 0) return best;
-  double best_us = 1e30;
-  const int64_t tiles = ((N + 127) / 128) * ((K + 127) / 128);
-  for (int s = 1; force != 256 && s <= 8 && (s == 1 || steps / s >= 2); s *= 2) {
-    const double rounds = (double)((tiles * s + kRuns - 1) / kRuns);
-    const double us = 8.0 + rounds * (2.0 + 0.9 * (double)((steps + s - 1) / s)) +
-                      (s > 1 ? 3.0 + (double)s * (double)N * (double)K * 8.0 / 4e6 : 0.0);
-    if (us < best_us) {
-      best_us = us;
-      best = {128, s, 0};
-    }
-  }
-  if (force == 128) return best;
-  // Large tiles: one run per compute unit, of eight steps at least; as many
-  // runs as tiles where that leaves few units idle, for then no tile is shared.
-  const int64_t big = ((N + 255) / 256) * ((K + 255) / 256);
-  int64_t runs = std::min(kRuns, std::max<int64_t>(1, big * steps / 8));
-  if (big <= kRuns && big * 8 >= kRuns * 7) runs = big;
-  const double us = 10.0 + 12.0 * (double)((big + runs - 1) / runs) + 1.8 * (double)((big * steps + runs - 1) / runs) +
-                    (big % runs != 0 ? 4.0 + 0.12 * (double)runs : 0.0);
-  if (force == 256 || us < best_us) best = {256, 1, (int)runs};
-  return best;
-}
-
-namespace {
-struct BigShape {
-  int64_t tiles_n, tiles_k, tiles, steps, U, pieces;
-  bool shared;   // some tile belongs to several runs
-};
-BigShape big_shape(int64_t M, int64_t N, int64_t K, WgradPlan p) {
-  BigShape b;
-  b.tiles_n = (N + kBigT - 1) / kBigT;
-  b.tiles_k = (K + kBigT - 1) / kBigT;
-  b.tiles = b.tiles_n * b.tiles_k;
-  b.steps = (M + kWgStep - 1) / kWgStep;
-  b.U = b.tiles * b.steps;
-  b.shared = b.tiles % p.runs != 0;
-  b.pieces = b.shared ? b.steps / (b.U / p.runs) + 2 : 1;
-  return b;
-}
-}  // namespace
-
-size_t wgrad_dw_bytes(int64_t M, int64_t N, int64_t K, WgradPlan p) {
-  if (p.tile == 256) return big_shape(M, N, K, p).shared ? (size_t)p.runs * 2 * kBigTileFloats * 4 : 0;
-  return p.splits > 1 ? (size_t)p.splits * (size_t)N * (size_t)K * 4 : 0;
-}
-size_t wgrad_db_bytes(int64_t M, int64_t N, int64_t K, WgradPlan p) {
-  if (p.tile == 256) {
-    const BigShape b = big_shape(M, N, K, p);
-    return (size_t)b.tiles * (size_t)b.pieces * kBigT * 4;
-  }
-  return (size_t)p.splits * (size_t)((K + 127) / 128) * (size_t)N * 4;
-}
-
-namespace {
 template <bool kBias>
 int launch_big(const WgradArgs& a, WgradPlan p, hipStream_t stream) {
   static std::atomic<int> lds_set[kMaxDevices];
   if (!set_lds_limit_once((const void*)wgrad_big_kernel<kBias>, kBigLds, lds_set)) return -7;
-  const BigShape b = big_shape(a.M, a.N, a.K, p);
   hipLaunchKernelGGL(wgrad_big_kernel<kBias>, dim3((unsigned)p.runs), dim3(kWgThreads), kBigLds, stream,
                      (const uint16_t*)a.dy, a.M, (int)a.N, a.lddy, (const uint8_t*)a.qp, (const uint8_t*)a.sp,
-                     (int)a.K, (int)(2 * b128_blocks(a.K)), (int)b.tiles_k, (int)b.tiles, (int)b.steps, a.dw, a.lddw,
-                     a.out_bf16, a.accumulate, a.part_dw, a.part_db, (int)b.pieces);
+                     (int)a.K, (int)(2 * b128_blocks(a.K)), (int)p.tiles_k, (int)p.tiles(), (int)p.steps, a.dw, a.lddw,
+                     a.out_bf16, a.accumulate, a.part_dw, a.part_db, (int)p.pieces);
   if (hipGetLastError() != hipSuccess) return -7;
-  if (!b.shared && !kBias) return 0;
-  const int join = b.shared ? (int)b.tiles : 0, cols = kBias ? (int)((a.N + 15) / 16) : 0;
-  hipLaunchKernelGGL(wgrad_join_kernel, dim3((unsigned)(join * 16 + cols)), dim3(256), 0, stream, a.part_dw, b.U,
-                     p.runs, join, (int)b.tiles_k, (int)b.steps, (int)a.N, (int)a.K, a.dw, a.lddw, a.out_bf16,
-                     a.accumulate, a.part_db, (int)b.pieces, a.db, a.db_bf16);
+  if (!p.shared() && !kBias) return 0;
+  const int join = p.shared() ? (int)p.tiles() : 0, cols = kBias ? (int)((a.N + 15) / 16) : 0;
+  hipLaunchKernelGGL(wgrad_join_kernel, dim3((unsigned)(join * 16 + cols)), dim3(256), 0, stream, a.part_dw,
+                     p.tiles() * p.steps, p.runs, join, (int)p.tiles_k, (int)p.steps, (int)a.N, (int)a.K, a.dw,
+                     a.lddw, a.out_bf16, a.accumulate, a.part_db, (int)p.pieces, a.db, a.db_bf16);
   return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 }  // namespace

@@ -1,15 +1,13 @@
 // Device code that the two forms of the weight gradient share.
 #pragma once
 
-#include "common.hpp"
-#include "launch_b128.hpp"
+#include "b128.hpp"
 #include "tile_core.hpp"
 
 namespace mxfp8 {
 namespace wgrad {
 
 constexpr int kWgThreads = 256;
-constexpr int kWgStep = 64;   // tokens per step
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
