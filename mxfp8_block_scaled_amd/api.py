@@ -251,6 +251,8 @@ def mxfp8_gemm_prequant(q, ldq, s, lds, M, K, wp, wsp, N, bias, y, ldy, ws, ws_b
 def gemm_prequant(q, s, pw, bias=None):
     """The block-scaled GEMM + epilogue on row-major quantized activations
     (uint8 E4M3 ``q[M, K]``, UE8M0 ``s[M, >= K/32]``, GPU): bf16 ``[M, N]``."""
+    if isinstance(pw, PreparedWeightB128):
+        raise ValueError("gemm_prequant takes an MXFP8 weight, not one with 128-blocks")
     q = _as_bytes(q)
     s = _as_bytes(s)
     _require_cuda(q, "q")
