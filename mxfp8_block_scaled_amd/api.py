@@ -647,7 +647,7 @@ def prepare_weight_b128(w_q, w_s, transpose=False):
     if w_q.stride(-1) != 1 or w_q.stride(0) % 16 != 0 or w_q.stride(0) < K or w_q.data_ptr() % 16 != 0:
         w_q = w_q.clone(memory_format=torch.contiguous_format)
     if w_s.stride(-1) != 1 or w_s.stride(0) < w_s.shape[1]:
-        w_s = w_s.contiguous()
+        w_s = w_s.clone(memory_format=torch.contiguous_format)
     with _on(w_q.device):
         pw = _empty_b128(K, N, w_q.device) if transpose else _empty_b128(N, K, w_q.device)
         _check(lib().mxfp8_prepare_weight_b128(_ptr(w_q), _ptr(w_s), N, K, w_q.stride(0), w_s.stride(0),
@@ -784,36 +784,69 @@ def _layer_bytes(M, N, K, keep):
     return tuple(o.value for o in out)
 
 
+def _linear_b128_forward(x, w, bias, keep):
+    """(y, what the backward call needs, its workspace bytes) of a step that
+    keeps what MXFP8_KEEP_DX (1) and MXFP8_KEEP_DW (2) in ``keep`` ask for."""
+    x2, w2, bias = _rows(x, "x"), _rows(w, "w"), _bias(bias, w.shape[0])
+    (M, K), N, d = x2.shape, w2.shape[0], x.device
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=d)
+    with _on(d):
+        kept_bytes, ws_bytes, back_bytes = _layer_bytes(M, N, K, keep)
+        kept, ws = _scratch(kept_bytes, d), _scratch(ws_bytes, d)
+        _check(lib().mxfp8_linear_b128_forward(_ptr(x2), M, K, x2.stride(0), _ptr(w2), N, w2.stride(0), _ptr(bias),
+                                               _ptr(y), N, keep, _ptr(kept), _ptr(ws), ws_bytes, _stream(d)),
+               "mxfp8_linear_b128_forward")
+    return y if x.dim() == 2 else y.view(*x.shape[:-1], N), kept, back_bytes
+
+
+def _mark_leaves(out, stream):
+    """Notes on each leaf's gradient accumulator, which lives as long as some
+    graph of that leaf, the stream it belongs to: the one of its first use."""
+    for node, _ in out.grad_fn.next_functions:
+        if hasattr(node, "variable"):
+            node.metadata.setdefault("mxfp8_stream", stream)
+
+
+def _check_capture(node, stream, capturing):
+    """A captured backward pass cannot hand a gradient to an accumulator of
+    another stream: torch would make that stream wait for a captured event, and
+    the process ends.  That is the case where a graph from before the capture
+    still holds the leaf's accumulator."""
+    if not capturing:
+        return
+    for n, _ in node.next_functions:
+        if hasattr(n, "variable") and n.metadata.get("mxfp8_stream", stream) != stream:
+            raise RuntimeError("backward pass captured while an earlier autograd graph of the same leaf tensors is "
+                               "alive on another stream: delete its outputs before the capture")
+
+
 class _LinearB128(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, bias):
         need_x, need_w, need_b = ctx.needs_input_grad
-        x2, w2, bias = _rows(x, "x"), _rows(w, "w"), _bias(bias, w.shape[0])
-        (M, K), N, d = x2.shape, w2.shape[0], x.device
-        keep = (1 if need_x else 0) | (2 if need_w or need_b else 0)
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=d)
-        with _on(d):
-            kept_bytes, ws_bytes, ctx.ws_bytes = _layer_bytes(M, N, K, keep)
-            kept, ws = _scratch(kept_bytes, d), _scratch(ws_bytes, d)
-            _check(lib().mxfp8_linear_b128_forward(_ptr(x2), M, K, x2.stride(0), _ptr(w2), N, w2.stride(0), _ptr(bias),
-                                                   _ptr(y), N, keep, _ptr(kept), _ptr(ws), ws_bytes, _stream(d)),
-                   "mxfp8_linear_b128_forward")
-        ctx.kept, ctx.keep, ctx.sizes, ctx.shape = kept, keep, (M, N, K), x.shape
-        return y if x.dim() == 2 else y.view(*x.shape[:-1], N)
+        ctx.keep = (1 if need_x else 0) | (2 if need_w or need_b else 0)
+        y, kept, ctx.ws_bytes = _linear_b128_forward(x, w, bias, ctx.keep)
+        ctx.save_for_backward(kept)   # freed with the graph's other saved tensors
+        ctx.shape = x.shape
+        return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         need_x, need_w, need_b = ctx.needs_input_grad
-        d2, (M, N, K), d = _rows(dy, "dy"), ctx.sizes, dy.device
+        kept, = ctx.saved_tensors
+        d = dy.device
+        _check_capture(ctx, _stream(d), torch.cuda.is_current_stream_capturing())
+        d2 = _rows(dy, "dy")
+        (M, N), K = d2.shape, ctx.shape[-1]
         new = functools.partial(torch.empty, dtype=torch.bfloat16, device=d)
         dx = new((M, K)) if need_x else None
         dw = new((N, K)) if need_w or need_b else None
         db = new(N) if need_b else None
         with _on(d):
             ws = _scratch(ctx.ws_bytes, d)
-            _check(lib().mxfp8_linear_b128_backward(_ptr(d2), M, N, d2.stride(0), K, ctx.keep, _ptr(ctx.kept), _ptr(dx),
-                                                    K, _ptr(dw), 1, K, _ptr(db), 1, _ptr(ws), ws.numel(), _stream(d)),
+            _check(lib().mxfp8_linear_b128_backward(_ptr(d2), M, N, d2.stride(0), K, ctx.keep, _ptr(kept), _ptr(dx), K,
+                                                    _ptr(dw), 1, K, _ptr(db), 1, _ptr(ws), ws.numel(), _stream(d)),
                    "mxfp8_linear_b128_backward")
         if need_x and len(ctx.shape) != 2:
             dx = dx.view(ctx.shape)
@@ -829,7 +862,12 @@ def linear_b128(x, w, bias=None):
     keeps the activations as the 8-bit checkpoint its GEMM reads.  Backward:
     ``dx = deq(q(dy)) @ deq(q(w))``, dy quantized like activations;
     ``dw = dy^T @ deq(q(x))`` and ``db`` from bf16 dy.  The quantizations
-    are passed straight through."""
+    are passed straight through.  Where no gradient can be asked for
+    (torch.no_grad, or no operand requires one) nothing is kept.
+
+    A step can be captured into a graph.  The backward pass of one is refused
+    while an eager autograd graph of the same leaves is alive on another
+    stream."""
     for t, name in ((x, "x"), (w, "w")) + (((bias, "bias"),) if bias is not None else ()):
         if t.dtype != torch.bfloat16:
             raise ValueError(f"{name} must be bfloat16, got {t.dtype}")
@@ -837,7 +875,12 @@ def linear_b128(x, w, bias=None):
     if w.dim() != 2 or x.shape[-1] != w.shape[1] or w.shape[0] % 16 or w.shape[1] % 16:
         raise ValueError(f"x [..., K] and w [N, K] with N and K multiples of 16, got {tuple(x.shape)}, {tuple(w.shape)}")
     _same_device(x, w, bias)
-    return _LinearB128.apply(x, w, bias)
+    if not torch.is_grad_enabled() or not (x.requires_grad or w.requires_grad or
+                                           (bias is not None and bias.requires_grad)):
+        return _linear_b128_forward(x, w, bias, 0)[0]
+    y = _LinearB128.apply(x, w, bias)
+    _mark_leaves(y, _stream(x.device))
+    return y
 
 
 # ---------------------------------------------------------------------------
@@ -938,7 +981,7 @@ def _router_args(logits, valid):
         raise ValueError(f"logits must be float32 or bfloat16 [T, E], got {logits.dtype} {tuple(logits.shape)}")
     _require_cuda(logits, "logits")
     if logits.stride(-1) != 1 or logits.stride(0) < logits.shape[1]:
-        logits = logits.contiguous()
+        logits = logits.clone(memory_format=torch.contiguous_format)
     if valid is not None:
         if valid.dtype not in (torch.bool, torch.uint8) or tuple(valid.shape) != (logits.shape[0],):
             raise ValueError(f"valid must be bool or uint8 [{logits.shape[0]}]")
@@ -1003,6 +1046,7 @@ class _MoEBalance(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad, _):
+        _check_capture(ctx, _stream(grad.device), torch.cuda.is_current_stream_capturing())
         logits, counts, used, valid = ctx.saved_tensors
         topk, coef, z_coef = ctx.args
         return moe_balance_backward(logits, topk, counts, used, valid, coef, z_coef, grad), None, None, None, None
@@ -1010,5 +1054,9 @@ class _MoEBalance(torch.autograd.Function):
 
 def moe_balance_loss(logits, topk, valid=None, coef=1e-2, z_coef=0.0):
     """``moe_balance`` for autograd: ``(loss, counts)``, the loss
-    differentiable with respect to ``logits``."""
-    return _MoEBalance.apply(logits, topk, valid, coef, z_coef)
+    differentiable with respect to ``logits``.  In captured graphs as
+    ``linear_b128``."""
+    loss, counts = _MoEBalance.apply(logits, topk, valid, coef, z_coef)
+    if loss.requires_grad:
+        _mark_leaves(loss, _stream(loss.device))
+    return loss, counts
