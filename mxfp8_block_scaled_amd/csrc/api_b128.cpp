@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
+#include <numeric>
 
 #include "launch_b128.hpp"
 #include "mxfp8.h"
@@ -99,55 +100,55 @@ mxfp8::B128Plan b128_plan(int64_t M, int64_t N, int64_t K) {
 
 constexpr int64_t kRuns = 256;   // compute units
 
-// The form with the least estimated time (us, lines through measurements on
-// MI355X: N and K 256 .. 8192, M 64 .. 16384): a start, a cost per 64-token
-// step and per tile of a workgroup, and the second launch with its partials'
-// way to memory and back where a tile's tokens are shared.  For example, small
-// and large tiles: 512 x 1024 x 1024 (M, N, K) 16 and 31; 1000 x 2064 x 2032
-// 43 and 43; 1000 x 4096 x 4096 83 and 54; 4096^3 255 and 142.  Without tokens
-// the small form writes the zeros.
+// The form and the runs with the least estimated time (us, lines through
+// measurements on MI355X: N and K 160 .. 8192, M 64 .. 16384): a start, a cost
+// per tile and per 64-token step of a workgroup, and where tiles are shared
+// the partials' way to memory and back and the launch that joins them.  For
+// example (M, N, K; small tiles whole and in equal runs, large tiles the same):
+//   512 x 1024 x 1024     17   21   32   32
+//   16384 x 256 x 256    260   33  455   37
+//   1000 x 2064 x 2032    44   39   48   43
+//   4096 x 4096 x 4096   270  268  142  139
+//   16384 x 5120 x 2048  765  656  439  362
 mxfp8::WgradPlan wgrad_plan(int64_t M, int64_t N, int64_t K) {
-  const int64_t steps = (M + mxfp8::kWgStep - 1) / mxfp8::kWgStep;
+  const int64_t steps = std::max<int64_t>(1, (M + mxfp8::kWgStep - 1) / mxfp8::kWgStep);
   const int force = g_force_wgrad.load(std::memory_order_relaxed);
-  auto small = [&](int s) {
-    return mxfp8::WgradPlan{128, s, 0, (N + 127) / 128, (K + 127) / 128, steps, 1};
-  };
-  mxfp8::WgradPlan best = small(1);
-  if (steps == 0) return best;
+  mxfp8::WgradPlan best = {};
   double best_us = 1e30;
-  const int64_t tiles = best.tiles();
-  for (int s = 1; force != 256 && s <= 8 && (s == 1 || steps / s >= 2); s *= 2) {
-    const double rounds = (double)((tiles * s + kRuns - 1) / kRuns);
-    const double us = 8.0 + rounds * (2.0 + 0.9 * (double)((steps + s - 1) / s)) +
-                      (s > 1 ? 3.0 + (double)s * (double)N * (double)K * 8.0 / 4e6 : 0.0);
-    if (us < best_us) {
+  for (int tile : {128, 256}) {
+    if (M == 0 ? tile != 128 : force && force != tile) continue;   // without tokens the small form writes the zeros
+    const int64_t tn = (N + tile - 1) / tile, tk = (K + tile - 1) / tile, tiles = tn * tk, units = tiles * steps;
+    auto offer = [&](mxfp8::Runs runs, int64_t pieces, double us) {
+      if (us >= best_us) return;
       best_us = us;
-      best = small(s);
+      best = {tile, runs, tn, tk, steps, pieces};
+    };
+    auto ceil_div = [](int64_t a, int64_t b) { return (double)((a + b - 1) / b); };
+    const bool small = tile == 128;
+    // Whole tiles, one run per compute unit at most.
+    const int64_t whole = std::min(kRuns, tiles);
+    const double per_step = small ? 1.0 : whole == kRuns ? 1.95 : 1.62, per_tile = small ? 3.3 : 23.0;
+    offer({tiles, (int)steps, (int)whole}, 1,
+          (small ? 5.0 : 0.0) + ceil_div(tiles, whole) * (per_tile + per_step * (double)steps));
+    // Equal runs, of two or eight steps at least.
+    for (int64_t r = std::min(kRuns, units / (small ? 2 : 8)); r >= 2; r /= 2) {
+      // a shared tile's pieces: its steps over the shortest run, and one more at either end
+      const int64_t pieces = steps / (units / r) + 2;
+      const double join = small ? 0.045 * (double)r + 0.12 * (double)pieces
+                                : 0.08 * (double)(r + tiles - std::gcd(r, tiles));
+      const double touched = ceil_div(tiles, r) + (!small && tiles > r ? 1.0 : 0.0);
+      offer({units, 1, (int)r}, pieces,
+            (small ? 5.0 + 3.3 * touched : 18.0 * touched) + (small ? 1.0 : 2.0) * ceil_div(units, r) + join);
     }
   }
-  if (force == 128) return best;
-  // Large tiles: one run per compute unit, of eight steps at least; as many
-  // runs as tiles where that leaves few units idle, for then no tile is shared.
-  const int64_t bn = (N + 255) / 256, bk = (K + 255) / 256, big = bn * bk;
-  int64_t runs = std::min(kRuns, std::max<int64_t>(1, big * steps / 8));
-  if (big <= kRuns && big * 8 >= kRuns * 7) runs = big;
-  const double us = 10.0 + 12.0 * (double)((big + runs - 1) / runs) + 1.8 * (double)((big * steps + runs - 1) / runs) +
-                    (big % runs != 0 ? 4.0 + 0.12 * (double)runs : 0.0);
-  // A shared tile's pieces: its steps over the shortest run, and one more at either end.
-  const int64_t pieces = big % runs != 0 ? steps / (big * steps / runs) + 2 : 1;
-  if (force == 256 || us < best_us) best = {256, 1, (int)runs, bn, bk, steps, pieces};
   return best;
 }
 
 // fp32 partials of dW, then of db.
-size_t wgrad_dw_bytes(int64_t N, int64_t K, const mxfp8::WgradPlan& p) {
-  if (p.tile == 256) return p.shared() ? (size_t)p.runs * 2 * mxfp8::kWgradTileFloats * 4 : 0;
-  return p.splits > 1 ? (size_t)p.splits * (size_t)N * (size_t)K * 4 : 0;
+size_t wgrad_dw_bytes(const mxfp8::WgradPlan& p) {
+  return p.shared() ? (size_t)p.runs.count * 2 * p.tile * p.tile * 4 : 0;
 }
-size_t wgrad_db_bytes(int64_t N, const mxfp8::WgradPlan& p) {
-  if (p.tile == 256) return (size_t)p.tiles() * (size_t)p.pieces * 256 * 4;
-  return (size_t)p.splits * (size_t)p.tiles_k * (size_t)N * 4;
-}
+size_t wgrad_db_bytes(const mxfp8::WgradPlan& p) { return (size_t)p.tiles() * (size_t)p.pieces * p.tile * 4; }
 
 size_t part_bytes(int64_t M, int64_t N, mxfp8::B128Plan p) {
   return p.splits > 1 ? round_up((size_t)p.splits * (size_t)M * (size_t)((N + 3) / 4 * 4) * 4, 256) : 0;
@@ -359,7 +360,7 @@ int mxfp8_linear_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* 
   if (!bytes) return MXFP8_E_NULLPTR;
   if (M < 0 || M > kMaxRows || !rows_ok(N) || N % 8 != 0 || !summed_ok(K)) return MXFP8_E_SHAPE;
   const mxfp8::WgradPlan p = wgrad_plan(M, N, K);
-  *bytes = round_up(wgrad_dw_bytes(N, K, p), 256) + round_up(wgrad_db_bytes(N, p), 256);
+  *bytes = round_up(wgrad_dw_bytes(p), 256) + round_up(wgrad_db_bytes(p), 256);
   return MXFP8_OK;
 }
 
@@ -382,7 +383,8 @@ int mxfp8_linear_wgrad(const void* dy_bf16, int64_t M, int64_t N, int64_t lddy, 
   if (!aligned(dw, 16) || !aligned(db, db_dtype == MXFP8_F32 ? 4 : 2)) return MXFP8_E_ALIGN;
   if (M > 0 && (!aligned(dy_bf16, 16) || !aligned(q_packed, 256) || !aligned(s_packed, 256))) return MXFP8_E_ALIGN;
   const mxfp8::WgradPlan p = wgrad_plan(M, N, K);
-  if (b128_blocks(N) * b128_blocks(K) * p.splits > INT32_MAX || N * (K / 4) / 256 >= INT32_MAX - N)
+  // the join's grid, and a run's units in 32 bits
+  if (b128_blocks(N) * b128_blocks(K) > INT32_MAX / 64 || p.tiles() * p.steps / p.runs.count >= INT32_MAX)
     return MXFP8_E_SHAPE;
   size_t need = 0;
   mxfp8_linear_wgrad_workspace_bytes(M, N, K, &need);
@@ -404,7 +406,7 @@ int mxfp8_linear_wgrad(const void* dy_bf16, int64_t M, int64_t N, int64_t lddy, 
   a.db = db;
   a.db_bf16 = db_dtype == MXFP8_BF16;
   a.part_dw = (float*)workspace;
-  a.part_db = (float*)((uint8_t*)workspace + round_up(wgrad_dw_bytes(N, K, p), 256));
+  a.part_db = (float*)((uint8_t*)workspace + round_up(wgrad_dw_bytes(p), 256));
   return mxfp8::launch_wgrad(a, p, (hipStream_t)stream);
 }
 

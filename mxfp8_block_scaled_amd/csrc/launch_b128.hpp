@@ -47,18 +47,26 @@ int launch_gemm_b128_tile(const void* qp, const void* sp, int64_t M, int64_t K, 
 
 // Weight gradient dW[n, k] = sum_m dY[m, n] X[m, k] from packed 8-bit
 // activations (either scale block), and db[n] = sum_m dY[m, n].
+// The (tile, 64-token step) units, tile by tile, are cut into one run of
+// consecutive units per workgroup, at multiples of `granule` units (one unit,
+// or a tile's steps where no tile is shared).
+struct Runs {
+  int64_t granules;
+  int granule;
+  int count;
+  __host__ __device__ int64_t start(int64_t w) const { return granules * w / count * granule; }
+  __host__ __device__ int of(int64_t unit) const { return (int)(((unit / granule + 1) * count - 1) / granules); }
+};
 struct WgradPlan {
-  int tile;          // edge of a workgroup's dW tile: 128 or 256
-  int splits;        // tile 128: runs of 64-token steps each tile's tokens are cut into
-  int runs;          // tile 256: workgroups, one equal run of the (tile, step) units each
+  int tile;          // edge of a dW tile: 128 or 256
+  Runs runs;
   int64_t tiles_n, tiles_k;
-  int64_t steps;     // 64-token steps
-  int64_t pieces;    // tile 256: most runs that share a tile (1: none is shared)
+  int64_t steps;     // 64-token steps, at least one
+  int64_t pieces;    // most runs that share a tile (1: none is shared)
   int64_t tiles() const { return tiles_n * tiles_k; }
   bool shared() const { return pieces > 1; }
 };
-constexpr int kWgStep = 64;                        // tokens per step
-constexpr int64_t kWgradTileFloats = 256 * 256;    // a large tile's partial in the workspace
+constexpr int kWgStep = 64;   // tokens per step
 struct WgradArgs {
   const void* dy;       // bf16 [M, N], row stride lddy
   int64_t M, N, lddy;
@@ -75,8 +83,8 @@ struct WgradArgs {
   float* part_db;
 };
 int launch_wgrad(const WgradArgs& a, WgradPlan p, hipStream_t stream);
-// Its small-tile form (wgrad_small.hip).
-int launch_wgrad_small(const WgradArgs& a, int splits, hipStream_t stream);
+// Its small-tile kernel (wgrad_small.hip), without the join.
+int launch_wgrad_small(const WgradArgs& a, const WgradPlan& p, hipStream_t stream);
 
 // Load-balance and z loss of a router (balance.hip).
 struct BalanceArgs {

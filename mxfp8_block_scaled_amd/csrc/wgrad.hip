@@ -21,9 +21,12 @@
 //
 // db takes the dY fragments as they come by: step s is added by the
 // workgroups with tile index s % tiles_k along k, so each does 1 / tiles_k.
-// Partial sums of tiles whose tokens several workgroups share, and of db, go
-// to the workspace and are added in a fixed order: results do not depend on
-// timing.
+// The (tile, 64-token step) units, tile by tile, are cut into one run per
+// workgroup, equal ones, so that the chip is full whatever the number of
+// tiles, or whole tiles.  A run holds at most two tiles it does not own whole,
+// its first and its last; their sums go to the workgroup's two slots of the
+// workspace in lane order, and wgrad_join adds a tile's pieces in token order,
+// and the partial sums of db: results do not depend on timing.
 //
 // This file: the large tiles; wgrad_small.hip: the small tiles.
 #include "wgrad.hpp"
@@ -35,11 +38,6 @@ using namespace wgrad;
 // ---------------------------------------------------------------------------
 // Large tiles: 256 x 256 of dW per workgroup, four waves 2 x 2, each 128 x 128
 // (64 MFMAs per 32 tokens and wave, accumulators in the 256 AGPRs).
-//  * The (tile, step) units, tile by tile, are cut into one equal run per
-//    workgroup, so the chip is full whatever the number of tiles.  A run
-//    holds at most two tiles it does not own whole, its first and its last;
-//    their sums go to the workgroup's two slots of the workspace in lane
-//    order, and wgrad_join adds a tile's pieces in token order.
 //  * A step has two 32-token halves with a fragment set each.  During half 0
 //    the fragments of half 1 are read; then everything in flight has landed,
 //    the step's one barrier, and during half 1 the next step's first
@@ -54,25 +52,20 @@ constexpr int kBigPitch = kBigT * 2;
 constexpr int kBigOp = kWgStep * kBigPitch;        // 32 KiB: one operand's stage
 constexpr int kBigLds = 4 * kBigOp;                // dY x 2, X x 2
 
-// Runs: workgroup w of G takes units [U w / G, U (w + 1) / G) of U.
-__host__ __device__ inline int64_t run_start(int64_t U, int G, int64_t w) { return U * w / G; }
-__host__ __device__ inline int run_of(int64_t U, int G, int64_t unit) { return (int)(((unit + 1) * G - 1) / U); }
-
 }  // namespace
 
 template <bool kBias>
 __global__ __launch_bounds__(kWgThreads, 1) void wgrad_big_kernel(
     const uint16_t* __restrict__ dy, int64_t M, int N, int64_t lddy, const uint8_t* __restrict__ qp,
-    const uint8_t* __restrict__ sp, int K, int KS, int tiles_k, int tiles, int steps, void* __restrict__ dw,
+    const uint8_t* __restrict__ sp, int K, int KS, int tiles_k, int steps, Runs runs, void* __restrict__ dw,
     int64_t lddw, int out_bf16, int accumulate, float* __restrict__ part, float* __restrict__ part_db, int pieces) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wk = wave & 1, wn = wave >> 1;
   const int i = lane & 15, g = lane >> 4;
-  const int G = (int)gridDim.x, w = (int)blockIdx.x;
-  const int64_t U = (int64_t)tiles * steps;
-  const int64_t u0 = run_start(U, G, w), u1 = run_start(U, G, w + 1);
+  const int w = (int)blockIdx.x;
+  const int64_t u0 = runs.start(w), u1 = runs.start(w + 1);
 
   // Fragment addresses (see wgrad_kernel): the swizzle is the lane's own, so
   // buffer, half and row offset are immediates.
@@ -265,7 +258,7 @@ __global__ __launch_bounds__(kWgThreads, 1) void wgrad_big_kernel(
       }
     } else {
       // slot 0: the piece at the start of the run, 1: at its end
-      v4f* d = reinterpret_cast<v4f*>(part + ((size_t)w * 2 + (u == u0 ? 0 : 1)) * kWgradTileFloats);
+      v4f* d = reinterpret_cast<v4f*>(part + ((size_t)w * 2 + (u == u0 ? 0 : 1)) * (kBigT * kBigT));
       d += wave * 4096 + lane;
 #pragma unroll
       for (int a = 0; a < 8; ++a)
@@ -273,7 +266,7 @@ __global__ __launch_bounds__(kWgThreads, 1) void wgrad_big_kernel(
         for (int b = 0; b < 8; ++b) d[(a * 8 + b) * 64] = acc[a][b];
     }
     if constexpr (kBias) {
-      const int piece = w - run_of(U, G, (int64_t)t * steps);
+      const int piece = w - runs.of((int64_t)t * steps);
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         float v = accb[b];
@@ -287,26 +280,32 @@ __global__ __launch_bounds__(kWgThreads, 1) void wgrad_big_kernel(
   tile::wait_vmcnt<0>();   // no copy may land after the workgroup's LDS is given away
 }
 
-// Joins the large tiles that several runs share, in token order (grid: 16
-// workgroups per tile; those of whole tiles leave), and the parts of db (the
-// last workgroups, sixteen columns each): over the tiles of a column of tiles and their pieces.
-__global__ __launch_bounds__(256) void wgrad_join_kernel(const float* __restrict__ part, int64_t U, int G, int tiles,
+// Joins the tiles that several runs share, in token order (grid: kSub
+// workgroups, of 256 sums of four, per tile, or per border between two runs if
+// those are fewer; the ones without work leave), and the parts of db (the last
+// workgroups, sixteen columns each): over the tiles of a column of tiles and
+// their pieces.
+template <int kT>
+__global__ __launch_bounds__(256) void wgrad_join_kernel(const float* __restrict__ part, Runs runs, int parts, int by_border,
                                                          int tiles_k, int steps, int N, int K, void* __restrict__ dw,
                                                          int64_t lddw, int out_bf16, int accumulate,
                                                          const float* __restrict__ part_db, int pieces,
                                                          void* __restrict__ db, int db_bf16) {
+  constexpr int kF = kT / 32;                // fragments per wave and axis
+  constexpr int kSub = kT * kT / 1024;       // workgroups per tile
   const int tid = threadIdx.x;
-  if ((int)blockIdx.x >= tiles * 16) {
+  if ((int)blockIdx.x >= parts * kSub) {
     // sixteen columns: thread (q, c) adds the tiles q, q + 16, ... along k
     __shared__ float red[16][17];
     const int c = tid & 15, q = tid >> 4;
-    const int n = ((int)blockIdx.x - tiles * 16) * 16 + c, tn = n / kBigT;
+    const int n = ((int)blockIdx.x - parts * kSub) * 16 + c, tn = n / kT;
     float v = 0.0f;
     if (n < N) {
       for (int tk = q; tk < tiles_k; tk += 16) {
         const int t = tn * tiles_k + tk;
-        const int np = run_of(U, G, (int64_t)(t + 1) * steps - 1) - run_of(U, G, (int64_t)t * steps) + 1;
-        for (int p = 0; p < np; ++p) v += part_db[((size_t)t * pieces + p) * kBigT + n % kBigT];
+        int np = 1;
+        if (pieces > 1) np = runs.of((int64_t)(t + 1) * steps - 1) - runs.of((int64_t)t * steps) + 1;
+        for (int p = 0; p < np; ++p) v += part_db[((size_t)t * pieces + p) * kT + n % kT];
       }
     }
     red[q][c] = v;
@@ -318,54 +317,76 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(const float* __restrict
     store_db(db, db_bf16, accumulate, n, v);
     return;
   }
-  const int t = (int)blockIdx.x >> 4, sub = (int)blockIdx.x & 15;
-  const int w0 = run_of(U, G, (int64_t)t * steps), w1 = run_of(U, G, (int64_t)(t + 1) * steps - 1);
+  int t = (int)blockIdx.x / kSub;
+  const int sub = (int)blockIdx.x % kSub;
+  if (by_border) {   // the tile this border cuts, if it is the tile's first
+    const int64_t u = runs.start(t + 1), before = runs.start(t);
+    t = (int)(u / steps);
+    if (u == (int64_t)t * steps || before > (int64_t)t * steps) return;
+  }
+  const int w0 = runs.of((int64_t)t * steps), w1 = runs.of((int64_t)(t + 1) * steps - 1);
   if (w0 == w1) return;   // one run owns the tile (and stored it)
   const int tn = t / tiles_k, tk = t - tn * tiles_k;
-  for (int c = 0; c < 4; ++c) {
-    const int e = sub * 1024 + c * 256 + tid;   // v4f of the tile, lane order: wave, (a, b), lane
-    v4f v = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int w = w0; w <= w1; ++w) {
-      // a piece lies at the start of its run unless the run began in an earlier tile
-      const int slot = run_start(U, G, w) >= (int64_t)t * steps ? 0 : 1;
-      v += reinterpret_cast<const v4f*>(part + ((size_t)w * 2 + slot) * kWgradTileFloats)[e];
-    }
-    const int wave = e >> 12, ab = (e >> 6) & 63, lane = e & 63;
-    const int n = tn * kBigT + (wave >> 1) * 128 + (ab & 7) * 16 + (lane & 15);
-    const int k = tk * kBigT + (wave & 1) * 128 + (ab >> 3) * 16 + 4 * (lane >> 4);
-    if (n >= N || k >= K) continue;
-    if (out_bf16) {
-      *reinterpret_cast<uint2*>((uint16_t*)dw + (size_t)n * lddw + k) =
-          make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-    } else {
-      v4f* d = reinterpret_cast<v4f*>((float*)dw + (size_t)n * lddw + k);
-      *d = accumulate ? *d + v : v;
-    }
+  const int e = sub * 256 + tid;   // v4f of the tile, lane order: wave, (a, b), lane
+  // a piece lies at the start of its run unless the run began in an earlier tile
+  const v4f* p = reinterpret_cast<const v4f*>(part) + (size_t)w0 * 2 * (kT * kT / 4) + e;
+  v4f v = runs.start(w0) >= (int64_t)t * steps ? *p : p[kT * kT / 4];
+  // eight loads on their way at a time; added one after the other
+  for (int w = w0; w < w1;) {
+    const int m = min(8, w1 - w);
+    v4f x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = p[(size_t)min(j + 1, m) * 2 * (kT * kT / 4)];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < m) v += x[j];
+    w += m;
+    p += (size_t)m * 2 * (kT * kT / 4);
+  }
+  const int wave = e / (kF * kF * 64), ab = (e >> 6) & (kF * kF - 1), lane = e & 63;
+  const int n = tn * kT + (wave >> 1) * (kT / 2) + (ab % kF) * 16 + (lane & 15);
+  const int k = tk * kT + (wave & 1) * (kT / 2) + (ab / kF) * 16 + 4 * (lane >> 4);
+  if (n >= N || k >= K) return;
+  if (out_bf16) {
+    *reinterpret_cast<uint2*>((uint16_t*)dw + (size_t)n * lddw + k) =
+        make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  } else {
+    v4f* d = reinterpret_cast<v4f*>((float*)dw + (size_t)n * lddw + k);
+    *d = accumulate ? *d + v : v;
   }
 }
 
 namespace {
 template <bool kBias>
-int launch_big(const WgradArgs& a, WgradPlan p, hipStream_t stream) {
+int launch_big(const WgradArgs& a, const WgradPlan& p, hipStream_t stream) {
   static std::atomic<int> lds_set[kMaxDevices];
   if (!set_lds_limit_once((const void*)wgrad_big_kernel<kBias>, kBigLds, lds_set)) return -7;
-  hipLaunchKernelGGL(wgrad_big_kernel<kBias>, dim3((unsigned)p.runs), dim3(kWgThreads), kBigLds, stream,
+  hipLaunchKernelGGL(wgrad_big_kernel<kBias>, dim3((unsigned)p.runs.count), dim3(kWgThreads), kBigLds, stream,
                      (const uint16_t*)a.dy, a.M, (int)a.N, a.lddy, (const uint8_t*)a.qp, (const uint8_t*)a.sp,
-                     (int)a.K, (int)(2 * b128_blocks(a.K)), (int)p.tiles_k, (int)p.tiles(), (int)p.steps, a.dw, a.lddw,
+                     (int)a.K, (int)(2 * b128_blocks(a.K)), (int)p.tiles_k, (int)p.steps, p.runs, a.dw, a.lddw,
                      a.out_bf16, a.accumulate, a.part_dw, a.part_db, (int)p.pieces);
-  if (hipGetLastError() != hipSuccess) return -7;
-  if (!p.shared() && !kBias) return 0;
-  const int join = p.shared() ? (int)p.tiles() : 0, cols = kBias ? (int)((a.N + 15) / 16) : 0;
-  hipLaunchKernelGGL(wgrad_join_kernel, dim3((unsigned)(join * 16 + cols)), dim3(256), 0, stream, a.part_dw,
-                     p.tiles() * p.steps, p.runs, join, (int)p.tiles_k, (int)p.steps, (int)a.N, (int)a.K, a.dw,
-                     a.lddw, a.out_bf16, a.accumulate, a.part_db, (int)p.pieces, a.db, a.db_bf16);
+  return hipGetLastError() == hipSuccess ? 0 : -7;
+}
+
+template <int kT>
+int launch_join(const WgradArgs& a, const WgradPlan& p, hipStream_t stream) {
+  const int borders = p.runs.count - 1, by_border = borders < p.tiles();
+  const int join = !p.shared() ? 0 : by_border ? borders : (int)p.tiles(), cols = a.db ? (int)((a.N + 15) / 16) : 0;
+  if (join + cols == 0) return 0;
+  hipLaunchKernelGGL(wgrad_join_kernel<kT>, dim3((unsigned)(join * (kT * kT / 1024) + cols)), dim3(256), 0, stream,
+                     a.part_dw, p.runs, join, by_border, (int)p.tiles_k, (int)p.steps, (int)a.N, (int)a.K, a.dw, a.lddw,
+                     a.out_bf16, a.accumulate, a.part_db, (int)p.pieces, a.db, a.db_bf16);
   return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 }  // namespace
 
 int launch_wgrad(const WgradArgs& a, WgradPlan p, hipStream_t stream) {
-  if (p.tile == 128) return launch_wgrad_small(a, p.splits, stream);
-  return a.db != nullptr ? launch_big<true>(a, p, stream) : launch_big<false>(a, p, stream);
+  if (p.tile == 128) {
+    if (int st = launch_wgrad_small(a, p, stream)) return st;
+    return launch_join<128>(a, p, stream);
+  }
+  if (int st = a.db != nullptr ? launch_big<true>(a, p, stream) : launch_big<false>(a, p, stream)) return st;
+  return launch_join<256>(a, p, stream);
 }
 
 }  // namespace mxfp8

@@ -1,5 +1,5 @@
 // The small-tile form of the weight gradient (see wgrad.hip for the
-// mathematics and the LDS layout they share), and the join of its split runs.
+// mathematics, the LDS layout and the runs, which both forms share).
 #include "wgrad.hpp"
 
 namespace mxfp8 {
@@ -25,18 +25,21 @@ static_assert(WgLds::kBytes <= 160 * 1024, "LDS of a compute unit");
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// Small tiles: 128 x 128 of dW per workgroup, four waves 2 x 2, each 64 x 64,
-// for the problems whose large tiles would leave the chip empty.  There a
-// step's time is the latency of its loads, so everything comes by copies into
-// LDS, three steps ahead.  Every wave widens the sixteen token rows of X that
-// it copied itself, one step ahead of their MFMAs, into one of two buffers:
-// one barrier per step.
+// Small tiles: 128 x 128 of dW, four waves 2 x 2, each 64 x 64, for the
+// problems whose large tiles would leave the chip empty or idle at the end.
+// There a step's time is the latency of its loads, so everything comes by
+// copies into LDS, three steps ahead.  Every wave widens the sixteen token
+// rows of X that it copied itself, one step ahead of their MFMAs, into one of
+// two buffers: one barrier per step.  A workgroup goes through its run of
+// (tile, step) units without a stop: copies and fragments of the next tile are
+// on their way while a tile is stored (one tile per launched workgroup: 72 us
+// instead of 41 at 67 x 7640 x 5888).
 // ---------------------------------------------------------------------------
 template <bool kBias>
 __global__ __launch_bounds__(kWgThreads, 1) void wgrad_kernel(
     const uint16_t* __restrict__ dy, int64_t M, int N, int64_t lddy, const uint8_t* __restrict__ qp,
-    const uint8_t* __restrict__ sp, int K, int KS, int tiles_n, int tiles_k, int splits, void* __restrict__ out,
-    int64_t ldo, int64_t split_stride, int out_bf16, int accumulate, float* __restrict__ part_db) {
+    const uint8_t* __restrict__ sp, int K, int KS, int tiles_k, int steps, Runs runs, void* __restrict__ dw,
+    int64_t lddw, int out_bf16, int accumulate, float* __restrict__ part, float* __restrict__ part_db, int pieces) {
   using L = WgLds;
   constexpr int kF = 4;             // 16-wide fragments per wave and axis
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -44,14 +47,11 @@ __global__ __launch_bounds__(kWgThreads, 1) void wgrad_kernel(
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wk = wave & 1, wn = wave >> 1;
   const int i = lane & 15, g = lane >> 4;
-  const int item = xcd_remap((int)blockIdx.x, (int)gridDim.x);
-  const int split = item % splits, t = item / splits;
-  const int tn = t / tiles_k, tk = t - tn * tiles_k;
-  const int n0 = tn * L::kT, k0 = tk * L::kT;
-  const int64_t steps = (M + kWgStep - 1) / kWgStep;
-  const int64_t s0 = steps * split / splits, s1 = steps * (split + 1) / splits;
-  const int ks0 = k0 / kStepK;
-  const uint32_t gbytes = (uint32_t)KS * kTileBytes, sbytes = (uint32_t)KS * kTileScaleBytes;
+  const int w = xcd_remap((int)blockIdx.x, (int)gridDim.x);
+  const int64_t u0 = runs.start(w);
+  const int n_units = (int)(runs.start(w + 1) - u0);
+  // no tokens: one step whose reads all lie past the ends of their resources
+  const uint32_t gbytes = M > 0 ? (uint32_t)KS * kTileBytes : 0, sbytes = M > 0 ? (uint32_t)KS * kTileScaleBytes : 0;
 
   // dY: lane l of a copy takes LDS bytes [16 l, 16 l + 16) of its KiB (four
   // token rows of 256 bytes), i.e. half h of slot c of row m, which holds
@@ -61,24 +61,24 @@ __global__ __launch_bounds__(kWgThreads, 1) void wgrad_kernel(
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     const int m = (wave * 4 + c) * 4 + (lane >> 4), p = lane & 15;
-    vy[c] = (uint32_t)((int64_t)m * lddy + n0 + ((p >> 1) ^ slot_xor(m)) * 16 + (p & 1) * 8) * 2u;
+    vy[c] = (uint32_t)((int64_t)m * lddy + ((p >> 1) ^ slot_xor(m)) * 16 + (p & 1) * 8) * 2u;
   }
   auto stage = [&](int b) { return smem + b * L::kStage; };
   auto widened = [&](int b) { return smem + L::kDepth * L::kStage + b * L::kX; };
-  // The copies of the next step to be copied, step by step; past the run's
-  // end those of its last step again (never used), so the waits need no other
+  const int t0 = (int)(u0 / steps), sa0 = (int)(u0 - (int64_t)t0 * steps);
+  // The copies of the next unit to be copied, unit by unit; past the run's
+  // end those of its last unit again (never used), so the waits need no other
   // counts.  (Addresses advance: at one wave per SIMD every scalar
   // instruction counts.)
-  const uint16_t* yp = dy + s0 * kWgStep * lddy;
-  int64_t left = s1 - s0, rows = M - s0 * kWgStep;       // steps and token rows from here
-  int half = (int)(s0 & 1);
-  const uint8_t* xp = qp + (size_t)(s0 >> 1) * gbytes;
-  const uint8_t* scp = sp + (size_t)(s0 >> 1) * sbytes;
-  const uint32_t ybytes = (uint32_t)((63 * lddy + N) * 2);
+  int left = n_units, cs = sa0, ctn = t0 / tiles_k, ctk = t0 - ctn * tiles_k;
+  const uint16_t* yp = dy + cs * kWgStep * lddy + ctn * L::kT;
+  int64_t rows = M - (int64_t)cs * kWgStep;              // token rows from this step on
+  const uint8_t* xp = qp + (size_t)(cs >> 1) * gbytes;
+  const uint8_t* scp = sp + (size_t)(cs >> 1) * sbytes;
   const uint32_t vx0 = (uint32_t)wave * KS * kPieceBytes + (uint32_t)lane * 16u, vx1 = vx0 + 4u * KS * kPieceBytes;
   auto issue = [&](uint8_t* st) {
-    const uint32_t yb = rows >= kWgStep ? ybytes : (uint32_t)((((int)rows - 1) * (int)lddy + N) * 2);
-    const tile::i4v ry = tile::buffer_rsrc(yp, yb);
+    const int r = rows >= kWgStep ? kWgStep : (int)rows;
+    const tile::i4v ry = tile::buffer_rsrc(yp, r > 0 ? (uint32_t)((r - 1) * (int)lddy + N - ctn * L::kT) * 2u : 0u);
     const tile::i4v rx = tile::buffer_rsrc(xp, gbytes);
     const tile::i4v rs = tile::buffer_rsrc(scp, sbytes);
 #pragma unroll
@@ -86,24 +86,36 @@ __global__ __launch_bounds__(kWgThreads, 1) void wgrad_kernel(
     // pieces past K read other columns' data or, past the group, zeros
 #pragma unroll
     for (int v = 0; v < 2; ++v)
-      tile::b2l_16(half ? vx1 : vx0, rx, (uint32_t)(ks0 + v) * kPieceBytes, st + L::kY + (v * 4 + wave) * 1024);
+      tile::b2l_16((cs & 1) ? vx1 : vx0, rx, (uint32_t)(2 * ctk + v) * kPieceBytes,
+                   st + L::kY + (v * 4 + wave) * 1024);
 #pragma unroll
     for (int v = 0; v < 2; ++v)
-      tile::b2l_4((uint32_t)lane * 4u, rs, (uint32_t)(ks0 + v) * kTileScaleBytes,
+      tile::b2l_4((uint32_t)lane * 4u, rs, (uint32_t)(2 * ctk + v) * kTileScaleBytes,
                   st + L::kY + L::kRaw + wave * 512 + v * 256);
     if (left > 1) {
       --left;
-      yp += kWgStep * lddy;
-      rows -= kWgStep;
-      xp += half ? gbytes : 0;
-      scp += half ? sbytes : 0;
-      half ^= 1;
+      if (++cs < steps) {
+        yp += kWgStep * lddy;
+        rows -= kWgStep;
+        xp += (cs & 1) ? 0 : gbytes;
+        scp += (cs & 1) ? 0 : sbytes;
+      } else {
+        cs = 0;
+        if (++ctk == tiles_k) {
+          ctk = 0;
+          ++ctn;
+        }
+        yp = dy + ctn * L::kT;
+        rows = M;
+        xp = qp;
+        scp = sp;
+      }
     }
   };
   // Widening: the thread's two chunks are in token row m = 16 wave + lane / 4.
   const int xm = 16 * wave + (lane >> 2), xc = (lane & 3) ^ swz(lane >> 2);
-  auto widen = [&](int64_t s, const uint8_t* st, uint8_t* to) {
-    const int half = (int)(s & 1);
+  auto widen = [&](int s, const uint8_t* st, uint8_t* to) {
+    const int half = s & 1;
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
       const uint4 q = *reinterpret_cast<const uint4*>(st + L::kY + (v * 4 + wave) * 1024 + lane * 16);
@@ -130,57 +142,63 @@ __global__ __launch_bounds__(kWgThreads, 1) void wgrad_kernel(
 
   v4f acc[kF][kF];
   v4f accb[kF];
+  auto clear = [&] {
 #pragma unroll
-  for (int a = 0; a < kF; ++a) {
-    accb[a] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int a = 0; a < kF; ++a) {
+      accb[a] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int b = 0; b < kF; ++b) acc[a][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  }
+      for (int b = 0; b < kF; ++b) acc[a][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+  };
+  clear();
   bf16x8 ones;
 #pragma unroll
   for (int e = 0; e < 8; ++e) ones[e] = (__bf16)1.0f;
 
   bf16x8 ax[kF], ay[kF], bx[kF], by[kF];   // fragments of half 0 and of half 1
-  if (s0 < s1) {
 #pragma unroll
-    for (int d = 0; d < L::kDepth - 1; ++d) issue(stage(d));
-    tile::wait_vmcnt<(L::kDepth - 2) * L::kCopies>();
-    widen(s0, stage(0), widened(0));
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
+  for (int d = 0; d < L::kDepth - 1; ++d) issue(stage(d));
+  tile::wait_vmcnt<(L::kDepth - 2) * L::kCopies>();
+  widen(sa0, stage(0), widened(0));
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
 #pragma unroll
-    for (int a = 0; a < kF; ++a) {
-      ax[a] = frag(widened(0), wk * kF + a, 0);
-      ay[a] = frag(stage(0), wn * kF + a, 0);
-    }
+  for (int a = 0; a < kF; ++a) {
+    ax[a] = frag(widened(0), wk * kF + a, 0);
+    ay[a] = frag(stage(0), wn * kF + a, 0);
   }
-  int phase = (int)(s0 % tiles_k), at = 0;
-  for (int64_t s = s0; s < s1; ++s) {
+  int t = t0, tn = t0 / tiles_k, tk = t0 - tn * tiles_k;
+  int s = sa0, sa = sa0, phase = sa0 % tiles_k, at = 0;
+  int stored = 0;   // bit 0 / 1: the last unit / the one before it ended with kF * kF stores at least
+  for (int r = 0; r < n_units; ++r) {
     const int next = at + 1 == L::kDepth ? 0 : at + 1, last = at == 0 ? L::kDepth - 1 : at - 1;
-    const int par = (int)(s - s0) & 1;
+    const int par = r & 1, sn = s + 1 == steps ? 0 : s + 1;
     const uint8_t *const y = stage(at), *const x = widened(par);
     const uint8_t *const yn = stage(next), *const xn = widened(par ^ 1);
     const bool with_bias = kBias && wk == 0 && phase == tk;
     phase = phase + 1 == tiles_k ? 0 : phase + 1;
     // Half 0, with the reads of half 1 and the widening of the next step (this
-    // wave's copies of it have landed).  The empty asm statements keep the
-    // MFMAs in their places.
-    tile::wait_vmcnt<(L::kDepth - 3) * L::kCopies>();
+    // wave's copies of it have landed: only the copies of the step after it
+    // and stores issued since are in flight).  The empty asm statements keep
+    // the MFMAs in their places.
+    if (stored == 0) tile::wait_vmcnt<(L::kDepth - 3) * L::kCopies>();
+    else if (stored == 3) tile::wait_vmcnt<(L::kDepth - 3) * L::kCopies + 2 * kF * kF>();
+    else tile::wait_vmcnt<(L::kDepth - 3) * L::kCopies + kF * kF>();
     tile::static_for<0, 16>([&](auto J) {
       constexpr int j = decltype(J)::value, a = j >> 2, c = j & 3;
       acc[a][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ax[a], ay[c], acc[a][c], 0, 0, 0);
       asm volatile("" : "+v"(acc[a][c]));
       if constexpr (j < 4) by[j] = frag(y, wn * kF + j, 1);
       else if constexpr (j < 8) bx[j - 4] = frag(x, wk * kF + j - 4, 1);
-      if constexpr (j == 8) widen(s + 1, yn, widened(par ^ 1));   // (at the run's end: a copy of the last step)
+      if constexpr (j == 8) widen(sn, yn, widened(par ^ 1));   // (at the run's end: a copy of the last unit)
       __builtin_amdgcn_sched_barrier(0);
     });
     if (with_bias) {
 #pragma unroll
       for (int b = 0; b < kF; ++b) accb[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, ay[b], accb[b], 0, 0, 0);
     }
-    // Past this barrier step s + 1 has landed and is widened for all waves,
-    // and nobody reads step s from LDS any more.
+    // Past this barrier the next unit has landed and is widened for all waves,
+    // and nobody reads the last one from LDS any more.
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     issue(stage(last));
@@ -197,101 +215,78 @@ __global__ __launch_bounds__(kWgThreads, 1) void wgrad_kernel(
       for (int b = 0; b < kF; ++b) accb[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, by[b], accb[b], 0, 0, 0);
     }
     at = next;
-  }
-  tile::wait_vmcnt<0>();   // no copy may land after the workgroup's LDS is given away
-
-  // Lane (i, g) holds D[k = 16 a + 4 g + j][n = 16 b + i] of its wave's tile.
-  float* of = (float*)out + (size_t)split * split_stride;
+    stored = (stored << 1) & 2;
+    if (sn == 0 || r + 1 == n_units) {
+      // Lane (i, g) holds D[k = 64 wk + 16 a + 4 g + j][n = 64 wn + 16 b + i].
+      const int n0 = tn * L::kT, k0 = tk * L::kT;
+      if (sa == 0 && sn == 0) {
 #pragma unroll
-  for (int b = 0; b < kF; ++b) {
-    const int n = n0 + (wn * kF + b) * 16 + i;
-    if (n >= N) continue;
+        for (int b = 0; b < kF; ++b) {
+          const int n = n0 + (wn * kF + b) * 16 + i;
+          if (n >= N) continue;
 #pragma unroll
-    for (int a = 0; a < kF; ++a) {
-      const int k = k0 + (wk * kF + a) * 16 + 4 * g;
-      if (k >= K) continue;   // K % 16 == 0: a quad is all in or all out
-      if (out_bf16) {
-        *reinterpret_cast<uint2*>((uint16_t*)out + (size_t)n * ldo + k) =
-            make_uint2(pack_bf16x2(acc[a][b][0], acc[a][b][1]), pack_bf16x2(acc[a][b][2], acc[a][b][3]));
+          for (int a = 0; a < kF; ++a) {
+            const int k = k0 + (wk * kF + a) * 16 + 4 * g;
+            if (k >= K) continue;   // K % 16 == 0: a quad is all in or all out
+            if (out_bf16) {
+              *reinterpret_cast<uint2*>((uint16_t*)dw + (size_t)n * lddw + k) =
+                  make_uint2(pack_bf16x2(acc[a][b][0], acc[a][b][1]), pack_bf16x2(acc[a][b][2], acc[a][b][3]));
+            } else {
+              v4f* d = reinterpret_cast<v4f*>((float*)dw + (size_t)n * lddw + k);
+              *d = accumulate ? *d + acc[a][b] : acc[a][b];
+            }
+          }
+        }
+        // at the matrix's edge a wave may have skipped some
+        if (n0 + L::kT <= N && k0 + L::kT <= K) stored |= 1;
       } else {
-        v4f* d = reinterpret_cast<v4f*>(of + (size_t)n * ldo + k);
-        *d = accumulate ? *d + acc[a][b] : acc[a][b];
+        // slot 0: the piece at the start of the run, 1: at its end
+        v4f* d = reinterpret_cast<v4f*>(part + ((size_t)w * 2 + (t == t0 ? 0 : 1)) * (L::kT * L::kT));
+        d += wave * 1024 + lane;
+#pragma unroll
+        for (int a = 0; a < kF; ++a)
+#pragma unroll
+          for (int b = 0; b < kF; ++b) d[(a * kF + b) * 64] = acc[a][b];
+        stored |= 1;
+      }
+      // every row of the ones product holds the column sums
+      if (kBias && wk == 0 && g == 0) {
+        const int piece = w - runs.of((int64_t)t * steps);
+#pragma unroll
+        for (int b = 0; b < kF; ++b)
+          part_db[((size_t)t * pieces + piece) * L::kT + (wn * kF + b) * 16 + i] = accb[b][0];
+      }
+      clear();
+      ++t;
+      sa = 0;
+      phase = 0;
+      if (++tk == tiles_k) {
+        tk = 0;
+        ++tn;
       }
     }
-    // every row of the ones product holds the column sums
-    if (kBias && wk == 0 && g == 0) part_db[((size_t)split * tiles_k + tk) * N + n] = accb[b][0];
+    s = sn;
   }
-}
-
-// dw = sum of the split partials in order (+ dw): one thread per 4 k.  db =
-// sum of its partials: the last workgroups, sixteen columns each, thread
-// (q, c) parts q, q + 16, ... of column c, then the sixteen sums in order.
-__global__ __launch_bounds__(256) void wgrad_reduce_kernel(const float* __restrict__ part, int splits, int64_t N,
-                                                           int64_t K, void* __restrict__ dw, int64_t lddw,
-                                                           int out_bf16, int accumulate, int64_t quads,
-                                                           const float* __restrict__ part_db, int parts_db,
-                                                           void* __restrict__ db, int db_bf16) {
-  const int64_t dw_blocks = (quads + 255) / 256;
-  if ((int64_t)blockIdx.x >= dw_blocks) {
-    __shared__ float red[16][17];
-    const int c = threadIdx.x & 15, q = threadIdx.x >> 4;
-    const int64_t n = ((int64_t)blockIdx.x - dw_blocks) * 16 + c;
-    float v = 0.0f;
-    if (n < N)
-      for (int p = q; p < parts_db; p += 16) v += part_db[(size_t)p * N + n];
-    red[q][c] = v;
-    __syncthreads();
-    if (q != 0 || n >= N) return;
-    v = 0.0f;
-#pragma unroll
-    for (int p = 0; p < 16; ++p) v += red[p][c];
-    store_db(db, db_bf16, accumulate, n, v);
-    return;
-  }
-  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (t < quads) {
-    const int64_t per_row = K / 4, n = t / per_row, k = (t - n * per_row) * 4;
-    v4f a = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 0; s < splits; ++s) a += *reinterpret_cast<const v4f*>(part + ((size_t)s * N + n) * K + k);
-    if (out_bf16) {
-      *reinterpret_cast<uint2*>((uint16_t*)dw + (size_t)n * lddw + k) =
-          make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
-    } else {
-      v4f* d = reinterpret_cast<v4f*>((float*)dw + (size_t)n * lddw + k);
-      *d = accumulate ? *d + a : a;
-    }
-    return;
-  }
+  tile::wait_vmcnt<0>();   // no copy may land after the workgroup's LDS is given away
 }
 
 namespace {
 template <bool kBias>
-int launch_small(const WgradArgs& a, int splits, hipStream_t stream) {
+int launch_small(const WgradArgs& a, const WgradPlan& p, hipStream_t stream) {
   constexpr int lds = WgLds::kBytes;
   static std::atomic<int> lds_set[kMaxDevices];
   if (!set_lds_limit_once((const void*)wgrad_kernel<kBias>, lds, lds_set)) return -7;
-  const int tiles_n = (int)((a.N + 127) / 128), tiles_k = (int)((a.K + 127) / 128);
-  const bool direct = splits == 1;
-  hipLaunchKernelGGL((wgrad_kernel<kBias>), dim3((unsigned)(tiles_n * tiles_k * splits)), dim3(kWgThreads), lds,
-                     stream, (const uint16_t*)a.dy, a.M, (int)a.N, a.lddy, (const uint8_t*)a.qp,
-                     (const uint8_t*)a.sp, (int)a.K, (int)(2 * b128_blocks(a.K)), tiles_n, tiles_k, splits,
-                     direct ? a.dw : (void*)a.part_dw, direct ? a.lddw : a.K, a.N * a.K, direct ? a.out_bf16 : 0,
-                     direct ? a.accumulate : 0, a.part_db);
+  hipLaunchKernelGGL((wgrad_kernel<kBias>), dim3((unsigned)p.runs.count), dim3(kWgThreads), lds, stream,
+                     (const uint16_t*)a.dy, a.M, (int)a.N, a.lddy, (const uint8_t*)a.qp, (const uint8_t*)a.sp,
+                     (int)a.K, (int)(2 * b128_blocks(a.K)), (int)p.tiles_k, (int)p.steps, p.runs, a.dw, a.lddw,
+                     a.out_bf16, a.accumulate, a.part_dw, a.part_db, (int)p.pieces);
   return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 
 }  // namespace
 
-int launch_wgrad_small(const WgradArgs& a, int splits, hipStream_t stream) {
-  const bool bias = a.db != nullptr;
-  const int st = bias ? launch_small<true>(a, splits, stream) : launch_small<false>(a, splits, stream);
-  if (st || (splits == 1 && !bias)) return st;
-  const int64_t quads = splits > 1 ? a.N * (a.K / 4) : 0;
-  const int64_t blocks = (quads + 255) / 256 + (bias ? (a.N + 15) / 16 : 0);
-  const int parts_db = splits * (int)((a.K + 127) / 128);
-  hipLaunchKernelGGL(wgrad_reduce_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a.part_dw, splits, a.N, a.K,
-                     a.dw, a.lddw, a.out_bf16, a.accumulate, quads, a.part_db, parts_db, a.db, a.db_bf16);
-  return hipGetLastError() == hipSuccess ? 0 : -7;
+int launch_wgrad_small(const WgradArgs& a, const WgradPlan& p, hipStream_t stream) {
+  return a.db != nullptr ? launch_small<true>(a, p, stream) : launch_small<false>(a, p, stream);
 }
 
 }  // namespace mxfp8

@@ -158,42 +158,39 @@ int launch_wgrad(const WgradArgs& a, WgradPlan p, hipStream_t) {
   ++g_launches;
   const int64_t T = p.tile;
   CHECK(T == 128 || T == 256);
-  CHECK(p.tiles_n == (a.N + T - 1) / T && p.tiles_k == (a.K + T - 1) / T && p.steps == (a.M + 63) / 64);
+  CHECK(p.tiles_n == (a.N + T - 1) / T && p.tiles_k == (a.K + T - 1) / T);
+  CHECK(p.steps == std::max<int64_t>(1, (a.M + 63) / 64) && (a.M > 0 || T == 128));
   read_rows(a.dy, a.M, a.N, a.lddy, 2);
   if (a.M > 0) CHECK(holds(a.qp, packed(a.M, a.K), kAct) && holds(a.sp, packed(a.M, a.K) / 32, kActScale));
+  // Runs in order: they cover every unit once, each tile's pieces fit the
+  // count, and a run leaves partials of its first and its last tile at most.
+  const int64_t U = p.tiles() * p.steps;
+  const size_t slot_floats = (size_t)T * T;
   size_t dw_part = 0;
-  if (T == 128) {
-    if (p.splits > 1) dw_part = (size_t)p.splits * a.N * a.K * 4;
-    fill(a.part_dw, dw_part, kPart);
-    if (a.db) fill(a.part_db, (size_t)p.splits * p.tiles_k * a.N * 4, kPart + 1);
-  } else {
-    // Runs in order: each tile's pieces fit the count, and a run leaves
-    // partials of its first and its last tile at most.
-    const int64_t U = p.tiles() * p.steps;
-    auto start = [&](int64_t w) { return U * w / p.runs; };
-    std::vector<int64_t> pieces((size_t)p.tiles(), 0);
-    for (int64_t w = 0; w < p.runs; ++w) {
-      CHECK(start(w + 1) > start(w));
-      for (int64_t u = start(w); u < start(w + 1);) {
-        const int64_t t = u / p.steps, end = std::min(start(w + 1), (t + 1) * p.steps);
-        const bool whole = u == t * p.steps && end == (t + 1) * p.steps;
-        CHECK(p.shared() || whole);
-        if (!whole) {
-          const int slot = u == start(w) ? 0 : 1;
-          fill(a.part_dw + ((size_t)w * 2 + slot) * kWgradTileFloats, (size_t)kWgradTileFloats * 4, kPart);
-          dw_part = std::max(dw_part, ((size_t)w * 2 + slot + 1) * (size_t)kWgradTileFloats * 4);
-        }
-        ++pieces[(size_t)t];
-        u = end;
+  std::vector<int64_t> pieces((size_t)p.tiles(), 0);
+  CHECK(p.runs.count >= 1 && p.runs.count <= 256 && p.runs.start(0) == 0 && p.runs.start(p.runs.count) == U);
+  for (int64_t w = 0; w < p.runs.count; ++w) {
+    const int64_t u0 = p.runs.start(w), u1 = p.runs.start(w + 1);
+    CHECK(u1 > u0);
+    for (int64_t u = u0; u < u1;) {
+      const int64_t t = u / p.steps, end = std::min(u1, (t + 1) * p.steps);
+      const bool whole = u == t * p.steps && end == (t + 1) * p.steps;
+      CHECK(p.shared() || whole);
+      CHECK(whole || u == u0 || end == u1);
+      CHECK(p.runs.of(u) == w && p.runs.of(end - 1) == w);
+      CHECK(w - p.runs.of(t * p.steps) == pieces[(size_t)t]);
+      if (!whole) {
+        const size_t slot = (size_t)w * 2 + (u == u0 ? 0 : 1);
+        fill(a.part_dw + slot * slot_floats, slot_floats * 4, kPart);
+        dw_part = std::max(dw_part, (slot + 1) * slot_floats * 4);
       }
+      ++pieces[(size_t)t];
+      u = end;
     }
-    CHECK(*std::max_element(pieces.begin(), pieces.end()) <= p.pieces);
-    if (a.db) fill(a.part_db, (size_t)p.tiles() * p.pieces * 256 * 4, kPart + 1);
   }
-  if (dw_part) {
-    CHECK(((uint8_t*)a.part_dw)[0] == kPart || T == 256);
-    CHECK((uint8_t*)a.part_dw + dw_part <= (uint8_t*)a.part_db);
-  }
+  CHECK(*std::max_element(pieces.begin(), pieces.end()) <= p.pieces);
+  CHECK((uint8_t*)a.part_dw + dw_part <= (uint8_t*)a.part_db);
+  if (a.db) fill(a.part_db, (size_t)(p.tiles() * p.pieces * T) * 4, kPart + 1);
   fill_rows(a.dw, a.N, a.K, a.lddw, a.out_bf16 ? 2 : 4);
   if (a.db) fill(a.db, (size_t)a.N * (a.db_bf16 ? 2 : 4), 0x5A);
   return 0;

@@ -303,3 +303,37 @@ def test_step_calls_are_their_parts(M):
     assert torch.equal(y, api.gemm_packed(pa, pw, b))
     for p, q, r in zip(got, (api.linear(dy, pt), dw, db), again):
         assert torch.equal(p, q) and torch.equal(p, r)
+
+
+@pytest.mark.parametrize("M,N,K,form", [(70, 4104, 1040, "b128"), (30, 2600, 2064, "b128"), (130, 4224, 1024, "mx"),
+                                        (700, 1032, 4240, "b128")])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_wgrad_several_tiles_per_workgroup(M, N, K, form, dtype):
+    """More small tiles than compute units, of one to eleven steps: the copies
+    of a workgroup's next tiles run ahead while it stores one, at the edges of
+    the matrix too."""
+    x, dy = spiky(M, K, M + K), randn((M, N), N, 1e-3)
+    pa = keep(x, form)
+    X = f64(pa.dequantize())
+    base, base_b = torch.randn(N, K), torch.randn(N)
+    prev = api.mxfp8_debug_force_wgrad(128)
+    try:
+        dw, db = api.linear_wgrad(dy.to(dev()), pa, dtype=dtype, bias_grad=True)
+        again = api.linear_wgrad(dy.to(dev()), pa, dtype=dtype)
+        acc = api.linear_wgrad(dy.to(dev()), pa, bias_grad=True, out=base.to(dev()), out_bias=base_b.to(dev()),
+                               accumulate=True)
+    finally:
+        api.mxfp8_debug_force_wgrad(prev)
+    check_dw(dw, db, dy, X)
+    check_dw(*acc, dy, X, base, base_b)
+    assert torch.equal(dw, again)
+
+
+@pytest.mark.parametrize("M,N,K", [(16384, 64, 48), (9000, 256, 256), (5000, 136, 1040)])
+def test_wgrad_tiles_of_many_runs(M, N, K):
+    """Few tiles and many tokens: a tile in up to 128 pieces."""
+    x, dy = spiky(M, K, 1), randn((M, N), 2, 1e-3)
+    pa = keep(x, "b128")
+    dw, db = api.linear_wgrad(dy.to(dev()), pa, bias_grad=True)
+    check_dw(dw, db, dy, f64(pa.dequantize()))
+    assert torch.equal(dw, api.linear_wgrad(dy.to(dev()), pa))
