@@ -446,7 +446,8 @@ int mxfp8_debug_force_b128(int tile);
  *   db      [N] or NULL, fp32 or bf16 (db_dtype)
  *   accumulate != 0: dw += and db += (fp32 only; MXFP8_E_SHAPE else)
  * M == 0 writes zeros (or leaves dw, db as they are if accumulating).
- * workspace of mxfp8_linear_wgrad_workspace_bytes, 256-byte aligned.
+ * workspace of mxfp8_linear_wgrad_workspace_bytes, 256-byte aligned (0: NULL
+ * is fine).
  */
 int mxfp8_linear_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes);
 int mxfp8_linear_wgrad(const void* dy_bf16, int64_t M, int64_t N, int64_t lddy, const void* q_packed,
@@ -503,6 +504,8 @@ int mxfp8_debug_force_wgrad(int tile);
  *   logits, dlogits [T, E], row strides ldl, ldd >= E, fp32 or bf16 (`dtype`)
  *   valid bytes [T]; loss fp32 [1]; counts int32 [E]; used int32 [1]
  * 1 <= E <= 256, 1 <= topk <= min(E, 16), T >= 0 (T == 0: loss 0, counts 0).
+ * workspace of mxfp8_moe_balance_workspace_bytes, 256-byte aligned (0: NULL is
+ * fine).
  * The backward call takes counts and used as the forward call (or a sum of
  * several forward calls' over data-parallel ranks) left them, on the device.
  */

@@ -557,8 +557,9 @@ def _same_device(first, *rest):
 def _scratch(need, device):
     """A workspace for one call.  From torch's caching allocator each time, so
     that it follows the allocator's rules for streams and captured graphs: a
-    graph keeps its own, and no two calls share one unless their order allows."""
-    return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    graph keeps its own, and no two calls share one unless their order allows.
+    None where none is needed."""
+    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
 
 
 @functools.lru_cache(maxsize=4096)
@@ -670,7 +671,7 @@ def _linear_prepared_b128(x, pw, bias, out, workspace):
     _same_device(x2, pw.w_packed, bias, out, workspace)
     with _on(x.device):
         need = _bytes("mxfp8_linear_b128_workspace_bytes", M, N, K)
-        ws = workspace if workspace is not None or need == 0 else _scratch(need, x.device)
+        ws = workspace if workspace is not None else _scratch(need, x.device)
         _check(lib().mxfp8_linear_b128(_ptr(x2), M, K, x2.stride(0), _ptr(pw.w_packed), _ptr(pw.s_packed), N,
                                        _ptr(bias), _ptr(out), out.stride(0), _ptr(ws), 0 if ws is None else ws.numel(),
                                        _stream(x.device)), "mxfp8_linear_b128")
@@ -767,10 +768,11 @@ def linear_wgrad(dy, pa, dtype=torch.float32, bias_grad=False, out=None, out_bia
         raise ValueError("accumulate needs float32 outputs")
     _same_device(d2, pa.q_packed, out, db)
     with _on(dy.device):
-        ws = _scratch(_bytes("mxfp8_linear_wgrad_workspace_bytes", M, N, pa.K), dy.device)
+        need = _bytes("mxfp8_linear_wgrad_workspace_bytes", M, N, pa.K)
+        ws = _scratch(need, dy.device)
         _check(lib().mxfp8_linear_wgrad(_ptr(d2), M, N, d2.stride(0), _ptr(pa.q_packed), _ptr(pa.s_packed), pa.K,
                                         _ptr(out), _DTYPES[out.dtype], out.stride(0), _ptr(db),
-                                        0 if db is None else _DTYPES[db.dtype], int(accumulate), _ptr(ws), ws.numel(),
+                                        0 if db is None else _DTYPES[db.dtype], int(accumulate), _ptr(ws), need,
                                         _stream(dy.device)), "mxfp8_linear_wgrad")
     return (out, db) if bias_grad else out
 
@@ -846,7 +848,7 @@ class _LinearB128(torch.autograd.Function):
         with _on(d):
             ws = _scratch(ctx.ws_bytes, d)
             _check(lib().mxfp8_linear_b128_backward(_ptr(d2), M, N, d2.stride(0), K, ctx.keep, _ptr(kept), _ptr(dx), K,
-                                                    _ptr(dw), 1, K, _ptr(db), 1, _ptr(ws), ws.numel(), _stream(d)),
+                                                    _ptr(dw), 1, K, _ptr(db), 1, _ptr(ws), ctx.ws_bytes, _stream(d)),
                    "mxfp8_linear_b128_backward")
         if need_x and len(ctx.shape) != 2:
             dx = dx.view(ctx.shape)
@@ -1006,10 +1008,11 @@ def moe_balance(logits, topk, valid=None, coef=1e-2, z_coef=0.0):
         loss = torch.empty((), dtype=torch.float32, device=d)
         counts = torch.empty(E, dtype=torch.int32, device=d)
         used = torch.empty(1, dtype=torch.int32, device=d)
-        ws = _scratch(_bytes("mxfp8_moe_balance_workspace_bytes", T, E), d)
+        need = _bytes("mxfp8_moe_balance_workspace_bytes", T, E)
+        ws = _scratch(need, d)
         _check(lib().mxfp8_moe_balance(_ptr(logits), _DTYPES[logits.dtype], T, E, logits.stride(0), topk,
                                        _ptr(valid), coef, z_coef, _ptr(loss), _ptr(counts), _ptr(used), _ptr(ws),
-                                       ws.numel(), _stream(d)), "mxfp8_moe_balance")
+                                       need, _stream(d)), "mxfp8_moe_balance")
     return loss, counts, used
 
 

@@ -127,7 +127,7 @@ mxfp8::WgradPlan wgrad_plan(int64_t M, int64_t N, int64_t K) {
     const bool small = tile == 128;
     // Whole tiles, one run per compute unit at most.
     const int64_t whole = std::min(kRuns, tiles);
-    const double per_step = small ? 1.0 : whole == kRuns ? 1.95 : 1.62, per_tile = small ? 3.3 : 23.0;
+    const double per_step = small ? 0.87 : whole == kRuns ? 1.95 : 1.62, per_tile = small ? 3.3 : 23.0;
     offer({tiles, (int)steps, (int)whole}, 1,
           (small ? 5.0 : 0.0) + ceil_div(tiles, whole) * (per_tile + per_step * (double)steps));
     // Equal runs, of two or eight steps at least.
@@ -138,7 +138,7 @@ mxfp8::WgradPlan wgrad_plan(int64_t M, int64_t N, int64_t K) {
                                 : 0.08 * (double)(r + tiles - std::gcd(r, tiles));
       const double touched = ceil_div(tiles, r) + (!small && tiles > r ? 1.0 : 0.0);
       offer({units, 1, (int)r}, pieces,
-            (small ? 5.0 + 3.3 * touched : 18.0 * touched) + (small ? 1.0 : 2.0) * ceil_div(units, r) + join);
+            (small ? 5.0 + 3.3 * touched : 18.0 * touched) + (small ? 0.87 : 2.0) * ceil_div(units, r) + join);
     }
   }
   return best;
@@ -148,7 +148,9 @@ mxfp8::WgradPlan wgrad_plan(int64_t M, int64_t N, int64_t K) {
 size_t wgrad_dw_bytes(const mxfp8::WgradPlan& p) {
   return p.shared() ? (size_t)p.runs.count * 2 * p.tile * p.tile * 4 : 0;
 }
-size_t wgrad_db_bytes(const mxfp8::WgradPlan& p) { return (size_t)p.tiles() * (size_t)p.pieces * p.tile * 4; }
+size_t wgrad_db_bytes(const mxfp8::WgradPlan& p) {
+  return p.db_direct() ? 0 : (size_t)p.tiles() * (size_t)p.pieces * p.tile * 4;
+}
 
 size_t part_bytes(int64_t M, int64_t N, mxfp8::B128Plan p) {
   return p.splits > 1 ? round_up((size_t)p.splits * (size_t)M * (size_t)((N + 3) / 4 * 4) * 4, 256) : 0;
@@ -388,7 +390,7 @@ int mxfp8_linear_wgrad(const void* dy_bf16, int64_t M, int64_t N, int64_t lddy, 
     return MXFP8_E_SHAPE;
   size_t need = 0;
   mxfp8_linear_wgrad_workspace_bytes(M, N, K, &need);
-  if (!workspace || workspace_bytes < need) return MXFP8_E_WORKSPACE;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MXFP8_E_WORKSPACE;
   if (!aligned(workspace, 256)) return MXFP8_E_ALIGN;
   if (int st = mxfp8::check_device_current()) return st;
   mxfp8::WgradArgs a;
@@ -490,7 +492,7 @@ int mxfp8_linear_b128_backward(const void* dy_bf16, int64_t M, int64_t N, int64_
 int mxfp8_moe_balance_workspace_bytes(int64_t T, int64_t E, size_t* bytes) {
   if (!bytes) return MXFP8_E_NULLPTR;
   if (T < 0 || E < 1 || E > mxfp8::kMoeMaxExperts) return MXFP8_E_SHAPE;
-  *bytes = mxfp8::balance_ws_bytes(E);
+  *bytes = mxfp8::balance_ws_bytes(T, E);
   return MXFP8_OK;
 }
 
@@ -500,7 +502,8 @@ int mxfp8_moe_balance(const void* logits, int dtype, int64_t T, int64_t E, int64
   if (int st = check_logits(logits, dtype, T, E, ldl, topk)) return st;
   if (!loss || !counts || !used) return MXFP8_E_NULLPTR;
   if (!aligned(loss, 4) || !aligned(counts, 4) || !aligned(used, 4)) return MXFP8_E_ALIGN;
-  if (!workspace || workspace_bytes < mxfp8::balance_ws_bytes(E)) return MXFP8_E_WORKSPACE;
+  const size_t need = mxfp8::balance_ws_bytes(T, E);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MXFP8_E_WORKSPACE;
   if (!aligned(workspace, 256)) return MXFP8_E_ALIGN;
   if (int st = mxfp8::check_device_current()) return st;
   mxfp8::BalanceArgs a = {};

@@ -35,7 +35,7 @@ namespace mxfp8 {
 namespace {
 
 constexpr int kBalThreads = 512;
-constexpr int kBalTokens = kBalThreads / 16;   // tokens a workgroup works on at a time
+static_assert(kBalTokens == kBalThreads / 16, "tokens a workgroup works on at a time");
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu, kKeyPosInf = 0xFF800000u;   // order_key of the infinities
 
 template <int kCtrl>
@@ -186,7 +186,9 @@ __host__ __device__ inline BalParts bal_parts(void* ws, int64_t E) {
 template <int kC, int kV, int kTop, bool kBf16>
 __global__ __launch_bounds__(kBalThreads) void balance_kernel(const void* __restrict__ logits, int64_t T, int E,
                                                               int64_t ldl, int topk,
-                                                              const uint8_t* __restrict__ valid, void* ws) {
+                                                              const uint8_t* __restrict__ valid, void* ws, float coef,
+                                                              float z_coef, int* __restrict__ counts,
+                                                              int* __restrict__ used, float* __restrict__ loss) {
   constexpr int kWaves = kBalThreads / 64;
   __shared__ float lp[kWaves][16 * kC];
   __shared__ int lc[kWaves][16 * kC];
@@ -292,25 +294,44 @@ __global__ __launch_bounds__(kBalThreads) void balance_kernel(const void* __rest
     ln[wave] = ns;
   }
   __syncthreads();
-  const BalParts parts = bal_parts(ws, E);
+  float p = 0.0f, z = 0.0f;
+  int k = 0, n = 0;
   if (tid < E) {
-    float p = 0.0f;
-    int c = 0;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
       p += lp[w][tid];
-      c += lc[w][tid];
+      k += lc[w][tid];
     }
+  }
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    z += lz[w];
+    n += ln[w];
+  }
+  if (gridDim.x == 1) {
+    // The only workgroup has all the sums and needs no second launch.
+    __shared__ double ll[kWaves];
+    const double d = n > 0 ? (double)n : 1.0;
+    double mine = tid < E ? (double)coef * E / ((double)topk * d * d) * p * k : 0.0;
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) mine += __shfl_xor(mine, o);
+    if (lane == 0) ll[wave] = mine;
+    if (tid < E) counts[tid] = k;
+    __syncthreads();
+    if (tid != 0) return;
+    mine = z_coef != 0.0f ? (double)z * (double)z_coef / d : 0.0;   // as in the reduction below
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) mine += ll[w];
+    *used = n;
+    *loss = (float)mine;
+    return;
+  }
+  const BalParts parts = bal_parts(ws, E);
+  if (tid < E) {
     parts.p[(int64_t)blockIdx.x * E + tid] = p;
-    parts.c[(int64_t)blockIdx.x * E + tid] = c;
+    parts.c[(int64_t)blockIdx.x * E + tid] = k;
   }
   if (tid == 0) {
-    float z = 0.0f;
-    int n = 0;
-    for (int w = 0; w < kWaves; ++w) {
-      z += lz[w];
-      n += ln[w];
-    }
     parts.z[blockIdx.x] = z;
     parts.n[blockIdx.x] = n;
     if (blockIdx.x == 0) *parts.arrived = 0;
@@ -493,14 +514,14 @@ void by_width(int64_t E, int bf16, int64_t ld, const void* p, const void* p2, F 
 
 int launch_balance(const BalanceArgs& a, hipStream_t stream) {
   static_assert(kMoeMaxExperts <= 256 && kMoeMaxTopk <= 16, "sixteen lanes x sixteen registers hold a row of logits");
-  // one workgroup at least: it clears the arrival count
+  // one workgroup at least: it writes the results of no tokens
   const int64_t need = std::max<int64_t>(1, (a.T + kBalTokens - 1) / kBalTokens);
   const int blocks = (int)std::min<int64_t>(need, kBalMaxBlocks);
   by_width(a.E, a.bf16, a.ldl, a.logits, nullptr, [&](auto C, auto V) {
     constexpr int c = decltype(C)::value, v = decltype(V)::value;
     auto go = [&](auto kern) {
       hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kBalThreads), 0, stream, a.logits, a.T, (int)a.E, a.ldl,
-                         (int)a.topk, a.valid, a.ws);
+                         (int)a.topk, a.valid, a.ws, a.coef, a.z_coef, a.counts, a.used, a.loss);
     };
     constexpr int top = c < 8 ? c : 8;
     if (a.topk <= 8) {
@@ -512,6 +533,7 @@ int launch_balance(const BalanceArgs& a, hipStream_t stream) {
     }
   });
   if (hipGetLastError() != hipSuccess) return -7;
+  if (blocks == 1) return 0;
   hipLaunchKernelGGL(balance_reduce_kernel, dim3((unsigned)((a.E + 15) / 16)), dim3(1024), 0, stream, a.ws, blocks,
                      (int)a.E, (int)a.topk, a.coef, a.z_coef, a.counts, a.used, a.loss);
   return hipGetLastError() == hipSuccess ? 0 : -7;

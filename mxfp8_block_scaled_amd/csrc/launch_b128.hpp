@@ -65,6 +65,9 @@ struct WgradPlan {
   int64_t pieces;    // most runs that share a tile (1: none is shared)
   int64_t tiles() const { return tiles_n * tiles_k; }
   bool shared() const { return pieces > 1; }
+  // Whole small tiles: those with k = 0 add up all of db, which needs no parts
+  // and no second launch (their steps have MFMAs to spare, the large form's do not).
+  bool db_direct() const { return tile == 128 && !shared(); }
 };
 constexpr int kWgStep = 64;   // tokens per step
 struct WgradArgs {
@@ -102,8 +105,12 @@ struct BalanceArgs {
   void* ws;                // forward partials
 };
 constexpr int kBalMaxBlocks = 512;   // forward workgroups, each with partials in the workspace
-// [16] doubles, then per forward workgroup sums and counts of the experts, z and n, then the arrival count.
-inline size_t balance_ws_bytes(int64_t E) { return 16 * 8 + (size_t)kBalMaxBlocks * ((size_t)E * 8 + 8) + 8; }
+constexpr int kBalTokens = 32;       // tokens a forward workgroup works on at a time
+// [16] doubles, then per forward workgroup sums and counts of the experts, z
+// and n, then the arrival count; nothing where there is one forward workgroup.
+inline size_t balance_ws_bytes(int64_t T, int64_t E) {
+  return T <= kBalTokens ? 0 : 16 * 8 + (size_t)kBalMaxBlocks * ((size_t)E * 8 + 8) + 8;
+}
 int launch_balance(const BalanceArgs& a, hipStream_t stream);
 int launch_balance_backward(const BalanceArgs& a, hipStream_t stream);
 

@@ -285,13 +285,13 @@ __global__ __launch_bounds__(kWgThreads, 1) void wgrad_big_kernel(
 // those are fewer; the ones without work leave), and the parts of db (the last
 // workgroups, sixteen columns each): over the tiles of a column of tiles and
 // their pieces.
-template <int kT>
+template <int kT, int kWavesN>
 __global__ __launch_bounds__(256) void wgrad_join_kernel(const float* __restrict__ part, Runs runs, int parts, int by_border,
                                                          int tiles_k, int steps, int N, int K, void* __restrict__ dw,
                                                          int64_t lddw, int out_bf16, int accumulate,
                                                          const float* __restrict__ part_db, int pieces,
                                                          void* __restrict__ db, int db_bf16) {
-  constexpr int kF = kT / 32;                // fragments per wave and axis
+  constexpr int kA = kT / 32, kB = kT / 16 / kWavesN;   // fragments per wave along k and n
   constexpr int kSub = kT * kT / 1024;       // workgroups per tile
   const int tid = threadIdx.x;
   if ((int)blockIdx.x >= parts * kSub) {
@@ -343,9 +343,9 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(const float* __restrict
     w += m;
     p += (size_t)m * 2 * (kT * kT / 4);
   }
-  const int wave = e / (kF * kF * 64), ab = (e >> 6) & (kF * kF - 1), lane = e & 63;
-  const int n = tn * kT + (wave >> 1) * (kT / 2) + (ab % kF) * 16 + (lane & 15);
-  const int k = tk * kT + (wave & 1) * (kT / 2) + (ab / kF) * 16 + 4 * (lane >> 4);
+  const int wave = e / (kA * kB * 64), ab = (e >> 6) % (kA * kB), lane = e & 63;
+  const int n = tn * kT + (wave >> 1) * (kB * 16) + (ab % kB) * 16 + (lane & 15);
+  const int k = tk * kT + (wave & 1) * (kT / 2) + (ab / kB) * 16 + 4 * (lane >> 4);
   if (n >= N || k >= K) return;
   if (out_bf16) {
     *reinterpret_cast<uint2*>((uint16_t*)dw + (size_t)n * lddw + k) =
@@ -368,12 +368,13 @@ int launch_big(const WgradArgs& a, const WgradPlan& p, hipStream_t stream) {
   return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 
-template <int kT>
+template <int kT, int kWavesN>
 int launch_join(const WgradArgs& a, const WgradPlan& p, hipStream_t stream) {
   const int borders = p.runs.count - 1, by_border = borders < p.tiles();
-  const int join = !p.shared() ? 0 : by_border ? borders : (int)p.tiles(), cols = a.db ? (int)((a.N + 15) / 16) : 0;
+  const int join = !p.shared() ? 0 : by_border ? borders : (int)p.tiles();
+  const int cols = a.db && !p.db_direct() ? (int)((a.N + 15) / 16) : 0;
   if (join + cols == 0) return 0;
-  hipLaunchKernelGGL(wgrad_join_kernel<kT>, dim3((unsigned)(join * (kT * kT / 1024) + cols)), dim3(256), 0, stream,
+  hipLaunchKernelGGL((wgrad_join_kernel<kT, kWavesN>), dim3((unsigned)(join * (kT * kT / 1024) + cols)), dim3(256), 0, stream,
                      a.part_dw, p.runs, join, by_border, (int)p.tiles_k, (int)p.steps, (int)a.N, (int)a.K, a.dw, a.lddw,
                      a.out_bf16, a.accumulate, a.part_db, (int)p.pieces, a.db, a.db_bf16);
   return hipGetLastError() == hipSuccess ? 0 : -7;
@@ -383,10 +384,10 @@ int launch_join(const WgradArgs& a, const WgradPlan& p, hipStream_t stream) {
 int launch_wgrad(const WgradArgs& a, WgradPlan p, hipStream_t stream) {
   if (p.tile == 128) {
     if (int st = launch_wgrad_small(a, p, stream)) return st;
-    return launch_join<128>(a, p, stream);
+    return launch_join<128, 4>(a, p, stream);
   }
   if (int st = a.db != nullptr ? launch_big<true>(a, p, stream) : launch_big<false>(a, p, stream)) return st;
-  return launch_join<256>(a, p, stream);
+  return launch_join<256, 2>(a, p, stream);
 }
 
 }  // namespace mxfp8

@@ -8,24 +8,25 @@ namespace {
 
 using namespace wgrad;
 
-// Small tiles (128 x 128), 1 workgroup per compute unit.
+// Small tiles (128 x 128), 1 workgroup of eight waves per compute unit.
 struct WgLds {
   static constexpr int kT = 128;
+  static constexpr int kThreads = 512;
   static constexpr int kPitch = kT * 2;
   static constexpr int kY = kWgStep * kPitch;        // dY of a step, bf16
   static constexpr int kRaw = kWgStep * kT;          // X of a step, E4M3: eight 1 KiB pieces [64-K half][band]
-  static constexpr int kStage = kY + kRaw + 4 * 512; // + per wave the two 256-byte scale tiles
+  static constexpr int kStage = kY + kRaw + 8 * 256; // + per wave a 256-byte scale tile
   static constexpr int kDepth = 4;                   // steps in LDS
   static constexpr int kX = kWgStep * kPitch;        // X widened
   static constexpr int kBytes = kDepth * kStage + 2 * kX;
-  static constexpr int kCopies = 4 + 2 + 2;          // per wave and step
+  static constexpr int kCopies = 2 + 1 + 1;          // per wave and step
 };
 static_assert(WgLds::kBytes <= 160 * 1024, "LDS of a compute unit");
 
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// Small tiles: 128 x 128 of dW, four waves 2 x 2, each 64 x 64, for the
+// Small tiles: 128 x 128 of dW, eight waves 2 (k) x 4 (n), each 64 x 32, for the
 // problems whose large tiles would leave the chip empty or idle at the end.
 // There a step's time is the latency of its loads, so everything comes by
 // copies into LDS, three steps ahead.  Every wave widens the sixteen token
@@ -36,12 +37,13 @@ static_assert(WgLds::kBytes <= 160 * 1024, "LDS of a compute unit");
 // instead of 41 at 67 x 7640 x 5888).
 // ---------------------------------------------------------------------------
 template <bool kBias>
-__global__ __launch_bounds__(kWgThreads, 1) void wgrad_kernel(
+__global__ __launch_bounds__(WgLds::kThreads, 1) void wgrad_kernel(
     const uint16_t* __restrict__ dy, int64_t M, int N, int64_t lddy, const uint8_t* __restrict__ qp,
     const uint8_t* __restrict__ sp, int K, int KS, int tiles_k, int steps, Runs runs, void* __restrict__ dw,
-    int64_t lddw, int out_bf16, int accumulate, float* __restrict__ part, float* __restrict__ part_db, int pieces) {
+    int64_t lddw, int out_bf16, int accumulate, float* __restrict__ part, float* __restrict__ part_db, int pieces,
+    void* __restrict__ db, int db_bf16) {
   using L = WgLds;
-  constexpr int kF = 4;             // 16-wide fragments per wave and axis
+  constexpr int kA = 4, kB = 2;     // 16-wide fragments per wave along k and n
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -57,10 +59,10 @@ __global__ __launch_bounds__(kWgThreads, 1) void wgrad_kernel(
   // token rows of 256 bytes), i.e. half h of slot c of row m, which holds
   // logical slot c ^ f(m).  Rows past M are past the resource's end and read
   // zero; columns past N belong to outputs that are not stored.
-  uint32_t vy[4];
+  uint32_t vy[2];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const int m = (wave * 4 + c) * 4 + (lane >> 4), p = lane & 15;
+  for (int c = 0; c < 2; ++c) {
+    const int m = (wave * 2 + c) * 4 + (lane >> 4), p = lane & 15;
     vy[c] = (uint32_t)((int64_t)m * lddy + ((p >> 1) ^ slot_xor(m)) * 16 + (p & 1) * 8) * 2u;
   }
   auto stage = [&](int b) { return smem + b * L::kStage; };
@@ -75,23 +77,21 @@ __global__ __launch_bounds__(kWgThreads, 1) void wgrad_kernel(
   int64_t rows = M - (int64_t)cs * kWgStep;              // token rows from this step on
   const uint8_t* xp = qp + (size_t)(cs >> 1) * gbytes;
   const uint8_t* scp = sp + (size_t)(cs >> 1) * sbytes;
-  const uint32_t vx0 = (uint32_t)wave * KS * kPieceBytes + (uint32_t)lane * 16u, vx1 = vx0 + 4u * KS * kPieceBytes;
+  // X: the wave's piece of the eight of a step: 64-K half, band of 16 tokens
+  const int xv = wave & 1, band = wave >> 1;
+  const uint32_t vx0 = (uint32_t)band * KS * kPieceBytes + (uint32_t)lane * 16u, vx1 = vx0 + 4u * KS * kPieceBytes;
   auto issue = [&](uint8_t* st) {
     const int r = rows >= kWgStep ? kWgStep : (int)rows;
     const tile::i4v ry = tile::buffer_rsrc(yp, r > 0 ? (uint32_t)((r - 1) * (int)lddy + N - ctn * L::kT) * 2u : 0u);
     const tile::i4v rx = tile::buffer_rsrc(xp, gbytes);
     const tile::i4v rs = tile::buffer_rsrc(scp, sbytes);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) tile::b2l_16(vy[c], ry, 0u, st + (wave * 4 + c) * 1024);
+    for (int c = 0; c < 2; ++c) tile::b2l_16(vy[c], ry, 0u, st + (wave * 2 + c) * 1024);
     // pieces past K read other columns' data or, past the group, zeros
-#pragma unroll
-    for (int v = 0; v < 2; ++v)
-      tile::b2l_16((cs & 1) ? vx1 : vx0, rx, (uint32_t)(2 * ctk + v) * kPieceBytes,
-                   st + L::kY + (v * 4 + wave) * 1024);
-#pragma unroll
-    for (int v = 0; v < 2; ++v)
-      tile::b2l_4((uint32_t)lane * 4u, rs, (uint32_t)(2 * ctk + v) * kTileScaleBytes,
-                  st + L::kY + L::kRaw + wave * 512 + v * 256);
+    tile::b2l_16((cs & 1) ? vx1 : vx0, rx, (uint32_t)(2 * ctk + xv) * kPieceBytes,
+                 st + L::kY + (xv * 4 + band) * 1024);
+    tile::b2l_4((uint32_t)lane * 4u, rs, (uint32_t)(2 * ctk + xv) * kTileScaleBytes,
+                st + L::kY + L::kRaw + wave * 256);
     if (left > 1) {
       --left;
       if (++cs < steps) {
@@ -112,20 +112,23 @@ __global__ __launch_bounds__(kWgThreads, 1) void wgrad_kernel(
       }
     }
   };
-  // Widening: the thread's two chunks are in token row m = 16 wave + lane / 4.
-  const int xm = 16 * wave + (lane >> 2), xc = (lane & 3) ^ swz(lane >> 2);
-  auto widen = [&](int s, const uint8_t* st, uint8_t* to) {
-    const int half = s & 1;
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const uint4 q = *reinterpret_cast<const uint4*>(st + L::kY + (v * 4 + wave) * 1024 + lane * 16);
-      const uint32_t sb = st[L::kY + L::kRaw + wave * 512 + v * 256 + scale_off(xm, xc >> 1) + 2 * half];
-      uint4 d[2];
-      widen16(q, b128_scale_value(sb), d);
-      uint4* o = reinterpret_cast<uint4*>(to + xm * L::kPitch + (((v * 4 + xc) ^ slot_xor(xm)) * 32));
-      o[0] = d[0];
-      o[1] = d[1];
-    }
+  // Widening: the thread's chunk is in token row m = 16 band + lane / 4.
+  const int xm = 16 * band + (lane >> 2), xc = (lane & 3) ^ swz(lane >> 2);
+  const int xdst = xm * L::kPitch + (((xv * 4 + xc) ^ slot_xor(xm)) * 32);
+  struct Raw {
+    uint4 q;
+    uint32_t s;
+  };
+  auto load_raw = [&](int s, const uint8_t* st) {
+    return Raw{*reinterpret_cast<const uint4*>(st + L::kY + (xv * 4 + band) * 1024 + lane * 16),
+               st[L::kY + L::kRaw + wave * 256 + scale_off(xm, xc >> 1) + 2 * (s & 1)]};
+  };
+  auto widen = [&](const Raw& x, uint8_t* to) {
+    uint4 d[2];
+    widen16(x.q, b128_scale_value(x.s), d);
+    uint4* o = reinterpret_cast<uint4*>(to + xdst);
+    o[0] = d[0];
+    o[1] = d[1];
   };
 
   // Fragment f (sixteen columns) and 32-token half h of a tile: lane (i, g)
@@ -140,14 +143,14 @@ __global__ __launch_bounds__(kWgThreads, 1) void wgrad_kernel(
     return __builtin_bit_cast(bf16x8, r);
   };
 
-  v4f acc[kF][kF];
-  v4f accb[kF];
+  v4f acc[kA][kB];
+  v4f accb[kB];
   auto clear = [&] {
 #pragma unroll
-    for (int a = 0; a < kF; ++a) {
-      accb[a] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int b = 0; b < kB; ++b) {
+      accb[b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int b = 0; b < kF; ++b) acc[a][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int a = 0; a < kA; ++a) acc[a][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     }
   };
   clear();
@@ -155,78 +158,78 @@ __global__ __launch_bounds__(kWgThreads, 1) void wgrad_kernel(
 #pragma unroll
   for (int e = 0; e < 8; ++e) ones[e] = (__bf16)1.0f;
 
-  bf16x8 ax[kF], ay[kF], bx[kF], by[kF];   // fragments of half 0 and of half 1
+  bf16x8 ax[kA], ay[kB], bx[kA], by[kB];   // fragments of half 0 and of half 1
 #pragma unroll
   for (int d = 0; d < L::kDepth - 1; ++d) issue(stage(d));
   tile::wait_vmcnt<(L::kDepth - 2) * L::kCopies>();
-  widen(sa0, stage(0), widened(0));
+  widen(load_raw(sa0, stage(0)), widened(0));
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();
 #pragma unroll
-  for (int a = 0; a < kF; ++a) {
-    ax[a] = frag(widened(0), wk * kF + a, 0);
-    ay[a] = frag(stage(0), wn * kF + a, 0);
-  }
+  for (int a = 0; a < kA; ++a) ax[a] = frag(widened(0), wk * kA + a, 0);
+#pragma unroll
+  for (int b = 0; b < kB; ++b) ay[b] = frag(stage(0), wn * kB + b, 0);
   int t = t0, tn = t0 / tiles_k, tk = t0 - tn * tiles_k;
   int s = sa0, sa = sa0, phase = sa0 % tiles_k, at = 0;
-  int stored = 0;   // bit 0 / 1: the last unit / the one before it ended with kF * kF stores at least
+  int stored = 0;   // bit 0 / 1: the last unit / the one before it ended with kA * kB stores at least
   for (int r = 0; r < n_units; ++r) {
     const int next = at + 1 == L::kDepth ? 0 : at + 1, last = at == 0 ? L::kDepth - 1 : at - 1;
     const int par = r & 1, sn = s + 1 == steps ? 0 : s + 1;
     const uint8_t *const y = stage(at), *const x = widened(par);
     const uint8_t *const yn = stage(next), *const xn = widened(par ^ 1);
-    const bool with_bias = kBias && wk == 0 && phase == tk;
+    const bool with_bias = kBias && wk == 0 && (db != nullptr ? 0 : phase) == tk;
     phase = phase + 1 == tiles_k ? 0 : phase + 1;
     // Half 0, with the reads of half 1 and the widening of the next step (this
     // wave's copies of it have landed: only the copies of the step after it
     // and stores issued since are in flight).  The empty asm statements keep
     // the MFMAs in their places.
     if (stored == 0) tile::wait_vmcnt<(L::kDepth - 3) * L::kCopies>();
-    else if (stored == 3) tile::wait_vmcnt<(L::kDepth - 3) * L::kCopies + 2 * kF * kF>();
-    else tile::wait_vmcnt<(L::kDepth - 3) * L::kCopies + kF * kF>();
-    tile::static_for<0, 16>([&](auto J) {
-      constexpr int j = decltype(J)::value, a = j >> 2, c = j & 3;
+    else if (stored == 3) tile::wait_vmcnt<(L::kDepth - 3) * L::kCopies + 2 * kA * kB>();
+    else tile::wait_vmcnt<(L::kDepth - 3) * L::kCopies + kA * kB>();
+    const Raw raw = load_raw(sn, yn);   // (at the run's end: a copy of the last unit)
+    tile::static_for<0, 8>([&](auto J) {
+      constexpr int j = decltype(J)::value, a = j >> 1, c = j & 1;
       acc[a][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ax[a], ay[c], acc[a][c], 0, 0, 0);
       asm volatile("" : "+v"(acc[a][c]));
-      if constexpr (j < 4) by[j] = frag(y, wn * kF + j, 1);
-      else if constexpr (j < 8) bx[j - 4] = frag(x, wk * kF + j - 4, 1);
-      if constexpr (j == 8) widen(sn, yn, widened(par ^ 1));   // (at the run's end: a copy of the last unit)
+      if constexpr (j < 2) by[j] = frag(y, wn * kB + j, 1);
+      else if constexpr (j < 6) bx[j - 2] = frag(x, wk * kA + j - 2, 1);
+      if constexpr (j == 5) widen(raw, widened(par ^ 1));
       __builtin_amdgcn_sched_barrier(0);
     });
     if (with_bias) {
 #pragma unroll
-      for (int b = 0; b < kF; ++b) accb[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, ay[b], accb[b], 0, 0, 0);
+      for (int b = 0; b < kB; ++b) accb[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, ay[b], accb[b], 0, 0, 0);
     }
     // Past this barrier the next unit has landed and is widened for all waves,
     // and nobody reads the last one from LDS any more.
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     issue(stage(last));
-    tile::static_for<0, 16>([&](auto J) {
-      constexpr int j = decltype(J)::value, a = j >> 2, c = j & 3;
+    tile::static_for<0, 8>([&](auto J) {
+      constexpr int j = decltype(J)::value, a = j >> 1, c = j & 1;
       acc[a][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bx[a], by[c], acc[a][c], 0, 0, 0);
       asm volatile("" : "+v"(acc[a][c]));
-      if constexpr (j < 4) ay[j] = frag(yn, wn * kF + j, 0);
-      else if constexpr (j < 8) ax[j - 4] = frag(xn, wk * kF + j - 4, 0);
+      if constexpr (j < 2) ay[j] = frag(yn, wn * kB + j, 0);
+      else if constexpr (j < 6) ax[j - 2] = frag(xn, wk * kA + j - 2, 0);
       __builtin_amdgcn_sched_barrier(0);
     });
     if (with_bias) {
 #pragma unroll
-      for (int b = 0; b < kF; ++b) accb[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, by[b], accb[b], 0, 0, 0);
+      for (int b = 0; b < kB; ++b) accb[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, by[b], accb[b], 0, 0, 0);
     }
     at = next;
     stored = (stored << 1) & 2;
     if (sn == 0 || r + 1 == n_units) {
-      // Lane (i, g) holds D[k = 64 wk + 16 a + 4 g + j][n = 64 wn + 16 b + i].
+      // Lane (i, g) holds D[k = 64 wk + 16 a + 4 g + j][n = 32 wn + 16 b + i].
       const int n0 = tn * L::kT, k0 = tk * L::kT;
       if (sa == 0 && sn == 0) {
 #pragma unroll
-        for (int b = 0; b < kF; ++b) {
-          const int n = n0 + (wn * kF + b) * 16 + i;
+        for (int b = 0; b < kB; ++b) {
+          const int n = n0 + (wn * kB + b) * 16 + i;
           if (n >= N) continue;
 #pragma unroll
-          for (int a = 0; a < kF; ++a) {
-            const int k = k0 + (wk * kF + a) * 16 + 4 * g;
+          for (int a = 0; a < kA; ++a) {
+            const int k = k0 + (wk * kA + a) * 16 + 4 * g;
             if (k >= K) continue;   // K % 16 == 0: a quad is all in or all out
             if (out_bf16) {
               *reinterpret_cast<uint2*>((uint16_t*)dw + (size_t)n * lddw + k) =
@@ -242,19 +245,25 @@ __global__ __launch_bounds__(kWgThreads, 1) void wgrad_kernel(
       } else {
         // slot 0: the piece at the start of the run, 1: at its end
         v4f* d = reinterpret_cast<v4f*>(part + ((size_t)w * 2 + (t == t0 ? 0 : 1)) * (L::kT * L::kT));
-        d += wave * 1024 + lane;
+        d += wave * 512 + lane;
 #pragma unroll
-        for (int a = 0; a < kF; ++a)
+        for (int a = 0; a < kA; ++a)
 #pragma unroll
-          for (int b = 0; b < kF; ++b) d[(a * kF + b) * 64] = acc[a][b];
+          for (int b = 0; b < kB; ++b) d[(a * kB + b) * 64] = acc[a][b];
         stored |= 1;
       }
       // every row of the ones product holds the column sums
-      if (kBias && wk == 0 && g == 0) {
+      if (kBias && wk == 0 && g == 0 && db != nullptr) {
+#pragma unroll
+        for (int b = 0; b < kB; ++b) {
+          const int n = n0 + (wn * kB + b) * 16 + i;
+          if (tk == 0 && n < N) store_db(db, db_bf16, accumulate, n, accb[b][0]);
+        }
+      } else if (kBias && wk == 0 && g == 0) {
         const int piece = w - runs.of((int64_t)t * steps);
 #pragma unroll
-        for (int b = 0; b < kF; ++b)
-          part_db[((size_t)t * pieces + piece) * L::kT + (wn * kF + b) * 16 + i] = accb[b][0];
+        for (int b = 0; b < kB; ++b)
+          part_db[((size_t)t * pieces + piece) * L::kT + (wn * kB + b) * 16 + i] = accb[b][0];
       }
       clear();
       ++t;
@@ -276,10 +285,11 @@ int launch_small(const WgradArgs& a, const WgradPlan& p, hipStream_t stream) {
   constexpr int lds = WgLds::kBytes;
   static std::atomic<int> lds_set[kMaxDevices];
   if (!set_lds_limit_once((const void*)wgrad_kernel<kBias>, lds, lds_set)) return -7;
-  hipLaunchKernelGGL((wgrad_kernel<kBias>), dim3((unsigned)p.runs.count), dim3(kWgThreads), lds, stream,
+  hipLaunchKernelGGL((wgrad_kernel<kBias>), dim3((unsigned)p.runs.count), dim3(WgLds::kThreads), lds, stream,
                      (const uint16_t*)a.dy, a.M, (int)a.N, a.lddy, (const uint8_t*)a.qp, (const uint8_t*)a.sp,
                      (int)a.K, (int)(2 * b128_blocks(a.K)), (int)p.tiles_k, (int)p.steps, p.runs, a.dw, a.lddw,
-                     a.out_bf16, a.accumulate, a.part_dw, a.part_db, (int)p.pieces);
+                     a.out_bf16, a.accumulate, a.part_dw, a.part_db, (int)p.pieces,
+                     p.db_direct() ? a.db : nullptr, a.db_bf16);
   return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 
