@@ -105,11 +105,11 @@ constexpr int64_t kRuns = 256;   // compute units
 // per tile and per 64-token step of a workgroup, and where tiles are shared
 // the partials' way to memory and back and the launch that joins them.  For
 // example (M, N, K; small tiles whole and in equal runs, large tiles the same):
-//   512 x 1024 x 1024     17   21   32   32
-//   16384 x 256 x 256    260   33  455   37
-//   1000 x 2064 x 2032    44   39   48   43
-//   4096 x 4096 x 4096   270  268  142  139
-//   16384 x 5120 x 2048  765  656  439  362
+//   512 x 1024 x 1024     14   17   32   32
+//   16384 x 256 x 256    226   26  454   37
+//   1000 x 2064 x 2032    37   38   48   43
+//   4096 x 4096 x 4096   247  243  143  151
+//   16384 x 5120 x 2048  665  561  435  374
 mxfp8::WgradPlan wgrad_plan(int64_t M, int64_t N, int64_t K) {
   const int64_t steps = std::max<int64_t>(1, (M + mxfp8::kWgStep - 1) / mxfp8::kWgStep);
   const int force = g_force_wgrad.load(std::memory_order_relaxed);
