@@ -242,19 +242,19 @@ __global__ __launch_bounds__(kWgThreads, 1) void wgrad_big_kernel(
 #pragma unroll
       for (int b = 0; b < 8; ++b) {
         const int n = n0 + wn * 128 + b * 16 + i;
-        if (n < N) {
+        if (out_bf16) {
+#pragma unroll
+          for (int a = 0; a < 8; a += 2) {
+            const int k = k0 + wk * 128 + a * 16 + k_of_pair(g);
+            store_pair(acc[a][b], acc[a + 1][b], n < N && k < K, (uint16_t*)dw + (size_t)n * lddw + k);
+          }
+        } else if (n < N) {
 #pragma unroll
           for (int a = 0; a < 8; ++a) {
             const int k = k0 + wk * 128 + a * 16 + 4 * g;
-            if (k < K) {
-              if (out_bf16) {
-                *reinterpret_cast<uint2*>((uint16_t*)dw + (size_t)n * lddw + k) =
-                    make_uint2(pack_bf16x2(acc[a][b][0], acc[a][b][1]), pack_bf16x2(acc[a][b][2], acc[a][b][3]));
-              } else {
-                v4f* d = reinterpret_cast<v4f*>((float*)dw + (size_t)n * lddw + k);
-                *d = accumulate ? *d + acc[a][b] : acc[a][b];
-              }
-            }
+            if (k >= K) continue;   // K % 16 == 0: a quad is all in or all out
+            v4f* d = reinterpret_cast<v4f*>((float*)dw + (size_t)n * lddw + k);
+            *d = accumulate ? *d + acc[a][b] : acc[a][b];
           }
         }
       }

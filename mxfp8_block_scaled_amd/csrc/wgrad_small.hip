@@ -34,7 +34,7 @@ static_assert(WgLds::kBytes <= 160 * 1024, "LDS of a compute unit");
 // two buffers: one barrier per step.  A workgroup goes through its run of
 // (tile, step) units without a stop: copies and fragments of the next tile are
 // on their way while a tile is stored (67 x 7640 x 5888, bf16: 72 us with one
-// tile per launched workgroup, 42 now; writing dW alone takes 18).  Eight waves
+// tile per launched workgroup, 34 now; writing dW alone takes 18).  Eight waves
 // rather than four of 64 x 64, which read a third less from LDS but wait more:
 // 0.87 us a step against 1.0.
 // ---------------------------------------------------------------------------
@@ -173,7 +173,9 @@ __global__ __launch_bounds__(WgLds::kThreads, 1) void wgrad_kernel(
   for (int b = 0; b < kB; ++b) ay[b] = frag(stage(0), wn * kB + b, 0);
   int t = t0, tn = t0 / tiles_k, tk = t0 - tn * tiles_k;
   int s = sa0, sa = sa0, phase = sa0 % tiles_k, at = 0;
-  int stored = 0;   // bit 0 / 1: the last unit / the one before it ended with kA * kB stores at least
+  // Stores at the end of the last unit and of the one before it, at least, in
+  // halves of a tile's kA * kB; and the last unit's alone.
+  int stored = 0, stored_last = 0;
   for (int r = 0; r < n_units; ++r) {
     const int next = at + 1 == L::kDepth ? 0 : at + 1, last = at == 0 ? L::kDepth - 1 : at - 1;
     const int par = r & 1, sn = s + 1 == steps ? 0 : s + 1;
@@ -185,9 +187,11 @@ __global__ __launch_bounds__(WgLds::kThreads, 1) void wgrad_kernel(
     // wave's copies of it have landed: only the copies of the step after it
     // and stores issued since are in flight).  The empty asm statements keep
     // the MFMAs in their places.
-    if (stored == 0) tile::wait_vmcnt<(L::kDepth - 3) * L::kCopies>();
-    else if (stored == 3) tile::wait_vmcnt<(L::kDepth - 3) * L::kCopies + 2 * kA * kB>();
-    else tile::wait_vmcnt<(L::kDepth - 3) * L::kCopies + kA * kB>();
+    constexpr int kNewer = (L::kDepth - 3) * L::kCopies, kHalf = kA * kB / 2;
+    if (stored == 0) tile::wait_vmcnt<kNewer>();
+    else if (stored == 1) tile::wait_vmcnt<kNewer + kHalf>();
+    else if (stored < 4) tile::wait_vmcnt<kNewer + 2 * kHalf>();
+    else tile::wait_vmcnt<kNewer + 4 * kHalf>();
     const Raw raw = load_raw(sn, yn);   // (at the run's end: a copy of the last unit)
     tile::static_for<0, 8>([&](auto J) {
       constexpr int j = decltype(J)::value, a = j >> 1, c = j & 1;
@@ -220,7 +224,8 @@ __global__ __launch_bounds__(WgLds::kThreads, 1) void wgrad_kernel(
       for (int b = 0; b < kB; ++b) accb[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, by[b], accb[b], 0, 0, 0);
     }
     at = next;
-    stored = (stored << 1) & 2;
+    stored = stored_last;
+    stored_last = 0;
     if (sn == 0 || r + 1 == n_units) {
       // Lane (i, g) holds D[k = 64 wk + 16 a + 4 g + j][n = 32 wn + 16 b + i].
       const int n0 = tn * L::kT, k0 = tk * L::kT;
@@ -228,22 +233,28 @@ __global__ __launch_bounds__(WgLds::kThreads, 1) void wgrad_kernel(
 #pragma unroll
         for (int b = 0; b < kB; ++b) {
           const int n = n0 + (wn * kB + b) * 16 + i;
-          if (n >= N) continue;
+          if (out_bf16) {
 #pragma unroll
-          for (int a = 0; a < kA; ++a) {
-            const int k = k0 + (wk * kA + a) * 16 + 4 * g;
-            if (k >= K) continue;   // K % 16 == 0: a quad is all in or all out
-            if (out_bf16) {
-              *reinterpret_cast<uint2*>((uint16_t*)dw + (size_t)n * lddw + k) =
-                  make_uint2(pack_bf16x2(acc[a][b][0], acc[a][b][1]), pack_bf16x2(acc[a][b][2], acc[a][b][3]));
+            for (int a = 0; a < kA; a += 2) {
+              const int k = k0 + (wk * kA + a) * 16 + k_of_pair(g);
+              store_pair(acc[a][b], acc[a + 1][b], n < N && k < K, (uint16_t*)dw + (size_t)n * lddw + k);
+            }
+          } else if (n < N) {
+            float* const row = (float*)dw + (size_t)n * lddw;
+            const int k = k0 + wk * kA * 16 + 4 * g;   // K % 16 == 0: a quad is all in or all out
+            if (accumulate) {
+#pragma unroll
+              for (int a = 0; a < kA; ++a)
+                if (k + 16 * a < K) *reinterpret_cast<v4f*>(row + k + 16 * a) += acc[a][b];
             } else {
-              v4f* d = reinterpret_cast<v4f*>((float*)dw + (size_t)n * lddw + k);
-              *d = accumulate ? *d + acc[a][b] : acc[a][b];
+#pragma unroll
+              for (int a = 0; a < kA; ++a)
+                if (k + 16 * a < K) *reinterpret_cast<v4f*>(row + k + 16 * a) = acc[a][b];
             }
           }
         }
         // at the matrix's edge a wave may have skipped some
-        if (n0 + L::kT <= N && k0 + L::kT <= K) stored |= 1;
+        if (n0 + L::kT <= N && k0 + L::kT <= K) stored_last = out_bf16 ? 1 : 2;
       } else {
         // slot 0: the piece at the start of the run, 1: at its end
         v4f* d = reinterpret_cast<v4f*>(part + ((size_t)w * 2 + (t == t0 ? 0 : 1)) * (L::kT * L::kT));
@@ -252,7 +263,7 @@ __global__ __launch_bounds__(WgLds::kThreads, 1) void wgrad_kernel(
         for (int a = 0; a < kA; ++a)
 #pragma unroll
           for (int b = 0; b < kB; ++b) d[(a * kB + b) * 64] = acc[a][b];
-        stored |= 1;
+        stored_last = 2;
       }
       // every row of the ones product holds the column sums
       if (kBias && wk == 0 && g == 0 && db != nullptr) {
@@ -276,6 +287,7 @@ __global__ __launch_bounds__(WgLds::kThreads, 1) void wgrad_kernel(
         ++tn;
       }
     }
+    stored += stored_last;
     s = sn;
   }
   tile::wait_vmcnt<0>();   // no copy may land after the workgroup's LDS is given away
