@@ -522,7 +522,7 @@ def gemm_packed(pa, pw, bias=None):
         bias = _bias(bias, pw.N)
         _same_device(pa.q_packed, pw.w_packed, bias)
         with _on(pa.device):
-            ws = _scratch(_bytes("mxfp8_gemm_packed_b128_workspace_bytes", pa.M, pw.N, pa.K), pa.device)
+            ws = _scratch(_bytes("mxfp8_gemm_packed_b128_workspace_bytes", pa.M, pw.N, pa.K), y)
             _check(lib().mxfp8_gemm_packed_b128(_ptr(pa.q_packed), _ptr(pa.s_packed), pa.M, pa.K, _ptr(pw.w_packed),
                                                 _ptr(pw.s_packed), pw.N, _ptr(bias), _ptr(y), y.stride(0), _ptr(ws),
                                                 ws.numel(), _stream(pa.device)), "mxfp8_gemm_packed_b128")
@@ -554,12 +554,12 @@ def _same_device(first, *rest):
             raise ValueError(f"operands on {first.device} and {t.device}")
 
 
-def _scratch(need, device):
-    """A workspace for one call.  From torch's caching allocator each time, so
+def _scratch(need, like):
+    """A workspace on ``like``'s device for one call.  From torch's caching allocator each time, so
     that it follows the allocator's rules for streams and captured graphs: a
     graph keeps its own, and no two calls share one unless their order allows.
     None where none is needed."""
-    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    return like.new_empty(need, dtype=torch.uint8) if need else None
 
 
 @functools.lru_cache(maxsize=4096)
@@ -665,13 +665,13 @@ def _linear_prepared_b128(x, pw, bias, out, workspace):
         raise ValueError(f"x has {K} columns, the weight {pw.K}")
     bias = _bias(bias, N)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        out = x.new_empty(M, N)
     elif out.dtype != torch.bfloat16 or tuple(out.shape) != (M, N) or out.stride(1) != 1 or out.stride(0) < N:
         raise ValueError(f"out must be bfloat16 [{M}, {N}] with contiguous rows that do not overlap")
     _same_device(x2, pw.w_packed, bias, out, workspace)
     with _on(x.device):
         need = _bytes("mxfp8_linear_b128_workspace_bytes", M, N, K)
-        ws = workspace if workspace is not None else _scratch(need, x.device)
+        ws = workspace if workspace is not None else _scratch(need, x)
         _check(lib().mxfp8_linear_b128(_ptr(x2), M, K, x2.stride(0), _ptr(pw.w_packed), _ptr(pw.s_packed), N,
                                        _ptr(bias), _ptr(out), out.stride(0), _ptr(ws), 0 if ws is None else ws.numel(),
                                        _stream(x.device)), "mxfp8_linear_b128")
@@ -756,12 +756,12 @@ def linear_wgrad(dy, pa, dtype=torch.float32, bias_grad=False, out=None, out_bia
     if accumulate and (out is None or (bias_grad and out_bias is None)):
         raise ValueError("accumulate needs the tensors to add to")
     if out is None:
-        out = torch.empty((N, pa.K), dtype=dtype, device=dy.device)
+        out = d2.new_empty((N, pa.K), dtype=dtype)
     if tuple(out.shape) != (N, pa.K) or out.dtype not in _DTYPES or out.stride(-1) != 1:
         raise ValueError(f"out must be float32 or bfloat16 [{N}, {pa.K}] with contiguous rows")
     db = None
     if bias_grad:
-        db = out_bias if out_bias is not None else torch.empty(N, dtype=torch.float32, device=dy.device)
+        db = out_bias if out_bias is not None else d2.new_empty(N, dtype=torch.float32)
         if db.dtype not in _DTYPES or tuple(db.shape) != (N,) or not db.is_contiguous():
             raise ValueError(f"out_bias must be contiguous float32 or bfloat16 [{N}]")
     if accumulate and (out.dtype != torch.float32 or (db is not None and db.dtype != torch.float32)):
@@ -769,7 +769,7 @@ def linear_wgrad(dy, pa, dtype=torch.float32, bias_grad=False, out=None, out_bia
     _same_device(d2, pa.q_packed, out, db)
     with _on(dy.device):
         need = _bytes("mxfp8_linear_wgrad_workspace_bytes", M, N, pa.K)
-        ws = _scratch(need, dy.device)
+        ws = _scratch(need, d2)
         _check(lib().mxfp8_linear_wgrad(_ptr(d2), M, N, d2.stride(0), _ptr(pa.q_packed), _ptr(pa.s_packed), pa.K,
                                         _ptr(out), _DTYPES[out.dtype], out.stride(0), _ptr(db),
                                         0 if db is None else _DTYPES[db.dtype], int(accumulate), _ptr(ws), need,
@@ -791,10 +791,10 @@ def _linear_b128_forward(x, w, bias, keep):
     keeps what MXFP8_KEEP_DX (1) and MXFP8_KEEP_DW (2) in ``keep`` ask for."""
     x2, w2, bias = _rows(x, "x"), _rows(w, "w"), _bias(bias, w.shape[0])
     (M, K), N, d = x2.shape, w2.shape[0], x.device
-    y = torch.empty((M, N), dtype=torch.bfloat16, device=d)
+    y = x.new_empty(M, N)
     with _on(d):
         kept_bytes, ws_bytes, back_bytes = _layer_bytes(M, N, K, keep)
-        kept, ws = _scratch(kept_bytes, d), _scratch(ws_bytes, d)
+        kept, ws = _scratch(kept_bytes, y), _scratch(ws_bytes, y)
         _check(lib().mxfp8_linear_b128_forward(_ptr(x2), M, K, x2.stride(0), _ptr(w2), N, w2.stride(0), _ptr(bias),
                                                _ptr(y), N, keep, _ptr(kept), _ptr(ws), ws_bytes, _stream(d)),
                "mxfp8_linear_b128_forward")
@@ -841,12 +841,11 @@ class _LinearB128(torch.autograd.Function):
         _check_capture(ctx, _stream(d), torch.cuda.is_current_stream_capturing())
         d2 = _rows(dy, "dy")
         (M, N), K = d2.shape, ctx.shape[-1]
-        new = functools.partial(torch.empty, dtype=torch.bfloat16, device=d)
-        dx = new((M, K)) if need_x else None
-        dw = new((N, K)) if need_w or need_b else None
-        db = new(N) if need_b else None
+        dx = d2.new_empty(M, K) if need_x else None
+        dw = d2.new_empty(N, K) if need_w or need_b else None
+        db = d2.new_empty(N) if need_b else None
         with _on(d):
-            ws = _scratch(ctx.ws_bytes, d)
+            ws = _scratch(ctx.ws_bytes, d2)
             _check(lib().mxfp8_linear_b128_backward(_ptr(d2), M, N, d2.stride(0), K, ctx.keep, _ptr(kept), _ptr(dx), K,
                                                     _ptr(dw), 1, K, _ptr(db), 1, _ptr(ws), ctx.ws_bytes, _stream(d)),
                    "mxfp8_linear_b128_backward")
@@ -1005,11 +1004,11 @@ def moe_balance(logits, topk, valid=None, coef=1e-2, z_coef=0.0):
     T, E = logits.shape
     d = logits.device
     with _on(d):
-        loss = torch.empty((), dtype=torch.float32, device=d)
-        counts = torch.empty(E, dtype=torch.int32, device=d)
-        used = torch.empty(1, dtype=torch.int32, device=d)
+        loss = logits.new_empty((), dtype=torch.float32)
+        counts = logits.new_empty(E, dtype=torch.int32)
+        used = logits.new_empty(1, dtype=torch.int32)
         need = _bytes("mxfp8_moe_balance_workspace_bytes", T, E)
-        ws = _scratch(need, d)
+        ws = _scratch(need, counts)
         _check(lib().mxfp8_moe_balance(_ptr(logits), _DTYPES[logits.dtype], T, E, logits.stride(0), topk,
                                        _ptr(valid), coef, z_coef, _ptr(loss), _ptr(counts), _ptr(used), _ptr(ws),
                                        need, _stream(d)), "mxfp8_moe_balance")
@@ -1030,7 +1029,7 @@ def moe_balance_backward(logits, topk, counts, used, valid=None, coef=1e-2, z_co
     counts = counts.contiguous()
     _same_device(logits, counts, used, grad)
     with _on(logits.device):
-        d = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+        d = logits.new_empty(T, E)
         _check(lib().mxfp8_moe_balance_backward(_ptr(logits), _DTYPES[logits.dtype], T, E, logits.stride(0), topk,
                                                 _ptr(valid), coef, z_coef, _ptr(counts), _ptr(used), _ptr(grad),
                                                 _ptr(d), E, _stream(logits.device)), "mxfp8_moe_balance_backward")
