@@ -292,7 +292,7 @@ const char* mxfp8_status_string(int status) {
   switch (status) {
     case MXFP8_OK: return "ok";
     case MXFP8_E_NULLPTR: return "a required pointer is NULL";
-    case MXFP8_E_SHAPE: return "invalid shape (sizes must be non-negative, K % 32 == 0 for quantize, K % 256 == 0 and N >= 1 for the GEMM)";
+    case MXFP8_E_SHAPE: return "invalid shape (sizes must be non-negative, K % 32 == 0 for quantize, K % 256 == 0 and N >= 1 for the GEMM; 128-block entries: K % 16 == 0, N % 16 == 0 where it is summed over)";
     case MXFP8_E_ALIGN: return "pointer misaligned (see mxfp8.h for each argument's alignment)";
     case MXFP8_E_LD: return "leading dimension too small or not a required multiple";
     case MXFP8_E_WORKSPACE: return "workspace missing or smaller than mxfp8_linear_workspace_bytes";
