@@ -68,17 +68,17 @@ std::atomic<int> g_force_mt{0}, g_force_wgrad{0};
 //   M = 4096  100   90   69   59
 // All four forms move 10 to 20 TB/s from L2 into LDS, so the bytes a tile
 // reads for its products decide, where there are tiles for all compute units.
-mxfp8::B128Plan b128_plan(int64_t M, int64_t N, int64_t K) {
+mxfp8::B128Plan b128_plan(int64_t M, int64_t N, int64_t K, int force, double* us) {
   const int64_t G = b128_blocks(N), KB = b128_blocks(K), GM = b128_blocks(M);
-  const int force = g_force_mt.load(std::memory_order_relaxed);
   // the larger forms write whole 16-byte pieces and address a tile's rows with 32 bits
   const bool whole = N % 8 == 0 && N <= ((int64_t)1 << 22);
   mxfp8::B128Plan best = {64, 1};
   double best_us = 1e30;
-  auto offer = [&](int mt, int splits, double us) {
-    if (us < best_us) {
-      best_us = us;
+  auto offer = [&](int mt, int splits, double t) {
+    if (t < best_us) {
+      best_us = t;
       best = {mt, splits};
+      if (us) *us = t;
     }
   };
   auto join = [&](int s) { return s > 1 ? 3.0 + (double)s * (double)M * (double)N * 8.0 / 4e6 : 0.0; };
@@ -96,6 +96,25 @@ mxfp8::B128Plan b128_plan(int64_t M, int64_t N, int64_t K) {
   if (wanted(256)) offer(256, 1, 5.0 + (large <= 128 ? 0.75 : 0.95 * (double)((large + 255) / 256)) * blocks(1));
   if (wanted(512)) offer(512, 1, 5.0 + (wide <= 128 ? 1.25 : 1.7 * (double)((wide + 255) / 256)) * blocks(1));
   return best;
+}
+
+mxfp8::B128Plan b128_plan(int64_t M, int64_t N, int64_t K) {
+  return b128_plan(M, N, K, g_force_mt.load(std::memory_order_relaxed), nullptr);
+}
+
+// The training step's weights are quantized from bf16, so their scales are
+// powers of two and the scaled MFMA can apply them as well.  Where its 256 x
+// 256 tiles are faster than the forms above, the step's GEMMs take the MXFP8
+// tile GEMM, which has no v_fma: the same kind of line, measured with them
+// (8192 x 4096 x 4096: 100 us against 116; 4096^3: 52, 62; 4096 x 2048 x 2048:
+// 27, 25).  By the sizes alone: the forward call lays out scales that the
+// backward call reads.
+bool mx_gemm(int64_t M, int64_t N, int64_t K) {
+  if (M <= mxfp8::kB128DecodeMaxM || K % 256 != 0) return false;
+  double us = 0.0;
+  b128_plan(M, N, K, 0, &us);
+  const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
+  return 5.0 + (tiles <= 128 ? 1.1 : 1.42 * (double)((tiles + 255) / 256)) * (double)b128_blocks(K) < us;
 }
 
 constexpr int64_t kRuns = 256;   // compute units
@@ -162,6 +181,10 @@ size_t linear_ws(int64_t M, int64_t N, int64_t K) {
          part_bytes(M, N, b128_plan(M, N, K));
 }
 
+size_t weight_scale_bytes(int64_t N, int64_t K, bool mx) {
+  return mx ? act_scale_bytes(N, K) : (size_t)b128_blocks(N) * b128_blocks(K) * 4;
+}
+
 // What the layer's forward call keeps for its backward call: the transposed
 // prepared weight (MXFP8_KEEP_DX), then the packed activations (MXFP8_KEEP_DW).
 struct Kept {
@@ -177,7 +200,7 @@ size_t kept_layout(int64_t M, int64_t N, int64_t K, int keep, uint8_t* base, Kep
   const bool dx = keep & MXFP8_KEEP_DX, dw = (keep & MXFP8_KEEP_DW) && M > 0;
   Kept v;
   v.wt = take(dx, act_bytes(K, N));
-  v.st = take(dx, (size_t)b128_blocks(N) * b128_blocks(K) * 4);
+  v.st = take(dx, weight_scale_bytes(K, N, mx_gemm(M, K, N)));
   v.q = take(dw, act_bytes(M, K));
   v.s = take(dw, act_scale_bytes(M, K));
   if (k) *k = v;
@@ -186,8 +209,8 @@ size_t kept_layout(int64_t M, int64_t N, int64_t K, int keep, uint8_t* base, Kep
 
 // Forward workspace: the prepared weight and its scales, then the GEMM's
 // (activations that are not kept, partials).
-size_t forward_weight_bytes(int64_t N, int64_t K) {
-  return round_up(act_bytes(N, K), 256) + round_up((size_t)b128_blocks(N) * b128_blocks(K) * 4, 256);
+size_t forward_weight_bytes(int64_t M, int64_t N, int64_t K) {
+  return round_up(act_bytes(N, K), 256) + round_up(weight_scale_bytes(N, K, mx_gemm(M, N, K)), 256);
 }
 
 int check_layer(int64_t M, int64_t N, int64_t K, int keep) {
@@ -289,7 +312,7 @@ int mxfp8_quantize_weight_b128(const void* w_bf16, int64_t N, int64_t K, int64_t
   if (!tiles_ok(N, K)) return MXFP8_E_SHAPE;
   if (int st = mxfp8::check_device_current()) return st;
   return mxfp8::launch_quantize_weight_b128(w_bf16, N, K, ldw, q_e4m3, ldq, s, lds, w_packed, s_packed, wt_packed,
-                                            st_packed, (hipStream_t)stream);
+                                            st_packed, 0, (hipStream_t)stream);
 }
 
 int mxfp8_linear_b128_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes) {
@@ -420,7 +443,7 @@ int mxfp8_linear_b128_layer_bytes(int64_t M, int64_t N, int64_t K, int keep, siz
   size_t fwd = 0;
   if (M > 0 && (keep & MXFP8_KEEP_DW)) mxfp8_gemm_packed_b128_workspace_bytes(M, N, K, &fwd);
   else if (M > 0) mxfp8_linear_b128_workspace_bytes(M, N, K, &fwd);
-  *forward_ws_bytes = forward_weight_bytes(N, K) + fwd;
+  *forward_ws_bytes = forward_weight_bytes(M, N, K) + fwd;
   // the two products of the backward call run one after the other
   size_t dx = 0, dw = 0;
   if (keep & MXFP8_KEEP_DX) mxfp8_linear_b128_workspace_bytes(M, K, N, &dx);
@@ -447,15 +470,23 @@ int mxfp8_linear_b128_forward(const void* x_bf16, int64_t M, int64_t K, int64_t 
   kept_layout(M, N, K, keep, (uint8_t*)kept, &k);
   uint8_t* wp = (uint8_t*)workspace;
   uint8_t* sp = wp + round_up(act_bytes(N, K), 256);
-  uint8_t* rest = wp + forward_weight_bytes(N, K);
-  const size_t rest_bytes = workspace_bytes - forward_weight_bytes(N, K);
-  if (int st = mxfp8_quantize_weight_b128(w_bf16, N, K, ldw, nullptr, 0, nullptr, 0, wp, sp, k.wt, k.st, stream))
+  uint8_t* rest = wp + forward_weight_bytes(M, N, K);
+  const size_t rest_bytes = workspace_bytes - forward_weight_bytes(M, N, K);
+  const bool mx = mx_gemm(M, N, K), mx_dx = k.wt != nullptr && mx_gemm(M, K, N);
+  if (int st = mxfp8::check_device_current()) return st;
+  hipStream_t s = (hipStream_t)stream;
+  if (int st = mxfp8::launch_quantize_weight_b128(w_bf16, N, K, ldw, nullptr, 0, nullptr, 0, wp, sp, k.wt, k.st,
+                                                  (mx ? 1 : 0) | (mx_dx ? 2 : 0), s))
     return st;
   if (M == 0) return MXFP8_OK;
-  if (!(keep & MXFP8_KEEP_DW))
+  const bool dw = keep & MXFP8_KEEP_DW;
+  if (!dw && !mx)
     return mxfp8_linear_b128(x_bf16, M, K, ldx, wp, sp, N, bias_bf16, y_bf16, ldy, rest, rest_bytes, stream);
-  if (int st = mxfp8_quantize_act_packed_b128(x_bf16, M, K, ldx, k.q, k.s, stream)) return st;
-  return mxfp8_gemm_packed_b128(k.q, k.s, M, K, wp, sp, N, bias_bf16, y_bf16, ldy, rest, rest_bytes, stream);
+  uint8_t* q = dw ? k.q : rest;
+  uint8_t* qs = dw ? k.s : rest + round_up(act_bytes(M, K), 256);
+  if (int st = mxfp8_quantize_act_packed_b128(x_bf16, M, K, ldx, q, qs, stream)) return st;
+  if (mx) return mxfp8::launch_gemm_tile(q, qs, M, K, wp, sp, N, bias_bf16, y_bf16, ldy, s);
+  return mxfp8_gemm_packed_b128(q, qs, M, K, wp, sp, N, bias_bf16, y_bf16, ldy, rest, rest_bytes, stream);
 }
 
 int mxfp8_linear_b128_backward(const void* dy_bf16, int64_t M, int64_t N, int64_t lddy, int64_t K, int keep,
@@ -485,6 +516,12 @@ int mxfp8_linear_b128_backward(const void* dy_bf16, int64_t M, int64_t N, int64_
       return st;
   }
   if (!dx_bf16 || M == 0) return MXFP8_OK;
+  if (mx_gemm(M, K, N)) {
+    uint8_t* q = (uint8_t*)workspace;
+    uint8_t* qs = q + round_up(act_bytes(M, N), 256);
+    if (int st = mxfp8_quantize_act_packed_b128(dy_bf16, M, N, lddy, q, qs, stream)) return st;
+    return mxfp8::launch_gemm_tile(q, qs, M, N, k.wt, k.st, K, nullptr, dx_bf16, lddx, (hipStream_t)stream);
+  }
   return mxfp8_linear_b128(dy_bf16, M, N, lddy, k.wt, k.st, K, nullptr, dx_bf16, lddx, workspace, workspace_bytes,
                            stream);
 }

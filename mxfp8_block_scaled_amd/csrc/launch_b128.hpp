@@ -25,9 +25,10 @@ int launch_dequantize_packed(const void* qp, const void* sp, int64_t M, int64_t 
 int launch_pack_b128(const void* w, const void* ws, int64_t N, int64_t K, int64_t ldw, int64_t ldws, int transpose,
                      void* wp, void* sp, hipStream_t stream);
 // bf16 weight [N, K] -> any of row-major (q, s), packed (wp, sp) and packed
-// transposed (wtp, stp); null outputs are skipped.
+// transposed (wtp, stp); null outputs are skipped.  mx: bit 0 / 1: sp / stp in
+// the MX format's scale tiles (N_pad K_pad / 32 bytes), for launch_gemm_tile.
 int launch_quantize_weight_b128(const void* w, int64_t N, int64_t K, int64_t ldw, void* q, int64_t ldq, void* s,
-                                int64_t lds, void* wp, void* sp, void* wtp, void* stp, hipStream_t stream);
+                                int64_t lds, void* wp, void* sp, void* wtp, void* stp, int mx, hipStream_t stream);
 
 // Decode GEMM: M <= 16 bf16 rows, quantized inside, against the packed weight.
 constexpr int64_t kB128DecodeMaxM = 16;

@@ -228,14 +228,17 @@ int launch_pack_b128(const void* w, const void* ws, int64_t N, int64_t K, int64_
 
 // bf16 [N, K] -> any of: row-major bytes (q) and scales (s); packed W
 // (wp, sp); packed W^T (wtp, stp).  Null outputs are skipped.  One read of
-// the weight serves them all.  HBM-bound: 4096 x 4096 to both packed forms
+// the weight serves them all.  mx: bit 0 / 1: sp / stp is in the scale tiles
+// of the MX format instead of one fp32 per block: the block's two tiles hold
+// its byte throughout.  HBM-bound: 4096 x 4096 to both packed forms
 // 16 us (4.2 TB/s).
 __global__ __launch_bounds__(256) void quant_weight_b128_kernel(const uint16_t* __restrict__ w, int64_t ldw, int64_t N,
                                                                 int64_t K, int64_t NB, int64_t KB,
                                                                 uint8_t* __restrict__ q, int64_t ldq,
                                                                 float* __restrict__ s, int64_t lds,
-                                                                uint8_t* __restrict__ wp, float* __restrict__ sp,
-                                                                uint8_t* __restrict__ wtp, float* __restrict__ stp) {
+                                                                uint8_t* __restrict__ wp, void* __restrict__ sp,
+                                                                uint8_t* __restrict__ wtp, void* __restrict__ stp,
+                                                                int mx) {
   __shared__ __attribute__((aligned(16))) uint8_t t[128 * kTilePitch];
   __shared__ uint32_t wmax[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -272,8 +275,13 @@ __global__ __launch_bounds__(256) void quant_weight_b128_kernel(const uint16_t* 
   }
   if (tid == 0) {
     if (s != nullptr) s[nb * lds + kb] = scale;
-    if (wp != nullptr) sp[nb * KB + kb] = scale;
-    if (wtp != nullptr) stp[kb * NB + nb] = scale;
+    if (wp != nullptr && !(mx & 1)) ((float*)sp)[nb * KB + kb] = scale;
+    if (wtp != nullptr && !(mx & 2)) ((float*)stp)[kb * NB + nb] = scale;
+  }
+  if (tid < 2 * kTileScaleBytes / 4) {
+    const uint32_t four = sb * 0x01010101u;
+    if (wp != nullptr && (mx & 1)) ((uint32_t*)sp)[(nb * KB + kb) * (2 * kTileScaleBytes / 4) + tid] = four;
+    if (wtp != nullptr && (mx & 2)) ((uint32_t*)stp)[(kb * NB + nb) * (2 * kTileScaleBytes / 4) + tid] = four;
   }
   if (wp == nullptr && wtp == nullptr) return;
   __syncthreads();
@@ -282,11 +290,10 @@ __global__ __launch_bounds__(256) void quant_weight_b128_kernel(const uint16_t* 
 }
 
 int launch_quantize_weight_b128(const void* w, int64_t N, int64_t K, int64_t ldw, void* q, int64_t ldq, void* s,
-                                int64_t lds, void* wp, void* sp, void* wtp, void* stp, hipStream_t stream) {
+                                int64_t lds, void* wp, void* sp, void* wtp, void* stp, int mx, hipStream_t stream) {
   const int64_t NB = b128_blocks(N), KB = b128_blocks(K);
   hipLaunchKernelGGL(quant_weight_b128_kernel, dim3((unsigned)(NB * KB)), dim3(256), 0, stream, (const uint16_t*)w,
-                     ldw, N, K, NB, KB, (uint8_t*)q, ldq, (float*)s, lds, (uint8_t*)wp, (float*)sp, (uint8_t*)wtp,
-                     (float*)stp);
+                     ldw, N, K, NB, KB, (uint8_t*)q, ldq, (float*)s, lds, (uint8_t*)wp, sp, (uint8_t*)wtp, stp, mx);
   return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 

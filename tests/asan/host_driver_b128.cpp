@@ -20,7 +20,7 @@
 #include "mxfp8.h"
 
 namespace {
-int g_fail = 0, g_launches = 0;
+int g_fail = 0, g_launches = 0, g_mx = 0;
 volatile uint8_t g_sink;
 #define CHECK(cond)                                                          \
   do {                                                                       \
@@ -107,7 +107,7 @@ int launch_pack_b128(const void* w, const void* ws, int64_t N, int64_t K, int64_
   return 0;
 }
 int launch_quantize_weight_b128(const void* w, int64_t N, int64_t K, int64_t ldw, void* q, int64_t ldq, void* s,
-                                int64_t lds, void* wp, void* sp, void* wtp, void* stp, hipStream_t) {
+                                int64_t lds, void* wp, void* sp, void* wtp, void* stp, int mx, hipStream_t) {
   ++g_launches;
   read_rows(w, N, K, ldw, 2);
   if (q) {
@@ -116,11 +116,11 @@ int launch_quantize_weight_b128(const void* w, int64_t N, int64_t K, int64_t ldw
   }
   if (wp) {
     fill(wp, packed(N, K), kWeight);
-    fill(sp, wscales(N, K), kWeightScale);
+    fill(sp, mx & 1 ? packed(N, K) / 32 : wscales(N, K), kWeightScale);
   }
   if (wtp) {
     fill(wtp, packed(N, K), kWeightT);
-    fill(stp, wscales(N, K), kWeightTScale);
+    fill(stp, mx & 2 ? packed(N, K) / 32 : wscales(N, K), kWeightTScale);
   }
   return 0;
 }
@@ -150,6 +150,19 @@ int launch_gemm_b128_tile(const void* qp, const void* sp, int64_t M, int64_t K, 
   if (plan.splits > 1) fill(part, (size_t)plan.splits * M * ((N + 3) / 4 * 4) * 4, kPart);
   CHECK(holds(qp, packed(M, K), kAct) && holds(sp, packed(M, K) / 32, kActScale));
   CHECK(weight_ok(wp, wsc, N, K));
+  if (bias) read_rows(bias, 1, N, N, 2);
+  fill_rows(y, M, N, ldy, 2);
+  return 0;
+}
+int launch_gemm_tile(const void* qp, const void* sp, int64_t M, int64_t K, const void* wp, const void* wsp, int64_t N,
+                     const void* bias, void* y, int64_t ldy, hipStream_t, int splits, void*) {
+  ++g_launches;
+  ++g_mx;
+  CHECK(K % 256 == 0 && splits == 1);
+  const size_t w = packed(N, K);
+  CHECK(holds(qp, packed(M, K), kAct) && holds(sp, packed(M, K) / 32, kActScale));
+  CHECK((holds(wp, w, kWeight) && holds(wsp, w / 32, kWeightScale)) ||
+        (holds(wp, w, kWeightT) && holds(wsp, w / 32, kWeightTScale)));
   if (bias) read_rows(bias, 1, N, N, 2);
   fill_rows(y, M, N, ldy, 2);
   return 0;
@@ -339,6 +352,15 @@ int main() {
   for (const auto& s : layer)
     for (int keep = 0; keep < 4; ++keep)
       for (int dtype : {MXFP8_F32, MXFP8_BF16}) layer_case(s[0], s[1], s[2], keep, dtype);
+  // both products, one of them, on the MXFP8 GEMM, the choice not the hook's
+  for (int force : {0, 64}) {
+    const int prev = mxfp8_debug_force_b128(force), before = g_mx;
+    for (int keep = 0; keep < 4; ++keep) layer_case(4096, 4096, 256, keep, MXFP8_BF16);
+    CHECK(g_mx == before + 4);
+    layer_case(8192, 2048, 2048, 3, MXFP8_BF16);
+    CHECK(g_mx == before + 6);
+    mxfp8_debug_force_b128(prev);
+  }
   for (int64_t T : {0, 1, 16, 5000})
     for (int64_t E : {1, 8, 130, 256})
       for (int dtype : {MXFP8_F32, MXFP8_BF16})
