@@ -393,7 +393,8 @@ typedef enum { MXFP8_F32 = 0, MXFP8_BF16 = 1 } mxfp8_dtype;
  *   scale is its transpose's.  Outputs 256-byte aligned, of
  *   mxfp8_prepared_weight_b128_bytes(N, K), or (K, N) if transposed.
  * mxfp8_linear_b128: arguments as mxfp8_linear, workspace of
- *   mxfp8_linear_b128_workspace_bytes (0 for M <= 16: NULL is fine then).
+ *   mxfp8_linear_b128_workspace_bytes (0 for few rows of a weight that is not
+ *   large: NULL is fine then).
  * mxfp8_gemm_packed_b128: the GEMM alone on activations of
  *   mxfp8_quantize_act_packed_b128; workspace of
  *   mxfp8_gemm_packed_b128_workspace_bytes (fp32 partials where K is split).
@@ -424,7 +425,7 @@ int mxfp8_gemm_packed_b128(const void* q_packed, const void* s_packed, int64_t M
 
 /*
  * Test hook: pin the tiles of the 128-block GEMM (M > 16 and the packed
- * entry): 0 = by shape, 64 / 128 = 128 weight rows x that many activation
+ * entry; not the training step's products that the MXFP8 GEMM runs): 0 = by shape, 64 / 128 = 128 weight rows x that many activation
  * rows (with K splits), 256 / 512 = 256 x 128 / 256 x 256.  All but 64 need
  * N % 8 == 0, and y 16-byte aligned with ldy % 8 == 0 where K is not split;
  * else the 64-row tiles run.  The workspace queries follow it.  Process-wide;

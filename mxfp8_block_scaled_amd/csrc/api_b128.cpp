@@ -98,6 +98,22 @@ mxfp8::B128Plan b128_plan(int64_t M, int64_t N, int64_t K, int force, double* us
   return best;
 }
 
+// Few rows: one launch that quantizes inside, without a workspace, or the
+// quantizer and a tile form.  Lines through measurements (us; M 1 .. 32, N 512
+// .. 28672, K 2048 .. 16384): every decode workgroup (16 weight rows) converts
+// all activations, the second group of 16 rows costs a turn more; the tile
+// forms read the weight faster but start later.  For example, decode and tile:
+// 16 x 4096 x 4096 6.6, 12; 32 x 4096 x 4096 9.8, 13; 8 x 8192 x 8192 16.5, 19;
+// 16 x 8192 x 8192 21.6, 19; 1 x 28672 x 8192 41, 37; 16 rows of it 66, 37.
+bool decode_form(int64_t M, int64_t N, int64_t K) {
+  if (M > mxfp8::kB128DecodeMaxM) return false;
+  if (M > 16 && g_force_mt.load(std::memory_order_relaxed) != 0) return false;
+  const double wgs = (double)((N + 15) / 16), weight = (double)N * (double)K;
+  const double decode = 3.0 + weight / 6.2e6 + 1.25e-7 * (double)(M - 1) * std::max(wgs, 256.0) * (double)K +
+                        (M > 16 ? 0.8 * std::max(1.0, wgs / 256.0) : 0.0);
+  return decode <= 10.0 + weight / 8.5e6;
+}
+
 mxfp8::B128Plan b128_plan(int64_t M, int64_t N, int64_t K) {
   return b128_plan(M, N, K, g_force_mt.load(std::memory_order_relaxed), nullptr);
 }
@@ -176,7 +192,7 @@ size_t part_bytes(int64_t M, int64_t N, mxfp8::B128Plan p) {
 }
 
 size_t linear_ws(int64_t M, int64_t N, int64_t K) {
-  if (M <= mxfp8::kB128DecodeMaxM) return 0;
+  if (decode_form(M, N, K)) return 0;
   return round_up(act_bytes(M, K), 256) + round_up(act_scale_bytes(M, K), 256) +
          part_bytes(M, N, b128_plan(M, N, K));
 }
@@ -339,7 +355,7 @@ int mxfp8_linear_b128(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, con
   if (int st = mxfp8::check_device_current()) return st;
   hipStream_t s = (hipStream_t)stream;
   const float* wsc = (const float*)s_packed;
-  if (M <= mxfp8::kB128DecodeMaxM)
+  if (decode_form(M, N, K))
     return mxfp8::launch_gemm_b128_decode(x_bf16, ldx, M, K, w_packed, wsc, N, bias_bf16, y_bf16, ldy, s);
   uint8_t* q = (uint8_t*)workspace;
   uint8_t* sc = q + round_up(act_bytes(M, K), 256);

@@ -30,8 +30,8 @@ int launch_pack_b128(const void* w, const void* ws, int64_t N, int64_t K, int64_
 int launch_quantize_weight_b128(const void* w, int64_t N, int64_t K, int64_t ldw, void* q, int64_t ldq, void* s,
                                 int64_t lds, void* wp, void* sp, void* wtp, void* stp, int mx, hipStream_t stream);
 
-// Decode GEMM: M <= 16 bf16 rows, quantized inside, against the packed weight.
-constexpr int64_t kB128DecodeMaxM = 16;
+// Decode GEMM: M <= 32 bf16 rows, quantized inside, against the packed weight.
+constexpr int64_t kB128DecodeMaxM = 32;
 int launch_gemm_b128_decode(const void* x, int64_t ldx, int64_t M, int64_t K, const void* wp, const float* wsc,
                             int64_t N, const void* bias, void* y, int64_t ldy, hipStream_t stream);
 

@@ -302,3 +302,47 @@ def test_many_tiles_per_workgroup():
     assert torch.equal(y[128], y[256]) and torch.equal(y[128], y[512])    # the same blocks in the same order
     rows = torch.arange(0, M, 97)
     check_linear(x[rows], wq, ws, bias.cpu(), y[256][rows.to(dev())])
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 28672, 1040), (9, 300, 2048), (16, 40, 2064), (17, 1, 16), (18, 130, 2048),
+                                   (24, 515, 2064), (32, 4000, 4096), (31, 100, 8208), (32, 264, 16400), (25, 16400, 2048),
+                                   (32, 70000, 1024), (16, 70000, 4096)])
+def test_few_rows(M, N, K):
+    """One and two groups of sixteen rows, turns of one, two and four blocks,
+    and sizes whose few rows take the tiles."""
+    x = spiky(M, K, M + K)
+    wq, ws = make_weight(N, K, N)
+    bias = randn((N,), 4)
+    pw = api.prepare_weight_b128(wq.to(dev()), ws.to(dev()))
+    y = api.linear(x.to(dev()), pw, bias.to(dev()))
+    check_linear(x, wq, ws, bias, y)
+    assert torch.equal(y, api.linear(x.to(dev()), pw, bias.to(dev())))
+    # strides, and the surroundings of y
+    wide = torch.full((M + 2, N + 13), 7.0, dtype=torch.bfloat16, device=dev())
+    xs = torch.zeros(M, K + 24, dtype=torch.bfloat16, device=dev())
+    xs[:, 8:8 + K] = x.to(dev())
+    api.linear(xs[:, 8:8 + K], pw, bias.to(dev()), out=wide[1:1 + M, 5:5 + N])
+    assert torch.equal(wide[1:1 + M, 5:5 + N], y)
+    wide[1:1 + M, 5:5 + N] = 7.0
+    assert bool((wide == 7.0).all())
+
+
+@pytest.mark.parametrize("M", [20, 32])
+def test_two_row_groups_place_every_element(M):
+    """One-hot weights: y[m, n] is one dequantized activation."""
+    K = N = 272
+    x = spiky(M, K, 3)
+    q = torch.eye(N).to(torch.float8_e4m3fn).view(torch.uint8)
+    pw = api.prepare_weight_b128(q.to(dev()), torch.ones(3, 3, device=dev()))
+    _, _, A = ref.quantize(f64(x))
+    assert np.array_equal(f64(api.linear(x.to(dev()), pw)), A)
+
+
+def test_non_finite_rows_of_two_groups():
+    x = randn((30, 512), 1)
+    x[3, 5], x[20, 300] = float("inf"), float("nan")
+    wq, ws = make_weight(64, 512, 2)
+    y = api.linear(x.to(dev()), api.prepare_weight_b128(wq.to(dev()), ws.to(dev()))).cpu()
+    bad = torch.zeros(30, dtype=torch.bool)
+    bad[[3, 20]] = True
+    assert torch.isnan(y[bad]).all() and torch.isfinite(y[~bad]).all()
