@@ -100,18 +100,20 @@ mxfp8::B128Plan b128_plan(int64_t M, int64_t N, int64_t K, int force, double* us
 
 // Few rows: one launch that quantizes inside, without a workspace, or the
 // quantizer and a tile form.  Lines through measurements (us; M 1 .. 32, N 512
-// .. 28672, K 2048 .. 16384): every decode workgroup (16 weight rows) converts
-// all activations, the second group of 16 rows costs a turn more; the tile
-// forms read the weight faster but start later.  For example, decode and tile:
-// 16 x 4096 x 4096 6.6, 12; 32 x 4096 x 4096 9.8, 13; 8 x 8192 x 8192 16.5, 19;
-// 16 x 8192 x 8192 21.6, 19; 1 x 28672 x 8192 41, 37; 16 rows of it 66, 37.
+// .. 28672, K 2048 .. 16384): a decode workgroup (16 weight rows) converts all
+// activations, a second group of 16 rows costs another pass; the tile forms
+// read the weight faster but start later.  For example, decode and tiles: 16 x
+// 4096 x 4096 6.2, 12; 32 x 4096 x 4096 9.3, 13; 12 x 8192 x 8192 15.3, 19; 32
+// x 8192 x 8192 29, 20; 1 x 28672 x 8192 38, 38; 16 rows of it 54, 38.
 bool decode_form(int64_t M, int64_t N, int64_t K) {
   if (M > mxfp8::kB128DecodeMaxM) return false;
   if (M > 16 && g_force_mt.load(std::memory_order_relaxed) != 0) return false;
-  const double wgs = (double)((N + 15) / 16), weight = (double)N * (double)K;
-  const double decode = 3.0 + weight / 6.2e6 + 1.25e-7 * (double)(M - 1) * std::max(wgs, 256.0) * (double)K +
-                        (M > 16 ? 0.8 * std::max(1.0, wgs / 256.0) : 0.0);
-  return decode <= 10.0 + weight / 8.5e6;
+  double tile = 0.0;
+  b128_plan(std::max<int64_t>(M, 1), N, K, 0, &tile);
+  const double weight = (double)N * (double)K, rounds = std::max(1.0, (double)((N + 15) / 16) / 256.0);
+  tile = std::max(tile, 4.5 + weight / 8e6) + 3.0;
+  const double convert = 256.0 * rounds * (double)K * (1.17e-6 + 1.45e-7 * (double)M + (M > 16 ? 5.5e-7 : 0.0));
+  return 3.0 + std::max(weight / 6.5e6, convert + 0.5 * (rounds - 1.0)) <= tile;
 }
 
 mxfp8::B128Plan b128_plan(int64_t M, int64_t N, int64_t K) {

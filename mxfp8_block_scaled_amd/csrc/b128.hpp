@@ -30,4 +30,21 @@ __device__ inline void widen16(const uint4& q, float scale, uint4* out) {
   out[1] = make_uint4(d[4], d[5], d[6], d[7]);
 }
 
+// Maximum over the sixteen lanes of a DPP row: quads, then half and whole
+// row mirrors (VALU only).
+__device__ inline uint32_t row16_max(uint32_t m) {
+  m = quad_max(m);
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x141, 0xF, 0xF, true));   // row_half_mirror
+  return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x140, 0xF, 0xF, true));   // row_mirror
+}
+
+__device__ inline uint32_t absmax8(const uint4& v) {
+  u16x2 m = {0, 0};
+  m = absmax_pk(m, v.x);
+  m = absmax_pk(m, v.y);
+  m = absmax_pk(m, v.z);
+  m = absmax_pk(m, v.w);
+  return max((uint32_t)m[0], (uint32_t)m[1]);
+}
+
 }  // namespace mxfp8

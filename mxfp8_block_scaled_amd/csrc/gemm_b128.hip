@@ -32,10 +32,13 @@ __device__ inline float scalar_scale(const float* p, int at) {
 // ---------------------------------------------------------------------------
 // Decode (M <= 32): a workgroup owns 16 weight rows over the whole K, its 16
 // waves one run of 128-blocks each; activations are quantized on the way in.
-// Bound by the weight's bytes (N K) and how many loads are in flight.  The
-// run is walked kSteps blocks at a time, all loads of a turn ahead of its
-// first conversion; the waves' sums meet once, in wave order, through LDS.
-// M = 1, N = K = 4096: 4.7 us (3.5 TB/s); 13 x 4000 x 2064: 6.6 us.
+// Bound by the weight's bytes (N K) and how many loads are in flight; the
+// waves' sums meet once, in wave order, through LDS.  One block at a time: two
+// or four per turn keep half the registers of two workgroups per compute unit
+// busy (16 x 2048 x 2048: 6.2 us against 4.8; 8 x 8192 x 8192: 16.5, 13.7), and
+// so does loading a block ahead (15.5).
+// M = 1, N = K = 4096: 4.6 us (3.6 TB/s); 13 x 4000 x 2064: 5.5 us; 32 x 4096 x
+// 4096: 9.5.
 // ---------------------------------------------------------------------------
 namespace {
 constexpr int kDecWaves = 16;
@@ -43,21 +46,21 @@ constexpr int kDecThreads = 64 * kDecWaves;
 }  // namespace
 
 // kMG groups of sixteen activation rows; a wave stages one at a time.
-template <int kSteps, int kMG>
+template <int kMG>
 struct DecodeLds {
-  static constexpr int kChunksRow = kSteps * 16;    // 16-byte bf16 chunks per row of a turn
-  static constexpr int kPitch = kSteps * 128 + 16;  // staged E4M3 row (+16: rows on distinct banks)
-  static constexpr int kWave = 16 * kPitch + 16 * kSteps;
+  static constexpr int kChunksRow = 16;             // 16-byte bf16 chunks per row of a block
+  static constexpr int kPitch = 128 + 16;           // staged E4M3 row (+16: rows on distinct banks)
+  static constexpr int kWave = 16 * kPitch + 16;
   static constexpr int kRed = kMG * kDecWaves * 64 * 16;
   static constexpr int kBytes = kRed + kDecWaves * kWave;
 };
 
-template <int kSteps, int kMG>
+template <int kMG>
 __global__ __launch_bounds__(kDecThreads) void gemm_b128_decode_kernel(
     const uint16_t* __restrict__ x, int64_t ldx, int M, int64_t K, const uint8_t* __restrict__ wp,
     const float* __restrict__ wsc, int N, const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, int64_t ldy,
     int vec_store) {
-  using L = DecodeLds<kSteps, kMG>;
+  using L = DecodeLds<kMG>;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -81,78 +84,52 @@ __global__ __launch_bounds__(kDecThreads) void gemm_b128_decode_kernel(
   v4f acc[kMG];
 #pragma unroll
   for (int h = 0; h < kMG; ++h) acc[h] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int u0 = kb; u0 < ke; u0 += kSteps) {
-    uint4 xa[kSteps * 4];
+  for (int u = kb; u < ke; ++u) {
+    uint4 xa[4];   // a row group's block: sixteen lanes own a row of it
     auto load_x = [&](int h) {
-      const int total = min(M - 16 * h, 16) * L::kChunksRow;   // a multiple of 16: whole blocks of lanes are in or out
 #pragma unroll
-      for (int q = 0; q < kSteps * 4; ++q) {
+      for (int q = 0; q < 4; ++q) {
         xa[q] = make_uint4(0u, 0u, 0u, 0u);
-        const int c = lane + 64 * q;
-        if (c < total) {
-          const int row = 16 * h + c / L::kChunksRow, col = c % L::kChunksRow;
-          const int64_t k = (int64_t)(u0 + col / 16) * 128 + (col % 16) * 8;
-          if (k < K) xa[q] = *reinterpret_cast<const uint4*>(x + (size_t)row * ldx + k);
-        }
+        const int row = 16 * h + 4 * q + (lane >> 4);
+        const int64_t k = (int64_t)u * 128 + (lane & 15) * 8;
+        if (row < M && k < K) xa[q] = *reinterpret_cast<const uint4*>(x + (size_t)row * ldx + k);
       }
     };
     load_x(0);
-    uint4 w0[kSteps], w1[kSteps];
-    float ws[kSteps];
-#pragma unroll
-    for (int u = 0; u < kSteps; ++u) {
-      const int b = min(u0 + u, KB - 1);   // blocks past the run reload a valid one, times zero elements
-      const uint8_t* wt = wrow + (size_t)(2 * b) * kPieceBytes;
-      w0[u] = *reinterpret_cast<const uint4*>(wt);
-      w1[u] = *reinterpret_cast<const uint4*>(wt + kPieceBytes);
-      ws[u] = scalar_scale(wsg, b);
-    }
-    __builtin_amdgcn_sched_barrier(0);   // every load of the turn above the first conversion
+    const uint8_t* wt = wrow + (size_t)(2 * u) * kPieceBytes;
+    const uint4 w0 = *reinterpret_cast<const uint4*>(wt), w1 = *reinterpret_cast<const uint4*>(wt + kPieceBytes);
+    const float ws = scalar_scale(wsg, u);
+    __builtin_amdgcn_sched_barrier(0);   // every load above the first conversion
 #pragma unroll
     for (int h = 0; h < kMG; ++h) {
-      const int rows = min(M - 16 * h, 16), total = rows * L::kChunksRow;
+      const int rows = min(M - 16 * h, 16);
 #pragma unroll
-      for (int q = 0; q < kSteps * 4; ++q) {
-        if (64 * q < total) {
-          const int c = lane + 64 * q;
-          const int row = c / L::kChunksRow, col = c % L::kChunksRow;
+      for (int q = 0; q < 4; ++q) {
+        if (4 * q < rows) {
+          const int row = 4 * q + (lane >> 4);
           const uint32_t wv[4] = {xa[q].x, xa[q].y, xa[q].z, xa[q].w};
-          u16x2 m = {0, 0};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) m = absmax_pk(m, wv[e]);
-          uint32_t mm = quad_max(max((uint32_t)m[0], (uint32_t)m[1]));
-          mm = max(mm, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)mm, 0x141, 0xF, 0xF, true));
-          mm = max(mm, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)mm, 0x140, 0xF, 0xF, true));
-          const uint32_t sb = b128_scale_byte(mm);
+          const uint32_t sb = b128_scale_byte(row16_max(absmax8(xa[q])));
           uint32_t qv[2];
           cvt8s(wv, mx_scale_value(sb), qv);
-          *reinterpret_cast<uint2*>(xq + row * L::kPitch + col * 8) = make_uint2(qv[0], qv[1]);
-          if ((lane & 15) == 0) xs[row * kSteps + col / 16] = (uint8_t)sb;
+          *reinterpret_cast<uint2*>(xq + row * L::kPitch + (lane & 15) * 8) = make_uint2(qv[0], qv[1]);
+          if ((lane & 15) == 0) xs[row] = (uint8_t)sb;
         }
       }
-      if (h + 1 < kMG) load_x(h + 1);   // on its way during this group's products
+      if (h + 1 < kMG) load_x(h + 1);   // on its way during this group's product
       // One wave's LDS accesses execute in order; this keeps the compiler from
       // moving the reads above the writes, and the next group's writes above these.
       asm volatile("" ::: "memory");
       const int rr = min(i, rows - 1);   // lanes past M repeat the last row; their outputs are dropped
+      const uint8_t* p = xq + rr * L::kPitch + 16 * g;
+      const uint4 b0 = *reinterpret_cast<const uint4*>(p);
+      const uint4 b1 = *reinterpret_cast<const uint4*>(p + 64);
+      const int sx = xs[rr];
+      const v8i xb = {(int)b0.x, (int)b0.y, (int)b0.z, (int)b0.w, (int)b1.x, (int)b1.y, (int)b1.z, (int)b1.w};
+      const v8i wa = {(int)w0.x, (int)w0.y, (int)w0.z, (int)w0.w, (int)w1.x, (int)w1.y, (int)w1.z, (int)w1.w};
+      const v4f part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, xb, v4f{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0,
+                                                                        kUnitScales, 0, sx);
 #pragma unroll
-      for (int u = 0; u < kSteps; ++u) {
-        const uint8_t* p = xq + rr * L::kPitch + u * 128 + 16 * g;
-        const uint4 b0 = *reinterpret_cast<const uint4*>(p);
-        const uint4 b1 = *reinterpret_cast<const uint4*>(p + 64);
-        int sx = xs[rr * kSteps + u];
-        v8i xb = {(int)b0.x, (int)b0.y, (int)b0.z, (int)b0.w, (int)b1.x, (int)b1.y, (int)b1.z, (int)b1.w};
-        if (u0 + u >= ke) {
-          xb = v8i{0, 0, 0, 0, 0, 0, 0, 0};
-          sx = 0;
-        }
-        const v8i wa = {(int)w0[u].x, (int)w0[u].y, (int)w0[u].z, (int)w0[u].w,
-                        (int)w1[u].x, (int)w1[u].y, (int)w1[u].z, (int)w1[u].w};
-        const v4f part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, xb, v4f{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0,
-                                                                          0, kUnitScales, 0, sx);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[h][e] = fmaf(part[e], ws[u], acc[h][e]);
-      }
+      for (int e = 0; e < 4; ++e) acc[h][e] = fmaf(part[e], ws, acc[h][e]);
       asm volatile("" ::: "memory");
     }
   }
@@ -188,14 +165,14 @@ __global__ __launch_bounds__(kDecThreads) void gemm_b128_decode_kernel(
 }
 
 namespace {
-template <int kSteps, int kMG>
+template <int kMG>
 int launch_decode_k(const void* x, int64_t ldx, int64_t M, int64_t K, const void* wp, const float* wsc, int64_t N,
                     const void* bias, void* y, int64_t ldy, hipStream_t stream) {
-  constexpr int lds = DecodeLds<kSteps, kMG>::kBytes;
+  constexpr int lds = DecodeLds<kMG>::kBytes;
   static std::atomic<int> lds_set[kMaxDevices];
-  if (!set_lds_limit_once((const void*)gemm_b128_decode_kernel<kSteps, kMG>, lds, lds_set)) return -7;
+  if (!set_lds_limit_once((const void*)gemm_b128_decode_kernel<kMG>, lds, lds_set)) return -7;
   const int vec = (ldy % 4 == 0) && (((uintptr_t)y & 7) == 0);
-  hipLaunchKernelGGL((gemm_b128_decode_kernel<kSteps, kMG>), dim3((unsigned)((N + 15) / 16)), dim3(kDecThreads), lds,
+  hipLaunchKernelGGL(gemm_b128_decode_kernel<kMG>, dim3((unsigned)((N + 15) / 16)), dim3(kDecThreads), lds,
                      stream, (const uint16_t*)x, ldx, (int)M, K, (const uint8_t*)wp, wsc, (int)N,
                      (const uint16_t*)bias, (uint16_t*)y, ldy, vec);
   return hipGetLastError() == hipSuccess ? 0 : -7;
@@ -204,14 +181,8 @@ int launch_decode_k(const void* x, int64_t ldx, int64_t M, int64_t K, const void
 
 int launch_gemm_b128_decode(const void* x, int64_t ldx, int64_t M, int64_t K, const void* wp, const float* wsc,
                             int64_t N, const void* bias, void* y, int64_t ldy, hipStream_t stream) {
-  // One row group: one turn where a wave's blocks fit it, of one block up to K =
-  // 2048 (two were 6.2 us against 4.8 at 16 x 2048 x 2048), two up to 4096, four
-  // above.  Two groups: turns of one block (two spill: 13.8 us against 9.8 at 32
-  // x 4096 x 4096).
-  auto go = [&](auto kern) { return kern(x, ldx, M, K, wp, wsc, N, bias, y, ldy, stream); };
-  if (M > 16) return go(launch_decode_k<1, 2>);
-  if (K <= kDecWaves * 128) return go(launch_decode_k<1, 1>);
-  return K <= kDecWaves * 2 * 128 ? go(launch_decode_k<2, 1>) : go(launch_decode_k<4, 1>);
+  return M > 16 ? launch_decode_k<2>(x, ldx, M, K, wp, wsc, N, bias, y, ldy, stream)
+                : launch_decode_k<1>(x, ldx, M, K, wp, wsc, N, bias, y, ldy, stream);
 }
 
 // ---------------------------------------------------------------------------

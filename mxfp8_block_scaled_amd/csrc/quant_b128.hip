@@ -15,27 +15,6 @@
 
 namespace mxfp8 {
 
-namespace {
-
-// Maximum over the sixteen lanes of a DPP row: quads, then half and whole
-// row mirrors (VALU only).
-__device__ inline uint32_t row16_max(uint32_t m) {
-  m = quad_max(m);
-  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x141, 0xF, 0xF, true));   // row_half_mirror
-  return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x140, 0xF, 0xF, true));   // row_mirror
-}
-
-__device__ inline uint32_t absmax8(const uint4& v) {
-  u16x2 m = {0, 0};
-  m = absmax_pk(m, v.x);
-  m = absmax_pk(m, v.y);
-  m = absmax_pk(m, v.z);
-  m = absmax_pk(m, v.w);
-  return max((uint32_t)m[0], (uint32_t)m[1]);
-}
-
-}  // namespace
-
 // Row-major: x [M, K] -> q [M, K], s [M, P], P = ceil(K / 128).  Sixteen
 // consecutive lanes own one block, 16 bytes of bf16 each; a row takes 16 P
 // lanes, those past K (K % 16 == 0) hold zeros and store nothing.  HBM-bound:
