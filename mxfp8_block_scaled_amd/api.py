@@ -833,12 +833,19 @@ class _LinearB128(torch.autograd.Function):
         return y
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
+        # (torch's wrapper, which makes second derivatives an error, costs a
+        # small layer some microseconds and changes nothing in an ordinary pass)
+        run = _LinearB128._differentiable_once if torch.is_grad_enabled() else _LinearB128._backward
+        return run(ctx, dy)
+
+    @staticmethod
+    def _backward(ctx, dy):
         need_x, need_w, need_b = ctx.needs_input_grad
         kept, = ctx.saved_tensors
         d = dy.device
-        _check_capture(ctx, _stream(d), torch.cuda.is_current_stream_capturing())
+        stream = _stream(d)
+        _check_capture(ctx, stream, torch.cuda.is_current_stream_capturing())
         d2 = _rows(dy, "dy")
         (M, N), K = d2.shape, ctx.shape[-1]
         dx = d2.new_empty(M, K) if need_x else None
@@ -847,11 +854,13 @@ class _LinearB128(torch.autograd.Function):
         with _on(d):
             ws = _scratch(ctx.ws_bytes, d2)
             _check(lib().mxfp8_linear_b128_backward(_ptr(d2), M, N, d2.stride(0), K, ctx.keep, _ptr(kept), _ptr(dx), K,
-                                                    _ptr(dw), 1, K, _ptr(db), 1, _ptr(ws), ctx.ws_bytes, _stream(d)),
+                                                    _ptr(dw), 1, K, _ptr(db), 1, _ptr(ws), ctx.ws_bytes, stream),
                    "mxfp8_linear_b128_backward")
         if need_x and len(ctx.shape) != 2:
             dx = dx.view(ctx.shape)
         return dx, dw if need_w else None, db
+
+    _differentiable_once = staticmethod(torch.autograd.function.once_differentiable(_backward.__func__))
 
 
 def linear_b128(x, w, bias=None):

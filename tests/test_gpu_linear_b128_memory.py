@@ -135,3 +135,13 @@ def test_capture_beside_a_living_graph_is_refused():
     again = torch.autograd.grad(api.linear_b128(x, w, b), (x, w, b), dy)
     for p, q in zip(again, want):
         assert torch.equal(p, q)
+
+
+def test_second_derivative_is_an_error():
+    x, w, b = leaves()
+    dy = torch.ones(M, N, dtype=torch.bfloat16, device=dev())
+    plain = torch.autograd.grad(api.linear_b128(x, w, b), (x, w, b), dy)
+    dx, dw, db = torch.autograd.grad(api.linear_b128(x, w, b), (x, w, b), dy.requires_grad_(), create_graph=True)
+    assert all(torch.equal(g, h) for g, h in zip((dx, dw, db), plain))
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        dw.float().sum().backward()
