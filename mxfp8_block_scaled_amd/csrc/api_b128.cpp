@@ -93,7 +93,10 @@ mxfp8::B128Plan b128_plan(int64_t M, int64_t N, int64_t K, int force, double* us
   for (int s = 1; wanted(128) && s <= mxfp8::kMaxSplitK && (s == 1 || KB / s >= 2); s *= 2)
     offer(128, s, 4.5 + 0.65 * (double)((G * GM * s + 255) / 256) * blocks(s) + join(s));
   const int64_t large = (G + 1) / 2 * GM, wide = (G + 1) / 2 * ((GM + 1) / 2);
-  if (wanted(256)) offer(256, 1, 5.0 + (large <= 128 ? 0.75 : 0.95 * (double)((large + 255) / 256)) * blocks(1));
+  if (wanted(256)) {
+    const double rounds = (double)((large + 255) / 256);
+    offer(256, 1, 5.0 + (large <= 128 ? 0.75 : (rounds > 1.0 ? 1.03 : 0.95) * rounds) * blocks(1));
+  }
   if (wanted(512)) offer(512, 1, 5.0 + (wide <= 128 ? 1.25 : 1.7 * (double)((wide + 255) / 256)) * blocks(1));
   return best;
 }
