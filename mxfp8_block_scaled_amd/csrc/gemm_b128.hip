@@ -425,19 +425,33 @@ __device__ inline BigTile big_tile(int item, int tiles_n, int tiles_m) {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-// Stores two neighbouring 16-column tiles of a wave (lane (i, g) holds columns
-// 4 g .. + 3 of row i of each) as bf16: exchanging the odd 16-lane rows of the
-// first with the even ones of the second gives every lane eight consecutive
-// columns, of the first tile for even g, of the second for odd g.  at: the
-// byte offset of its eight, past the end to drop them.
-__device__ inline void store_pair(const v4f& lo, const v4f& hi, const float (&bl)[4], const float (&bh)[4],
-                                  __amdgpu_buffer_rsrc_t yr, uint32_t at) {
+// Two neighbouring 16-column tiles of a wave (lane (i, g) holds columns 4 g ..
+// + 3 of row i of each) as bf16: exchanging the odd 16-lane rows of the first
+// with the even ones of the second gives every lane eight consecutive columns,
+// of the first tile for even g, of the second for odd g.
+__device__ inline u32x4 pack_pair(const v4f& lo, const v4f& hi, const float (&bl)[4], const float (&bh)[4]) {
   const uint32_t l0 = pack_bf16x2(lo[0] + bl[0], lo[1] + bl[1]), l1 = pack_bf16x2(lo[2] + bl[2], lo[3] + bl[3]);
   const uint32_t h0 = pack_bf16x2(hi[0] + bh[0], hi[1] + bh[1]), h1 = pack_bf16x2(hi[2] + bh[2], hi[3] + bh[3]);
   const auto s0 = __builtin_amdgcn_permlane16_swap(l0, h0, false, false);
   const auto s1 = __builtin_amdgcn_permlane16_swap(l1, h1, false, false);
-  const u32x4 o = {s0[0], s1[0], s0[1], s1[1]};
-  __builtin_amdgcn_raw_buffer_store_b128(o, yr, at, 0, 0);
+  return u32x4{s0[0], s1[0], s0[1], s1[1]};
+}
+// Stores the 64 columns of two such pairs in whole 128-byte rows: half the
+// lanes of each exchange rows 8 .. 15 of the first for rows 0 .. 7 of the
+// second.  Byte offsets of a lane's eight columns (past the end to drop them):
+// at0 row i % 8, at1 row 8 + i % 8, in both column 32 (i / 8) +
+// col_of_pair(g) from the first pair's start on.  (Rows of 64 bytes: 8192 x
+// 28672 x 8192 1522 us against 1487, 16384 x 8192 x 2048 290 against 272.)
+__device__ inline int col_of_pair(int g) { return 16 * (g & 1) + 8 * (g >> 1); }
+__device__ inline void store_pairs(u32x4 p0, u32x4 p1, __amdgpu_buffer_rsrc_t yr, uint32_t at0, uint32_t at1) {
+  u32x4 a, b;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {   // row_ror:8 into lanes 8 .. 15, or 0 .. 7, of each sixteen
+    a[e] = (uint32_t)__builtin_amdgcn_update_dpp((int)p0[e], (int)p1[e], 0x128, 0xF, 0xC, false);
+    b[e] = (uint32_t)__builtin_amdgcn_update_dpp((int)p1[e], (int)p0[e], 0x128, 0xF, 0x3, false);
+  }
+  __builtin_amdgcn_raw_buffer_store_b128(a, yr, at0, 0, 0);
+  __builtin_amdgcn_raw_buffer_store_b128(b, yr, at1, 0, 0);
 }
 constexpr uint32_t kDrop = 0xFFFFFFF0u;
 
@@ -602,20 +616,21 @@ __global__ __launch_bounds__(kB128Threads, 1) void gemm_b128_big_kernel(
           __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[a][b]), pr, at, 0, 0);
         }
     } else {
-      const int nl = 16 * (g & 1) + 8 * (g >> 1);
       const __amdgpu_buffer_rsrc_t yr =
           raw_rsrc(y + (size_t)m0 * ldy, (uint32_t)(((int64_t)(rows - 1) * ldy + N) * 2));
 #pragma unroll
-      for (int a = 0; a < kA; a += 2) {
-        const int n = n0 + 16 * a + nl;
-        float bl[4], bh[4];
-        bias4(bias, N, n0 + 16 * a + 4 * g, bl);
-        bias4(bias, N, n0 + 16 * a + 16 + 4 * g, bh);
+      for (int a = 0; a < kA; a += 4) {
+        float bias_n[4][4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) bias4(bias, N, n0 + 16 * (a + q) + 4 * g, bias_n[q]);
+        const int n = n0 + 16 * a + 32 * (i >> 3) + col_of_pair(g);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          const int m = 32 * b + 16 * wm + i;   // N % 8 == 0: eight columns are all in or all out
-          store_pair(acc[a][b], acc[a + 1][b], bl, bh, yr,
-                     (n < N && m < rows) ? (uint32_t)(((int64_t)m * ldy + n) * 2) : kDrop);
+          const int m = 32 * b + 16 * wm + (i & 7);   // N % 8 == 0: eight columns are all in or all out
+          const uint32_t at = (uint32_t)(((int64_t)m * ldy + n) * 2);
+          store_pairs(pack_pair(acc[a][b], acc[a + 1][b], bias_n[0], bias_n[1]),
+                      pack_pair(acc[a + 2][b], acc[a + 3][b], bias_n[2], bias_n[3]), yr,
+                      n < N && m < rows ? at : kDrop, n < N && m + 8 < rows ? at + (uint32_t)ldy * 16u : kDrop);
         }
       }
     }
@@ -693,7 +708,7 @@ __global__ __launch_bounds__(kB128Threads, 1) void gemm_b128_big_kernel(
 //    buffer is free, the first fragments of p + 1 are read under the last
 //    MFMAs of p, and the copies of p + 2 go out with the MFMAs of p + 1.
 //  * Persistent, with the same epilogue.
-// 8192 x 28672 x 8192: 1538 us (2.50 PFLOP/s; 256 x 128 tiles 1769, 128 x 128
+// 8192 x 28672 x 8192: 1487 us (2.59 PFLOP/s; 256 x 128 tiles 1769, 128 x 128
 // 2304); 4096^3: 60, 67, 84.  What bounds it: the MFMAs alone, without v_fma,
 // reads and copies, take 1250 us of the 256 x 128 form's time at the clock
 // the card holds under them, the v_fma 250 more.
@@ -810,21 +825,22 @@ __global__ __launch_bounds__(kWideThreads, 1) void gemm_b128_wide_kernel(
 
   auto epilogue = [&](BigTile t) {
     const int n0 = t.tn * 256 + wn * 128, m0 = t.tm * 256 + wx * 128;
-    const int nl = 16 * (g & 1) + 8 * (g >> 1);
     const int rows = max(0, min(128, M - m0));
     const __amdgpu_buffer_rsrc_t yr = raw_rsrc(
         y + (size_t)min(m0, M - 1) * ldy, rows > 0 ? (uint32_t)(((int64_t)(rows - 1) * ldy + N) * 2) : 0u);
 #pragma unroll
-    for (int a = 0; a < 8; a += 2) {
-      const int n = n0 + 16 * a + nl;
-      float bl[4], bh[4];
-      bias4(bias, N, n0 + 16 * a + 4 * g, bl);
-      bias4(bias, N, n0 + 16 * a + 16 + 4 * g, bh);
+    for (int a = 0; a < 8; a += 4) {
+      float bias_n[4][4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) bias4(bias, N, n0 + 16 * (a + q) + 4 * g, bias_n[q]);
+      const int n = n0 + 16 * a + 32 * (i >> 3) + col_of_pair(g);
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const int m = 32 * b + 16 * wm + i;
-        store_pair(acc[a][b], acc[a + 1][b], bl, bh, yr,
-                   (n < N && m < rows) ? (uint32_t)(((int64_t)m * ldy + n) * 2) : kDrop);
+        const int m = 32 * b + 16 * wm + (i & 7);   // N % 8 == 0: eight columns are all in or all out
+        const uint32_t at = (uint32_t)(((int64_t)m * ldy + n) * 2);
+        store_pairs(pack_pair(acc[a][b], acc[a + 1][b], bias_n[0], bias_n[1]),
+                    pack_pair(acc[a + 2][b], acc[a + 3][b], bias_n[2], bias_n[3]), yr,
+                    n < N && m < rows ? at : kDrop, n < N && m + 8 < rows ? at + (uint32_t)ldy * 16u : kDrop);
       }
     }
     clear();
