@@ -791,14 +791,15 @@ def _linear_b128_forward(x, w, bias, keep):
     keeps what MXFP8_KEEP_DX (1) and MXFP8_KEEP_DW (2) in ``keep`` ask for."""
     x2, w2, bias = _rows(x, "x"), _rows(w, "w"), _bias(bias, w.shape[0])
     (M, K), N, d = x2.shape, w2.shape[0], x.device
-    y = x.new_empty(M, N)
+    # in its last shape: of a view made in here, autograd refuses in-place use
+    y = x.new_empty(M, N) if x.dim() == 2 else x.new_empty(*x.shape[:-1], N)
     with _on(d):
         kept_bytes, ws_bytes, back_bytes = _layer_bytes(M, N, K, keep)
         kept, ws = _scratch(kept_bytes, y), _scratch(ws_bytes, y)
         _check(lib().mxfp8_linear_b128_forward(_ptr(x2), M, K, x2.stride(0), _ptr(w2), N, w2.stride(0), _ptr(bias),
                                                _ptr(y), N, keep, _ptr(kept), _ptr(ws), ws_bytes, _stream(d)),
                "mxfp8_linear_b128_forward")
-    return y if x.dim() == 2 else y.view(*x.shape[:-1], N), kept, back_bytes
+    return y, kept, back_bytes
 
 
 def _mark_leaves(out, stream):
