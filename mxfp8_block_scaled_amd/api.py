@@ -1052,6 +1052,12 @@ class _MoEBalance(torch.autograd.Function):
         loss, counts, used = moe_balance(logits, topk, valid, coef, z_coef)
         ctx.save_for_backward(logits, counts, used, valid)
         ctx.args = topk, coef, z_coef
+        if ctx.needs_input_grad[0]:
+            # The caller gets counts of its own: a collective over ranks writes
+            # into them without autograd's notice, and the gradient needs the
+            # ones that go with this call's tokens.  (A kernel, not a copy: it
+            # may be captured.)
+            counts = counts + 0
         ctx.mark_non_differentiable(counts)
         return loss, counts
 
@@ -1066,8 +1072,9 @@ class _MoEBalance(torch.autograd.Function):
 
 def moe_balance_loss(logits, topk, valid=None, coef=1e-2, z_coef=0.0):
     """``moe_balance`` for autograd: ``(loss, counts)``, the loss
-    differentiable with respect to ``logits``.  In captured graphs as
-    ``linear_b128``."""
+    differentiable with respect to ``logits``.  ``counts`` are the caller's to
+    change (an all-reduce over ranks, say): the gradient does not read them.
+    In captured graphs as ``linear_b128``."""
     loss, counts = _MoEBalance.apply(logits, topk, valid, coef, z_coef)
     if loss.requires_grad:
         _mark_leaves(loss, _stream(loss.device))
