@@ -802,25 +802,56 @@ def _linear_b128_forward(x, w, bias, keep):
     return y, kept, back_bytes
 
 
+# Captured backward passes.  A leaf's gradient accumulator belongs to the stream
+# on which it was made and lives as long as some graph of that leaf, or something
+# else that holds it.  A captured backward pass that hands it a gradient makes its
+# stream wait for a captured event.  Any stream joins the capture by that but the
+# legacy default one, which cannot, and the process ends.  So the accumulators'
+# metadata note their streams, and a captured backward pass with one of the
+# default stream, or of a stream that is not known, is refused.
+_LEGACY, _UNKNOWN = 0, -1
+
+
+def _mark_leaves_before(leaves, stream):
+    """Before a node of these operands is made: accumulators that some other
+    operator made are of an unknown stream.  (The mark goes with an accumulator
+    that nothing holds.)  Not on the default stream, where the note would be
+    the refused kind anyway: some microseconds per operand."""
+    if stream == _LEGACY:
+        return
+    for t in leaves:
+        if t is not None and t.requires_grad and t.is_leaf:
+            torch.autograd.graph.get_gradient_edge(t).node.metadata.setdefault("mxfp8_stream", _UNKNOWN)
+
+
 def _mark_leaves(out, stream):
-    """Notes on each leaf's gradient accumulator, which lives as long as some
-    graph of that leaf, the stream it belongs to: the one of its first use."""
+    """Notes the stream of accumulators made with this node.  One of unknown
+    stream shows it the first time that it runs, which torch does on its own
+    stream."""
     for node, _ in out.grad_fn.next_functions:
-        if hasattr(node, "variable"):
-            node.metadata.setdefault("mxfp8_stream", stream)
+        if not hasattr(node, "variable"):
+            continue
+        meta = node.metadata
+        if meta.setdefault("mxfp8_stream", stream) == _UNKNOWN and "mxfp8_shows" not in meta:
+            meta["mxfp8_shows"] = True
+            device = node.variable.device
+            node.register_prehook(lambda grads, meta=meta, device=device: meta.update(mxfp8_stream=_stream(device)))
 
 
 def _check_capture(node, stream, capturing):
-    """A captured backward pass cannot hand a gradient to an accumulator of
-    another stream: torch would make that stream wait for a captured event, and
-    the process ends.  That is the case where a graph from before the capture
-    still holds the leaf's accumulator."""
+    """Raises where a captured backward pass of ``node`` would reach an
+    accumulator of the default stream, or may."""
     if not capturing:
         return
     for n, _ in node.next_functions:
-        if hasattr(n, "variable") and n.metadata.get("mxfp8_stream", stream) != stream:
+        if not hasattr(n, "variable"):
+            continue
+        of = n.metadata.get("mxfp8_stream", stream)
+        if of != stream and of in (_LEGACY, _UNKNOWN):
             raise RuntimeError("backward pass captured while an earlier autograd graph of the same leaf tensors is "
-                               "alive on another stream: delete its outputs before the capture")
+                               "alive on another stream, the default one, or was made by another operator on a stream "
+                               "that is not known: delete its outputs before the capture, and in the capture give "
+                               "those leaves to this operator first")
 
 
 class _LinearB128(torch.autograd.Function):
@@ -876,9 +907,14 @@ def linear_b128(x, w, bias=None):
     are passed straight through.  Where no gradient can be asked for
     (torch.no_grad, or no operand requires one) nothing is kept.
 
-    A step can be captured into a graph.  The backward pass of one is refused
-    while an eager autograd graph of the same leaves is alive on another
-    stream."""
+    A step can be captured into a graph, after a warm-up on a side stream whose
+    outputs may stay alive.  The backward pass of one is refused where a leaf's
+    gradient accumulator is of the default stream, which no capture takes in:
+    while an autograd graph of that leaf from there is alive, or something
+    else holds it (a data-parallel wrapper: make it on the side stream).  So is
+    one that another operator made first, on a stream not known here: until a
+    backward() runs it on a side stream, or, in the capture itself, unless this
+    operator is the first to be given the leaf."""
     for t, name in ((x, "x"), (w, "w")) + (((bias, "bias"),) if bias is not None else ()):
         if t.dtype != torch.bfloat16:
             raise ValueError(f"{name} must be bfloat16, got {t.dtype}")
@@ -889,8 +925,10 @@ def linear_b128(x, w, bias=None):
     if not torch.is_grad_enabled() or not (x.requires_grad or w.requires_grad or
                                            (bias is not None and bias.requires_grad)):
         return _linear_b128_forward(x, w, bias, 0)[0]
+    stream = _stream(x.device)
+    _mark_leaves_before((x, w, bias), stream)
     y = _LinearB128.apply(x, w, bias)
-    _mark_leaves(y, _stream(x.device))
+    _mark_leaves(y, stream)
     return y
 
 
@@ -1075,7 +1113,10 @@ def moe_balance_loss(logits, topk, valid=None, coef=1e-2, z_coef=0.0):
     differentiable with respect to ``logits``.  ``counts`` are the caller's to
     change (an all-reduce over ranks, say): the gradient does not read them.
     In captured graphs as ``linear_b128``."""
+    stream = _stream(logits.device) if logits.is_cuda else _LEGACY   # (moe_balance refuses the others)
+    if torch.is_grad_enabled():
+        _mark_leaves_before((logits,), stream)
     loss, counts = _MoEBalance.apply(logits, topk, valid, coef, z_coef)
     if loss.requires_grad:
-        _mark_leaves(loss, _stream(loss.device))
+        _mark_leaves(loss, stream)
     return loss, counts
