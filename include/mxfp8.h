@@ -364,8 +364,13 @@ typedef enum { MXFP8_F32 = 0, MXFP8_BF16 = 1 } mxfp8_dtype;
  *   scale = the smallest power of two s with amax / s <= 448, elements
  *   RNE(v / s); a block of zeros gets byte 0, a block that holds an infinity
  *   or NaN gets byte 0xFF (NaN) and makes the outputs it enters NaN.
- * Sums in fp32, one rounding to bf16.  K is any multiple of 16 (>= 16, at most
- * 2^24), N any; the last blocks may be partial.
+ * Sums over blocks in fp32, one rounding to bf16.  Inside a block of 128 the sum
+ * is the scaled MFMA's own (measured: off by up to 2^-12 of the block's largest
+ * product).  s times that sum is an fp32 number, so activations above about
+ * 2^111 can overflow whatever W is.  K is any multiple of 16 (>= 16, at most
+ * 2^24), N any; the last blocks may be partial.  Where the tiles are large (from
+ * some hundred rows on), an N that is no multiple of 8, or y whose rows are not
+ * 16-byte aligned, takes 1.6 to 2 times as long.
  *
  * mxfp8_quantize_b128: x_bf16 [M, K] row stride ldx (ldx >= K, ldx % 8 == 0,
  *   16-byte aligned) -> q_e4m3 [M, K] row stride ldq (ldq >= K, ldq % 16 == 0,
@@ -465,7 +470,8 @@ int mxfp8_linear_wgrad(const void* dy_bf16, int64_t M, int64_t N, int64_t lddy, 
  *             (MXFP8_KEEP_DX) and the packed activations (MXFP8_KEEP_DW).
  *   backward  dx = deq(q(dy)) deq(q(w)) (dy quantized like activations),
  *             dw = dy^T deq(q(x)), db = column sums of dy; each NULL if not
- *             wanted (db needs dw), MXFP8_E_SHAPE if its operand was not kept.
+ *             wanted (db needs dw, so a bias gradient alone costs what dw
+ *             does), MXFP8_E_SHAPE if its operand was not kept.
  * N and K multiples of 16; arguments as in the entries above; kept and
  * workspaces 256-byte aligned, sizes from mxfp8_linear_b128_layer_bytes.
  * `kept` is not changed by the backward call (it can be called again).

@@ -905,7 +905,8 @@ def linear_b128(x, w, bias=None):
     ``dx = deq(q(dy)) @ deq(q(w))``, dy quantized like activations;
     ``dw = dy^T @ deq(q(x))`` and ``db`` from bf16 dy.  The quantizations
     are passed straight through.  Where no gradient can be asked for
-    (torch.no_grad, or no operand requires one) nothing is kept.
+    (torch.no_grad, or no operand requires one) nothing is kept.  A bias
+    gradient alone keeps and computes what the weight's would.
 
     A step can be captured into a graph, after a warm-up on a side stream whose
     outputs may stay alive.  The backward pass of one is refused where a leaf's

@@ -70,7 +70,12 @@ std::atomic<int> g_force_mt{0}, g_force_wgrad{0};
 // reads for its products decide, where there are tiles for all compute units.
 mxfp8::B128Plan b128_plan(int64_t M, int64_t N, int64_t K, int force, double* us) {
   const int64_t G = b128_blocks(N), KB = b128_blocks(K), GM = b128_blocks(M);
-  // the larger forms write whole 16-byte pieces and address a tile's rows with 32 bits
+  // The larger forms write whole 16-byte pieces and address a tile's rows with
+  // 32 bits; any other N, and at launch a y whose rows are not 16-byte aligned,
+  // takes the 64-row tiles at every size.  What that costs (us, GEMM alone, N
+  // just below and at a multiple of 8): 4096 x 4095 x 4096 117, 4096^3 61 (its
+  // y off by one element 120); 4096 x 9001 and 9008 x 4096 250, 153; 2048 x
+  // 32001 and 32008 x 4096 453, 247; 8192 x 28671 and 28672 x 8192 2840, 1571.
   const bool whole = N % 8 == 0 && N <= ((int64_t)1 << 22);
   mxfp8::B128Plan best = {64, 1};
   double best_us = 1e30;

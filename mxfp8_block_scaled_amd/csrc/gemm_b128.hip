@@ -11,6 +11,12 @@
 // register.  Four v_fma (16 cycles) against one MFMA (32 cycles) fit in the
 // MFMA's shadow; the price is that the accumulators have to be ordinary
 // vector registers, half of the register file.
+//
+// Precision: between blocks everything is fp32.  Inside a block the sum is the
+// scaled MFMA's own, measured off by up to 2^-12 of its largest product, which
+// is coarser than fp32 and finer than the E4M3 operands (2^-4) and the bf16
+// output.  s times that sum is an fp32 number before W is applied: activations
+// above about 2^111 can overflow there though the product with a small W would not.
 #include "b128.hpp"
 #include "tile_core.hpp"
 
@@ -37,8 +43,8 @@ __device__ inline float scalar_scale(const float* p, int at) {
 // or four per turn keep half the registers of two workgroups per compute unit
 // busy (16 x 2048 x 2048: 6.2 us against 4.8; 8 x 8192 x 8192: 16.5, 13.7), and
 // so does loading a block ahead (15.5).
-// M = 1, N = K = 4096: 4.6 us (3.6 TB/s); 13 x 4000 x 2064: 5.5 us; 32 x 4096 x
-// 4096: 9.5.
+// M = 1, N = K = 4096: 4.8 us (3.5 TB/s); 13 x 4000 x 2064: 6.0 us; 32 x 4096 x
+// 4096: 9.5 (traced, in steady calls).
 // ---------------------------------------------------------------------------
 namespace {
 constexpr int kDecWaves = 16;
@@ -703,15 +709,15 @@ __global__ __launch_bounds__(kB128Threads, 1) void gemm_b128_big_kernel(
 // the 256 x 128 tiles; 256 registers per wave leave no room for a second set
 // of fragments, so weight fragments are read two ahead and the SIMD's other
 // wave covers what latency is left.
-//  * LDS holds two blocks (2 x 65 KiB).  After a wave's last reads of block p
+//  * LDS holds two blocks (2 x 66 KiB).  After a wave's last reads of block p
 //    comes the step's one barrier: then p + 1 has landed everywhere, p's
 //    buffer is free, the first fragments of p + 1 are read under the last
 //    MFMAs of p, and the copies of p + 2 go out with the MFMAs of p + 1.
 //  * Persistent, with the same epilogue.
-// 8192 x 28672 x 8192: 1487 us (2.59 PFLOP/s; 256 x 128 tiles 1769, 128 x 128
-// 2304); 4096^3: 60, 67, 84.  What bounds it: the MFMAs alone, without v_fma,
-// reads and copies, take 1250 us of the 256 x 128 form's time at the clock
-// the card holds under them, the v_fma 250 more.
+// 8192 x 28672 x 8192: 1571 us (2.45 PFLOP/s; 256 x 128 tiles 1805, 128 x 128
+// 2302, 128 x 64 2660); 4096^3: 60, 69, 89, 102 (traced, in steady calls).  The
+// MFMA pipes are busy 0.65 of the time.  Timed one by one in the 256 x 128 form:
+// the MFMAs alone, without v_fma, reads and copies, 1250 us, the v_fma 250 more.
 // ---------------------------------------------------------------------------
 namespace {
 constexpr int kWideThreads = 512;

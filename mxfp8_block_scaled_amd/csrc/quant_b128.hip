@@ -18,7 +18,8 @@ namespace mxfp8 {
 // Row-major: x [M, K] -> q [M, K], s [M, P], P = ceil(K / 128).  Sixteen
 // consecutive lanes own one block, 16 bytes of bf16 each; a row takes 16 P
 // lanes, those past K (K % 16 == 0) hold zeros and store nothing.  HBM-bound:
-// 2 bytes read and 1 + 1/128 written per element.
+// 2 bytes read and 1 + 1/128 written per element.  8192 x 8192: 31 us (6.4 TB/s,
+// part of x still cached from the call before).
 __global__ __launch_bounds__(256) void quant_act_b128_kernel(const uint16_t* __restrict__ x, int64_t ldx, int64_t K,
                                                              int64_t lanes_per_row, int64_t total,
                                                              uint8_t* __restrict__ q, int64_t ldq,
@@ -50,7 +51,7 @@ int launch_quantize_b128(const void* x, int64_t M, int64_t K, int64_t ldx, void*
 // four times, once for each of its 32-blocks, so the layout is the MX one and
 // every reader of packed activations takes it.  A workgroup owns one 16-row
 // band and SPW consecutive 64-K steps, staged in LDS and written as one
-// contiguous run of SPW KiB.  HBM-bound: 8192 x 8192 48 us (4.2 TB/s).
+// contiguous run of SPW KiB.  HBM-bound: 8192 x 8192 47 us (4.3 TB/s).
 template <int SPW>
 __global__ __launch_bounds__(256) void quant_act_packed_b128_kernel(const uint16_t* __restrict__ x, int64_t ldx,
                                                                     int64_t M, int64_t K, int64_t KS, int64_t nsg,
@@ -107,6 +108,7 @@ int launch_quantize_packed_b128(const void* x, int64_t M, int64_t K, int64_t ldx
 // power of two, exact in bf16 for scale bytes 9 .. 246 (outside, a product can
 // leave bf16's normal range).  One thread per 16-byte chunk of the real rows
 // and columns; four consecutive lanes read one 64-byte row of a piece.
+// HBM-bound: 8192 x 8192 42 us (4.9 TB/s).
 __global__ __launch_bounds__(256) void dequant_packed_kernel(const uint8_t* __restrict__ qp,
                                                              const uint8_t* __restrict__ sp, int64_t K, int64_t KS,
                                                              int64_t chunks, int64_t total,

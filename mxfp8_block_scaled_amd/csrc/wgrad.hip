@@ -44,8 +44,11 @@ using namespace wgrad;
 //    fragments are read while the step's own buffer is refilled for the step
 //    after next (dY copies and the widened X) and X is loaded one step
 //    further.
-// 16384 x 5120 x 2048: 300 us (1150 TFLOP/s; a bf16 library product of 8192^3
-// reaches 1230) and 28 for the join; 4096^3: 139.  The MFMAs bound it.
+// 16384 x 5120 x 2048: 331 us with bf16 results (1040 TFLOP/s; a bf16 library
+// product of 8192^3 reaches 1230), 318 with fp32, and 28 for the join; 4096^3:
+// 132, added to what is there 154.  The MFMA pipes are busy 0.47 of the time (at
+// the library product's rate they would be 0.49).  No counter tells how the rest
+// divides: LDS reads, and the wait for everything in flight at half a step.
 // ---------------------------------------------------------------------------
 namespace {
 
