@@ -524,6 +524,117 @@ int mxfp8_moe_balance_backward(const void* logits, int dtype, int64_t T, int64_t
                                const uint8_t* valid, float coef, float z_coef, const int* counts, const int* used,
                                const float* grad_loss, void* dlogits, int64_t ldd, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * MXFP4 on both sides: the linear layer with E2M1 weights and E2M1
+ * activations (gfx950 multiplies 4-bit by 4-bit operands in half the cycles of
+ * 8-bit ones):
+ *   y[m, n] = bf16( sum_k deq4(q4(x))[m, k] * deq4(W)[n, k] + bias[n] )
+ * W is the prepared MXFP4 weight of mxfp8_prepare_weight_fp4 (the one that
+ * mxfp8_linear_w4a8 takes), q4 the rule of mxfp8_quantize_fp4: scale =
+ * 2^(floor(log2 amax) - 2) per 32 elements, round to nearest even, saturate
+ * to +-6; a block of zeros gets byte 0.  A block with an infinity or a NaN
+ * gets byte 0xFF (NaN) and makes the outputs that it enters NaN.  fp32
+ * accumulation, bias (4-byte aligned) added in fp32, one rounding.  K % 256 ==
+ * 0, K <= 2^24; M <= 2^30, N <= 2^24.
+ *
+ * mxfp8_packed_act_fp4_bytes: host-only sizes of the packed activations (M >=
+ *   1): *q_bytes = M_pad * K / 2, *s_bytes = M_pad * K / 32, M_pad =
+ *   ceil(M / 128) * 128.
+ * mxfp8_quantize_act_packed_fp4: x_bf16 [M, K] row stride ldx (ldx >= K, ldx %
+ *   8 == 0, 16-byte aligned) into them (256-byte aligned; pad rows zero).
+ *   mxfp8_unpack_weight_fp4(qp, sp, M, K, ...) returns plain bytes.
+ * mxfp8_gemm_packed_fp4: the product and epilogue on packed activations; other
+ *   arguments as mxfp8_linear.  No workspace.
+ * mxfp8_linear_w4a4: both; arguments as mxfp8_linear, workspace of
+ *   mxfp8_linear_w4a4_workspace_bytes (0 for few rows: NULL is fine then),
+ *   256-byte aligned, without initialization.
+ */
+int mxfp8_packed_act_fp4_bytes(int64_t M, int64_t K, size_t* q_bytes, size_t* s_bytes);
+int mxfp8_quantize_act_packed_fp4(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, void* q_packed,
+                                  void* s_packed, void* stream);
+int mxfp8_gemm_packed_fp4(const void* q_packed, const void* s_packed, int64_t M, int64_t K, const void* w_packed,
+                          const void* ws_packed, int64_t N, const void* bias_bf16, void* y_bf16, int64_t ldy,
+                          void* stream);
+int mxfp8_linear_w4a4_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes);
+int mxfp8_linear_w4a4(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, const void* w_packed,
+                      const void* s_packed, int64_t N, const void* bias_bf16, void* y_bf16, int64_t ldy,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Test hook: pin the form of mxfp8_linear_w4a4, mxfp8_gemm_packed_fp4 and
+ * mxfp8_moe_linear_w4a4: 0 = by shape, 1 = the decode form where it applies
+ * (dense M <= 16, K <= 8192), 64 / 128 / 256 = tiles of 128 weight rows x 64 /
+ * 128 rows, or 256 weight rows x 256 (dense) / 128 (experts) rows.  The
+ * workspace queries follow it.  Process-wide; returns the previous value, or
+ * MXFP8_E_SHAPE.
+ */
+int mxfp8_debug_force_w4a4(int form);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Tokens sorted by expert and back, for T tokens with topk slots each over E
+ * experts (1 <= E <= 256, 1 <= topk <= 16, T <= 2^24, T topk <= 2^26).
+ *
+ * mxfp8_moe_sort: ids [slots] int32 or int64 (id_bytes 4 or 8), slots = T topk,
+ *   the expert of each slot; any other value (negative, or E and above: padding
+ *   or an expert of another rank) is a slot without an expert here.  A stable
+ *   sort: row_of_slot [slots] is the row of each slot, ordered by expert and
+ *   within an expert by slot, the slots without an expert behind all others;
+ *   slot_of_row [slots] its inverse; offsets [E + 1] the first row of each
+ *   expert, and offsets[E] the number of rows that have one.  workspace of
+ *   mxfp8_moe_sort_workspace_bytes (0: NULL is fine), 256-byte aligned.
+ * mxfp8_moe_permute: xs[row_of_slot[t, j]] = x[t]; zeros in the rows of slots
+ *   without an expert.
+ * mxfp8_moe_unpermute: y[t] = sum_j weights[t, j] ys[row_of_slot[t, j]] over
+ *   the slots with an expert, fp32 in slot order, rounded once.  weights NULL:
+ *   all 1, which makes it mxfp8_moe_permute's gradient.  The rows of slots
+ *   without an expert are not read.
+ * mxfp8_moe_unpermute_backward: dys[row_of_slot[t, j]] = weights[t, j] dy[t]
+ *   (zeros for slots without an expert) and dweights[t, j] = sum_h dy[t, h]
+ *   ys[row_of_slot[t, j], h] (fp32 in a fixed order; 0 for them); dys or
+ *   dweights may be NULL, and ys where dweights is.
+ * Matrices: x, y, dy, [T, H] and xs, ys, dys [T topk, H], fp32 or bf16 (dtype),
+ *   any row strides >= H, aligned to their elements (rows on 16 bytes are
+ *   faster), 1 <= H <= 2^24.  kept: offsets + E of the sort, on the device.
+ *   weights, dweights fp32 [T, topk].
+ */
+int mxfp8_moe_sort_workspace_bytes(int64_t slots, int64_t E, size_t* bytes);
+int mxfp8_moe_sort(const void* ids, int id_bytes, int64_t slots, int64_t E, int32_t* row_of_slot,
+                   int32_t* slot_of_row, int32_t* offsets, void* workspace, size_t workspace_bytes, void* stream);
+int mxfp8_moe_permute(const void* x, int dtype, int64_t T, int64_t H, int64_t ldx, int64_t topk,
+                      const int32_t* row_of_slot, const int32_t* kept, void* xs, int64_t ldxs, void* stream);
+int mxfp8_moe_unpermute(const void* ys, int dtype, int64_t T, int64_t H, int64_t ldys, int64_t topk,
+                        const int32_t* row_of_slot, const int32_t* kept, const float* weights, void* y, int64_t ldy,
+                        void* stream);
+int mxfp8_moe_unpermute_backward(const void* dy, int dtype, int64_t T, int64_t H, int64_t lddy, int64_t topk,
+                                 const int32_t* row_of_slot, const int32_t* kept, const void* ys, int64_t ldys,
+                                 const float* weights, void* dys, int64_t lddys, float* dweights, void* stream);
+
+/*
+ * The experts' products on sorted rows, MXFP4 on both sides:
+ *   y[r, n] = bf16( sum_k deq4(q4(x))[i(r), k] * deq4(W[e(r)])[n, k] )
+ * with e(r) the expert whose rows offsets[e] .. offsets[e + 1] - 1 hold r, and
+ * i(r) = r (slot_of_row NULL: x is sorted, x_rows == R) or slot_of_row[r] /
+ * topk (x holds the tokens, x_rows topk == R).  Rows from offsets[E] on are
+ * zeros.  offsets and slot_of_row as mxfp8_moe_sort left them.
+ *   x_bf16 [x_rows, K] row stride ldx (ldx % 8 == 0, 16-byte aligned), y_bf16
+ *   [R, N] row stride ldy; K % 256 == 0, x_rows K / 2 < 2^32, N <= 2^24
+ *   workspace of mxfp8_moe_linear_w4a4_workspace_bytes (0: NULL is fine),
+ *   256-byte aligned, without initialization
+ * mxfp8_moe_prepare_experts_fp4: one-time layout of the experts' weights
+ *   w_e2m1 [E, N, K/2] (16-byte aligned) and w_s_e8m0 [E, N, K/32], contiguous,
+ *   into 256-byte aligned buffers of mxfp8_moe_prepared_experts_fp4_bytes.
+ */
+int mxfp8_moe_prepared_experts_fp4_bytes(int64_t E, int64_t N, int64_t K, size_t* w_bytes, size_t* s_bytes);
+int mxfp8_moe_prepare_experts_fp4(const void* w_e2m1, const void* w_s_e8m0, int64_t E, int64_t N, int64_t K,
+                                  void* w_packed, void* s_packed, void* stream);
+int mxfp8_moe_linear_w4a4_workspace_bytes(int64_t x_rows, int64_t R, int64_t N, int64_t K, int64_t E, size_t* bytes);
+int mxfp8_moe_linear_w4a4(const void* x_bf16, int64_t x_rows, int64_t K, int64_t ldx, const int32_t* slot_of_row,
+                          int64_t topk, const int32_t* offsets, int64_t R, int64_t E, const void* w_packed,
+                          const void* s_packed, int64_t N, void* y_bf16, int64_t ldy, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

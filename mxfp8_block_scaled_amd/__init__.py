@@ -22,6 +22,10 @@ _API = (
     "quantize_act_b128", "quantize_act_packed_b128", "linear_b128", "linear_wgrad",
     "mxfp8_linear_b128", "mxfp8_linear_b128_workspace_bytes", "mxfp8_prepared_weight_b128_bytes",
     "moe_balance", "moe_balance_backward", "moe_balance_loss",
+    "linear_w4a4", "quantize_act_packed_fp4", "PackedActivationFP4", "mxfp8_linear_w4a4",
+    "mxfp8_linear_w4a4_workspace_bytes",
+    "MoEOrder", "moe_sort", "moe_permute", "moe_unpermute", "ExpertWeightsFP4", "moe_prepare_experts_fp4",
+    "moe_linear_w4a4",
     "mxfp8_status_string", "MXFP8Error",
 )
 

@@ -87,6 +87,24 @@ _SIGNATURES = {
                            _vp, _vp, _sz, _vp], ctypes.c_int),
     "mxfp8_moe_balance_backward": ([_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, ctypes.c_float, ctypes.c_float,
                                     _vp, _vp, _vp, _vp, _i64, _vp], ctypes.c_int),
+    "mxfp8_packed_act_fp4_bytes": ([_i64, _i64, ctypes.POINTER(_sz), ctypes.POINTER(_sz)], ctypes.c_int),
+    "mxfp8_quantize_act_packed_fp4": ([_vp, _i64, _i64, _i64, _vp, _vp, _vp], ctypes.c_int),
+    "mxfp8_gemm_packed_fp4": ([_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _vp], ctypes.c_int),
+    "mxfp8_linear_w4a4_workspace_bytes": ([_i64, _i64, _i64, ctypes.POINTER(_sz)], ctypes.c_int),
+    "mxfp8_linear_w4a4": ([_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _sz, _vp], ctypes.c_int),
+    "mxfp8_debug_force_w4a4": ([ctypes.c_int], ctypes.c_int),
+    "mxfp8_moe_sort_workspace_bytes": ([_i64, _i64, ctypes.POINTER(_sz)], ctypes.c_int),
+    "mxfp8_moe_sort": ([_vp, ctypes.c_int, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "mxfp8_moe_permute": ([_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp], ctypes.c_int),
+    "mxfp8_moe_unpermute": ([_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _vp], ctypes.c_int),
+    "mxfp8_moe_unpermute_backward": ([_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _i64,
+                                      _vp, _vp], ctypes.c_int),
+    "mxfp8_moe_prepared_experts_fp4_bytes": ([_i64, _i64, _i64, ctypes.POINTER(_sz), ctypes.POINTER(_sz)],
+                                             ctypes.c_int),
+    "mxfp8_moe_prepare_experts_fp4": ([_vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp], ctypes.c_int),
+    "mxfp8_moe_linear_w4a4_workspace_bytes": ([_i64, _i64, _i64, _i64, _i64, ctypes.POINTER(_sz)], ctypes.c_int),
+    "mxfp8_moe_linear_w4a4": ([_vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _sz,
+                               _vp], ctypes.c_int),
 }
 
 # Static scratch of mxfp8_linear_noalloc (bytes; MXFP8_NOALLOC_SCRATCH_BYTES).
@@ -515,9 +533,20 @@ def gemm_packed(pa, pw, bias=None):
     large-M path), for activations and a weight of the same scale block."""
     assert pa.K == pw.K
     b128 = isinstance(pw, PreparedWeightB128)
+    fp4 = isinstance(pa, PackedActivationFP4)
     if pa.block != (128 if b128 else 32):
         raise ValueError(f"activations with a scale per {pa.block} elements do not go with this weight")
+    if fp4 != isinstance(pw, PreparedWeightFP4):
+        raise ValueError("MXFP4 activations and an MXFP4 weight go together")
     y = torch.empty((pa.M, pw.N), dtype=torch.bfloat16, device=pa.q_packed.device)
+    if fp4:
+        bias = _bias(bias, pw.N, align=4)
+        _same_device(pa.q_packed, pw.w_packed, bias)
+        with _on(pa.device):
+            _check(lib().mxfp8_gemm_packed_fp4(_ptr(pa.q_packed), _ptr(pa.s_packed), pa.M, pa.K, _ptr(pw.w_packed),
+                                               _ptr(pw.s_packed), pw.N, _ptr(bias), _ptr(y), y.stride(0),
+                                               _stream(pa.device)), "mxfp8_gemm_packed_fp4")
+        return y
     if b128:
         bias = _bias(bias, pw.N)
         _same_device(pa.q_packed, pw.w_packed, bias)
@@ -584,12 +613,12 @@ def _rows(x, name):
     return x2
 
 
-def _bias(bias, N):
+def _bias(bias, N, align=2):
     if bias is None:
         return None
     if bias.dtype != torch.bfloat16 or bias.numel() != N:
         raise ValueError(f"bias must be bfloat16 [{N}]")
-    return bias.contiguous()
+    return bias.contiguous() if bias.data_ptr() % align == 0 else bias.clone(memory_format=torch.contiguous_format)
 
 
 def mxfp8_linear_b128_workspace_bytes(M, N, K):
@@ -934,6 +963,85 @@ def linear_b128(x, w, bias=None):
 
 
 # ---------------------------------------------------------------------------
+# MXFP4 on both sides
+# ---------------------------------------------------------------------------
+
+def mxfp8_linear_w4a4_workspace_bytes(M, N, K):
+    return _bytes("mxfp8_linear_w4a4_workspace_bytes", M, N, K)
+
+
+def mxfp8_linear_w4a4(x, M, K, ldx, wp, sp, N, bias, y, ldy, ws, ws_bytes, stream):
+    return lib().mxfp8_linear_w4a4(x, M, K, ldx, wp, sp, N, bias, y, ldy, ws, ws_bytes, stream)
+
+
+def mxfp8_debug_force_w4a4(form):
+    _bytes.cache_clear()
+    return lib().mxfp8_debug_force_w4a4(form)
+
+
+class PackedActivationFP4(PackedActivation):
+    """Activations quantized to MXFP4 in the packed operand layout (rows
+    padded to 128): the activations of ``gemm_packed`` with a
+    PreparedWeightFP4."""
+
+    def dequantize(self):
+        raise NotImplementedError("MXFP4 activations have no dequantize entry")
+
+    def unpack(self):
+        """(E2M1 ``[M_pad, K/2]``, two codes per byte, UE8M0 ``[M_pad, K/32]``)
+        as uint8 tensors."""
+        with _on(self.device):
+            return PreparedWeightFP4(self.q_packed, self.s_packed, self.M, self.K).unpack()
+
+
+def quantize_act_packed_fp4(x):
+    """bf16 ``x[..., K]`` (GPU, K % 256 == 0) -> PackedActivationFP4 (the rule
+    of ``quantize_fp4``; a block with an infinity or a NaN gets the scale
+    byte 0xFF, NaN)."""
+    x2 = _rows(x, "x")
+    M, K = x2.shape
+    q, s = _sz(), _sz()
+    _check(lib().mxfp8_packed_act_fp4_bytes(max(M, 1), K, ctypes.byref(q), ctypes.byref(s)),
+           "mxfp8_packed_act_fp4_bytes")
+    with _on(x.device):
+        qp = x2.new_empty(q.value if M else 0, dtype=torch.uint8)
+        sp = x2.new_empty(s.value if M else 0, dtype=torch.uint8)
+        _check(lib().mxfp8_quantize_act_packed_fp4(_ptr(x2), M, K, x2.stride(0), _ptr(qp), _ptr(sp),
+                                                   _stream(x.device)), "mxfp8_quantize_act_packed_fp4")
+    return PackedActivationFP4(qp, sp, M, K)
+
+
+def linear_w4a4(x, pw, bias=None, out=None):
+    """The linear layer with MXFP4 on both sides: ``y = bf16(deq4(q4(x)) @
+    deq4(W).T + bias)``, x bf16 ``[..., K]`` quantized to MXFP4 on the fly, pw
+    a PreparedWeightFP4 (the weight ``linear`` multiplies with 8-bit
+    activations), bias bf16 ``[N]`` or None.  Returns bf16 ``[..., N]``; ``out``:
+    bf16 ``[M, N]`` to write into, M the rows of x."""
+    if not isinstance(pw, PreparedWeightFP4):
+        raise ValueError("linear_w4a4 takes an MXFP4 weight (prepare_weight_fp4)")
+    x2 = _rows(x, "x")
+    (M, K), N = x2.shape, pw.N
+    if K != pw.K:
+        raise ValueError(f"x has {K} columns, the weight {pw.K}")
+    bias = _bias(bias, N, align=4)
+    if out is None:
+        y = x.new_empty(M, N) if x.dim() == 2 else x.new_empty(*x.shape[:-1], N)
+        ldy = N
+    else:
+        if out.dtype != torch.bfloat16 or tuple(out.shape) != (M, N) or out.stride(1) != 1 or out.stride(0) < N:
+            raise ValueError(f"out must be bfloat16 [{M}, {N}] with contiguous rows that do not overlap")
+        y, ldy = out, out.stride(0)
+    _same_device(x2, pw.w_packed, bias, y)
+    with _on(x.device):
+        need = _bytes("mxfp8_linear_w4a4_workspace_bytes", M, N, K)
+        ws = _scratch(need, x2)
+        _check(lib().mxfp8_linear_w4a4(_ptr(x2), M, K, x2.stride(0), _ptr(pw.w_packed), _ptr(pw.s_packed), N,
+                                       _ptr(bias), _ptr(y), ldy, _ptr(ws), need, _stream(x.device)),
+               "mxfp8_linear_w4a4")
+    return y if out is None or x.dim() == 2 else y.view(*x.shape[:-1], N)
+
+
+# ---------------------------------------------------------------------------
 # Routed MoE
 # ---------------------------------------------------------------------------
 
@@ -1121,3 +1229,240 @@ def moe_balance_loss(logits, topk, valid=None, coef=1e-2, z_coef=0.0):
     if loss.requires_grad:
         _mark_leaves(loss, stream)
     return loss, counts
+
+
+# ---------------------------------------------------------------------------
+# Tokens sorted by expert and back, and the experts' MXFP4 products
+# ---------------------------------------------------------------------------
+
+class MoEOrder:
+    """The slots of T tokens (``topk`` each) sorted by expert.
+
+    ``rows`` int32 ``[T, topk]``: the sorted row of each slot, by expert and
+    within one by slot; slots without an expert come behind all others.
+    ``slots`` int32 ``[T * topk]``: the slot of each row.  ``offsets`` int32
+    ``[E + 1]``: the first row of each expert, and the number of rows that have
+    one."""
+
+    def __init__(self, rows, slots, offsets):
+        self.rows, self.slots, self.offsets = rows, slots, offsets
+        self.T, self.topk = rows.shape
+        self.E = offsets.numel() - 1
+
+    @property
+    def _kept(self):
+        """Address of the number of rows with an expert."""
+        return self.offsets.data_ptr() + 4 * self.E
+
+    @property
+    def device(self):
+        return self.rows.device
+
+
+def moe_sort(ids, E):
+    """Sorts the slots of a routed batch by their expert (stable): ``ids`` int32
+    or int64 ``[T, topk]`` (``torch.topk``'s indices, say) over experts 0 .. E -
+    1 -> MoEOrder.  Any other id (-1 for padding, or an expert of another rank)
+    is a slot without an expert here."""
+    if ids.dtype not in (torch.int32, torch.int64) or ids.dim() != 2:
+        raise ValueError(f"ids must be int32 or int64 [T, topk], got {ids.dtype} {tuple(ids.shape)}")
+    _require_cuda(ids, "ids")
+    ids = ids.contiguous()
+    T, topk = ids.shape
+    if not 1 <= topk <= 16:
+        raise ValueError(f"topk must be 1 to 16, got {topk}")
+    R = T * topk
+    with _on(ids.device):
+        rows = ids.new_empty(T, topk, dtype=torch.int32)
+        slots = ids.new_empty(R, dtype=torch.int32)
+        need = _bytes("mxfp8_moe_sort_workspace_bytes", R, E)
+        offsets = ids.new_empty(E + 1, dtype=torch.int32)
+        ws = _scratch(need, ids)
+        _check(lib().mxfp8_moe_sort(_ptr(ids), ids.element_size(), R, E, _ptr(rows), _ptr(slots), _ptr(offsets),
+                                    _ptr(ws), need, _stream(ids.device)), "mxfp8_moe_sort")
+    return MoEOrder(rows, slots, offsets)
+
+
+def _matrix(x, rows, name):
+    """fp32 or bf16 ``[rows, H]`` with contiguous rows that do not overlap."""
+    if x.dtype not in _DTYPES or x.dim() != 2 or x.shape[0] != rows:
+        raise ValueError(f"{name} must be float32 or bfloat16 [{rows}, H], got {x.dtype} {tuple(x.shape)}")
+    _require_cuda(x, name)
+    if x.stride(1) != 1 or x.stride(0) < x.shape[1]:
+        x = x.clone(memory_format=torch.contiguous_format)
+    return x
+
+
+def _order(order):
+    if not isinstance(order, MoEOrder):
+        raise ValueError("order must be a MoEOrder (moe_sort)")
+    return order
+
+
+def _weights(weights, order):
+    if weights is None:
+        return None
+    if weights.dtype != torch.float32 or tuple(weights.shape) != (order.T, order.topk):
+        raise ValueError(f"weights must be float32 [{order.T}, {order.topk}]")
+    return weights.contiguous()
+
+
+def _permute(x, order):
+    H, R = x.shape[1], order.T * order.topk
+    with _on(x.device):
+        xs = x.new_empty(R, H)
+        _check(lib().mxfp8_moe_permute(_ptr(x), _DTYPES[x.dtype], order.T, H, x.stride(0), order.topk,
+                                       _ptr(order.rows), order._kept, _ptr(xs), H, _stream(x.device)),
+               "mxfp8_moe_permute")
+    return xs
+
+
+def _unpermute(ys, order, weights):
+    H = ys.shape[1]
+    with _on(ys.device):
+        y = ys.new_empty(order.T, H)
+        _check(lib().mxfp8_moe_unpermute(_ptr(ys), _DTYPES[ys.dtype], order.T, H, ys.stride(0), order.topk,
+                                         _ptr(order.rows), order._kept, _ptr(weights), _ptr(y), H,
+                                         _stream(ys.device)), "mxfp8_moe_unpermute")
+    return y
+
+
+class _MoEPermute(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, order):
+        ctx.order = order
+        return _permute(x, order)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dxs):
+        _check_capture(ctx, _stream(dxs.device), torch.cuda.is_current_stream_capturing())
+        return _unpermute(_matrix(dxs, ctx.order.T * ctx.order.topk, "dxs"), ctx.order, None), None
+
+
+class _MoEUnpermute(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ys, weights, order):
+        need_ys, need_w, _ = ctx.needs_input_grad
+        ctx.order = order
+        ctx.save_for_backward(ys if need_w else None, weights)
+        return _unpermute(ys, order, weights)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        stream = _stream(dy.device)
+        _check_capture(ctx, stream, torch.cuda.is_current_stream_capturing())
+        need_ys, need_w, _ = ctx.needs_input_grad
+        ys, weights = ctx.saved_tensors
+        order = ctx.order
+        dy = _matrix(dy, order.T, "dy")
+        H = dy.shape[1]
+        with _on(dy.device):
+            dys = dy.new_empty(order.T * order.topk, H) if need_ys else None
+            dw = dy.new_empty(order.T, order.topk, dtype=torch.float32) if need_w else None
+            _check(lib().mxfp8_moe_unpermute_backward(_ptr(dy), _DTYPES[dy.dtype], order.T, H, dy.stride(0), order.topk,
+                                                      _ptr(order.rows), order._kept, _ptr(ys),
+                                                      0 if ys is None else ys.stride(0), _ptr(weights), _ptr(dys), H,
+                                                      _ptr(dw), stream), "mxfp8_moe_unpermute_backward")
+        return dys, dw, None
+
+
+def moe_permute(x, order):
+    """The rows of ``x`` fp32 or bf16 ``[T, H]`` in the order of their experts:
+    ``xs[order.rows[t, j]] = x[t]``, ``[T * topk, H]``, zeros in the rows of
+    slots without an expert.  Differentiable; the gradient adds a token's rows
+    in fp32, in slot order.  In captured graphs as ``linear_b128``."""
+    order = _order(order)
+    x = _matrix(x, order.T, "x")
+    _same_device(x, order.rows)
+    if not (torch.is_grad_enabled() and x.requires_grad):
+        return _permute(x, order)
+    stream = _stream(x.device)
+    _mark_leaves_before((x,), stream)
+    xs = _MoEPermute.apply(x, order)
+    _mark_leaves(xs, stream)
+    return xs
+
+
+def moe_unpermute(ys, order, weights=None):
+    """The experts' rows back with their tokens: ``y[t] = sum_j weights[t, j]
+    ys[order.rows[t, j]]`` over the slots with an expert, ``ys`` fp32 or bf16
+    ``[T * topk, H]`` -> ``[T, H]``, summed in fp32 in slot order and rounded
+    once.  ``weights`` fp32 ``[T, topk]``, or None for all 1.  Differentiable
+    with respect to ys and weights (0 for slots without an expert).  In captured
+    graphs as ``linear_b128``."""
+    order = _order(order)
+    ys = _matrix(ys, order.T * order.topk, "ys")
+    weights = _weights(weights, order)
+    _same_device(ys, order.rows, weights)
+    if not torch.is_grad_enabled() or not (ys.requires_grad or (weights is not None and weights.requires_grad)):
+        return _unpermute(ys, order, weights)
+    stream = _stream(ys.device)
+    _mark_leaves_before((ys, weights), stream)
+    y = _MoEUnpermute.apply(ys, weights, order)
+    _mark_leaves(y, stream)
+    return y
+
+
+class ExpertWeightsFP4:
+    """The experts' MXFP4 weights ``[E, N, K]`` after the one-time preparation
+    (opaque packed layout)."""
+
+    def __init__(self, w_packed, s_packed, E, N, K):
+        self.w_packed, self.s_packed = w_packed, s_packed
+        self.E, self.N, self.K = E, N, K
+
+    @property
+    def device(self):
+        return self.w_packed.device
+
+
+def moe_prepare_experts_fp4(w_e2m1, w_s):
+    """MXFP4 expert weights ``w_e2m1`` uint8 ``[E, N, K/2]`` (two E2M1 codes per
+    byte, element 2j in the low nibble) with UE8M0 scales ``w_s`` ``[E, N,
+    K/32]`` -> ExpertWeightsFP4."""
+    w, s = _as_bytes(w_e2m1).contiguous(), _as_bytes(w_s).contiguous()
+    _require_cuda(w, "w_e2m1")
+    if w.dim() != 3 or tuple(s.shape) != (w.shape[0], w.shape[1], w.shape[2] // 16):
+        raise ValueError(f"w_e2m1 [E, N, K/2] and w_s [E, N, K/32], got {tuple(w.shape)}, {tuple(s.shape)}")
+    _same_device(w, s)
+    if w.data_ptr() % 16 != 0:
+        w = w.clone()
+    E, N, K = w.shape[0], w.shape[1], 2 * w.shape[2]
+    wb, sb = _sz(), _sz()
+    _check(lib().mxfp8_moe_prepared_experts_fp4_bytes(E, N, K, ctypes.byref(wb), ctypes.byref(sb)),
+           "mxfp8_moe_prepared_experts_fp4_bytes")
+    with _on(w.device):
+        wp, sp = w.new_empty(wb.value), w.new_empty(sb.value)
+        _check(lib().mxfp8_moe_prepare_experts_fp4(_ptr(w), _ptr(s), E, N, K, _ptr(wp), _ptr(sp), _stream(w.device)),
+               "mxfp8_moe_prepare_experts_fp4")
+    return ExpertWeightsFP4(wp, sp, E, N, K)
+
+
+def moe_linear_w4a4(x, ew, order, gather=False):
+    """The experts' products on sorted rows, MXFP4 on both sides: ``y[r] =
+    bf16(deq4(q4(x[r])) @ deq4(W[e(r)]).T)``, e(r) the expert of row r; zeros in
+    the rows of slots without an expert.
+
+    ``x`` bf16 ``[T * topk, K]`` in ``order``'s rows or, with ``gather``, ``[T, K]``:
+    the tokens, each row r taking its own (``moe_permute(x)`` without the copy).
+    ``ew`` ExpertWeightsFP4.  Returns bf16 ``[T * topk, N]``.  No gradients."""
+    order = _order(order)
+    if not isinstance(ew, ExpertWeightsFP4):
+        raise ValueError("ew must be ExpertWeightsFP4 (moe_prepare_experts_fp4)")
+    R = order.T * order.topk
+    if x.dim() != 2 or x.shape[0] != (order.T if gather else R) or x.shape[1] != ew.K or order.E != ew.E:
+        raise ValueError(f"x [{order.T if gather else R}, {ew.K}] and an order over {ew.E} experts, got "
+                         f"{tuple(x.shape)} and {order.E}")
+    x = _rows(x, "x")
+    _same_device(x, ew.w_packed, order.rows)
+    with _on(x.device):
+        y = x.new_empty(R, ew.N)
+        need = _bytes("mxfp8_moe_linear_w4a4_workspace_bytes", x.shape[0], R, ew.N, ew.K, ew.E)
+        ws = _scratch(need, x)
+        _check(lib().mxfp8_moe_linear_w4a4(_ptr(x), x.shape[0], ew.K, x.stride(0), _ptr(order.slots) if gather else None,
+                                           order.topk, _ptr(order.offsets), R, ew.E, _ptr(ew.w_packed),
+                                           _ptr(ew.s_packed), ew.N, _ptr(y), ew.N, _ptr(ws), need, _stream(x.device)),
+               "mxfp8_moe_linear_w4a4")
+    return y

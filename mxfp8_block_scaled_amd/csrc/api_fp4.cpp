@@ -1,0 +1,377 @@
+// C ABI (include/mxfp8.h) of the MXFP4 x MXFP4 linear layer, of tokens sorted
+// by expert and back, and of the experts' MXFP4 products: argument validation
+// on the host, device check, launches.  Nothing here allocates device memory
+// or synchronizes.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+
+#include "launch_fp4.hpp"
+#include "mxfp8.h"
+
+namespace {
+
+bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+
+constexpr int64_t kMaxRows = (int64_t)1 << 30, kMaxK = (int64_t)1 << 24, kMaxN = (int64_t)1 << 24;
+constexpr int64_t kMaxTokens = (int64_t)1 << 24, kMaxSlots = (int64_t)1 << 26;
+
+bool summed_ok(int64_t K) { return K >= 256 && K % 256 == 0 && K <= kMaxK; }
+int64_t pad128(int64_t n) { return (n + 127) / 128 * 128; }
+
+size_t act_bytes(int64_t M, int64_t K) { return (size_t)pad128(M) * (size_t)(K / 2); }
+size_t act_scale_bytes(int64_t M, int64_t K) { return (size_t)pad128(M) * (size_t)(K / 32); }
+// The quantizer's grid: a workgroup per 16 rows and 128-K step at most; the
+// tile GEMM's list in 32-bit range.
+bool act_grid_ok(int64_t M, int64_t K) { return pad128(M) / 16 * (K / 128) <= INT32_MAX; }
+bool gemm_grid_ok(int64_t M, int64_t N) { return (M + 63) / 64 * ((N + 127) / 128) <= INT32_MAX / 2; }
+
+// Test hook: pinned form (0: by shape).
+std::atomic<int> g_force{0};
+
+bool decode_form(int64_t M, int64_t N, int64_t K) {
+  (void)N;
+  const int force = g_force.load(std::memory_order_relaxed);
+  return M <= mxfp8::kFp4DecodeMaxM && K <= mxfp8::kFp4DecodeMaxK && (force == 0 || force == 1);
+}
+
+mxfp8::Fp4Plan tile_plan(int64_t M, int64_t N, int64_t K) {
+  (void)K;
+  const int force = g_force.load(std::memory_order_relaxed);
+  if (force == 256) return {256, 256};
+  if (force == 128) return {128, 128};
+  if (force == 64) return {128, 64};
+  const int64_t large = (M + 255) / 256 * ((N + 255) / 256);
+  if (large >= 192) return {256, 256};
+  const int64_t medium = (M + 127) / 128 * ((N + 127) / 128);
+  return medium >= 192 ? mxfp8::Fp4Plan{128, 128} : mxfp8::Fp4Plan{128, 64};
+}
+
+int check_weight(const void* wp, const void* sp, int64_t N, int64_t K) {
+  if (!wp || !sp) return MXFP8_E_NULLPTR;
+  if (N < 1 || N > kMaxN || !summed_ok(K)) return MXFP8_E_SHAPE;
+  if (!aligned(wp, 256) || !aligned(sp, 256)) return MXFP8_E_ALIGN;
+  return MXFP8_OK;
+}
+
+int check_out(const void* y, int64_t N, int64_t ldy, const void* bias) {
+  if (!y) return MXFP8_E_NULLPTR;
+  if (ldy < N) return MXFP8_E_LD;
+  if (!aligned(y, 2) || (bias && !aligned(bias, 4))) return MXFP8_E_ALIGN;
+  return MXFP8_OK;
+}
+
+size_t linear_ws(int64_t M, int64_t N, int64_t K) {
+  if (M == 0 || decode_form(M, N, K)) return 0;
+  return round_up(act_bytes(M, K), 256) + round_up(act_scale_bytes(M, K), 256);
+}
+
+// T tokens with topk slots each over E experts.
+bool slots_ok(int64_t T, int64_t topk) {
+  return T >= 0 && T <= kMaxTokens && topk >= 1 && topk <= mxfp8::kMoeMaxTopk && T * topk <= kMaxSlots;
+}
+bool experts_ok(int64_t E) { return E >= 1 && E <= mxfp8::kMoeMaxExperts; }
+
+int check_matrix(const void* p, int64_t H, int64_t ld, int size) {
+  if (!p) return MXFP8_E_NULLPTR;
+  if (ld < H) return MXFP8_E_LD;
+  return aligned(p, size) ? MXFP8_OK : MXFP8_E_ALIGN;
+}
+int check_rows(int dtype, int64_t T, int64_t H, int64_t topk) {
+  if ((dtype != MXFP8_F32 && dtype != MXFP8_BF16) || !slots_ok(T, topk) || H < 1 || H > kMaxK) return MXFP8_E_SHAPE;
+  const int64_t per = dtype == MXFP8_BF16 ? 8 : 4;
+  return T * ((H + per - 1) / per) / 256 < INT32_MAX ? MXFP8_OK : MXFP8_E_SHAPE;
+}
+
+struct ExpertsForm {
+  bool decode;
+  mxfp8::Fp4Plan plan;
+};
+ExpertsForm experts_form(int64_t R, int64_t N, int64_t K, int64_t E) {
+  (void)N;
+  const int force = g_force.load(std::memory_order_relaxed);
+  const bool can = K <= mxfp8::kFp4DecodeMaxK;
+  if (can && (force == 1 || (force == 0 && R <= 4 * E))) return {true, {}};
+  if (force == 256) return {false, {256, 128}};
+  if (force == 128) return {false, {128, 128}};
+  if (force == 64) return {false, {128, 64}};
+  return {false, R >= 64 * E ? mxfp8::Fp4Plan{128, 128} : mxfp8::Fp4Plan{128, 64}};
+}
+bool experts_shape_ok(int64_t x_rows, int64_t R, int64_t N, int64_t K, int64_t E) {
+  return x_rows >= 0 && R >= 0 && R <= kMaxSlots && x_rows <= R && N >= 1 && N <= kMaxN && summed_ok(K) &&
+         experts_ok(E) && x_rows * (K / 2) < ((int64_t)1 << 32) &&
+         (R / 64 + std::min(E, R)) * ((N + 127) / 128) <= INT32_MAX / 2 && std::min(E, R) * ((N + 15) / 16) <= INT32_MAX;
+}
+size_t experts_q_bytes(int64_t x_rows, int64_t K) { return round_up((size_t)x_rows * (size_t)(K / 2), 256); }
+size_t experts_ws(int64_t x_rows, int64_t R, int64_t N, int64_t K, int64_t E) {
+  if (R == 0 || experts_form(R, N, K, E).decode) return 0;
+  return experts_q_bytes(x_rows, K) + round_up((size_t)x_rows * (size_t)(K / 32), 256);
+}
+
+}  // namespace
+
+extern "C" {
+
+int mxfp8_packed_act_fp4_bytes(int64_t M, int64_t K, size_t* q_bytes, size_t* s_bytes) {
+  if (!q_bytes || !s_bytes) return MXFP8_E_NULLPTR;
+  if (M < 1 || M > kMaxRows || !summed_ok(K)) return MXFP8_E_SHAPE;
+  *q_bytes = act_bytes(M, K);
+  *s_bytes = act_scale_bytes(M, K);
+  return MXFP8_OK;
+}
+
+int mxfp8_quantize_act_packed_fp4(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, void* q_packed,
+                                  void* s_packed, void* stream) {
+  if (M < 0 || M > kMaxRows || !summed_ok(K)) return MXFP8_E_SHAPE;
+  if (M == 0) return MXFP8_OK;
+  if (!x_bf16 || !q_packed || !s_packed) return MXFP8_E_NULLPTR;
+  if (ldx < K || ldx % 8 != 0) return MXFP8_E_LD;
+  if (!aligned(x_bf16, 16) || !aligned(q_packed, 256) || !aligned(s_packed, 256)) return MXFP8_E_ALIGN;
+  if (!act_grid_ok(M, K)) return MXFP8_E_SHAPE;
+  if (int st = mxfp8::check_device_current()) return st;
+  return mxfp8::launch_quantize_packed_fp4(x_bf16, M, K, ldx, q_packed, s_packed, (hipStream_t)stream);
+}
+
+int mxfp8_gemm_packed_fp4(const void* q_packed, const void* s_packed, int64_t M, int64_t K, const void* w_packed,
+                          const void* ws_packed, int64_t N, const void* bias_bf16, void* y_bf16, int64_t ldy,
+                          void* stream) {
+  if (M < 0 || M > kMaxRows) return MXFP8_E_SHAPE;
+  if (int st = check_weight(w_packed, ws_packed, N, K)) return st;
+  if (M == 0) return MXFP8_OK;
+  if (!q_packed || !s_packed) return MXFP8_E_NULLPTR;
+  if (!aligned(q_packed, 256) || !aligned(s_packed, 256)) return MXFP8_E_ALIGN;
+  if (int st = check_out(y_bf16, N, ldy, bias_bf16)) return st;
+  if (!gemm_grid_ok(M, N)) return MXFP8_E_SHAPE;
+  if (int st = mxfp8::check_device_current()) return st;
+  return mxfp8::launch_gemm_fp4_tile(q_packed, s_packed, M, K, w_packed, ws_packed, N, bias_bf16, y_bf16, ldy,
+                                     (hipStream_t)stream, tile_plan(M, N, K));
+}
+
+int mxfp8_linear_w4a4_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  if (!bytes) return MXFP8_E_NULLPTR;
+  if (M < 0 || M > kMaxRows || N < 1 || N > kMaxN || !summed_ok(K)) return MXFP8_E_SHAPE;
+  *bytes = linear_ws(M, N, K);
+  return MXFP8_OK;
+}
+
+int mxfp8_linear_w4a4(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, const void* w_packed,
+                      const void* s_packed, int64_t N, const void* bias_bf16, void* y_bf16, int64_t ldy,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  if (M < 0 || M > kMaxRows) return MXFP8_E_SHAPE;
+  if (int st = check_weight(w_packed, s_packed, N, K)) return st;
+  if (M == 0) return MXFP8_OK;
+  if (!x_bf16) return MXFP8_E_NULLPTR;
+  if (ldx < K || ldx % 8 != 0) return MXFP8_E_LD;
+  if (!aligned(x_bf16, 16)) return MXFP8_E_ALIGN;
+  if (int st = check_out(y_bf16, N, ldy, bias_bf16)) return st;
+  if (!act_grid_ok(M, K) || !gemm_grid_ok(M, N)) return MXFP8_E_SHAPE;
+  const size_t need = linear_ws(M, N, K);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MXFP8_E_WORKSPACE;
+  if (!aligned(workspace, 256)) return MXFP8_E_ALIGN;
+  if (int st = mxfp8::check_device_current()) return st;
+  if (decode_form(M, N, K))
+    return mxfp8::launch_gemm_fp4_decode(x_bf16, ldx, M, K, w_packed, s_packed, N, bias_bf16, y_bf16, ldy,
+                                         (hipStream_t)stream);
+  uint8_t* q = (uint8_t*)workspace;
+  uint8_t* s = q + round_up(act_bytes(M, K), 256);
+  if (int st = mxfp8::launch_quantize_packed_fp4(x_bf16, M, K, ldx, q, s, (hipStream_t)stream)) return st;
+  return mxfp8::launch_gemm_fp4_tile(q, s, M, K, w_packed, s_packed, N, bias_bf16, y_bf16, ldy, (hipStream_t)stream,
+                                     tile_plan(M, N, K));
+}
+
+int mxfp8_debug_force_w4a4(int form) {
+  if (form != 0 && form != 1 && form != 64 && form != 128 && form != 256) return MXFP8_E_SHAPE;
+  return g_force.exchange(form);
+}
+
+int mxfp8_moe_sort_workspace_bytes(int64_t slots, int64_t E, size_t* bytes) {
+  if (!bytes) return MXFP8_E_NULLPTR;
+  if (slots < 0 || slots > kMaxSlots || !experts_ok(E)) return MXFP8_E_SHAPE;
+  *bytes = mxfp8::sort_ws_bytes(slots, E);
+  return MXFP8_OK;
+}
+
+int mxfp8_moe_sort(const void* ids, int id_bytes, int64_t slots, int64_t E, int32_t* row_of_slot,
+                   int32_t* slot_of_row, int32_t* offsets, void* workspace, size_t workspace_bytes, void* stream) {
+  if (slots < 0 || slots > kMaxSlots || !experts_ok(E) || (id_bytes != 4 && id_bytes != 8)) return MXFP8_E_SHAPE;
+  if (!offsets || (slots > 0 && (!ids || !row_of_slot || !slot_of_row))) return MXFP8_E_NULLPTR;
+  if (!aligned(ids, id_bytes) || !aligned(row_of_slot, 4) || !aligned(slot_of_row, 4) || !aligned(offsets, 4))
+    return MXFP8_E_ALIGN;
+  const size_t need = mxfp8::sort_ws_bytes(slots, E);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MXFP8_E_WORKSPACE;
+  if (!aligned(workspace, 256)) return MXFP8_E_ALIGN;
+  if (int st = mxfp8::check_device_current()) return st;
+  mxfp8::SortArgs a = {};
+  a.ids = ids;
+  a.wide = id_bytes == 8;
+  a.R = slots;
+  a.E = E;
+  a.rows = row_of_slot;
+  a.slots = slot_of_row;
+  a.offsets = offsets;
+  a.ws = (int*)workspace;
+  return mxfp8::launch_moe_sort(a, (hipStream_t)stream);
+}
+
+int mxfp8_moe_permute(const void* x, int dtype, int64_t T, int64_t H, int64_t ldx, int64_t topk,
+                      const int32_t* row_of_slot, const int32_t* kept, void* xs, int64_t ldxs, void* stream) {
+  if (int st = check_rows(dtype, T, H, topk)) return st;
+  if (T == 0) return MXFP8_OK;
+  const int size = dtype == MXFP8_BF16 ? 2 : 4;
+  if (!row_of_slot || !kept) return MXFP8_E_NULLPTR;
+  if (int st = check_matrix(x, H, ldx, size)) return st;
+  if (int st = check_matrix(xs, H, ldxs, size)) return st;
+  if (!aligned(row_of_slot, 4) || !aligned(kept, 4)) return MXFP8_E_ALIGN;
+  if (int st = mxfp8::check_device_current()) return st;
+  mxfp8::PermuteArgs a = {};
+  a.bf16 = dtype == MXFP8_BF16;
+  a.T = T;
+  a.H = H;
+  a.topk = topk;
+  a.rows = row_of_slot;
+  a.kept = kept;
+  a.tokens = x;
+  a.ldt = ldx;
+  a.out_sorted = xs;
+  a.ldo = ldxs;
+  return mxfp8::launch_moe_permute(a, (hipStream_t)stream);
+}
+
+int mxfp8_moe_unpermute(const void* ys, int dtype, int64_t T, int64_t H, int64_t ldys, int64_t topk,
+                        const int32_t* row_of_slot, const int32_t* kept, const float* weights, void* y, int64_t ldy,
+                        void* stream) {
+  if (int st = check_rows(dtype, T, H, topk)) return st;
+  if (T == 0) return MXFP8_OK;
+  const int size = dtype == MXFP8_BF16 ? 2 : 4;
+  if (!row_of_slot || !kept) return MXFP8_E_NULLPTR;
+  if (int st = check_matrix(ys, H, ldys, size)) return st;
+  if (int st = check_matrix(y, H, ldy, size)) return st;
+  if (!aligned(row_of_slot, 4) || !aligned(kept, 4) || !aligned(weights, 4)) return MXFP8_E_ALIGN;
+  if (int st = mxfp8::check_device_current()) return st;
+  mxfp8::PermuteArgs a = {};
+  a.bf16 = dtype == MXFP8_BF16;
+  a.T = T;
+  a.H = H;
+  a.topk = topk;
+  a.rows = row_of_slot;
+  a.kept = kept;
+  a.sorted = ys;
+  a.lds = ldys;
+  a.weights = weights;
+  a.out_tokens = y;
+  a.ldo = ldy;
+  return mxfp8::launch_moe_unpermute(a, (hipStream_t)stream);
+}
+
+int mxfp8_moe_unpermute_backward(const void* dy, int dtype, int64_t T, int64_t H, int64_t lddy, int64_t topk,
+                                 const int32_t* row_of_slot, const int32_t* kept, const void* ys, int64_t ldys,
+                                 const float* weights, void* dys, int64_t lddys, float* dweights, void* stream) {
+  if (int st = check_rows(dtype, T, H, topk)) return st;
+  if (T == 0) return MXFP8_OK;
+  const int size = dtype == MXFP8_BF16 ? 2 : 4;
+  if (!row_of_slot || !kept || (!dys && !dweights)) return MXFP8_E_NULLPTR;
+  if (int st = check_matrix(dy, H, lddy, size)) return st;
+  if (dweights)
+    if (int st = check_matrix(ys, H, ldys, size)) return st;
+  if (dys)
+    if (int st = check_matrix(dys, H, lddys, size)) return st;
+  if (!aligned(row_of_slot, 4) || !aligned(kept, 4) || !aligned(weights, 4) || !aligned(dweights, 4))
+    return MXFP8_E_ALIGN;
+  if (int st = mxfp8::check_device_current()) return st;
+  mxfp8::PermuteArgs a = {};
+  a.bf16 = dtype == MXFP8_BF16;
+  a.T = T;
+  a.H = H;
+  a.topk = topk;
+  a.rows = row_of_slot;
+  a.kept = kept;
+  a.tokens = dy;
+  a.ldt = lddy;
+  a.sorted = dweights ? ys : nullptr;
+  a.lds = ldys;
+  a.weights = weights;
+  a.out_sorted = dys;
+  a.ldo = lddys;
+  a.dweights = dweights;
+  return mxfp8::launch_moe_unpermute_backward(a, (hipStream_t)stream);
+}
+
+int mxfp8_moe_prepared_experts_fp4_bytes(int64_t E, int64_t N, int64_t K, size_t* w_bytes, size_t* s_bytes) {
+  if (!w_bytes || !s_bytes) return MXFP8_E_NULLPTR;
+  if (!experts_ok(E) || N < 1 || N > kMaxN || !summed_ok(K)) return MXFP8_E_SHAPE;
+  *w_bytes = (size_t)E * act_bytes(N, K);
+  *s_bytes = (size_t)E * act_scale_bytes(N, K);
+  return MXFP8_OK;
+}
+
+int mxfp8_moe_prepare_experts_fp4(const void* w_e2m1, const void* w_s_e8m0, int64_t E, int64_t N, int64_t K,
+                                  void* w_packed, void* s_packed, void* stream) {
+  if (!experts_ok(E)) return MXFP8_E_SHAPE;
+  if (int st = check_weight(w_packed, s_packed, N, K)) return st;
+  if (!w_e2m1 || !w_s_e8m0) return MXFP8_E_NULLPTR;
+  if (!aligned(w_e2m1, 16)) return MXFP8_E_ALIGN;
+  // (the pack kernels' grids: one thread per 16 bytes, one per scale pair)
+  const int64_t rows = N % 128 == 0 ? E * N : N, passes = N % 128 == 0 ? 1 : E;
+  if (pad128(rows) * (K / 64) > (int64_t)INT32_MAX * 256) return MXFP8_E_SHAPE;
+  if (int st = mxfp8::check_device_current()) return st;
+  for (int64_t e = 0; e < passes; ++e) {
+    const size_t w = (size_t)e * N * (K / 2), s = (size_t)e * N * (K / 32);
+    if (int st = mxfp8::launch_pack_weight_fp4((const uint8_t*)w_e2m1 + w, (const uint8_t*)w_s_e8m0 + s, rows, K,
+                                               K / 2, K / 32, (uint8_t*)w_packed + (size_t)e * act_bytes(N, K),
+                                               (uint8_t*)s_packed + (size_t)e * act_scale_bytes(N, K),
+                                               (hipStream_t)stream))
+      return st;
+  }
+  return MXFP8_OK;
+}
+
+int mxfp8_moe_linear_w4a4_workspace_bytes(int64_t x_rows, int64_t R, int64_t N, int64_t K, int64_t E, size_t* bytes) {
+  if (!bytes) return MXFP8_E_NULLPTR;
+  if (!experts_shape_ok(x_rows, R, N, K, E)) return MXFP8_E_SHAPE;
+  *bytes = experts_ws(x_rows, R, N, K, E);
+  return MXFP8_OK;
+}
+
+int mxfp8_moe_linear_w4a4(const void* x_bf16, int64_t x_rows, int64_t K, int64_t ldx, const int32_t* slot_of_row,
+                          int64_t topk, const int32_t* offsets, int64_t R, int64_t E, const void* w_packed,
+                          const void* s_packed, int64_t N, void* y_bf16, int64_t ldy, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  if (!experts_shape_ok(x_rows, R, N, K, E)) return MXFP8_E_SHAPE;
+  if (slot_of_row ? topk < 1 || topk > mxfp8::kMoeMaxTopk || x_rows * topk != R : x_rows != R) return MXFP8_E_SHAPE;
+  if (int st = check_weight(w_packed, s_packed, N, K)) return st;
+  if (R == 0) return MXFP8_OK;
+  if (!x_bf16 || !offsets) return MXFP8_E_NULLPTR;
+  if (ldx < K || ldx % 8 != 0) return MXFP8_E_LD;
+  if (!aligned(x_bf16, 16) || !aligned(offsets, 4) || !aligned(slot_of_row, 4)) return MXFP8_E_ALIGN;
+  if (int st = check_out(y_bf16, N, ldy, nullptr)) return st;
+  const size_t need = experts_ws(x_rows, R, N, K, E);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MXFP8_E_WORKSPACE;
+  if (!aligned(workspace, 256)) return MXFP8_E_ALIGN;
+  if (int st = mxfp8::check_device_current()) return st;
+  mxfp8::ExpertsArgs a = {};
+  a.x = x_bf16;
+  a.x_rows = x_rows;
+  a.ldx = ldx;
+  a.R = R;
+  a.K = K;
+  a.N = N;
+  a.E = E;
+  a.slots = slot_of_row;
+  a.topk = slot_of_row ? topk : 1;
+  a.offsets = offsets;
+  a.wp = w_packed;
+  a.wsp = s_packed;
+  a.y = y_bf16;
+  a.ldy = ldy;
+  const ExpertsForm f = experts_form(R, N, K, E);
+  if (f.decode) return mxfp8::launch_experts_fp4_decode(a, (hipStream_t)stream);
+  uint8_t* q = (uint8_t*)workspace;
+  uint8_t* s = q + experts_q_bytes(x_rows, K);
+  if (int st = mxfp8::launch_quantize_rows_fp4(x_bf16, x_rows, K, ldx, q, s, (hipStream_t)stream)) return st;
+  return mxfp8::launch_experts_fp4_tile(a, q, s, f.plan, (hipStream_t)stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,561 @@
+// Tile GEMM of two MXFP4 operands (both E2M1 with a UE8M0 scale per 32 along
+// K) for the dense layer and for the experts' products on sorted rows.
+//
+// On gfx950 the scaled MFMA multiplies 4-bit by 4-bit operands in half the
+// cycles of 8-bit ones, with half the operand bytes, so a 128-K step of a 256
+// x 256 tile is 64 MFMAs of 16 cycles per wave against 32 KiB of operands.
+//
+//  * Workgroup tile 32 NA weight rows x 32 NB activation rows, four waves as 2
+//    x 2, each 16 NA x 16 NB: NA x NB v_mfma_scale_f32_16x16x128 per 128-K
+//    step, the weight as the A operand; lane (i, g) ends with acc[a][b][j] =
+//    D[n = wn 16 NA + 16a + 4g + j][m = wm 16 NB + 16b + i].
+//  * A step's operands are copied straight into one of four LDS slots
+//    (buffer_load ... lds); the slot's fragments are read into registers one
+//    step ahead, while the MFMAs of the step before run, and the slot is
+//    refilled right after: at the start of step s the copies of s + 1 have
+//    landed, those of s + 2 and s + 3 are in flight and those of s + 4 go out
+//    between its MFMAs.  One barrier per step.
+//  * Persistent: a workgroup runs tiles b, b + gridDim.x, ...  The copy stream
+//    has its own position ("cursor"), four steps ahead, and runs on into the
+//    next tiles while a tile ends and is stored.
+//  * Scales: the packed operands' scale tiles of a pair of steps (256 K) are
+//    1 KiB per 128-row group: one copy per pair.  Gathered rows (kGather)
+//    bring four scale bytes per step each.
+#include <algorithm>
+
+#include "fp4.hpp"
+
+namespace mxfp8 {
+
+namespace {
+
+using tile::b2l_16;
+using tile::b2l_4;
+using tile::buffer_rsrc;
+using tile::i4v;
+
+constexpr int kThreads = 256;
+constexpr int kRing = 4;
+
+template <int NA, int NB, bool kGather>
+struct Fp4Lds {
+  static constexpr int kRowsN = 32 * NA, kRowsM = 32 * NB;
+  static constexpr int kW = kRowsN * 64, kX = kRowsM * 64;
+  static constexpr int kXScale = kGather ? 1024 : 0;       // 256 bytes per wave
+  static constexpr int kSlot = kW + kX + kXScale;          // one 128-K step
+  static constexpr int kRunsW = NA / 4, kRunsX = kGather ? 0 : (NB + 3) / 4;   // scale runs of 1 KiB per pair
+  static constexpr int kScale = (kRunsW + kRunsX) * 1024;  // one pair of steps
+  static constexpr int kPitch = 16 * NA + 8;               // bf16 per staged output row
+  static constexpr int kEpiWave = 16 * kPitch * 2;
+  static constexpr int kBiasSlot = 512;                    // a tile's bias, 256 bytes per wave column
+  static constexpr int kScaleAt = kRing * kSlot;
+  static constexpr int kEpiAt = kScaleAt + 2 * kScale;
+  static constexpr int kBiasAt = kEpiAt + 4 * kEpiWave;
+  static constexpr int kIndexAt = kBiasAt;                 // kGather: row indices instead of a bias
+  static constexpr int kBytes = kBiasAt + (kGather ? 2 * 1024 : 4 * kBiasSlot);
+  static constexpr int kCopies = NA / 2 + NB / 2 + (kGather ? 1 : 0);   // per wave and step, without scale runs
+};
+
+struct Fp4Args {
+  const uint8_t* q;        // activations: packed, or row-major [x_rows, K / 2]
+  const uint8_t* s;
+  uint32_t q_bytes, s_bytes;   // kGather: sizes of q and s
+  int M, K;                // dense: activation rows
+  const uint8_t* wp;
+  const uint8_t* wsp;
+  int N;
+  const uint16_t* bias;
+  uint16_t* y;
+  int64_t ldy;
+  int vec;                 // y 16-byte aligned, ldy % 8 == 0
+  // experts
+  int R, E, topk;
+  const int* slots;        // or null: row r of q
+  const int* offsets;
+};
+
+// One tile of the list.
+struct Fp4Job {
+  int row0, row_end;       // output rows [row0, row_end) at most
+  int col0;
+  int64_t wgroup;          // its first 128-row group of the packed weight
+  bool live;
+};
+
+// Tiles of the dense layer: groups of kGroupM M-tiles, N inside, so that the
+// workgroups of a die share operands in its L2.
+constexpr int kGroupM = 4;
+template <int NA, int NB>
+struct DenseTiles {
+  int tiles_m, tiles_n, total;
+  __device__ DenseTiles(const Fp4Args& p) {
+    tiles_m = (p.M + 32 * NB - 1) / (32 * NB);
+    tiles_n = (p.N + 32 * NA - 1) / (32 * NA);
+    total = tiles_m * tiles_n;
+  }
+  __device__ Fp4Job job(const Fp4Args& p, int b) const {
+    Fp4Job j;
+    j.live = b < total;
+    const int logical = xcd_remap(j.live ? b : 0, total);
+    const int per_group = kGroupM * tiles_n;
+    const int group = logical / per_group, first_m = group * kGroupM;
+    const int gm = min(tiles_m - first_m, kGroupM);
+    const int in_group = logical - group * per_group;
+    const int tm = first_m + in_group % gm, tn = in_group / gm;
+    j.row0 = tm * 32 * NB;
+    j.row_end = p.M;
+    j.col0 = tn * 32 * NA;
+    j.wgroup = (int64_t)j.col0 / kGroupRows;
+    return j;
+  }
+};
+
+// Tiles of the experts: expert by expert, weight tile by weight tile, the
+// expert's row tiles inside.  Lane l holds experts 4 l .. 4 l + 3.
+template <int NA, int NB>
+struct ExpertTiles {
+  int first[4], rows[4], start[4];
+  int tiles_n, total, kept;
+  __device__ ExpertTiles(const Fp4Args& p) {
+    const int lane = threadIdx.x & 63;
+    tiles_n = (p.N + 32 * NA - 1) / (32 * NA);
+    int sum = 0, n[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int e = 4 * lane + u;
+      first[u] = min(max(p.offsets[min(e, p.E)], 0), p.R);
+      rows[u] = max(min(p.offsets[min(e + 1, p.E)], p.R) - first[u], 0);
+      n[u] = (rows[u] + 32 * NB - 1) / (32 * NB) * tiles_n;
+      sum += n[u];
+    }
+    int run = sum;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int o = __shfl_up(run, off);
+      if (lane >= off) run += o;
+    }
+    total = __builtin_amdgcn_readlane(run, 63);
+    run -= sum;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      start[u] = run;
+      run += n[u];
+    }
+    kept = max(__builtin_amdgcn_readfirstlane(p.offsets[p.E]), 0);
+  }
+  __device__ Fp4Job job(const Fp4Args& p, int b) const {
+    Fp4Job j;
+    j.live = b < total;
+    if (!j.live) {
+      j.row0 = j.row_end = j.col0 = 0;
+      j.wgroup = 0;
+      return j;
+    }
+    const int t = xcd_remap(b, total);
+    // The last expert that starts at or before t (one without tiles starts
+    // where the next one does).
+    int at = -1;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) at += __popcll(__ballot(start[u] <= t));
+    const int e = __builtin_amdgcn_readfirstlane(at);
+    const int l = e >> 2, u = e & 3;
+    auto pick = [&](const int (&v)[4]) {
+      return __builtin_amdgcn_readlane(u == 0 ? v[0] : u == 1 ? v[1] : u == 2 ? v[2] : v[3], l);
+    };
+    const int n = pick(rows), r0 = pick(first), inside = t - pick(start);
+    const int tiles_m = (n + 32 * NB - 1) / (32 * NB);
+    const int tn = inside / tiles_m, tm = inside - tn * tiles_m;
+    j.row0 = r0 + tm * 32 * NB;
+    j.row_end = r0 + n;
+    j.col0 = tn * 32 * NA;
+    j.wgroup = (int64_t)e * ((p.N + kGroupRows - 1) / kGroupRows) + j.col0 / kGroupRows;
+    return j;
+  }
+};
+
+}  // namespace
+
+template <int NA, int NB, bool kGather, bool kExperts>
+__global__ __launch_bounds__(kThreads, (NA * NB >= 32 ? 1 : 2)) void gemm_fp4_kernel(Fp4Args p) {
+  using L = Fp4Lds<NA, NB, kGather>;
+  using Tiles = typename std::conditional<kExperts, ExpertTiles<NA, NB>, DenseTiles<NA, NB>>::type;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wave >> 1, wm = wave & 1;
+  const int li = lane & 15, lg = lane >> 4;
+  const int KS4 = p.K / 128;                                  // 128-K steps: even, at least 2
+  const int GN = (p.N + kGroupRows - 1) / kGroupRows;         // weight groups (of one expert)
+  const int GM = kGather ? 0 : (p.M + kGroupRows - 1) / kGroupRows;
+  const uint32_t gbytes = (uint32_t)KS4 * kTileBytes, sbytes = (uint32_t)KS4 * 2 * kTileScaleBytes;
+  const Tiles tiles(p);
+
+  if constexpr (kExperts) {
+    // Rows of slots without an expert: zeros.
+    const int64_t n = (int64_t)(p.R - tiles.kept) * p.N;
+    const int64_t stride = (int64_t)gridDim.x * kThreads;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + tid; i < n; i += stride) {
+      const int64_t r = i / p.N;
+      p.y[(tiles.kept + r) * p.ldy + (i - r * p.N)] = 0;
+    }
+  }
+  int b = blockIdx.x;
+  if (b >= tiles.total) return;
+
+  // ------------------------------------------------------------ the copies
+  // The cursor: tile cb, step cq of it; sources of its tile.  Past the last
+  // tile the sources are empty: the copies bring zeros, without touching
+  // memory, and every wait counts the same.
+  int cb = b, cq = 0, ctile = 0;
+  i4v w0, w1, x0, x1, sc, xsr;
+  uint32_t vx[NB / 2], vxs = 0;
+  const uint32_t lo16 = (uint32_t)lane * 16u;
+  const uint32_t band = (uint32_t)KS4 * kPieceBytes;          // bytes of a 16-row band
+  auto bias_slot = [&](int t) { return smem + L::kBiasAt + (t & 3) * L::kBiasSlot; };
+  auto index_slot = [&](int t) { return smem + L::kIndexAt + (t & 1) * 1024 + wave * 256; };
+  // The row of the tile that entry `lane` of the wave's share stands for:
+  // rows 16 wave + 64 i + (0 .. 15), i = lane / 16.
+  const int my_row = 64 * (lane >> 4) + 16 * wave + (lane & 15);
+  auto fetch_index = [&](const Fp4Job& j, int t) {
+    if constexpr (kGather) {
+      if (p.slots != nullptr) {
+        const i4v r = buffer_rsrc(p.slots, j.live ? (uint32_t)p.R * 4u : 0u);
+        b2l_4((uint32_t)min(j.row0 + my_row, j.row_end - 1) * 4u, r, 0u, index_slot(t));
+      }
+    }
+  };
+  auto set_sources = [&](const Fp4Job& j, int t) {
+    const int last = GN - 1 - j.col0 / kGroupRows;            // groups behind the first one
+    const uint32_t live = j.live ? 1u : 0u;
+    w0 = buffer_rsrc(p.wp + (size_t)j.wgroup * gbytes, live * gbytes);
+    if constexpr (NA == 8) w1 = buffer_rsrc(p.wp + (size_t)(j.wgroup + min(1, last)) * gbytes, live * gbytes);
+    const uint8_t* srun = p.wsp + (size_t)j.wgroup * sbytes;  // this wave's scale run
+    if (NA == 8 && wave == 1) srun = p.wsp + (size_t)(j.wgroup + min(1, last)) * sbytes;
+    if constexpr (kGather) {
+      int row = min(j.row0 + my_row, j.row_end - 1);
+      if (p.slots != nullptr) {
+        row = *reinterpret_cast<const int*>(index_slot(t) + lane * 4);
+        row = j.live ? row / p.topk : 0;
+      }
+      row = j.live ? row : 0;
+      xsr = buffer_rsrc(p.s, live * p.s_bytes);
+      x0 = buffer_rsrc(p.q, live * p.q_bytes);
+      vxs = (uint32_t)row * (uint32_t)(p.K / 32);
+#pragma unroll
+      for (int i = 0; i < NB / 2; ++i) {
+        const uint32_t r = (uint32_t)__shfl(row, 16 * i + (lane >> 2));
+        const int tr = 64 * i + 16 * wave + (lane >> 2);      // its row in the tile
+        vx[i] = r * (uint32_t)(p.K / 2) + (uint32_t)((lane & 3) ^ swz(tr)) * 16u;
+      }
+    } else {
+      const int xg = j.row0 / kGroupRows;
+      x0 = buffer_rsrc(p.q + (size_t)xg * gbytes, live * gbytes);
+      if constexpr (NB == 8) x1 = buffer_rsrc(p.q + (size_t)min(xg + 1, GM - 1) * gbytes, live * gbytes);
+      const int first = NB == 2 ? (j.row0 % kGroupRows) / 16 : 0;
+      vx[0] = (uint32_t)(first + wave) * band + lo16;
+      if (wave >= L::kRunsW) srun = p.s + (size_t)min(xg + wave - L::kRunsW, GM - 1) * sbytes;
+    }
+    sc = buffer_rsrc(srun, live * sbytes);
+    if constexpr (!kGather) {
+      if (p.bias != nullptr && wm == 0) {
+        // this wave column's 16 NA bias values, by whole words (an odd N's last
+        // word holds one value that is not the bias's and reaches no output)
+        const int c = j.col0 + wn * 16 * NA;
+        const uint32_t words = (uint32_t)(max(0, min(16 * NA, p.N - c)) + 1) / 2;
+        const i4v r = buffer_rsrc(reinterpret_cast<const uint8_t*>(p.bias) + 2 * (size_t)c, live * words * 4u);
+        b2l_4((uint32_t)lane * 4u, r, 0u, bias_slot(t) + wn * 256);
+      }
+    }
+  };
+  const uint32_t vw = (uint32_t)wave * band + lo16;
+  // Copy k of step cq into ring slot st (k < kCopies: the operands).
+  auto issue = [&](int k, int q, uint8_t* st) {
+    const uint32_t off = (uint32_t)q * kPieceBytes;
+    uint8_t* base = st + wave * 1024;
+    if (k < NA / 2) {
+      const uint32_t v = vw + (uint32_t)(k & 1) * 4u * band;
+      b2l_16(v, k < 2 ? w0 : w1, off, base + k * 4096);
+    } else if (k < NA / 2 + NB / 2) {
+      const int i = k - NA / 2;
+      if constexpr (kGather) b2l_16(vx[i], x0, (uint32_t)q * 64u, base + L::kW + i * 4096);
+      else b2l_16(vx[0] + (uint32_t)(i & 1) * 4u * band, i < 2 ? x0 : x1, off, base + L::kW + i * 4096);
+    } else {
+      b2l_4(vxs, xsr, (uint32_t)q * 4u, st + L::kW + L::kX + wave * 256);
+    }
+  };
+  const bool has_run = wave < L::kRunsW + L::kRunsX;
+  auto issue_scales = [&](int q, int pair) {
+    if (has_run)
+      b2l_16(lo16, sc, (uint32_t)q * 2u * kTileScaleBytes, smem + L::kScaleAt + pair * L::kScale + wave * 1024);
+  };
+  auto advance_tile = [&](const Fp4Job& next_next) {
+    // (called with cb already on the new tile; its indices are in LDS)
+    set_sources(tiles.job(p, cb), ctile);
+    fetch_index(next_next, ctile + 1);
+  };
+
+  // ------------------------------------------------------------ fragments
+  struct Frags {
+    i4v a[NA], b[NB];
+    int sa[2], sb[kGather ? NB : 2];
+  };
+  // A wave's rows of a 128-row group start at 16 NA wn (NA = 8: its own group)
+  // and share the swizzle of row li.
+  const int offA = tile_off(wn * 16 * NA + li, lg);
+  const int offB = L::kW + tile_off(wm * 16 * NB + li, lg);
+  // Scale words of a packed operand: lane (i, g) supplies MX block g of the
+  // step, block g % 2 of its scale tile g / 2; word e holds rows 16e + i + 32k
+  // in byte k; rows that start at 32 z of the group: the word shifted by 8 z.
+  const int offS = (lg >> 1) * kTileScaleBytes + scale_off(li, lg & 1);
+  const int shiftA = NA == 8 ? 0 : 16 * wn;
+  const int offSA = (NA == 8 ? wn * 1024 : 0) + offS;
+  const int offSB = L::kRunsW * 1024 + (NB == 8 ? wm * 1024 : 0) + offS;
+  // Gathered rows: bytes [wave][entry] of 4 scale bytes, row 64 i + 16 w + r at
+  // entry 16 i + r of wave w's share.
+  const int offXS = L::kW + L::kX + li * 4 + lg + (NB == 8 ? wm * 128 : NB == 4 ? wm * 64 : wm * 512);
+  int shiftB = NB == 8 ? 0 : NB == 4 ? 16 * wm : 8 * wm;     // NB == 2: and the tile's half of its group
+  constexpr int kReads = 4 + NA + NB + (kGather ? NB - 2 : 0);
+  // Read r of a step's fragments: the scales first.
+  auto read_part = [&](int r, Frags& f, const uint8_t* st, const uint8_t* sct) {
+    constexpr int kSB = kGather ? NB : 2;
+    if (r < 2) {
+      f.sa[r] = (int)((uint32_t)*reinterpret_cast<const int*>(sct + offSA + 128 * r) >> shiftA);
+    } else if (r < 2 + kSB) {
+      const int e = r - 2;
+      if constexpr (kGather) {
+        // 16-row block q = NB wm + e: wave q % 4's share, entries 16 (q / 4) ..
+        f.sb[e] = st[offXS + (NB == 8 ? (e & 3) * 256 + (e >> 2) * 64 : e * 256)];
+      } else {
+        f.sb[e] = (int)((uint32_t)*reinterpret_cast<const int*>(sct + offSB + 128 * e) >> shiftB);
+      }
+    } else if (r < 2 + kSB + NA) {
+      const int a = r - 2 - kSB;
+      f.a[a] = *reinterpret_cast<const i4v*>(st + offA + 1024 * a);
+    } else {
+      const int bb = r - 2 - kSB - NA;
+      f.b[bb] = *reinterpret_cast<const i4v*>(st + offB + 1024 * bb);
+    }
+  };
+
+  v4f acc[NA][NB];
+  // One step: its fragments are in cur; reads those of the step behind it from
+  // slot `next` (scales at nsc) and copies step q of the cursor's tile into
+  // slot `free`.  The scales of the cursor's pair go out first in a pair's
+  // second step (kSecond): until then the pair they replace is still read.
+  auto step = [&](auto kSecond, const Frags& cur, Frags& nxt, uint8_t* free, const uint8_t* next, int pair,
+                  const uint8_t* nsc, int q) {
+    constexpr int kJ = NA * NB;
+    // The operand copies of two steps behind the next one may be in flight;
+    // what else was issued since makes the wait only stricter.
+    tile::wait_vmcnt<2 * L::kCopies>();
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    constexpr int kSpan = kJ >= 32 ? kJ * 3 / 4 : kJ;       // MFMAs over which reads and copies are spread
+    if constexpr (decltype(kSecond)::value) issue_scales(q - 1, pair);
+    tile::static_for<0, kJ>([&](auto J) {
+      constexpr int j = decltype(J)::value;
+      constexpr int a = j % NA, bb = j / NA;
+      // op_sel: the byte of the scale word (packed), byte 0 of the lane's own
+      // (gathered).
+      constexpr int selA = a >> 1, selB = kGather ? 0 : (NB == 2 ? 0 : bb >> 1);
+      mfma16_fp4<selA, selB>(acc[a][bb], cur.a[a], cur.b[bb], cur.sa[a & 1], cur.sb[kGather ? bb : bb & 1]);
+      if constexpr (j < kSpan) {
+        tile::static_for<j * kReads / kSpan, (j + 1) * kReads / kSpan>(
+            [&](auto R) { read_part(decltype(R)::value, nxt, next, nsc); });
+        tile::static_for<j * L::kCopies / kSpan, (j + 1) * L::kCopies / kSpan>(
+            [&](auto C) { issue(decltype(C)::value, q, free); });
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  using T = std::true_type;
+  using F = std::false_type;
+
+  // ------------------------------------------------------------ start
+  auto slot = [&](int s) { return smem + s * L::kSlot; };
+  auto scale_slot = [&](int pair) { return smem + L::kScaleAt + pair * L::kScale; };
+  // Moves the cursor over a pair of steps.
+  auto move_cursor = [&]() {
+    cq += 2;
+    if (cq == KS4) {
+      cq = 0;
+      cb += (int)gridDim.x;
+      ++ctile;
+      if constexpr (kGather) {
+        // The new tile's indices were fetched a tile ago: with fewer than four
+        // steps per tile their copies may not have been waited for.
+        if (KS4 < 4) tile::wait_vmcnt<0>();
+      }
+      advance_tile(kGather ? tiles.job(p, cb + (int)gridDim.x) : Fp4Job{});
+    }
+  };
+  {
+    const Fp4Job j = tiles.job(p, b);
+    fetch_index(j, 0);
+    if constexpr (kGather) tile::wait_vmcnt<0>();
+    set_sources(j, 0);
+    if constexpr (kGather) fetch_index(tiles.job(p, b + (int)gridDim.x), 1);
+  }
+  for (int pair = 0; pair < 2; ++pair) {
+    issue_scales(cq, pair);
+#pragma unroll
+    for (int k = 0; k < L::kCopies; ++k) issue(k, cq, slot(2 * pair));
+#pragma unroll
+    for (int k = 0; k < L::kCopies; ++k) issue(k, cq + 1, slot(2 * pair + 1));
+    if (kGather && pair == 1) tile::wait_vmcnt<0>();   // (the second tile's indices)
+    move_cursor();
+  }
+  tile::wait_vmcnt<0>();
+  __builtin_amdgcn_s_barrier();
+  Frags f0, f1;
+  auto tile_shift = [&](const Fp4Job& j) {
+    if constexpr (NB == 2 && !kGather) shiftB = 8 * (2 * ((j.row0 % kGroupRows) / 64) + wm);
+  };
+  Fp4Job cur = tiles.job(p, b);
+  tile_shift(cur);
+  tile::static_for<0, kReads>([&](auto R) { read_part(decltype(R)::value, f0, slot(0), scale_slot(0)); });
+
+  int pair = 0, t = 0;
+  for (;;) {
+    if (!kGather && p.bias != nullptr) {
+      const uint8_t* bs = bias_slot(t) + wn * 256;
+#pragma unroll
+      for (int a = 0; a < NA; ++a) {
+        const uint2 w = *reinterpret_cast<const uint2*>(bs + (16 * a + 4 * lg) * 2);
+        const v4f v = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+#pragma unroll
+        for (int c = 0; c < NB; ++c) acc[a][c] = v;
+      }
+    } else {
+#pragma unroll
+      for (int a = 0; a < NA; ++a)
+#pragma unroll
+        for (int c = 0; c < NB; ++c) acc[a][c] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+#pragma unroll
+    for (int a = 0; a < NA; ++a)
+#pragma unroll
+      for (int c = 0; c < NB; ++c) asm volatile("" : "+a"(acc[a][c]));
+    const int nb = b + (int)gridDim.x;
+    const Fp4Job nxt = tiles.job(p, nb);
+    for (int q = 0; q < KS4; q += 2) {
+      step(F{}, f0, f1, slot(2 * pair), slot(2 * pair + 1), pair, scale_slot(pair) + 2 * kTileScaleBytes, cq);
+      // (the last step of a tile reads the next tile's first fragments)
+      if (q + 2 == KS4) tile_shift(nxt);
+      step(T{}, f1, f0, slot(2 * pair + 1), slot(2 * (pair ^ 1)), pair, scale_slot(pair ^ 1), cq + 1);
+      move_cursor();
+      pair ^= 1;
+    }
+    // The last MFMAs must retire before the accumulators are read.
+    asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15" ::: "memory");
+
+    // ---------------------------------------------------------- epilogue
+    // The wave stages 16 rows at a time as bf16 and stores 16-byte pieces of
+    // whole row segments (a wave's LDS accesses run in order: no waits).
+    {
+      typedef unsigned int u4v __attribute__((ext_vector_type(4)));
+      uint8_t* reg = smem + L::kEpiAt + wave * L::kEpiWave;
+      const int nw = cur.col0 + wn * 16 * NA, mw = cur.row0 + wm * 16 * NB;
+      constexpr int kLanesRow = 2 * NA, kRows = 64 / kLanesRow, kPasses = 16 / kRows;
+      const int rr = lane / kLanesRow, cc = (lane % kLanesRow) * 8;
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+#pragma unroll
+        for (int a = 0; a < NA; ++a) {
+          const v4f v = acc[a][k];
+          *reinterpret_cast<uint2*>(reg + (li * L::kPitch + 16 * a + 4 * lg) * 2) =
+              make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        }
+        u4v o[kPasses];
+#pragma unroll
+        for (int r = 0; r < kPasses; ++r)
+          o[r] = *reinterpret_cast<const u4v*>(reg + ((rr + kRows * r) * L::kPitch + cc) * 2);
+#pragma unroll
+        for (int r = 0; r < kPasses; ++r) {
+          const int m = mw + 16 * k + rr + kRows * r, n = nw + cc;
+          if (m >= cur.row_end || n >= p.N) continue;
+          uint16_t* d = p.y + (size_t)m * p.ldy + n;
+          if (p.vec && n + 7 < p.N) {
+            __builtin_nontemporal_store(o[r], reinterpret_cast<u4v*>(d));
+          } else {
+            for (int e = 0; e < 8; ++e)
+              if (n + e < p.N) d[e] = (uint16_t)(o[r][e >> 1] >> (16 * (e & 1)));
+          }
+        }
+      }
+    }
+    if (!nxt.live) break;
+    b = nb;
+    cur = nxt;
+    ++t;
+  }
+  // No copy may write into LDS that is no longer this workgroup's.
+  tile::wait_vmcnt<0>();
+}
+
+namespace {
+
+template <int NA, int NB, bool kGather, bool kExperts>
+int go(const Fp4Args& p, int64_t tiles, hipStream_t stream) {
+  using L = Fp4Lds<NA, NB, kGather>;
+  auto kern = gemm_fp4_kernel<NA, NB, kGather, kExperts>;
+  static std::atomic<int> lds_set[kMaxDevices];
+  if (!set_lds_limit_once((const void*)kern, L::kBytes, lds_set)) return -7;
+  const int64_t per_cu = L::kBytes <= 80 * 1024 ? 2 : 1;
+  const int64_t cus = device_cu_count();
+  const int64_t most = std::max<int64_t>(1, (cus >= 8 ? cus - cus % 8 : cus) * per_cu);
+  hipLaunchKernelGGL(kern, dim3((unsigned)std::min(tiles, most)), dim3(kThreads), L::kBytes, stream, p);
+  return hipGetLastError() == hipSuccess ? 0 : -7;
+}
+
+}  // namespace
+
+int launch_gemm_fp4_tile(const void* qp, const void* sp, int64_t M, int64_t K, const void* wp, const void* wsp,
+                         int64_t N, const void* bias, void* y, int64_t ldy, hipStream_t stream, Fp4Plan plan) {
+  Fp4Args p = {};
+  p.q = (const uint8_t*)qp;
+  p.s = (const uint8_t*)sp;
+  p.M = (int)M;
+  p.K = (int)K;
+  p.wp = (const uint8_t*)wp;
+  p.wsp = (const uint8_t*)wsp;
+  p.N = (int)N;
+  p.bias = (const uint16_t*)bias;
+  p.y = (uint16_t*)y;
+  p.ldy = ldy;
+  p.vec = ldy % 8 == 0 && ((uintptr_t)y & 15) == 0;
+  const int64_t tiles = ((M + plan.mt - 1) / plan.mt) * ((N + plan.nt - 1) / plan.nt);
+  if (plan.nt == 256) return go<8, 8, false, false>(p, tiles, stream);
+  if (plan.mt == 128) return go<4, 4, false, false>(p, tiles, stream);
+  return go<4, 2, false, false>(p, tiles, stream);
+}
+
+int launch_experts_fp4_tile(const ExpertsArgs& a, const void* q, const void* s, Fp4Plan plan, hipStream_t stream) {
+  Fp4Args p = {};
+  p.q = (const uint8_t*)q;
+  p.s = (const uint8_t*)s;
+  p.q_bytes = (uint32_t)(a.x_rows * (a.K / 2));
+  p.s_bytes = (uint32_t)(a.x_rows * (a.K / 32));
+  p.K = (int)a.K;
+  p.wp = (const uint8_t*)a.wp;
+  p.wsp = (const uint8_t*)a.wsp;
+  p.N = (int)a.N;
+  p.y = (uint16_t*)a.y;
+  p.ldy = a.ldy;
+  p.vec = a.ldy % 8 == 0 && ((uintptr_t)a.y & 15) == 0;
+  p.R = (int)a.R;
+  p.E = (int)a.E;
+  p.topk = (int)a.topk;
+  p.slots = a.slots;
+  p.offsets = a.offsets;
+  // At most one more row tile per expert than the rows fill.
+  const int64_t row_tiles = a.R / plan.mt + std::min(a.E, a.R);
+  const int64_t tiles = row_tiles * ((a.N + plan.nt - 1) / plan.nt);
+  if (plan.nt == 256) return go<8, 4, true, true>(p, tiles, stream);
+  if (plan.mt == 128) return go<4, 4, true, true>(p, tiles, stream);
+  return go<4, 2, true, true>(p, tiles, stream);
+}
+
+}  // namespace mxfp8

@@ -1,0 +1,93 @@
+// Internal launchers of the MXFP4 x MXFP4 linear layer, of tokens sorted by
+// expert and back, and of the experts' MXFP4 products.  As in launch.hpp,
+// arguments were validated by the C entry points (api_fp4.cpp), and each
+// returns 0 or -7 (launch error).
+#pragma once
+
+#include "launch.hpp"
+
+namespace mxfp8 {
+
+constexpr int64_t kFp4Step = 128;   // elements of one 4-bit K step (64 bytes of a row)
+
+// x bf16 [M, K] -> the packed 4-bit operand (the layout of
+// launch_pack_weight_fp4 with M in place of N; pad rows zero).
+int launch_quantize_packed_fp4(const void* x, int64_t M, int64_t K, int64_t ldx, void* qp, void* sp,
+                               hipStream_t stream);
+// The same as row-major bytes: q [M, K / 2], s [M, K / 32].
+int launch_quantize_rows_fp4(const void* x, int64_t M, int64_t K, int64_t ldx, void* q, void* s, hipStream_t stream);
+
+// Decode GEMM: M <= 16 bf16 rows, quantized inside, against a packed MXFP4
+// weight; K <= kFp4DecodeMaxK.
+constexpr int64_t kFp4DecodeMaxM = 16;
+constexpr int64_t kFp4DecodeMaxK = 8192;
+int launch_gemm_fp4_decode(const void* x, int64_t ldx, int64_t M, int64_t K, const void* wp, const void* wsp,
+                           int64_t N, const void* bias, void* y, int64_t ldy, hipStream_t stream);
+
+// Tile GEMM of two packed MXFP4 operands.
+struct Fp4Plan {
+  int nt, mt;   // weight and activation rows of a workgroup's tile: 256 x 256, 128 x 128 or 128 x 64
+};
+int launch_gemm_fp4_tile(const void* qp, const void* sp, int64_t M, int64_t K, const void* wp, const void* wsp,
+                         int64_t N, const void* bias, void* y, int64_t ldy, hipStream_t stream, Fp4Plan plan);
+
+// Rows by expert (moe_order.hip).  R = T topk slots; `rows` [R]: the sorted
+// row of each slot, `slots` [R]: its inverse, `offsets` [E + 1]: the first row
+// of each expert and the number of rows that have one (kept = offsets + E).
+struct SortArgs {
+  const void* ids;   // [R] int32, or int64 if wide
+  int wide;
+  int64_t R, E;
+  int* rows;
+  int* slots;
+  int* offsets;
+  int* ws;
+};
+constexpr int kSortChunk = 1024;       // least slots of a workgroup
+constexpr int kSortMaxBlocks = 256;
+int64_t sort_blocks(int64_t R);
+inline size_t sort_ws_bytes(int64_t R, int64_t E) {
+  const int64_t n = sort_blocks(R);
+  return n <= 1 ? 0 : (size_t)n * (size_t)(E + 1) * 4;
+}
+int launch_moe_sort(const SortArgs& a, hipStream_t stream);
+
+struct PermuteArgs {
+  int bf16;                // element type of the matrices: bf16, or fp32
+  int64_t T, H, topk;
+  const int* rows;         // [T, topk]
+  const int* kept;         // [1]
+  const void* tokens;      // [T, H], row stride ldt: x (permute), dy (unpermute's gradient)
+  int64_t ldt;
+  const void* sorted;      // [T topk, H], row stride lds: ys
+  int64_t lds;
+  const float* weights;    // [T, topk] or null (all 1)
+  void* out_tokens;        // [T, H], row stride ldo: y, dx
+  void* out_sorted;        // [T topk, H], row stride ldo: xs, dys
+  int64_t ldo;
+  float* dweights;         // [T, topk] or null
+};
+int launch_moe_permute(const PermuteArgs& a, hipStream_t stream);             // out_sorted = tokens by row
+int launch_moe_unpermute(const PermuteArgs& a, hipStream_t stream);           // out_tokens = weighted sums of sorted
+int launch_moe_unpermute_backward(const PermuteArgs& a, hipStream_t stream);  // out_sorted, dweights
+
+// The experts' products on sorted rows: y[r] = deq(q(x[r])) deq(W[e(r)])^T.
+struct ExpertsArgs {
+  const void* x;           // bf16 [rows, K], row stride ldx
+  int64_t x_rows, ldx;
+  int64_t R, K, N, E;
+  const int* slots;        // [R]: row r reads x row slots[r] / topk; null: x row r
+  int64_t topk;
+  const int* offsets;      // [E + 1]
+  const void* wp;          // packed weights, experts one after the other
+  const void* wsp;
+  void* y;                 // bf16 [R, N], row stride ldy
+  int64_t ldy;
+  void* ws;                // quantized rows
+};
+// Decode form: quantizes inside, no workspace.
+int launch_experts_fp4_decode(const ExpertsArgs& a, hipStream_t stream);
+// Tile form on rows quantized into q [x_rows, K / 2], s [x_rows, K / 32].
+int launch_experts_fp4_tile(const ExpertsArgs& a, const void* q, const void* s, Fp4Plan plan, hipStream_t stream);
+
+}  // namespace mxfp8
