@@ -36,17 +36,40 @@ __device__ inline uint32_t fp4_absmax8(const uint4& v) {
   return max((uint32_t)m[0], (uint32_t)m[1]);
 }
 
-// c += A x B on v_mfma_scale_f32_16x16x128_f8f6f4 with both operands in E2M1
-// (cbsz, blgp 4): lane (i, g) holds K [32g, 32g + 32) of row i in four
-// registers; scales, in-place accumulation and wait states as in
-// tile::mfma16.
-template <int kSelA, int kSelB>
-__device__ __forceinline__ void mfma16_fp4(v4f& c, const tile::i4v& a, const tile::i4v& b, int sa, int sb) {
-  asm volatile(
-      "s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%6,0] op_sel_hi:[%7,%8,0] "
-      "cbsz:4 blgp:4"
-      : "+a"(c)
-      : "v"(a), "v"(b), "v"(sa), "v"(sb), "n"(kSelA & 1), "n"(kSelB & 1), "n"(kSelA >> 1), "n"(kSelB >> 1));
+// c[u] += A[u] x B, u = 0 .. 3, on v_mfma_scale_f32_16x16x128_f8f6f4 with both
+// operands in E2M1 (cbsz, blgp 4): lane (i, g) holds K [32g, 32g + 32) of row i
+// in four registers; scales (A[u]: word u % 2, byte kSelA + u / 2), in-place
+// accumulation and wait states as in tile::mfma16.  Four in one block: nothing
+// can come between them, so the wait states in front of the first serve all.
+// A 4-bit MFMA takes 16 cycles, in which the wave issues few other
+// instructions; with kCopy a copy into LDS (16 bytes per lane from voff + soff
+// of rsrc to lds + kAt + 16 lane) is issued between them, an MFMA in the place
+// of the wait state between the m0 write and the copy.
+template <int kSelA, int kSelB, bool kCopy, int kAt>
+__device__ __forceinline__ void mfma16x4_fp4(v4f& c0, v4f& c1, v4f& c2, v4f& c3, const tile::i4v* a,
+                                             const tile::i4v& b, int sa0, int sa1, int sb, uint32_t voff = 0,
+                                             tile::i4v rsrc = {}, uint32_t soff = 0, uint32_t lds = 0) {
+#define MXFP8_MFMA(C, A, S, LO, HI) \
+  "v_mfma_scale_f32_16x16x128_f8f6f4 " C ", " A ", %8, " C ", " S ", %11 op_sel:[" LO ",%16,0] op_sel_hi:[" HI ",%17,0] cbsz:4 blgp:4\n\t"
+#define MXFP8_OPERANDS                                                                                              \
+  "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "v"(b), "v"(sa0), "v"(sa1), "v"(sb), "n"(kSelA & 1), "n"(kSelA >> 1), \
+      "n"((kSelA + 1) & 1), "n"((kSelA + 1) >> 1), "n"(kSelB & 1), "n"(kSelB >> 1)
+  if constexpr (kCopy) {
+    asm volatile("s_nop 1\n\t" MXFP8_MFMA("%0", "%4", "%9", "%12", "%13")
+                 "s_add_u32 m0, %21, %22\n\t" MXFP8_MFMA("%1", "%5", "%10", "%12", "%13")
+                 "buffer_load_dwordx4 %18, %19, %20 offen lds\n\t" MXFP8_MFMA("%2", "%6", "%9", "%14", "%15")
+                 MXFP8_MFMA("%3", "%7", "%10", "%14", "%15")
+                 : "+a"(c0), "+a"(c1), "+a"(c2), "+a"(c3)
+                 : MXFP8_OPERANDS, "v"(voff), "s"(rsrc), "s"(soff), "s"(lds), "n"(kAt)
+                 : "memory", "m0", "scc");
+  } else {
+    asm volatile("s_nop 1\n\t" MXFP8_MFMA("%0", "%4", "%9", "%12", "%13") MXFP8_MFMA("%1", "%5", "%10", "%12", "%13")
+                 MXFP8_MFMA("%2", "%6", "%9", "%14", "%15") MXFP8_MFMA("%3", "%7", "%10", "%14", "%15")
+                 : "+a"(c0), "+a"(c1), "+a"(c2), "+a"(c3)
+                 : MXFP8_OPERANDS);
+  }
+#undef MXFP8_MFMA
+#undef MXFP8_OPERANDS
 }
 
 }  // namespace mxfp8

@@ -29,13 +29,27 @@ namespace mxfp8 {
 
 namespace {
 
-using tile::b2l_16;
-using tile::b2l_4;
 using tile::buffer_rsrc;
 using tile::i4v;
 
 constexpr int kThreads = 256;
 constexpr int kRing = 4;
+
+// tile::b2l_16 and b2l_4 with the LDS address as a base and a constant: one
+// scalar add into m0.
+template <int kAt>
+__device__ __forceinline__ void b2l_16(uint32_t voff, i4v rsrc, uint32_t soff, uint32_t lds) {
+  asm volatile("s_add_u32 m0, %3, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(rsrc),
+               "s"(soff), "s"(lds), "n"(kAt)
+               : "memory", "m0", "scc");
+}
+template <int kAt>
+__device__ __forceinline__ void b2l_4(uint32_t voff, i4v rsrc, uint32_t soff, uint32_t lds) {
+  asm volatile("s_add_u32 m0, %3, %4\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds" ::"v"(voff), "s"(rsrc),
+               "s"(soff), "s"(lds), "n"(kAt)
+               : "memory", "m0", "scc");
+}
+using tile::lds_addr;
 
 template <int NA, int NB, bool kGather>
 struct Fp4Lds {
@@ -45,8 +59,8 @@ struct Fp4Lds {
   static constexpr int kSlot = kW + kX + kXScale;          // one 128-K step
   static constexpr int kRunsW = NA / 4, kRunsX = kGather ? 0 : (NB + 3) / 4;   // scale runs of 1 KiB per pair
   static constexpr int kScale = (kRunsW + kRunsX) * 1024;  // one pair of steps
-  static constexpr int kPitch = 16 * NA + 8;               // bf16 per staged output row
-  static constexpr int kEpiWave = 16 * kPitch * 2;
+  static constexpr int kPitch = 32 * NA;                   // bytes of a staged output row
+  static constexpr int kEpiWave = 16 * kPitch;
   static constexpr int kBiasSlot = 512;                    // a tile's bias, 256 bytes per wave column
   static constexpr int kScaleAt = kRing * kSlot;
   static constexpr int kEpiAt = kScaleAt + 2 * kScale;
@@ -209,7 +223,8 @@ __global__ __launch_bounds__(kThreads, (NA * NB >= 32 ? 1 : 2)) void gemm_fp4_ke
   // memory, and every wait counts the same.
   int cb = b, cq = 0, ctile = 0;
   i4v w0, w1, x0, x1, sc, xsr;
-  uint32_t vx[NB / 2], vxs = 0;
+  uint32_t vx[NB / 2], vxhi = 0, vxs = 0;
+  const uint32_t lds0 = lds_addr(smem) + (uint32_t)wave * 1024u;   // this wave's share of a region
   const uint32_t lo16 = (uint32_t)lane * 16u;
   const uint32_t band = (uint32_t)KS4 * kPieceBytes;          // bytes of a 16-row band
   auto bias_slot = [&](int t) { return smem + L::kBiasAt + (t & 3) * L::kBiasSlot; };
@@ -221,7 +236,7 @@ __global__ __launch_bounds__(kThreads, (NA * NB >= 32 ? 1 : 2)) void gemm_fp4_ke
     if constexpr (kGather) {
       if (p.slots != nullptr) {
         const i4v r = buffer_rsrc(p.slots, j.live ? (uint32_t)p.R * 4u : 0u);
-        b2l_4((uint32_t)min(j.row0 + my_row, j.row_end - 1) * 4u, r, 0u, index_slot(t));
+        b2l_4<0>((uint32_t)min(j.row0 + my_row, j.row_end - 1) * 4u, r, 0u, lds_addr(index_slot(t)));
       }
     }
   };
@@ -254,6 +269,7 @@ __global__ __launch_bounds__(kThreads, (NA * NB >= 32 ? 1 : 2)) void gemm_fp4_ke
       if constexpr (NB == 8) x1 = buffer_rsrc(p.q + (size_t)min(xg + 1, GM - 1) * gbytes, live * gbytes);
       const int first = NB == 2 ? (j.row0 % kGroupRows) / 16 : 0;
       vx[0] = (uint32_t)(first + wave) * band + lo16;
+      vxhi = vx[0] + 4u * band;
       if (wave >= L::kRunsW) srun = p.s + (size_t)min(xg + wave - L::kRunsW, GM - 1) * sbytes;
     }
     sc = buffer_rsrc(srun, live * sbytes);
@@ -264,30 +280,39 @@ __global__ __launch_bounds__(kThreads, (NA * NB >= 32 ? 1 : 2)) void gemm_fp4_ke
         const int c = j.col0 + wn * 16 * NA;
         const uint32_t words = (uint32_t)(max(0, min(16 * NA, p.N - c)) + 1) / 2;
         const i4v r = buffer_rsrc(reinterpret_cast<const uint8_t*>(p.bias) + 2 * (size_t)c, live * words * 4u);
-        b2l_4((uint32_t)lane * 4u, r, 0u, bias_slot(t) + wn * 256);
+        b2l_4<0>((uint32_t)lane * 4u, r, 0u, lds_addr(bias_slot(t) + wn * 256));
       }
     }
   };
   const uint32_t vw = (uint32_t)wave * band + lo16;
-  // Copy k of step cq into ring slot st (k < kCopies: the operands).
-  auto issue = [&](int k, int q, uint8_t* st) {
+  // Copy k of step q of the cursor's tile into the ring slot at st (of this
+  // wave's share: + 1024 wave): calls go(LDS offset in the slot, vector offset,
+  // source, scalar offset).
+  const uint32_t vwhi = vw + 4u * band;
+  auto source = [&](auto kCopy, int q, auto&& go) {
+    constexpr int k = decltype(kCopy)::value;
     const uint32_t off = (uint32_t)q * kPieceBytes;
-    uint8_t* base = st + wave * 1024;
-    if (k < NA / 2) {
-      const uint32_t v = vw + (uint32_t)(k & 1) * 4u * band;
-      b2l_16(v, k < 2 ? w0 : w1, off, base + k * 4096);
-    } else if (k < NA / 2 + NB / 2) {
-      const int i = k - NA / 2;
-      if constexpr (kGather) b2l_16(vx[i], x0, (uint32_t)q * 64u, base + L::kW + i * 4096);
-      else b2l_16(vx[0] + (uint32_t)(i & 1) * 4u * band, i < 2 ? x0 : x1, off, base + L::kW + i * 4096);
+    if constexpr (k < NA / 2) {
+      go(std::integral_constant<int, k * 4096>{}, k & 1 ? vwhi : vw, k < 2 ? w0 : w1, off);
     } else {
-      b2l_4(vxs, xsr, (uint32_t)q * 4u, st + L::kW + L::kX + wave * 256);
+      constexpr int i = k - NA / 2;
+      constexpr std::integral_constant<int, L::kW + i * 4096> at;
+      if constexpr (kGather) go(at, vx[i], x0, (uint32_t)q * 64u);
+      else go(at, i & 1 ? vxhi : vx[0], i < 2 ? x0 : x1, off);
+    }
+  };
+  constexpr int kData = NA / 2 + NB / 2;                      // (and with gathered rows their scales)
+  auto issue = [&](auto kCopy, int q, uint32_t st) {
+    if constexpr (decltype(kCopy)::value < kData) {
+      source(kCopy, q, [&](auto at, uint32_t v, i4v r, uint32_t off) { b2l_16<decltype(at)::value>(v, r, off, st); });
+    } else {
+      b2l_4<0>(vxs, xsr, (uint32_t)q * 4u, st - (uint32_t)wave * 768u + (uint32_t)(L::kW + L::kX));
     }
   };
   const bool has_run = wave < L::kRunsW + L::kRunsX;
   auto issue_scales = [&](int q, int pair) {
     if (has_run)
-      b2l_16(lo16, sc, (uint32_t)q * 2u * kTileScaleBytes, smem + L::kScaleAt + pair * L::kScale + wave * 1024);
+      b2l_16<L::kScaleAt>(lo16, sc, (uint32_t)q * 2u * kTileScaleBytes, lds0 + (uint32_t)(pair * L::kScale));
   };
   auto advance_tile = [&](const Fp4Job& next_next) {
     // (called with cb already on the new tile; its indices are in LDS)
@@ -343,29 +368,45 @@ __global__ __launch_bounds__(kThreads, (NA * NB >= 32 ? 1 : 2)) void gemm_fp4_ke
   // slot `next` (scales at nsc) and copies step q of the cursor's tile into
   // slot `free`.  The scales of the cursor's pair go out first in a pair's
   // second step (kSecond): until then the pair they replace is still read.
-  auto step = [&](auto kSecond, const Frags& cur, Frags& nxt, uint8_t* free, const uint8_t* next, int pair,
+  // The MFMAs go in blocks of four, each with a copy inside where there is one
+  // to issue, and the fragment reads spread between them.  The first kHead
+  // blocks run before the barrier, over the end of the step's own reads.
+  auto step = [&](auto kSecond, const Frags& cur, Frags& nxt, uint32_t free, const uint8_t* next, int pair,
                   const uint8_t* nsc, int q) {
-    constexpr int kJ = NA * NB;
-    // The operand copies of two steps behind the next one may be in flight;
-    // what else was issued since makes the wait only stricter.
-    tile::wait_vmcnt<2 * L::kCopies>();
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    constexpr int kSpan = kJ >= 32 ? kJ * 3 / 4 : kJ;       // MFMAs over which reads and copies are spread
-    if constexpr (decltype(kSecond)::value) issue_scales(q - 1, pair);
-    tile::static_for<0, kJ>([&](auto J) {
-      constexpr int j = decltype(J)::value;
-      constexpr int a = j % NA, bb = j / NA;
+    constexpr int kBlocks = NA * NB / 4, kHead = kBlocks / 8, kGaps = kBlocks - kHead;
+    tile::static_for<0, kBlocks>([&](auto J) {
+      constexpr int j = decltype(J)::value, g = j - kHead;
+      constexpr int a = 4 * j % NA, bb = 4 * j / NA;
+      if constexpr (g == 0) {
+        // Every wave has read this step's fragments (the slot may be refilled),
+        // and the next step's copies have landed: the operand copies of two
+        // steps behind it may be in flight; what else was issued since makes
+        // the wait only stricter.
+        tile::wait_vmcnt<2 * L::kCopies>();
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (decltype(kSecond)::value) issue_scales(q - 1, pair);
+      }
       // op_sel: the byte of the scale word (packed), byte 0 of the lane's own
       // (gathered).
-      constexpr int selA = a >> 1, selB = kGather ? 0 : (NB == 2 ? 0 : bb >> 1);
-      mfma16_fp4<selA, selB>(acc[a][bb], cur.a[a], cur.b[bb], cur.sa[a & 1], cur.sb[kGather ? bb : bb & 1]);
-      if constexpr (j < kSpan) {
-        tile::static_for<j * kReads / kSpan, (j + 1) * kReads / kSpan>(
+      constexpr int selA = a >> 1, selB = kGather ? 0 : (NB == 2 ? 0 : bb >> 1), sb = kGather ? bb : bb & 1;
+      constexpr int c0 = g < 0 ? 0 : g * L::kCopies / kGaps, c1 = g < 0 ? 0 : (g + 1) * L::kCopies / kGaps;
+      if constexpr (c1 > c0 && c0 < kData) {
+        source(std::integral_constant<int, c0>{}, q, [&](auto at, uint32_t v, i4v r, uint32_t off) {
+          mfma16x4_fp4<selA, selB, true, decltype(at)::value>(acc[a][bb], acc[a + 1][bb], acc[a + 2][bb], acc[a + 3][bb],
+                                                              cur.a + a, cur.b[bb], cur.sa[0], cur.sa[1], cur.sb[sb], v,
+                                                              r, off, free);
+        });
+      } else {
+        mfma16x4_fp4<selA, selB, false, 0>(acc[a][bb], acc[a + 1][bb], acc[a + 2][bb], acc[a + 3][bb], cur.a + a,
+                                           cur.b[bb], cur.sa[0], cur.sa[1], cur.sb[sb]);
+        if constexpr (c1 > c0) issue(std::integral_constant<int, c0>{}, q, free);
+      }
+      if constexpr (g >= 0) {
+        tile::static_for<c0 + 1, c1>([&](auto C) { issue(C, q, free); });
+        tile::static_for<g * kReads / kGaps, (g + 1) * kReads / kGaps>(
             [&](auto R) { read_part(decltype(R)::value, nxt, next, nsc); });
-        tile::static_for<j * L::kCopies / kSpan, (j + 1) * L::kCopies / kSpan>(
-            [&](auto C) { issue(decltype(C)::value, q, free); });
       }
       __builtin_amdgcn_sched_barrier(0);
     });
@@ -375,6 +416,7 @@ __global__ __launch_bounds__(kThreads, (NA * NB >= 32 ? 1 : 2)) void gemm_fp4_ke
 
   // ------------------------------------------------------------ start
   auto slot = [&](int s) { return smem + s * L::kSlot; };
+  auto fill = [&](int s) { return lds0 + (uint32_t)(s * L::kSlot); };
   auto scale_slot = [&](int pair) { return smem + L::kScaleAt + pair * L::kScale; };
   // Moves the cursor over a pair of steps.
   auto move_cursor = [&]() {
@@ -400,10 +442,8 @@ __global__ __launch_bounds__(kThreads, (NA * NB >= 32 ? 1 : 2)) void gemm_fp4_ke
   }
   for (int pair = 0; pair < 2; ++pair) {
     issue_scales(cq, pair);
-#pragma unroll
-    for (int k = 0; k < L::kCopies; ++k) issue(k, cq, slot(2 * pair));
-#pragma unroll
-    for (int k = 0; k < L::kCopies; ++k) issue(k, cq + 1, slot(2 * pair + 1));
+    tile::static_for<0, L::kCopies>([&](auto C) { issue(C, cq, fill(2 * pair)); });
+    tile::static_for<0, L::kCopies>([&](auto C) { issue(C, cq + 1, fill(2 * pair + 1)); });
     if (kGather && pair == 1) tile::wait_vmcnt<0>();   // (the second tile's indices)
     move_cursor();
   }
@@ -441,10 +481,10 @@ __global__ __launch_bounds__(kThreads, (NA * NB >= 32 ? 1 : 2)) void gemm_fp4_ke
     const int nb = b + (int)gridDim.x;
     const Fp4Job nxt = tiles.job(p, nb);
     for (int q = 0; q < KS4; q += 2) {
-      step(F{}, f0, f1, slot(2 * pair), slot(2 * pair + 1), pair, scale_slot(pair) + 2 * kTileScaleBytes, cq);
+      step(F{}, f0, f1, fill(2 * pair), slot(2 * pair + 1), pair, scale_slot(pair) + 2 * kTileScaleBytes, cq);
       // (the last step of a tile reads the next tile's first fragments)
       if (q + 2 == KS4) tile_shift(nxt);
-      step(T{}, f1, f0, slot(2 * pair + 1), slot(2 * (pair ^ 1)), pair, scale_slot(pair ^ 1), cq + 1);
+      step(T{}, f1, f0, fill(2 * pair + 1), slot(2 * (pair ^ 1)), pair, scale_slot(pair ^ 1), cq + 1);
       move_cursor();
       pair ^= 1;
     }
@@ -452,8 +492,9 @@ __global__ __launch_bounds__(kThreads, (NA * NB >= 32 ? 1 : 2)) void gemm_fp4_ke
     asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15" ::: "memory");
 
     // ---------------------------------------------------------- epilogue
-    // The wave stages 16 rows at a time as bf16 and stores 16-byte pieces of
-    // whole row segments (a wave's LDS accesses run in order: no waits).
+    // The wave stages 16 rows at a time as bf16 (16-byte chunk c of row r at c ^
+    // r % 8, against bank conflicts) and stores 16-byte pieces of whole row
+    // segments (a wave's LDS accesses run in order: no waits).
     {
       typedef unsigned int u4v __attribute__((ext_vector_type(4)));
       uint8_t* reg = smem + L::kEpiAt + wave * L::kEpiWave;
@@ -465,13 +506,13 @@ __global__ __launch_bounds__(kThreads, (NA * NB >= 32 ? 1 : 2)) void gemm_fp4_ke
 #pragma unroll
         for (int a = 0; a < NA; ++a) {
           const v4f v = acc[a][k];
-          *reinterpret_cast<uint2*>(reg + (li * L::kPitch + 16 * a + 4 * lg) * 2) =
+          *reinterpret_cast<uint2*>(reg + li * L::kPitch + (((2 * a + (lg >> 1)) ^ (li & 7)) << 4) + (lg & 1) * 8) =
               make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
         }
         u4v o[kPasses];
 #pragma unroll
         for (int r = 0; r < kPasses; ++r)
-          o[r] = *reinterpret_cast<const u4v*>(reg + ((rr + kRows * r) * L::kPitch + cc) * 2);
+          o[r] = *reinterpret_cast<const u4v*>(reg + (rr + kRows * r) * L::kPitch + (((cc >> 3) ^ ((rr + kRows * r) & 7)) << 4));
 #pragma unroll
         for (int r = 0; r < kPasses; ++r) {
           const int m = mw + 16 * k + rr + kRows * r, n = nw + cc;
