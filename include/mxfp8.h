@@ -564,9 +564,11 @@ int mxfp8_linear_w4a4(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, con
 /*
  * Test hook: pin the form of mxfp8_linear_w4a4, mxfp8_gemm_packed_fp4 and
  * mxfp8_moe_linear_w4a4: 0 = by shape, 1 = the decode form where it applies
- * (dense M <= 16, K <= 8192), 64 / 128 / 256 = tiles of 128 weight rows x 64 /
- * 128 rows, or 256 weight rows x 256 (dense) / 128 (experts) rows.  The
- * workspace queries follow it.  Process-wide; returns the previous value, or
+ * (dense M <= 16 and K <= 8192, or M <= 32 and K <= 4096; experts K <= 8192),
+ * 16 = the dense layer's form of 16 weight rows on packed activations where it
+ * applies (M <= 128), 64 / 128 / 256 = tiles of 128 weight rows x 64 / 128
+ * rows, or 256 weight rows x 256 (dense) / 128 (experts) rows.  The workspace
+ * queries follow it.  Process-wide; returns the previous value, or
  * MXFP8_E_SHAPE.
  */
 int mxfp8_debug_force_w4a4(int form);

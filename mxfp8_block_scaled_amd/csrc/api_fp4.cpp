@@ -35,19 +35,29 @@ std::atomic<int> g_force{0};
 bool decode_form(int64_t M, int64_t N, int64_t K) {
   (void)N;
   const int force = g_force.load(std::memory_order_relaxed);
-  return M <= mxfp8::kFp4DecodeMaxM && K <= mxfp8::kFp4DecodeMaxK && (force == 0 || force == 1);
+  return M <= mxfp8::fp4_decode_max_m(K) && (force == 0 || force == 1);
 }
 
+// The GEMM on packed activations: nt == 16 is the mid form.
 mxfp8::Fp4Plan tile_plan(int64_t M, int64_t N, int64_t K) {
   (void)K;
   const int force = g_force.load(std::memory_order_relaxed);
+  if (force == 16 && M <= mxfp8::kFp4MidMaxM) return {16, 128};
   if (force == 256) return {256, 256};
   if (force == 128) return {128, 128};
   if (force == 64) return {128, 64};
+  if (M <= mxfp8::kFp4MidMaxM) return {16, 128};
   const int64_t large = (M + 255) / 256 * ((N + 255) / 256);
   if (large >= 192) return {256, 256};
   const int64_t medium = (M + 127) / 128 * ((N + 127) / 128);
   return medium >= 192 ? mxfp8::Fp4Plan{128, 128} : mxfp8::Fp4Plan{128, 64};
+}
+
+int gemm(const void* q, const void* s, int64_t M, int64_t K, const void* wp, const void* wsp, int64_t N,
+         const void* bias, void* y, int64_t ldy, hipStream_t stream) {
+  const mxfp8::Fp4Plan plan = tile_plan(M, N, K);
+  if (plan.nt == 16) return mxfp8::launch_gemm_fp4_mid(q, s, M, K, wp, wsp, N, bias, y, ldy, stream);
+  return mxfp8::launch_gemm_fp4_tile(q, s, M, K, wp, wsp, N, bias, y, ldy, stream, plan);
 }
 
 int check_weight(const void* wp, const void* sp, int64_t N, int64_t K) {
@@ -108,7 +118,7 @@ bool experts_shape_ok(int64_t x_rows, int64_t R, int64_t N, int64_t K, int64_t E
 size_t experts_q_bytes(int64_t x_rows, int64_t K) { return round_up((size_t)x_rows * (size_t)(K / 2), 256); }
 size_t experts_ws(int64_t x_rows, int64_t R, int64_t N, int64_t K, int64_t E) {
   if (R == 0 || experts_form(R, N, K, E).decode) return 0;
-  return experts_q_bytes(x_rows, K) + round_up((size_t)x_rows * (size_t)(K / 32), 256);
+  return experts_q_bytes(x_rows, K) + round_up((size_t)x_rows * (size_t)mxfp8::fp4_scale_pitch(K), 256);
 }
 
 }  // namespace
@@ -146,8 +156,7 @@ int mxfp8_gemm_packed_fp4(const void* q_packed, const void* s_packed, int64_t M,
   if (int st = check_out(y_bf16, N, ldy, bias_bf16)) return st;
   if (!gemm_grid_ok(M, N)) return MXFP8_E_SHAPE;
   if (int st = mxfp8::check_device_current()) return st;
-  return mxfp8::launch_gemm_fp4_tile(q_packed, s_packed, M, K, w_packed, ws_packed, N, bias_bf16, y_bf16, ldy,
-                                     (hipStream_t)stream, tile_plan(M, N, K));
+  return gemm(q_packed, s_packed, M, K, w_packed, ws_packed, N, bias_bf16, y_bf16, ldy, (hipStream_t)stream);
 }
 
 int mxfp8_linear_w4a4_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes) {
@@ -178,12 +187,11 @@ int mxfp8_linear_w4a4(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, con
   uint8_t* q = (uint8_t*)workspace;
   uint8_t* s = q + round_up(act_bytes(M, K), 256);
   if (int st = mxfp8::launch_quantize_packed_fp4(x_bf16, M, K, ldx, q, s, (hipStream_t)stream)) return st;
-  return mxfp8::launch_gemm_fp4_tile(q, s, M, K, w_packed, s_packed, N, bias_bf16, y_bf16, ldy, (hipStream_t)stream,
-                                     tile_plan(M, N, K));
+  return gemm(q, s, M, K, w_packed, s_packed, N, bias_bf16, y_bf16, ldy, (hipStream_t)stream);
 }
 
 int mxfp8_debug_force_w4a4(int form) {
-  if (form != 0 && form != 1 && form != 64 && form != 128 && form != 256) return MXFP8_E_SHAPE;
+  if (form != 0 && form != 1 && form != 16 && form != 64 && form != 128 && form != 256) return MXFP8_E_SHAPE;
   return g_force.exchange(form);
 }
 

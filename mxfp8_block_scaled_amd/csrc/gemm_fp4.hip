@@ -9,18 +9,20 @@
 //    x 2, each 16 NA x 16 NB: NA x NB v_mfma_scale_f32_16x16x128 per 128-K
 //    step, the weight as the A operand; lane (i, g) ends with acc[a][b][j] =
 //    D[n = wn 16 NA + 16a + 4g + j][m = wm 16 NB + 16b + i].
-//  * A step's operands are copied straight into one of four LDS slots
-//    (buffer_load ... lds); the slot's fragments are read into registers one
-//    step ahead, while the MFMAs of the step before run, and the slot is
-//    refilled right after: at the start of step s the copies of s + 1 have
-//    landed, those of s + 2 and s + 3 are in flight and those of s + 4 go out
-//    between its MFMAs.  One barrier per step.
+//  * A step's operands are copied straight into one of kRing (four or eight)
+//    LDS slots (buffer_load ... lds); the slot's fragments are read into
+//    registers one step ahead, while the MFMAs of the step before run, and the
+//    slot is refilled right after: early in step s the copies of s + 1 have
+//    landed, those of s + 2 .. s + kRing - 1 are in flight and those of s +
+//    kRing go out between its MFMAs.  One barrier per step.
 //  * Persistent: a workgroup runs tiles b, b + gridDim.x, ...  The copy stream
-//    has its own position ("cursor"), four steps ahead, and runs on into the
+//    has its own position ("cursor"), kRing steps ahead, and runs on into the
 //    next tiles while a tile ends and is stored.
 //  * Scales: the packed operands' scale tiles of a pair of steps (256 K) are
-//    1 KiB per 128-row group: one copy per pair.  Gathered rows (kGather)
-//    bring four scale bytes per step each.
+//    1 KiB per 128-row group: one copy per pair.  Of gathered rows (kGather) a
+//    copy touches one cache line per row, so it brings four steps' bytes of each
+//    (per step instead: a quarter slower on 4096 tokens, 128 experts, 1536 x
+//    2048).
 #include <algorithm>
 
 #include "fp4.hpp"
@@ -33,7 +35,6 @@ using tile::buffer_rsrc;
 using tile::i4v;
 
 constexpr int kThreads = 256;
-constexpr int kRing = 4;
 
 // tile::b2l_16 and b2l_4 with the LDS address as a base and a constant: one
 // scalar add into m0.
@@ -51,29 +52,37 @@ __device__ __forceinline__ void b2l_4(uint32_t voff, i4v rsrc, uint32_t soff, ui
 }
 using tile::lds_addr;
 
-template <int NA, int NB, bool kGather>
+template <int NA, int NB, bool kGather, int kRing>
 struct Fp4Lds {
   static constexpr int kRowsN = 32 * NA, kRowsM = 32 * NB;
   static constexpr int kW = kRowsN * 64, kX = kRowsM * 64;
-  static constexpr int kXScale = kGather ? 1024 : 0;       // 256 bytes per wave
-  static constexpr int kSlot = kW + kX + kXScale;          // one 128-K step
+  static constexpr int kSlot = kW + kX;                    // one 128-K step
   static constexpr int kRunsW = NA / 4, kRunsX = kGather ? 0 : (NB + 3) / 4;   // scale runs of 1 KiB per pair
   static constexpr int kScale = (kRunsW + kRunsX) * 1024;  // one pair of steps
   static constexpr int kPitch = 32 * NA;                   // bytes of a staged output row
-  static constexpr int kEpiWave = 16 * kPitch;
+  // Rows staged at a time: eight where that lets two workgroups share a compute
+  // unit's 160 KiB.
+  static constexpr int kEpiRows = kGather && NA == 4 ? 8 : 16;
+  static constexpr int kEpiWave = kEpiRows * kPitch;
   static constexpr int kBiasSlot = 512;                    // a tile's bias, 256 bytes per wave column
   static constexpr int kScaleAt = kRing * kSlot;
-  static constexpr int kEpiAt = kScaleAt + 2 * kScale;
+  // Scales of gathered rows: one copy brings 16 bytes (four steps) of 64 / kEntry
+  // times a wave's kEntry rows, kChunk steps; two chunks.
+  static constexpr int kEntry = 8 * NB, kChunk = 32 / NB;
+  static constexpr int kXsAt = kScaleAt + kRing / 2 * kScale;
+  static constexpr int kEpiAt = kXsAt + (kGather ? 2 * 4096 : 0);
   static constexpr int kBiasAt = kEpiAt + 4 * kEpiWave;
   static constexpr int kIndexAt = kBiasAt;                 // kGather: row indices instead of a bias
-  static constexpr int kBytes = kBiasAt + (kGather ? 2 * 1024 : 4 * kBiasSlot);
-  static constexpr int kCopies = NA / 2 + NB / 2 + (kGather ? 1 : 0);   // per wave and step, without scale runs
+  static constexpr int kJobAt = kBiasAt + (kGather ? 1024 : kRing * kBiasSlot);
+  static constexpr int kBytes = kJobAt + 8 * 32;           // (the cursor is at most five tiles ahead)
+  static_assert(kBytes <= 160 * 1024, "LDS of a compute unit");
+  static constexpr int kCopies = NA / 2 + NB / 2;          // per wave and step, without scales
 };
 
 struct Fp4Args {
   const uint8_t* q;        // activations: packed, or row-major [x_rows, K / 2]
-  const uint8_t* s;
-  uint32_t q_bytes, s_bytes;   // kGather: sizes of q and s
+  const uint8_t* s;        // their scales; row-major rows are s_pitch bytes apart
+  uint32_t q_bytes, s_bytes, s_pitch;   // kGather: sizes of q and s
   int M, K;                // dense: activation rows
   const uint8_t* wp;
   const uint8_t* wsp;
@@ -92,8 +101,8 @@ struct Fp4Args {
 struct Fp4Job {
   int row0, row_end;       // output rows [row0, row_end) at most
   int col0;
-  int64_t wgroup;          // its first 128-row group of the packed weight
-  bool live;
+  int wgroup;              // its first 128-row group of the packed weight
+  int live;
 };
 
 // Tiles of the dense layer: groups of kGroupM M-tiles, N inside, so that the
@@ -119,7 +128,7 @@ struct DenseTiles {
     j.row0 = tm * 32 * NB;
     j.row_end = p.M;
     j.col0 = tn * 32 * NA;
-    j.wgroup = (int64_t)j.col0 / kGroupRows;
+    j.wgroup = j.col0 / kGroupRows;
     return j;
   }
 };
@@ -182,16 +191,17 @@ struct ExpertTiles {
     j.row0 = r0 + tm * 32 * NB;
     j.row_end = r0 + n;
     j.col0 = tn * 32 * NA;
-    j.wgroup = (int64_t)e * ((p.N + kGroupRows - 1) / kGroupRows) + j.col0 / kGroupRows;
+    j.wgroup = e * ((p.N + kGroupRows - 1) / kGroupRows) + j.col0 / kGroupRows;
     return j;
   }
 };
 
 }  // namespace
 
-template <int NA, int NB, bool kGather, bool kExperts>
-__global__ __launch_bounds__(kThreads, (NA * NB >= 32 ? 1 : 2)) void gemm_fp4_kernel(Fp4Args p) {
-  using L = Fp4Lds<NA, NB, kGather>;
+template <int NA, int NB, bool kGather, bool kExperts, int kRing>
+__global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kGather, kRing>::kBytes > 80 * 1024 ? 1 : 2)) void gemm_fp4_kernel(
+    Fp4Args p) {
+  using L = Fp4Lds<NA, NB, kGather, kRing>;
   using Tiles = typename std::conditional<kExperts, ExpertTiles<NA, NB>, DenseTiles<NA, NB>>::type;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
 
@@ -214,29 +224,48 @@ __global__ __launch_bounds__(kThreads, (NA * NB >= 32 ? 1 : 2)) void gemm_fp4_ke
       p.y[(tiles.kept + r) * p.ldy + (i - r * p.N)] = 0;
     }
   }
-  int b = blockIdx.x;
-  if (b >= tiles.total) return;
+  if ((int)blockIdx.x >= tiles.total) return;
 
   // ------------------------------------------------------------ the copies
-  // The cursor: tile cb, step cq of it; sources of its tile.  Past the last
+  // The cursor: step cq of this workgroup's tile ctile; sources of its tile.  Past the last
   // tile the sources are empty: the copies bring zeros, without touching
   // memory, and every wait counts the same.
-  int cb = b, cq = 0, ctile = 0;
+  int cq = 0, ctile = 0;
   i4v w0, w1, x0, x1, sc, xsr;
   uint32_t vx[NB / 2], vxhi = 0, vxs = 0;
   const uint32_t lds0 = lds_addr(smem) + (uint32_t)wave * 1024u;   // this wave's share of a region
   const uint32_t lo16 = (uint32_t)lane * 16u;
   const uint32_t band = (uint32_t)KS4 * kPieceBytes;          // bytes of a 16-row band
-  auto bias_slot = [&](int t) { return smem + L::kBiasAt + (t & 3) * L::kBiasSlot; };
-  auto index_slot = [&](int t) { return smem + L::kIndexAt + (t & 1) * 1024 + wave * 256; };
+  auto bias_slot = [&](int t) { return smem + L::kBiasAt + (t & (kRing - 1)) * L::kBiasSlot; };
+  uint8_t* const index_slot = smem + L::kIndexAt + wave * 256;
+  // Decoding a tile takes a wave some hundred instructions, so each is decoded
+  // once, a tile before the cursor gets to it, and kept in LDS (every wave
+  // writes the same values and reads its own).
+  auto job_slot = [&](int t) { return reinterpret_cast<int4*>(smem + L::kJobAt + (t & 7) * 32); };
+  auto put_job = [&](int t) {
+    const Fp4Job j = tiles.job(p, (int)blockIdx.x + t * (int)gridDim.x);
+    job_slot(t)[0] = make_int4(j.row0, j.row_end, j.col0, j.wgroup);
+    job_slot(t)[1].x = j.live;
+    return j;
+  };
+  auto get_job = [&](int t) {
+    const int4 v = job_slot(t)[0];
+    Fp4Job j;
+    j.row0 = __builtin_amdgcn_readfirstlane(v.x);
+    j.row_end = __builtin_amdgcn_readfirstlane(v.y);
+    j.col0 = __builtin_amdgcn_readfirstlane(v.z);
+    j.wgroup = __builtin_amdgcn_readfirstlane(v.w);
+    j.live = __builtin_amdgcn_readfirstlane(job_slot(t)[1].x);
+    return j;
+  };
   // The row of the tile that entry `lane` of the wave's share stands for:
   // rows 16 wave + 64 i + (0 .. 15), i = lane / 16.
   const int my_row = 64 * (lane >> 4) + 16 * wave + (lane & 15);
-  auto fetch_index = [&](const Fp4Job& j, int t) {
+  auto fetch_index = [&](const Fp4Job& j) {
     if constexpr (kGather) {
       if (p.slots != nullptr) {
         const i4v r = buffer_rsrc(p.slots, j.live ? (uint32_t)p.R * 4u : 0u);
-        b2l_4<0>((uint32_t)min(j.row0 + my_row, j.row_end - 1) * 4u, r, 0u, lds_addr(index_slot(t)));
+        b2l_4<0>((uint32_t)min(j.row0 + my_row, j.row_end - 1) * 4u, r, 0u, lds_addr(index_slot));
       }
     }
   };
@@ -250,13 +279,13 @@ __global__ __launch_bounds__(kThreads, (NA * NB >= 32 ? 1 : 2)) void gemm_fp4_ke
     if constexpr (kGather) {
       int row = min(j.row0 + my_row, j.row_end - 1);
       if (p.slots != nullptr) {
-        row = *reinterpret_cast<const int*>(index_slot(t) + lane * 4);
+        row = *reinterpret_cast<const int*>(index_slot + lane * 4);
         row = j.live ? row / p.topk : 0;
       }
       row = j.live ? row : 0;
       xsr = buffer_rsrc(p.s, live * p.s_bytes);
       x0 = buffer_rsrc(p.q, live * p.q_bytes);
-      vxs = (uint32_t)row * (uint32_t)(p.K / 32);
+      vxs = (uint32_t)__shfl(row, lane % L::kEntry) * p.s_pitch + (uint32_t)(lane / L::kEntry) * 16u;
 #pragma unroll
       for (int i = 0; i < NB / 2; ++i) {
         const uint32_t r = (uint32_t)__shfl(row, 16 * i + (lane >> 2));
@@ -301,23 +330,33 @@ __global__ __launch_bounds__(kThreads, (NA * NB >= 32 ? 1 : 2)) void gemm_fp4_ke
       else go(at, i & 1 ? vxhi : vx[0], i < 2 ? x0 : x1, off);
     }
   };
-  constexpr int kData = NA / 2 + NB / 2;                      // (and with gathered rows their scales)
   auto issue = [&](auto kCopy, int q, uint32_t st) {
-    if constexpr (decltype(kCopy)::value < kData) {
-      source(kCopy, q, [&](auto at, uint32_t v, i4v r, uint32_t off) { b2l_16<decltype(at)::value>(v, r, off, st); });
-    } else {
-      b2l_4<0>(vxs, xsr, (uint32_t)q * 4u, st - (uint32_t)wave * 768u + (uint32_t)(L::kW + L::kX));
-    }
+    source(kCopy, q, [&](auto at, uint32_t v, i4v r, uint32_t off) { b2l_16<decltype(at)::value>(v, r, off, st); });
   };
   const bool has_run = wave < L::kRunsW + L::kRunsX;
   auto issue_scales = [&](int q, int pair) {
     if (has_run)
       b2l_16<L::kScaleAt>(lo16, sc, (uint32_t)q * 2u * kTileScaleBytes, lds0 + (uint32_t)(pair * L::kScale));
   };
-  auto advance_tile = [&](const Fp4Job& next_next) {
-    // (called with cb already on the new tile; its indices are in LDS)
-    set_sources(tiles.job(p, cb), ctile);
-    fetch_index(next_next, ctile + 1);
+  // The scales of the cursor's pair of steps (q the first): a packed operand's
+  // run, and at the start of a chunk the gathered rows'.
+  int xput = 0;                                               // chunk buffer to fill next
+  auto issue_all_scales = [&](int q, int pair) {
+    issue_scales(q, pair);
+    if constexpr (kGather) {
+      if (q % L::kChunk == 0) {
+        b2l_16<L::kXsAt>(vxs, xsr, (uint32_t)q * 4u, lds0 + (uint32_t)xput * 4096u);
+        xput ^= 1;
+      }
+    }
+  };
+  // Sources of tile ctile (its indices are in LDS), and the next one decoded and
+  // its indices on their way: into the place of those just read.
+  auto advance_tile = [&]() {
+    set_sources(get_job(ctile), ctile);
+    const Fp4Job next = put_job(ctile + 1);
+    if constexpr (kGather) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    fetch_index(next);
   };
 
   // ------------------------------------------------------------ fragments
@@ -336,21 +375,21 @@ __global__ __launch_bounds__(kThreads, (NA * NB >= 32 ? 1 : 2)) void gemm_fp4_ke
   const int shiftA = NA == 8 ? 0 : 16 * wn;
   const int offSA = (NA == 8 ? wn * 1024 : 0) + offS;
   const int offSB = L::kRunsW * 1024 + (NB == 8 ? wm * 1024 : 0) + offS;
-  // Gathered rows: bytes [wave][entry] of 4 scale bytes, row 64 i + 16 w + r at
-  // entry 16 i + r of wave w's share.
-  const int offXS = L::kW + L::kX + li * 4 + lg + (NB == 8 ? wm * 128 : NB == 4 ? wm * 64 : wm * 512);
+  // Gathered rows: [wave][four steps][entry] of 16 scale bytes, row 64 i + 16 w +
+  // r at entry 16 i + r of wave w's share, so 16-row block q in wave q % 4's, at
+  // entries 16 (q / 4) ..
+  const int offXS = li * 16 + lg + (NB == 8 ? wm * 512 : NB == 4 ? wm * 256 : wm * 2048);
   int shiftB = NB == 8 ? 0 : NB == 4 ? 16 * wm : 8 * wm;     // NB == 2: and the tile's half of its group
   constexpr int kReads = 4 + NA + NB + (kGather ? NB - 2 : 0);
   // Read r of a step's fragments: the scales first.
-  auto read_part = [&](int r, Frags& f, const uint8_t* st, const uint8_t* sct) {
+  auto read_part = [&](int r, Frags& f, const uint8_t* st, const uint8_t* sct, const uint8_t* xs) {
     constexpr int kSB = kGather ? NB : 2;
     if (r < 2) {
       f.sa[r] = (int)((uint32_t)*reinterpret_cast<const int*>(sct + offSA + 128 * r) >> shiftA);
     } else if (r < 2 + kSB) {
       const int e = r - 2;
       if constexpr (kGather) {
-        // 16-row block q = NB wm + e: wave q % 4's share, entries 16 (q / 4) ..
-        f.sb[e] = st[offXS + (NB == 8 ? (e & 3) * 256 + (e >> 2) * 64 : e * 256)];
+        f.sb[e] = xs[offXS + (NB == 8 ? (e & 3) * 1024 + (e >> 2) * 256 : e * 1024)];   // block q = NB wm + e
       } else {
         f.sb[e] = (int)((uint32_t)*reinterpret_cast<const int*>(sct + offSB + 128 * e) >> shiftB);
       }
@@ -372,27 +411,31 @@ __global__ __launch_bounds__(kThreads, (NA * NB >= 32 ? 1 : 2)) void gemm_fp4_ke
   // to issue, and the fragment reads spread between them.  The first kHead
   // blocks run before the barrier, over the end of the step's own reads.
   auto step = [&](auto kSecond, const Frags& cur, Frags& nxt, uint32_t free, const uint8_t* next, int pair,
-                  const uint8_t* nsc, int q) {
+                  const uint8_t* nsc, const uint8_t* xs, int q) {
     constexpr int kBlocks = NA * NB / 4, kHead = kBlocks / 8, kGaps = kBlocks - kHead;
+    // (A small tile's few MFMAs only cover the reads if all go out before them.)
+    constexpr bool kReadsFirst = kBlocks <= 4;
     tile::static_for<0, kBlocks>([&](auto J) {
       constexpr int j = decltype(J)::value, g = j - kHead;
       constexpr int a = 4 * j % NA, bb = 4 * j / NA;
       if constexpr (g == 0) {
         // Every wave has read this step's fragments (the slot may be refilled),
-        // and the next step's copies have landed: the operand copies of two
-        // steps behind it may be in flight; what else was issued since makes
-        // the wait only stricter.
-        tile::wait_vmcnt<2 * L::kCopies>();
+        // and the next step's copies have landed: the operand copies of the
+        // kRing - 2 steps behind it may be in flight; what else was issued since
+        // makes the wait only stricter.
+        tile::wait_vmcnt<(kRing - 2) * L::kCopies>();
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (decltype(kSecond)::value) issue_scales(q - 1, pair);
+        if constexpr (decltype(kSecond)::value) issue_all_scales(q - 1, pair);
+        if constexpr (kReadsFirst)
+          tile::static_for<0, kReads>([&](auto R) { read_part(decltype(R)::value, nxt, next, nsc, xs); });
       }
       // op_sel: the byte of the scale word (packed), byte 0 of the lane's own
       // (gathered).
       constexpr int selA = a >> 1, selB = kGather ? 0 : (NB == 2 ? 0 : bb >> 1), sb = kGather ? bb : bb & 1;
       constexpr int c0 = g < 0 ? 0 : g * L::kCopies / kGaps, c1 = g < 0 ? 0 : (g + 1) * L::kCopies / kGaps;
-      if constexpr (c1 > c0 && c0 < kData) {
+      if constexpr (c1 > c0) {
         source(std::integral_constant<int, c0>{}, q, [&](auto at, uint32_t v, i4v r, uint32_t off) {
           mfma16x4_fp4<selA, selB, true, decltype(at)::value>(acc[a][bb], acc[a + 1][bb], acc[a + 2][bb], acc[a + 3][bb],
                                                               cur.a + a, cur.b[bb], cur.sa[0], cur.sa[1], cur.sb[sb], v,
@@ -401,12 +444,12 @@ __global__ __launch_bounds__(kThreads, (NA * NB >= 32 ? 1 : 2)) void gemm_fp4_ke
       } else {
         mfma16x4_fp4<selA, selB, false, 0>(acc[a][bb], acc[a + 1][bb], acc[a + 2][bb], acc[a + 3][bb], cur.a + a,
                                            cur.b[bb], cur.sa[0], cur.sa[1], cur.sb[sb]);
-        if constexpr (c1 > c0) issue(std::integral_constant<int, c0>{}, q, free);
       }
       if constexpr (g >= 0) {
         tile::static_for<c0 + 1, c1>([&](auto C) { issue(C, q, free); });
-        tile::static_for<g * kReads / kGaps, (g + 1) * kReads / kGaps>(
-            [&](auto R) { read_part(decltype(R)::value, nxt, next, nsc); });
+        if constexpr (!kReadsFirst)
+          tile::static_for<g * kReads / kGaps, (g + 1) * kReads / kGaps>(
+              [&](auto R) { read_part(decltype(R)::value, nxt, next, nsc, xs); });
       }
       __builtin_amdgcn_sched_barrier(0);
     });
@@ -417,34 +460,35 @@ __global__ __launch_bounds__(kThreads, (NA * NB >= 32 ? 1 : 2)) void gemm_fp4_ke
   // ------------------------------------------------------------ start
   auto slot = [&](int s) { return smem + s * L::kSlot; };
   auto fill = [&](int s) { return lds0 + (uint32_t)(s * L::kSlot); };
+  // Scales of gathered rows for step q of a tile, in the chunk buffer in use.
+  int xget = 0;
+  auto xs_at = [&](int q) -> const uint8_t* {
+    if constexpr (!kGather) return nullptr;
+    return smem + L::kXsAt + xget * 4096 + q % L::kChunk / 4 * (L::kEntry * 16) + (q & 3) * 4;
+  };
   auto scale_slot = [&](int pair) { return smem + L::kScaleAt + pair * L::kScale; };
   // Moves the cursor over a pair of steps.
   auto move_cursor = [&]() {
     cq += 2;
     if (cq == KS4) {
       cq = 0;
-      cb += (int)gridDim.x;
       ++ctile;
       if constexpr (kGather) {
-        // The new tile's indices were fetched a tile ago: with fewer than four
-        // steps per tile their copies may not have been waited for.
-        if (KS4 < 4) tile::wait_vmcnt<0>();
+        // The new tile's indices were fetched a tile ago: with fewer steps per
+        // tile than slots their copies may not have been waited for.
+        if (KS4 < kRing) tile::wait_vmcnt<0>();
       }
-      advance_tile(kGather ? tiles.job(p, cb + (int)gridDim.x) : Fp4Job{});
+      advance_tile();
     }
   };
-  {
-    const Fp4Job j = tiles.job(p, b);
-    fetch_index(j, 0);
-    if constexpr (kGather) tile::wait_vmcnt<0>();
-    set_sources(j, 0);
-    if constexpr (kGather) fetch_index(tiles.job(p, b + (int)gridDim.x), 1);
-  }
-  for (int pair = 0; pair < 2; ++pair) {
-    issue_scales(cq, pair);
+  fetch_index(put_job(0));
+  if constexpr (kGather) tile::wait_vmcnt<0>();
+  advance_tile();
+  for (int pair = 0; pair < kRing / 2; ++pair) {
+    issue_all_scales(cq, pair);
     tile::static_for<0, L::kCopies>([&](auto C) { issue(C, cq, fill(2 * pair)); });
     tile::static_for<0, L::kCopies>([&](auto C) { issue(C, cq + 1, fill(2 * pair + 1)); });
-    if (kGather && pair == 1) tile::wait_vmcnt<0>();   // (the second tile's indices)
+    if (kGather && pair == kRing / 2 - 1) tile::wait_vmcnt<0>();   // (the second tile's indices)
     move_cursor();
   }
   tile::wait_vmcnt<0>();
@@ -453,9 +497,9 @@ __global__ __launch_bounds__(kThreads, (NA * NB >= 32 ? 1 : 2)) void gemm_fp4_ke
   auto tile_shift = [&](const Fp4Job& j) {
     if constexpr (NB == 2 && !kGather) shiftB = 8 * (2 * ((j.row0 % kGroupRows) / 64) + wm);
   };
-  Fp4Job cur = tiles.job(p, b);
+  Fp4Job cur = get_job(0);
   tile_shift(cur);
-  tile::static_for<0, kReads>([&](auto R) { read_part(decltype(R)::value, f0, slot(0), scale_slot(0)); });
+  tile::static_for<0, kReads>([&](auto R) { read_part(decltype(R)::value, f0, slot(0), scale_slot(0), xs_at(0)); });
 
   int pair = 0, t = 0;
   for (;;) {
@@ -478,57 +522,66 @@ __global__ __launch_bounds__(kThreads, (NA * NB >= 32 ? 1 : 2)) void gemm_fp4_ke
     for (int a = 0; a < NA; ++a)
 #pragma unroll
       for (int c = 0; c < NB; ++c) asm volatile("" : "+a"(acc[a][c]));
-    const int nb = b + (int)gridDim.x;
-    const Fp4Job nxt = tiles.job(p, nb);
+    const Fp4Job nxt = get_job(t + 1);
     for (int q = 0; q < KS4; q += 2) {
-      step(F{}, f0, f1, fill(2 * pair), slot(2 * pair + 1), pair, scale_slot(pair) + 2 * kTileScaleBytes, cq);
+      const int npair = (pair + 1) & (kRing / 2 - 1);
+      step(F{}, f0, f1, fill(2 * pair), slot(2 * pair + 1), pair, scale_slot(pair) + 2 * kTileScaleBytes,
+           xs_at(q + 1), cq);
       // (the last step of a tile reads the next tile's first fragments)
-      if (q + 2 == KS4) tile_shift(nxt);
-      step(T{}, f1, f0, fill(2 * pair + 1), slot(2 * (pair ^ 1)), pair, scale_slot(pair ^ 1), cq + 1);
+      const int qn = q + 2 == KS4 ? 0 : q + 2;
+      if (qn == 0) tile_shift(nxt);
+      if (kGather && qn % L::kChunk == 0) xget ^= 1;
+      step(T{}, f1, f0, fill(2 * pair + 1), slot(2 * npair), pair, scale_slot(npair), xs_at(qn), cq + 1);
       move_cursor();
-      pair ^= 1;
+      pair = npair;
     }
     // The last MFMAs must retire before the accumulators are read.
     asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15" ::: "memory");
 
     // ---------------------------------------------------------- epilogue
-    // The wave stages 16 rows at a time as bf16 (16-byte chunk c of row r at c ^
+    // The wave stages kEpiRows rows at a time as bf16 (16-byte chunk c of row r at c ^
     // r % 8, against bank conflicts) and stores 16-byte pieces of whole row
     // segments (a wave's LDS accesses run in order: no waits).
     {
       typedef unsigned int u4v __attribute__((ext_vector_type(4)));
       uint8_t* reg = smem + L::kEpiAt + wave * L::kEpiWave;
       const int nw = cur.col0 + wn * 16 * NA, mw = cur.row0 + wm * 16 * NB;
-      constexpr int kLanesRow = 2 * NA, kRows = 64 / kLanesRow, kPasses = 16 / kRows;
+      constexpr int kLanesRow = 2 * NA, kRows = 64 / kLanesRow, kPasses = L::kEpiRows / kRows;
       const int rr = lane / kLanesRow, cc = (lane % kLanesRow) * 8;
 #pragma unroll
-      for (int k = 0; k < NB; ++k) {
+      for (int k = 0; k < NB; ++k)
 #pragma unroll
-        for (int a = 0; a < NA; ++a) {
-          const v4f v = acc[a][k];
-          *reinterpret_cast<uint2*>(reg + li * L::kPitch + (((2 * a + (lg >> 1)) ^ (li & 7)) << 4) + (lg & 1) * 8) =
-              make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-        }
-        u4v o[kPasses];
+        for (int part = 0; part < 16 / L::kEpiRows; ++part) {
+          if (L::kEpiRows == 16 || li / L::kEpiRows == part) {
 #pragma unroll
-        for (int r = 0; r < kPasses; ++r)
-          o[r] = *reinterpret_cast<const u4v*>(reg + (rr + kRows * r) * L::kPitch + (((cc >> 3) ^ ((rr + kRows * r) & 7)) << 4));
-#pragma unroll
-        for (int r = 0; r < kPasses; ++r) {
-          const int m = mw + 16 * k + rr + kRows * r, n = nw + cc;
-          if (m >= cur.row_end || n >= p.N) continue;
-          uint16_t* d = p.y + (size_t)m * p.ldy + n;
-          if (p.vec && n + 7 < p.N) {
-            __builtin_nontemporal_store(o[r], reinterpret_cast<u4v*>(d));
-          } else {
-            for (int e = 0; e < 8; ++e)
-              if (n + e < p.N) d[e] = (uint16_t)(o[r][e >> 1] >> (16 * (e & 1)));
+            for (int a = 0; a < NA; ++a) {
+              const v4f v = acc[a][k];
+              *reinterpret_cast<uint2*>(reg + li % L::kEpiRows * L::kPitch + (((2 * a + (lg >> 1)) ^ (li & 7)) << 4) +
+                                        (lg & 1) * 8) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+            }
           }
+          asm volatile("" ::: "memory");
+          u4v o[kPasses];
+#pragma unroll
+          for (int r = 0; r < kPasses; ++r)
+            o[r] = *reinterpret_cast<const u4v*>(reg + (rr + kRows * r) * L::kPitch +
+                                                 (((cc >> 3) ^ ((rr + kRows * r) & 7)) << 4));
+#pragma unroll
+          for (int r = 0; r < kPasses; ++r) {
+            const int m = mw + 16 * k + L::kEpiRows * part + rr + kRows * r, n = nw + cc;
+            if (m >= cur.row_end || n >= p.N) continue;
+            uint16_t* d = p.y + (size_t)m * p.ldy + n;
+            if (p.vec && n + 7 < p.N) {
+              __builtin_nontemporal_store(o[r], reinterpret_cast<u4v*>(d));
+            } else {
+              for (int e = 0; e < 8; ++e)
+                if (n + e < p.N) d[e] = (uint16_t)(o[r][e >> 1] >> (16 * (e & 1)));
+            }
+          }
+          asm volatile("" ::: "memory");
         }
-      }
     }
     if (!nxt.live) break;
-    b = nb;
     cur = nxt;
     ++t;
   }
@@ -538,10 +591,10 @@ __global__ __launch_bounds__(kThreads, (NA * NB >= 32 ? 1 : 2)) void gemm_fp4_ke
 
 namespace {
 
-template <int NA, int NB, bool kGather, bool kExperts>
+template <int NA, int NB, bool kGather, bool kExperts, int kRing>
 int go(const Fp4Args& p, int64_t tiles, hipStream_t stream) {
-  using L = Fp4Lds<NA, NB, kGather>;
-  auto kern = gemm_fp4_kernel<NA, NB, kGather, kExperts>;
+  using L = Fp4Lds<NA, NB, kGather, kRing>;
+  auto kern = gemm_fp4_kernel<NA, NB, kGather, kExperts, kRing>;
   static std::atomic<int> lds_set[kMaxDevices];
   if (!set_lds_limit_once((const void*)kern, L::kBytes, lds_set)) return -7;
   const int64_t per_cu = L::kBytes <= 80 * 1024 ? 2 : 1;
@@ -568,9 +621,12 @@ int launch_gemm_fp4_tile(const void* qp, const void* sp, int64_t M, int64_t K, c
   p.ldy = ldy;
   p.vec = ldy % 8 == 0 && ((uintptr_t)y & 15) == 0;
   const int64_t tiles = ((M + plan.mt - 1) / plan.mt) * ((N + plan.nt - 1) / plan.nt);
-  if (plan.nt == 256) return go<8, 8, false, false>(p, tiles, stream);
-  if (plan.mt == 128) return go<4, 4, false, false>(p, tiles, stream);
-  return go<4, 2, false, false>(p, tiles, stream);
+  if (plan.nt == 256) return go<8, 8, false, false, 4>(p, tiles, stream);
+  // One tile per compute unit: twice the slots; more: two workgroups on each.
+  const bool deep = tiles <= device_cu_count();
+  if (plan.mt == 128)
+    return deep ? go<4, 4, false, false, 8>(p, tiles, stream) : go<4, 4, false, false, 4>(p, tiles, stream);
+  return deep ? go<4, 2, false, false, 8>(p, tiles, stream) : go<4, 2, false, false, 4>(p, tiles, stream);
 }
 
 int launch_experts_fp4_tile(const ExpertsArgs& a, const void* q, const void* s, Fp4Plan plan, hipStream_t stream) {
@@ -578,7 +634,8 @@ int launch_experts_fp4_tile(const ExpertsArgs& a, const void* q, const void* s, 
   p.q = (const uint8_t*)q;
   p.s = (const uint8_t*)s;
   p.q_bytes = (uint32_t)(a.x_rows * (a.K / 2));
-  p.s_bytes = (uint32_t)(a.x_rows * (a.K / 32));
+  p.s_pitch = (uint32_t)fp4_scale_pitch(a.K);
+  p.s_bytes = (uint32_t)(a.x_rows * fp4_scale_pitch(a.K));
   p.K = (int)a.K;
   p.wp = (const uint8_t*)a.wp;
   p.wsp = (const uint8_t*)a.wsp;
@@ -594,9 +651,10 @@ int launch_experts_fp4_tile(const ExpertsArgs& a, const void* q, const void* s, 
   // At most one more row tile per expert than the rows fill.
   const int64_t row_tiles = a.R / plan.mt + std::min(a.E, a.R);
   const int64_t tiles = row_tiles * ((a.N + plan.nt - 1) / plan.nt);
-  if (plan.nt == 256) return go<8, 4, true, true>(p, tiles, stream);
-  if (plan.mt == 128) return go<4, 4, true, true>(p, tiles, stream);
-  return go<4, 2, true, true>(p, tiles, stream);
+  if (plan.nt == 256 && plan.mt == 256) return go<8, 8, true, true, 4>(p, tiles, stream);
+  if (plan.nt == 256) return go<8, 4, true, true, 4>(p, tiles, stream);
+  if (plan.mt == 128) return go<4, 4, true, true, 4>(p, tiles, stream);
+  return go<4, 2, true, true, 4>(p, tiles, stream);
 }
 
 }  // namespace mxfp8

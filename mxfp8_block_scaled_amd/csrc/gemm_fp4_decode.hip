@@ -1,5 +1,6 @@
-// Few rows against a packed MXFP4 weight (the dense layer's M <= 16, and the
-// experts' rows of a small batch), the rows quantized to MXFP4 inside.
+// Few rows against a packed MXFP4 weight (the dense layer's M <= 128, and the
+// experts' rows of a small batch), up to 32 and the experts' quantized to MXFP4
+// inside.
 //
 // Bound by the weight's way from HBM, and at small weights by the launch and
 // the chain of dependent loads.  One workgroup owns 16 weight rows over the
@@ -19,9 +20,6 @@ namespace mxfp8 {
 
 namespace {
 
-constexpr int kWaves = 16;
-constexpr int kThreads = 64 * kWaves;
-
 struct DecodeArgs {
   const uint16_t* x;
   int64_t ldx;
@@ -39,11 +37,42 @@ struct DecodeArgs {
   const int* offsets;
 };
 
+// The waves' partial sums of a lane, in K order.
+template <int kWaves>
+__device__ inline v4f sum_waves(const v4f* red, int lane) {
+  v4f part[kWaves];
+#pragma unroll
+  for (int k = 0; k < kWaves; ++k) part[k] = red[k * 64 + lane];
+  v4f v = part[0];
+#pragma unroll
+  for (int k = 1; k < kWaves; ++k) v += part[k];
+  return v;
+}
+
+// Columns n .. n + 3 of output row m.
+__device__ inline void store4(const DecodeArgs& p, const v4f& v, const float* bv, int m, int row_end, int n) {
+  if (m >= row_end || n >= p.N) return;
+  const uint32_t lo = pack_bf16x2(v[0] + bv[0], v[1] + bv[1]);
+  const uint32_t hi = pack_bf16x2(v[2] + bv[2], v[3] + bv[3]);
+  uint16_t* yr = p.y + (size_t)m * p.ldy + n;
+  if (p.vec && n + 3 < p.N) {
+    *reinterpret_cast<uint2*>(yr) = make_uint2(lo, hi);
+  } else {
+    yr[0] = (uint16_t)lo;
+    if (n + 1 < p.N) yr[1] = (uint16_t)(lo >> 16);
+    if (n + 2 < p.N) yr[2] = (uint16_t)hi;
+    if (n + 3 < p.N) yr[3] = (uint16_t)(hi >> 16);
+  }
+}
+
 }  // namespace
 
-template <int kSteps, bool kExperts>
-__global__ __launch_bounds__(kThreads) void gemm_fp4_decode_kernel(DecodeArgs p) {
-  __shared__ v4f red[kWaves * 64];
+// kSteps: the most steps a wave owns; kGroups: 16-row groups in flight together
+// (experts: one).
+template <int kWaves, int kSteps, int kGroups, bool kExperts>
+__global__ __launch_bounds__(64 * kWaves) void gemm_fp4_decode_kernel(DecodeArgs p) {
+  constexpr int kThreads = 64 * kWaves;
+  __shared__ v4f red[kGroups][kWaves * 64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i = lane & 15, g = lane >> 4;
@@ -96,22 +125,26 @@ __global__ __launch_bounds__(kThreads) void gemm_fp4_decode_kernel(DecodeArgs p)
   // in flight together with the first rows.
   const uint8_t* wrow = p.wp + (size_t)group * KS * kTileBytes + packed_off(r, 0, g, KS);
   const uint8_t* srow = p.wsp + (size_t)group * KS * 2 * kTileScaleBytes + (g >> 1) * kTileScaleBytes + scale_off(r, g & 1);
-  uint4 xv[kSteps][4];
+  uint4 xv[kGroups][kSteps][4];
   auto load_rows = [&](int m0) {
     // Lane (i, g): block g of row m0 + i.  (A step past the wave's run, and a
     // row past the last, stay zero.)
-    const int m = m0 + i;
-    const bool in = m < row_end;
-    int64_t row = in ? m : 0;
-    if constexpr (kExperts) {
-      if (p.slots != nullptr && in) row = min((uint32_t)p.slots[m] / (uint32_t)p.topk, (uint32_t)p.x_rows - 1u);
+#pragma unroll
+    for (int t = 0; t < kGroups; ++t) {
+      const int m = m0 + 16 * t + i;
+      const bool in = m < row_end;
+      int64_t row = in ? m : 0;
+      if constexpr (kExperts) {
+        if (p.slots != nullptr && in) row = min((uint32_t)p.slots[m] / (uint32_t)p.topk, (uint32_t)p.x_rows - 1u);
+      }
+      const uint16_t* xr = p.x + row * p.ldx + (int64_t)kb * 128 + g * 32;
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          xv[t][u][c] =
+              in && u < nsteps ? *reinterpret_cast<const uint4*>(xr + u * 128 + c * 8) : make_uint4(0u, 0u, 0u, 0u);
     }
-    const uint16_t* xr = p.x + row * p.ldx + (int64_t)kb * 128 + g * 32;
-#pragma unroll
-    for (int u = 0; u < kSteps; ++u)
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        xv[u][c] = in && u < nsteps ? *reinterpret_cast<const uint4*>(xr + u * 128 + c * 8) : make_uint4(0u, 0u, 0u, 0u);
   };
   load_rows(row0);
   uint4 w[kSteps];
@@ -124,68 +157,165 @@ __global__ __launch_bounds__(kThreads) void gemm_fp4_decode_kernel(DecodeArgs p)
   }
   const int n = n0 + 4 * g;
   float bv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (p.bias != nullptr && wave == 0) {
+  if (p.bias != nullptr && wave < kGroups) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) bv[e] = __uint_as_float((uint32_t)p.bias[min(n + e, p.N - 1)] << 16);
   }
   __builtin_amdgcn_sched_barrier(0);
 
-  for (int m0 = row0; m0 < row_end; m0 += 16) {
+  for (int m0 = row0; m0 < row_end; m0 += 16 * kGroups) {
     if (m0 != row0) load_rows(m0);
-    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int u = 0; u < kSteps; ++u) {
-      uint32_t m = fp4_absmax8(xv[u][0]);
+    for (int t = 0; t < kGroups; ++t) {
+      v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int c = 1; c < 4; ++c) m = max(m, fp4_absmax8(xv[u][c]));
-      const uint32_t sb = fp4_scale_byte(m);
-      const float scale = fp4_scale_value(sb);
-      v8i b = {(int)cvt8_fp4(xv[u][0], scale), (int)cvt8_fp4(xv[u][1], scale), (int)cvt8_fp4(xv[u][2], scale),
-               (int)cvt8_fp4(xv[u][3], scale), 0, 0, 0, 0};
-      v8i a = {(int)w[u].x, (int)w[u].y, (int)w[u].z, (int)w[u].w, 0, 0, 0, 0};
-      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, 4, 0, wsc[u], 0, (int)sb);
-    }
-    red[wave * 64 + lane] = acc;
-    __syncthreads();
-    if (wave == 0) {
-      v4f part[kWaves];
-#pragma unroll
-      for (int k = 0; k < kWaves; ++k) part[k] = red[k * 64 + lane];
-      acc = part[0];
-#pragma unroll
-      for (int k = 1; k < kWaves; ++k) acc += part[k];
-      // D[n = 4g + e][m = i]
-      if (m0 + i < row_end && n < p.N) {
-        const uint32_t lo = pack_bf16x2(acc[0] + bv[0], acc[1] + bv[1]);
-        const uint32_t hi = pack_bf16x2(acc[2] + bv[2], acc[3] + bv[3]);
-        uint16_t* yr = p.y + (size_t)(m0 + i) * p.ldy + n;
-        if (p.vec && n + 3 < p.N) {
-          *reinterpret_cast<uint2*>(yr) = make_uint2(lo, hi);
-        } else {
-          yr[0] = (uint16_t)lo;
-          if (n + 1 < p.N) yr[1] = (uint16_t)(lo >> 16);
-          if (n + 2 < p.N) yr[2] = (uint16_t)hi;
-          if (n + 3 < p.N) yr[3] = (uint16_t)(hi >> 16);
-        }
+      for (int u = 0; u < kSteps; ++u) {
+        const uint4(&x)[4] = xv[t][u];
+        const uint32_t sb = fp4_scale_byte(max(max(fp4_absmax8(x[0]), fp4_absmax8(x[1])), max(fp4_absmax8(x[2]), fp4_absmax8(x[3]))));
+        const float scale = fp4_scale_value(sb);
+        const v8i b = {(int)cvt8_fp4(x[0], scale), (int)cvt8_fp4(x[1], scale), (int)cvt8_fp4(x[2], scale),
+                       (int)cvt8_fp4(x[3], scale), 0, 0, 0, 0};
+        const v8i a = {(int)w[u].x, (int)w[u].y, (int)w[u].z, (int)w[u].w, 0, 0, 0, 0};
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, 4, 0, wsc[u], 0, (int)sb);
       }
+      red[t][wave * 64 + lane] = acc;
+    }
+    __syncthreads();
+    if (wave < kGroups) {
+      const v4f v = sum_waves<kWaves>(red[wave], lane);
+      store4(p, v, bv, m0 + 16 * wave + i, row_end, n);   // D[n = 4g + e][m = i]
     }
     if constexpr (kExperts) __syncthreads();   // red is written again
   }
 }
 
+// 16 < M <= 128 rows, quantized beforehand into one packed 128-row group (the
+// decode kernel's waves would each convert all of them again).  Waves and
+// weight as there; per step a wave reads the kGroups 1 KiB pieces of the
+// activations (L2) and runs an MFMA on each, the loads of the next kBatch
+// steps in flight.
+template <int kWaves, int kGroups, int kBatch>
+__global__ __launch_bounds__(64 * kWaves) void gemm_fp4_mid_kernel(const uint8_t* __restrict__ qp,
+                                                            const uint8_t* __restrict__ sp, DecodeArgs p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  v4f* red = reinterpret_cast<v4f*>(smem);   // [kGroups][kWaves][64]
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int i = lane & 15, g = lane >> 4;
+  const int KS = p.K / 128;
+  const int kb = KS * wave / kWaves, ke = KS * (wave + 1) / kWaves;
+  const int n0 = xcd_remap((int)blockIdx.x, (int)gridDim.x) * 16;
+  const int r = n0 % kGroupRows + i;
+  const int64_t group = n0 / kGroupRows;
+  const uint8_t* wrow = p.wp + (size_t)group * KS * kTileBytes + packed_off(r, 0, g, KS);
+  const uint8_t* srow = p.wsp + (size_t)group * KS * 2 * kTileScaleBytes + (g >> 1) * kTileScaleBytes + scale_off(r, g & 1);
+  const uint8_t* xrow = qp + packed_off(i, 0, g, KS);                                   // + band * KS pieces
+  const uint8_t* xsrow = sp + (g >> 1) * kTileScaleBytes + scale_off(i, g & 1);         // + 128 for odd bands
+  struct Batch {
+    uint4 w[kBatch], x[kBatch][kGroups];
+    int ws[kBatch], xs[kBatch][2];
+  };
+  auto load = [&](Batch& f, int k) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int ks = min(k + u, KS - 1);
+      f.w[u] = *reinterpret_cast<const uint4*>(wrow + (size_t)ks * kPieceBytes);
+      f.ws[u] = srow[(size_t)ks * 2 * kTileScaleBytes];
+#pragma unroll
+      for (int t = 0; t < kGroups; ++t)
+        f.x[u][t] = *reinterpret_cast<const uint4*>(xrow + ((size_t)t * KS + ks) * kPieceBytes);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        f.xs[u][e] = *reinterpret_cast<const int*>(xsrow + (size_t)ks * 2 * kTileScaleBytes + 128 * e);
+    }
+  };
+  v4f acc[kGroups];
+#pragma unroll
+  for (int t = 0; t < kGroups; ++t) acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  auto multiply = [&](const Batch& f, int k) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (k + u >= ke) continue;
+      const v8i a = {(int)f.w[u].x, (int)f.w[u].y, (int)f.w[u].z, (int)f.w[u].w, 0, 0, 0, 0};
+      // band t: word t % 2 of its lane's scales, byte t / 2
+      tile::static_for<0, kGroups>([&](auto T) {
+        constexpr int t = decltype(T)::value;
+        const uint4 x = f.x[u][t];
+        const v8i b = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
+        acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc[t], 4, 4, 0, f.ws[u], t >> 1, f.xs[u][t & 1]);
+      });
+    }
+  };
+  Batch f0, f1;
+  load(f0, kb);
+  const int n = n0 + 4 * g;
+  float bv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (p.bias != nullptr && wave < kGroups) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) bv[e] = __uint_as_float((uint32_t)p.bias[min(n + e, p.N - 1)] << 16);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  for (int k = kb; k < ke; k += 2 * kBatch) {
+    if (k + kBatch < ke) load(f1, k + kBatch);
+    multiply(f0, k);
+    if (k + kBatch >= ke) break;
+    if (k + 2 * kBatch < ke) load(f0, k + 2 * kBatch);
+    multiply(f1, k + kBatch);
+  }
+#pragma unroll
+  for (int t = 0; t < kGroups; ++t) red[(t * kWaves + wave) * 64 + lane] = acc[t];
+  __syncthreads();
+  if (wave < kGroups) store4(p, sum_waves<kWaves>(red + wave * kWaves * 64, lane), bv, 16 * wave + i, p.M, n);
+}
+
 namespace {
 template <bool kExperts>
 int decode(const DecodeArgs& p, int64_t blocks, hipStream_t stream) {
-  auto go = [&](auto kern) {
-    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kThreads), 0, stream, p);
+  auto go = [&](auto kern, int waves) {
+    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(64 * waves), 0, stream, p);
     return hipGetLastError() == hipSuccess ? 0 : -7;
   };
-  static_assert(kFp4DecodeMaxK == kWaves * 4 * 128, "a wave owns at most four steps");
-  if (p.K <= kWaves * 128) return go(gemm_fp4_decode_kernel<1, kExperts>);
-  if (p.K <= kWaves * 2 * 128) return go(gemm_fp4_decode_kernel<2, kExperts>);
-  return go(gemm_fp4_decode_kernel<4, kExperts>);
+  static_assert(kFp4DecodeMaxK == 16 * 4 * 128, "a wave owns at most four steps");
+  const int KS = p.K / 128;
+  if constexpr (!kExperts) {
+    if (p.M > 16) {
+      if (KS <= 16) return go(gemm_fp4_decode_kernel<16, 1, 2, false>, 16);
+      return go(gemm_fp4_decode_kernel<16, 2, 2, false>, 16);
+    }
+  }
+  if (KS <= 8) return go(gemm_fp4_decode_kernel<8, 1, 1, kExperts>, 8);
+  if (KS <= 16) return go(gemm_fp4_decode_kernel<8, 2, 1, kExperts>, 8);
+  if (KS <= 32) return go(gemm_fp4_decode_kernel<16, 2, 1, kExperts>, 16);
+  return go(gemm_fp4_decode_kernel<16, 4, 1, kExperts>, 16);
+}
+template <int kWaves, int kGroups, int kBatch>
+int mid(const void* qp, const void* sp, const DecodeArgs& p, hipStream_t stream) {
+  constexpr int lds = kGroups * kWaves * 64 * 16;
+  auto kern = gemm_fp4_mid_kernel<kWaves, kGroups, kBatch>;
+  static std::atomic<int> lds_set[kMaxDevices];
+  if (!set_lds_limit_once((const void*)kern, lds, lds_set)) return -7;
+  hipLaunchKernelGGL(kern, dim3((unsigned)((p.N + 15) / 16)), dim3(64 * kWaves), lds, stream, (const uint8_t*)qp,
+                     (const uint8_t*)sp, p);
+  return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 }  // namespace
+
+int launch_gemm_fp4_mid(const void* qp, const void* sp, int64_t M, int64_t K, const void* wp, const void* wsp,
+                        int64_t N, const void* bias, void* y, int64_t ldy, hipStream_t stream) {
+  DecodeArgs p = {};
+  p.M = (int)M;
+  p.K = (int)K;
+  p.wp = (const uint8_t*)wp;
+  p.wsp = (const uint8_t*)wsp;
+  p.N = (int)N;
+  p.bias = (const uint16_t*)bias;
+  p.y = (uint16_t*)y;
+  p.ldy = ldy;
+  p.vec = ldy % 4 == 0 && ((uintptr_t)y & 7) == 0;
+  if (M <= 32) return mid<16, 2, 2>(qp, sp, p, stream);
+  if (M <= 64) return mid<16, 4, 2>(qp, sp, p, stream);
+  return mid<8, 8, 2>(qp, sp, p, stream);
+}
 
 int launch_gemm_fp4_decode(const void* x, int64_t ldx, int64_t M, int64_t K, const void* wp, const void* wsp,
                            int64_t N, const void* bias, void* y, int64_t ldy, hipStream_t stream) {

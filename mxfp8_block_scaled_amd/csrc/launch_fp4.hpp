@@ -14,15 +14,22 @@ constexpr int64_t kFp4Step = 128;   // elements of one 4-bit K step (64 bytes of
 // launch_pack_weight_fp4 with M in place of N; pad rows zero).
 int launch_quantize_packed_fp4(const void* x, int64_t M, int64_t K, int64_t ldx, void* qp, void* sp,
                                hipStream_t stream);
-// The same as row-major bytes: q [M, K / 2], s [M, K / 32].
+// The same as row-major bytes: q [M, K / 2], s [M, K / 32] with rows of whole 16
+// bytes (fp4_scale_pitch apart).
+inline int64_t fp4_scale_pitch(int64_t K) { return (K / 32 + 15) / 16 * 16; }
 int launch_quantize_rows_fp4(const void* x, int64_t M, int64_t K, int64_t ldx, void* q, void* s, hipStream_t stream);
 
-// Decode GEMM: M <= 16 bf16 rows, quantized inside, against a packed MXFP4
-// weight; K <= kFp4DecodeMaxK.
-constexpr int64_t kFp4DecodeMaxM = 16;
+// Decode GEMM: M <= 16 bf16 rows (32 where K <= 4096), quantized inside,
+// against a packed MXFP4 weight; K <= kFp4DecodeMaxK.
 constexpr int64_t kFp4DecodeMaxK = 8192;
+inline int64_t fp4_decode_max_m(int64_t K) { return K <= 4096 ? 32 : K <= kFp4DecodeMaxK ? 16 : 0; }
 int launch_gemm_fp4_decode(const void* x, int64_t ldx, int64_t M, int64_t K, const void* wp, const void* wsp,
                            int64_t N, const void* bias, void* y, int64_t ldy, hipStream_t stream);
+
+// The same on packed activations (one 128-row group), M <= kFp4MidMaxM.
+constexpr int64_t kFp4MidMaxM = 128;
+int launch_gemm_fp4_mid(const void* qp, const void* sp, int64_t M, int64_t K, const void* wp, const void* wsp,
+                        int64_t N, const void* bias, void* y, int64_t ldy, hipStream_t stream);
 
 // Tile GEMM of two packed MXFP4 operands.
 struct Fp4Plan {
@@ -87,7 +94,7 @@ struct ExpertsArgs {
 };
 // Decode form: quantizes inside, no workspace.
 int launch_experts_fp4_decode(const ExpertsArgs& a, hipStream_t stream);
-// Tile form on rows quantized into q [x_rows, K / 2], s [x_rows, K / 32].
+// Tile form on rows of launch_quantize_rows_fp4.
 int launch_experts_fp4_tile(const ExpertsArgs& a, const void* q, const void* s, Fp4Plan plan, hipStream_t stream);
 
 }  // namespace mxfp8

@@ -69,7 +69,7 @@ template <int kPieces>
 __global__ __launch_bounds__(kQuantThreads) void quant_rows_fp4_kernel(const uint16_t* __restrict__ x, int64_t ldx,
                                                                        uint32_t per_row, int64_t total,
                                                                        uint8_t* __restrict__ q,
-                                                                       uint8_t* __restrict__ s) {
+                                                                       uint8_t* __restrict__ s, int pitch) {
   const int64_t base = (int64_t)blockIdx.x * (kQuantThreads * kPieces) + threadIdx.x;
   uint4 v[kPieces];
 #pragma unroll
@@ -87,7 +87,10 @@ __global__ __launch_bounds__(kQuantThreads) void quant_rows_fp4_kernel(const uin
     const Fp4Piece p = quant8(v[u]);
     if (i < total) {
       reinterpret_cast<uint32_t*>(q)[i] = p.codes;
-      if ((i & 3) == 0) s[i >> 2] = (uint8_t)p.scale;
+      if ((i & 3) == 0) {
+        const int64_t row = i / per_row;
+        s[row * pitch + ((i - row * per_row) >> 2)] = (uint8_t)p.scale;
+      }
     }
   }
 }
@@ -97,7 +100,7 @@ int launch_quantize_rows_fp4(const void* x, int64_t M, int64_t K, int64_t ldx, v
   auto go = [&](auto kern, int pieces) {
     const int64_t n = (int64_t)kQuantThreads * pieces;
     hipLaunchKernelGGL(kern, dim3((unsigned)((total + n - 1) / n)), dim3(kQuantThreads), 0, stream, (const uint16_t*)x,
-                       ldx, (uint32_t)per_row, total, (uint8_t*)q, (uint8_t*)s);
+                       ldx, (uint32_t)per_row, total, (uint8_t*)q, (uint8_t*)s, (int)fp4_scale_pitch(K));
   };
   if (total >= (int64_t)kQuantThreads * 4 * 1024) go(quant_rows_fp4_kernel<4>, 4);
   else go(quant_rows_fp4_kernel<1>, 1);

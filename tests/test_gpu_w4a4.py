@@ -40,10 +40,17 @@ def test_quantize_packed(M, K):
     assert bool((q[M:] == 0).all())
 
 
-@pytest.mark.parametrize("form", [1, 64, 128, 256])
-@pytest.mark.parametrize("M,N,K", [(1, 1, 256), (3, 130, 512), (16, 257, 768), (16, 1000, 2048), (9, 64, 4096), (2, 33, 8192)])
+@pytest.mark.parametrize("form", [1, 16, 64, 128, 256])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 256), (3, 130, 512), (16, 257, 768), (16, 1000, 2048), (9, 64, 4096), (2, 33, 8192),
+                                   (17, 70, 256), (32, 100, 2048), (27, 300, 4096), (20, 64, 2304)])
 def test_few_rows(form, M, N, K):
     case(M, N, K, form=form, seed=M + N)
+
+
+@pytest.mark.parametrize("M,N,K", [(33, 130, 256), (64, 200, 768), (65, 257, 2048), (100, 64, 4352), (128, 131, 8192),
+                                   (50, 40, 12544), (128, 16, 20480)])
+def test_mid_form(M, N, K):
+    case(M, N, K, bias=(M % 2 == 1), form=16, seed=M)
 
 
 @pytest.mark.parametrize("form", [64, 128, 256])
@@ -66,7 +73,7 @@ def test_chosen_forms():
         case(M, N, K, seed=M)
 
 
-@pytest.mark.parametrize("M", [4, 200])
+@pytest.mark.parametrize("M", [4, 30, 128, 200])
 def test_one_hot(M):
     """One-hot weights return single activations: every K position and row."""
     K, N = 512, 512
@@ -76,13 +83,13 @@ def test_one_hot(M):
     codes, s = oracle.quantize_mxfp4(w)
     pw = api.prepare_weight_fp4(torch.from_numpy(oracle.pack_fp4(codes)).to(dev()), torch.from_numpy(s).to(dev()))
     A = ref.quantized(x)
-    for form in (1, 64, 128, 256):
+    for form in (1, 16, 64, 128, 256):
         with ref.forced(form):
             y = api.linear_w4a4(x.to(dev()), pw).double().cpu().numpy()
         assert np.array_equal(y, A[:, (np.arange(N) * 37) % K])
 
 
-@pytest.mark.parametrize("form", [1, 64, 128, 256])
+@pytest.mark.parametrize("form", [1, 16, 64, 128, 256])
 def test_not_finite(form):
     """An infinity or a NaN makes its own row's outputs NaN, and no other's."""
     M, N, K = 16, 200, 512
@@ -99,7 +106,7 @@ def test_not_finite(form):
     ref.check(y[keep], ref.quantized(x[keep]), W)
 
 
-@pytest.mark.parametrize("M", [5, 150])
+@pytest.mark.parametrize("M", [5, 25, 90, 150])
 def test_strides(M):
     """Rows of a wider matrix, unaligned rows, a strided and an unaligned output."""
     N, K = 264, 512
