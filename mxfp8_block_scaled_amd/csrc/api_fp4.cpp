@@ -32,25 +32,65 @@ bool gemm_grid_ok(int64_t M, int64_t N) { return (M + 63) / 64 * ((N + 127) / 12
 // Test hook: pinned form (0: by shape).
 std::atomic<int> g_force{0};
 
-bool decode_form(int64_t M, int64_t N, int64_t K) {
-  (void)N;
-  const int force = g_force.load(std::memory_order_relaxed);
-  return M <= mxfp8::fp4_decode_max_m(K) && (force == 0 || force == 1);
+// The forms with the least estimated time: lines through measurements on
+// MI355X (us, calls in a captured graph, the quantizer's launch included).  For
+// example (form 1: decode; 16: 16 weight rows on packed activations; 64, 128,
+// 256: tiles), N x K = 4096 x 4096:
+//   M = 1      4.8    7.2   13.4
+//   M = 32    11.4    7.4   13.8   16.1
+//   M = 128           11.5  13.6   16.3   31
+//   M = 1000                19.9   20.1   33.7
+//   M = 2048                33     27     37
+//   M = 4096                63     49     47
+// and 16384 x 8192:
+//   M = 32            24.7  20.9   24.8
+//   M = 2048               219    162    136
+double turns(int64_t N) { return std::max(1.0, (double)N / 4096.0); }   // of one workgroup per compute unit, 16 rows each
+double decode_us(int64_t M, int64_t N, int64_t K) {
+  return 3.0 + (double)K * turns(N) * (4.0e-4 + 4.5e-5 * (double)M + (M > 16 ? 3.0e-4 : 0.0));
+}
+double mid_us(int64_t M, int64_t N, int64_t K) {
+  const double k = (double)K;
+  return 4.0 + turns(N) * (M <= 32 ? 2.6 + 3.0e-4 * k : M <= 64 ? 3.5 + 5.0e-4 * k : 2.6 + 1.15e-3 * k);
+}
+double tile_us(int nt, int mt, int64_t M, int64_t N, int64_t K) {
+  const double k = (double)K;
+  const int64_t tiles = (M + mt - 1) / mt * ((N + nt - 1) / nt);
+  const double more = std::max(0.0, (double)tiles / 256.0 - 1.0);      // rounds of the chip behind the first
+  const bool full = tiles > 128;
+  if (nt == 256)
+    return 11.0 + 5.0e-3 * k + (full ? 3.5 + 1.8e-3 * k : 0.0) + (double)((tiles + 255) / 256 - 1) * (5.0 + 7.3e-3 * k);
+  if (mt == 128) return 7.7 + 2.0e-3 * k + (full ? 0.6 + 8.0e-4 * k : 0.0) + more * (0.6 + 2.1e-3 * k);
+  return 7.1 + 1.6e-3 * k + more * (0.4 + 1.45e-3 * k);
 }
 
-// The GEMM on packed activations: nt == 16 is the mid form.
-mxfp8::Fp4Plan tile_plan(int64_t M, int64_t N, int64_t K) {
-  (void)K;
+// The GEMM on packed activations: nt == 16 is the 16-row form.
+mxfp8::Fp4Plan tile_plan(int64_t M, int64_t N, int64_t K, double* us = nullptr) {
   const int force = g_force.load(std::memory_order_relaxed);
-  if (force == 16 && M <= mxfp8::kFp4MidMaxM) return {16, 128};
-  if (force == 256) return {256, 256};
-  if (force == 128) return {128, 128};
-  if (force == 64) return {128, 64};
-  if (M <= mxfp8::kFp4MidMaxM) return {16, 128};
-  const int64_t large = (M + 255) / 256 * ((N + 255) / 256);
-  if (large >= 192) return {256, 256};
-  const int64_t medium = (M + 127) / 128 * ((N + 127) / 128);
-  return medium >= 192 ? mxfp8::Fp4Plan{128, 128} : mxfp8::Fp4Plan{128, 64};
+  mxfp8::Fp4Plan best = {128, 64};
+  double best_us = 1e30;
+  auto offer = [&](int form, int nt, int mt, double t) {
+    if (force == form) t = -1.0;
+    if (t >= best_us) return;
+    best_us = t;
+    best = {nt, mt};
+  };
+  if (M <= mxfp8::kFp4MidMaxM) offer(16, 16, 128, mid_us(M, N, K));
+  offer(64, 128, 64, tile_us(128, 64, M, N, K));
+  offer(128, 128, 128, tile_us(128, 128, M, N, K));
+  offer(256, 256, 256, tile_us(256, 256, M, N, K));
+  if (us) *us = best_us;
+  return best;
+}
+
+// One launch that quantizes inside, without a workspace.
+bool decode_form(int64_t M, int64_t N, int64_t K) {
+  if (M > mxfp8::fp4_decode_max_m(K)) return false;
+  const int force = g_force.load(std::memory_order_relaxed);
+  if (force != 0) return force == 1;
+  double us = 0.0;
+  tile_plan(M, N, K, &us);
+  return decode_us(M, N, K) <= us;
 }
 
 int gemm(const void* q, const void* s, int64_t M, int64_t K, const void* wp, const void* wsp, int64_t N,
@@ -100,15 +140,30 @@ struct ExpertsForm {
   bool decode;
   mxfp8::Fp4Plan plan;
 };
+// The same for the experts, whose rows' spread the host does not know: X
+// experts with rows at most, R / X rows each.  Decode reads all their weights
+// with its rows converted again for each 16 weight rows; tiles take the longer
+// start.  For example (R / E; decode, tiles of 128 x 64, 128 x 128, 256 x 128),
+// 128 experts, N x K = 1536 x 2048:
+//   8 rows in all   7.6   11.7
+//   0.25           17.7   16.4
+//   1              45     25     30     31
+//   64                    60     61     62
+//   256                  140    124    114
 ExpertsForm experts_form(int64_t R, int64_t N, int64_t K, int64_t E) {
-  (void)N;
   const int force = g_force.load(std::memory_order_relaxed);
   const bool can = K <= mxfp8::kFp4DecodeMaxK;
-  if (can && (force == 1 || (force == 0 && R <= 4 * E))) return {true, {}};
+  const double X = (double)std::max<int64_t>(1, std::min(E, R)), rows = (double)R / X;
+  const double work = 1e-6 * X * (double)N * (double)K;
+  const bool decode = 4.0 + 0.15 * work * (1.0 + rows / 16.0) <= 7.1 + 2.0e-3 * (double)K + 0.05 * work;
+  if (can && (force == 1 || (force == 0 && decode))) return {true, {}};
   if (force == 256) return {false, {256, 128}};
   if (force == 128) return {false, {128, 128}};
-  if (force == 64) return {false, {128, 64}};
-  return {false, R >= 64 * E ? mxfp8::Fp4Plan{128, 128} : mxfp8::Fp4Plan{128, 64}};
+  if (force == 64 || rows < 128.0) return {false, {128, 64}};
+  // Wide tiles read the least through L2, but one workgroup fills a compute
+  // unit: where there are several rounds of them.
+  return {false, (double)R / 128.0 * ((double)N / 256.0) >= 6.0 * 256.0 ? mxfp8::Fp4Plan{256, 128}
+                                                                         : mxfp8::Fp4Plan{128, 128}};
 }
 bool experts_shape_ok(int64_t x_rows, int64_t R, int64_t N, int64_t K, int64_t E) {
   return x_rows >= 0 && R >= 0 && R <= kMaxSlots && x_rows <= R && N >= 1 && N <= kMaxN && summed_ok(K) &&

@@ -544,6 +544,7 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kGather, kRing>::kBytes >
     // segments (a wave's LDS accesses run in order: no waits).
     {
       typedef unsigned int u4v __attribute__((ext_vector_type(4)));
+      typedef u4v u4a2 __attribute__((aligned(2)));
       uint8_t* reg = smem + L::kEpiAt + wave * L::kEpiWave;
       const int nw = cur.col0 + wn * 16 * NA, mw = cur.row0 + wm * 16 * NB;
       constexpr int kLanesRow = 2 * NA, kRows = 64 / kLanesRow, kPasses = L::kEpiRows / kRows;
@@ -571,8 +572,11 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kGather, kRing>::kBytes >
             const int m = mw + 16 * k + L::kEpiRows * part + rr + kRows * r, n = nw + cc;
             if (m >= cur.row_end || n >= p.N) continue;
             uint16_t* d = p.y + (size_t)m * p.ldy + n;
-            if (p.vec && n + 7 < p.N) {
-              __builtin_nontemporal_store(o[r], reinterpret_cast<u4v*>(d));
+            if (n + 7 < p.N) {
+              // (pieces that are not on 16 bytes: the hardware serves them too,
+              // but parts of cache lines are better left for L2 to join)
+              if (p.vec) __builtin_nontemporal_store(o[r], reinterpret_cast<u4v*>(d));
+              else *reinterpret_cast<u4a2*>(d) = o[r];
             } else {
               for (int e = 0; e < 8; ++e)
                 if (n + e < p.N) d[e] = (uint16_t)(o[r][e >> 1] >> (16 * (e & 1)));
@@ -651,7 +655,6 @@ int launch_experts_fp4_tile(const ExpertsArgs& a, const void* q, const void* s, 
   // At most one more row tile per expert than the rows fill.
   const int64_t row_tiles = a.R / plan.mt + std::min(a.E, a.R);
   const int64_t tiles = row_tiles * ((a.N + plan.nt - 1) / plan.nt);
-  if (plan.nt == 256 && plan.mt == 256) return go<8, 8, true, true, 4>(p, tiles, stream);
   if (plan.nt == 256) return go<8, 4, true, true, 4>(p, tiles, stream);
   if (plan.mt == 128) return go<4, 4, true, true, 4>(p, tiles, stream);
   return go<4, 2, true, true, 4>(p, tiles, stream);

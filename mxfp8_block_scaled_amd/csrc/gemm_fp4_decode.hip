@@ -30,7 +30,6 @@ struct DecodeArgs {
   const uint16_t* bias;
   uint16_t* y;
   int64_t ldy;
-  int vec;                 // y 8-byte aligned, ldy % 4 == 0
   // experts
   int R, E, topk, x_rows;
   const int* slots;
@@ -55,8 +54,9 @@ __device__ inline void store4(const DecodeArgs& p, const v4f& v, const float* bv
   const uint32_t lo = pack_bf16x2(v[0] + bv[0], v[1] + bv[1]);
   const uint32_t hi = pack_bf16x2(v[2] + bv[2], v[3] + bv[3]);
   uint16_t* yr = p.y + (size_t)m * p.ldy + n;
-  if (p.vec && n + 3 < p.N) {
-    *reinterpret_cast<uint2*>(yr) = make_uint2(lo, hi);
+  typedef uint32_t u2a2 __attribute__((ext_vector_type(2), aligned(2)));   // (the hardware serves any address)
+  if (n + 3 < p.N) {
+    *reinterpret_cast<u2a2*>(yr) = u2a2{lo, hi};
   } else {
     yr[0] = (uint16_t)lo;
     if (n + 1 < p.N) yr[1] = (uint16_t)(lo >> 16);
@@ -98,21 +98,22 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_fp4_decode_kernel(DecodeArgs
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int c = 64 * u + lane;
-      const uint64_t m = __ballot(p.offsets[min(c + 1, p.E)] > p.offsets[min(c, p.E)]);
+      const int first = max(p.offsets[min(c, p.E)], 0), last = min(p.offsets[min(c + 1, p.E)], p.R);
+      const uint64_t m = __ballot(last > first);
       const int n = __popcll(m);
       if (e < 0) {
         if (at < n) {
           const bool mine = ((m >> lane) & 1) && __popcll(m & ((1ull << lane) - 1ull)) == at;
-          e = 64 * u + __ffsll((unsigned long long)__ballot(mine)) - 1;
+          const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(mine)) - 1);
+          e = 64 * u + l;
+          row0 = __builtin_amdgcn_readlane(first, l);
+          row_end = __builtin_amdgcn_readlane(last, l);
         } else {
           at -= n;
         }
       }
     }
-    e = __builtin_amdgcn_readfirstlane(e);
     if (e < 0) return;                       // (fewer experts with rows than workgroups)
-    row0 = __builtin_amdgcn_readfirstlane(max(p.offsets[e], 0));
-    row_end = __builtin_amdgcn_readfirstlane(min(p.offsets[e + 1], p.R));
     group = (int64_t)e * ((p.N + kGroupRows - 1) / kGroupRows);
   } else {
     // Dies take contiguous runs of 16-row blocks.
@@ -146,7 +147,7 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_fp4_decode_kernel(DecodeArgs
               in && u < nsteps ? *reinterpret_cast<const uint4*>(xr + u * 128 + c * 8) : make_uint4(0u, 0u, 0u, 0u);
     }
   };
-  load_rows(row0);
+  // The weight first: with gathered rows the others wait for their indices.
   uint4 w[kSteps];
   int wsc[kSteps];
 #pragma unroll
@@ -155,6 +156,7 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_fp4_decode_kernel(DecodeArgs
     w[u] = *reinterpret_cast<const uint4*>(wrow + (size_t)ks * kPieceBytes);
     wsc[u] = srow[(size_t)ks * 2 * kTileScaleBytes];
   }
+  load_rows(row0);
   const int n = n0 + 4 * g;
   float bv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (p.bias != nullptr && wave < kGroups) {
@@ -283,7 +285,7 @@ int decode(const DecodeArgs& p, int64_t blocks, hipStream_t stream) {
       return go(gemm_fp4_decode_kernel<16, 2, 2, false>, 16);
     }
   }
-  if (KS <= 8) return go(gemm_fp4_decode_kernel<8, 1, 1, kExperts>, 8);
+  if (KS <= 8) return go(gemm_fp4_decode_kernel<4, 2, 1, kExperts>, 4);
   if (KS <= 16) return go(gemm_fp4_decode_kernel<8, 2, 1, kExperts>, 8);
   if (KS <= 32) return go(gemm_fp4_decode_kernel<16, 2, 1, kExperts>, 16);
   return go(gemm_fp4_decode_kernel<16, 4, 1, kExperts>, 16);
@@ -311,7 +313,6 @@ int launch_gemm_fp4_mid(const void* qp, const void* sp, int64_t M, int64_t K, co
   p.bias = (const uint16_t*)bias;
   p.y = (uint16_t*)y;
   p.ldy = ldy;
-  p.vec = ldy % 4 == 0 && ((uintptr_t)y & 7) == 0;
   if (M <= 32) return mid<16, 2, 2>(qp, sp, p, stream);
   if (M <= 64) return mid<16, 4, 2>(qp, sp, p, stream);
   return mid<8, 8, 2>(qp, sp, p, stream);
@@ -330,7 +331,6 @@ int launch_gemm_fp4_decode(const void* x, int64_t ldx, int64_t M, int64_t K, con
   p.bias = (const uint16_t*)bias;
   p.y = (uint16_t*)y;
   p.ldy = ldy;
-  p.vec = ldy % 4 == 0 && ((uintptr_t)y & 7) == 0;
   return decode<false>(p, (N + 15) / 16, stream);
 }
 
@@ -344,7 +344,6 @@ int launch_experts_fp4_decode(const ExpertsArgs& a, hipStream_t stream) {
   p.N = (int)a.N;
   p.y = (uint16_t*)a.y;
   p.ldy = a.ldy;
-  p.vec = a.ldy % 4 == 0 && ((uintptr_t)a.y & 7) == 0;
   p.R = (int)a.R;
   p.E = (int)a.E;
   p.topk = (int)a.topk;

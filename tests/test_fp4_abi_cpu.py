@@ -72,9 +72,9 @@ def test_experts():
     refuse(api.lib().mxfp8_moe_prepare_experts_fp4, (P, P, 4, 130, 512, P, P, None), [
         (2, 0, SHAPE), (2, 257, SHAPE), (3, 0, SHAPE), (4, 128, SHAPE), (0, None, NULLPTR), (1, None, NULLPTR),
         (5, None, NULLPTR), (6, None, NULLPTR), (0, P + 8, ALIGN), (5, P + 16, ALIGN), (6, P + 16, ALIGN)])
-    ok = (P, 600, 512, 512, P, 4, P, 2400, 8, P, P, 130, P, 130, P, BIG, None)
+    ok = (P, 6000, 512, 512, P, 4, P, 24000, 8, P, P, 130, P, 130, P, BIG, None)
     refuse(api.lib().mxfp8_moe_linear_w4a4, ok, [
-        (1, 599, SHAPE), (1, -1, SHAPE), (2, 128, SHAPE), (5, 0, SHAPE), (5, 17, SHAPE), (7, 2401, SHAPE), (8, 0, SHAPE),
+        (1, 5999, SHAPE), (1, -1, SHAPE), (2, 128, SHAPE), (5, 0, SHAPE), (5, 17, SHAPE), (7, 24001, SHAPE), (8, 0, SHAPE),
         (8, 257, SHAPE), (11, 0, SHAPE), (0, None, NULLPTR), (6, None, NULLPTR), (9, None, NULLPTR), (10, None, NULLPTR),
         (12, None, NULLPTR), (3, 504, LD), (3, 514, LD), (13, 129, LD), (0, P + 8, ALIGN), (4, P + 2, ALIGN),
         (6, P + 2, ALIGN), (9, P + 16, ALIGN), (14, None, WORKSPACE), (15, 100, WORKSPACE), (14, P + 16, ALIGN),
