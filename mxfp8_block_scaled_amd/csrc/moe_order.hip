@@ -75,6 +75,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const Id* __re
     const int parts = kSortThreads / bins, b = tid % bins, part = tid / bins;
     if (part < parts) {
       int lower = 0, all = 0;
+#pragma unroll 8
       for (int g = part; g < (int)gridDim.x; g += parts) {
         const int n = counts[(int64_t)g * bins + b];
         all += n;
@@ -208,10 +209,13 @@ struct Piece {
     for (int e = 0; e < kN; ++e) v[e] = e < n ? p[e] : El(0);
     return __builtin_bit_cast(u4, v);
   }
+  // kPast: around the caches (non-temporal)
+  template <bool kPast>
   __device__ static void store(El* p, u4 v, int n) {
+    using To = typename std::conditional<kAligned, u4, Any>::type;
     if (n >= kN) {
-      if constexpr (kAligned) *reinterpret_cast<u4*>(p) = v;
-      else *reinterpret_cast<Any*>(p) = v;
+      if constexpr (kPast) __builtin_nontemporal_store((To)v, reinterpret_cast<To*>(p));
+      else *reinterpret_cast<To*>(p) = v;
       return;
     }
     El w[kN];
@@ -249,7 +253,7 @@ constexpr int kRowThreads = 256;
 
 }  // namespace
 
-template <typename El, bool kAligned>
+template <typename El, bool kAligned, bool kPast>
 __global__ __launch_bounds__(kRowThreads) void permute_kernel(const El* __restrict__ x, int64_t ldx, int64_t total,
                                                               int H, int pieces, int topk, int R,
                                                               const int* __restrict__ rows,
@@ -265,11 +269,12 @@ __global__ __launch_bounds__(kRowThreads) void permute_kernel(const El* __restri
   const u4 zero = {0, 0, 0, 0};
   for (int j = 0; j < topk; ++j) {
     const int r = rows[t * topk + j];
-    if ((uint32_t)r < (uint32_t)R) P::store(xs + (int64_t)r * lds + c, r < here ? v : zero, n);
+    if ((uint32_t)r < (uint32_t)R) P::template store<kPast>(xs + (int64_t)r * lds + c, r < here ? v : zero, n);
   }
 }
 
-template <typename El, bool kAligned>
+// kBatch: rows in flight.
+template <typename El, bool kAligned, bool kPast, int kBatch>
 __global__ __launch_bounds__(kRowThreads) void unpermute_kernel(const El* __restrict__ ys, int64_t lds, int64_t total,
                                                                 int H, int pieces, int topk, int R,
                                                                 const int* __restrict__ rows,
@@ -283,7 +288,6 @@ __global__ __launch_bounds__(kRowThreads) void unpermute_kernel(const El* __rest
   const int c = (int)(i - t * pieces) * P::kN, n = H - c;
   const uint32_t here = (uint32_t)min(max(*kept, 0), R);
   float acc[P::kN] = {};
-  constexpr int kBatch = 4;   // rows in flight
   for (int j0 = 0; j0 < topk; j0 += kBatch) {
     u4 v[kBatch];
     float w[kBatch];
@@ -306,13 +310,13 @@ __global__ __launch_bounds__(kRowThreads) void unpermute_kernel(const El* __rest
       }
     }
   }
-  P::store(y + t * ldy + c, P::narrow(acc), n);
+  P::template store<kPast>(y + t * ldy + c, P::narrow(acc), n);
 }
 
 // kWaves waves per token, their lanes along the row; the partial dot products
 // of a token's slots are added over lanes and then over waves, in a fixed
 // order.  A workgroup has four tokens with one wave each, or one with four.
-template <typename El, bool kAligned, int kWaves>
+template <typename El, bool kAligned, bool kPast, int kWaves>
 __global__ __launch_bounds__(kRowThreads) void unpermute_backward_kernel(
     const El* __restrict__ dy, int64_t lddy, int64_t T, int H, int pieces, int topk, int R,
     const int* __restrict__ rows,
@@ -357,7 +361,7 @@ __global__ __launch_bounds__(kRowThreads) void unpermute_backward_kernel(
             float d[P::kN];
 #pragma unroll
             for (int e = 0; e < P::kN; ++e) d[e] = r[u] < here ? w[u] * g[e] : 0.0f;
-            P::store(dys + (int64_t)r[u] * ldd + c, P::narrow(d), n);
+            P::template store<kPast>(dys + (int64_t)r[u] * ldd + c, P::narrow(d), n);
           }
         }
       }
@@ -387,16 +391,23 @@ __global__ __launch_bounds__(kRowThreads) void unpermute_backward_kernel(
 namespace {
 bool rows16(const void* p, int64_t ld, int64_t size) { return p == nullptr || (((uintptr_t)p | (uintptr_t)(ld * size)) & 15) == 0; }
 
-// Calls go(element, aligned) with the types as values.
+// Matrices larger than the chip's L2s: results go around the caches (4096
+// tokens, top 8, H 2048 in bf16: there 29 to 28 us, back 29 to 26, gradient 67
+// to 61; a few kilobytes written that way come back slower, 3.2 to 3.7 us).
+bool past_caches(const PermuteArgs& a) { return a.T * a.topk * a.H * (a.bf16 ? 2 : 4) > (int64_t)32 << 20; }
+
+// Calls go(element, aligned, past the caches) with the types as values.
 template <typename Go>
-void by_type(int bf16, bool aligned, Go&& go) {
-  if (bf16) {
-    if (aligned) go(uint16_t{}, std::true_type{});
-    else go(uint16_t{}, std::false_type{});
-  } else {
-    if (aligned) go(float{}, std::true_type{});
-    else go(float{}, std::false_type{});
-  }
+void by_type(const PermuteArgs& a, bool aligned, Go&& go) {
+  auto with = [&](auto el) {
+    const bool past = past_caches(a);
+    if (aligned && past) go(el, std::true_type{}, std::true_type{});
+    else if (aligned) go(el, std::true_type{}, std::false_type{});
+    else if (past) go(el, std::false_type{}, std::true_type{});
+    else go(el, std::false_type{}, std::false_type{});
+  };
+  if (a.bf16) with(uint16_t{});
+  else with(float{});
 }
 }  // namespace
 
@@ -404,9 +415,9 @@ int launch_moe_permute(const PermuteArgs& a, hipStream_t stream) {
   const int size = a.bf16 ? 2 : 4;
   const int pieces = (int)((a.H + 16 / size - 1) / (16 / size));
   const int64_t total = a.T * pieces;
-  by_type(a.bf16, rows16(a.tokens, a.ldt, size) && rows16(a.out_sorted, a.ldo, size), [&](auto el, auto al) {
+  by_type(a, rows16(a.tokens, a.ldt, size) && rows16(a.out_sorted, a.ldo, size), [&](auto el, auto al, auto past) {
     using El = decltype(el);
-    hipLaunchKernelGGL((permute_kernel<El, decltype(al)::value>), dim3((unsigned)((total + kRowThreads - 1) / kRowThreads)),
+    hipLaunchKernelGGL((permute_kernel<El, decltype(al)::value, decltype(past)::value>), dim3((unsigned)((total + kRowThreads - 1) / kRowThreads)),
                        dim3(kRowThreads), 0, stream, (const El*)a.tokens, a.ldt, total, (int)a.H, pieces, (int)a.topk,
                        (int)(a.T * a.topk), a.rows, a.kept, (El*)a.out_sorted, a.ldo);
   });
@@ -417,13 +428,16 @@ int launch_moe_unpermute(const PermuteArgs& a, hipStream_t stream) {
   const int size = a.bf16 ? 2 : 4;
   const int pieces = (int)((a.H + 16 / size - 1) / (16 / size));
   const int64_t total = a.T * pieces;
-  by_type(a.bf16, rows16(a.sorted, a.lds, size) && rows16(a.out_tokens, a.ldo, size), [&](auto el, auto al) {
+  by_type(a, rows16(a.sorted, a.lds, size) && rows16(a.out_tokens, a.ldo, size), [&](auto el, auto al, auto past) {
     using El = decltype(el);
-    hipLaunchKernelGGL((unpermute_kernel<El, decltype(al)::value>),
-                       dim3((unsigned)((total + kRowThreads - 1) / kRowThreads)), dim3(kRowThreads), 0, stream,
-                       (const El*)a.sorted, a.lds, total, (int)a.H, pieces, (int)a.topk,
-                       (int)(a.T * a.topk), a.rows, a.kept, a.weights,
-                       (El*)a.out_tokens, a.ldo);
+    auto go = [&](auto kern) {
+      hipLaunchKernelGGL(kern, dim3((unsigned)((total + kRowThreads - 1) / kRowThreads)), dim3(kRowThreads), 0, stream,
+                         (const El*)a.sorted, a.lds, total, (int)a.H, pieces, (int)a.topk, (int)(a.T * a.topk), a.rows,
+                         a.kept, a.weights, (El*)a.out_tokens, a.ldo);
+    };
+    if (a.topk <= 2) go(unpermute_kernel<El, decltype(al)::value, decltype(past)::value, 2>);
+    else if (a.topk <= 4) go(unpermute_kernel<El, decltype(al)::value, decltype(past)::value, 4>);
+    else go(unpermute_kernel<El, decltype(al)::value, decltype(past)::value, 8>);
   });
   return hipGetLastError() == hipSuccess ? 0 : -7;
 }
@@ -432,7 +446,7 @@ int launch_moe_unpermute_backward(const PermuteArgs& a, hipStream_t stream) {
   const int size = a.bf16 ? 2 : 4;
   const int pieces = (int)((a.H + 16 / size - 1) / (16 / size));
   const bool al16 = rows16(a.tokens, a.ldt, size) && rows16(a.sorted, a.lds, size) && rows16(a.out_sorted, a.ldo, size);
-  by_type(a.bf16, al16, [&](auto el, auto al) {
+  by_type(a, al16, [&](auto el, auto al, auto past) {
     using El = decltype(el);
     auto go = [&](auto kern, int tokens) {
       hipLaunchKernelGGL(kern, dim3((unsigned)((a.T + tokens - 1) / tokens)), dim3(kRowThreads), 0, stream,
@@ -440,8 +454,8 @@ int launch_moe_unpermute_backward(const PermuteArgs& a, hipStream_t stream) {
                          (const El*)a.sorted, a.lds, a.weights, (El*)a.out_sorted, a.ldo, a.dweights);
     };
     // Few tokens: four waves for each, or most of the chip would idle.
-    if (a.T < 2048) go(unpermute_backward_kernel<El, decltype(al)::value, 4>, 1);
-    else go(unpermute_backward_kernel<El, decltype(al)::value, 1>, 4);
+    if (a.T < 2048) go(unpermute_backward_kernel<El, decltype(al)::value, decltype(past)::value, 4>, 1);
+    else go(unpermute_backward_kernel<El, decltype(al)::value, decltype(past)::value, 1>, 4);
   });
   return hipGetLastError() == hipSuccess ? 0 : -7;
 }
