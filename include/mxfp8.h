@@ -565,6 +565,7 @@ int mxfp8_linear_w4a4(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, con
  * Test hook: pin the form of mxfp8_linear_w4a4, mxfp8_gemm_packed_fp4 and
  * mxfp8_moe_linear_w4a4: 0 = by shape, 1 = the decode form where it applies
  * (dense M <= 16 and K <= 8192, or M <= 32 and K <= 4096; experts K <= 8192),
+ * 2 = 128 x 64 tiles that quantize their rows themselves (K <= 2048),
  * 16 = the dense layer's form of 16 weight rows on packed activations where it
  * applies (M <= 128), 64 / 128 / 256 = tiles of 128 weight rows x 64 / 128
  * rows, or 256 weight rows x 256 (dense) / 128 (experts) rows.  The workspace

@@ -1327,32 +1327,40 @@ def _unpermute(ys, order, weights):
     return y
 
 
+def _backward_once(backward):
+    """``backward`` for a Function whose gradient has none of its own: torch's
+    wrapper, which makes second derivatives an error, costs some microseconds
+    and changes nothing in an ordinary pass."""
+    once = torch.autograd.function.once_differentiable(backward)
+    return staticmethod(lambda ctx, d: once(ctx, d) if torch.is_grad_enabled() else backward(ctx, d))
+
+
 class _MoEPermute(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, order):
         ctx.order = order
         return _permute(x, order)
 
-    @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_backward_once
     def backward(ctx, dxs):
-        _check_capture(ctx, _stream(dxs.device), torch.cuda.is_current_stream_capturing())
-        return _unpermute(_matrix(dxs, ctx.order.T * ctx.order.topk, "dxs"), ctx.order, None), None
+        if torch.cuda.is_current_stream_capturing():
+            _check_capture(ctx, _stream(dxs.device), True)
+        order = ctx.order
+        return _unpermute(_matrix(dxs, order.T * order.topk, "dxs"), order, None), None
 
 
 class _MoEUnpermute(torch.autograd.Function):
     @staticmethod
     def forward(ctx, ys, weights, order):
-        need_ys, need_w, _ = ctx.needs_input_grad
         ctx.order = order
-        ctx.save_for_backward(ys if need_w else None, weights)
+        ctx.save_for_backward(ys if ctx.needs_input_grad[1] else None, weights)
         return _unpermute(ys, order, weights)
 
-    @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_backward_once
     def backward(ctx, dy):
         stream = _stream(dy.device)
-        _check_capture(ctx, stream, torch.cuda.is_current_stream_capturing())
+        if torch.cuda.is_current_stream_capturing():
+            _check_capture(ctx, stream, True)
         need_ys, need_w, _ = ctx.needs_input_grad
         ys, weights = ctx.saved_tensors
         order = ctx.order

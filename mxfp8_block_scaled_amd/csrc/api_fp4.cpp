@@ -64,6 +64,13 @@ double tile_us(int nt, int mt, int64_t M, int64_t N, int64_t K) {
   return 7.1 + 1.6e-3 * k + more * (0.4 + 1.45e-3 * k);
 }
 
+double fused_us(int64_t M, int64_t N, int64_t K) {
+  const double k = (double)K;
+  const int64_t tiles = (M + 63) / 64 * ((N + 127) / 128);
+  return 4.6 + (1.3e-3 + 8.0e-5 * (double)std::min<int64_t>(64, M)) * k +
+         std::max(0.0, (double)tiles / 256.0 - 1.0) * (1.2 + 2.7e-3 * k);
+}
+
 // The GEMM on packed activations: nt == 16 is the 16-row form.
 mxfp8::Fp4Plan tile_plan(int64_t M, int64_t N, int64_t K, double* us = nullptr) {
   const int force = g_force.load(std::memory_order_relaxed);
@@ -83,14 +90,19 @@ mxfp8::Fp4Plan tile_plan(int64_t M, int64_t N, int64_t K, double* us = nullptr) 
   return best;
 }
 
-// One launch that quantizes inside, without a workspace.
-bool decode_form(int64_t M, int64_t N, int64_t K) {
-  if (M > mxfp8::fp4_decode_max_m(K)) return false;
+// The forms of one launch that quantizes inside, without a workspace: decode,
+// and 128 x 64 tiles.  0: neither.
+enum { kTwoLaunches = 0, kDecode = 1, kFusedTiles = 2 };
+int one_launch(int64_t M, int64_t N, int64_t K) {
+  const bool decode = M <= mxfp8::fp4_decode_max_m(K), fused = K <= mxfp8::kFp4FusedMaxK;
   const int force = g_force.load(std::memory_order_relaxed);
-  if (force != 0) return force == 1;
+  if (force != 0) return force == 1 && decode ? kDecode : force == 2 && fused ? kFusedTiles : kTwoLaunches;
   double us = 0.0;
   tile_plan(M, N, K, &us);
-  return decode_us(M, N, K) <= us;
+  us += 1.0;   // (outside of a captured graph a second launch costs the host about 5 us)
+  const double td = decode ? decode_us(M, N, K) : 1e30, tf = fused ? fused_us(M, N, K) : 1e30;
+  if (td <= std::min(tf, us)) return kDecode;
+  return tf <= us ? kFusedTiles : kTwoLaunches;
 }
 
 int gemm(const void* q, const void* s, int64_t M, int64_t K, const void* wp, const void* wsp, int64_t N,
@@ -115,7 +127,7 @@ int check_out(const void* y, int64_t N, int64_t ldy, const void* bias) {
 }
 
 size_t linear_ws(int64_t M, int64_t N, int64_t K) {
-  if (M == 0 || decode_form(M, N, K)) return 0;
+  if (M == 0 || one_launch(M, N, K) != kTwoLaunches) return 0;
   return round_up(act_bytes(M, K), 256) + round_up(act_scale_bytes(M, K), 256);
 }
 
@@ -137,32 +149,43 @@ int check_rows(int dtype, int64_t T, int64_t H, int64_t topk) {
 }
 
 struct ExpertsForm {
-  bool decode;
+  int one;               // as one_launch
   mxfp8::Fp4Plan plan;
 };
 // The same for the experts, whose rows' spread the host does not know: X
 // experts with rows at most, R / X rows each.  Decode reads all their weights
-// with its rows converted again for each 16 weight rows; tiles take the longer
-// start.  For example (R / E; decode, tiles of 128 x 64, 128 x 128, 256 x 128),
-// 128 experts, N x K = 1536 x 2048:
-//   8 rows in all   7.6   11.7
-//   0.25           17.7   16.4
-//   1              45     25     30     31
-//   64                    60     61     62
-//   256                  140    124    114
+// with its rows converted again for each 16 weight rows; tiles that quantize
+// their rows take a longer start, a quantizer before them one more launch.  For
+// example (rows per expert; decode, 128 x 64 tiles that quantize, tiles of 128 x
+// 64, 128 x 128, 256 x 128), 128 experts, N x K = 1536 x 2048 and 2048 x 768:
+//   8 rows in all   7.6   11.3   11.7                     5.8    6.8    8.4
+//   0.25           17.7   20.8   16.4                    13.1    9.7   11.6
+//   1              45     30.8   25     30     31        28.7   15.3   16.0
+//   64                           60     61     62                       40    42    42
+//   256                         140    124    114                       98    89    84
 ExpertsForm experts_form(int64_t R, int64_t N, int64_t K, int64_t E) {
   const int force = g_force.load(std::memory_order_relaxed);
   const bool can = K <= mxfp8::kFp4DecodeMaxK;
   const double X = (double)std::max<int64_t>(1, std::min(E, R)), rows = (double)R / X;
   const double work = 1e-6 * X * (double)N * (double)K;
-  const bool decode = 4.0 + 0.15 * work * (1.0 + rows / 16.0) <= 7.1 + 2.0e-3 * (double)K + 0.05 * work;
-  if (can && (force == 1 || (force == 0 && decode))) return {true, {}};
-  if (force == 256) return {false, {256, 128}};
-  if (force == 128) return {false, {128, 128}};
-  if (force == 64 || rows < 128.0) return {false, {128, 64}};
+  const bool can_decode = K <= mxfp8::kFp4DecodeMaxK, can_fuse = K <= mxfp8::kFp4FusedMaxK;
+  if (force == 1 && can_decode) return {kDecode, {}};
+  if (force == 2 && can_fuse) return {kFusedTiles, {}};
+  if (force == 0) {
+    const double k = (double)K, tiles = X * (double)((N + 127) / 128);
+    const double two = 8.1 + 2.0e-3 * k + 0.05 * work;
+    const double td = can_decode && rows <= 8.0 ? 4.0 + 0.15 * work * (1.0 + rows / 4.0) : 1e30;
+    const double tf = can_fuse && (K <= 1024 || tiles <= 256.0)
+                          ? 4.6 + 2.7e-3 * k + work * (0.045 + 8.0e-3 * rows) : 1e30;
+    if (td <= std::min(tf, two)) return {kDecode, {}};
+    if (tf <= two) return {kFusedTiles, {}};
+  }
+  if (force == 256) return {kTwoLaunches, {256, 128}};
+  if (force == 128) return {kTwoLaunches, {128, 128}};
+  if (force == 64 || rows < 128.0) return {kTwoLaunches, {128, 64}};
   // Wide tiles read the least through L2, but one workgroup fills a compute
   // unit: where there are several rounds of them.
-  return {false, (double)R / 128.0 * ((double)N / 256.0) >= 6.0 * 256.0 ? mxfp8::Fp4Plan{256, 128}
+  return {kTwoLaunches, (double)R / 128.0 * ((double)N / 256.0) >= 6.0 * 256.0 ? mxfp8::Fp4Plan{256, 128}
                                                                          : mxfp8::Fp4Plan{128, 128}};
 }
 bool experts_shape_ok(int64_t x_rows, int64_t R, int64_t N, int64_t K, int64_t E) {
@@ -172,7 +195,7 @@ bool experts_shape_ok(int64_t x_rows, int64_t R, int64_t N, int64_t K, int64_t E
 }
 size_t experts_q_bytes(int64_t x_rows, int64_t K) { return round_up((size_t)x_rows * (size_t)(K / 2), 256); }
 size_t experts_ws(int64_t x_rows, int64_t R, int64_t N, int64_t K, int64_t E) {
-  if (R == 0 || experts_form(R, N, K, E).decode) return 0;
+  if (R == 0 || experts_form(R, N, K, E).one != kTwoLaunches) return 0;
   return experts_q_bytes(x_rows, K) + round_up((size_t)x_rows * (size_t)mxfp8::fp4_scale_pitch(K), 256);
 }
 
@@ -236,9 +259,13 @@ int mxfp8_linear_w4a4(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, con
   if (need > 0 && (!workspace || workspace_bytes < need)) return MXFP8_E_WORKSPACE;
   if (!aligned(workspace, 256)) return MXFP8_E_ALIGN;
   if (int st = mxfp8::check_device_current()) return st;
-  if (decode_form(M, N, K))
+  const int form = one_launch(M, N, K);
+  if (form == kDecode)
     return mxfp8::launch_gemm_fp4_decode(x_bf16, ldx, M, K, w_packed, s_packed, N, bias_bf16, y_bf16, ldy,
                                          (hipStream_t)stream);
+  if (form == kFusedTiles)
+    return mxfp8::launch_gemm_fp4_fused(x_bf16, ldx, M, K, w_packed, s_packed, N, bias_bf16, y_bf16, ldy,
+                                        (hipStream_t)stream);
   uint8_t* q = (uint8_t*)workspace;
   uint8_t* s = q + round_up(act_bytes(M, K), 256);
   if (int st = mxfp8::launch_quantize_packed_fp4(x_bf16, M, K, ldx, q, s, (hipStream_t)stream)) return st;
@@ -246,7 +273,7 @@ int mxfp8_linear_w4a4(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, con
 }
 
 int mxfp8_debug_force_w4a4(int form) {
-  if (form != 0 && form != 1 && form != 16 && form != 64 && form != 128 && form != 256) return MXFP8_E_SHAPE;
+  if (form != 0 && form != 1 && form != 2 && form != 16 && form != 64 && form != 128 && form != 256) return MXFP8_E_SHAPE;
   return g_force.exchange(form);
 }
 
@@ -430,7 +457,8 @@ int mxfp8_moe_linear_w4a4(const void* x_bf16, int64_t x_rows, int64_t K, int64_t
   a.y = y_bf16;
   a.ldy = ldy;
   const ExpertsForm f = experts_form(R, N, K, E);
-  if (f.decode) return mxfp8::launch_experts_fp4_decode(a, (hipStream_t)stream);
+  if (f.one == kDecode) return mxfp8::launch_experts_fp4_decode(a, (hipStream_t)stream);
+  if (f.one == kFusedTiles) return mxfp8::launch_experts_fp4_fused(a, (hipStream_t)stream);
   uint8_t* q = (uint8_t*)workspace;
   uint8_t* s = q + experts_q_bytes(x_rows, K);
   if (int st = mxfp8::launch_quantize_rows_fp4(x_bf16, x_rows, K, ldx, q, s, (hipStream_t)stream)) return st;

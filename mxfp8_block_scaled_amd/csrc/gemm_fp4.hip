@@ -19,7 +19,7 @@
 //    has its own position ("cursor"), kRing steps ahead, and runs on into the
 //    next tiles while a tile ends and is stored.
 //  * Scales: the packed operands' scale tiles of a pair of steps (256 K) are
-//    1 KiB per 128-row group: one copy per pair.  Of gathered rows (kGather) a
+//    1 KiB per 128-row group: one copy per pair.  Of rows by index (kRows) a
 //    copy touches one cache line per row, so it brings four steps' bytes of each
 //    (per step instead: a quarter slower on 4096 tokens, 128 experts, 1536 x
 //    2048).
@@ -52,17 +52,21 @@ __device__ __forceinline__ void b2l_4(uint32_t voff, i4v rsrc, uint32_t soff, ui
 }
 using tile::lds_addr;
 
-template <int NA, int NB, bool kGather, int kRing>
+// How the activations come: the packed operand; rows by index from row-major
+// quantized ones; or bf16 rows, quantized by the workgroup itself.
+constexpr int kPacked = 0, kRows = 1, kFused = 2;
+
+template <int NA, int NB, int kX, int kRing>
 struct Fp4Lds {
   static constexpr int kRowsN = 32 * NA, kRowsM = 32 * NB;
-  static constexpr int kW = kRowsN * 64, kX = kRowsM * 64;
-  static constexpr int kSlot = kW + kX;                    // one 128-K step
-  static constexpr int kRunsW = NA / 4, kRunsX = kGather ? 0 : (NB + 3) / 4;   // scale runs of 1 KiB per pair
+  static constexpr int kW = kRowsN * 64;
+  static constexpr int kSlot = kW + (kX == kFused ? 0 : kRowsM * 64);   // one 128-K step
+  static constexpr int kRunsW = NA / 4, kRunsX = kX == kPacked ? (NB + 3) / 4 : 0;   // scale runs of 1 KiB per pair
   static constexpr int kScale = (kRunsW + kRunsX) * 1024;  // one pair of steps
   static constexpr int kPitch = 32 * NA;                   // bytes of a staged output row
   // Rows staged at a time: eight where that lets two workgroups share a compute
   // unit's 160 KiB.
-  static constexpr int kEpiRows = kGather && NA == 4 ? 8 : 16;
+  static constexpr int kEpiRows = kX != kPacked && NA == 4 ? 8 : 16;
   static constexpr int kEpiWave = kEpiRows * kPitch;
   static constexpr int kBiasSlot = 512;                    // a tile's bias, 256 bytes per wave column
   static constexpr int kScaleAt = kRing * kSlot;
@@ -70,19 +74,24 @@ struct Fp4Lds {
   // times a wave's kEntry rows, kChunk steps; two chunks.
   static constexpr int kEntry = 8 * NB, kChunk = 32 / NB;
   static constexpr int kXsAt = kScaleAt + kRing / 2 * kScale;
-  static constexpr int kEpiAt = kXsAt + (kGather ? 2 * 4096 : 0);
+  static constexpr int kEpiAt = kXsAt + (kX == kRows ? 2 * 4096 : 0);
   static constexpr int kBiasAt = kEpiAt + 4 * kEpiWave;
-  static constexpr int kIndexAt = kBiasAt;                 // kGather: row indices instead of a bias
-  static constexpr int kJobAt = kBiasAt + (kGather ? 1024 : kRing * kBiasSlot);
+  static constexpr int kIndexAt = kBiasAt;                 // kRows: row indices instead of a bias
+  static constexpr int kJobAt = kBiasAt + (kX == kRows ? 1024 : kRing * kBiasSlot);
   static constexpr int kBytes = kJobAt + 8 * 32;           // (the cursor is at most five tiles ahead)
   static_assert(kBytes <= 160 * 1024, "LDS of a compute unit");
-  static constexpr int kCopies = NA / 2 + NB / 2;          // per wave and step, without scales
+  // kFused, behind all that: per step the tile's rows and their scale bytes.
+  static constexpr int kFusedStep = kX == kFused ? kRowsM * 64 + kRowsM * 4 : 0;
+  static constexpr int kCopies = NA / 2 + (kX == kFused ? 0 : NB / 2);   // per wave and step, without scales
 };
 
 struct Fp4Args {
   const uint8_t* q;        // activations: packed, or row-major [x_rows, K / 2]
   const uint8_t* s;        // their scales; row-major rows are s_pitch bytes apart
-  uint32_t q_bytes, s_bytes, s_pitch;   // kGather: sizes of q and s
+  uint32_t q_bytes, s_bytes, s_pitch;   // kRows: sizes of q and s
+  const uint16_t* x;       // kFused: bf16 [x_rows, K], row stride ldx
+  int64_t ldx;
+  int x_rows;
   int M, K;                // dense: activation rows
   const uint8_t* wp;
   const uint8_t* wsp;
@@ -198,10 +207,11 @@ struct ExpertTiles {
 
 }  // namespace
 
-template <int NA, int NB, bool kGather, bool kExperts, int kRing>
-__global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kGather, kRing>::kBytes > 80 * 1024 ? 1 : 2)) void gemm_fp4_kernel(
+template <int NA, int NB, int kX, bool kExperts, int kRing>
+__global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kX, kRing>::kBytes > 80 * 1024 ? 1 : 2)) void gemm_fp4_kernel(
     Fp4Args p) {
-  using L = Fp4Lds<NA, NB, kGather, kRing>;
+  using L = Fp4Lds<NA, NB, kX, kRing>;
+  constexpr bool kOwnScales = kX != kPacked;   // a lane's scale in a byte of its own
   using Tiles = typename std::conditional<kExperts, ExpertTiles<NA, NB>, DenseTiles<NA, NB>>::type;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
 
@@ -211,7 +221,7 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kGather, kRing>::kBytes >
   const int li = lane & 15, lg = lane >> 4;
   const int KS4 = p.K / 128;                                  // 128-K steps: even, at least 2
   const int GN = (p.N + kGroupRows - 1) / kGroupRows;         // weight groups (of one expert)
-  const int GM = kGather ? 0 : (p.M + kGroupRows - 1) / kGroupRows;
+  const int GM = kX != kPacked ? 0 : (p.M + kGroupRows - 1) / kGroupRows;
   const uint32_t gbytes = (uint32_t)KS4 * kTileBytes, sbytes = (uint32_t)KS4 * 2 * kTileScaleBytes;
   const Tiles tiles(p);
 
@@ -262,7 +272,7 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kGather, kRing>::kBytes >
   // rows 16 wave + 64 i + (0 .. 15), i = lane / 16.
   const int my_row = 64 * (lane >> 4) + 16 * wave + (lane & 15);
   auto fetch_index = [&](const Fp4Job& j) {
-    if constexpr (kGather) {
+    if constexpr (kX == kRows) {
       if (p.slots != nullptr) {
         const i4v r = buffer_rsrc(p.slots, j.live ? (uint32_t)p.R * 4u : 0u);
         b2l_4<0>((uint32_t)min(j.row0 + my_row, j.row_end - 1) * 4u, r, 0u, lds_addr(index_slot));
@@ -276,7 +286,7 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kGather, kRing>::kBytes >
     if constexpr (NA == 8) w1 = buffer_rsrc(p.wp + (size_t)(j.wgroup + min(1, last)) * gbytes, live * gbytes);
     const uint8_t* srun = p.wsp + (size_t)j.wgroup * sbytes;  // this wave's scale run
     if (NA == 8 && wave == 1) srun = p.wsp + (size_t)(j.wgroup + min(1, last)) * sbytes;
-    if constexpr (kGather) {
+    if constexpr (kX == kRows) {
       int row = min(j.row0 + my_row, j.row_end - 1);
       if (p.slots != nullptr) {
         row = *reinterpret_cast<const int*>(index_slot + lane * 4);
@@ -292,7 +302,7 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kGather, kRing>::kBytes >
         const int tr = 64 * i + 16 * wave + (lane >> 2);      // its row in the tile
         vx[i] = r * (uint32_t)(p.K / 2) + (uint32_t)((lane & 3) ^ swz(tr)) * 16u;
       }
-    } else {
+    } else if constexpr (kX == kPacked) {
       const int xg = j.row0 / kGroupRows;
       x0 = buffer_rsrc(p.q + (size_t)xg * gbytes, live * gbytes);
       if constexpr (NB == 8) x1 = buffer_rsrc(p.q + (size_t)min(xg + 1, GM - 1) * gbytes, live * gbytes);
@@ -302,7 +312,7 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kGather, kRing>::kBytes >
       if (wave >= L::kRunsW) srun = p.s + (size_t)min(xg + wave - L::kRunsW, GM - 1) * sbytes;
     }
     sc = buffer_rsrc(srun, live * sbytes);
-    if constexpr (!kGather) {
+    if constexpr (!kExperts) {
       if (p.bias != nullptr && wm == 0) {
         // this wave column's 16 NA bias values, by whole words (an odd N's last
         // word holds one value that is not the bias's and reaches no output)
@@ -326,7 +336,7 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kGather, kRing>::kBytes >
     } else {
       constexpr int i = k - NA / 2;
       constexpr std::integral_constant<int, L::kW + i * 4096> at;
-      if constexpr (kGather) go(at, vx[i], x0, (uint32_t)q * 64u);
+      if constexpr (kX == kRows) go(at, vx[i], x0, (uint32_t)q * 64u);
       else go(at, i & 1 ? vxhi : vx[0], i < 2 ? x0 : x1, off);
     }
   };
@@ -343,7 +353,7 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kGather, kRing>::kBytes >
   int xput = 0;                                               // chunk buffer to fill next
   auto issue_all_scales = [&](int q, int pair) {
     issue_scales(q, pair);
-    if constexpr (kGather) {
+    if constexpr (kX == kRows) {
       if (q % L::kChunk == 0) {
         b2l_16<L::kXsAt>(vxs, xsr, (uint32_t)q * 4u, lds0 + (uint32_t)xput * 4096u);
         xput ^= 1;
@@ -355,19 +365,19 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kGather, kRing>::kBytes >
   auto advance_tile = [&]() {
     set_sources(get_job(ctile), ctile);
     const Fp4Job next = put_job(ctile + 1);
-    if constexpr (kGather) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if constexpr (kX == kRows) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     fetch_index(next);
   };
 
   // ------------------------------------------------------------ fragments
   struct Frags {
     i4v a[NA], b[NB];
-    int sa[2], sb[kGather ? NB : 2];
+    int sa[2], sb[kOwnScales ? NB : 2];
   };
   // A wave's rows of a 128-row group start at 16 NA wn (NA = 8: its own group)
   // and share the swizzle of row li.
   const int offA = tile_off(wn * 16 * NA + li, lg);
-  const int offB = L::kW + tile_off(wm * 16 * NB + li, lg);
+  const int offB = (kX == kFused ? L::kBytes : L::kW) + tile_off(wm * 16 * NB + li, lg);
   // Scale words of a packed operand: lane (i, g) supplies MX block g of the
   // step, block g % 2 of its scale tile g / 2; word e holds rows 16e + i + 32k
   // in byte k; rows that start at 32 z of the group: the word shifted by 8 z.
@@ -380,16 +390,19 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kGather, kRing>::kBytes >
   // entries 16 (q / 4) ..
   const int offXS = li * 16 + lg + (NB == 8 ? wm * 512 : NB == 4 ? wm * 256 : wm * 2048);
   int shiftB = NB == 8 ? 0 : NB == 4 ? 16 * wm : 8 * wm;     // NB == 2: and the tile's half of its group
-  constexpr int kReads = 4 + NA + NB + (kGather ? NB - 2 : 0);
+  constexpr int kReads = 4 + NA + NB + (kOwnScales ? NB - 2 : 0);
   // Read r of a step's fragments: the scales first.
   auto read_part = [&](int r, Frags& f, const uint8_t* st, const uint8_t* sct, const uint8_t* xs) {
-    constexpr int kSB = kGather ? NB : 2;
+    constexpr int kSB = kOwnScales ? NB : 2;
     if (r < 2) {
       f.sa[r] = (int)((uint32_t)*reinterpret_cast<const int*>(sct + offSA + 128 * r) >> shiftA);
     } else if (r < 2 + kSB) {
       const int e = r - 2;
-      if constexpr (kGather) {
-        f.sb[e] = xs[offXS + (NB == 8 ? (e & 3) * 1024 + (e >> 2) * 256 : e * 1024)];   // block q = NB wm + e
+      // xs: kRows block q = NB wm + e; kFused: the step's rows
+      if constexpr (kX == kRows) {
+        f.sb[e] = xs[offXS + (NB == 8 ? (e & 3) * 1024 + (e >> 2) * 256 : e * 1024)];
+      } else if constexpr (kX == kFused) {
+        f.sb[e] = xs[L::kBytes + L::kRowsM * 64 + (wm * 16 * NB + 16 * e + li) * 4 + lg];
       } else {
         f.sb[e] = (int)((uint32_t)*reinterpret_cast<const int*>(sct + offSB + 128 * e) >> shiftB);
       }
@@ -398,7 +411,7 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kGather, kRing>::kBytes >
       f.a[a] = *reinterpret_cast<const i4v*>(st + offA + 1024 * a);
     } else {
       const int bb = r - 2 - kSB - NA;
-      f.b[bb] = *reinterpret_cast<const i4v*>(st + offB + 1024 * bb);
+      f.b[bb] = *reinterpret_cast<const i4v*>((kX == kFused ? xs : st) + offB + 1024 * bb);
     }
   };
 
@@ -433,7 +446,7 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kGather, kRing>::kBytes >
       }
       // op_sel: the byte of the scale word (packed), byte 0 of the lane's own
       // (gathered).
-      constexpr int selA = a >> 1, selB = kGather ? 0 : (NB == 2 ? 0 : bb >> 1), sb = kGather ? bb : bb & 1;
+      constexpr int selA = a >> 1, selB = kOwnScales || NB == 2 ? 0 : bb >> 1, sb = kOwnScales ? bb : bb & 1;
       constexpr int c0 = g < 0 ? 0 : g * L::kCopies / kGaps, c1 = g < 0 ? 0 : (g + 1) * L::kCopies / kGaps;
       if constexpr (c1 > c0) {
         source(std::integral_constant<int, c0>{}, q, [&](auto at, uint32_t v, i4v r, uint32_t off) {
@@ -463,7 +476,8 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kGather, kRing>::kBytes >
   // Scales of gathered rows for step q of a tile, in the chunk buffer in use.
   int xget = 0;
   auto xs_at = [&](int q) -> const uint8_t* {
-    if constexpr (!kGather) return nullptr;
+    if constexpr (kX == kPacked) return nullptr;
+    if constexpr (kX == kFused) return smem + q * L::kFusedStep;
     return smem + L::kXsAt + xget * 4096 + q % L::kChunk / 4 * (L::kEntry * 16) + (q & 3) * 4;
   };
   auto scale_slot = [&](int pair) { return smem + L::kScaleAt + pair * L::kScale; };
@@ -473,7 +487,7 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kGather, kRing>::kBytes >
     if (cq == KS4) {
       cq = 0;
       ++ctile;
-      if constexpr (kGather) {
+      if constexpr (kX == kRows) {
         // The new tile's indices were fetched a tile ago: with fewer steps per
         // tile than slots their copies may not have been waited for.
         if (KS4 < kRing) tile::wait_vmcnt<0>();
@@ -482,28 +496,73 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kGather, kRing>::kBytes >
     }
   };
   fetch_index(put_job(0));
-  if constexpr (kGather) tile::wait_vmcnt<0>();
+  if constexpr (kX == kRows) tile::wait_vmcnt<0>();
   advance_tile();
   for (int pair = 0; pair < kRing / 2; ++pair) {
     issue_all_scales(cq, pair);
     tile::static_for<0, L::kCopies>([&](auto C) { issue(C, cq, fill(2 * pair)); });
     tile::static_for<0, L::kCopies>([&](auto C) { issue(C, cq + 1, fill(2 * pair + 1)); });
-    if (kGather && pair == kRing / 2 - 1) tile::wait_vmcnt<0>();   // (the second tile's indices)
+    if (kX == kRows && pair == kRing / 2 - 1) tile::wait_vmcnt<0>();   // (the second tile's indices)
     move_cursor();
   }
   tile::wait_vmcnt<0>();
   __builtin_amdgcn_s_barrier();
   Frags f0, f1;
   auto tile_shift = [&](const Fp4Job& j) {
-    if constexpr (NB == 2 && !kGather) shiftB = 8 * (2 * ((j.row0 % kGroupRows) / 64) + wm);
+    if constexpr (NB == 2 && kX == kPacked) shiftB = 8 * (2 * ((j.row0 % kGroupRows) / 64) + wm);
   };
   Fp4Job cur = get_job(0);
   tile_shift(cur);
   tile::static_for<0, kReads>([&](auto R) { read_part(decltype(R)::value, f0, slot(0), scale_slot(0), xs_at(0)); });
 
+  // kFused: the tile's rows into LDS, sixteen lanes per row and step, as in the
+  // packed quantizer; rows past the last keep what was there (their outputs are
+  // not stored).  One wave per SIMD: bound by its chain of instructions (64
+  // rows of 1024: 5 us), not by the loads (all rows' in flight: slower).
+  auto quantize_rows = [&](const Fp4Job& j) {
+    constexpr int kBatch = 4;
+    const int l = tid & 15, n = j.row_end - j.row0;
+#pragma unroll
+    for (int r0 = 0; r0 < L::kRowsM; r0 += 16) {
+      if (r0 >= n) break;
+      const int r = r0 + (tid >> 4);
+      const bool in = r < n;
+      int64_t row = in ? j.row0 + r : j.row0;
+      if (kExperts && p.slots != nullptr) row = min((uint32_t)p.slots[row] / (uint32_t)p.topk, (uint32_t)p.x_rows - 1u);
+      const uint16_t* xr = p.x + row * p.ldx + l * 8;
+      for (int k0 = 0; k0 < KS4; k0 += kBatch) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+          v[u] = k0 + u < KS4 ? *reinterpret_cast<const uint4*>(xr + (k0 + u) * 128) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const uint32_t sb = fp4_scale_byte(quad_max(fp4_absmax8(v[u])));
+          const uint32_t code = cvt8_fp4(v[u], fp4_scale_value(sb));
+          uint8_t* d = smem + L::kBytes + (k0 + u) * L::kFusedStep;
+          if (in && k0 + u < KS4) {
+            *reinterpret_cast<uint32_t*>(d + tile_off(r, l >> 2) + (l & 3) * 4) = code;
+            if ((l & 3) == 0) d[L::kRowsM * 64 + r * 4 + (l >> 2)] = (uint8_t)sb;
+          }
+        }
+      }
+    }
+    __syncthreads();
+  };
+
   int pair = 0, t = 0;
   for (;;) {
-    if (!kGather && p.bias != nullptr) {
+    if constexpr (kX == kFused) {
+      // (every wave's reads of the last tile's rows are done at its last step's
+      // barrier, but for those of that step itself)
+      if (t > 0) __syncthreads();
+      quantize_rows(cur);
+      tile::static_for<0, kReads>([&](auto R) {
+        constexpr int r = decltype(R)::value;
+        if constexpr ((r >= 2 && r < 2 + NB) || r >= 2 + NB + NA) read_part(r, f0, nullptr, nullptr, xs_at(0));
+      });
+    }
+    if (!kExperts && p.bias != nullptr) {
       const uint8_t* bs = bias_slot(t) + wn * 256;
 #pragma unroll
       for (int a = 0; a < NA; ++a) {
@@ -530,7 +589,7 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kGather, kRing>::kBytes >
       // (the last step of a tile reads the next tile's first fragments)
       const int qn = q + 2 == KS4 ? 0 : q + 2;
       if (qn == 0) tile_shift(nxt);
-      if (kGather && qn % L::kChunk == 0) xget ^= 1;
+      if (kX == kRows && qn % L::kChunk == 0) xget ^= 1;
       step(T{}, f1, f0, fill(2 * pair + 1), slot(2 * npair), pair, scale_slot(npair), xs_at(qn), cq + 1);
       move_cursor();
       pair = npair;
@@ -595,16 +654,19 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kGather, kRing>::kBytes >
 
 namespace {
 
-template <int NA, int NB, bool kGather, bool kExperts, int kRing>
+template <int NA, int NB, int kX, bool kExperts, int kRing>
 int go(const Fp4Args& p, int64_t tiles, hipStream_t stream) {
-  using L = Fp4Lds<NA, NB, kGather, kRing>;
-  auto kern = gemm_fp4_kernel<NA, NB, kGather, kExperts, kRing>;
+  using L = Fp4Lds<NA, NB, kX, kRing>;
+  auto kern = gemm_fp4_kernel<NA, NB, kX, kExperts, kRing>;
   static std::atomic<int> lds_set[kMaxDevices];
-  if (!set_lds_limit_once((const void*)kern, L::kBytes, lds_set)) return -7;
-  const int64_t per_cu = L::kBytes <= 80 * 1024 ? 2 : 1;
+  constexpr int most_lds = L::kBytes + (int)(kFp4FusedMaxK / 128) * L::kFusedStep;
+  static_assert(most_lds <= 160 * 1024, "LDS of a compute unit");
+  if (!set_lds_limit_once((const void*)kern, most_lds, lds_set)) return -7;
+  const int lds = L::kBytes + p.K / 128 * L::kFusedStep;
+  const int64_t per_cu = lds <= 80 * 1024 ? 2 : 1;
   const int64_t cus = device_cu_count();
   const int64_t most = std::max<int64_t>(1, (cus >= 8 ? cus - cus % 8 : cus) * per_cu);
-  hipLaunchKernelGGL(kern, dim3((unsigned)std::min(tiles, most)), dim3(kThreads), L::kBytes, stream, p);
+  hipLaunchKernelGGL(kern, dim3((unsigned)std::min(tiles, most)), dim3(kThreads), lds, stream, p);
   return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 
@@ -625,12 +687,12 @@ int launch_gemm_fp4_tile(const void* qp, const void* sp, int64_t M, int64_t K, c
   p.ldy = ldy;
   p.vec = ldy % 8 == 0 && ((uintptr_t)y & 15) == 0;
   const int64_t tiles = ((M + plan.mt - 1) / plan.mt) * ((N + plan.nt - 1) / plan.nt);
-  if (plan.nt == 256) return go<8, 8, false, false, 4>(p, tiles, stream);
+  if (plan.nt == 256) return go<8, 8, kPacked, false, 4>(p, tiles, stream);
   // One tile per compute unit: twice the slots; more: two workgroups on each.
   const bool deep = tiles <= device_cu_count();
   if (plan.mt == 128)
-    return deep ? go<4, 4, false, false, 8>(p, tiles, stream) : go<4, 4, false, false, 4>(p, tiles, stream);
-  return deep ? go<4, 2, false, false, 8>(p, tiles, stream) : go<4, 2, false, false, 4>(p, tiles, stream);
+    return deep ? go<4, 4, kPacked, false, 8>(p, tiles, stream) : go<4, 4, kPacked, false, 4>(p, tiles, stream);
+  return deep ? go<4, 2, kPacked, false, 8>(p, tiles, stream) : go<4, 2, kPacked, false, 4>(p, tiles, stream);
 }
 
 int launch_experts_fp4_tile(const ExpertsArgs& a, const void* q, const void* s, Fp4Plan plan, hipStream_t stream) {
@@ -655,9 +717,47 @@ int launch_experts_fp4_tile(const ExpertsArgs& a, const void* q, const void* s, 
   // At most one more row tile per expert than the rows fill.
   const int64_t row_tiles = a.R / plan.mt + std::min(a.E, a.R);
   const int64_t tiles = row_tiles * ((a.N + plan.nt - 1) / plan.nt);
-  if (plan.nt == 256) return go<8, 4, true, true, 4>(p, tiles, stream);
-  if (plan.mt == 128) return go<4, 4, true, true, 4>(p, tiles, stream);
-  return go<4, 2, true, true, 4>(p, tiles, stream);
+  if (plan.nt == 256) return go<8, 4, kRows, true, 4>(p, tiles, stream);
+  if (plan.mt == 128) return go<4, 4, kRows, true, 4>(p, tiles, stream);
+  return go<4, 2, kRows, true, 4>(p, tiles, stream);
+}
+
+int launch_gemm_fp4_fused(const void* x, int64_t ldx, int64_t M, int64_t K, const void* wp, const void* wsp, int64_t N,
+                          const void* bias, void* y, int64_t ldy, hipStream_t stream) {
+  Fp4Args p = {};
+  p.x = (const uint16_t*)x;
+  p.ldx = ldx;
+  p.x_rows = (int)M;
+  p.M = (int)M;
+  p.K = (int)K;
+  p.wp = (const uint8_t*)wp;
+  p.wsp = (const uint8_t*)wsp;
+  p.N = (int)N;
+  p.bias = (const uint16_t*)bias;
+  p.y = (uint16_t*)y;
+  p.ldy = ldy;
+  p.vec = ldy % 8 == 0 && ((uintptr_t)y & 15) == 0;
+  return go<4, 2, kFused, false, 4>(p, (M + 63) / 64 * ((N + 127) / 128), stream);
+}
+
+int launch_experts_fp4_fused(const ExpertsArgs& a, hipStream_t stream) {
+  Fp4Args p = {};
+  p.x = (const uint16_t*)a.x;
+  p.ldx = a.ldx;
+  p.x_rows = (int)a.x_rows;
+  p.K = (int)a.K;
+  p.wp = (const uint8_t*)a.wp;
+  p.wsp = (const uint8_t*)a.wsp;
+  p.N = (int)a.N;
+  p.y = (uint16_t*)a.y;
+  p.ldy = a.ldy;
+  p.vec = a.ldy % 8 == 0 && ((uintptr_t)a.y & 15) == 0;
+  p.R = (int)a.R;
+  p.E = (int)a.E;
+  p.topk = (int)a.topk;
+  p.slots = a.slots;
+  p.offsets = a.offsets;
+  return go<4, 2, kFused, true, 4>(p, (a.R / 64 + std::min(a.E, a.R)) * ((a.N + 127) / 128), stream);
 }
 
 }  // namespace mxfp8

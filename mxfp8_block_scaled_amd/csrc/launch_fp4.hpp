@@ -38,6 +38,12 @@ struct Fp4Plan {
 int launch_gemm_fp4_tile(const void* qp, const void* sp, int64_t M, int64_t K, const void* wp, const void* wsp,
                          int64_t N, const void* bias, void* y, int64_t ldy, hipStream_t stream, Fp4Plan plan);
 
+// The 128 x 64 tiles with the rows quantized by each workgroup: one launch, no
+// workspace; K <= kFp4FusedMaxK.
+constexpr int64_t kFp4FusedMaxK = 2048;
+int launch_gemm_fp4_fused(const void* x, int64_t ldx, int64_t M, int64_t K, const void* wp, const void* wsp, int64_t N,
+                          const void* bias, void* y, int64_t ldy, hipStream_t stream);
+
 // Rows by expert (moe_order.hip).  R = T topk slots; `rows` [R]: the sorted
 // row of each slot, `slots` [R]: its inverse, `offsets` [E + 1]: the first row
 // of each expert and the number of rows that have one (kept = offsets + E).
@@ -94,6 +100,8 @@ struct ExpertsArgs {
 };
 // Decode form: quantizes inside, no workspace.
 int launch_experts_fp4_decode(const ExpertsArgs& a, hipStream_t stream);
+// As launch_gemm_fp4_fused.
+int launch_experts_fp4_fused(const ExpertsArgs& a, hipStream_t stream);
 // Tile form on rows of launch_quantize_rows_fp4.
 int launch_experts_fp4_tile(const ExpertsArgs& a, const void* q, const void* s, Fp4Plan plan, hipStream_t stream);
 

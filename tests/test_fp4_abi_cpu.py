@@ -28,9 +28,9 @@ def test_products():
         (2, -1, SHAPE), (2, 0, OK), (3, 128, SHAPE), (6, 0, SHAPE), (6, (1 << 24) + 1, SHAPE), (0, None, NULLPTR),
         (1, None, NULLPTR), (4, None, NULLPTR), (5, None, NULLPTR), (8, None, NULLPTR), (9, 129, LD), (0, P + 128, ALIGN),
         (4, P + 16, ALIGN), (7, P + 2, ALIGN), (8, P + 1, ALIGN)])
-    refuse(api.lib().mxfp8_linear_w4a4, (P, 40, 512, 512, P, P, 130, P, P, 130, P, BIG, None), [
+    refuse(api.lib().mxfp8_linear_w4a4, (P, 400, 4096, 4096, P, P, 130, P, P, 130, P, BIG, None), [
         (1, -1, SHAPE), (1, 0, OK), (2, 128, SHAPE), (6, 0, SHAPE), (0, None, NULLPTR), (4, None, NULLPTR),
-        (5, None, NULLPTR), (8, None, NULLPTR), (3, 504, LD), (3, 513, LD), (9, 129, LD), (0, P + 8, ALIGN),
+        (5, None, NULLPTR), (8, None, NULLPTR), (3, 4088, LD), (3, 4097, LD), (9, 129, LD), (0, P + 8, ALIGN),
         (4, P + 16, ALIGN), (5, P + 16, ALIGN), (7, P + 2, ALIGN), (10, None, WORKSPACE), (11, 100, WORKSPACE),
         (10, P + 16, ALIGN)])
     # few rows need no workspace

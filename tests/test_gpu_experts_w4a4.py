@@ -38,7 +38,7 @@ def case(T, topk, E, N, K, gather, form=0, drop=0.0, seed=0, ids=None):
     assert bool((y[int(offsets[E]):] == 0).all())
 
 
-FORMS = [1, 64, 128, 256]
+FORMS = [1, 2, 64, 128, 256]
 
 
 @pytest.mark.parametrize("form", FORMS)

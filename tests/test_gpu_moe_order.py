@@ -227,3 +227,16 @@ def test_capture_with_a_live_eager_graph_is_refused():
             api.moe_permute(x, order).sum().backward()
     torch.cuda.synchronize()
     assert alive.shape == (40, 8)
+
+
+def test_no_second_derivatives():
+    order = api.moe_sort(make_ids(5, 2, 3, 1).to(dev()), 3)
+    x = torch.randn(5, 8, device=dev(), requires_grad=True)
+    xs = api.moe_permute(x, order)
+    g, = torch.autograd.grad(xs.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(g.sum(), x)
+    y = api.moe_unpermute(api.moe_permute(x, order), order, torch.ones(5, 2, device=dev()))
+    g, = torch.autograd.grad(y.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(g.sum(), x)

@@ -40,7 +40,7 @@ def test_quantize_packed(M, K):
     assert bool((q[M:] == 0).all())
 
 
-@pytest.mark.parametrize("form", [1, 16, 64, 128, 256])
+@pytest.mark.parametrize("form", [1, 2, 16, 64, 128, 256])
 @pytest.mark.parametrize("M,N,K", [(1, 1, 256), (3, 130, 512), (16, 257, 768), (16, 1000, 2048), (9, 64, 4096), (2, 33, 8192),
                                    (17, 70, 256), (32, 100, 2048), (27, 300, 4096), (20, 64, 2304)])
 def test_few_rows(form, M, N, K):
@@ -53,14 +53,14 @@ def test_mid_form(M, N, K):
     case(M, N, K, bias=(M % 2 == 1), form=16, seed=M)
 
 
-@pytest.mark.parametrize("form", [64, 128, 256])
+@pytest.mark.parametrize("form", [2, 64, 128, 256])
 @pytest.mark.parametrize("M,N,K", [(17, 128, 256), (64, 129, 512), (129, 131, 768), (300, 515, 1024), (513, 260, 1280),
                                    (1000, 1030, 512)])
 def test_forms(form, M, N, K):
     case(M, N, K, bias=(M % 2 == 1), form=form, seed=M)
 
 
-@pytest.mark.parametrize("form", [64, 128, 256])
+@pytest.mark.parametrize("form", [2, 64, 128, 256])
 @pytest.mark.parametrize("K", [256, 512, 768])
 def test_many_tiles_per_workgroup(form, K):
     """More tiles than workgroups: the copy stream runs over tile ends."""
@@ -83,13 +83,13 @@ def test_one_hot(M):
     codes, s = oracle.quantize_mxfp4(w)
     pw = api.prepare_weight_fp4(torch.from_numpy(oracle.pack_fp4(codes)).to(dev()), torch.from_numpy(s).to(dev()))
     A = ref.quantized(x)
-    for form in (1, 16, 64, 128, 256):
+    for form in (1, 2, 16, 64, 128, 256):
         with ref.forced(form):
             y = api.linear_w4a4(x.to(dev()), pw).double().cpu().numpy()
         assert np.array_equal(y, A[:, (np.arange(N) * 37) % K])
 
 
-@pytest.mark.parametrize("form", [1, 16, 64, 128, 256])
+@pytest.mark.parametrize("form", [1, 2, 16, 64, 128, 256])
 def test_not_finite(form):
     """An infinity or a NaN makes its own row's outputs NaN, and no other's."""
     M, N, K = 16, 200, 512
