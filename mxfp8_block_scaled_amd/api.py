@@ -572,14 +572,17 @@ _HERE_ALREADY = contextlib.nullcontext()
 def _on(device):
     """Context in which ``device`` is the current one (the library launches on
     the current device)."""
-    if device.index is None or device.index == torch.cuda.current_device():
+    # (torch.cuda.current_device without its check that CUDA is initialized,
+    # which a GPU tensor's device has passed)
+    if device.index is None or device.index == torch._C._cuda_getDevice():
         return _HERE_ALREADY
     return torch.cuda.device(device)
 
 
 def _same_device(first, *rest):
+    index = first.get_device()
     for t in rest:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"operands on {first.device} and {t.device}")
 
 
@@ -1267,7 +1270,8 @@ def moe_sort(ids, E):
     if ids.dtype not in (torch.int32, torch.int64) or ids.dim() != 2:
         raise ValueError(f"ids must be int32 or int64 [T, topk], got {ids.dtype} {tuple(ids.shape)}")
     _require_cuda(ids, "ids")
-    ids = ids.contiguous()
+    if not ids.is_contiguous():
+        ids = ids.contiguous()
     T, topk = ids.shape
     if not 1 <= topk <= 16:
         raise ValueError(f"topk must be 1 to 16, got {topk}")
@@ -1293,18 +1297,17 @@ def _matrix(x, rows, name):
     return x
 
 
-def _order(order):
+def _require_order(order):
     if not isinstance(order, MoEOrder):
         raise ValueError("order must be a MoEOrder (moe_sort)")
-    return order
 
 
 def _weights(weights, order):
     if weights is None:
         return None
-    if weights.dtype != torch.float32 or tuple(weights.shape) != (order.T, order.topk):
+    if weights.dtype != torch.float32 or weights.shape != order.rows.shape:
         raise ValueError(f"weights must be float32 [{order.T}, {order.topk}]")
-    return weights.contiguous()
+    return weights if weights.is_contiguous() else weights.contiguous()
 
 
 def _permute(x, order):
@@ -1381,7 +1384,7 @@ def moe_permute(x, order):
     ``xs[order.rows[t, j]] = x[t]``, ``[T * topk, H]``, zeros in the rows of
     slots without an expert.  Differentiable; the gradient adds a token's rows
     in fp32, in slot order.  In captured graphs as ``linear_b128``."""
-    order = _order(order)
+    _require_order(order)
     x = _matrix(x, order.T, "x")
     _same_device(x, order.rows)
     if not (torch.is_grad_enabled() and x.requires_grad):
@@ -1400,7 +1403,7 @@ def moe_unpermute(ys, order, weights=None):
     once.  ``weights`` fp32 ``[T, topk]``, or None for all 1.  Differentiable
     with respect to ys and weights (0 for slots without an expert).  In captured
     graphs as ``linear_b128``."""
-    order = _order(order)
+    _require_order(order)
     ys = _matrix(ys, order.T * order.topk, "ys")
     weights = _weights(weights, order)
     _same_device(ys, order.rows, weights)
@@ -1456,7 +1459,7 @@ def moe_linear_w4a4(x, ew, order, gather=False):
     ``x`` bf16 ``[T * topk, K]`` in ``order``'s rows or, with ``gather``, ``[T, K]``:
     the tokens, each row r taking its own (``moe_permute(x)`` without the copy).
     ``ew`` ExpertWeightsFP4.  Returns bf16 ``[T * topk, N]``.  No gradients."""
-    order = _order(order)
+    _require_order(order)
     if not isinstance(ew, ExpertWeightsFP4):
         raise ValueError("ew must be ExpertWeightsFP4 (moe_prepare_experts_fp4)")
     R = order.T * order.topk

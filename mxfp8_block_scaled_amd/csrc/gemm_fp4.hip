@@ -502,10 +502,11 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kX, kRing>::kBytes > 80 *
     issue_all_scales(cq, pair);
     tile::static_for<0, L::kCopies>([&](auto C) { issue(C, cq, fill(2 * pair)); });
     tile::static_for<0, L::kCopies>([&](auto C) { issue(C, cq + 1, fill(2 * pair + 1)); });
-    if (kX == kRows && pair == kRing / 2 - 1) tile::wait_vmcnt<0>();   // (the second tile's indices)
+    if (kX == kRows && cq + 2 == KS4) tile::wait_vmcnt<0>();   // (the second tile's indices)
     move_cursor();
   }
-  tile::wait_vmcnt<0>();
+  // Step 0 has landed: at most the operand copies behind it are in flight.
+  tile::wait_vmcnt<(kRing - 1) * L::kCopies>();
   __builtin_amdgcn_s_barrier();
   Frags f0, f1;
   auto tile_shift = [&](const Fp4Job& j) {
