@@ -36,6 +36,22 @@ __device__ inline uint32_t fp4_absmax8(const uint4& v) {
   return max((uint32_t)m[0], (uint32_t)m[1]);
 }
 
+// Zeros in rows [from, to) of y [.., N] (bf16, row stride ldy): the rows of slots
+// without an expert.  A wave takes whole rows, 16 bytes per lane (4096 tokens, 64
+// experts, k 8, half of the ids none, 2048 x 768: 59 us; 120 with a division and
+// two bytes per element).
+__device__ inline void zero_rows(uint16_t* y, int64_t ldy, int from, int to, int N, int waves) {
+  typedef uint32_t u4a2 __attribute__((ext_vector_type(4), aligned(2)));   // (the hardware serves any address)
+  const int lane = threadIdx.x & 63;
+  for (int64_t r = from + (int64_t)blockIdx.x * waves + (threadIdx.x >> 6); r < to; r += (int64_t)gridDim.x * waves)
+    for (int n = lane * 8; n < N; n += 64 * 8) {
+      uint16_t* d = y + r * ldy + n;
+      if (n + 7 < N) *reinterpret_cast<u4a2*>(d) = u4a2{0u, 0u, 0u, 0u};
+      else
+        for (int e = 0; n + e < N; ++e) d[e] = 0;
+    }
+}
+
 // c[u] += A[u] x B, u = 0 .. 3, on v_mfma_scale_f32_16x16x128_f8f6f4 with both
 // operands in E2M1 (cbsz, blgp 4): lane (i, g) holds K [32g, 32g + 32) of row i
 // in four registers; scales (A[u]: word u % 2, byte kSelA + u / 2), in-place

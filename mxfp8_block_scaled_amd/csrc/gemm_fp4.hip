@@ -225,15 +225,7 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kX, kRing>::kBytes > 80 *
   const uint32_t gbytes = (uint32_t)KS4 * kTileBytes, sbytes = (uint32_t)KS4 * 2 * kTileScaleBytes;
   const Tiles tiles(p);
 
-  if constexpr (kExperts) {
-    // Rows of slots without an expert: zeros.
-    const int64_t n = (int64_t)(p.R - tiles.kept) * p.N;
-    const int64_t stride = (int64_t)gridDim.x * kThreads;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + tid; i < n; i += stride) {
-      const int64_t r = i / p.N;
-      p.y[(tiles.kept + r) * p.ldy + (i - r * p.N)] = 0;
-    }
-  }
+  if constexpr (kExperts) zero_rows(p.y, p.ldy, tiles.kept, p.R, p.N, kThreads / 64);
   if ((int)blockIdx.x >= tiles.total) return;
 
   // ------------------------------------------------------------ the copies

@@ -71,7 +71,6 @@ __device__ inline void store4(const DecodeArgs& p, const v4f& v, const float* bv
 // (experts: one).
 template <int kWaves, int kSteps, int kGroups, bool kExperts>
 __global__ __launch_bounds__(64 * kWaves) void gemm_fp4_decode_kernel(DecodeArgs p) {
-  constexpr int kThreads = 64 * kWaves;
   __shared__ v4f red[kGroups][kWaves * 64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -85,15 +84,7 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_fp4_decode_kernel(DecodeArgs
     const int blocks = (p.N + 15) / 16;
     const int j = (int)blockIdx.x / blocks;
     n0 = ((int)blockIdx.x - j * blocks) * 16;
-    const int kept = max(p.offsets[p.E], 0);
-    {
-      // Rows of slots without an expert: zeros.
-      const int64_t n = (int64_t)(p.R - kept) * p.N, stride = (int64_t)gridDim.x * kThreads;
-      for (int64_t z = (int64_t)blockIdx.x * kThreads + tid; z < n; z += stride) {
-        const int64_t r = z / p.N;
-        p.y[(kept + r) * p.ldy + (z - r * p.N)] = 0;
-      }
-    }
+    zero_rows(p.y, p.ldy, max(p.offsets[p.E], 0), p.R, p.N, kWaves);
     int at = j, e = -1;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {

@@ -251,6 +251,24 @@ struct Piece {
 
 constexpr int kRowThreads = 256;
 
+// (token, piece) of this thread, in 32 bits where they do (a 64-bit division
+// takes some hundred instructions).
+struct Place {
+  int64_t t;
+  int piece;
+  bool in;
+};
+__device__ inline Place place(int64_t total, int pieces) {
+  const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
+  if (i >= total) return {0, 0, false};
+  if (total <= 0xFFFFFFFFll) {
+    const uint32_t t = (uint32_t)i / (uint32_t)pieces;
+    return {(int64_t)t, (int)((uint32_t)i - t * (uint32_t)pieces), true};
+  }
+  const int64_t t = i / pieces;
+  return {t, (int)(i - t * pieces), true};
+}
+
 }  // namespace
 
 template <typename El, bool kAligned, bool kPast>
@@ -260,10 +278,10 @@ __global__ __launch_bounds__(kRowThreads) void permute_kernel(const El* __restri
                                                               const int* __restrict__ kept, El* __restrict__ xs,
                                                               int64_t lds) {
   using P = Piece<El, kAligned>;
-  const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
-  if (i >= total) return;
-  const int64_t t = i / pieces;
-  const int c = (int)(i - t * pieces) * P::kN, n = H - c;
+  const Place at = place(total, pieces);
+  if (!at.in) return;
+  const int64_t t = at.t;
+  const int c = at.piece * P::kN, n = H - c;
   const int here = *kept;
   const u4 v = P::load(x + t * ldx + c, n);
   const u4 zero = {0, 0, 0, 0};
@@ -282,10 +300,10 @@ __global__ __launch_bounds__(kRowThreads) void unpermute_kernel(const El* __rest
                                                                 const float* __restrict__ weights,
                                                                 El* __restrict__ y, int64_t ldy) {
   using P = Piece<El, kAligned>;
-  const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
-  if (i >= total) return;
-  const int64_t t = i / pieces;
-  const int c = (int)(i - t * pieces) * P::kN, n = H - c;
+  const Place at = place(total, pieces);
+  if (!at.in) return;
+  const int64_t t = at.t;
+  const int c = at.piece * P::kN, n = H - c;
   const uint32_t here = (uint32_t)min(max(*kept, 0), R);
   float acc[P::kN] = {};
   for (int j0 = 0; j0 < topk; j0 += kBatch) {

@@ -64,33 +64,29 @@ int launch_quantize_packed_fp4(const void* x, int64_t M, int64_t K, int64_t ldx,
   return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 
-// Row-major: thread -> kPieces pieces of eight elements, kQuantThreads apart.
+// Row-major: a thread takes kPieces pieces of eight elements, kQuantThreads
+// apart.
 template <int kPieces>
 __global__ __launch_bounds__(kQuantThreads) void quant_rows_fp4_kernel(const uint16_t* __restrict__ x, int64_t ldx,
-                                                                       uint32_t per_row, int64_t total,
+                                                                       uint32_t per_row, uint32_t total,
                                                                        uint8_t* __restrict__ q,
                                                                        uint8_t* __restrict__ s, int pitch) {
-  const int64_t base = (int64_t)blockIdx.x * (kQuantThreads * kPieces) + threadIdx.x;
+  const uint32_t base = (uint32_t)blockIdx.x * (kQuantThreads * kPieces) + threadIdx.x;
   uint4 v[kPieces];
+  uint32_t row[kPieces], at[kPieces];
 #pragma unroll
   for (int u = 0; u < kPieces; ++u) {
-    const int64_t i = base + u * kQuantThreads;
-    v[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (i < total) {
-      const int64_t row = i / per_row;
-      v[u] = *reinterpret_cast<const uint4*>(x + row * ldx + (i - row * per_row) * 8);
-    }
+    const uint32_t i = min((uint32_t)(base + u * kQuantThreads), (uint32_t)(total - 1));
+    row[u] = i / per_row;
+    at[u] = i - row[u] * per_row;
+    v[u] = *reinterpret_cast<const uint4*>(x + (int64_t)row[u] * ldx + (int64_t)at[u] * 8);
   }
 #pragma unroll
   for (int u = 0; u < kPieces; ++u) {
-    const int64_t i = base + u * kQuantThreads;
     const Fp4Piece p = quant8(v[u]);
-    if (i < total) {
-      reinterpret_cast<uint32_t*>(q)[i] = p.codes;
-      if ((i & 3) == 0) {
-        const int64_t row = i / per_row;
-        s[row * pitch + ((i - row * per_row) >> 2)] = (uint8_t)p.scale;
-      }
+    if ((uint32_t)(base + u * kQuantThreads) < total) {
+      reinterpret_cast<uint32_t*>(q)[base + u * kQuantThreads] = p.codes;
+      if ((at[u] & 3) == 0) s[(int64_t)row[u] * pitch + (int64_t)(at[u] >> 2)] = (uint8_t)p.scale;
     }
   }
 }
@@ -100,8 +96,9 @@ int launch_quantize_rows_fp4(const void* x, int64_t M, int64_t K, int64_t ldx, v
   auto go = [&](auto kern, int pieces) {
     const int64_t n = (int64_t)kQuantThreads * pieces;
     hipLaunchKernelGGL(kern, dim3((unsigned)((total + n - 1) / n)), dim3(kQuantThreads), 0, stream, (const uint16_t*)x,
-                       ldx, (uint32_t)per_row, total, (uint8_t*)q, (uint8_t*)s, (int)fp4_scale_pitch(K));
+                       ldx, (uint32_t)per_row, (uint32_t)total, (uint8_t*)q, (uint8_t*)s, (int)fp4_scale_pitch(K));
   };
+  // (less than 2^30 pieces: the callers bound the M K / 2 bytes of codes to 32 bits)
   if (total >= (int64_t)kQuantThreads * 4 * 1024) go(quant_rows_fp4_kernel<4>, 4);
   else go(quant_rows_fp4_kernel<1>, 1);
   return hipGetLastError() == hipSuccess ? 0 : -7;
