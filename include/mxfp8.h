@@ -536,7 +536,7 @@ int mxfp8_moe_balance_backward(const void* logits, int dtype, int64_t T, int64_t
  * to +-6; a block of zeros gets byte 0.  A block with an infinity or a NaN
  * gets byte 0xFF (NaN) and makes the outputs that it enters NaN.  fp32
  * accumulation, bias (4-byte aligned) added in fp32, one rounding.  K % 256 ==
- * 0, K <= 2^24; M <= 2^30, N <= 2^24.
+ * 0, K <= 2^24; M <= 2^30, M_pad / 16 ceil(K / 512) < 2^24, N <= 2^24.
  *
  * mxfp8_packed_act_fp4_bytes: host-only sizes of the packed activations (M >=
  *   1): *q_bytes = M_pad * K / 2, *s_bytes = M_pad * K / 32, M_pad =
@@ -599,8 +599,9 @@ int mxfp8_debug_force_w4a4(int form);
  *   dweights may be NULL, and ys where dweights is.
  * Matrices: x, y, dy, [T, H] and xs, ys, dys [T topk, H], fp32 or bf16 (dtype),
  *   any row strides >= H, aligned to their elements (rows on 16 bytes are
- *   faster), 1 <= H <= 2^24.  kept: offsets + E of the sort, on the device.
- *   weights, dweights fp32 [T, topk].
+ *   faster), 1 <= H <= 2^24, [T, H] less than 2^32 - 256 pieces of 16 bytes.
+ *   kept: offsets + E of the sort, on the device.  weights, dweights fp32 [T,
+ *   topk].
  */
 int mxfp8_moe_sort_workspace_bytes(int64_t slots, int64_t E, size_t* bytes);
 int mxfp8_moe_sort(const void* ids, int id_bytes, int64_t slots, int64_t E, int32_t* row_of_slot,

@@ -993,6 +993,8 @@ class PackedActivationFP4(PackedActivation):
     def unpack(self):
         """(E2M1 ``[M_pad, K/2]``, two codes per byte, UE8M0 ``[M_pad, K/32]``)
         as uint8 tensors."""
+        if self.M == 0:
+            return self.q_packed.view(0, self.K // 2), self.s_packed.view(0, self.K // 32)
         with _on(self.device):
             return PreparedWeightFP4(self.q_packed, self.s_packed, self.M, self.K).unpack()
 
@@ -1019,7 +1021,7 @@ def linear_w4a4(x, pw, bias=None, out=None):
     deq4(W).T + bias)``, x bf16 ``[..., K]`` quantized to MXFP4 on the fly, pw
     a PreparedWeightFP4 (the weight ``linear`` multiplies with 8-bit
     activations), bias bf16 ``[N]`` or None.  Returns bf16 ``[..., N]``; ``out``:
-    bf16 ``[M, N]`` to write into, M the rows of x."""
+    bf16 ``[M, N]`` to write into, M the rows of x.  No gradients."""
     if not isinstance(pw, PreparedWeightFP4):
         raise ValueError("linear_w4a4 takes an MXFP4 weight (prepare_weight_fp4)")
     x2 = _rows(x, "x")

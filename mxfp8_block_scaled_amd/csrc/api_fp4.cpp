@@ -24,9 +24,10 @@ int64_t pad128(int64_t n) { return (n + 127) / 128 * 128; }
 
 size_t act_bytes(int64_t M, int64_t K) { return (size_t)pad128(M) * (size_t)(K / 2); }
 size_t act_scale_bytes(int64_t M, int64_t K) { return (size_t)pad128(M) * (size_t)(K / 32); }
-// The quantizer's grid: a workgroup per 16 rows and 128-K step at most; the
-// tile GEMM's list in 32-bit range.
-bool act_grid_ok(int64_t M, int64_t K) { return pad128(M) / 16 * (K / 128) <= INT32_MAX; }
+// A launch has fewer than 2^32 threads: the quantizer's (256 per 16 rows and
+// four 128-K steps), and the tile GEMM's list in 32-bit range.
+constexpr int64_t kMaxThreads = UINT32_MAX;
+bool act_grid_ok(int64_t M, int64_t K) { return pad128(M) / 16 * ((K + 511) / 512) * 256 <= kMaxThreads; }
 bool gemm_grid_ok(int64_t M, int64_t N) { return (M + 63) / 64 * ((N + 127) / 128) <= INT32_MAX / 2; }
 
 // Test hook: pinned form (0: by shape).
@@ -145,7 +146,7 @@ int check_matrix(const void* p, int64_t H, int64_t ld, int size) {
 int check_rows(int dtype, int64_t T, int64_t H, int64_t topk) {
   if ((dtype != MXFP8_F32 && dtype != MXFP8_BF16) || !slots_ok(T, topk) || H < 1 || H > kMaxK) return MXFP8_E_SHAPE;
   const int64_t per = dtype == MXFP8_BF16 ? 8 : 4;
-  return T * ((H + per - 1) / per) / 256 < INT32_MAX ? MXFP8_OK : MXFP8_E_SHAPE;
+  return T * ((H + per - 1) / per) <= kMaxThreads - 255 ? MXFP8_OK : MXFP8_E_SHAPE;
 }
 
 struct ExpertsForm {
@@ -165,10 +166,10 @@ struct ExpertsForm {
 //   256                         140    124    114                       98    89    84
 ExpertsForm experts_form(int64_t R, int64_t N, int64_t K, int64_t E) {
   const int force = g_force.load(std::memory_order_relaxed);
-  const bool can = K <= mxfp8::kFp4DecodeMaxK;
   const double X = (double)std::max<int64_t>(1, std::min(E, R)), rows = (double)R / X;
   const double work = 1e-6 * X * (double)N * (double)K;
-  const bool can_decode = K <= mxfp8::kFp4DecodeMaxK, can_fuse = K <= mxfp8::kFp4FusedMaxK;
+  const bool can_decode = K <= mxfp8::kFp4DecodeMaxK && std::min(E, R) * ((N + 15) / 16) * 1024 <= kMaxThreads,
+             can_fuse = K <= mxfp8::kFp4FusedMaxK;
   if (force == 1 && can_decode) return {kDecode, {}};
   if (force == 2 && can_fuse) return {kFusedTiles, {}};
   if (force == 0) {
@@ -191,7 +192,7 @@ ExpertsForm experts_form(int64_t R, int64_t N, int64_t K, int64_t E) {
 bool experts_shape_ok(int64_t x_rows, int64_t R, int64_t N, int64_t K, int64_t E) {
   return x_rows >= 0 && R >= 0 && R <= kMaxSlots && x_rows <= R && N >= 1 && N <= kMaxN && summed_ok(K) &&
          experts_ok(E) && x_rows * (K / 2) < ((int64_t)1 << 32) &&
-         (R / 64 + std::min(E, R)) * ((N + 127) / 128) <= INT32_MAX / 2 && std::min(E, R) * ((N + 15) / 16) <= INT32_MAX;
+         (R / 64 + std::min(E, R)) * ((N + 127) / 128) <= INT32_MAX / 2;
 }
 size_t experts_q_bytes(int64_t x_rows, int64_t K) { return round_up((size_t)x_rows * (size_t)(K / 2), 256); }
 size_t experts_ws(int64_t x_rows, int64_t R, int64_t N, int64_t K, int64_t E) {
@@ -404,8 +405,10 @@ int mxfp8_moe_prepare_experts_fp4(const void* w_e2m1, const void* w_s_e8m0, int6
   if (!w_e2m1 || !w_s_e8m0) return MXFP8_E_NULLPTR;
   if (!aligned(w_e2m1, 16)) return MXFP8_E_ALIGN;
   // (the pack kernels' grids: one thread per 16 bytes, one per scale pair)
-  const int64_t rows = N % 128 == 0 ? E * N : N, passes = N % 128 == 0 ? 1 : E;
-  if (pad128(rows) * (K / 64) > (int64_t)INT32_MAX * 256) return MXFP8_E_SHAPE;
+  const int64_t per_row = K / 32;
+  const bool at_once = N % 128 == 0 && E * N * per_row <= kMaxThreads - 255;
+  const int64_t rows = at_once ? E * N : N, passes = at_once ? 1 : E;
+  if (pad128(rows) * per_row > kMaxThreads - 255) return MXFP8_E_SHAPE;
   if (int st = mxfp8::check_device_current()) return st;
   for (int64_t e = 0; e < passes; ++e) {
     const size_t w = (size_t)e * N * (K / 2), s = (size_t)e * N * (K / 32);

@@ -251,28 +251,22 @@ struct Piece {
 
 constexpr int kRowThreads = 256;
 
-// (token, piece) of this thread, in 32 bits where they do (a 64-bit division
-// takes some hundred instructions).
+// (token, piece) of this thread: T pieces fit 32 bits (a 64-bit division takes
+// some hundred instructions).
 struct Place {
   int64_t t;
   int piece;
   bool in;
 };
-__device__ inline Place place(int64_t total, int pieces) {
-  const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
-  if (i >= total) return {0, 0, false};
-  if (total <= 0xFFFFFFFFll) {
-    const uint32_t t = (uint32_t)i / (uint32_t)pieces;
-    return {(int64_t)t, (int)((uint32_t)i - t * (uint32_t)pieces), true};
-  }
-  const int64_t t = i / pieces;
-  return {t, (int)(i - t * pieces), true};
+__device__ inline Place place(uint32_t total, int pieces) {
+  const uint32_t i = blockIdx.x * (uint32_t)kRowThreads + threadIdx.x, t = i / (uint32_t)pieces;
+  return {(int64_t)t, (int)(i - t * pieces), i < total};
 }
 
 }  // namespace
 
 template <typename El, bool kAligned, bool kPast>
-__global__ __launch_bounds__(kRowThreads) void permute_kernel(const El* __restrict__ x, int64_t ldx, int64_t total,
+__global__ __launch_bounds__(kRowThreads) void permute_kernel(const El* __restrict__ x, int64_t ldx, uint32_t total,
                                                               int H, int pieces, int topk, int R,
                                                               const int* __restrict__ rows,
                                                               const int* __restrict__ kept, El* __restrict__ xs,
@@ -293,7 +287,7 @@ __global__ __launch_bounds__(kRowThreads) void permute_kernel(const El* __restri
 
 // kBatch: rows in flight.
 template <typename El, bool kAligned, bool kPast, int kBatch>
-__global__ __launch_bounds__(kRowThreads) void unpermute_kernel(const El* __restrict__ ys, int64_t lds, int64_t total,
+__global__ __launch_bounds__(kRowThreads) void unpermute_kernel(const El* __restrict__ ys, int64_t lds, uint32_t total,
                                                                 int H, int pieces, int topk, int R,
                                                                 const int* __restrict__ rows,
                                                                 const int* __restrict__ kept,
@@ -432,10 +426,10 @@ void by_type(const PermuteArgs& a, bool aligned, Go&& go) {
 int launch_moe_permute(const PermuteArgs& a, hipStream_t stream) {
   const int size = a.bf16 ? 2 : 4;
   const int pieces = (int)((a.H + 16 / size - 1) / (16 / size));
-  const int64_t total = a.T * pieces;
+  const uint32_t total = (uint32_t)(a.T * pieces);
   by_type(a, rows16(a.tokens, a.ldt, size) && rows16(a.out_sorted, a.ldo, size), [&](auto el, auto al, auto past) {
     using El = decltype(el);
-    hipLaunchKernelGGL((permute_kernel<El, decltype(al)::value, decltype(past)::value>), dim3((unsigned)((total + kRowThreads - 1) / kRowThreads)),
+    hipLaunchKernelGGL((permute_kernel<El, decltype(al)::value, decltype(past)::value>), dim3((total + kRowThreads - 1) / kRowThreads),
                        dim3(kRowThreads), 0, stream, (const El*)a.tokens, a.ldt, total, (int)a.H, pieces, (int)a.topk,
                        (int)(a.T * a.topk), a.rows, a.kept, (El*)a.out_sorted, a.ldo);
   });
@@ -445,11 +439,11 @@ int launch_moe_permute(const PermuteArgs& a, hipStream_t stream) {
 int launch_moe_unpermute(const PermuteArgs& a, hipStream_t stream) {
   const int size = a.bf16 ? 2 : 4;
   const int pieces = (int)((a.H + 16 / size - 1) / (16 / size));
-  const int64_t total = a.T * pieces;
+  const uint32_t total = (uint32_t)(a.T * pieces);
   by_type(a, rows16(a.sorted, a.lds, size) && rows16(a.out_tokens, a.ldo, size), [&](auto el, auto al, auto past) {
     using El = decltype(el);
     auto go = [&](auto kern) {
-      hipLaunchKernelGGL(kern, dim3((unsigned)((total + kRowThreads - 1) / kRowThreads)), dim3(kRowThreads), 0, stream,
+      hipLaunchKernelGGL(kern, dim3((total + kRowThreads - 1) / kRowThreads), dim3(kRowThreads), 0, stream,
                          (const El*)a.sorted, a.lds, total, (int)a.H, pieces, (int)a.topk, (int)(a.T * a.topk), a.rows,
                          a.kept, a.weights, (El*)a.out_tokens, a.ldo);
     };

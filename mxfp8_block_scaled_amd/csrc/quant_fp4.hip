@@ -59,7 +59,7 @@ int launch_quantize_packed_fp4(const void* x, int64_t M, int64_t K, int64_t ldx,
                        (int)M, KS4, chunks, (uint8_t*)qp, (uint8_t*)sp);
   };
   // Four steps per workgroup where that still gives the chip over a thousand.
-  if (bands * (KS4 / 4) >= 1024) go(quant_packed_fp4_kernel<4>, 4);
+  if (bands * ((KS4 + 3) / 4) >= 1024) go(quant_packed_fp4_kernel<4>, 4);
   else go(quant_packed_fp4_kernel<1>, 1);
   return hipGetLastError() == hipSuccess ? 0 : -7;
 }

@@ -107,3 +107,15 @@ def test_python_refusals():
         api.moe_linear_w4a4(torch.zeros(4, 256, dtype=torch.bfloat16), object(), order)
     with pytest.raises(ValueError):
         api.quantize_act_packed_fp4(torch.zeros(4, 256))
+
+
+def test_launches_of_more_than_32_bits():
+    """Refused, not wrapped: a launch has fewer than 2^32 threads."""
+    lib = api.lib()
+    assert lib.mxfp8_moe_permute(P, 1, 1 << 24, 2048, 2048, 1, P, P, P, 2048, None) == SHAPE
+    assert lib.mxfp8_moe_unpermute(P, 1, 1 << 24, 2048, 2048, 1, P, P, None, P, 2048, None) == SHAPE
+    assert lib.mxfp8_quantize_act_packed_fp4(P, 1 << 28, 512, 512, P, P, None) == SHAPE
+    assert lib.mxfp8_moe_prepare_experts_fp4(P, P, 1, 1 << 24, 8192, P, P, None) == SHAPE
+    # one below each: past the shape checks
+    assert lib.mxfp8_moe_permute(None, 1, (1 << 24) - 1, 2048, 2048, 1, P, P, P, 2048, None) == NULLPTR
+    assert lib.mxfp8_quantize_act_packed_fp4(None, (1 << 28) - 128, 512, 512, P, P, None) == NULLPTR
