@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 
 #include "launch_fp4.hpp"
@@ -34,42 +35,54 @@ bool gemm_grid_ok(int64_t M, int64_t N) { return (M + 63) / 64 * ((N + 127) / 12
 std::atomic<int> g_force{0};
 
 // The forms with the least estimated time: lines through measurements on
-// MI355X (us, calls in a captured graph, the quantizer's launch included).  For
-// example (form 1: decode; 16: 16 weight rows on packed activations; 64, 128,
-// 256: tiles), N x K = 4096 x 4096:
-//   M = 1      4.8    7.2   13.4
-//   M = 32    11.4    7.4   13.8   16.1
-//   M = 128           11.5  13.6   16.3   31
-//   M = 1000                19.9   20.1   33.7
-//   M = 2048                33     27     37
-//   M = 4096                63     49     47
+// MI355X (us, calls in a captured graph, the quantizer's launch included), K in
+// thousands (1024).  For example (decode; 16 weight rows on packed activations;
+// 128 x 64 tiles that quantize their rows; tiles of 128 x 64, 128 x 128, 256 x
+// 256), N x K = 4096 x 1024:
+//   M = 1      4.6    8.1    6.4    9.2
+//   M = 32     8.2    8.1    8.4    9.3   10.3
+//   M = 128           8.5    9.8    9.6   10.6
+//   M = 1000                14.8   11.9   12.1   18.3
+//   M = 4096                       26.1   21.9   22.6
+// 4096 x 4096:
+//   M = 1      5.9    8.2          12.8
+//   M = 32    12.0    8.4          13.0   15.4
+//   M = 128          12.1          13.2   15.6
+//   M = 1000                       21.0   20.0   34.5
+//   M = 4096                       60.6   48.1   45.6
 // and 16384 x 8192:
-//   M = 32            24.7  20.9   24.8
-//   M = 2048               219    162    136
+//   M = 32           24.8          19.0   22.8
+//   M = 2048                        190    143    129
+double thousands(int64_t K) { return (double)K / 1024.0; }
 double turns(int64_t N) { return std::max(1.0, (double)N / 4096.0); }   // of one workgroup per compute unit, 16 rows each
 double decode_us(int64_t M, int64_t N, int64_t K) {
-  return 3.0 + (double)K * turns(N) * (4.0e-4 + 4.5e-5 * (double)M + (M > 16 ? 3.0e-4 : 0.0));
+  const double t = turns(N), k = t * thousands(K);
+  return 4.2 + 0.1 * (t - 1.0) + k * (0.42 + 0.04 * (double)M + (M > 16 ? 0.52 : 0.0));
 }
 double mid_us(int64_t M, int64_t N, int64_t K) {
-  const double k = (double)K;
-  return 4.0 + turns(N) * (M <= 32 ? 2.6 + 3.0e-4 * k : M <= 64 ? 3.5 + 5.0e-4 * k : 2.6 + 1.15e-3 * k);
+  const double k = thousands(K), t = std::ceil((double)N / 4096.0);
+  if (M <= 32) return 5.4 + t * std::max(2.6, 0.84 + 0.54 * k);
+  if (M <= 64) return 5.1 + t * std::max(4.0, 1.4 + 0.77 * k);
+  return 5.2 + t * std::max(3.1, 1.8 + 1.29 * k);
 }
 double tile_us(int nt, int mt, int64_t M, int64_t N, int64_t K) {
-  const double k = (double)K;
-  const int64_t tiles = (M + mt - 1) / mt * ((N + nt - 1) / nt);
-  const double more = std::max(0.0, (double)tiles / 256.0 - 1.0);      // rounds of the chip behind the first
-  const bool full = tiles > 128;
+  const double k = thousands(K), q = k * (double)M / 1024.0;   // q: the quantizer's share
+  const double r = (double)((M + mt - 1) / mt * ((N + nt - 1) / nt)) / 256.0;   // rounds of the chip
   if (nt == 256)
-    return 11.0 + 5.0e-3 * k + (full ? 3.5 + 1.8e-3 * k : 0.0) + (double)((tiles + 255) / 256 - 1) * (5.0 + 7.3e-3 * k);
-  if (mt == 128) return 7.7 + 2.0e-3 * k + (full ? 0.6 + 8.0e-4 * k : 0.0) + more * (0.6 + 2.1e-3 * k);
-  return 7.1 + 1.6e-3 * k + more * (0.4 + 1.45e-3 * k);
+    return r <= 1.0 ? 13.2 + 4.4 * k + r * (1.3 + 2.6 * k) + 0.33 * q
+                    : 6.5 - 0.07 * k + std::ceil(r) * (7.7 + 6.35 * k) + 0.47 * q;
+  if (mt == 128)
+    return r <= 1.0 ? 8.9 + 1.53 * k + r * (0.9 + 0.4 * k) + 0.44 * q
+                    : 8.3 + 0.45 * k + r * (1.3 + 1.93 * k) + 0.36 * q;
+  return r <= 1.0 ? 8.2 + 1.12 * k + r * (0.36 + 0.35 * k) + 0.41 * q : 7.9 + 0.12 * k + r * (0.85 + 1.32 * k) + 0.36 * q;
 }
-
+// (Past one round and K 1024 their LDS holds one workgroup per compute unit:
+// more than twice the time of two launches.)
+bool can_fuse(int64_t tiles, int64_t K) { return K <= mxfp8::kFp4FusedMaxK && (K <= 1024 || tiles <= 256); }
 double fused_us(int64_t M, int64_t N, int64_t K) {
-  const double k = (double)K;
-  const int64_t tiles = (M + 63) / 64 * ((N + 127) / 128);
-  return 4.6 + (1.3e-3 + 8.0e-5 * (double)std::min<int64_t>(64, M)) * k +
-         std::max(0.0, (double)tiles / 256.0 - 1.0) * (1.2 + 2.7e-3 * k);
+  const double k = thousands(K), r = (double)((M + 63) / 64 * ((N + 127) / 128)) / 256.0;
+  return r <= 1.0 ? 5.8 + k * (1.5 + 0.037 * (double)std::min<int64_t>(64, M)) + r * (0.7 + 0.25 * k)
+                  : 5.9 + r * (1.2 + 3.75 * k);
 }
 
 // The GEMM on packed activations: nt == 16 is the 16-row form.
@@ -101,7 +114,8 @@ int one_launch(int64_t M, int64_t N, int64_t K) {
   double us = 0.0;
   tile_plan(M, N, K, &us);
   us += 1.0;   // (outside of a captured graph a second launch costs the host about 5 us)
-  const double td = decode ? decode_us(M, N, K) : 1e30, tf = fused ? fused_us(M, N, K) : 1e30;
+  const double td = decode ? decode_us(M, N, K) : 1e30;
+  const double tf = can_fuse((M + 63) / 64 * ((N + 127) / 128), K) ? fused_us(M, N, K) : 1e30;
   if (td <= std::min(tf, us)) return kDecode;
   return tf <= us ? kFusedTiles : kTwoLaunches;
 }
@@ -169,15 +183,17 @@ ExpertsForm experts_form(int64_t R, int64_t N, int64_t K, int64_t E) {
   const double X = (double)std::max<int64_t>(1, std::min(E, R)), rows = (double)R / X;
   const double work = 1e-6 * X * (double)N * (double)K;
   const bool can_decode = K <= mxfp8::kFp4DecodeMaxK && std::min(E, R) * ((N + 15) / 16) * 1024 <= kMaxThreads,
-             can_fuse = K <= mxfp8::kFp4FusedMaxK;
+             fused = K <= mxfp8::kFp4FusedMaxK;
   if (force == 1 && can_decode) return {kDecode, {}};
-  if (force == 2 && can_fuse) return {kFusedTiles, {}};
+  if (force == 2 && fused) return {kFusedTiles, {}};
   if (force == 0) {
-    const double k = (double)K, tiles = X * (double)((N + 127) / 128);
-    const double two = 8.1 + 2.0e-3 * k + 0.05 * work;
+    const double k = thousands(K);
+    const int64_t cols = (N + 127) / 128, most = (R / 64 + std::min(E, R)) * cols;   // (row tiles: one per expert is partial)
+    const double two = 8.1 + 2.05 * k + 0.05 * work;
     const double td = can_decode && rows <= 8.0 ? 4.0 + 0.15 * work * (1.0 + rows / 4.0) : 1e30;
-    const double tf = can_fuse && (K <= 1024 || tiles <= 256.0)
-                          ? 4.6 + 2.7e-3 * k + work * (0.045 + 8.0e-3 * rows) : 1e30;
+    const double tf = !can_fuse(std::min(E, R) * cols, K) ? 1e30
+                      : most <= 256                       ? 6.3 + k * (2.0 + 0.037 * std::min(64.0, rows))
+                                                          : 4.6 + 2.76 * k + work * (0.045 + 8.0e-3 * rows);
     if (td <= std::min(tf, two)) return {kDecode, {}};
     if (tf <= two) return {kFusedTiles, {}};
   }

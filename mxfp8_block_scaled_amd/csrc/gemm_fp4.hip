@@ -9,15 +9,22 @@
 //    x 2, each 16 NA x 16 NB: NA x NB v_mfma_scale_f32_16x16x128 per 128-K
 //    step, the weight as the A operand; lane (i, g) ends with acc[a][b][j] =
 //    D[n = wn 16 NA + 16a + 4g + j][m = wm 16 NB + 16b + i].
-//  * A step's operands are copied straight into one of kRing (four or eight)
-//    LDS slots (buffer_load ... lds); the slot's fragments are read into
-//    registers one step ahead, while the MFMAs of the step before run, and the
-//    slot is refilled right after: early in step s the copies of s + 1 have
-//    landed, those of s + 2 .. s + kRing - 1 are in flight and those of s +
-//    kRing go out between its MFMAs.  One barrier per step.
-//  * Persistent: a workgroup runs tiles b, b + gridDim.x, ...  The copy stream
-//    has its own position ("cursor"), kRing steps ahead, and runs on into the
-//    next tiles while a tile ends and is stored.
+//  * A step's operands are copied straight into one of four LDS slots
+//    (buffer_load ... lds); the slot's fragments are read into registers one step
+//    ahead, while the MFMAs of the step before run, and the slot is refilled
+//    right after: early in step s the copies of s + 1 have landed, those of s + 2
+//    and s + 3 are in flight and those of s + 4 go out between its MFMAs.  One
+//    barrier per step.
+//  * Where a round of the chip holds all tiles, a workgroup has one, and two
+//    groups of four waves: each group runs every other pair of steps on slots of
+//    its own, so that a SIMD has a second wave to run while one waits for its
+//    reads, and the two add their sums through LDS at the end.  (1000 x 4096 x
+//    4096, the GEMM alone: 14.3 us, with one group 15.5; 2048 x 2048 x 8192 23.2
+//    and 26.4.  A step takes 0.26 us then: its copies alone 0.18, its MFMAs 0.16,
+//    its reads 0.11.)
+//  * Persistent beyond that: a workgroup runs tiles b, b + gridDim.x, ...  The
+//    copy stream has its own position ("cursor"), four steps ahead, and runs on
+//    into the next tiles while a tile ends and is stored.
 //  * Scales: the packed operands' scale tiles of a pair of steps (256 K) are
 //    1 KiB per 128-row group: one copy per pair.  Of rows by index (kRows) a
 //    copy touches one cache line per row, so it brings four steps' bytes of each
@@ -34,7 +41,8 @@ namespace {
 using tile::buffer_rsrc;
 using tile::i4v;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;   // of a group of waves
+constexpr int kRing = 4;        // steps in LDS
 
 // tile::b2l_16 and b2l_4 with the LDS address as a base and a constant: one
 // scalar add into m0.
@@ -56,7 +64,7 @@ using tile::lds_addr;
 // quantized ones; or bf16 rows, quantized by the workgroup itself.
 constexpr int kPacked = 0, kRows = 1, kFused = 2;
 
-template <int NA, int NB, int kX, int kRing>
+template <int NA, int NB, int kX, int kGroups>
 struct Fp4Lds {
   static constexpr int kRowsN = 32 * NA, kRowsM = 32 * NB;
   static constexpr int kW = kRowsN * 64;
@@ -70,12 +78,13 @@ struct Fp4Lds {
   static constexpr int kEpiWave = kEpiRows * kPitch;
   static constexpr int kBiasSlot = 512;                    // a tile's bias, 256 bytes per wave column
   static constexpr int kScaleAt = kRing * kSlot;
+  static constexpr int kGroup = kScaleAt + kRing / 2 * kScale;   // one wave group's slots and scales
   // Scales of gathered rows: one copy brings 16 bytes (four steps) of 64 / kEntry
   // times a wave's kEntry rows, kChunk steps; two chunks.
   static constexpr int kEntry = 8 * NB, kChunk = 32 / NB;
-  static constexpr int kXsAt = kScaleAt + kRing / 2 * kScale;
+  static constexpr int kXsAt = kGroups * kGroup;
   static constexpr int kEpiAt = kXsAt + (kX == kRows ? 2 * 4096 : 0);
-  static constexpr int kBiasAt = kEpiAt + 4 * kEpiWave;
+  static constexpr int kBiasAt = kEpiAt + kGroups * 4 * kEpiWave;
   static constexpr int kIndexAt = kBiasAt;                 // kRows: row indices instead of a bias
   static constexpr int kJobAt = kBiasAt + (kX == kRows ? 1024 : kRing * kBiasSlot);
   static constexpr int kBytes = kJobAt + 8 * 32;           // (the cursor is at most five tiles ahead)
@@ -99,7 +108,7 @@ struct Fp4Args {
   const uint16_t* bias;
   uint16_t* y;
   int64_t ldy;
-  int vec;                 // y 16-byte aligned, ldy % 8 == 0
+  int past;                // y is stored around the caches
   // experts
   int R, E, topk;
   const int* slots;        // or null: row r of q
@@ -207,16 +216,17 @@ struct ExpertTiles {
 
 }  // namespace
 
-template <int NA, int NB, int kX, bool kExperts, int kRing>
-__global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kX, kRing>::kBytes > 80 * 1024 ? 1 : 2)) void gemm_fp4_kernel(
-    Fp4Args p) {
-  using L = Fp4Lds<NA, NB, kX, kRing>;
+template <int NA, int NB, int kX, bool kExperts, int kGroups>
+__global__ __launch_bounds__(kThreads * kGroups, (kGroups == 2 || Fp4Lds<NA, NB, kX, kGroups>::kBytes > 80 * 1024
+                                                      ? 1 : 2)) void gemm_fp4_kernel(Fp4Args p) {
+  using L = Fp4Lds<NA, NB, kX, kGroups>;
   constexpr bool kOwnScales = kX != kPacked;   // a lane's scale in a byte of its own
   using Tiles = typename std::conditional<kExperts, ExpertTiles<NA, NB>, DenseTiles<NA, NB>>::type;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
 
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int group = kGroups == 1 ? 0 : __builtin_amdgcn_readfirstlane(tid >> 8);
+  const int wave = __builtin_amdgcn_readfirstlane((tid >> 6) & 3);   // in its group
   const int wn = wave >> 1, wm = wave & 1;
   const int li = lane & 15, lg = lane >> 4;
   const int KS4 = p.K / 128;                                  // 128-K steps: even, at least 2
@@ -225,17 +235,18 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kX, kRing>::kBytes > 80 *
   const uint32_t gbytes = (uint32_t)KS4 * kTileBytes, sbytes = (uint32_t)KS4 * 2 * kTileScaleBytes;
   const Tiles tiles(p);
 
-  if constexpr (kExperts) zero_rows(p.y, p.ldy, tiles.kept, p.R, p.N, kThreads / 64);
+  if constexpr (kExperts) zero_rows(p.y, p.ldy, tiles.kept, p.R, p.N, kGroups * kThreads / 64);
   if ((int)blockIdx.x >= tiles.total) return;
 
   // ------------------------------------------------------------ the copies
   // The cursor: step cq of this workgroup's tile ctile; sources of its tile.  Past the last
   // tile the sources are empty: the copies bring zeros, without touching
   // memory, and every wait counts the same.
-  int cq = 0, ctile = 0;
+  int cq = 2 * group, ctile = 0;
   i4v w0, w1, x0, x1, sc, xsr;
   uint32_t vx[NB / 2], vxhi = 0, vxs = 0;
-  const uint32_t lds0 = lds_addr(smem) + (uint32_t)wave * 1024u;   // this wave's share of a region
+  uint8_t* const ring = smem + group * L::kGroup;
+  const uint32_t lds0 = lds_addr(ring) + (uint32_t)wave * 1024u;   // this wave's share of a region
   const uint32_t lo16 = (uint32_t)lane * 16u;
   const uint32_t band = (uint32_t)KS4 * kPieceBytes;          // bytes of a 16-row band
   auto bias_slot = [&](int t) { return smem + L::kBiasAt + (t & (kRing - 1)) * L::kBiasSlot; };
@@ -305,7 +316,7 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kX, kRing>::kBytes > 80 *
     }
     sc = buffer_rsrc(srun, live * sbytes);
     if constexpr (!kExperts) {
-      if (p.bias != nullptr && wm == 0) {
+      if (p.bias != nullptr && wm == 0 && group == 0) {
         // this wave column's 16 NA bias values, by whole words (an odd N's last
         // word holds one value that is not the bias's and reaches no output)
         const int c = j.col0 + wn * 16 * NA;
@@ -463,20 +474,27 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kX, kRing>::kBytes > 80 *
   using F = std::false_type;
 
   // ------------------------------------------------------------ start
-  auto slot = [&](int s) { return smem + s * L::kSlot; };
+  auto slot = [&](int s) { return ring + s * L::kSlot; };
   auto fill = [&](int s) { return lds0 + (uint32_t)(s * L::kSlot); };
   // Scales of gathered rows for step q of a tile, in the chunk buffer in use.
   int xget = 0;
   auto xs_at = [&](int q) -> const uint8_t* {
     if constexpr (kX == kPacked) return nullptr;
-    if constexpr (kX == kFused) return smem + q * L::kFusedStep;
+    if constexpr (kX == kFused) return smem + (kGroups == 1 ? q : min(q, KS4 - 1)) * L::kFusedStep;
     return smem + L::kXsAt + xget * 4096 + q % L::kChunk / 4 * (L::kEntry * 16) + (q & 3) * 4;
   };
-  auto scale_slot = [&](int pair) { return smem + L::kScaleAt + pair * L::kScale; };
+  auto scale_slot = [&](int pair) { return ring + L::kScaleAt + pair * L::kScale; };
   // Moves the cursor over a pair of steps.
+  auto stop_copies = [&]() {
+    w0[2] = 0;
+    if constexpr (kX == kPacked) x0[2] = 0;
+    sc[2] = 0;
+  };
   auto move_cursor = [&]() {
-    cq += 2;
-    if (cq == KS4) {
+    cq += 2 * kGroups;
+    if constexpr (kGroups == 2) {
+      if (cq >= KS4) stop_copies();
+    } else if (cq == KS4) {
       cq = 0;
       ++ctile;
       if constexpr (kX == kRows) {
@@ -490,6 +508,7 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kX, kRing>::kBytes > 80 *
   fetch_index(put_job(0));
   if constexpr (kX == kRows) tile::wait_vmcnt<0>();
   advance_tile();
+  if (kGroups == 2 && cq >= KS4) stop_copies();
   for (int pair = 0; pair < kRing / 2; ++pair) {
     issue_all_scales(cq, pair);
     tile::static_for<0, L::kCopies>([&](auto C) { issue(C, cq, fill(2 * pair)); });
@@ -506,17 +525,17 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kX, kRing>::kBytes > 80 *
   };
   Fp4Job cur = get_job(0);
   tile_shift(cur);
-  tile::static_for<0, kReads>([&](auto R) { read_part(decltype(R)::value, f0, slot(0), scale_slot(0), xs_at(0)); });
+  tile::static_for<0, kReads>([&](auto R) { read_part(decltype(R)::value, f0, slot(0), scale_slot(0), xs_at(2 * group)); });
 
   // kFused: the tile's rows into LDS, sixteen lanes per row and step, as in the
   // packed quantizer; rows past the last keep what was there (their outputs are
-  // not stored).  One wave per SIMD: bound by its chain of instructions (64
-  // rows of 1024: 5 us), not by the loads (all rows' in flight: slower).
+  // not stored).  Bound by each wave's chain of instructions (64 rows of 1024: 3
+  // us, with one group of waves 5), not by the loads (all rows' in flight: slower).
   auto quantize_rows = [&](const Fp4Job& j) {
     constexpr int kBatch = 4;
     const int l = tid & 15, n = j.row_end - j.row0;
 #pragma unroll
-    for (int r0 = 0; r0 < L::kRowsM; r0 += 16) {
+    for (int r0 = 0; r0 < L::kRowsM; r0 += 16 * kGroups) {
       if (r0 >= n) break;
       const int r = r0 + (tid >> 4);
       const bool in = r < n;
@@ -552,10 +571,10 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kX, kRing>::kBytes > 80 *
       quantize_rows(cur);
       tile::static_for<0, kReads>([&](auto R) {
         constexpr int r = decltype(R)::value;
-        if constexpr ((r >= 2 && r < 2 + NB) || r >= 2 + NB + NA) read_part(r, f0, nullptr, nullptr, xs_at(0));
+        if constexpr ((r >= 2 && r < 2 + NB) || r >= 2 + NB + NA) read_part(r, f0, nullptr, nullptr, xs_at(2 * group));
       });
     }
-    if (!kExperts && p.bias != nullptr) {
+    if (!kExperts && p.bias != nullptr && group == 0) {
       const uint8_t* bs = bias_slot(t) + wn * 256;
 #pragma unroll
       for (int a = 0; a < NA; ++a) {
@@ -575,12 +594,14 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kX, kRing>::kBytes > 80 *
 #pragma unroll
       for (int c = 0; c < NB; ++c) asm volatile("" : "+a"(acc[a][c]));
     const Fp4Job nxt = get_job(t + 1);
-    for (int q = 0; q < KS4; q += 2) {
+    // (an odd number of pairs: the second group's last one is zeros)
+    const int KSe = kGroups == 1 ? KS4 : (KS4 + 3) / 4 * 4;
+    for (int q = 2 * group; q < KSe; q += 2 * kGroups) {
       const int npair = (pair + 1) & (kRing / 2 - 1);
       step(F{}, f0, f1, fill(2 * pair), slot(2 * pair + 1), pair, scale_slot(pair) + 2 * kTileScaleBytes,
            xs_at(q + 1), cq);
       // (the last step of a tile reads the next tile's first fragments)
-      const int qn = q + 2 == KS4 ? 0 : q + 2;
+      const int qn = kGroups == 2 ? q + 4 : q + 2 == KS4 ? 0 : q + 2;
       if (qn == 0) tile_shift(nxt);
       if (kX == kRows && qn % L::kChunk == 0) xget ^= 1;
       step(T{}, f1, f0, fill(2 * pair + 1), slot(2 * npair), pair, scale_slot(npair), xs_at(qn), cq + 1);
@@ -590,6 +611,28 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kX, kRing>::kBytes > 80 *
     // The last MFMAs must retire before the accumulators are read.
     asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15" ::: "memory");
 
+    if constexpr (kGroups == 2) {
+      // The two groups' sums: each takes half of the columns, k = NB / 2 group ..,
+      // and gets the other's part of them through LDS, in the place of the slots.
+      tile::wait_vmcnt<0>();
+      __syncthreads();
+      constexpr int kH = NB / 2;
+      static_assert(2 * 4 * NA * kH * 1024 <= 2 * L::kGroup, "the exchanged sums");
+      v4f* const out = reinterpret_cast<v4f*>(smem) + ((group * 4 + wave) * NA * kH) * 64 + lane;
+      const v4f* const in = reinterpret_cast<const v4f*>(smem) + (((1 - group) * 4 + wave) * NA * kH) * 64 + lane;
+#pragma unroll
+      for (int k = 0; k < NB; ++k)
+        if (k / kH != group)
+#pragma unroll
+          for (int a = 0; a < NA; ++a) out[(a * kH + k % kH) * 64] = acc[a][k];
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < NB; ++k)
+        if (k / kH == group)
+#pragma unroll
+          for (int a = 0; a < NA; ++a) acc[a][k] += in[(a * kH + k % kH) * 64];
+    }
+
     // ---------------------------------------------------------- epilogue
     // The wave stages kEpiRows rows at a time as bf16 (16-byte chunk c of row r at c ^
     // r % 8, against bank conflicts) and stores 16-byte pieces of whole row
@@ -597,12 +640,13 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kX, kRing>::kBytes > 80 *
     {
       typedef unsigned int u4v __attribute__((ext_vector_type(4)));
       typedef u4v u4a2 __attribute__((aligned(2)));
-      uint8_t* reg = smem + L::kEpiAt + wave * L::kEpiWave;
+      uint8_t* reg = smem + L::kEpiAt + (group * 4 + wave) * L::kEpiWave;
       const int nw = cur.col0 + wn * 16 * NA, mw = cur.row0 + wm * 16 * NB;
       constexpr int kLanesRow = 2 * NA, kRows = 64 / kLanesRow, kPasses = L::kEpiRows / kRows;
       const int rr = lane / kLanesRow, cc = (lane % kLanesRow) * 8;
 #pragma unroll
-      for (int k = 0; k < NB; ++k)
+      for (int k = 0; k < NB; ++k) {
+        if (kGroups == 2 && k / (NB / 2) != group) continue;
 #pragma unroll
         for (int part = 0; part < 16 / L::kEpiRows; ++part) {
           if (L::kEpiRows == 16 || li / L::kEpiRows == part) {
@@ -625,9 +669,8 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kX, kRing>::kBytes > 80 *
             if (m >= cur.row_end || n >= p.N) continue;
             uint16_t* d = p.y + (size_t)m * p.ldy + n;
             if (n + 7 < p.N) {
-              // (pieces that are not on 16 bytes: the hardware serves them too,
-              // but parts of cache lines are better left for L2 to join)
-              if (p.vec) __builtin_nontemporal_store(o[r], reinterpret_cast<u4v*>(d));
+              // (the hardware serves pieces that are not on 16 bytes, too)
+              if (p.past) __builtin_nontemporal_store(o[r], reinterpret_cast<u4v*>(d));
               else *reinterpret_cast<u4a2*>(d) = o[r];
             } else {
               for (int e = 0; e < 8; ++e)
@@ -636,8 +679,9 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kX, kRing>::kBytes > 80 *
           }
           asm volatile("" ::: "memory");
         }
+      }
     }
-    if (!nxt.live) break;
+    if (kGroups == 2 || !nxt.live) break;
     cur = nxt;
     ++t;
   }
@@ -647,10 +691,23 @@ __global__ __launch_bounds__(kThreads, (Fp4Lds<NA, NB, kX, kRing>::kBytes > 80 *
 
 namespace {
 
-template <int NA, int NB, int kX, bool kExperts, int kRing>
+bool rows_on(const void* y, int64_t ldy, int64_t bytes) { return (((uintptr_t)y | (uintptr_t)(ldy * 2)) & (bytes - 1)) == 0; }
+
+// y goes around the caches where its rows allow 16-byte pieces, but for a large
+// one that a short K leaves as what counts, in parts of cache lines: those are
+// better left for L2 to join (8192 x 6000 x 256 54 us around, 34 through L2; 4096
+// x 6008 x 512 35 and 25, 2048 x 16008 x 1024 42 and 36; but 8192 x 6000 x 1024
+// 56 and 60, 4096 x 6008 x 4096 69 and 74, and for the experts 2008 x 768, 4096
+// tokens, 77 and 92).
+bool past_caches(const void* y, int64_t ldy, int64_t M, int64_t N, int64_t K) {
+  if (!rows_on(y, ldy, 16)) return false;
+  return rows_on(y, ldy, 128) || K > (rows_on(y, ldy, 32) ? 512 : 1024) || M * N <= (int64_t)16 << 20;
+}
+
+template <int NA, int NB, int kX, bool kExperts, int kGroups = 1>
 int go(const Fp4Args& p, int64_t tiles, hipStream_t stream) {
-  using L = Fp4Lds<NA, NB, kX, kRing>;
-  auto kern = gemm_fp4_kernel<NA, NB, kX, kExperts, kRing>;
+  using L = Fp4Lds<NA, NB, kX, kGroups>;
+  auto kern = gemm_fp4_kernel<NA, NB, kX, kExperts, kGroups>;
   static std::atomic<int> lds_set[kMaxDevices];
   constexpr int most_lds = L::kBytes + (int)(kFp4FusedMaxK / 128) * L::kFusedStep;
   static_assert(most_lds <= 160 * 1024, "LDS of a compute unit");
@@ -658,8 +715,8 @@ int go(const Fp4Args& p, int64_t tiles, hipStream_t stream) {
   const int lds = L::kBytes + p.K / 128 * L::kFusedStep;
   const int64_t per_cu = lds <= 80 * 1024 ? 2 : 1;
   const int64_t cus = device_cu_count();
-  const int64_t most = std::max<int64_t>(1, (cus >= 8 ? cus - cus % 8 : cus) * per_cu);
-  hipLaunchKernelGGL(kern, dim3((unsigned)std::min(tiles, most)), dim3(kThreads), lds, stream, p);
+  const int64_t most = kGroups == 2 ? tiles : std::max<int64_t>(1, (cus >= 8 ? cus - cus % 8 : cus) * per_cu);
+  hipLaunchKernelGGL(kern, dim3((unsigned)std::min(tiles, most)), dim3(kThreads * kGroups), lds, stream, p);
   return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 
@@ -678,14 +735,14 @@ int launch_gemm_fp4_tile(const void* qp, const void* sp, int64_t M, int64_t K, c
   p.bias = (const uint16_t*)bias;
   p.y = (uint16_t*)y;
   p.ldy = ldy;
-  p.vec = ldy % 8 == 0 && ((uintptr_t)y & 15) == 0;
+  p.past = past_caches(y, ldy, M, N, K);
   const int64_t tiles = ((M + plan.mt - 1) / plan.mt) * ((N + plan.nt - 1) / plan.nt);
-  if (plan.nt == 256) return go<8, 8, kPacked, false, 4>(p, tiles, stream);
-  // One tile per compute unit: twice the slots; more: two workgroups on each.
-  const bool deep = tiles <= device_cu_count();
+  if (plan.nt == 256) return go<8, 8, kPacked, false>(p, tiles, stream);
+  // One tile per compute unit: two groups of waves; more: two workgroups on each.
+  const bool one = tiles <= device_cu_count();
   if (plan.mt == 128)
-    return deep ? go<4, 4, kPacked, false, 8>(p, tiles, stream) : go<4, 4, kPacked, false, 4>(p, tiles, stream);
-  return deep ? go<4, 2, kPacked, false, 8>(p, tiles, stream) : go<4, 2, kPacked, false, 4>(p, tiles, stream);
+    return one ? go<4, 4, kPacked, false, 2>(p, tiles, stream) : go<4, 4, kPacked, false>(p, tiles, stream);
+  return one ? go<4, 2, kPacked, false, 2>(p, tiles, stream) : go<4, 2, kPacked, false>(p, tiles, stream);
 }
 
 int launch_experts_fp4_tile(const ExpertsArgs& a, const void* q, const void* s, Fp4Plan plan, hipStream_t stream) {
@@ -701,7 +758,7 @@ int launch_experts_fp4_tile(const ExpertsArgs& a, const void* q, const void* s, 
   p.N = (int)a.N;
   p.y = (uint16_t*)a.y;
   p.ldy = a.ldy;
-  p.vec = a.ldy % 8 == 0 && ((uintptr_t)a.y & 15) == 0;
+  p.past = rows_on(a.y, a.ldy, 16);
   p.R = (int)a.R;
   p.E = (int)a.E;
   p.topk = (int)a.topk;
@@ -710,9 +767,9 @@ int launch_experts_fp4_tile(const ExpertsArgs& a, const void* q, const void* s, 
   // At most one more row tile per expert than the rows fill.
   const int64_t row_tiles = a.R / plan.mt + std::min(a.E, a.R);
   const int64_t tiles = row_tiles * ((a.N + plan.nt - 1) / plan.nt);
-  if (plan.nt == 256) return go<8, 4, kRows, true, 4>(p, tiles, stream);
-  if (plan.mt == 128) return go<4, 4, kRows, true, 4>(p, tiles, stream);
-  return go<4, 2, kRows, true, 4>(p, tiles, stream);
+  if (plan.nt == 256) return go<8, 4, kRows, true>(p, tiles, stream);
+  if (plan.mt == 128) return go<4, 4, kRows, true>(p, tiles, stream);
+  return go<4, 2, kRows, true>(p, tiles, stream);
 }
 
 int launch_gemm_fp4_fused(const void* x, int64_t ldx, int64_t M, int64_t K, const void* wp, const void* wsp, int64_t N,
@@ -729,8 +786,10 @@ int launch_gemm_fp4_fused(const void* x, int64_t ldx, int64_t M, int64_t K, cons
   p.bias = (const uint16_t*)bias;
   p.y = (uint16_t*)y;
   p.ldy = ldy;
-  p.vec = ldy % 8 == 0 && ((uintptr_t)y & 15) == 0;
-  return go<4, 2, kFused, false, 4>(p, (M + 63) / 64 * ((N + 127) / 128), stream);
+  p.past = past_caches(y, ldy, M, N, K);
+  const int64_t tiles = (M + 63) / 64 * ((N + 127) / 128);
+  return tiles <= device_cu_count() ? go<4, 2, kFused, false, 2>(p, tiles, stream)
+                                    : go<4, 2, kFused, false>(p, tiles, stream);
 }
 
 int launch_experts_fp4_fused(const ExpertsArgs& a, hipStream_t stream) {
@@ -744,13 +803,15 @@ int launch_experts_fp4_fused(const ExpertsArgs& a, hipStream_t stream) {
   p.N = (int)a.N;
   p.y = (uint16_t*)a.y;
   p.ldy = a.ldy;
-  p.vec = a.ldy % 8 == 0 && ((uintptr_t)a.y & 15) == 0;
+  p.past = rows_on(a.y, a.ldy, 16);
   p.R = (int)a.R;
   p.E = (int)a.E;
   p.topk = (int)a.topk;
   p.slots = a.slots;
   p.offsets = a.offsets;
-  return go<4, 2, kFused, true, 4>(p, (a.R / 64 + std::min(a.E, a.R)) * ((a.N + 127) / 128), stream);
+  const int64_t tiles = (a.R / 64 + std::min(a.E, a.R)) * ((a.N + 127) / 128);
+  return tiles <= device_cu_count() ? go<4, 2, kFused, true, 2>(p, tiles, stream)
+                                    : go<4, 2, kFused, true>(p, tiles, stream);
 }
 
 }  // namespace mxfp8
