@@ -4,6 +4,14 @@
 // On gfx950 the scaled MFMA multiplies 4-bit by 4-bit operands in half the
 // cycles of 8-bit ones, with half the operand bytes, so a 128-K step of a 256
 // x 256 tile is 64 MFMAs of 16 cycles per wave against 32 KiB of operands.
+// Bound by the matrix cores' power where tiles are large: 8192 x 28672 x 8192
+// 790 us (4.9 PFLOP/s), of which MFMAs alone would take 588, with the copies 652,
+// with the LDS reads 686; the chip's clock falls with the work between them (a
+// loop of MFMAs on registers: 7.5 PFLOP/s on random codes, 9.0 on zeros).  The
+// experts' tiles by their start and end, which nothing else covers: 4096 tokens,
+// 128 experts, k 8, 1536 x 2048 102 us (3.2 TB/s of the 331 MB that they cannot do
+// without); 14 us per 256 x 128 tile, of which the sixteen steps are 7.5, the
+// stores 2, staging them 1, the next tile's decoding and sources 1.5.
 //
 //  * Workgroup tile 32 NA weight rows x 32 NB activation rows, four waves as 2
 //    x 2, each 16 NA x 16 NB: NA x NB v_mfma_scale_f32_16x16x128 per 128-K
@@ -635,8 +643,8 @@ __global__ __launch_bounds__(kThreads * kGroups, (kGroups == 2 || Fp4Lds<NA, NB,
 
     // ---------------------------------------------------------- epilogue
     // The wave stages kEpiRows rows at a time as bf16 (16-byte chunk c of row r at c ^
-    // r % 8, against bank conflicts) and stores 16-byte pieces of whole row
-    // segments (a wave's LDS accesses run in order: no waits).
+    // turn(r): the same chunk of sixteen rows on all banks) and stores 16-byte
+    // pieces of whole row segments (a wave's LDS accesses run in order: no waits).
     {
       typedef unsigned int u4v __attribute__((ext_vector_type(4)));
       typedef u4v u4a2 __attribute__((aligned(2)));
@@ -644,6 +652,8 @@ __global__ __launch_bounds__(kThreads * kGroups, (kGroups == 2 || Fp4Lds<NA, NB,
       const int nw = cur.col0 + wn * 16 * NA, mw = cur.row0 + wm * 16 * NB;
       constexpr int kLanesRow = 2 * NA, kRows = 64 / kLanesRow, kPasses = L::kEpiRows / kRows;
       const int rr = lane / kLanesRow, cc = (lane % kLanesRow) * 8;
+      auto turn = [](int r) { return NA == 8 ? r & 15 : (r >> 1) & 7; };
+      const int lr = li % L::kEpiRows;
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
         if (kGroups == 2 && k / (NB / 2) != group) continue;
@@ -653,7 +663,7 @@ __global__ __launch_bounds__(kThreads * kGroups, (kGroups == 2 || Fp4Lds<NA, NB,
 #pragma unroll
             for (int a = 0; a < NA; ++a) {
               const v4f v = acc[a][k];
-              *reinterpret_cast<uint2*>(reg + li % L::kEpiRows * L::kPitch + (((2 * a + (lg >> 1)) ^ (li & 7)) << 4) +
+              *reinterpret_cast<uint2*>(reg + lr * L::kPitch + (((2 * a + (lg >> 1)) ^ turn(lr)) << 4) +
                                         (lg & 1) * 8) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
             }
           }
@@ -662,7 +672,7 @@ __global__ __launch_bounds__(kThreads * kGroups, (kGroups == 2 || Fp4Lds<NA, NB,
 #pragma unroll
           for (int r = 0; r < kPasses; ++r)
             o[r] = *reinterpret_cast<const u4v*>(reg + (rr + kRows * r) * L::kPitch +
-                                                 (((cc >> 3) ^ ((rr + kRows * r) & 7)) << 4));
+                                                 (((cc >> 3) ^ turn(rr + kRows * r)) << 4));
 #pragma unroll
           for (int r = 0; r < kPasses; ++r) {
             const int m = mw + 16 * k + L::kEpiRows * part + rr + kRows * r, n = nw + cc;

@@ -8,7 +8,10 @@
 // added through LDS in K order.  A lane of the 4-bit 16x16x128 MFMA holds K
 // [32g, 32g + 32) of its row, which is one MX block: lane (i, g) loads the 64
 // bytes of that block of row i, finds its largest magnitude and converts it by
-// itself, with no exchange between lanes and no staging.
+// itself, with no exchange between lanes and no staging.  (1 x 4096 x 4096: 4.8
+// us in a graph of such calls, of which about 2.5 are the launch; 8 rows of eight
+// experts, 1536 x 2048: 8.0 us, 1.7 TB/s.  The 16-row form below, 32 x 16384 x
+// 8192: 24.8 us with the quantizer, 2.9 TB/s.)
 //
 // Experts: workgroup (n, j) takes weight rows 16 n .. of the j-th expert that
 // has rows, and all of those, 16 at a time, against the weight it holds.

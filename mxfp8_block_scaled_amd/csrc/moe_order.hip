@@ -12,6 +12,12 @@
 // Permute's gradient is unpermute without weights.  No atomics across
 // workgroups: results do not depend on timing.  (Rows out of range, which
 // sort never makes, are skipped.)
+//
+// Measured, 4096 tokens, top 8 of 128, H 2048 bf16: sort 8.3 us (two launches,
+// 5 of them the second's chain of LDS steps); permute 27.7 and unpermute 25.3,
+// 5.4 and 6.0 TB/s of the 151 MB that they read and write; the gradient of both
+// operands 50, 5.7 TB/s.  32768 tokens, top 2, H 4096: 137, 131 and 255 us (5.9,
+// 6.1 and 5.3 TB/s).
 #include <algorithm>
 
 #include "common.hpp"

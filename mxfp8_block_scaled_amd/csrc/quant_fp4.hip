@@ -1,7 +1,8 @@
 // bf16 rows -> MXFP4 activations (the MX rule with E2M1 elements: shared
 // exponent floor(log2 amax) - 2, round to nearest even, saturate to +-6), in
 // the packed operand layout or row-major.  Bound by memory: 2 bytes read and
-// 0.53 written per element.  Four lanes share a block, 16 bytes each.
+// 0.53 written per element (8192 x 8192 packed 28 us, 6.0 TB/s; 32768 x 768 by
+// rows 13 us, 4.9 TB/s).  Four lanes share a block, 16 bytes each.
 #include "fp4.hpp"
 
 namespace mxfp8 {
