@@ -51,13 +51,20 @@ std::atomic<int> g_force{0};
 //   M = 1000                       21.0   20.0   34.5
 //   M = 4096                       60.6   48.1   45.6
 // and 16384 x 8192:
+//   M = 1     17.3   24.1          18.8   22.6
+//   M = 16    21.9   24.8          18.8   22.6
 //   M = 32           24.8          19.0   22.8
 //   M = 2048                        190    143    129
 double thousands(int64_t K) { return (double)K / 1024.0; }
-double turns(int64_t N) { return std::max(1.0, (double)N / 4096.0); }   // of one workgroup per compute unit, 16 rows each
+// Blocks of 16 weight rows, one for each workgroup of the chip's first turn.
+bool decode_one(int64_t parts, int64_t M, int64_t N, int64_t K) {
+  return parts * ((N + 15) / 16) <= 256 * mxfp8::fp4_decode_per_cu(M, K);
+}
 double decode_us(int64_t M, int64_t N, int64_t K) {
-  const double t = turns(N), k = t * thousands(K);
-  return 4.2 + 0.1 * (t - 1.0) + k * (0.42 + 0.04 * (double)M + (M > 16 ? 0.52 : 0.0));
+  const double t = std::max(1.0, (double)N / 4096.0), m = (double)M;
+  if (decode_one(1, M, N, K))
+    return 4.2 + 0.1 * (t - 1.0) + t * thousands(K) * (0.42 + 0.04 * m + (M > 16 ? 0.52 : 0.0));
+  return 3.6 + (M > 16 ? 3.5 : 0.0) + 0.115e-6 * (double)N * (double)K * (1.0 + 0.014 * m);   // (bytes at 4.6 TB/s)
 }
 double mid_us(int64_t M, int64_t N, int64_t K) {
   const double k = thousands(K), t = std::ceil((double)N / 4096.0);
@@ -172,12 +179,14 @@ struct ExpertsForm {
 // with its rows converted again for each 16 weight rows; tiles that quantize
 // their rows take a longer start, a quantizer before them one more launch.  For
 // example (rows per expert; decode, 128 x 64 tiles that quantize, tiles of 128 x
-// 64, 128 x 128, 256 x 128), 128 experts, N x K = 1536 x 2048 and 2048 x 768:
-//   8 rows in all   7.6   11.3   11.7                     5.8    6.8    8.4
-//   0.25           17.7   20.8   16.4                    13.1    9.7   11.6
-//   1              45     30.8   25     30     31        28.7   15.3   16.0
-//   64                           60     61     62                       40    42    42
-//   256                         140    124    114                       98    89    84
+// 64, 128 x 128, 256 x 128), N x K = 2048 x 2048 and 2048 x 768:
+//   8 experts, 1    10.6   12.0   12.1                    6.7    7.9    9.0
+//   32, 1           14.1   18.5   16.2                   10.1    9.9   11.4
+//   64, 2           21.8   27.7   23.2                   11.9   13.2   14.4
+//   64, 6           41.3   46.4   31.7                   20.1   17.9   17.3
+// and 128 experts, 1536 x 2048 and 2048 x 768:
+//   64                            60     61     62                      40    42    42
+//   256                          140    124    114                      98    89    84
 ExpertsForm experts_form(int64_t R, int64_t N, int64_t K, int64_t E) {
   const int force = g_force.load(std::memory_order_relaxed);
   const double X = (double)std::max<int64_t>(1, std::min(E, R)), rows = (double)R / X;
@@ -190,10 +199,12 @@ ExpertsForm experts_form(int64_t R, int64_t N, int64_t K, int64_t E) {
     const double k = thousands(K);
     const int64_t cols = (N + 127) / 128, most = (R / 64 + std::min(E, R)) * cols;   // (row tiles: one per expert is partial)
     const double two = 8.1 + 2.05 * k + 0.05 * work;
-    const double td = can_decode && rows <= 8.0 ? 4.0 + 0.15 * work * (1.0 + rows / 4.0) : 1e30;
+    const double td = !can_decode || rows > 8.0                  ? 1e30
+                      : decode_one(std::min(E, R), 1, N, K) ? 4.3 + 0.15 * work * (1.0 + rows / 8.0)
+                                                            : 6.5 + 0.07 * work * (1.0 + rows / 7.0);
     const double tf = !can_fuse(std::min(E, R) * cols, K) ? 1e30
                       : most <= 256                       ? 6.3 + k * (2.0 + 0.037 * std::min(64.0, rows))
-                                                          : 4.6 + 2.76 * k + work * (0.045 + 8.0e-3 * rows);
+                                                          : 5.4 + 2.76 * k + work * (0.045 + 8.0e-3 * rows);
     if (td <= std::min(tf, two)) return {kDecode, {}};
     if (tf <= two) return {kFusedTiles, {}};
   }

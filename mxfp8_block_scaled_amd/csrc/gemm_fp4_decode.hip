@@ -35,19 +35,23 @@ struct DecodeArgs {
   int64_t ldy;
   // experts
   int R, E, topk, x_rows;
+  int runs;                // workgroups of an expert
   const int* slots;
   const int* offsets;
 };
 
-// The waves' partial sums of a lane, in K order.
-template <int kWaves>
+// The waves' partial sums of a lane, in K order; kBatch of them in flight.
+template <int kWaves, int kBatch = kWaves>
 __device__ inline v4f sum_waves(const v4f* red, int lane) {
-  v4f part[kWaves];
+  v4f v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int k = 0; k < kWaves; ++k) part[k] = red[k * 64 + lane];
-  v4f v = part[0];
+  for (int k0 = 0; k0 < kWaves; k0 += kBatch) {
+    v4f part[kBatch];
 #pragma unroll
-  for (int k = 1; k < kWaves; ++k) v += part[k];
+    for (int k = 0; k < kBatch; ++k) part[k] = red[(k0 + k) * 64 + lane];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) v += part[k];
+  }
   return v;
 }
 
@@ -71,22 +75,27 @@ __device__ inline void store4(const DecodeArgs& p, const v4f& v, const float* bv
 }  // namespace
 
 // kSteps: the most steps a wave owns; kGroups: 16-row groups in flight together
-// (experts: one).
-template <int kWaves, int kSteps, int kGroups, bool kExperts>
-__global__ __launch_bounds__(64 * kWaves) void gemm_fp4_decode_kernel(DecodeArgs p) {
-  __shared__ v4f red[kGroups][kWaves * 64];
+// (experts: one).  kDepth: 1 for workgroups of one block of 16 weight rows; more
+// for such with a run of blocks, that many in flight, where a turn of the chip does
+// not hold all blocks: the rows are quantized once for the run, and the weight
+// streams while sums are joined (16 rows, 16384 x 8192: 22 us, one block each 44; 1
+// row 17 and 25; but 1 row, 4096 x 4096, 7.2 and 5.7: more registers, later rows).
+template <int kWaves, int kSteps, int kGroups, int kDepth, bool kExperts>
+__global__ __launch_bounds__(64 * kWaves, kDepth == 1 ? 1 : 4) void gemm_fp4_decode_kernel(DecodeArgs p) {
+  __shared__ v4f red[kDepth == 1 ? 1 : 2][kGroups][kWaves * 64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i = lane & 15, g = lane >> 4;
   const int KS = p.K / 128;
   const int kb = KS * wave / kWaves, nsteps = KS * (wave + 1) / kWaves - kb;
 
-  int row0 = 0, row_end = p.M, n0;
-  int64_t group = 0;
+  const int blocks = (p.N + 15) / 16;
+  int row0 = 0, row_end = p.M, run, runs;   // this workgroup's run of so many
+  int64_t group0 = 0;                       // the expert's first 128-row group
   if constexpr (kExperts) {
-    const int blocks = (p.N + 15) / 16;
-    const int j = (int)blockIdx.x / blocks;
-    n0 = ((int)blockIdx.x - j * blocks) * 16;
+    runs = p.runs;
+    const int j = (int)blockIdx.x / runs;
+    run = (int)blockIdx.x - j * runs;
     zero_rows(p.y, p.ldy, max(p.offsets[p.E], 0), p.R, p.N, kWaves);
     int at = j, e = -1;
 #pragma unroll
@@ -108,22 +117,48 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_fp4_decode_kernel(DecodeArgs
       }
     }
     if (e < 0) return;                       // (fewer experts with rows than workgroups)
-    group = (int64_t)e * ((p.N + kGroupRows - 1) / kGroupRows);
+    group0 = (int64_t)e * ((p.N + kGroupRows - 1) / kGroupRows);
   } else {
-    // Dies take contiguous runs of 16-row blocks.
-    n0 = xcd_remap((int)blockIdx.x, (int)gridDim.x) * 16;
+    runs = (int)gridDim.x;
+    // Dies take contiguous runs of blocks.
+    run = xcd_remap((int)blockIdx.x, runs);
   }
-  group += n0 / kGroupRows;
-  const int r = n0 % kGroupRows + i;
+  // (at most 2^20 blocks and 2^11 runs)
+  const int b0 = kDepth == 1 ? run : (int)((uint32_t)blocks * (uint32_t)run / (uint32_t)runs);
+  const int b1 = kDepth == 1 ? run + 1 : (int)((uint32_t)blocks * (uint32_t)(run + 1) / (uint32_t)runs);
 
-  // The weight: chunk g of row r and the scale of block g for each step, all
-  // in flight together with the first rows.
-  const uint8_t* wrow = p.wp + (size_t)group * KS * kTileBytes + packed_off(r, 0, g, KS);
-  const uint8_t* srow = p.wsp + (size_t)group * KS * 2 * kTileScaleBytes + (g >> 1) * kTileScaleBytes + scale_off(r, g & 1);
-  uint4 xv[kGroups][kSteps][4];
+  // A block's weight: chunk g of row i and the scale of MX block g for each step;
+  // and the bias of columns 4 g .. 4 g + 3, by whole words (an odd N's last word
+  // holds one value that is not the bias's and reaches no output).
+  struct Block {
+    uint4 w[kSteps];
+    int s[kSteps];
+    uint32_t bias[2];
+  };
+  auto load_block = [&](Block& f, int b) {
+    const int n0 = min(b, b1 - 1) * 16, r = n0 % kGroupRows + i;
+    const int64_t group = group0 + n0 / kGroupRows;
+    const uint8_t* wrow = p.wp + (size_t)group * KS * kTileBytes + packed_off(r, 0, g, KS);
+    const uint8_t* srow = p.wsp + (size_t)group * KS * 2 * kTileScaleBytes + (g >> 1) * kTileScaleBytes + scale_off(r, g & 1);
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) {
+      const int ks = min(kb + u, KS - 1);
+      f.w[u] = *reinterpret_cast<const uint4*>(wrow + (size_t)ks * kPieceBytes);
+      f.s[u] = srow[(size_t)ks * 2 * kTileScaleBytes];
+    }
+    if (!kExperts && p.bias != nullptr) {
+      const uint32_t* words = reinterpret_cast<const uint32_t*>(p.bias);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) f.bias[e] = words[min(n0 / 2 + 2 * g + e, (p.N - 1) / 2)];
+    } else {
+      f.bias[0] = f.bias[1] = 0u;
+    }
+  };
+  // 16 kGroups rows from m0 on, quantized: lane (i, g) holds block g of row m0 + i.
+  // (A step past the wave's run, and a row past the last, are zeros.)
+  int xq[kGroups][kSteps][4], xs[kGroups][kSteps];
   auto load_rows = [&](int m0) {
-    // Lane (i, g): block g of row m0 + i.  (A step past the wave's run, and a
-    // row past the last, stay zero.)
+    uint4 v[kGroups][kSteps][4];
 #pragma unroll
     for (int t = 0; t < kGroups; ++t) {
       const int m = m0 + 16 * t + i;
@@ -137,51 +172,63 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_fp4_decode_kernel(DecodeArgs
       for (int u = 0; u < kSteps; ++u)
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          xv[t][u][c] =
+          v[t][u][c] =
               in && u < nsteps ? *reinterpret_cast<const uint4*>(xr + u * 128 + c * 8) : make_uint4(0u, 0u, 0u, 0u);
     }
-  };
-  // The weight first: with gathered rows the others wait for their indices.
-  uint4 w[kSteps];
-  int wsc[kSteps];
 #pragma unroll
-  for (int u = 0; u < kSteps; ++u) {
-    const int ks = min(kb + u, KS - 1);
-    w[u] = *reinterpret_cast<const uint4*>(wrow + (size_t)ks * kPieceBytes);
-    wsc[u] = srow[(size_t)ks * 2 * kTileScaleBytes];
-  }
-  load_rows(row0);
-  const int n = n0 + 4 * g;
-  float bv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (p.bias != nullptr && wave < kGroups) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) bv[e] = __uint_as_float((uint32_t)p.bias[min(n + e, p.N - 1)] << 16);
-  }
-  __builtin_amdgcn_sched_barrier(0);
-
-  for (int m0 = row0; m0 < row_end; m0 += 16 * kGroups) {
-    if (m0 != row0) load_rows(m0);
-#pragma unroll
-    for (int t = 0; t < kGroups; ++t) {
-      v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t = 0; t < kGroups; ++t)
 #pragma unroll
       for (int u = 0; u < kSteps; ++u) {
-        const uint4(&x)[4] = xv[t][u];
+        const uint4(&x)[4] = v[t][u];
         const uint32_t sb = fp4_scale_byte(max(max(fp4_absmax8(x[0]), fp4_absmax8(x[1])), max(fp4_absmax8(x[2]), fp4_absmax8(x[3]))));
         const float scale = fp4_scale_value(sb);
-        const v8i b = {(int)cvt8_fp4(x[0], scale), (int)cvt8_fp4(x[1], scale), (int)cvt8_fp4(x[2], scale),
-                       (int)cvt8_fp4(x[3], scale), 0, 0, 0, 0};
-        const v8i a = {(int)w[u].x, (int)w[u].y, (int)w[u].z, (int)w[u].w, 0, 0, 0, 0};
-        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, 4, 0, wsc[u], 0, (int)sb);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) xq[t][u][c] = (int)cvt8_fp4(x[c], scale);
+        xs[t][u] = (int)sb;
       }
-      red[t][wave * 64 + lane] = acc;
+  };
+
+  // The weight first: with gathered rows the others wait for their indices.
+  Block f[kDepth];
+  if constexpr (kDepth == 1) load_block(f[0], b0);
+  for (int m0 = row0; m0 < row_end; m0 += 16 * kGroups) {
+#pragma unroll
+    for (int d = 0; d < kDepth - 1; ++d) load_block(f[d], b0 + d);
+    __builtin_amdgcn_sched_barrier(0);
+    load_rows(m0);
+    for (int base = b0; base < b1; base += kDepth) {
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {
+        const int b = base + d;
+        if (b >= b1) break;
+        if constexpr (kDepth > 1) load_block(f[(d + kDepth - 1) % kDepth], b + kDepth - 1);
+        v4f(&out)[kGroups][kWaves * 64] = red[kDepth == 1 ? 0 : (b - b0) & 1];
+#pragma unroll
+        for (int t = 0; t < kGroups; ++t) {
+          v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int u = 0; u < kSteps; ++u) {
+            const v8i bx = {xq[t][u][0], xq[t][u][1], xq[t][u][2], xq[t][u][3], 0, 0, 0, 0};
+            const v8i aw = {(int)f[d].w[u].x, (int)f[d].w[u].y, (int)f[d].w[u].z, (int)f[d].w[u].w, 0, 0, 0, 0};
+            acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(aw, bx, acc, 4, 4, 0, f[d].s[u], 0, xs[t][u]);
+          }
+          out[t][wave * 64 + lane] = acc;
+        }
+        // (one barrier per block: `out` is written again two blocks on, when
+        // every wave has passed the next one)
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        const int who = (wave - (b - b0)) & (kWaves - 1);   // the waves take turns
+        if (who < kGroups) {
+          const v4f v = sum_waves<kWaves, kDepth == 1 ? kWaves : 4>(out[who], lane);
+          const float bv[4] = {bf16_lo(f[d].bias[0]), bf16_hi(f[d].bias[0]), bf16_lo(f[d].bias[1]), bf16_hi(f[d].bias[1])};
+          store4(p, v, bv, m0 + 16 * who + i, row_end, b * 16 + 4 * g);   // D[n = 4g + e][m = i]
+        }
+      }
     }
-    __syncthreads();
-    if (wave < kGroups) {
-      const v4f v = sum_waves<kWaves>(red[wave], lane);
-      store4(p, v, bv, m0 + 16 * wave + i, row_end, n);   // D[n = 4g + e][m = i]
-    }
-    if constexpr (kExperts) __syncthreads();   // red is written again
+    // (the last block's sums are read before the next rows' are written)
+    if (kExperts && m0 + 16 * kGroups < row_end) __syncthreads();
   }
 }
 
@@ -265,24 +312,33 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_fp4_mid_kernel(const uint8_t
 }
 
 namespace {
+// parts: 1, or the experts with rows at most.
 template <bool kExperts>
-int decode(const DecodeArgs& p, int64_t blocks, hipStream_t stream) {
-  auto go = [&](auto kern, int waves) {
-    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(64 * waves), 0, stream, p);
+int decode(DecodeArgs p, int64_t parts, hipStream_t stream) {
+  const int64_t blocks = (p.N + 15) / 16, cus = device_cu_count();
+  auto go = [&](auto kern, int waves, int64_t runs) {
+    p.runs = (int)runs;
+    hipLaunchKernelGGL(kern, dim3((unsigned)(parts * runs)), dim3(64 * waves), 0, stream, p);
     return hipGetLastError() == hipSuccess ? 0 : -7;
+  };
+  // Workgroups with runs have 16 waves per compute unit.
+  auto pick = [&](auto one, auto many, int waves) {
+    if (blocks * parts <= cus * fp4_decode_per_cu(kExperts ? 1 : p.M, p.K)) return go(one, waves, blocks);
+    return go(many, waves, std::min(blocks, (cus * (16 / waves) + parts - 1) / parts));
   };
   static_assert(kFp4DecodeMaxK == 16 * 4 * 128, "a wave owns at most four steps");
   const int KS = p.K / 128;
   if constexpr (!kExperts) {
     if (p.M > 16) {
-      if (KS <= 16) return go(gemm_fp4_decode_kernel<16, 1, 2, false>, 16);
-      return go(gemm_fp4_decode_kernel<16, 2, 2, false>, 16);
+      if (KS <= 16) return pick(gemm_fp4_decode_kernel<16, 1, 2, 1, false>, gemm_fp4_decode_kernel<16, 1, 2, 4, false>, 16);
+      return pick(gemm_fp4_decode_kernel<16, 2, 2, 1, false>, gemm_fp4_decode_kernel<16, 2, 2, 2, false>, 16);
     }
   }
-  if (KS <= 8) return go(gemm_fp4_decode_kernel<4, 2, 1, kExperts>, 4);
-  if (KS <= 16) return go(gemm_fp4_decode_kernel<8, 2, 1, kExperts>, 8);
-  if (KS <= 32) return go(gemm_fp4_decode_kernel<16, 2, 1, kExperts>, 16);
-  return go(gemm_fp4_decode_kernel<16, 4, 1, kExperts>, 16);
+  constexpr bool X = kExperts;
+  if (KS <= 8) return pick(gemm_fp4_decode_kernel<4, 2, 1, 1, X>, gemm_fp4_decode_kernel<4, 2, 1, 4, X>, 4);
+  if (KS <= 16) return pick(gemm_fp4_decode_kernel<8, 2, 1, 1, X>, gemm_fp4_decode_kernel<8, 2, 1, 4, X>, 8);
+  if (KS <= 32) return pick(gemm_fp4_decode_kernel<16, 2, 1, 1, X>, gemm_fp4_decode_kernel<16, 2, 1, 3, X>, 16);
+  return pick(gemm_fp4_decode_kernel<16, 4, 1, 1, X>, gemm_fp4_decode_kernel<16, 4, 1, 2, X>, 16);
 }
 template <int kWaves, int kGroups, int kBatch>
 int mid(const void* qp, const void* sp, const DecodeArgs& p, hipStream_t stream) {
@@ -325,7 +381,7 @@ int launch_gemm_fp4_decode(const void* x, int64_t ldx, int64_t M, int64_t K, con
   p.bias = (const uint16_t*)bias;
   p.y = (uint16_t*)y;
   p.ldy = ldy;
-  return decode<false>(p, (N + 15) / 16, stream);
+  return decode<false>(p, 1, stream);
 }
 
 int launch_experts_fp4_decode(const ExpertsArgs& a, hipStream_t stream) {
@@ -344,7 +400,7 @@ int launch_experts_fp4_decode(const ExpertsArgs& a, hipStream_t stream) {
   p.x_rows = (int)a.x_rows;
   p.slots = a.slots;
   p.offsets = a.offsets;
-  return decode<true>(p, (a.N + 15) / 16 * std::min(a.E, a.R), stream);
+  return decode<true>(p, std::min(a.E, a.R), stream);
 }
 
 }  // namespace mxfp8
