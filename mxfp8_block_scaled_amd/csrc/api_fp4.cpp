@@ -35,61 +35,62 @@ bool gemm_grid_ok(int64_t M, int64_t N) { return (M + 63) / 64 * ((N + 127) / 12
 std::atomic<int> g_force{0};
 
 // The forms with the least estimated time: lines through measurements on
-// MI355X (us, calls in a captured graph, the quantizer's launch included), K in
-// thousands (1024).  For example (decode; 16 weight rows on packed activations;
+// MI355X (us, 16 calls in a captured graph, the quantizer's launch included), K
+// in thousands (1024).  For example (decode; 16 weight rows on packed activations;
 // 128 x 64 tiles that quantize their rows; tiles of 128 x 64, 128 x 128, 256 x
 // 256), N x K = 4096 x 1024:
-//   M = 1      4.6    8.1    6.4    9.2
-//   M = 32     8.2    8.1    8.4    9.3   10.3
-//   M = 128           8.5    9.8    9.6   10.6
-//   M = 1000                14.8   11.9   12.1   18.3
-//   M = 4096                       26.1   21.9   22.6
+//   M = 1        3.0    6.8    6.6    8.0    9.0
+//   M = 32       5.7    6.8    7.2    8.1    9.2
+//   M = 128             7.1    8.9    8.2    9.4   16.2
+//   M = 1000                  13.7   10.4   10.9   17.3
+//   M = 4096                  47.7   27.8   23.4   23.7
 // 4096 x 4096:
-//   M = 1      5.9    8.2          12.8
-//   M = 32    12.0    8.4          13.0   15.4
-//   M = 128          12.1          13.2   15.6
-//   M = 1000                       21.0   20.0   34.5
-//   M = 4096                       60.6   48.1   45.6
+//   M = 1        4.0    7.0          11.5   13.9
+//   M = 16       6.0    7.1          11.7   14.0
+//   M = 32       8.9    7.2          11.7   14.2
+//   M = 128            10.9          12.0   14.3   30.7
+//   M = 1000                         20.1   19.0   33.7
+//   M = 4096                         62.3   50.3   46.3
 // and 16384 x 8192:
-//   M = 1     17.3   24.1          18.8   22.6
-//   M = 16    21.9   24.8          18.8   22.6
-//   M = 32           24.8          19.0   22.8
-//   M = 2048                        190    143    129
+//   M = 1       14.6   23.9          17.6   20.9
+//   M = 16      16.8   23.6          17.9   21.2
+//   M = 32             23.8          17.6   21.3
+//   M = 2048                        186.8  148.2  134.0
 double thousands(int64_t K) { return (double)K / 1024.0; }
-// Blocks of 16 weight rows, one for each workgroup of the chip's first turn.
-bool decode_one(int64_t parts, int64_t M, int64_t N, int64_t K) {
-  return parts * ((N + 15) / 16) <= 256 * mxfp8::fp4_decode_per_cu(M, K);
+// One block of 16 weight rows for each decode workgroup.
+bool decode_one(bool experts, int64_t parts, int64_t M, int64_t N, int64_t K) {
+  return parts * ((N + 15) / 16) <= 256 * mxfp8::fp4_decode_per_cu(experts, M, K);
 }
 double decode_us(int64_t M, int64_t N, int64_t K) {
-  const double t = std::max(1.0, (double)N / 4096.0), m = (double)M;
-  if (decode_one(1, M, N, K))
-    return 4.2 + 0.1 * (t - 1.0) + t * thousands(K) * (0.42 + 0.04 * m + (M > 16 ? 0.52 : 0.0));
-  return 3.6 + (M > 16 ? 3.5 : 0.0) + 0.115e-6 * (double)N * (double)K * (1.0 + 0.014 * m);   // (bytes at 4.6 TB/s)
+  const double k = thousands(K), m = (double)M, t = std::max(1.0, (double)N / 4096.0), w = k * (double)N / 16384.0;
+  if (decode_one(false, 1, M, N, K))
+    return M > 16 ? 3.1 + 0.058 * m + k * (0.11 + (K > 2048 ? 0.0275 : 0.0175) * m)
+                  : 2.7 + 0.055 * m + k * (0.25 + 0.018 * m) + (t - 1.0) * (0.24 + 0.02 * k * m);
+  return M > 16 ? 4.4 + 0.07 * m + w * (0.42 + 0.016 * m) + 0.51 * t : 3.6 + 0.13 * m + 1.54 * w - 0.31 * t;
 }
 double mid_us(int64_t M, int64_t N, int64_t K) {
   const double k = thousands(K), t = std::ceil((double)N / 4096.0);
-  if (M <= 32) return 5.4 + t * std::max(2.6, 0.84 + 0.54 * k);
-  if (M <= 64) return 5.1 + t * std::max(4.0, 1.4 + 0.77 * k);
-  return 5.2 + t * std::max(3.1, 1.8 + 1.29 * k);
+  if (M <= 32) return 4.3 + t * std::max(2.5, 0.7 + 0.54 * k);
+  if (M <= 64) return 4.1 + t * std::max(3.9, 1.3 + 0.77 * k);
+  return 4.1 + t * std::max(3.0, 1.7 + 1.29 * k);
 }
 double tile_us(int nt, int mt, int64_t M, int64_t N, int64_t K) {
   const double k = thousands(K), q = k * (double)M / 1024.0;   // q: the quantizer's share
   const double r = (double)((M + mt - 1) / mt * ((N + nt - 1) / nt)) / 256.0;   // rounds of the chip
   if (nt == 256)
-    return r <= 1.0 ? 13.2 + 4.4 * k + r * (1.3 + 2.6 * k) + 0.33 * q
-                    : 6.5 - 0.07 * k + std::ceil(r) * (7.7 + 6.35 * k) + 0.47 * q;
+    return r <= 1.0 ? 11.9 + 4.48 * k + r * (1.8 + 2.28 * k) + 0.41 * q
+                    : 9.2 - 0.8 * k + std::ceil(r) * (6.1 + 6.37 * k) + 0.62 * q;
   if (mt == 128)
-    return r <= 1.0 ? 8.9 + 1.53 * k + r * (0.9 + 0.4 * k) + 0.44 * q
-                    : 8.3 + 0.45 * k + r * (1.3 + 1.93 * k) + 0.36 * q;
-  return r <= 1.0 ? 8.2 + 1.12 * k + r * (0.36 + 0.35 * k) + 0.41 * q : 7.9 + 0.12 * k + r * (0.85 + 1.32 * k) + 0.36 * q;
+    return r <= 1.0 ? 7.7 + 1.48 * k + r * (0.4 + 0.68 * k) + 0.5 * q : 7.1 + 0.82 * k + r * (1.3 + 1.85 * k) + 0.42 * q;
+  return r <= 1.0 ? 7.1 + 1.06 * k + 0.7 * r * k + 0.36 * q : 6.7 + 0.49 * k + r * (0.85 + 1.28 * k) + 0.43 * q;
 }
 // (Past one round and K 1024 their LDS holds one workgroup per compute unit:
 // more than twice the time of two launches.)
 bool can_fuse(int64_t tiles, int64_t K) { return K <= mxfp8::kFp4FusedMaxK && (K <= 1024 || tiles <= 256); }
 double fused_us(int64_t M, int64_t N, int64_t K) {
   const double k = thousands(K), r = (double)((M + 63) / 64 * ((N + 127) / 128)) / 256.0;
-  return r <= 1.0 ? 5.8 + k * (1.5 + 0.037 * (double)std::min<int64_t>(64, M)) + r * (0.7 + 0.25 * k)
-                  : 5.9 + r * (1.2 + 3.75 * k);
+  return r <= 1.0 ? 4.8 + k * (1.46 + 0.038 * (double)std::min<int64_t>(64, M)) + r * (0.4 + 0.35 * k)
+                  : 5.3 + r * (1.2 + 3.76 * k);
 }
 
 // The GEMM on packed activations: nt == 16 is the 16-row form.
@@ -200,7 +201,7 @@ ExpertsForm experts_form(int64_t R, int64_t N, int64_t K, int64_t E) {
     const int64_t cols = (N + 127) / 128, most = (R / 64 + std::min(E, R)) * cols;   // (row tiles: one per expert is partial)
     const double two = 8.1 + 2.05 * k + 0.05 * work;
     const double td = !can_decode || rows > 8.0                  ? 1e30
-                      : decode_one(std::min(E, R), 1, N, K) ? 4.3 + 0.15 * work * (1.0 + rows / 8.0)
+                      : decode_one(true, std::min(E, R), 0, N, K) ? 4.3 + 0.15 * work * (1.0 + rows / 8.0)
                                                             : 6.5 + 0.07 * work * (1.0 + rows / 7.0);
     const double tf = !can_fuse(std::min(E, R) * cols, K) ? 1e30
                       : most <= 256                       ? 6.3 + k * (2.0 + 0.037 * std::min(64.0, rows))

@@ -3,18 +3,20 @@
 // inside.
 //
 // Bound by the weight's way from HBM, and at small weights by the launch and
-// the chain of dependent loads.  One workgroup owns 16 weight rows over the
-// whole K, each of its 16 waves a run of 128-K steps; the 16 partial sums are
-// added through LDS in K order.  A lane of the 4-bit 16x16x128 MFMA holds K
-// [32g, 32g + 32) of its row, which is one MX block: lane (i, g) loads the 64
-// bytes of that block of row i, finds its largest magnitude and converts it by
-// itself, with no exchange between lanes and no staging.  (1 x 4096 x 4096: 4.8
-// us in a graph of such calls, of which about 2.5 are the launch; 8 rows of eight
-// experts, 1536 x 2048: 8.0 us, 1.7 TB/s.  The 16-row form below, 32 x 16384 x
-// 8192: 24.8 us with the quantizer, 2.9 TB/s.)
+// the chain of dependent loads.  One workgroup owns blocks of 16 weight rows over
+// the whole K, each of its waves (16 where K is long) a run of 128-K steps; the
+// partial sums are added through LDS in K order.  A lane of the 4-bit 16x16x128
+// MFMA holds K [32g, 32g + 32) of its row, one MX block, but 64 bytes per lane
+// would touch a cache line per four lanes: the rows are read and quantized
+// sixteen lanes to a row's 256 bytes, and the codes, a quarter of that, change
+// lanes through LDS (16 x 4096 x 4096: 6.2 us; each lane its own block 8.5; 1 row
+// 4.3 and 4.5).  In a graph of such calls 1 x 4096 x 4096 takes 4.0 us, of which
+// about 2.8 are the launch; 1 x 16384 x 8192 14.6, 4.9 TB/s; one token's eight
+// experts, 1536 x 2048, 7.4, 1.8 TB/s.  The 16-row form below, 32 x 16384 x 8192:
+// 23.8 us with the quantizer, 3.0 TB/s.
 //
-// Experts: workgroup (n, j) takes weight rows 16 n .. of the j-th expert that
-// has rows, and all of those, 16 at a time, against the weight it holds.
+// Experts: the j-th run of workgroups has the j-th expert that has rows, and all
+// of those, 16 at a time.
 #include <algorithm>
 
 #include "fp4.hpp"
@@ -79,10 +81,11 @@ __device__ inline void store4(const DecodeArgs& p, const v4f& v, const float* bv
 // for such with a run of blocks, that many in flight, where a turn of the chip does
 // not hold all blocks: the rows are quantized once for the run, and the weight
 // streams while sums are joined (16 rows, 16384 x 8192: 22 us, one block each 44; 1
-// row 17 and 25; but 1 row, 4096 x 4096, 7.2 and 5.7: more registers, later rows).
+// row 17 and 25; but 1 row, 4096 x 4096, 7.2 and 5.7: more registers, later rows.
+// All four before the rows were read sixteen lanes to a row).
 template <int kWaves, int kSteps, int kGroups, int kDepth, bool kExperts>
-__global__ __launch_bounds__(64 * kWaves, kDepth == 1 ? 1 : 4) void gemm_fp4_decode_kernel(DecodeArgs p) {
-  __shared__ v4f red[kDepth == 1 ? 1 : 2][kGroups][kWaves * 64];
+__global__ __launch_bounds__(64 * kWaves, kDepth > 1 || kSteps > 2 || kGroups > 1 ? 4 : 7) void gemm_fp4_decode_kernel(DecodeArgs p) {
+  __shared__ v4f red[2][kGroups][kWaves * 64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i = lane & 15, g = lane >> 4;
@@ -154,38 +157,58 @@ __global__ __launch_bounds__(64 * kWaves, kDepth == 1 ? 1 : 4) void gemm_fp4_dec
       f.bias[0] = f.bias[1] = 0u;
     }
   };
-  // 16 kGroups rows from m0 on, quantized: lane (i, g) holds block g of row m0 + i.
-  // (A step past the wave's run, and a row past the last, are zeros.)
+  // 16 kGroups rows from m0 on, quantized: lane (i, g) ends with block g of row m0
+  // + i.  Sixteen lanes read the 256 bytes of a row's step, and the codes of 16
+  // rows go through this wave's part of `red` (a wave's LDS accesses run in their
+  // order).  A step past the wave's run is zeros; of rows past the last, four at a
+  // time, what was in LDS stays (their columns are not stored).
   int xq[kGroups][kSteps][4], xs[kGroups][kSteps];
+  constexpr int kPart = kDepth > 1 && kSteps > 2 ? 2 : kSteps;   // steps at a time (registers)
   auto load_rows = [&](int m0) {
-    uint4 v[kGroups][kSteps][4];
+    const int l = lane & 15, rr = lane >> 4;
+    int mine[kGroups];                       // the x row of sorted row m0 + 16 t + i
+    if constexpr (kExperts) {
 #pragma unroll
-    for (int t = 0; t < kGroups; ++t) {
-      const int m = m0 + 16 * t + i;
-      const bool in = m < row_end;
-      int64_t row = in ? m : 0;
-      if constexpr (kExperts) {
-        if (p.slots != nullptr && in) row = min((uint32_t)p.slots[m] / (uint32_t)p.topk, (uint32_t)p.x_rows - 1u);
-      }
-      const uint16_t* xr = p.x + row * p.ldx + (int64_t)kb * 128 + g * 32;
-#pragma unroll
-      for (int u = 0; u < kSteps; ++u)
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          v[t][u][c] =
-              in && u < nsteps ? *reinterpret_cast<const uint4*>(xr + u * 128 + c * 8) : make_uint4(0u, 0u, 0u, 0u);
+      for (int t = 0; t < kGroups; ++t)
+        if (p.slots != nullptr)
+          mine[t] = (int)min((uint32_t)p.slots[min(m0 + 16 * t + i, row_end - 1)] / (uint32_t)p.topk, (uint32_t)p.x_rows - 1u);
     }
+    uint8_t* const stage = reinterpret_cast<uint8_t*>(&red[0][0][wave * 64]);
+    uint8_t* const scales = reinterpret_cast<uint8_t*>(&red[1][0][wave * 64]);
 #pragma unroll
-    for (int t = 0; t < kGroups; ++t)
+    for (int u0 = 0; u0 < kSteps; u0 += kPart) {
+      uint4 v[kGroups][kPart][4];
 #pragma unroll
-      for (int u = 0; u < kSteps; ++u) {
-        const uint4(&x)[4] = v[t][u];
-        const uint32_t sb = fp4_scale_byte(max(max(fp4_absmax8(x[0]), fp4_absmax8(x[1])), max(fp4_absmax8(x[2]), fp4_absmax8(x[3]))));
-        const float scale = fp4_scale_value(sb);
+      for (int t = 0; t < kGroups; ++t)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) xq[t][u][c] = (int)cvt8_fp4(x[c], scale);
-        xs[t][u] = (int)sb;
-      }
+        for (int r = 0; r < 4; ++r) {
+          if (m0 + 16 * t + 4 * r >= row_end) break;
+          const bool in = m0 + 16 * t + 4 * r + rr < row_end;
+          const int64_t row = kExperts && p.slots != nullptr ? __shfl(mine[t], 4 * r + rr) : m0 + 16 * t + 4 * r + rr;
+          const uint16_t* xr = p.x + row * p.ldx + (int64_t)(kb + u0) * 128 + l * 8;
+#pragma unroll
+          for (int u = 0; u < kPart; ++u)
+            v[t][u][r] = in && u0 + u < nsteps ? *reinterpret_cast<const uint4*>(xr + u * 128) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+      for (int t = 0; t < kGroups; ++t)
+#pragma unroll
+        for (int u = 0; u < kPart; ++u) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if (m0 + 16 * t + 4 * r >= row_end) break;
+            const uint32_t sb = fp4_scale_byte(quad_max(fp4_absmax8(v[t][u][r])));
+            reinterpret_cast<uint32_t*>(stage)[r * 64 + lane] = cvt8_fp4(v[t][u][r], fp4_scale_value(sb));
+            if ((l & 3) == 0) scales[(4 * r + rr) * 4 + (l >> 2)] = (uint8_t)sb;
+          }
+          const uint4 q = reinterpret_cast<const uint4*>(stage)[i * 4 + g];
+          xq[t][u0 + u][0] = (int)q.x;
+          xq[t][u0 + u][1] = (int)q.y;
+          xq[t][u0 + u][2] = (int)q.z;
+          xq[t][u0 + u][3] = (int)q.w;
+          xs[t][u0 + u] = scales[i * 4 + g];
+        }
+    }
   };
 
   // The weight first: with gathered rows the others wait for their indices.
@@ -323,7 +346,7 @@ int decode(DecodeArgs p, int64_t parts, hipStream_t stream) {
   };
   // Workgroups with runs have 16 waves per compute unit.
   auto pick = [&](auto one, auto many, int waves) {
-    if (blocks * parts <= cus * fp4_decode_per_cu(kExperts ? 1 : p.M, p.K)) return go(one, waves, blocks);
+    if (blocks * parts <= cus * fp4_decode_per_cu(kExperts, p.M, p.K)) return go(one, waves, blocks);
     return go(many, waves, std::min(blocks, (cus * (16 / waves) + parts - 1) / parts));
   };
   static_assert(kFp4DecodeMaxK == 16 * 4 * 128, "a wave owns at most four steps");
@@ -335,8 +358,8 @@ int decode(DecodeArgs p, int64_t parts, hipStream_t stream) {
     }
   }
   constexpr bool X = kExperts;
-  if (KS <= 8) return pick(gemm_fp4_decode_kernel<4, 2, 1, 1, X>, gemm_fp4_decode_kernel<4, 2, 1, 4, X>, 4);
-  if (KS <= 16) return pick(gemm_fp4_decode_kernel<8, 2, 1, 1, X>, gemm_fp4_decode_kernel<8, 2, 1, 4, X>, 8);
+  if (KS <= 8) return pick(gemm_fp4_decode_kernel<4, 2, 1, 1, X>, gemm_fp4_decode_kernel<4, 2, 1, 3, X>, 4);
+  if (KS <= 16) return pick(gemm_fp4_decode_kernel<8, 2, 1, 1, X>, gemm_fp4_decode_kernel<8, 2, 1, 3, X>, 8);
   if (KS <= 32) return pick(gemm_fp4_decode_kernel<16, 2, 1, 1, X>, gemm_fp4_decode_kernel<16, 2, 1, 3, X>, 16);
   return pick(gemm_fp4_decode_kernel<16, 4, 1, 1, X>, gemm_fp4_decode_kernel<16, 4, 1, 2, X>, 16);
 }

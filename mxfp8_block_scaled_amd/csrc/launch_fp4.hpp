@@ -23,10 +23,12 @@ int launch_quantize_rows_fp4(const void* x, int64_t M, int64_t K, int64_t ldx, v
 // against a packed MXFP4 weight; K <= kFp4DecodeMaxK.
 constexpr int64_t kFp4DecodeMaxK = 8192;
 inline int64_t fp4_decode_max_m(int64_t K) { return K <= 4096 ? 32 : K <= kFp4DecodeMaxK ? 16 : 0; }
-// Its workgroups of 16 weight rows each that a compute unit holds (by registers;
-// more than 16 rows: by what was faster).  Where those are not enough, each takes
-// a run of blocks.
-inline int64_t fp4_decode_per_cu(int64_t M, int64_t K) { return M > 16 ? 1 : K <= 1024 ? 8 : K <= 2048 ? 4 : K <= 4096 ? 2 : 1; }
+// Its workgroups of 16 weight rows each that a compute unit holds.  Where those
+// are not enough, each takes a run of blocks.  (The experts': of their number at
+// most, not all of which have rows.)
+inline int64_t fp4_decode_per_cu(bool experts, int64_t M, int64_t K) {
+  return M > 16 || K > 2048 ? 1 : K > 1024 ? (experts ? 4 : 3) : (experts ? 8 : 7);
+}
 int launch_gemm_fp4_decode(const void* x, int64_t ldx, int64_t M, int64_t K, const void* wp, const void* wsp,
                            int64_t N, const void* bias, void* y, int64_t ldy, hipStream_t stream);
 
