@@ -192,8 +192,7 @@ ExpertsForm experts_form(int64_t R, int64_t N, int64_t K, int64_t E) {
   const int force = g_force.load(std::memory_order_relaxed);
   const double X = (double)std::max<int64_t>(1, std::min(E, R)), rows = (double)R / X;
   const double work = 1e-6 * X * (double)N * (double)K;
-  const bool can_decode = K <= mxfp8::kFp4DecodeMaxK && std::min(E, R) * ((N + 15) / 16) * 1024 <= kMaxThreads,
-             fused = K <= mxfp8::kFp4FusedMaxK;
+  const bool can_decode = K <= mxfp8::kFp4DecodeMaxK, fused = K <= mxfp8::kFp4FusedMaxK;
   if (force == 1 && can_decode) return {kDecode, {}};
   if (force == 2 && fused) return {kFusedTiles, {}};
   if (force == 0) {

@@ -201,12 +201,14 @@ __global__ __launch_bounds__(64 * kWaves, kDepth > 1 || kSteps > 2 || kGroups > 
             reinterpret_cast<uint32_t*>(stage)[r * 64 + lane] = cvt8_fp4(v[t][u][r], fp4_scale_value(sb));
             if ((l & 3) == 0) scales[(4 * r + rr) * 4 + (l >> 2)] = (uint8_t)sb;
           }
+          asm volatile("" ::: "memory");
           const uint4 q = reinterpret_cast<const uint4*>(stage)[i * 4 + g];
           xq[t][u0 + u][0] = (int)q.x;
           xq[t][u0 + u][1] = (int)q.y;
           xq[t][u0 + u][2] = (int)q.z;
           xq[t][u0 + u][3] = (int)q.w;
           xs[t][u0 + u] = scales[i * 4 + g];
+          asm volatile("" ::: "memory");
         }
     }
   };

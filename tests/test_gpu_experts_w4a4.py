@@ -55,6 +55,14 @@ def test_many_tiles_per_workgroup(form, K):
     case(1500, 4, 24, 1100, K, True, form, drop=0.1, seed=K)
 
 
+@pytest.mark.parametrize("T,topk,E,N,K", [(100, 8, 40, 901, 512), (40, 4, 40, 420, 1536), (30, 3, 8, 530, 4096),
+                                          (20, 2, 3, 1401, 8192)])
+@pytest.mark.parametrize("gather", [True, False])
+def test_runs_of_weight_blocks(T, topk, E, N, K, gather):
+    """More blocks of 16 weight rows than the decode form's workgroups, experts with more rows than 16, and none."""
+    case(T, topk, E, N, K, gather, 1, drop=0.2, seed=K)
+
+
 @pytest.mark.parametrize("form", FORMS)
 def test_unusual_orders(form):
     """One expert for all, none at all, the last expert only, the same expert twice in a token."""

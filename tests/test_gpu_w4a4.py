@@ -47,6 +47,13 @@ def test_few_rows(form, M, N, K):
     case(M, N, K, form=form, seed=M + N)
 
 
+@pytest.mark.parametrize("M,N,K", [(5, 30001, 512), (16, 13001, 2048), (9, 4500, 4096), (3, 4203, 8192), (20, 4401, 1024),
+                                   (32, 4111, 4096)])
+def test_runs_of_weight_blocks(M, N, K):
+    """More blocks of 16 weight rows than the decode form's workgroups."""
+    case(M, N, K, form=1, seed=M)
+
+
 @pytest.mark.parametrize("M,N,K", [(33, 130, 256), (64, 200, 768), (65, 257, 2048), (100, 64, 4352), (128, 131, 8192),
                                    (50, 40, 12544), (128, 16, 20480)])
 def test_mid_form(M, N, K):
