@@ -1021,7 +1021,8 @@ def linear_w4a4(x, pw, bias=None, out=None):
     deq4(W).T + bias)``, x bf16 ``[..., K]`` quantized to MXFP4 on the fly, pw
     a PreparedWeightFP4 (the weight ``linear`` multiplies with 8-bit
     activations), bias bf16 ``[N]`` or None.  Returns bf16 ``[..., N]``; ``out``:
-    bf16 ``[M, N]`` to write into, M the rows of x.  No gradients."""
+    bf16 ``[M, N]`` to write into, M the rows of x, not overlapping x.  No
+    gradients."""
     if not isinstance(pw, PreparedWeightFP4):
         raise ValueError("linear_w4a4 takes an MXFP4 weight (prepare_weight_fp4)")
     x2 = _rows(x, "x")
