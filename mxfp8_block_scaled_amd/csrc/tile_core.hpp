@@ -893,7 +893,8 @@ struct Job16 {
 };
 
 // Resource over the bias of columns [col0, col0 + 256) that exist (none if
-// bias is null): loads past the end read zeros.
+// bias is null): loads past the end read zeros, and so does the word that an
+// odd N's last value shares with what is behind it (bias_init16 reads that one).
 __device__ inline i4v bias_rsrc(const uint16_t* bias, int col0, int N) {
   if (bias == nullptr) return buffer_rsrc(nullptr, 0);
   const int valid = max(0, min(256, N - col0));
@@ -902,10 +903,20 @@ __device__ inline i4v bias_rsrc(const uint16_t* bias, int col0, int N) {
 
 // The accumulators of a tile start at its bias (fp32, exact from bf16), so
 // that the MFMAs add the products to it and the epilogue only rounds: this
-// wave's 128 bias values are at bias_slot (zeros past N or without a bias);
-// acc[a][k][e] is column 16 a + 4 lg + e of the wave's 128.
-__device__ __forceinline__ void bias_init16(v4f (&acc)[8][8], const uint8_t* bias_slot) {
-  const int lg = (threadIdx.x & 63) >> 4;
+// wave's 128 bias values, of columns nw .., are at bias_slot (zeros past N or
+// without a bias); acc[a][k][e] is column 16 a + 4 lg + e of the wave's 128.
+// The last of an odd N comes by a load of its own (which waits for the copies in
+// flight) in the wave that has it, and is put into the slot: registers for it
+// cost the loop eighty.
+__device__ __forceinline__ void bias_init16(v4f (&acc)[8][8], uint8_t* bias_slot, const uint16_t* __restrict__ bias,
+                                            int nw, int N) {
+  const int lane = threadIdx.x & 63, lg = lane >> 4;
+  const int last = N - 1 - nw;
+  if (bias != nullptr && (N & 1) != 0 && last >= 0 && last < 128) {
+    if (lane == 0) *reinterpret_cast<uint16_t*>(bias_slot + 2 * last) = bias[N - 1];
+    // (a wave's LDS accesses run in their order)
+    asm volatile("" ::: "memory");
+  }
 #pragma unroll
   for (int a = 0; a < 8; ++a) {
     const uint2 w = *reinterpret_cast<const uint2*>(bias_slot + (16 * a + 4 * lg) * 2);
@@ -983,8 +994,8 @@ __device__ __forceinline__ bool epi16(uint8_t* epi, const v4f (&acc)[8][8], uint
 //  * tile_start(b_next) runs at the start of each tile with the index of the
 //    workgroup's next tile (may be >= total); vector memory operations it
 //    issues are complete by the tile's first barrier after its first wait.
-//  * kAccInit: acc_init(acc, slot) sets the tile's accumulators from its side
-//    data (this wave's own copies, complete when it runs); otherwise they
+//  * kAccInit: acc_init(acc, job, slot) sets the tile's accumulators from its
+//    side data (this wave's own copies, complete when it runs); otherwise they
 //    start at zero.
 //  * kCarry: the last step of a tile reads the next tile's first fragments
 //    (held in registers through the epilogue); otherwise they are read from
@@ -1184,7 +1195,7 @@ __device__ __forceinline__ void persistent16_run(uint8_t* st0, uint8_t* st1, uin
       if (vm_extra == 64) wait_vmcnt<63>();
       else if (vm_extra == 32) wait_vmcnt<32>();
       else wait_vmcnt<0>();
-      acc_init(acc, side_lds + buf * kSideSlot);
+      acc_init(acc, cur, side_lds + buf * kSideSlot);
     } else {
 #pragma unroll
       for (int a = 0; a < 8; ++a)
@@ -1253,7 +1264,10 @@ __device__ __forceinline__ void persistent16(uint8_t* st0, uint8_t* st1, uint8_t
       [&](const Job16& j) { return BufSrc(j.wga, j.wgb, j.xga, j.xgb, j.swa, j.swb, j.sxa, j.sxb, KS, KS); },
       [&](const Job16& j) { return bias_rsrc(bias, j.col0, N); },
       [&](i4v r, uint8_t* slot) { b2l_4((uint32_t)(wn * 256 + lane * 4), r, 0u, slot + wave * 256); },
-      [&](int) {}, [&](v4f (&acc)[8][8], const uint8_t* slot) { bias_init16(acc, slot + wave * 256); },
+      [&](int) {},
+      [&](v4f (&acc)[8][8], const Job16& j, uint8_t* slot) {
+        bias_init16(acc, slot + wave * 256, bias, j.col0 + wn * 128, N);
+      },
       [&](const v4f (&acc)[8][8], const Job16& j, const uint8_t*) {
         return epi16(epi, acc, y, ldy, j.row0, M, j.col0, N, vec_store) ? 32 : 0;
       });
