@@ -1291,10 +1291,16 @@ def moe_sort(ids, E):
 
 
 def _matrix(x, rows, name):
-    """fp32 or bf16 ``[rows, H]`` with contiguous rows that do not overlap."""
+    """Checks that x is fp32 or bf16 ``[rows, H]`` on the GPU."""
     if x.dtype not in _DTYPES or x.dim() != 2 or x.shape[0] != rows:
         raise ValueError(f"{name} must be float32 or bfloat16 [{rows}, H], got {x.dtype} {tuple(x.shape)}")
     _require_cuda(x, name)
+
+
+def _laid_out(x):
+    """x with contiguous rows that do not overlap.  Called inside of the autograd
+    nodes: a copy made before them would be a node of its own, and hide its
+    leaf from ``_mark_leaves`` and ``_check_capture``."""
     if x.stride(1) != 1 or x.stride(0) < x.shape[1]:
         x = x.clone(memory_format=torch.contiguous_format)
     return x
@@ -1303,14 +1309,6 @@ def _matrix(x, rows, name):
 def _require_order(order):
     if not isinstance(order, MoEOrder):
         raise ValueError("order must be a MoEOrder (moe_sort)")
-
-
-def _weights(weights, order):
-    if weights is None:
-        return None
-    if weights.dtype != torch.float32 or weights.shape != order.rows.shape:
-        raise ValueError(f"weights must be float32 [{order.T}, {order.topk}]")
-    return weights if weights.is_contiguous() else weights.contiguous()
 
 
 def _permute(x, order):
@@ -1345,20 +1343,20 @@ class _MoEPermute(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, order):
         ctx.order = order
-        return _permute(x, order)
+        return _permute(_laid_out(x), order)
 
     @_backward_once
     def backward(ctx, dxs):
         if torch.cuda.is_current_stream_capturing():
             _check_capture(ctx, _stream(dxs.device), True)
-        order = ctx.order
-        return _unpermute(_matrix(dxs, order.T * order.topk, "dxs"), order, None), None
+        return _unpermute(_laid_out(dxs), ctx.order, None), None
 
 
 class _MoEUnpermute(torch.autograd.Function):
     @staticmethod
     def forward(ctx, ys, weights, order):
         ctx.order = order
+        ys, weights = _laid_out(ys), None if weights is None else weights.contiguous()
         ctx.save_for_backward(ys if ctx.needs_input_grad[1] else None, weights)
         return _unpermute(ys, order, weights)
 
@@ -1370,7 +1368,7 @@ class _MoEUnpermute(torch.autograd.Function):
         need_ys, need_w, _ = ctx.needs_input_grad
         ys, weights = ctx.saved_tensors
         order = ctx.order
-        dy = _matrix(dy, order.T, "dy")
+        dy = _laid_out(dy)
         H = dy.shape[1]
         with _on(dy.device):
             dys = dy.new_empty(order.T * order.topk, H) if need_ys else None
@@ -1388,10 +1386,10 @@ def moe_permute(x, order):
     slots without an expert.  Differentiable; the gradient adds a token's rows
     in fp32, in slot order.  In captured graphs as ``linear_b128``."""
     _require_order(order)
-    x = _matrix(x, order.T, "x")
+    _matrix(x, order.T, "x")
     _same_device(x, order.rows)
     if not (torch.is_grad_enabled() and x.requires_grad):
-        return _permute(x, order)
+        return _permute(_laid_out(x), order)
     stream = _stream(x.device)
     _mark_leaves_before((x,), stream)
     xs = _MoEPermute.apply(x, order)
@@ -1407,11 +1405,12 @@ def moe_unpermute(ys, order, weights=None):
     with respect to ys and weights (0 for slots without an expert).  In captured
     graphs as ``linear_b128``."""
     _require_order(order)
-    ys = _matrix(ys, order.T * order.topk, "ys")
-    weights = _weights(weights, order)
+    _matrix(ys, order.T * order.topk, "ys")
+    if weights is not None and (weights.dtype != torch.float32 or weights.shape != order.rows.shape):
+        raise ValueError(f"weights must be float32 [{order.T}, {order.topk}]")
     _same_device(ys, order.rows, weights)
     if not torch.is_grad_enabled() or not (ys.requires_grad or (weights is not None and weights.requires_grad)):
-        return _unpermute(ys, order, weights)
+        return _unpermute(_laid_out(ys), order, None if weights is None else weights.contiguous())
     stream = _stream(ys.device)
     _mark_leaves_before((ys, weights), stream)
     y = _MoEUnpermute.apply(ys, weights, order)
