@@ -1248,12 +1248,32 @@ class MoEOrder:
     within one by slot; slots without an expert come behind all others.
     ``slots`` int32 ``[T * topk]``: the slot of each row.  ``offsets`` int32
     ``[E + 1]``: the first row of each expert, and the number of rows that have
-    one."""
+    one.  All contiguous and on one device.  ``moe_sort`` makes it; built from
+    tensors of one's own these are checked, but what they hold is not (values
+    that no sort gives make wrong or unwritten rows)."""
 
     def __init__(self, rows, slots, offsets):
+        for t, name, dim in ((rows, "rows", 2), (slots, "slots", 1), (offsets, "offsets", 1)):
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous int32 with {dim} dimension{'s'[:dim - 1]}")
+        if slots.numel() != rows.numel() or offsets.numel() < 2:
+            raise ValueError(f"slots must be int32 [{rows.numel()}] and offsets int32 [E + 1], got {slots.numel()} and "
+                             f"{offsets.numel()}")
+        if not rows.device == slots.device == offsets.device:
+            raise ValueError(f"operands on {rows.device}, {slots.device} and {offsets.device}")
+        self._hold(rows, slots, offsets)
+
+    def _hold(self, rows, slots, offsets):
         self.rows, self.slots, self.offsets = rows, slots, offsets
         self.T, self.topk = rows.shape
         self.E = offsets.numel() - 1
+
+    @classmethod
+    def _of(cls, *parts):
+        """Of tensors made here, without the checks."""
+        order = cls.__new__(cls)
+        order._hold(*parts)
+        return order
 
     @property
     def _kept(self):
@@ -1287,7 +1307,7 @@ def moe_sort(ids, E):
         ws = _scratch(need, ids)
         _check(lib().mxfp8_moe_sort(_ptr(ids), ids.element_size(), R, E, _ptr(rows), _ptr(slots), _ptr(offsets),
                                     _ptr(ws), need, _stream(ids.device)), "mxfp8_moe_sort")
-    return MoEOrder(rows, slots, offsets)
+    return MoEOrder._of(rows, slots, offsets)
 
 
 def _matrix(x, rows, name):
