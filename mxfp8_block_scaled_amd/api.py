@@ -1275,6 +1275,12 @@ class MoEOrder:
         order._hold(*parts)
         return order
 
+    def _versions(self):
+        """Of the tensors that gradients read (None: inference tensors have none)."""
+        if self.rows.is_inference() or self.offsets.is_inference():
+            return None
+        return self.rows._version, self.offsets._version
+
     @property
     def _kept(self):
         """Address of the number of rows with an expert."""
@@ -1359,23 +1365,38 @@ def _backward_once(backward):
     return staticmethod(lambda ctx, d: once(ctx, d) if torch.is_grad_enabled() else backward(ctx, d))
 
 
+def _keep_order(ctx, order):
+    """Keeps for the backward pass what the order holds now.  (Not by
+    save_for_backward: permute's gradient needs no retained graph for a second
+    pass.)"""
+    ctx.order = MoEOrder._of(order.rows, order.slots, order.offsets)
+    ctx.versions = order._versions()
+
+
+def _kept_order(ctx):
+    if ctx.order._versions() != ctx.versions:
+        raise RuntimeError("the rows or offsets of an order have been modified by an inplace operation between the "
+                           "forward and the backward pass")
+    return ctx.order
+
+
 class _MoEPermute(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, order):
-        ctx.order = order
+        _keep_order(ctx, order)
         return _permute(_laid_out(x), order)
 
     @_backward_once
     def backward(ctx, dxs):
         if torch.cuda.is_current_stream_capturing():
             _check_capture(ctx, _stream(dxs.device), True)
-        return _unpermute(_laid_out(dxs), ctx.order, None), None
+        return _unpermute(_laid_out(dxs), _kept_order(ctx), None), None
 
 
 class _MoEUnpermute(torch.autograd.Function):
     @staticmethod
     def forward(ctx, ys, weights, order):
-        ctx.order = order
+        _keep_order(ctx, order)
         ys, weights = _laid_out(ys), None if weights is None else weights.contiguous()
         ctx.save_for_backward(ys if ctx.needs_input_grad[1] else None, weights)
         return _unpermute(ys, order, weights)
@@ -1387,7 +1408,7 @@ class _MoEUnpermute(torch.autograd.Function):
             _check_capture(ctx, stream, True)
         need_ys, need_w, _ = ctx.needs_input_grad
         ys, weights = ctx.saved_tensors
-        order = ctx.order
+        order = _kept_order(ctx)
         dy = _laid_out(dy)
         H = dy.shape[1]
         with _on(dy.device):
