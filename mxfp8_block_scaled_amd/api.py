@@ -19,6 +19,7 @@ import os
 import threading
 
 import torch
+from torch.autograd import forward_ad
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libmxfp8.so")
@@ -886,6 +887,18 @@ def _check_capture(node, stream, capturing):
                                "those leaves to this operator first")
 
 
+def _reverse_only(name, *operands):
+    """Refuses operands with a tangent in a call that goes past its node, since no
+    reverse gradient is asked of it, and would lose them.  (The nodes refuse
+    them by themselves.)"""
+    # (outside of a level no tensor has one; where torch does not say, each is asked)
+    if getattr(forward_ad, "_current_level", 0) < 0:
+        return
+    for t in operands:
+        if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            raise RuntimeError(f"{name} is differentiable in reverse mode only")
+
+
 class _LinearB128(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, bias):
@@ -947,7 +960,7 @@ def linear_b128(x, w, bias=None):
     else holds it (a data-parallel wrapper: make it on the side stream).  So is
     one that another operator made first, on a stream not known here: until a
     backward() runs it on a side stream, or, in the capture itself, unless this
-    operator is the first to be given the leaf."""
+    operator is the first to be given the leaf.  Reverse mode only."""
     for t, name in ((x, "x"), (w, "w")) + (((bias, "bias"),) if bias is not None else ()):
         if t.dtype != torch.bfloat16:
             raise ValueError(f"{name} must be bfloat16, got {t.dtype}")
@@ -957,6 +970,7 @@ def linear_b128(x, w, bias=None):
     _same_device(x, w, bias)
     if not torch.is_grad_enabled() or not (x.requires_grad or w.requires_grad or
                                            (bias is not None and bias.requires_grad)):
+        _reverse_only("linear_b128", x, w, bias)
         return _linear_b128_forward(x, w, bias, 0)[0]
     stream = _stream(x.device)
     _mark_leaves_before((x, w, bias), stream)
@@ -1227,7 +1241,7 @@ def moe_balance_loss(logits, topk, valid=None, coef=1e-2, z_coef=0.0):
     """``moe_balance`` for autograd: ``(loss, counts)``, the loss
     differentiable with respect to ``logits``.  ``counts`` are the caller's to
     change (an all-reduce over ranks, say): the gradient does not read them.
-    In captured graphs as ``linear_b128``."""
+    In captured graphs, and in reverse mode only, as ``linear_b128``."""
     stream = _stream(logits.device) if logits.is_cuda else _LEGACY   # (moe_balance refuses the others)
     if torch.is_grad_enabled():
         _mark_leaves_before((logits,), stream)
@@ -1425,11 +1439,13 @@ def moe_permute(x, order):
     """The rows of ``x`` fp32 or bf16 ``[T, H]`` in the order of their experts:
     ``xs[order.rows[t, j]] = x[t]``, ``[T * topk, H]``, zeros in the rows of
     slots without an expert.  Differentiable; the gradient adds a token's rows
-    in fp32, in slot order.  In captured graphs as ``linear_b128``."""
+    in fp32, in slot order.  In captured graphs, and in reverse mode only, as
+    ``linear_b128``."""
     _require_order(order)
     _matrix(x, order.T, "x")
     _same_device(x, order.rows)
     if not (torch.is_grad_enabled() and x.requires_grad):
+        _reverse_only("moe_permute", x)
         return _permute(_laid_out(x), order)
     stream = _stream(x.device)
     _mark_leaves_before((x,), stream)
@@ -1444,13 +1460,14 @@ def moe_unpermute(ys, order, weights=None):
     ``[T * topk, H]`` -> ``[T, H]``, summed in fp32 in slot order and rounded
     once.  ``weights`` fp32 ``[T, topk]``, or None for all 1.  Differentiable
     with respect to ys and weights (0 for slots without an expert).  In captured
-    graphs as ``linear_b128``."""
+    graphs, and in reverse mode only, as ``linear_b128``."""
     _require_order(order)
     _matrix(ys, order.T * order.topk, "ys")
     if weights is not None and (weights.dtype != torch.float32 or weights.shape != order.rows.shape):
         raise ValueError(f"weights must be float32 [{order.T}, {order.topk}]")
     _same_device(ys, order.rows, weights)
     if not torch.is_grad_enabled() or not (ys.requires_grad or (weights is not None and weights.requires_grad)):
+        _reverse_only("moe_unpermute", ys, weights)
         return _unpermute(_laid_out(ys), order, None if weights is None else weights.contiguous())
     stream = _stream(ys.device)
     _mark_leaves_before((ys, weights), stream)
