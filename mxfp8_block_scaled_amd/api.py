@@ -1275,25 +1275,26 @@ class MoEOrder:
                              f"{offsets.numel()}")
         if not rows.device == slots.device == offsets.device:
             raise ValueError(f"operands on {rows.device}, {slots.device} and {offsets.device}")
-        self._hold(rows, slots, offsets)
-
-    def _hold(self, rows, slots, offsets):
         self.rows, self.slots, self.offsets = rows, slots, offsets
         self.T, self.topk = rows.shape
         self.E = offsets.numel() - 1
 
     @classmethod
-    def _of(cls, *parts):
+    def _of(cls, rows, slots, offsets, T, topk, E):
         """Of tensors made here, without the checks."""
         order = cls.__new__(cls)
-        order._hold(*parts)
+        order.rows, order.slots, order.offsets = rows, slots, offsets
+        order.T, order.topk, order.E = T, topk, E
         return order
 
-    def _versions(self):
-        """Of the tensors that gradients read (None: inference tensors have none)."""
-        if self.rows.is_inference() or self.offsets.is_inference():
-            return None
-        return self.rows._version, self.offsets._version
+    def _state(self):
+        """The tensors that gradients read, and their versions (inference tensors
+        have none)."""
+        rows, offsets = self.rows, self.offsets
+        try:
+            return rows, offsets, rows._version, offsets._version
+        except RuntimeError:
+            return rows, offsets, None, None
 
     @property
     def _kept(self):
@@ -1327,7 +1328,7 @@ def moe_sort(ids, E):
         ws = _scratch(need, ids)
         _check(lib().mxfp8_moe_sort(_ptr(ids), ids.element_size(), R, E, _ptr(rows), _ptr(slots), _ptr(offsets),
                                     _ptr(ws), need, _stream(ids.device)), "mxfp8_moe_sort")
-    return MoEOrder._of(rows, slots, offsets)
+    return MoEOrder._of(rows, slots, offsets, T, topk, E)
 
 
 def _matrix(x, rows, name):
@@ -1380,18 +1381,18 @@ def _backward_once(backward):
 
 
 def _keep_order(ctx, order):
-    """Keeps for the backward pass what the order holds now.  (Not by
-    save_for_backward: permute's gradient needs no retained graph for a second
-    pass.)"""
-    ctx.order = MoEOrder._of(order.rows, order.slots, order.offsets)
-    ctx.versions = order._versions()
+    """Keeps an order for the backward pass.  (Not by save_for_backward: permute's
+    gradient needs no retained graph for a second pass.)"""
+    ctx.order, ctx.state = order, order._state()
 
 
 def _kept_order(ctx):
-    if ctx.order._versions() != ctx.versions:
-        raise RuntimeError("the rows or offsets of an order have been modified by an inplace operation between the "
-                           "forward and the backward pass")
-    return ctx.order
+    order = ctx.order
+    was, now = ctx.state, order._state()
+    if now[0] is not was[0] or now[1] is not was[1] or now[2:] != was[2:]:
+        raise RuntimeError("the rows or offsets of an order have been modified by an inplace operation or replaced "
+                           "between the forward and the backward pass")
+    return order
 
 
 class _MoEPermute(torch.autograd.Function):

@@ -50,9 +50,18 @@ def test_unchanged(out):
     o = order()
     y = outputs(o)[out]
     o.slots.add_(1)                  # which no gradient reads
-    o.rows = o.rows + 1              # nor does one read what the order holds later
     y.sum().backward(retain_graph=True)
     y.sum().backward()
+
+
+@pytest.mark.parametrize("which", ["rows", "offsets"])
+@pytest.mark.parametrize("out", range(4))
+def test_replaced(which, out):
+    o = order()
+    y = outputs(o)[out]
+    setattr(o, which, getattr(o, which).clone())
+    with pytest.raises(RuntimeError, match="replaced"):
+        y.sum().backward()
 
 
 def test_permutes_gradient_needs_no_retained_graph():
