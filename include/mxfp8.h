@@ -535,8 +535,10 @@ int mxfp8_moe_balance_backward(const void* logits, int dtype, int64_t T, int64_t
  * 2^(floor(log2 amax) - 2) per 32 elements, round to nearest even, saturate
  * to +-6; a block of zeros gets byte 0.  A block with an infinity or a NaN
  * gets byte 0xFF (NaN) and makes the outputs that it enters NaN.  fp32
- * accumulation, bias (4-byte aligned) added in fp32, one rounding.  K % 256 ==
- * 0, K <= 2^24; M <= 2^30, M_pad / 16 ceil(K / 512) < 2^24, N <= 2^24.
+ * accumulation, bias added in fp32, one rounding.  The bias is 4-byte aligned
+ * and read by whole words: of an odd N the word of its last value is read whole
+ * (two bytes behind the bias, in the same aligned word; they reach no output).
+ * K % 256 == 0, K <= 2^24; M <= 2^30, M_pad / 16 ceil(K / 512) < 2^24, N <= 2^24.
  *
  * mxfp8_packed_act_fp4_bytes: host-only sizes of the packed activations (M >=
  *   1): *q_bytes = M_pad * K / 2, *s_bytes = M_pad * K / 32, M_pad =
