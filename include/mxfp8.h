@@ -538,7 +538,8 @@ int mxfp8_moe_balance_backward(const void* logits, int dtype, int64_t T, int64_t
  * accumulation, bias added in fp32, one rounding.  The bias is 4-byte aligned
  * and read by whole words: of an odd N the word of its last value is read whole
  * (two bytes behind the bias, in the same aligned word; they reach no output).
- * K % 256 == 0, K <= 2^24; M <= 2^30, M_pad / 16 ceil(K / 512) < 2^24, N <= 2^24.
+ * K % 256 == 0, K <= 2^24; M <= 2^30, M_pad / 16 ceil(K / 512) < 2^24, N <= 2^24,
+ * ceil(M / 64) ceil(N / 128) < 2^30: the size queries refuse the others, too.
  *
  * mxfp8_packed_act_fp4_bytes: host-only sizes of the packed activations (M >=
  *   1): *q_bytes = M_pad * K / 2, *s_bytes = M_pad * K / 32, M_pad =
@@ -625,12 +626,14 @@ int mxfp8_moe_unpermute_backward(const void* dy, int dtype, int64_t T, int64_t H
  * topk (x holds the tokens, x_rows topk == R).  Rows from offsets[E] on are
  * zeros.  offsets and slot_of_row as mxfp8_moe_sort left them.
  *   x_bf16 [x_rows, K] row stride ldx (ldx % 8 == 0, 16-byte aligned), y_bf16
- *   [R, N] row stride ldy; K % 256 == 0, x_rows K / 2 < 2^32, N <= 2^24
+ *   [R, N] row stride ldy; K % 256 == 0, x_rows K / 2 < 2^32, N <= 2^24,
+ *   (R / 64 + min(E, R)) ceil(N / 128) < 2^30
  *   workspace of mxfp8_moe_linear_w4a4_workspace_bytes (0: NULL is fine),
  *   256-byte aligned, without initialization
  * mxfp8_moe_prepare_experts_fp4: one-time layout of the experts' weights
  *   w_e2m1 [E, N, K/2] (16-byte aligned) and w_s_e8m0 [E, N, K/32], contiguous,
- *   into 256-byte aligned buffers of mxfp8_moe_prepared_experts_fp4_bytes.
+ *   into 256-byte aligned buffers of mxfp8_moe_prepared_experts_fp4_bytes;
+ *   N_pad K / 32 <= 2^32 - 256.
  */
 int mxfp8_moe_prepared_experts_fp4_bytes(int64_t E, int64_t N, int64_t K, size_t* w_bytes, size_t* s_bytes);
 int mxfp8_moe_prepare_experts_fp4(const void* w_e2m1, const void* w_s_e8m0, int64_t E, int64_t N, int64_t K,

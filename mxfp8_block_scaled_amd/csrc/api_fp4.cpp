@@ -30,6 +30,11 @@ size_t act_scale_bytes(int64_t M, int64_t K) { return (size_t)pad128(M) * (size_
 constexpr int64_t kMaxThreads = UINT32_MAX;
 bool act_grid_ok(int64_t M, int64_t K) { return pad128(M) / 16 * ((K + 511) / 512) * 256 <= kMaxThreads; }
 bool gemm_grid_ok(int64_t M, int64_t N) { return (M + 63) / 64 * ((N + 127) / 128) <= INT32_MAX / 2; }
+bool linear_grid_ok(int64_t M, int64_t N, int64_t K) { return act_grid_ok(M, K) && gemm_grid_ok(M, N); }
+// The pack kernels' grids: one thread per 16 bytes, one per scale pair.  Experts
+// of whole 128-row groups are packed at once where that fits.
+bool pack_at_once(int64_t E, int64_t N, int64_t K) { return N % 128 == 0 && E * N * (K / 32) <= kMaxThreads - 255; }
+bool pack_grid_ok(int64_t N, int64_t K) { return pad128(N) * (K / 32) <= kMaxThreads - 255; }
 
 // Test hook: pinned form (0: by shape).
 std::atomic<int> g_force{0};
@@ -233,7 +238,7 @@ extern "C" {
 
 int mxfp8_packed_act_fp4_bytes(int64_t M, int64_t K, size_t* q_bytes, size_t* s_bytes) {
   if (!q_bytes || !s_bytes) return MXFP8_E_NULLPTR;
-  if (M < 1 || M > kMaxRows || !summed_ok(K)) return MXFP8_E_SHAPE;
+  if (M < 1 || M > kMaxRows || !summed_ok(K) || !act_grid_ok(M, K)) return MXFP8_E_SHAPE;
   *q_bytes = act_bytes(M, K);
   *s_bytes = act_scale_bytes(M, K);
   return MXFP8_OK;
@@ -267,7 +272,7 @@ int mxfp8_gemm_packed_fp4(const void* q_packed, const void* s_packed, int64_t M,
 
 int mxfp8_linear_w4a4_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes) {
   if (!bytes) return MXFP8_E_NULLPTR;
-  if (M < 0 || M > kMaxRows || N < 1 || N > kMaxN || !summed_ok(K)) return MXFP8_E_SHAPE;
+  if (M < 0 || M > kMaxRows || N < 1 || N > kMaxN || !summed_ok(K) || !linear_grid_ok(M, N, K)) return MXFP8_E_SHAPE;
   *bytes = linear_ws(M, N, K);
   return MXFP8_OK;
 }
@@ -282,7 +287,7 @@ int mxfp8_linear_w4a4(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, con
   if (ldx < K || ldx % 8 != 0) return MXFP8_E_LD;
   if (!aligned(x_bf16, 16)) return MXFP8_E_ALIGN;
   if (int st = check_out(y_bf16, N, ldy, bias_bf16)) return st;
-  if (!act_grid_ok(M, K) || !gemm_grid_ok(M, N)) return MXFP8_E_SHAPE;
+  if (!linear_grid_ok(M, N, K)) return MXFP8_E_SHAPE;
   const size_t need = linear_ws(M, N, K);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MXFP8_E_WORKSPACE;
   if (!aligned(workspace, 256)) return MXFP8_E_ALIGN;
@@ -419,7 +424,7 @@ int mxfp8_moe_unpermute_backward(const void* dy, int dtype, int64_t T, int64_t H
 
 int mxfp8_moe_prepared_experts_fp4_bytes(int64_t E, int64_t N, int64_t K, size_t* w_bytes, size_t* s_bytes) {
   if (!w_bytes || !s_bytes) return MXFP8_E_NULLPTR;
-  if (!experts_ok(E) || N < 1 || N > kMaxN || !summed_ok(K)) return MXFP8_E_SHAPE;
+  if (!experts_ok(E) || N < 1 || N > kMaxN || !summed_ok(K) || !pack_grid_ok(N, K)) return MXFP8_E_SHAPE;
   *w_bytes = (size_t)E * act_bytes(N, K);
   *s_bytes = (size_t)E * act_scale_bytes(N, K);
   return MXFP8_OK;
@@ -431,12 +436,10 @@ int mxfp8_moe_prepare_experts_fp4(const void* w_e2m1, const void* w_s_e8m0, int6
   if (int st = check_weight(w_packed, s_packed, N, K)) return st;
   if (!w_e2m1 || !w_s_e8m0) return MXFP8_E_NULLPTR;
   if (!aligned(w_e2m1, 16)) return MXFP8_E_ALIGN;
-  // (the pack kernels' grids: one thread per 16 bytes, one per scale pair)
-  const int64_t per_row = K / 32;
-  const bool at_once = N % 128 == 0 && E * N * per_row <= kMaxThreads - 255;
-  const int64_t rows = at_once ? E * N : N, passes = at_once ? 1 : E;
-  if (pad128(rows) * per_row > kMaxThreads - 255) return MXFP8_E_SHAPE;
+  if (!pack_grid_ok(N, K)) return MXFP8_E_SHAPE;
   if (int st = mxfp8::check_device_current()) return st;
+  const bool at_once = pack_at_once(E, N, K);
+  const int64_t rows = at_once ? E * N : N, passes = at_once ? 1 : E;
   for (int64_t e = 0; e < passes; ++e) {
     const size_t w = (size_t)e * N * (K / 2), s = (size_t)e * N * (K / 32);
     if (int st = mxfp8::launch_pack_weight_fp4((const uint8_t*)w_e2m1 + w, (const uint8_t*)w_s_e8m0 + s, rows, K,
