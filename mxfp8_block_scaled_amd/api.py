@@ -573,9 +573,7 @@ _HERE_ALREADY = contextlib.nullcontext()
 def _on(device):
     """Context in which ``device`` is the current one (the library launches on
     the current device)."""
-    # (torch.cuda.current_device without its check that CUDA is initialized,
-    # which a GPU tensor's device has passed)
-    if device.index is None or device.index == torch._C._cuda_getDevice():
+    if device.index is None or device.index == torch.cuda.current_device():
         return _HERE_ALREADY
     return torch.cuda.device(device)
 
