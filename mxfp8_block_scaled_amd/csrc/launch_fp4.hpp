@@ -102,7 +102,6 @@ struct ExpertsArgs {
   const void* wsp;
   void* y;                 // bf16 [R, N], row stride ldy
   int64_t ldy;
-  void* ws;                // quantized rows
 };
 // Decode form: quantizes inside, no workspace.
 int launch_experts_fp4_decode(const ExpertsArgs& a, hipStream_t stream);
