@@ -41,7 +41,10 @@ std::atomic<int> g_force{0};
 
 // The forms with the least estimated time: lines through measurements on
 // MI355X (us, 16 calls in a captured graph, the quantizer's launch included), K
-// in thousands (1024).  For example (decode; 16 weight rows on packed activations;
+// in thousands (1024).  They are of the whole chip, 256 units: the size queries
+// run without a device.  On a part of one the launchers fit their grids to its
+// units, and the choice of form, which changes no result, may not be the best.
+// For example (decode; 16 weight rows on packed activations;
 // 128 x 64 tiles that quantize their rows; tiles of 128 x 64, 128 x 128, 256 x
 // 256), N x K = 4096 x 1024:
 //   M = 1        3.0    6.8    6.6    8.0    9.0
@@ -180,8 +183,10 @@ struct ExpertsForm {
   int one;               // as one_launch
   mxfp8::Fp4Plan plan;
 };
-// The same for the experts, whose rows' spread the host does not know: X
-// experts with rows at most, R / X rows each.  Decode reads all their weights
+// The same for the experts, whose rows' spread the host does not know, nor how
+// many slots have an expert here: as if all R had one, X experts with rows at
+// most, R / X rows each.  (A rank that holds an eighth of the experts plans for
+// eight times its rows.)  Decode reads all their weights
 // with its rows converted again for each 16 weight rows; tiles that quantize
 // their rows take a longer start, a quantizer before them one more launch.  For
 // example (rows per expert; decode, 128 x 64 tiles that quantize, tiles of 128 x

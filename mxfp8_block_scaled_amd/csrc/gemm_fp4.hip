@@ -4,11 +4,15 @@
 // On gfx950 the scaled MFMA multiplies 4-bit by 4-bit operands in half the
 // cycles of 8-bit ones, with half the operand bytes, so a 128-K step of a 256
 // x 256 tile is 64 MFMAs of 16 cycles per wave against 32 KiB of operands.
-// Bound by the matrix cores' power where tiles are large: 8192 x 28672 x 8192
-// 790 us (4.9 PFLOP/s), of which MFMAs alone would take 588, with the copies 652,
-// with the LDS reads 686; the chip's clock falls with the work between them (a
-// loop of MFMAs on registers: 7.5 PFLOP/s on random codes, 9.0 on zeros).  The
-// experts' tiles by their start and end, which nothing else covers: 4096 tokens,
+// Large tiles are bound by the issue of MFMAs among LDS reads and copies, and by
+// the clock that the chip's power leaves: 8192 x 28672 x 8192 takes 790 us (4.9
+// PFLOP/s; 830 to 870 called back to back), the matrix cores busy 0.62 of the
+// cycles at 1.9 GHz.  MFMAs alone would take 588 at 1.6 GHz, with the copies 652,
+// with the LDS reads 686: the clock rises with the idle cycles and makes up for a
+// part of them (a loop of MFMAs on registers: 7.5 PFLOP/s on random codes, 9.0 on
+// zeros).  The 256 x 256 tiles use all 512 registers and four spilled ones, read
+// back once a tile.  The experts' tiles are bound by their start and end, which
+// nothing covers: 4096 tokens,
 // 128 experts, k 8, 1536 x 2048 102 us (3.2 TB/s of the 331 MB that they cannot do
 // without); 14 us per 256 x 128 tile, of which the sixteen steps are 7.5, the
 // stores 2, staging them 1, the next tile's decoding and sources 1.5.

@@ -80,9 +80,10 @@ __device__ inline void store4(const DecodeArgs& p, const v4f& v, const float* bv
 // (experts: one).  kDepth: 1 for workgroups of one block of 16 weight rows; more
 // for such with a run of blocks, that many in flight, where a turn of the chip does
 // not hold all blocks: the rows are quantized once for the run, and the weight
-// streams while sums are joined (16 rows, 16384 x 8192: 22 us, one block each 44; 1
-// row 17 and 25; but 1 row, 4096 x 4096, 7.2 and 5.7: more registers, later rows.
-// All four before the rows were read sixteen lanes to a row).
+// streams while sums are joined (16 rows, 16384 x 8192: 16.4 us, one block each
+// 32.6; 1 row 14.0 and 19.4; 16 rows, 8192 x 4096 7.1 and 9.1; eight experts of 2048
+// x 7168 15.1 and 22.7; but 1 row, 4096 x 4096, 5.0 and 3.8: more registers, later
+// rows; near the border 1 row, 16384 x 2048, 5.3 and 4.8).
 template <int kWaves, int kSteps, int kGroups, int kDepth, bool kExperts>
 __global__ __launch_bounds__(64 * kWaves, kDepth > 1 || kSteps > 2 || kGroups > 1 ? 4 : 7) void gemm_fp4_decode_kernel(DecodeArgs p) {
   __shared__ v4f red[2][kGroups][kWaves * 64];

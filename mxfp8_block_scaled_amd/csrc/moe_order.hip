@@ -409,9 +409,11 @@ __global__ __launch_bounds__(kRowThreads) void unpermute_backward_kernel(
 namespace {
 bool rows16(const void* p, int64_t ld, int64_t size) { return p == nullptr || (((uintptr_t)p | (uintptr_t)(ld * size)) & 15) == 0; }
 
-// Matrices larger than the chip's L2s: results go around the caches (4096
-// tokens, top 8, H 2048 in bf16: there 29 to 28 us, back 29 to 26, gradient 67
-// to 61; a few kilobytes written that way come back slower, 3.2 to 3.7 us).
+// Matrices larger than the chip's L2s: results go around the caches.  In bf16,
+// there, back and gradient, us in graphs that use the same buffers again: 32768
+// tokens, top 2, H 4096 124, 135 and 280 around, 145, 139 and 276 through them;
+// 4096 tokens, top 8, H 2048 26.4, 23.5 and 49.1 around, 24.6, 24.0 and 55.7
+// through.  Smaller results stay for who reads them next.
 bool past_caches(const PermuteArgs& a) { return a.T * a.topk * a.H * (a.bf16 ? 2 : 4) > (int64_t)32 << 20; }
 
 // Calls go(element, aligned, past the caches) with the types as values.
