@@ -270,8 +270,11 @@ def mxfp8_gemm_prequant(q, ldq, s, lds, M, K, wp, wsp, N, bias, y, ldy, ws, ws_b
 def gemm_prequant(q, s, pw, bias=None):
     """The block-scaled GEMM + epilogue on row-major quantized activations
     (uint8 E4M3 ``q[M, K]``, UE8M0 ``s[M, >= K/32]``, GPU): bf16 ``[M, N]``."""
+    _one_weight(pw)
     if isinstance(pw, PreparedWeightB128):
         raise ValueError("gemm_prequant takes an MXFP8 weight, not one with 128-blocks")
+    if isinstance(pw, PreparedWeightFP4):
+        raise ValueError("gemm_prequant takes an MXFP8 weight, not an MXFP4 one")
     q = _as_bytes(q)
     s = _as_bytes(s)
     _require_cuda(q, "q")
@@ -347,6 +350,12 @@ class PreparedWeight:
         _check(mxfp8_unpack_weight(_ptr(self.w_packed), _ptr(self.s_packed), self.N, self.K, _ptr(w), _ptr(s),
                                    _stream(self.device)), "mxfp8_unpack_weight")
         return w, s
+
+
+def _one_weight(pw):
+    """Refuses experts' weights, which have a single weight's fields."""
+    if isinstance(pw, ExpertWeightsFP4):
+        raise ValueError("experts' weights go to moe_linear_w4a4: this takes one MXFP8 weight, or one of another format")
 
 
 def _as_bytes(t):
@@ -455,6 +464,7 @@ def linear(x, pw, bias=None, out=None, workspace=None):
     ``mxfp8_linear_b128_workspace_bytes`` for 128-blocks) bytes, 256-byte
     aligned, owned by the caller; by default a cached buffer per (device,
     stream) is used (128-blocks: a fresh one from torch's allocator)."""
+    _one_weight(pw)
     if isinstance(pw, PreparedWeightB128):
         return _linear_prepared_b128(x, pw, bias, out, workspace)
     assert x.dtype == torch.bfloat16, f"MXFP8 linear requires bfloat16 activations, got {x.dtype}"
@@ -532,6 +542,7 @@ def quantize_act_packed(x):
 def gemm_packed(pa, pw, bias=None):
     """The GEMM + epilogue on packed activations (the second kernel of the
     large-M path), for activations and a weight of the same scale block."""
+    _one_weight(pw)
     assert pa.K == pw.K
     b128 = isinstance(pw, PreparedWeightB128)
     fp4 = isinstance(pa, PackedActivationFP4)
@@ -773,13 +784,15 @@ _DTYPES = {torch.float32: 0, torch.bfloat16: 1}   # mxfp8_dtype
 
 def linear_wgrad(dy, pa, dtype=torch.float32, bias_grad=False, out=None, out_bias=None, accumulate=False):
     """Weight gradient from the 8-bit activation checkpoint ``pa`` (a
-    PackedActivation of either quantizer): ``dw[N, K] = dy^T deq(pa)``.
+    PackedActivation of either 8-bit quantizer): ``dw[N, K] = dy^T deq(pa)``.
 
     ``dy`` bf16 ``[..., N]`` with M rows, N % 8 == 0.  Returns ``dw`` (``dtype``
     float32 or bfloat16; ``out`` if given), or ``(dw, db)`` with ``bias_grad``,
     ``db`` the column sums of dy (``out_bias``, float32 or bfloat16, if given,
     else fp32).  ``accumulate`` adds to ``out`` and ``out_bias`` (both fp32)
     instead of overwriting them."""
+    if isinstance(pa, PackedActivationFP4):
+        raise ValueError("the weight gradient takes 8-bit activations, not MXFP4 ones")
     d2 = _rows(dy, "dy")
     M, N = d2.shape
     if M != pa.M:
