@@ -1298,15 +1298,6 @@ class MoEOrder:
         order.T, order.topk, order.E = T, topk, E
         return order
 
-    def _state(self):
-        """The tensors that gradients read, and their versions (inference tensors
-        have none)."""
-        rows, offsets = self.rows, self.offsets
-        try:
-            return rows, offsets, rows._version, offsets._version
-        except RuntimeError:
-            return rows, offsets, None, None
-
     @property
     def _kept(self):
         """Address of the number of rows with an expert."""
@@ -1353,7 +1344,8 @@ def _laid_out(x):
     """x with contiguous rows that do not overlap.  Called inside of the autograd
     nodes: a copy made before them would be a node of its own, and hide its
     leaf from ``_mark_leaves`` and ``_check_capture``."""
-    if x.stride(1) != 1 or x.stride(0) < x.shape[1]:
+    row, col = x.stride()
+    if col != 1 or row < x.shape[1]:
         x = x.clone(memory_format=torch.contiguous_format)
     return x
 
@@ -1394,13 +1386,18 @@ def _backward_once(backward):
 def _keep_order(ctx, order):
     """Keeps an order for the backward pass.  (Not by save_for_backward: permute's
     gradient needs no retained graph for a second pass.)"""
-    ctx.order, ctx.state = order, order._state()
+    rows, offsets = order.rows, order.offsets
+    try:
+        version = rows._version + offsets._version
+    except RuntimeError:                           # inference tensors have none
+        version = None
+    ctx.kept = order, rows, offsets, version
 
 
 def _kept_order(ctx):
-    order = ctx.order
-    was, now = ctx.state, order._state()
-    if now[0] is not was[0] or now[1] is not was[1] or now[2:] != was[2:]:
+    order, rows, offsets, version = ctx.kept
+    if order.rows is not rows or order.offsets is not offsets or \
+            (version is not None and rows._version + offsets._version != version):
         raise RuntimeError("the rows or offsets of an order have been modified by an inplace operation or replaced "
                            "between the forward and the backward pass")
     return order
@@ -1423,7 +1420,9 @@ class _MoEUnpermute(torch.autograd.Function):
     @staticmethod
     def forward(ctx, ys, weights, order):
         _keep_order(ctx, order)
-        ys, weights = _laid_out(ys), None if weights is None else weights.contiguous()
+        ys = _laid_out(ys)
+        if weights is not None and not weights.is_contiguous():
+            weights = weights.contiguous()
         ctx.save_for_backward(ys if ctx.needs_input_grad[1] else None, weights)
         return _unpermute(ys, order, weights)
 
